@@ -403,6 +403,205 @@ qsa_status_t qsa_sparse_prefill(const qsa_geom_t *geom, const void *q_bf16,
                                 size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Rotary positions of a step.  Every layer of a step rotates its queries and
+ * keys by the same angles, so they are computed once per step: row r of cs
+ * holds cos and sin of its position times each of rotary_dim / 2 frequencies,
+ * and the prologue calls below read them.
+ *
+ * qsa_rope_init (host only; launches nothing) turns a configuration into a
+ * plan.  Frequency i is f_i = theta^(-2i / rotary_dim), scaled for contexts
+ * longer than the trained one by
+ *   QSA_ROPE_PLAIN       f_i
+ *   QSA_ROPE_LINEAR      f_i / factor
+ *   QSA_ROPE_YARN        f_i (1 - m_i) + f_i / factor * m_i, m_i rising from 0
+ *                        to 1 over the dims between the one that turns `high`
+ *                        times within original_context tokens (rounded down)
+ *                        and the one that turns `low` times (rounded up); cos
+ *                        and sin are multiplied by 0.1 ln(factor) + 1
+ *   QSA_ROPE_WAVELENGTH  f_i m_i + f_i / factor * (1 - m_i), m_i = (turns of
+ *                        f_i within original_context - low) / (high - low),
+ *                        clamped to [0, 1]
+ * A positive attention_factor replaces the factor on cos and sin.  A plan
+ * holds each frequency as a 64-bit fraction of a turn, so that the angle of
+ * any 32-bit position is its product modulo one turn, exact to the plan's
+ * 53-bit frequency.
+ *
+ *   rotary_dim  16..256, a multiple of 16
+ *   theta       > 1; factor > 0 (LINEAR, YARN, WAVELENGTH)
+ *   original_context > 0, 0 < low < high (YARN, WAVELENGTH)
+ *
+ * Returns QSA_ERR_INVALID_ARG for null pointers and values outside these.
+ */
+#define QSA_ROPE_MAX_PAIRS 128
+
+typedef enum {
+    QSA_ROPE_PLAIN = 0,
+    QSA_ROPE_LINEAR = 1,
+    QSA_ROPE_YARN = 2,
+    QSA_ROPE_WAVELENGTH = 3
+} qsa_rope_scaling_t;
+
+typedef struct {
+    int rotary_dim;
+    int scaling;               /* qsa_rope_scaling_t                   */
+    double theta;
+    double factor;
+    double original_context;
+    double low, high;          /* turns within original_context        */
+    double attention_factor;   /* 0: the scaling's own                 */
+} qsa_rope_config_t;
+
+typedef struct {
+    int rotary_dim;
+    float amplitude;                       /* factor on cos and sin    */
+    uint64_t turns[QSA_ROPE_MAX_PAIRS];    /* turns per position, 2^64 */
+} qsa_rope_t;
+
+qsa_status_t qsa_rope_init(const qsa_rope_config_t *config, qsa_rope_t *rope);
+
+/*
+ * The step's rotation rows.
+ *
+ *   seqlens    int32 [B]   row j of request b is at position L_b - R + j
+ *   positions  int32 [T]   or NULL: the rows' positions instead of seqlens'
+ *                          (seqlens may then be NULL)
+ *   cs         fp32 [T, rotary_dim / 2, 2]   output: (cos, sin) * amplitude
+ *
+ * Absolute error of cos and sin below 2e-7 * amplitude at any position.
+ * Returns QSA_ERR_INVALID_ARG for null pointers, a plan that qsa_rope_init
+ * did not fill or cs not 8-byte aligned; geometry and device checks as for
+ * the other calls (rows_per_req up to 4096; of the geometry only batch and
+ * rows_per_req matter).
+ */
+qsa_status_t qsa_rope_rows(const qsa_geom_t *geom, const qsa_rope_t *rope,
+                           const int32_t *seqlens, const int32_t *positions,
+                           float *cs, cudaStream_t stream);
+
+/*
+ * Norms of queries and keys for each head, with the rotation in the same
+ * pass.  TensorRT-LLM PR #20276 ("Qwen3.8-Flash-Next NVFP4 target"),
+ * Performance (what runs on the fast paths): the attention prologue does QK
+ * norm and rope before the stores.
+ *
+ *   q, k       bf16, row r at q + r * q_row_stride (elements), its Hq / Hkv
+ *              heads of D behind one another: e.g. the parts of one projection
+ *              row
+ *   q_weight, k_weight  bf16 [D], or NULL: heads are rotated without a norm
+ *   cs         fp32 [T, rotary_dim / 2, 2] as qsa_rope_rows writes it; may be
+ *              NULL when rotary_dim is 0
+ *   q_out, k_out  bf16 [T, Hq, D] and [T, Hkv, D]   output (k_out: this call
+ *              only); q_out may be q, and k_out k, where their rows are as far
+ *              apart as the output's; other overlaps are not allowed
+ *
+ * For each head x of D elements, every operation an IEEE fp32 operation in
+ * this order:
+ *   s = sum x_i^2, neighbours first (a pairwise tree: x_0^2 + x_1^2, ...,
+ *       then sums of neighbouring sums)
+ *   y_i = (x_i * (1 / sqrt(s / D + eps))) * w_i       (y = x without a weight;
+ *       w_i = 1 + weight_i with weight_plus_one)
+ *   a' = a * cos - b * sin, b' = b * cos + a * sin    for the pairs (a, b) of
+ *       the first rotary_dim dims: (y_i, y_{i + rotary_dim/2}), or
+ *       (y_{2i}, y_{2i+1}) when interleaved; the other dims stay
+ * and one rounding to bf16 at the end.
+ *
+ * q and q_out may both be NULL (keys alone).  Returns QSA_ERR_INVALID_ARG for
+ * other null pointers, a rotary_dim that is not a multiple of 16 in [0, D],
+ * eps negative or not finite, row strides below the heads' D elements or not
+ * a multiple of 8, or pointers not 16-byte aligned; geometry and device checks
+ * as for the other calls (rows_per_req up to 4096).
+ */
+typedef struct {
+    int rotary_dim;        /* rotated dims of a head: 0..D, a multiple of 16 */
+    int interleaved;       /* pairs (2i, 2i + 1); 0: (i, i + rotary_dim / 2) */
+    int weight_plus_one;   /* the norms' weights are 1 + weight              */
+    float eps;
+} qsa_norm_rope_t;
+
+qsa_status_t qsa_qk_norm_rope(const qsa_geom_t *geom, const qsa_norm_rope_t *norm_rope,
+                              const void *q_bf16, int64_t q_row_stride, const void *k_bf16,
+                              int64_t k_row_stride, const void *q_weight_bf16,
+                              const void *k_weight_bf16, const float *cs, void *q_out_bf16,
+                              void *k_out_bf16, cudaStream_t stream);
+
+/*
+ * Decode prologue with norms and rotation: qsa_qk_norm_rope on the step's
+ * queries and keys and qsa_store_kv_tokens on the rotated keys and the values
+ * (v rows v_row_stride elements apart) in one launch, with the same bytes as
+ * the two calls one after the other: keys are rounded to bf16 before they are
+ * quantised.  q and q_out may both be NULL.  Rows without a slot are skipped
+ * in the pools; their queries are written all the same.
+ * Returns QSA_ERR_INVALID_ARG as the two calls do (k_pool, v_pool and the
+ * index pointers 4-byte aligned).
+ */
+qsa_status_t qsa_store_kv_tokens_rope(const qsa_geom_t *geom, const qsa_norm_rope_t *norm_rope,
+                                      const void *q_bf16, int64_t q_row_stride,
+                                      const void *k_bf16, int64_t k_row_stride,
+                                      const void *v_bf16, int64_t v_row_stride,
+                                      const int8_t *ik_new, const void *q_weight_bf16,
+                                      const void *k_weight_bf16, const float *cs, float k_scale,
+                                      float v_scale, const int32_t *page_table,
+                                      const int32_t *seqlens, void *q_out_bf16, uint8_t *k_pool,
+                                      uint8_t *k_sf, uint8_t *v_pool, uint8_t *v_sf,
+                                      int8_t *ik_pool, cudaStream_t stream);
+
+/*
+ * Rows of the cache read back: the NVFP4 keys and values of each request's R
+ * newest tokens as bf16 (PR #20276, Known limitations: context rows read the
+ * NVFP4 pages dequantised to bf16).
+ *
+ *   k_out, v_out  bf16 [T, Hkv, D]   output: e2m1 * e4m3 * scale in fp32,
+ *                                    rounded once
+ *
+ * Rows without a slot (as in qsa_store_kv_tokens) are left as they were.
+ * Returns QSA_ERR_INVALID_ARG for null pointers, scales that are not finite,
+ * k_pool or v_pool not 4-byte or outputs not 16-byte aligned; geometry and
+ * device checks as for the other calls (rows_per_req up to 4096).
+ */
+qsa_status_t qsa_load_kv_tokens(const qsa_geom_t *geom, const int32_t *page_table,
+                                const int32_t *seqlens, const uint8_t *k_pool,
+                                const uint8_t *k_sf, const uint8_t *v_pool, const uint8_t *v_sf,
+                                float k_scale, float v_scale, void *k_out_bf16,
+                                void *v_out_bf16, cudaStream_t stream);
+
+/*
+ * Dense attention over the NVFP4 paged cache: the layers of a model that do
+ * not select blocks, for decode rows (R = 1), verify rows and context row
+ * groups (R up to 4096), over contexts of any length the page table holds.
+ *
+ *   q, pools, scales, page_table, seqlens, out, lse   as in qsa_sparse_decode
+ *   window    tokens a row looks back over, itself included; 0: all
+ *   sinks     fp32 [Hq], or NULL: a logit per query head that takes part in
+ *             the softmax's denominator without a value (-inf: none)
+ *   workspace >= qsa_dense_attention_workspace_bytes() bytes, 256-byte
+ *             aligned, zero-filled once by qsa_workspace_init(); calls that
+ *             share one must not overlap on the GPU
+ *
+ * Row j of request b sees n tokens (as above): those at positions
+ * max(0, n - window)..n - 1 whose page is valid.
+ *   z_t = sm_scale * q . K_t,  lse = ln(sum_t exp(z_t) [+ exp(sink)]),
+ *   out = sum_t exp(z_t - lse) V_t
+ * A row that sees no token gets out = 0 and lse = the sink, or -inf.  What the
+ * cache holds at positions that no row of the request sees is not looked at.
+ * The work is divided evenly over the GPU by the requests' actual lengths and
+ * joined by log-sum-exp in a fixed order: the same inputs give the same bits.
+ *
+ * Returns QSA_ERR_INVALID_ARG for null pointers, window < 0, k_scale or
+ * sm_scale not positive and finite, v_scale not finite, pools, scales, q or
+ * out not 16-byte aligned; QSA_ERR_UNSUPPORTED for more than 128 query heads
+ * per KV head; QSA_ERR_WORKSPACE for a missing, short or misaligned
+ * workspace.  A bounded device wait that gives up is reported through
+ * qsa_workspace_status().
+ */
+size_t qsa_dense_attention_workspace_bytes(const qsa_geom_t *geom);
+qsa_status_t qsa_dense_attention(const qsa_geom_t *geom, const void *q_bf16,
+                                 const uint8_t *k_pool, const uint8_t *k_sf,
+                                 const uint8_t *v_pool, const uint8_t *v_sf, float k_scale,
+                                 float v_scale, float sm_scale, const int32_t *page_table,
+                                 const int32_t *seqlens, int window, const float *sinks,
+                                 void *out_bf16, float *lse, void *workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Diagnostics: sets the bound, in nanoseconds, of the waits of the head_dim
  * 128 sparse decode kernel for its page copies (2 s by default; 0 restores
  * the default).  Process-wide, for tests of the timeout reporting: a bound
@@ -426,7 +625,8 @@ void qsa_debug_set_wait_ns(unsigned long long ns);
  * -1 in a build without the checks (the normal library) or on a CUDA error.
  * Codes are 0xF0S: F the source file (1 decode-row attention, 2 decode and
  * verify attention, 3 index scores, 4 selection, 5 token store, 6 rollback,
- * 7 row-tile attention), S the check.  Not thread-safe against concurrent
+ * 7 row-tile attention, 8 norms, rotation and cache rows, 9 and A dense
+ * attention), S the check.  Not thread-safe against concurrent
  * calls of the library.
  */
 int qsa_debug_bounds_status(void);

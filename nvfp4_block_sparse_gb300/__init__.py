@@ -21,7 +21,9 @@ from .binding import (EXPORTS, QsaError, load, make_geom, qsa_geom_t, qsa_index_
                       qsa_rollback_gather, qsa_rollback_restore, qsa_rollback_state_bytes,
                       qsa_sparse_prefill, qsa_sparse_prefill_workspace_bytes,
                       qsa_status_string, qsa_store_kv_tokens, qsa_workspace_init,
-                      qsa_workspace_status)
+                      qsa_workspace_status, make_rope, make_norm_rope, qsa_rope_t, qsa_norm_rope_t,
+                      qsa_rope_rows, qsa_qk_norm_rope, qsa_store_kv_tokens_rope,
+                      qsa_load_kv_tokens, qsa_dense_attention, qsa_dense_attention_workspace_bytes)
 
 __all__ = [
     "EXPORTS", "QsaError", "load", "make_geom", "qsa_geom_t", "qsa_index_scores",
@@ -33,7 +35,10 @@ __all__ = [
     "qsa_rollback_gather", "qsa_rollback_restore", "qsa_rollback_state_bytes",
     "qsa_sparse_prefill", "qsa_sparse_prefill_workspace_bytes",
     "qsa_status_string", "qsa_store_kv_tokens", "qsa_workspace_init", "qsa_workspace_status",
-    "DecodeStep", "MAX_DECODE_ROWS",
+    "make_rope", "make_norm_rope", "qsa_rope_t", "qsa_norm_rope_t", "qsa_rope_rows",
+    "qsa_qk_norm_rope", "qsa_store_kv_tokens_rope", "qsa_load_kv_tokens", "qsa_dense_attention",
+    "qsa_dense_attention_workspace_bytes",
+    "DecodeStep", "DenseStep", "MAX_DECODE_ROWS",
 ]
 
 # Rows per request the decode / verify attention takes; longer row groups
@@ -160,3 +165,57 @@ class DecodeStep:
     @staticmethod
     def default_sm_scale(head_dim: int = 128) -> float:
         return 1.0 / math.sqrt(head_dim)
+
+
+class DenseStep:
+    """Device buffers for one dense attention step of a fixed geometry: the
+    layers that attend to every cached token (or the newest ``window``) instead
+    of selected blocks, over the same cache and page table as DecodeStep, with
+    any number of rows per request.  ``store`` is the prologue (norms, rotation,
+    append) into the workload's pools, ``run`` the attention."""
+
+    def __init__(self, geom: dict, window: int = 0, device="cuda"):
+        self.geom = {n: int(geom[n]) for n in GEOM_FIELDS}
+        self.cg = make_geom(**self.geom)
+        self.window = int(window)
+        T, Hq, D = (self.geom["batch"] * self.geom["rows_per_req"], self.geom["num_q_heads"],
+                    self.geom["head_dim"])
+        dev = torch.device(device)
+        # out and lse share one allocation, as in DecodeStep
+        out_bytes = T * Hq * D * 2
+        lse_off = (out_bytes + 255) // 256 * 256
+        self.results = torch.empty((lse_off + T * Hq * 4,), dtype=torch.uint8, device=dev)
+        self.out = self.results[:out_bytes].view(torch.bfloat16).view(T, Hq, D)
+        self.lse = self.results[lse_off:].view(torch.float32).view(T, Hq)
+        self.q = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        nbytes = qsa_dense_attention_workspace_bytes(self.cg)
+        if nbytes == 0:
+            raise QsaError("qsa_dense_attention_workspace_bytes", 1, "invalid geometry")
+        with torch.cuda.device(dev):
+            self.workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+            qsa_workspace_init(self.workspace)
+
+    def status(self) -> int:
+        """Device status word of this step's workspace: 0 when every bounded
+        wait completed."""
+        return qsa_workspace_status(self.workspace)
+
+    def store(self, w: dict, new: dict, norm_rope, cs, stream=None):
+        """Appends the rows ``new`` (q, k, v, ik_new, and the norms' q_weight and
+        k_weight or None) to the pools of ``w``; the rotated queries are left in
+        ``self.q``."""
+        qsa_store_kv_tokens_rope(self.cg, norm_rope, new["q"], new["k"], new["v"], new["ik_new"],
+                                 new["q_weight"], new["k_weight"], cs, w["k_scale"], w["v_scale"],
+                                 w["page_table"], w["seqlens"], self.q, w["k_pool"], w["k_sf"],
+                                 w["v_pool"], w["v_sf"], w["ik_pool"], stream)
+        return self
+
+    def run(self, w: dict, q=None, sinks=None, stream=None, sm_scale=None, out=None, lse=None):
+        """Attention of ``q`` (default: the workload's own) over the cache of ``w``."""
+        qsa_dense_attention(self.cg, w["q"] if q is None else q, w["k_pool"], w["k_sf"],
+                            w["v_pool"], w["v_sf"], w["k_scale"], w["v_scale"],
+                            float(w["sm_scale"]) if sm_scale is None else float(sm_scale),
+                            w["page_table"], w["seqlens"], self.out if out is None else out,
+                            self.lse if lse is None else lse, self.workspace, window=self.window,
+                            sinks=sinks, stream=stream)
+        return self

@@ -43,7 +43,16 @@ EXPORTS = (
     "qsa_rollback_restore",
     "qsa_sparse_prefill_workspace_bytes",
     "qsa_sparse_prefill",
+    "qsa_rope_init",
+    "qsa_rope_rows",
+    "qsa_qk_norm_rope",
+    "qsa_store_kv_tokens_rope",
+    "qsa_load_kv_tokens",
+    "qsa_dense_attention_workspace_bytes",
+    "qsa_dense_attention",
 )
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "yarn": 2, "wavelength": 3}
 
 
 class QsaError(RuntimeError):
@@ -56,6 +65,22 @@ class qsa_geom_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in (
         "batch", "rows_per_req", "num_q_heads", "num_kv_heads", "head_dim",
         "index_dim", "page_size", "max_blocks", "num_pages")]
+
+
+class qsa_rope_config_t(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("scaling", ctypes.c_int)] + [
+        (n, ctypes.c_double) for n in ("theta", "factor", "original_context", "low", "high",
+                                       "attention_factor")]
+
+
+class qsa_rope_t(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("amplitude", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * 128)]
+
+
+class qsa_norm_rope_t(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("weight_plus_one", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -128,6 +153,24 @@ def load(build_if_missing: bool = False):
     lib.qsa_sparse_prefill_workspace_bytes.argtypes = [G, ctypes.c_int]
     lib.qsa_sparse_prefill.restype = st
     lib.qsa_sparse_prefill.argtypes = dec + [_vp]
+    f32, i64 = ctypes.c_float, ctypes.c_int64
+    NR = ctypes.POINTER(qsa_norm_rope_t)
+    lib.qsa_rope_init.restype = st
+    lib.qsa_rope_init.argtypes = [ctypes.POINTER(qsa_rope_config_t), ctypes.POINTER(qsa_rope_t)]
+    lib.qsa_rope_rows.restype = st
+    lib.qsa_rope_rows.argtypes = [G, ctypes.POINTER(qsa_rope_t)] + [_vp] * 4
+    lib.qsa_qk_norm_rope.restype = st
+    lib.qsa_qk_norm_rope.argtypes = [G, NR, _vp, i64, _vp, i64] + [_vp] * 6
+    lib.qsa_store_kv_tokens_rope.restype = st
+    lib.qsa_store_kv_tokens_rope.argtypes = ([G, NR, _vp, i64, _vp, i64, _vp, i64] + [_vp] * 4 +
+                                             [f32, f32] + [_vp] * 9)
+    lib.qsa_load_kv_tokens.restype = st
+    lib.qsa_load_kv_tokens.argtypes = [G] + [_vp] * 6 + [f32, f32] + [_vp] * 3
+    lib.qsa_dense_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.qsa_dense_attention_workspace_bytes.argtypes = [G]
+    lib.qsa_dense_attention.restype = st
+    lib.qsa_dense_attention.argtypes = ([G] + [_vp] * 5 + [f32] * 3 + [_vp, _vp, ctypes.c_int] +
+                                        [_vp] * 4 + [ctypes.c_size_t, _vp])
     lib.qsa_sparse_decode_noalloc_status.restype = st
     lib.qsa_sparse_decode_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_int), _vp]
     lib.qsa_debug_set_wait_ns.restype = None
@@ -350,3 +393,169 @@ def qsa_workspace_status(workspace, stream=None) -> int:
     if st not in (QSA_OK, QSA_ERR_DEVICE_TIMEOUT):
         _check("qsa_workspace_status", st)
     return int(code.value)
+
+
+# ---------------------------------------------------------------------------
+# The calls below check that every tensor is on one device and make that device
+# current for the launch; `stream` defaults to its current stream.
+# ---------------------------------------------------------------------------
+
+class _On:
+    """Pointers of one call's tensors, all on one CUDA device."""
+
+    __slots__ = ("device",)
+
+    def __init__(self):
+        self.device = -1
+
+    def __call__(self, t, dtype, name, numel, rows=False):
+        """Pointer of ``t`` (None stays NULL); ``rows``: a [T, heads, D] view whose rows may be
+        further apart, else contiguous."""
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch tensor" % name)
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if t.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if t.numel() < numel:
+            raise ValueError("%s has %d elements, needs %d" % (name, t.numel(), numel))
+        if rows:
+            if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+                raise ValueError("%s must be [rows, heads, dims] with its heads behind one another"
+                                 % name)
+        elif not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        d = t.get_device()
+        if d != self.device:
+            if self.device >= 0:
+                raise ValueError("%s is on another device than the tensors before it" % name)
+            self.device = d
+        return t.data_ptr()
+
+    def call(self, fn, args, stream):
+        name = fn.__name__
+        if self.device == torch.cuda.current_device():
+            st = fn(*args, _stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                st = fn(*args, _stream(stream))
+        if st != QSA_OK:
+            _check(name, st)
+
+
+def _row_stride(t, heads):
+    """Elements between two rows of a [T, heads, D] view."""
+    return t.stride(0) if t.shape[0] > 1 else heads * t.shape[2]
+
+
+def make_rope(rotary_dim, theta, scaling="none", factor=1.0, original_context=0.0, beta_fast=32.0,
+              beta_slow=1.0, low_freq=1.0, high_freq=4.0, attention_factor=0.0) -> qsa_rope_t:
+    """A rotation plan (qsa_rope_init): ``scaling`` is "none", "linear", "yarn" (beta_fast,
+    beta_slow: turns within original_context) or "wavelength" (low_freq, high_freq likewise)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
+    low, high = (beta_slow, beta_fast) if scaling == "yarn" else (low_freq, high_freq)
+    cfg = qsa_rope_config_t(int(rotary_dim), ROPE_SCALINGS[scaling], float(theta), float(factor),
+                            float(original_context), float(low), float(high),
+                            float(attention_factor))
+    rope = qsa_rope_t()
+    _check("qsa_rope_init", load().qsa_rope_init(ctypes.byref(cfg), ctypes.byref(rope)))
+    return rope
+
+
+def make_norm_rope(rotary_dim, interleaved=False, eps=1e-6, weight_plus_one=False) -> qsa_norm_rope_t:
+    return qsa_norm_rope_t(int(rotary_dim), int(bool(interleaved)), int(bool(weight_plus_one)),
+                           float(eps))
+
+
+def qsa_rope_rows(geom, rope, seqlens, cs, positions=None, stream=None):
+    g, on = _geom(geom), _On()
+    T = g.batch * g.rows_per_req
+    args = [ctypes.byref(g), ctypes.byref(rope), on(seqlens, torch.int32, "seqlens", g.batch),
+            on(positions, torch.int32, "positions", T),
+            on(cs, torch.float32, "cs", T * rope.rotary_dim)]
+    on.call(load().qsa_rope_rows, args, stream)
+
+
+def _qk_args(g, nr, on, q, k, q_weight, k_weight, cs, q_out):
+    T, D = g.batch * g.rows_per_req, g.head_dim
+    nq, nk = T * g.num_q_heads * D, T * g.num_kv_heads * D
+    if q is not None and q.shape[1:] != (g.num_q_heads, D):
+        raise ValueError("q must be [rows, %d, %d]" % (g.num_q_heads, D))
+    if k.shape[1:] != (g.num_kv_heads, D):
+        raise ValueError("k must be [rows, %d, %d]" % (g.num_kv_heads, D))
+    bf = torch.bfloat16
+    rows = [on(q, bf, "q", nq, True), 0 if q is None else _row_stride(q, g.num_q_heads),
+            on(k, bf, "k", nk, True), _row_stride(k, g.num_kv_heads)]
+    tail = [on(q_weight, bf, "q_weight", D), on(k_weight, bf, "k_weight", D),
+            on(cs, torch.float32, "cs", T * nr.rotary_dim)]
+    return rows, tail, on(q_out, bf, "q_out", nq), nk
+
+
+def qsa_qk_norm_rope(geom, norm_rope, q, k, q_weight, k_weight, cs, q_out, k_out, stream=None):
+    """Norm of every query and key head with its rotation; q [T, Hq, D] and k [T, Hkv, D] may be
+    views into one projection's rows; weights may be None (no norm)."""
+    g, on = _geom(geom), _On()
+    rows, tail, qo, nk = _qk_args(g, norm_rope, on, q, k, q_weight, k_weight, cs, q_out)
+    args = [ctypes.byref(g), ctypes.byref(norm_rope)] + rows + tail + [
+        qo, on(k_out, torch.bfloat16, "k_out", nk)]
+    on.call(load().qsa_qk_norm_rope, args, stream)
+
+
+def _pool_ptrs(g, on, k_pool, k_sf, v_pool, v_sf):
+    n = g.num_pages * g.num_kv_heads * g.page_size * g.head_dim
+    u8 = torch.uint8
+    return [on(k_pool, u8, "k_pool", n // 2), on(k_sf, u8, "k_sf", n // 16),
+            on(v_pool, u8, "v_pool", n // 2), on(v_sf, u8, "v_sf", n // 16)]
+
+
+def qsa_store_kv_tokens_rope(geom, norm_rope, q, k, v, ik_new, q_weight, k_weight, cs, k_scale,
+                             v_scale, page_table, seqlens, q_out, k_pool, k_sf, v_pool, v_sf,
+                             ik_pool, stream=None):
+    """qsa_qk_norm_rope and qsa_store_kv_tokens in one launch; v [T, Hkv, D] as k; q and q_out may
+    be None."""
+    g, on = _geom(geom), _On()
+    rows, tail, qo, nk = _qk_args(g, norm_rope, on, q, k, q_weight, k_weight, cs, q_out)
+    if v.shape[1:] != (g.num_kv_heads, g.head_dim):
+        raise ValueError("v must be [rows, %d, %d]" % (g.num_kv_heads, g.head_dim))
+    T, i32 = g.batch * g.rows_per_req, torch.int32
+    args = [ctypes.byref(g), ctypes.byref(norm_rope)] + rows + [
+        on(v, torch.bfloat16, "v", nk, True), _row_stride(v, g.num_kv_heads),
+        on(ik_new, torch.int8, "ik_new", T * 64)] + tail + [
+        k_scale, v_scale, on(page_table, i32, "page_table", g.batch * g.max_blocks),
+        on(seqlens, i32, "seqlens", g.batch), qo] + _pool_ptrs(g, on, k_pool, k_sf, v_pool, v_sf) + [
+        on(ik_pool, torch.int8, "ik_pool", g.num_pages * g.page_size * 64)]
+    on.call(load().qsa_store_kv_tokens_rope, args, stream)
+
+
+def qsa_load_kv_tokens(geom, page_table, seqlens, k_pool, k_sf, v_pool, v_sf, k_scale, v_scale,
+                       k_out, v_out, stream=None):
+    g, on = _geom(geom), _On()
+    n, i32 = g.batch * g.rows_per_req * g.num_kv_heads * g.head_dim, torch.int32
+    args = [ctypes.byref(g), on(page_table, i32, "page_table", g.batch * g.max_blocks),
+            on(seqlens, i32, "seqlens", g.batch)] + _pool_ptrs(g, on, k_pool, k_sf, v_pool, v_sf) + [
+            k_scale, v_scale, on(k_out, torch.bfloat16, "k_out", n),
+            on(v_out, torch.bfloat16, "v_out", n)]
+    on.call(load().qsa_load_kv_tokens, args, stream)
+
+
+def qsa_dense_attention_workspace_bytes(geom) -> int:
+    return int(load().qsa_dense_attention_workspace_bytes(ctypes.byref(_geom(geom))))
+
+
+def qsa_dense_attention(geom, q, k_pool, k_sf, v_pool, v_sf, k_scale, v_scale, sm_scale, page_table,
+                        seqlens, out, lse, workspace, window=0, sinks=None, stream=None):
+    """Dense attention of every row over its request's cached tokens (the newest ``window`` of
+    them unless 0), with an optional sink logit per query head."""
+    g, on = _geom(geom), _On()
+    T, i32, f32 = g.batch * g.rows_per_req, torch.int32, torch.float32
+    n = T * g.num_q_heads
+    args = [ctypes.byref(g), on(q, torch.bfloat16, "q", n * g.head_dim)] + _pool_ptrs(
+        g, on, k_pool, k_sf, v_pool, v_sf) + [
+        k_scale, v_scale, sm_scale, on(page_table, i32, "page_table", g.batch * g.max_blocks),
+        on(seqlens, i32, "seqlens", g.batch), int(window), on(sinks, f32, "sinks", g.num_q_heads),
+        on(out, torch.bfloat16, "out", n * g.head_dim), on(lse, f32, "lse", n),
+        on(workspace, torch.uint8, "workspace", 0), workspace.numel()]
+    on.call(load().qsa_dense_attention, args, stream)

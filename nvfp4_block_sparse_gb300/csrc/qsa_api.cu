@@ -21,6 +21,8 @@ using qsa::Geom;
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};
 
+bool positive(double x) { return x > 0.0 && isfinite(x); }
+
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 // max_rows: 8 for the decode / verify attention and the rollback; the index
@@ -97,6 +99,49 @@ qsa_status_t check_decode_args(const qsa_geom_t* geom, int k) {
   return QSA_OK;
 }
 
+// A row of `heads` heads of D elements, 16-byte pieces.
+bool rows_ok(const void* p, int64_t stride, int heads, int d) {
+  return p && aligned(p, 16) && stride >= (int64_t)heads * d && stride % 8 == 0 &&
+         stride < (1LL << 40);
+}
+
+// What qsa_qk_norm_rope and qsa_store_kv_tokens_rope check alike.
+qsa_status_t check_norm_rope(const qsa_geom_t* geom, const qsa_norm_rope_t* nr, const void* q,
+                             int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* q_weight, const void* k_weight, const float* cs,
+                             const void* q_out) {
+  qsa_status_t st = check_geom(geom, qsa::kMaxContextRows);
+  if (st != QSA_OK) return st;
+  if (!nr || nr->rotary_dim < 0 || nr->rotary_dim > geom->head_dim || nr->rotary_dim % 16 != 0)
+    return QSA_ERR_INVALID_ARG;
+  if (!(nr->eps >= 0.f) || !isfinite(nr->eps)) return QSA_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return QSA_ERR_INVALID_ARG;
+  if (q && !rows_ok(q, q_stride, geom->num_q_heads, geom->head_dim)) return QSA_ERR_INVALID_ARG;
+  if (!rows_ok(k, k_stride, geom->num_kv_heads, geom->head_dim)) return QSA_ERR_INVALID_ARG;
+  if (!aligned(q_out, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(cs, 16))
+    return QSA_ERR_INVALID_ARG;
+  if (nr->rotary_dim > 0 && !cs) return QSA_ERR_INVALID_ARG;
+  // in place only where every row is read and written at the same address
+  if (q && q_out == q && q_stride != (int64_t)geom->num_q_heads * geom->head_dim)
+    return QSA_ERR_INVALID_ARG;
+  return QSA_OK;
+}
+
+qsa::NormRope to_norm_rope(const qsa_norm_rope_t* nr) {
+  qsa::NormRope r;
+  r.rot = nr->rotary_dim;
+  r.interleaved = nr->interleaved != 0;
+  r.plus_one = nr->weight_plus_one != 0;
+  r.eps = nr->eps;
+  return r;
+}
+
+qsa_status_t check_dense_geom(const qsa_geom_t* geom) {
+  qsa_status_t st = check_geom(geom, qsa::kMaxContextRows);
+  if (st != QSA_OK) return st;
+  return geom->num_q_heads / geom->num_kv_heads > 128 ? QSA_ERR_UNSUPPORTED : QSA_OK;
+}
+
 }  // namespace
 
 namespace qsa {
@@ -118,7 +163,7 @@ int qsa_debug_bounds_status(void) {
   int first = 0;
   for (int v : {qsa::bounds_word_attend(), qsa::bounds_word_decode(), qsa::bounds_word_index(),
                 qsa::bounds_word_select(), qsa::bounds_word_store(), qsa::bounds_word_rollback(),
-                qsa::bounds_word_prefill()}) {
+                qsa::bounds_word_prefill(), qsa::bounds_word_prologue(), qsa::bounds_word_dense()}) {
     if (v < 0) return -1;
     if (first == 0) first = v;
   }
@@ -326,6 +371,196 @@ qsa_status_t qsa_sparse_prefill(const qsa_geom_t* geom, const void* q_bf16,
                                               k_scale, v_scale, sm_scale, page_table, seqlens,
                                               sel, k, out_bf16, lse,
                                               reinterpret_cast<int*>(workspace), stream));
+}
+
+qsa_status_t qsa_rope_init(const qsa_rope_config_t* config, qsa_rope_t* rope) {
+  if (!config || !rope) return QSA_ERR_INVALID_ARG;
+  const qsa_rope_config_t& c = *config;
+  if (c.rotary_dim < 16 || c.rotary_dim > 2 * QSA_ROPE_MAX_PAIRS || c.rotary_dim % 16 != 0)
+    return QSA_ERR_INVALID_ARG;
+  if (c.scaling < QSA_ROPE_PLAIN || c.scaling > QSA_ROPE_WAVELENGTH) return QSA_ERR_INVALID_ARG;
+  if (!(c.theta > 1.0) || !isfinite(c.theta)) return QSA_ERR_INVALID_ARG;
+  if (!(c.attention_factor >= 0.0) || !isfinite(c.attention_factor)) return QSA_ERR_INVALID_ARG;
+  const bool banded = c.scaling == QSA_ROPE_YARN || c.scaling == QSA_ROPE_WAVELENGTH;
+  if (c.scaling != QSA_ROPE_PLAIN && !positive(c.factor)) return QSA_ERR_INVALID_ARG;
+  if (banded && (!positive(c.original_context) || !positive(c.low) || !positive(c.high) ||
+                 !(c.low < c.high)))
+    return QSA_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925;
+  const int pairs = c.rotary_dim / 2;
+  // YARN: the dims that turn `high` and `low` times within the original context
+  double first = 0.0, last = 1.0;
+  if (c.scaling == QSA_ROPE_YARN) {
+    const double per = c.rotary_dim / (2.0 * log(c.theta));
+    first = fmax(floor(per * log(c.original_context / (c.high * two_pi))), 0.0);
+    last = fmin(ceil(per * log(c.original_context / (c.low * two_pi))), c.rotary_dim - 1.0);
+    last = fmax(last, first + 1e-3);
+  }
+  for (int i = 0; i < QSA_ROPE_MAX_PAIRS; ++i) {
+    if (i >= pairs) {
+      rope->turns[i] = 0;
+      continue;
+    }
+    double f = pow(c.theta, -2.0 * i / c.rotary_dim);
+    if (c.scaling == QSA_ROPE_LINEAR) {
+      f /= c.factor;
+    } else if (c.scaling == QSA_ROPE_YARN) {
+      const double m = fmin(fmax((i - first) / (last - first), 0.0), 1.0);
+      f = f * (1.0 - m) + f / c.factor * m;
+    } else if (c.scaling == QSA_ROPE_WAVELENGTH) {
+      const double turns = c.original_context * f / two_pi;
+      const double m = fmin(fmax((turns - c.low) / (c.high - c.low), 0.0), 1.0);
+      f = f * m + f / c.factor * (1.0 - m);
+    }
+    double t = f / two_pi;
+    t -= floor(t);   // whole turns change nothing
+    rope->turns[i] = (uint64_t)ldexp(t, 64);
+  }
+  double amplitude = c.attention_factor;
+  if (amplitude == 0.0)
+    amplitude = c.scaling == QSA_ROPE_YARN && c.factor > 1.0 ? 0.1 * log(c.factor) + 1.0 : 1.0;
+  rope->amplitude = (float)amplitude;
+  rope->rotary_dim = c.rotary_dim;
+  return QSA_OK;
+}
+
+qsa_status_t qsa_rope_rows(const qsa_geom_t* geom, const qsa_rope_t* rope, const int32_t* seqlens,
+                           const int32_t* positions, float* cs, cudaStream_t stream) {
+  qsa_status_t st = check_geom(geom, qsa::kMaxContextRows);
+  if (st != QSA_OK) return st;
+  if (!rope || (!seqlens && !positions) || !cs || !aligned(cs, 8)) return QSA_ERR_INVALID_ARG;
+  if (rope->rotary_dim < 16 || rope->rotary_dim > 2 * QSA_ROPE_MAX_PAIRS ||
+      rope->rotary_dim % 16 != 0 || !positive(rope->amplitude))
+    return QSA_ERR_INVALID_ARG;
+  st = check_device();
+  if (st != QSA_OK) return st;
+  return from_cuda(qsa::launch_rope_rows(to_geom(geom), *rope, seqlens, positions, cs, true, stream));
+}
+
+qsa_status_t qsa_qk_norm_rope(const qsa_geom_t* geom, const qsa_norm_rope_t* norm_rope,
+                              const void* q_bf16, int64_t q_row_stride, const void* k_bf16,
+                              int64_t k_row_stride, const void* q_weight_bf16,
+                              const void* k_weight_bf16, const float* cs, void* q_out_bf16,
+                              void* k_out_bf16, cudaStream_t stream) {
+  qsa_status_t st = check_norm_rope(geom, norm_rope, q_bf16, q_row_stride, k_bf16, k_row_stride,
+                                    q_weight_bf16, k_weight_bf16, cs, q_out_bf16);
+  if (st != QSA_OK) return st;
+  if (!k_out_bf16 || !aligned(k_out_bf16, 16)) return QSA_ERR_INVALID_ARG;
+  if (k_out_bf16 == k_bf16 && k_row_stride != (int64_t)geom->num_kv_heads * geom->head_dim)
+    return QSA_ERR_INVALID_ARG;
+  st = check_device();
+  if (st != QSA_OK) return st;
+  qsa::PrologueArgs a = {};
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q_bf16);
+  a.k = reinterpret_cast<const __nv_bfloat16*>(k_bf16);
+  a.q_stride = q_row_stride;
+  a.k_stride = k_row_stride;
+  a.q_weight = reinterpret_cast<const __nv_bfloat16*>(q_weight_bf16);
+  a.k_weight = reinterpret_cast<const __nv_bfloat16*>(k_weight_bf16);
+  a.cs = cs;
+  a.q_out = reinterpret_cast<__nv_bfloat16*>(q_out_bf16);
+  a.k_out = reinterpret_cast<__nv_bfloat16*>(k_out_bf16);
+  return from_cuda(qsa::launch_prologue(to_geom(geom), to_norm_rope(norm_rope), a, true, stream));
+}
+
+qsa_status_t qsa_store_kv_tokens_rope(const qsa_geom_t* geom, const qsa_norm_rope_t* norm_rope,
+                                      const void* q_bf16, int64_t q_row_stride,
+                                      const void* k_bf16, int64_t k_row_stride,
+                                      const void* v_bf16, int64_t v_row_stride,
+                                      const int8_t* ik_new, const void* q_weight_bf16,
+                                      const void* k_weight_bf16, const float* cs, float k_scale,
+                                      float v_scale, const int32_t* page_table,
+                                      const int32_t* seqlens, void* q_out_bf16, uint8_t* k_pool,
+                                      uint8_t* k_sf, uint8_t* v_pool, uint8_t* v_sf,
+                                      int8_t* ik_pool, cudaStream_t stream) {
+  qsa_status_t st = check_norm_rope(geom, norm_rope, q_bf16, q_row_stride, k_bf16, k_row_stride,
+                                    q_weight_bf16, k_weight_bf16, cs, q_out_bf16);
+  if (st != QSA_OK) return st;
+  if (!rows_ok(v_bf16, v_row_stride, geom->num_kv_heads, geom->head_dim)) return QSA_ERR_INVALID_ARG;
+  if (!ik_new || !page_table || !seqlens || !k_pool || !k_sf || !v_pool || !v_sf || !ik_pool)
+    return QSA_ERR_INVALID_ARG;
+  if (!positive(k_scale) || !positive(v_scale)) return QSA_ERR_INVALID_ARG;
+  if (!aligned(ik_new, 4) || !aligned(ik_pool, 4) || !aligned(k_pool, 4) || !aligned(v_pool, 4))
+    return QSA_ERR_INVALID_ARG;
+  st = check_device();
+  if (st != QSA_OK) return st;
+  qsa::PrologueArgs a = {};
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q_bf16);
+  a.k = reinterpret_cast<const __nv_bfloat16*>(k_bf16);
+  a.v = reinterpret_cast<const __nv_bfloat16*>(v_bf16);
+  a.q_stride = q_row_stride;
+  a.k_stride = k_row_stride;
+  a.v_stride = v_row_stride;
+  a.ik = ik_new;
+  a.q_weight = reinterpret_cast<const __nv_bfloat16*>(q_weight_bf16);
+  a.k_weight = reinterpret_cast<const __nv_bfloat16*>(k_weight_bf16);
+  a.cs = cs;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.page_table = page_table;
+  a.seqlens = seqlens;
+  a.q_out = reinterpret_cast<__nv_bfloat16*>(q_out_bf16);
+  a.k_pool = k_pool;
+  a.k_sf = k_sf;
+  a.v_pool = v_pool;
+  a.v_sf = v_sf;
+  a.ik_pool = ik_pool;
+  return from_cuda(qsa::launch_prologue(to_geom(geom), to_norm_rope(norm_rope), a, true, stream));
+}
+
+qsa_status_t qsa_load_kv_tokens(const qsa_geom_t* geom, const int32_t* page_table,
+                                const int32_t* seqlens, const uint8_t* k_pool,
+                                const uint8_t* k_sf, const uint8_t* v_pool, const uint8_t* v_sf,
+                                float k_scale, float v_scale, void* k_out_bf16,
+                                void* v_out_bf16, cudaStream_t stream) {
+  qsa_status_t st = check_geom(geom, qsa::kMaxContextRows);
+  if (st != QSA_OK) return st;
+  if (!page_table || !seqlens || !k_pool || !k_sf || !v_pool || !v_sf || !k_out_bf16 || !v_out_bf16)
+    return QSA_ERR_INVALID_ARG;
+  if (!isfinite(k_scale) || !isfinite(v_scale)) return QSA_ERR_INVALID_ARG;
+  if (!aligned(k_pool, 4) || !aligned(v_pool, 4) || !aligned(k_out_bf16, 16) ||
+      !aligned(v_out_bf16, 16))
+    return QSA_ERR_INVALID_ARG;
+  st = check_device();
+  if (st != QSA_OK) return st;
+  return from_cuda(qsa::launch_load_tokens(to_geom(geom), page_table, seqlens, k_pool, k_sf, v_pool,
+                                           v_sf, k_scale, v_scale, k_out_bf16, v_out_bf16, true,
+                                           stream));
+}
+
+size_t qsa_dense_attention_workspace_bytes(const qsa_geom_t* geom) {
+  return check_dense_geom(geom) == QSA_OK ? qsa::dense_workspace_bytes(to_geom(geom)) : 0;
+}
+
+qsa_status_t qsa_dense_attention(const qsa_geom_t* geom, const void* q_bf16,
+                                 const uint8_t* k_pool, const uint8_t* k_sf,
+                                 const uint8_t* v_pool, const uint8_t* v_sf, float k_scale,
+                                 float v_scale, float sm_scale, const int32_t* page_table,
+                                 const int32_t* seqlens, int window, const float* sinks,
+                                 void* out_bf16, float* lse, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream) {
+  qsa_status_t st = check_dense_geom(geom);
+  if (st != QSA_OK) return st;
+  if (!q_bf16 || !k_pool || !k_sf || !v_pool || !v_sf || !page_table || !seqlens || !out_bf16 || !lse)
+    return QSA_ERR_INVALID_ARG;
+  if (window < 0) return QSA_ERR_INVALID_ARG;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_sf, 16) || !aligned(v_sf, 16) ||
+      !aligned(q_bf16, 16) || !aligned(out_bf16, 16))
+    return QSA_ERR_INVALID_ARG;
+  if (!positive(k_scale) || !positive(sm_scale) || !isfinite(v_scale)) return QSA_ERR_INVALID_ARG;
+  const Geom g = to_geom(geom);
+  if (!workspace || workspace_bytes < qsa::dense_workspace_bytes(g) || !aligned(workspace, 256))
+    return QSA_ERR_WORKSPACE;
+  st = check_device();
+  if (st != QSA_OK) return st;
+  qsa::DenseArgs a = {};
+  a.q = q_bf16;
+  a.k_pool = k_pool; a.k_sf = k_sf; a.v_pool = v_pool; a.v_sf = v_sf;
+  a.k_scale = k_scale; a.v_scale = v_scale; a.sm_scale = sm_scale;
+  a.page_table = page_table; a.seqlens = seqlens;
+  a.window = window; a.sinks = sinks;
+  a.out = out_bf16; a.lse = lse; a.workspace = workspace;
+  return from_cuda(qsa::launch_dense(g, a, stream));
 }
 
 int qsa_select_sparse_decode_fused(const qsa_geom_t* geom) {

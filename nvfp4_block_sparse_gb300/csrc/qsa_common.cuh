@@ -172,6 +172,44 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
+      "cvt.u32.u8 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return r;   // low nibble: lo, high nibble: hi
+}
+
+__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(r) : "f"(x));
+  return r & 0xFFu;
+}
+
+__device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
+  const uint32_t h2 = e4m3x2_to_f16x2(b & 0xFFu);
+  return __half2float(__ushort_as_half((unsigned short)(h2 & 0xFFFFu)));
+}
+
+// One e2m1 pair (the low byte of w) to two fp16 values, low nibble in the low half.
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+
+// A nibble whose magnitude bits are zero is stored as +0.
+__device__ __forceinline__ uint32_t canon_zero(uint32_t byte) {
+  if ((byte & 0x07u) == 0) byte &= 0xF0u;
+  if ((byte & 0x70u) == 0) byte &= 0x0Fu;
+  return byte;
+}
+
 // ---------------------------------------------------------------------------
 // Warp-level MMA and fragment transpose
 // ---------------------------------------------------------------------------
@@ -242,6 +280,50 @@ cudaError_t launch_select_topk(const Geom& g, const int32_t* scores, const int32
                                int k, int window, int32_t* sel, int32_t* nsel, bool pdl,
                                cudaStream_t stream);
 
+// The step's rotation rows, head norms with the rotation, and cache rows read
+// back (qsa_prologue.cu).  `rows` of q, k and v are row strides in elements.
+struct NormRope {
+  int rot;            // rotated dims (0: none)
+  int interleaved;    // pairs (2i, 2i + 1) instead of (i, i + rot / 2)
+  int plus_one;       // the norms' weights are 1 + w
+  float eps;
+};
+struct PrologueArgs {
+  const __nv_bfloat16 *q, *k, *v;           // q may be null; v null: norms only
+  long long q_stride, k_stride, v_stride;
+  const int8_t* ik;
+  const __nv_bfloat16 *q_weight, *k_weight; // null: no norm
+  const float* cs;                          // [T][rot / 2][2]
+  float k_scale, v_scale;
+  const int32_t *page_table, *seqlens;
+  __nv_bfloat16 *q_out, *k_out;             // k_out: norms only
+  uint8_t *k_pool, *k_sf, *v_pool, *v_sf;
+  int8_t* ik_pool;
+};
+cudaError_t launch_rope_rows(const Geom& g, const qsa_rope_t& rope, const int32_t* seqlens,
+                             const int32_t* positions, float* cs, bool pdl, cudaStream_t stream);
+cudaError_t launch_prologue(const Geom& g, const NormRope& nr, const PrologueArgs& a, bool pdl,
+                            cudaStream_t stream);
+cudaError_t launch_load_tokens(const Geom& g, const int32_t* page_table, const int32_t* seqlens,
+                               const uint8_t* k_pool, const uint8_t* k_sf, const uint8_t* v_pool,
+                               const uint8_t* v_sf, float k_scale, float v_scale, void* k_out,
+                               void* v_out, bool pdl, cudaStream_t stream);
+
+// Dense attention (qsa_dense.cu): the workspace's bytes and the launches.
+struct DenseArgs {
+  const void* q;
+  const uint8_t *k_pool, *k_sf, *v_pool, *v_sf;
+  float k_scale, v_scale, sm_scale;
+  const int32_t *page_table, *seqlens;
+  int window;                // tokens a row looks back over, itself included; 0: all
+  const float* sinks;        // [Hq], or null
+  void* out;
+  float* lse;
+  void* workspace;
+};
+size_t dense_workspace_bytes(const Geom& g);
+cudaError_t launch_dense(const Geom& g, const DenseArgs& a, cudaStream_t stream);
+
 struct DecodePlan {
   int splits;        // KV splits per (request, KV head, query group)
   int qgroups;       // query-column groups per (request, KV head)
@@ -261,6 +343,8 @@ int bounds_word_select();
 int bounds_word_store();
 int bounds_word_rollback();
 int bounds_word_prefill();
+int bounds_word_prologue();
+int bounds_word_dense();
 #endif
 
 // Bound of the attention kernels' waits for their chunk copies, in ns

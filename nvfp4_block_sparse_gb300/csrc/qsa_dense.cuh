@@ -1,0 +1,153 @@
+// qsa_dense.cuh -- what the two dense attention kernels share: the units of
+// work, their even division over the CTAs, and the records of a unit that is
+// divided between CTAs.
+//
+// A unit is (request b, tile t of its query vectors, KV head).  The R*G query
+// vectors of a request and KV head are numbered row j, head h -> j*G + h; tile
+// t holds vectors [t*VT, (t+1)*VT).  A unit walks the chunks of TOK tokens from
+// the first token that its first row sees to the last that its last row sees;
+// one with no token has one chunk all the same, so that somebody writes its
+// zeros.  The units' chunks, one behind the other, are divided evenly over the
+// CTAs of the grid by the requests' actual lengths: CTA i takes chunks
+// [i*share, (i+1)*share).  So every CTA ends at about the same time whatever
+// the lengths, and a single long request still uses the whole GPU.
+//
+// A unit inside one CTA is written out by it.  A unit that crosses CTAs leaves
+// a record (base, sum, unscaled output per vector) from each of them: in slot 1
+// of the CTA where it begins, in slot 0 of the others.  The CTA where it ends
+// names it in its descriptor, and a second kernel joins the records in the
+// CTAs' order, whatever order they ended in.
+#pragma once
+
+#include "qsa_common.cuh"
+
+namespace qsa {
+namespace dense {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// The softmax base before a vector has seen a token: low enough for every
+// logit to move it, finite so that differences with -inf stay -inf.
+constexpr float kNoBase = -1e30f;
+constexpr float kLazy = 8.f;       // log2-domain headroom of the softmax base
+
+struct Shape {
+  Geom g;
+  int G;         // query heads per KV head
+  int vt;        // query vectors per tile
+  int tiles;     // tiles per request
+  int tok;       // tokens per chunk
+  int window;    // tokens a row looks back over; 0: all
+  int least;     // chunks a CTA takes at least
+};
+
+// One unit's descriptor, written by the CTA where a divided unit ends.
+struct Desc {
+  int b, tile, kvh;   // b < 0: nothing to join
+  int first;          // CTA where the unit begins
+};
+
+struct Work {
+  const __nv_bfloat16* q;
+  const uint8_t *k_pool, *k_sf, *v_pool, *v_sf;
+  float k_scale, v_scale, sm_scale;
+  const int32_t *page_table, *seqlens;
+  const float* sinks;
+  __nv_bfloat16* out;
+  float* lse;
+  int* status;
+  Desc* desc;        // [CTAs]
+  float* records;    // [CTAs][2][vt][2 + D]: bases, sums, outputs
+};
+
+__host__ __device__ __forceinline__ size_t record_floats(int vt, int D) {
+  return (size_t)vt * (2 + D);
+}
+
+__device__ __forceinline__ int first_seen(int n, int window) {
+  return window > 0 && n > window ? n - window : 0;
+}
+
+// Chunks [x, y) of (request of length L, tile); x == y: no token.
+__device__ __forceinline__ int2 chunk_range(const Shape& s, int L, int tile) {
+  const int cap = s.g.MB * s.g.P;
+  const int v0 = tile * s.vt, v1 = min(v0 + s.vt, s.g.R * s.G);
+  const int hi = visible_tokens(L, s.g.R, (v1 - 1) / s.G, cap);
+  const int lo = first_seen(visible_tokens(L, s.g.R, v0 / s.G, cap), s.window);
+  if (hi <= lo) return make_int2(0, 0);
+  return make_int2(lo / s.tok, (hi + s.tok - 1) / s.tok);
+}
+
+__device__ __forceinline__ int chunk_count(const Shape& s, const int32_t* seqlens, int group) {
+  const int2 r = chunk_range(s, seqlens[group / s.tiles], group % s.tiles);
+  return max(1, r.y - r.x);
+}
+
+// This CTA's part of the work, in the groups (request, tile) in order, each
+// with Hkv units.  Called by all NTHR threads.
+struct Span {
+  long long begin, end;   // global chunks
+  long long share;
+  int group;              // group of `begin`
+  long long group_at;     // global chunk where that group begins
+};
+
+template <int NTHR>
+__device__ __forceinline__ Span plan_span(const Shape& s, const int32_t* seqlens, int cta,
+                                          int ctas) {
+  __shared__ long long s_warp[NTHR / 32];
+  __shared__ long long s_at;
+  __shared__ int s_group;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int groups = s.g.B * s.tiles;
+  const int per = (groups + NTHR - 1) / NTHR;
+  const int g0 = min(groups, tid * per), g1 = min(groups, g0 + per);
+  long long mine = 0;
+  for (int i = g0; i < g1; ++i) mine += chunk_count(s, seqlens, i);
+  long long x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  long long before = x - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < NTHR / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  const int hkv = s.g.Hkv;
+  total *= hkv;
+  before *= hkv;
+  Span span;
+  span.share = (total + ctas - 1) / ctas;
+  if (span.share < s.least) span.share = s.least;
+  span.begin = span.share * cta;
+  span.end = min(total, span.begin + span.share);
+  if (span.begin < span.end && before <= span.begin && span.begin < before + mine * hkv) {
+    long long at = before;
+    int i = g0;
+    for (; i < g1 - 1; ++i) {
+      const long long c = (long long)chunk_count(s, seqlens, i) * hkv;
+      if (span.begin < at + c) break;
+      at += c;
+    }
+    s_at = at;
+    s_group = i;
+  }
+  __syncthreads();
+  span.group = s_group;
+  span.group_at = s_at;
+  return span;
+}
+
+}  // namespace dense
+
+cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, int ctas,
+                              cudaStream_t stream);
+// The workspace's parts: status word, descriptors, records.
+size_t dense_carve(const dense::Shape& s, int ctas, void* workspace, dense::Work* w);
+
+}  // namespace qsa

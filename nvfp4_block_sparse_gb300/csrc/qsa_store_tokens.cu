@@ -32,34 +32,6 @@ constexpr int kWarpsPerCta = 8;
 // Bounds-check code (reported by bounds-checked builds only): pool row out of range.
 [[maybe_unused]] constexpr int kChkRow = 0x501;
 
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
-      "cvt.u32.u8 %0, t;\n\t}"
-      : "=r"(r)
-      : "f"(lo), "f"(hi));
-  return r;   // low nibble: lo, high nibble: hi
-}
-
-__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(r) : "f"(x));
-  return r & 0xFFu;
-}
-
-__device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
-  const uint32_t h2 = e4m3x2_to_f16x2(b & 0xFFu);
-  return __half2float(__ushort_as_half((unsigned short)(h2 & 0xFFFFu)));
-}
-
-// A nibble whose magnitude bits are zero is stored as +0.
-__device__ __forceinline__ uint32_t canon_zero(uint32_t byte) {
-  if ((byte & 0x07u) == 0) byte &= 0xF0u;
-  if ((byte & 0x70u) == 0) byte &= 0x0Fu;
-  return byte;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kWarpsPerCta * 32)
 store_tokens_kernel(Geom g, const __nv_bfloat16* __restrict__ k_new,
