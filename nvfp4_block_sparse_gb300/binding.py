@@ -396,58 +396,76 @@ def qsa_workspace_status(workspace, stream=None) -> int:
 
 
 # ---------------------------------------------------------------------------
-# The calls below check that every tensor is on one device and make that device
-# current for the launch; `stream` defaults to its current stream.
+# The calls below check every tensor's type, size, layout and device, make that
+# device current for the launch, and default to its current stream.  A decode
+# step makes one such call per layer, so the checks cost what they must: one
+# pass of tensor queries, and the reason for a refusal only when there is one.
 # ---------------------------------------------------------------------------
 
-class _On:
-    """Pointers of one call's tensors, all on one CUDA device."""
-
-    __slots__ = ("device",)
-
-    def __init__(self):
-        self.device = -1
-
-    def __call__(self, t, dtype, name, numel, rows=False):
-        """Pointer of ``t`` (None stays NULL); ``rows``: a [T, heads, D] view whose rows may be
-        further apart, else contiguous."""
-        if t is None:
-            return None
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a torch tensor" % name)
-        if not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % name)
-        if t.dtype is not dtype:
-            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-        if t.numel() < numel:
-            raise ValueError("%s has %d elements, needs %d" % (name, t.numel(), numel))
-        if rows:
-            if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-                raise ValueError("%s must be [rows, heads, dims] with its heads behind one another"
-                                 % name)
-        elif not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        d = t.get_device()
-        if d != self.device:
-            if self.device >= 0:
-                raise ValueError("%s is on another device than the tensors before it" % name)
-            self.device = d
-        return t.data_ptr()
-
-    def call(self, fn, args, stream):
-        name = fn.__name__
-        if self.device == torch.cuda.current_device():
-            st = fn(*args, _stream(stream))
-        else:
-            with torch.cuda.device(self.device):
-                st = fn(*args, _stream(stream))
-        if st != QSA_OK:
-            _check(name, st)
+_BF16, _F32, _I32, _U8, _I8 = (torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.int8)
 
 
-def _row_stride(t, heads):
-    """Elements between two rows of a [T, heads, D] view."""
-    return t.stride(0) if t.shape[0] > 1 else heads * t.shape[2]
+def _refuse(t, dtype, name, numel, dev):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s is on device %d, other tensors on %d" % (name, t.get_device(), dev))
+    if t.numel() < numel:
+        raise ValueError("%s has %d elements, needs %d" % (name, t.numel(), numel))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _device(t, name):
+    """The CUDA device of a call's first tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return dev
+
+
+def _at(t, dtype, name, numel, dev):
+    """Pointer of a contiguous tensor of at least ``numel`` elements on device ``dev``."""
+    try:
+        if (t.dtype is dtype and t.get_device() == dev and t.numel() >= numel
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, name, numel, dev)
+
+
+def _rows_at(t, heads, dims, name, rows, dev):
+    """Pointer and row stride of [rows, heads, dims] bf16 rows whose heads are behind one another."""
+    _device(t, name)
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        _refuse(t, _BF16, name, 0, dev)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] < rows or shape[1] != heads or shape[2] != dims:
+        raise ValueError("%s must be [%d, %d, %d], got %s" % (name, rows, heads, dims, list(shape)))
+    if stride[2] != 1 or (heads > 1 and stride[1] != dims):
+        raise ValueError("%s must have its heads behind one another" % name)
+    return t.data_ptr(), stride[0] if rows > 1 else heads * dims
+
+
+def _launch(fn, dev, stream, args):
+    """One library call on device ``dev``, on ``stream`` or the device's current one."""
+    here = torch._C._cuda_getDevice()
+    if dev != here:
+        with torch.cuda.device(dev):
+            return _launch(fn, dev, stream, args)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    st = fn(*args, raw)
+    if st:
+        _check(fn.__name__, st)
 
 
 def make_rope(rotary_dim, theta, scaling="none", factor=1.0, original_context=0.0, beta_fast=32.0,
@@ -471,44 +489,33 @@ def make_norm_rope(rotary_dim, interleaved=False, eps=1e-6, weight_plus_one=Fals
 
 
 def qsa_rope_rows(geom, rope, seqlens, cs, positions=None, stream=None):
-    g, on = _geom(geom), _On()
-    T = g.batch * g.rows_per_req
-    args = [ctypes.byref(g), ctypes.byref(rope), on(seqlens, torch.int32, "seqlens", g.batch),
-            on(positions, torch.int32, "positions", T),
-            on(cs, torch.float32, "cs", T * rope.rotary_dim)]
-    on.call(load().qsa_rope_rows, args, stream)
-
-
-def _qk_args(g, nr, on, q, k, q_weight, k_weight, cs, q_out):
-    T, D = g.batch * g.rows_per_req, g.head_dim
-    nq, nk = T * g.num_q_heads * D, T * g.num_kv_heads * D
-    if q is not None and q.shape[1:] != (g.num_q_heads, D):
-        raise ValueError("q must be [rows, %d, %d]" % (g.num_q_heads, D))
-    if k.shape[1:] != (g.num_kv_heads, D):
-        raise ValueError("k must be [rows, %d, %d]" % (g.num_kv_heads, D))
-    bf = torch.bfloat16
-    rows = [on(q, bf, "q", nq, True), 0 if q is None else _row_stride(q, g.num_q_heads),
-            on(k, bf, "k", nk, True), _row_stride(k, g.num_kv_heads)]
-    tail = [on(q_weight, bf, "q_weight", D), on(k_weight, bf, "k_weight", D),
-            on(cs, torch.float32, "cs", T * nr.rotary_dim)]
-    return rows, tail, on(q_out, bf, "q_out", nq), nk
+    """The step's rotation rows: cs fp32 [T, rotary_dim / 2, 2] from the lengths, or from
+    ``positions`` int32 [T] (then ``seqlens`` may be None)."""
+    g = _geom(geom)
+    B, T = g.batch, g.batch * g.rows_per_req
+    dev = _device(cs, "cs")
+    _launch(load().qsa_rope_rows, dev, stream, (
+        ctypes.byref(g), ctypes.byref(rope),
+        None if seqlens is None else _at(seqlens, _I32, "seqlens", B, dev),
+        None if positions is None else _at(positions, _I32, "positions", T, dev),
+        _at(cs, _F32, "cs", T * rope.rotary_dim, dev)))
 
 
 def qsa_qk_norm_rope(geom, norm_rope, q, k, q_weight, k_weight, cs, q_out, k_out, stream=None):
     """Norm of every query and key head with its rotation; q [T, Hq, D] and k [T, Hkv, D] may be
-    views into one projection's rows; weights may be None (no norm)."""
-    g, on = _geom(geom), _On()
-    rows, tail, qo, nk = _qk_args(g, norm_rope, on, q, k, q_weight, k_weight, cs, q_out)
-    args = [ctypes.byref(g), ctypes.byref(norm_rope)] + rows + tail + [
-        qo, on(k_out, torch.bfloat16, "k_out", nk)]
-    on.call(load().qsa_qk_norm_rope, args, stream)
-
-
-def _pool_ptrs(g, on, k_pool, k_sf, v_pool, v_sf):
-    n = g.num_pages * g.num_kv_heads * g.page_size * g.head_dim
-    u8 = torch.uint8
-    return [on(k_pool, u8, "k_pool", n // 2), on(k_sf, u8, "k_sf", n // 16),
-            on(v_pool, u8, "v_pool", n // 2), on(v_sf, u8, "v_sf", n // 16)]
+    views into one projection's rows; weights may be None (no norm), q and q_out too."""
+    g = _geom(geom)
+    T, Hq, Hkv, D = g.batch * g.rows_per_req, g.num_q_heads, g.num_kv_heads, g.head_dim
+    dev = _device(k, "k")
+    qp, qs = (None, 0) if q is None else _rows_at(q, Hq, D, "q", T, dev)
+    kp, ks = _rows_at(k, Hkv, D, "k", T, dev)
+    _launch(load().qsa_qk_norm_rope, dev, stream, (
+        ctypes.byref(g), ctypes.byref(norm_rope), qp, qs, kp, ks,
+        None if q_weight is None else _at(q_weight, _BF16, "q_weight", D, dev),
+        None if k_weight is None else _at(k_weight, _BF16, "k_weight", D, dev),
+        None if cs is None else _at(cs, _F32, "cs", T * norm_rope.rotary_dim, dev),
+        None if q_out is None else _at(q_out, _BF16, "q_out", T * Hq * D, dev),
+        _at(k_out, _BF16, "k_out", T * Hkv * D, dev)))
 
 
 def qsa_store_kv_tokens_rope(geom, norm_rope, q, k, v, ik_new, q_weight, k_weight, cs, k_scale,
@@ -516,29 +523,42 @@ def qsa_store_kv_tokens_rope(geom, norm_rope, q, k, v, ik_new, q_weight, k_weigh
                              ik_pool, stream=None):
     """qsa_qk_norm_rope and qsa_store_kv_tokens in one launch; v [T, Hkv, D] as k; q and q_out may
     be None."""
-    g, on = _geom(geom), _On()
-    rows, tail, qo, nk = _qk_args(g, norm_rope, on, q, k, q_weight, k_weight, cs, q_out)
-    if v.shape[1:] != (g.num_kv_heads, g.head_dim):
-        raise ValueError("v must be [rows, %d, %d]" % (g.num_kv_heads, g.head_dim))
-    T, i32 = g.batch * g.rows_per_req, torch.int32
-    args = [ctypes.byref(g), ctypes.byref(norm_rope)] + rows + [
-        on(v, torch.bfloat16, "v", nk, True), _row_stride(v, g.num_kv_heads),
-        on(ik_new, torch.int8, "ik_new", T * 64)] + tail + [
-        k_scale, v_scale, on(page_table, i32, "page_table", g.batch * g.max_blocks),
-        on(seqlens, i32, "seqlens", g.batch), qo] + _pool_ptrs(g, on, k_pool, k_sf, v_pool, v_sf) + [
-        on(ik_pool, torch.int8, "ik_pool", g.num_pages * g.page_size * 64)]
-    on.call(load().qsa_store_kv_tokens_rope, args, stream)
+    g = _geom(geom)
+    B, T, Hq, Hkv, D = (g.batch, g.batch * g.rows_per_req, g.num_q_heads, g.num_kv_heads,
+                        g.head_dim)
+    slots = g.num_pages * g.page_size
+    n = slots * Hkv * D
+    dev = _device(k, "k")
+    qp, qs = (None, 0) if q is None else _rows_at(q, Hq, D, "q", T, dev)
+    kp, ks = _rows_at(k, Hkv, D, "k", T, dev)
+    vp, vs = _rows_at(v, Hkv, D, "v", T, dev)
+    _launch(load().qsa_store_kv_tokens_rope, dev, stream, (
+        ctypes.byref(g), ctypes.byref(norm_rope), qp, qs, kp, ks, vp, vs,
+        _at(ik_new, _I8, "ik_new", T * 64, dev),
+        None if q_weight is None else _at(q_weight, _BF16, "q_weight", D, dev),
+        None if k_weight is None else _at(k_weight, _BF16, "k_weight", D, dev),
+        None if cs is None else _at(cs, _F32, "cs", T * norm_rope.rotary_dim, dev),
+        k_scale, v_scale, _at(page_table, _I32, "page_table", B * g.max_blocks, dev),
+        _at(seqlens, _I32, "seqlens", B, dev),
+        None if q_out is None else _at(q_out, _BF16, "q_out", T * Hq * D, dev),
+        _at(k_pool, _U8, "k_pool", n // 2, dev), _at(k_sf, _U8, "k_sf", n // 16, dev),
+        _at(v_pool, _U8, "v_pool", n // 2, dev), _at(v_sf, _U8, "v_sf", n // 16, dev),
+        _at(ik_pool, _I8, "ik_pool", slots * 64, dev)))
 
 
 def qsa_load_kv_tokens(geom, page_table, seqlens, k_pool, k_sf, v_pool, v_sf, k_scale, v_scale,
                        k_out, v_out, stream=None):
-    g, on = _geom(geom), _On()
-    n, i32 = g.batch * g.rows_per_req * g.num_kv_heads * g.head_dim, torch.int32
-    args = [ctypes.byref(g), on(page_table, i32, "page_table", g.batch * g.max_blocks),
-            on(seqlens, i32, "seqlens", g.batch)] + _pool_ptrs(g, on, k_pool, k_sf, v_pool, v_sf) + [
-            k_scale, v_scale, on(k_out, torch.bfloat16, "k_out", n),
-            on(v_out, torch.bfloat16, "v_out", n)]
-    on.call(load().qsa_load_kv_tokens, args, stream)
+    """The R newest rows of each request's cache as bf16 [T, Hkv, D]."""
+    g = _geom(geom)
+    B, m = g.batch, g.batch * g.rows_per_req * g.num_kv_heads * g.head_dim
+    n = g.num_pages * g.page_size * g.num_kv_heads * g.head_dim
+    dev = _device(k_out, "k_out")
+    _launch(load().qsa_load_kv_tokens, dev, stream, (
+        ctypes.byref(g), _at(page_table, _I32, "page_table", B * g.max_blocks, dev),
+        _at(seqlens, _I32, "seqlens", B, dev),
+        _at(k_pool, _U8, "k_pool", n // 2, dev), _at(k_sf, _U8, "k_sf", n // 16, dev),
+        _at(v_pool, _U8, "v_pool", n // 2, dev), _at(v_sf, _U8, "v_sf", n // 16, dev),
+        k_scale, v_scale, _at(k_out, _BF16, "k_out", m, dev), _at(v_out, _BF16, "v_out", m, dev)))
 
 
 def qsa_dense_attention_workspace_bytes(geom) -> int:
@@ -549,13 +569,16 @@ def qsa_dense_attention(geom, q, k_pool, k_sf, v_pool, v_sf, k_scale, v_scale, s
                         seqlens, out, lse, workspace, window=0, sinks=None, stream=None):
     """Dense attention of every row over its request's cached tokens (the newest ``window`` of
     them unless 0), with an optional sink logit per query head."""
-    g, on = _geom(geom), _On()
-    T, i32, f32 = g.batch * g.rows_per_req, torch.int32, torch.float32
-    n = T * g.num_q_heads
-    args = [ctypes.byref(g), on(q, torch.bfloat16, "q", n * g.head_dim)] + _pool_ptrs(
-        g, on, k_pool, k_sf, v_pool, v_sf) + [
-        k_scale, v_scale, sm_scale, on(page_table, i32, "page_table", g.batch * g.max_blocks),
-        on(seqlens, i32, "seqlens", g.batch), int(window), on(sinks, f32, "sinks", g.num_q_heads),
-        on(out, torch.bfloat16, "out", n * g.head_dim), on(lse, f32, "lse", n),
-        on(workspace, torch.uint8, "workspace", 0), workspace.numel()]
-    on.call(load().qsa_dense_attention, args, stream)
+    g = _geom(geom)
+    B, m, D = g.batch, g.batch * g.rows_per_req * g.num_q_heads, g.head_dim
+    n = g.num_pages * g.page_size * g.num_kv_heads * D
+    dev = _device(q, "q")
+    _launch(load().qsa_dense_attention, dev, stream, (
+        ctypes.byref(g), _at(q, _BF16, "q", m * D, dev),
+        _at(k_pool, _U8, "k_pool", n // 2, dev), _at(k_sf, _U8, "k_sf", n // 16, dev),
+        _at(v_pool, _U8, "v_pool", n // 2, dev), _at(v_sf, _U8, "v_sf", n // 16, dev),
+        k_scale, v_scale, sm_scale, _at(page_table, _I32, "page_table", B * g.max_blocks, dev),
+        _at(seqlens, _I32, "seqlens", B, dev), window,
+        None if sinks is None else _at(sinks, _F32, "sinks", g.num_q_heads, dev),
+        _at(out, _BF16, "out", m * D, dev), _at(lse, _F32, "lse", m, dev),
+        _at(workspace, _U8, "workspace", 0, dev), workspace.numel()))
