@@ -163,7 +163,8 @@ int qsa_debug_bounds_status(void) {
   int first = 0;
   for (int v : {qsa::bounds_word_attend(), qsa::bounds_word_decode(), qsa::bounds_word_index(),
                 qsa::bounds_word_select(), qsa::bounds_word_store(), qsa::bounds_word_rollback(),
-                qsa::bounds_word_prefill(), qsa::bounds_word_prologue(), qsa::bounds_word_dense()}) {
+                qsa::bounds_word_prefill(), qsa::bounds_word_prologue(), qsa::bounds_word_dense(),
+                qsa::bounds_word_dense_tile()}) {
     if (v < 0) return -1;
     if (first == 0) first = v;
   }

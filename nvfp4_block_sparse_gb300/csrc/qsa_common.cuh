@@ -345,6 +345,7 @@ int bounds_word_rollback();
 int bounds_word_prefill();
 int bounds_word_prologue();
 int bounds_word_dense();
+int bounds_word_dense_tile();
 #endif
 
 // Bound of the attention kernels' waits for their chunk copies, in ns

@@ -159,26 +159,14 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
   // (D = 256: four rows per copy, so every other one is four rows on in the swizzle)
   auto c_to = [&](int i) { return (D == 256 && (i & 1) ? c_dst ^ 64u : c_dst) + 512u * i; };
 
-  long long at = span.begin;
-  int group = span.group;
-  long long group_at = span.group_at;
-  while (at < span.end) {
+  Cursor cursor(span);
+  Seg seg;
+  while (cursor.next(sh, p.seqlens, seg)) {
     // ---- the unit and this CTA's chunks of it ---------------------------------
-    const int b = group / sh.tiles, tile = group % sh.tiles;
-    const int L = p.seqlens[b];
-    const int2 range = chunk_range(sh, L, tile);
-    const int count = max(1, range.y - range.x);
-    const long long in_group = at - group_at;
-    const int kvh = (int)(in_group / count);
-    const int c_at = (int)(in_group % count);           // first chunk of the unit here
-    const int todo = (int)min((long long)(count - c_at), span.end - at);
-    const bool begins = c_at == 0, ends = c_at + todo == count;
-    const int cap = g.MB * g.P;
-    const int vec0 = tile * sh.vt, vecs = min(sh.vt, g.R * sh.G - vec0);
-    const int n_all = visible_tokens(L, g.R, (vec0 + vecs - 1) / sh.G, cap);
-    const int n_least = visible_tokens(L, g.R, vec0 / sh.G, cap);
-    const int lo_all = first_seen(n_least, sh.window), lo_most = first_seen(n_all, sh.window);
-    const int chunk0 = range.x + c_at;
+    const int b = seg.b, kvh = seg.kvh, L = seg.L, todo = seg.todo, chunk0 = seg.chunk0;
+    const bool begins = seg.begins, ends = seg.ends;
+    const int vec0 = seg.vec0, vecs = seg.vecs, cap = g.MB * g.P;
+    const int n_all = seg.n_all, n_least = seg.n_least, lo_all = seg.lo_all, lo_most = seg.lo_most;
     const int mine = todo > warp ? (todo - warp + W - 1) / W : 0;   // this warp's chunks
 
     // ---- page ids and copies ---------------------------------------------------
@@ -517,18 +505,13 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
       }
     }
     if (tid == 0 && ends && !begins) {
-      // the unit's first chunk is c_at chunks before `at`
       Desc dsc;
-      dsc.b = b; dsc.tile = tile; dsc.kvh = kvh;
-      dsc.first = (int)((at - c_at) / span.share);
+      dsc.b = b; dsc.tile = seg.tile; dsc.kvh = kvh;
+      // the unit's first chunk is todo + c_at before the cursor
+      dsc.first = (int)((cursor.at - todo - seg.c_at) / span.share);
       p.desc[blockIdx.x] = dsc;
     }
     __syncthreads();
-    at += todo;
-    if (at == group_at + (long long)count * g.Hkv) {
-      group_at = at;
-      ++group;
-    }
   }
 }
 
@@ -726,13 +709,21 @@ cudaError_t launch_decode(const dense::Shape& s, const dense::Work& w, int ctas,
 
 }  // namespace
 
+// The tile kernel (128 or 256 query vectors per unit on tcgen05) takes more
+// query vectors per KV head than the decode kernel's sixteen.
+static bool use_tiles(const Geom& g) { return g.R * (g.Hq / g.Hkv) > 16; }
+
+static dense::Shape dense_shape(const Geom& g, int window) {
+  return use_tiles(g) ? dense_tile_shape(g, window) : decode_shape(g, window);
+}
+
 size_t dense_workspace_bytes(const Geom& g) {
-  return dense_carve(decode_shape(g, 0), dense_sms(), nullptr, nullptr);
+  return dense_carve(dense_shape(g, 0), dense_sms(), nullptr, nullptr);
 }
 
 cudaError_t launch_dense(const Geom& g, const DenseArgs& a, cudaStream_t stream) {
   const int ctas = dense_sms();
-  const dense::Shape s = decode_shape(g, a.window);
+  const dense::Shape s = dense_shape(g, a.window);
   dense::Work w = {};
   w.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
   w.k_pool = a.k_pool; w.k_sf = a.k_sf; w.v_pool = a.v_pool; w.v_sf = a.v_sf;
@@ -743,7 +734,9 @@ cudaError_t launch_dense(const Geom& g, const DenseArgs& a, cudaStream_t stream)
   w.lse = a.lse;
   dense_carve(s, ctas, a.workspace, &w);
   cudaError_t e;
-  if (g.D == 128)
+  if (use_tiles(g))
+    e = launch_dense_tile(s, w, ctas, stream);
+  else if (g.D == 128)
     e = s.vt == 8 ? launch_decode<C128a>(s, w, ctas, stream) : launch_decode<C128b>(s, w, ctas, stream);
   else
     e = s.vt == 8 ? launch_decode<C256a>(s, w, ctas, stream) : launch_decode<C256b>(s, w, ctas, stream);

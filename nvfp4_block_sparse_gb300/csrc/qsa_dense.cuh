@@ -143,8 +143,60 @@ __device__ __forceinline__ Span plan_span(const Shape& s, const int32_t* seqlens
   return span;
 }
 
+// The part of one unit that a CTA does.
+struct Seg {
+  int b, tile, kvh;
+  int c_at, todo;            // chunks of the unit before this part, and in it
+  bool begins, ends;         // the part holds the unit's first / last chunk
+  int chunk0;                // first chunk (token chunk0 * tok)
+  int L;
+  int vec0, vecs;            // query vectors of the unit
+  int n_all, n_least;        // tokens that the last / first row sees
+  int lo_all, lo_most;       // first token that the first / last row sees
+};
+
+// Walks a span's parts in order; every role of a CTA walks its own copy.
+struct Cursor {
+  long long at, end, group_at;
+  int group;
+  __device__ __forceinline__ explicit Cursor(const Span& s)
+      : at(s.begin), end(s.end), group_at(s.group_at), group(s.group) {}
+  __device__ __forceinline__ bool next(const Shape& s, const int32_t* seqlens, Seg& g) {
+    if (at >= end) return false;
+    g.b = group / s.tiles;
+    g.tile = group % s.tiles;
+    g.L = seqlens[g.b];
+    const int2 range = chunk_range(s, g.L, g.tile);
+    const int count = max(1, range.y - range.x);
+    const long long in_group = at - group_at;
+    g.kvh = (int)(in_group / count);
+    g.c_at = (int)(in_group % count);
+    g.todo = (int)min((long long)(count - g.c_at), end - at);
+    g.begins = g.c_at == 0;
+    g.ends = g.c_at + g.todo == count;
+    g.chunk0 = range.x + g.c_at;
+    const int cap = s.g.MB * s.g.P;
+    g.vec0 = g.tile * s.vt;
+    g.vecs = min(s.vt, s.g.R * s.G - g.vec0);
+    g.n_all = visible_tokens(g.L, s.g.R, (g.vec0 + g.vecs - 1) / s.G, cap);
+    g.n_least = visible_tokens(g.L, s.g.R, g.vec0 / s.G, cap);
+    g.lo_all = first_seen(g.n_least, s.window);
+    g.lo_most = first_seen(g.n_all, s.window);
+    at += g.todo;
+    if (at == group_at + (long long)count * s.g.Hkv) {
+      group_at = at;
+      ++group;
+    }
+    return true;
+  }
+};
+
 }  // namespace dense
 
+// The tile kernel (qsa_dense_tile.cu): its units for this geometry, and its launch.
+dense::Shape dense_tile_shape(const Geom& g, int window);
+cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, int ctas,
+                              cudaStream_t stream);
 cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, int ctas,
                               cudaStream_t stream);
 // The workspace's parts: status word, descriptors, records.

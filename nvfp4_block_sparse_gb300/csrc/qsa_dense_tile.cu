@@ -1,0 +1,643 @@
+// qsa_dense_tile.cu -- dense attention over the NVFP4 paged cache for many
+// query vectors per KV head (context row groups, wide verify rows), on the
+// fifth-generation tensor cores.
+//
+// TensorRT-LLM PR #20276 ("Qwen3.8-Flash-Next NVFP4 target"), Performance:
+// context rows run on tcgen05 with K/V tiles shared by a group of rows; Known
+// limitations: context rows read the NVFP4 pages dequantised on the way.
+//
+// A CTA takes tiles of 128 query vectors (row, head) of one request and KV
+// head: two tiles at head_dim 128, one at 256, which share every dequantised
+// chunk (128 tokens, 64 at head_dim 256).  4 D flops per (vector, token): the
+// tensor core bounds the work, at 128 x 128 x D fp16 products per chunk and tile for
+// each of
+//   S = Q K^T    A = Q, B = K from shared memory (K-major), D = S in tensor memory
+//   O += P V     A = P from tensor memory, B = V from shared memory (token rows, MN-major)
+//
+// Roles (one CTA per SM, one warp group each unless noted):
+//   softmax   a thread per vector (tensor-memory lane): its row of S to registers, base
+//             (moved only when the maximum grows by more than 2^8), P = exp2(S c - base) as
+//             fp16 over the columns of S it has read, sums in fp32; at the end
+//             of a part O from tensor memory to the output or to a record
+//   dequant   codes and scales from the pages straight to registers one chunk ahead (they
+//             are in flight while the chunk before is converted), e2m1 x e4m3 exact in
+//             fp16 into double-buffered K and V tiles (128-byte swizzle)
+//   MMA       one warp issues every MMA in order.  At head_dim 128 the tiles take
+//             turns: O_0, S_0 of the next chunk, O_1, S_1, so that one tile's softmax
+//             runs under the other's products.  At head_dim 256 S has two buffers
+//             and runs two chunks ahead.
+// P lies over S: S of the next chunk is issued behind the O that reads P, and
+// MMAs of one thread run in order, so no barrier guards the reuse.
+//
+// Tensor memory (512 columns): the S buffers from column 0, O from 256.
+// mbarriers, all waits bounded (2 s; a wait that gives up sets the status word):
+//   qready        Q tiles written; O, S of the part before read    (softmax threads)
+//   kready/vready[x]  K / V tile x written                         (its 128 converting threads)
+//   kfree/vfree[x]    MMAs that read tile x complete               (commit)
+//   barS[y]       S buffer y complete -- and, at head_dim 128, every MMA before it,
+//                 so also the tile's O so far; once more after a part's last O   (commit)
+//   barO          O complete (head_dim 256)                        (commit)
+//   pready[y][h]  half h of P in buffer y written                  (128 softmax threads)
+#include "qsa_dense.cuh"
+#include "qsa_tc.cuh"
+
+namespace qsa {
+namespace dense {
+namespace {
+
+using namespace tc;
+
+// Bounds-check codes (reported by bounds-checked builds only).
+[[maybe_unused]] constexpr int kChkChunk = 0xA01;   // chunk: token block past the page table
+[[maybe_unused]] constexpr int kChkOut = 0xA02;     // output row out of range
+
+template <int D_>
+struct TT {
+  static constexpr int D = D_;
+  static constexpr int kTiles = D == 128 ? 2 : 1;        // query tiles of a CTA
+  static constexpr int kTok = D == 128 ? 128 : 64;       // tokens per chunk
+  static constexpr int kHalves = kTok / 64;              // P is written 64 tokens at a time
+  static constexpr int kSoft = 4 * kTiles;               // softmax warps
+  static constexpr int kDeq = D == 128 ? 4 : 8;          // dequantisation warps
+  static constexpr int kMma = kSoft + kDeq;              // the MMA warp; its group's others idle
+  static constexpr int kThreads = 512;
+  // Registers per thread after the roles part (of 512 x 128 at launch).
+  static constexpr int kSoftRegs = D == 128 ? 160 : 184;
+  static constexpr int kDeqRegs = 112;
+  static constexpr int kMmaRegs = 80;
+  static_assert(32 * (kSoft * kSoftRegs + kDeq * kDeqRegs + 4 * kMmaRegs) <= 512 * 128, "registers");
+  static constexpr int kQBytes = 128 * D * 2;            // Q: D/64 blocks of 128 rows x 128 B
+  static constexpr int kBlk = kTok * 128;                // one 64-dim block of a K or V tile
+  static constexpr int kKV = (D / 64) * kBlk;            // 32 KB
+  static constexpr int kBars = 17;
+  static constexpr int kSmem = 1024 + kTiles * kQBytes + 4 * kKV + kBars * 8 + 24;
+  static constexpr uint32_t kOCol = 256;
+};
+
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ uint4 ldg128(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t ldg16(const void* p) {
+  uint16_t r;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
+  return r;
+}
+
+// Two fp32 multiply-adds / additions at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A warp's bounded wait: true when it gave up, in every lane.
+__device__ __forceinline__ bool gave_up(uint64_t* bar, uint32_t parity) {
+  return __any_sync(0xffffffffu, !wait_bounded(bar, parity & 1));
+}
+
+template <int D>
+__global__ void __launch_bounds__(TT<D>::kThreads, 1)
+dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work p) {
+  using T = TT<D>;
+  constexpr int kTok = T::kTok, kTiles = T::kTiles;
+  const Geom& g = sh.g;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;                                   // [kTiles][kQBytes]
+  uint8_t* sK = sQ + kTiles * T::kQBytes;               // [2][kKV]
+  uint8_t* sV = sK + 2 * T::kKV;                        // [2][kKV]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + 2 * T::kKV);
+  uint64_t* kready = bars;
+  uint64_t* vready = bars + 2;
+  uint64_t* kfree = bars + 4;
+  uint64_t* vfree = bars + 6;
+  uint64_t* barS = bars + 8;
+  uint64_t* pready = bars + 10;      // [buffer][half]
+  uint64_t* barO = bars + 14;
+  uint64_t* qready = bars + 15;
+  uint64_t* mdone = bars + 16;       // after a give-up: every MMA issued has completed
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + T::kBars);
+
+  if (tid == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&kready[x], 128);
+      mbar_init(&vready[x], 128);
+      mbar_init(&kfree[x], 1);
+      mbar_init(&vfree[x], 1);
+      mbar_init(&barS[x], 1);
+      mbar_init(&pready[2 * x], 128);
+      mbar_init(&pready[2 * x + 1], 128);
+    }
+    mbar_init(barO, 1);
+    mbar_init(mdone, 1);
+    mbar_init(qready, 32 * T::kSoft);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(s_tmem)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  const Span span = plan_span<T::kThreads>(sh, p.seqlens, blockIdx.x, gridDim.x);
+  pdl_trigger();
+  if (tid == 0) p.desc[blockIdx.x].b = -1;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  bool dead = false;
+  Cursor cursor(span);
+  Seg seg;
+
+  if (warp < T::kSoft) {
+    // ==== softmax ==================================================================
+    regs_up<T::kSoftRegs>();
+    const int t = warp >> 2, row = tid & 127;
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tO = tmem + T::kOCol + t * D + lane_off;
+    uint8_t* q_tile = sQ + t * T::kQBytes;
+    int chunks = 0, s_waits = 0;   // chunks so far; waits on barS (head_dim 128)
+    while (!dead && cursor.next(sh, p.seqlens, seg)) {
+      // this thread's vector, its Q row as fp16 scaled by a power of two into [256, 512)
+      const int vec = seg.vec0 + t * 128 + row;
+      const bool real = t * 128 + row < seg.vecs;
+      const int j = real ? vec / sh.G : 0, head = seg.kvh * sh.G + (real ? vec % sh.G : 0);
+      const size_t orow = ((size_t)seg.b * g.R + j) * g.Hq + head;
+      const int n = real ? visible_tokens(seg.L, g.R, j, g.MB * g.P) : 0;
+      const int lo = first_seen(n, sh.window);
+      float cq = 1.f;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * D);
+        float amax = 0.f;
+        if (real) {
+#pragma unroll 8
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 r = src[i];
+            const uint32_t w4[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              amax = fmax3(amax, fabsf(__uint_as_float(w4[u] << 16)),
+                           fabsf(__uint_as_float(w4[u] & 0xFFFF0000u)));
+          }
+        }
+        const int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
+        int sq = (amax > 0.f) ? 135 - ebits : 0;
+        sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
+        const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
+        const float down = __uint_as_float((uint32_t)(127 - sq) << 23);
+        if (real) cq = p.k_scale * p.sm_scale * kLog2e * down;
+#pragma unroll 8
+        for (int i = 0; i < D / 8; ++i) {
+          uint4 h = make_uint4(0u, 0u, 0u, 0u);
+          if (real) {
+            const uint4 r = src[i];
+            const uint32_t w4[4] = {r.x, r.y, r.z, r.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              o[u] = pack_half2(__uint_as_float(w4[u] << 16) * up,
+                                __uint_as_float(w4[u] & 0xFFFF0000u) * up);
+            h = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          *reinterpret_cast<uint4*>(q_tile + (i >> 3) * 16384 + sw128(row, i & 7)) = h;
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      ws_arrive(qready);
+
+      // pages of a chunk that are there: one bit per 32 tokens
+      auto live_of = [&](int chunk) {
+        const int tok = chunk * kTok + 32 * lane, beta = tok / g.P;
+        bool ok = false;
+        if (lane < kTok / 32 && beta < g.MB) {
+          const int page = __ldg(p.page_table + (size_t)seg.b * g.MB + beta);
+          ok = page >= 0 && page < g.NP;
+        }
+        return __ballot_sync(0xffffffffu, ok);
+      };
+      float base = kNoBase;
+      float2 sum = make_float2(0.f, 0.f);
+      uint32_t live = live_of(seg.chunk0);
+      for (int c = 0; c < seg.todo; ++c, ++chunks) {
+        const int y = kTiles == 2 ? t : chunks & 1;      // S buffer
+        const uint32_t tS = tmem + y * kTok + lane_off;
+        const uint32_t now_live = live;
+        if (c + 1 < seg.todo) live = live_of(seg.chunk0 + c + 1);
+        if (gave_up(&barS[y], kTiles == 2 ? s_waits : chunks >> 1)) { dead = true; break; }
+        ++s_waits;
+        tc_fence_after();
+        const int tok0 = (seg.chunk0 + c) * kTok;
+        const bool edge = tok0 + kTok > seg.n_least || tok0 < seg.lo_most ||
+                          now_live != (1u << (kTok / 32)) - 1u;
+        float z[64];
+        auto load = [&](int h) {       // 64 tokens of S, what the row does not see at -inf
+          tmem_ld32(tS + 64 * h, z);
+          tmem_ld32(tS + 64 * h + 32, z + 32);
+          tmem_wait_ld();
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+              const int tok = tok0 + 64 * h + i;
+              if (tok >= n || tok < lo || !((now_live >> (2 * h + (i >> 5))) & 1u)) z[i] = -INFINITY;
+            }
+          }
+        };
+        auto largest = [&]() {
+          float m8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m8[i] = z[i];
+#pragma unroll
+          for (int i = 8; i < 64; i += 2) m8[(i >> 1) & 7] = fmax3(m8[(i >> 1) & 7], z[i], z[i + 1]);
+          return fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        };
+        // The base needs the whole chunk's maximum; the last half stays in
+        // registers, the first is read again.
+        load(0);
+        float top = largest();
+        if (T::kHalves == 2) {
+          load(1);
+          top = fmaxf(top, largest());
+        }
+        top *= cq;
+        const bool moves = top > base + kLazy;
+        if (__any_sync(0xffffffffu, moves)) {
+          const float nb = moves ? top : base;
+          const float alpha = exp2_approx(base - nb);
+          base = nb;
+          sum.x *= alpha;
+          sum.y *= alpha;
+          if (c > 0) {
+            // O so far is complete: at head_dim 128 barS says so too
+            if (kTiles == 1 && gave_up(barO, chunks - 1)) { dead = true; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              float o16[16];
+              tmem_ld16(tO + 16 * i, o16);
+              tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 16; ++u) o16[u] *= alpha;
+              tmem_st16(tO + 16 * i, o16);
+            }
+            tmem_wait_st();
+          }
+        }
+        auto weights = [&](int h) {    // P of half h, over the columns it was read from
+          const float2 c2 = make_float2(cq, cq), b2 = make_float2(-base, -base);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 a = fma2(make_float2(z[32 * q + 2 * i], z[32 * q + 2 * i + 1]), c2, b2);
+              const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
+              sum = add2(sum, e);
+              pk[i] = pack_half2(e.x, e.y);
+            }
+            tmem_st16u(tS + 64 * h + 16 * q, pk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          ws_arrive(&pready[2 * y + h]);
+        };
+        if (T::kHalves == 2) {
+          weights(1);
+          load(0);
+          weights(0);
+        } else {
+          weights(0);
+        }
+      }
+      if (dead) break;
+      // ---- the part's output ---------------------------------------------------------
+      // (head_dim 256: barS of the last chunk says that the O of all but the last two chunks
+      // is complete; a phase is only told from its neighbours, so both are waited for)
+      const bool late = kTiles == 2 ? gave_up(&barS[t], s_waits)
+                                    : ((seg.todo > 1 && gave_up(barO, chunks - 2)) ||
+                                       gave_up(barO, chunks - 1));
+      ++s_waits;
+      if (late) { dead = true; break; }
+      tc_fence_after();
+      float l = sum.x + sum.y, m = base, f = 1.f;
+      const bool whole = seg.begins && seg.ends;
+      if (whole && p.sinks && real) {
+        const float s2 = p.sinks[head] * kLog2e, nm = fmaxf(m, s2);
+        f = exp2_approx(m - nm);
+        l = l * f + exp2_approx(s2 - nm);
+        m = nm;
+      }
+      const float r = whole ? (l > 0.f ? f * p.v_scale / l : 0.f) : 1.f;
+      const bool ok = real && QSA_IN_BOUNDS(seg.b < g.B && j < g.R && head < g.Hq, kChkOut);
+      float* rec = p.records + ((size_t)blockIdx.x * 2 + (seg.begins ? 1 : 0)) * record_floats(sh.vt, D);
+      const int c_rec = t * 128 + row;
+#pragma unroll 2
+      for (int i = 0; i < D / 16; ++i) {
+        float o16[16];
+        tmem_ld16(tO + 16 * i, o16);
+        tmem_wait_ld();
+        if (!ok) continue;
+        if (whole) {
+          uint32_t h[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(o16[2 * u] * r, o16[2 * u + 1] * r);
+            h[u] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 16 * i);
+          dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+          dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(rec + 2 * sh.vt + (size_t)c_rec * D + 16 * i);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            dst[u] = make_float4(o16[4 * u], o16[4 * u + 1], o16[4 * u + 2], o16[4 * u + 3]);
+        }
+      }
+      if (ok) {
+        if (whole) {
+          p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        } else {
+          rec[c_rec] = m;
+          rec[sh.vt + c_rec] = l;
+        }
+      }
+      if (tid == 0 && seg.ends && !seg.begins) {
+        Desc dsc;
+        dsc.b = seg.b; dsc.tile = seg.tile; dsc.kvh = seg.kvh;
+        dsc.first = (int)((cursor.at - seg.todo - seg.c_at) / span.share);
+        p.desc[blockIdx.x] = dsc;
+      }
+    }
+  } else if (warp < T::kMma) {
+    regs_down<T::kDeqRegs>();
+    // ==== dequantisation =============================================================
+    // A 16-byte piece (32 codes, two scales) of eight token rows and four neighbouring
+    // pieces per warp and step: 512 contiguous bytes (256 at a time at head_dim 256), and
+    // the eight lanes that store together hold eight rows, so the swizzle gives them
+    // distinct banks.  At head_dim 256 four warps convert K and four V.
+    const int dw = (warp - T::kSoft) & 3;
+    const bool does_k = T::kDeq == 4 || warp - T::kSoft < 4;
+    const bool does_v = T::kDeq == 4 || !does_k;
+    const int r8 = lane & 7, q = lane >> 3;
+    uint4 kc[4], vc[4];
+    uint32_t ks[4], vs[4];
+    int chunks = 0;
+    while (!dead && cursor.next(sh, p.seqlens, seg)) {
+      const int32_t* pt = p.page_table + (size_t)seg.b * g.MB;
+      auto group_of = [&](int i) { return (dw + 4 * i) % (kTok / 8); };   // 8-token group
+      auto half_of = [&](int i) { return (dw + 4 * i) / (kTok / 8); };    // 128-dim half
+      // the two pages of a chunk (the same one twice where pages are as long)
+      auto pages_of = [&](int chunk, int& pa, int& pb) {
+        const int b0 = chunk * kTok / g.P, b1 = (chunk * kTok + kTok - 1) / g.P;
+        pa = b0 < g.MB && seg.n_all > seg.lo_all ? __ldg(pt + b0) : -1;
+        pb = b1 < g.MB && seg.n_all > seg.lo_all ? __ldg(pt + b1) : -1;
+      };
+      auto fetch = [&](int chunk, int pa, int pb, const uint8_t* pool, const uint8_t* sfs,
+                       uint4 (&codes)[4], uint32_t (&sc)[4]) {
+        const int first = chunk * kTok / g.P;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = chunk * kTok + 8 * group_of(i) + r8;
+          const int page = tok / g.P == first ? pa : pb;
+          codes[i] = make_uint4(0u, 0u, 0u, 0u);
+          sc[i] = 0u;
+          // what no row of the tile sees is not looked at
+          if (page >= 0 && page < g.NP && tok >= seg.lo_all && tok < seg.n_all) {
+            const size_t row = ((size_t)page * g.Hkv + seg.kvh) * g.P + tok % g.P;
+            codes[i] = ldg128(pool + row * (D / 2) + 64 * half_of(i) + 16 * q);
+            sc[i] = ldg16(sfs + row * (D / 16) + 8 * half_of(i) + 2 * q);
+          }
+        }
+      };
+      auto convert = [&](const uint4 (&codes)[4], const uint32_t (&sc)[4], uint8_t* tile) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = 8 * group_of(i) + r8;
+          const uint32_t s2 = e4m3x2_to_f16x2(sc[i]);
+          const uint32_t sx[2] = {prmt(s2, 0, 0x1010), prmt(s2, 0, 0x3232)};
+          const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int piece = 16 * half_of(i) + 4 * q + u;   // 8 dims
+            *reinterpret_cast<uint4*>(tile + (piece >> 3) * T::kBlk + sw128(tok, piece & 7)) =
+                dequant8(w[u], sx[u >> 1]);
+          }
+        }
+      };
+      int pa, pb;
+      pages_of(seg.chunk0, pa, pb);
+      if (does_k) fetch(seg.chunk0, pa, pb, p.k_pool, p.k_sf, kc, ks);
+      if (does_v) fetch(seg.chunk0, pa, pb, p.v_pool, p.v_sf, vc, vs);
+      if (seg.todo > 1) pages_of(seg.chunk0 + 1, pa, pb);
+      for (int c = 0; c < seg.todo; ++c, ++chunks) {
+        const int x = chunks & 1, use = chunks >> 1;
+        const int next = seg.chunk0 + c + 1;
+        const bool more = c + 1 < seg.todo;
+        if (does_k) {
+          if (use > 0 && gave_up(&kfree[x], use - 1)) { dead = true; break; }
+          convert(kc, ks, sK + x * T::kKV);
+          fence_proxy_async_smem();
+          ws_arrive(&kready[x]);
+          if (more) fetch(next, pa, pb, p.k_pool, p.k_sf, kc, ks);
+        }
+        if (does_v) {
+          if (use > 0 && gave_up(&vfree[x], use - 1)) { dead = true; break; }
+          convert(vc, vs, sV + x * T::kKV);
+          fence_proxy_async_smem();
+          ws_arrive(&vready[x]);
+          if (more) fetch(next, pa, pb, p.v_pool, p.v_sf, vc, vs);
+        }
+        if (c + 2 < seg.todo) pages_of(next + 1, pa, pb);
+      }
+    }
+  } else if (regs_down<T::kMmaRegs>(), warp == T::kMma) {
+    // ==== MMA issue ==================================================================
+    const uint32_t id_s = f16_idesc(128, kTok), id_o = f16_idesc(128, D) | kIdescBMn;
+    int s_done = 0, parts = 0;     // chunks whose S was issued in earlier parts; parts
+    auto issue_s = [&](int t, int y, int x) {
+      const uint64_t dq = sw128_desc(smem_u32(sQ + t * T::kQBytes));
+      const uint64_t dk = sw128_desc(smem_u32(sK + x * T::kKV));
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_f16_elect(tmem + y * kTok, dq + (uint64_t)((h * 16384 + 32 * ks) >> 4),
+                        dk + (uint64_t)((h * T::kBlk + 32 * ks) >> 4), id_s, (h | ks) ? 1u : 0u);
+    };
+    auto issue_o = [&](int t, int y, int x, int h, bool first) {   // 64 tokens
+      const uint64_t dv = sw128_mn_desc(smem_u32(sV + x * T::kKV), T::kBlk);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mma_f16_ts_elect(tmem + T::kOCol + t * D, tmem + y * kTok + 64 * h + 8 * ks,
+                         dv + (uint64_t)((8192 * h + 2048 * ks) >> 4), id_o,
+                         (first && ks == 0) ? 0u : 1u);
+    };
+    while (!dead && cursor.next(sh, p.seqlens, seg)) {
+      if (gave_up(qready, parts)) { dead = true; break; }
+      ++parts;
+      tc_fence_after();
+      const int C = seg.todo;
+      auto chunk_s = [&](int c) {   // S of chunk c (head_dim 256), of both tiles' turns below
+        const int n = s_done + c, x = n & 1;
+        if (gave_up(&kready[x], n >> 1)) return false;
+        tc_fence_after();
+        return true;
+      };
+      if constexpr (kTiles == 2) {
+        if (!chunk_s(0)) { dead = true; break; }
+        issue_s(0, 0, s_done & 1);
+        mma_commit_elect(&barS[0]);
+        issue_s(1, 1, s_done & 1);
+        mma_commit_elect(&barS[1]);
+        mma_commit_elect(&kfree[s_done & 1]);
+        for (int c = 0; c < C && !dead; ++c) {
+          const int n = s_done + c, x = n & 1, xn = (n + 1) & 1;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t == 0 && gave_up(&vready[x], n >> 1)) { dead = true; break; }
+            if (gave_up(&pready[2 * t + 1], n)) { dead = true; break; }
+            tc_fence_after();
+            issue_o(t, t, x, 1, c == 0);
+            if (gave_up(&pready[2 * t], n)) { dead = true; break; }
+            tc_fence_after();
+            issue_o(t, t, x, 0, false);
+            if (t == 1) mma_commit_elect(&vfree[x]);
+            if (c + 1 < C) {
+              if (t == 0 && !chunk_s(c + 1)) { dead = true; break; }
+              issue_s(t, t, xn);
+            }
+            mma_commit_elect(&barS[t]);
+            if (t == 1 && c + 1 < C) mma_commit_elect(&kfree[xn]);
+          }
+        }
+      } else {
+        for (int c = 0; c < 2 && c < C; ++c) {
+          const int n = s_done + c;
+          if (!chunk_s(c)) { dead = true; break; }
+          issue_s(0, n & 1, n & 1);
+          mma_commit_elect(&barS[n & 1]);
+          mma_commit_elect(&kfree[n & 1]);
+        }
+        for (int c = 0; c < C && !dead; ++c) {
+          const int n = s_done + c, x = n & 1;
+          if (gave_up(&vready[x], n >> 1) || gave_up(&pready[2 * x], n >> 1)) { dead = true; break; }
+          tc_fence_after();
+          issue_o(0, x, x, 0, c == 0);
+          mma_commit_elect(&vfree[x]);
+          mma_commit_elect(barO);
+          if (c + 2 < C) {
+            if (!chunk_s(c + 2)) { dead = true; break; }
+            issue_s(0, x, x);
+            mma_commit_elect(&barS[x]);
+            mma_commit_elect(&kfree[x]);
+          }
+        }
+      }
+      s_done += C;
+    }
+  }
+
+  // Every MMA has completed where nothing gave up (the softmax waited for the last); after a
+  // give-up, wait for what the MMA warp issued before its memory goes.
+  if (dead) atomicExch(p.status, kStatusWaitTimeout);
+  tc_fence_before();
+  const bool any_dead = __syncthreads_or(dead);
+  tc_fence_after();
+  if (any_dead) {
+    if (warp == T::kMma) mma_commit_elect(mdone);
+    wait_bounded(mdone, 0);
+    __syncthreads();
+  }
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+}  // namespace
+}  // namespace dense
+
+dense::Shape dense_tile_shape(const Geom& g, int window) {
+  dense::Shape s;
+  s.g = g;
+  s.G = g.Hq / g.Hkv;
+  s.vt = 128 * (g.D == 128 ? dense::TT<128>::kTiles : dense::TT<256>::kTiles);
+  s.tiles = (g.R * s.G + s.vt - 1) / s.vt;
+  s.tok = g.D == 128 ? dense::TT<128>::kTok : dense::TT<256>::kTok;
+  s.window = window;
+  s.least = 4;
+  return s;
+}
+
+namespace {
+
+template <int D>
+cudaError_t launch_tile(const dense::Shape& s, const dense::Work& w, int ctas, cudaStream_t stream) {
+  using T = dense::TT<D>;
+  auto* kern = dense::dense_tile_kernel<D>;
+  static_assert(T::kSmem <= 227 * 1024, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(T::kThreads);
+  cfg.dynamicSmemBytes = T::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, s, w);
+}
+
+}  // namespace
+
+cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, int ctas,
+                              cudaStream_t stream) {
+  return s.g.D == 256 ? launch_tile<256>(s, w, ctas, stream) : launch_tile<128>(s, w, ctas, stream);
+}
+
+}  // namespace qsa
+
+QSA_BOUNDS_READER(bounds_word_dense_tile)
