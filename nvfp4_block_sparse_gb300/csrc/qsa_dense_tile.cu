@@ -16,8 +16,9 @@
 //
 // Roles (one CTA per SM, one warp group each unless noted):
 //   softmax   a thread per vector (tensor-memory lane): its row of S to registers, base
-//             (moved only when the maximum grows by more than 2^8), P = exp2(S c - base) as
-//             fp16 over the columns of S it has read, sums in fp32; at the end
+//             (moved only where a weight would overflow), P = exp2(S c - base) as
+//             fp16 over the columns of S it has read, sums in fp32; 64 tokens at a time, so that
+//             no pass over the chunk comes before the exponentials; at the end
 //             of a part O from tensor memory to the output or to a record
 //   dequant   codes and scales from the pages straight to registers one chunk ahead (they
 //             are in flight while the chunk before is converted), e2m1 x e4m3 exact in
@@ -62,9 +63,9 @@ struct TT {
   static constexpr int kMma = kSoft + kDeq;              // the MMA warp; its group's others idle
   static constexpr int kThreads = 512;
   // Registers per thread after the roles part (of 512 x 128 at launch).
-  static constexpr int kSoftRegs = D == 128 ? 160 : 184;
-  static constexpr int kDeqRegs = 112;
-  static constexpr int kMmaRegs = 80;
+  static constexpr int kSoftRegs = D == 128 ? 168 : 184;
+  static constexpr int kDeqRegs = D == 128 ? 104 : 112;
+  static constexpr int kMmaRegs = 72;
   static_assert(32 * (kSoft * kSoftRegs + kDeq * kDeqRegs + 4 * kMmaRegs) <= 512 * 128, "registers");
   static constexpr int kQBytes = 128 * D * 2;            // Q: D/64 blocks of 128 rows x 128 B
   static constexpr int kBlk = kTok * 128;                // one 64-dim block of a K or V tile
@@ -89,6 +90,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+
+// How far (log2) a logit may exceed the base: fp16 weights reach 65504, and as long as
+// every weight is finite its relative precision does not depend on the base.
+constexpr float kHeadroom = 15.f;
 
 __device__ __forceinline__ uint4 ldg128(const void* p) {
   uint4 r;
@@ -292,25 +297,36 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           for (int i = 8; i < 64; i += 2) m8[(i >> 1) & 7] = fmax3(m8[(i >> 1) & 7], z[i], z[i + 1]);
           return fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
         };
-        // The base needs the whole chunk's maximum; the last half stays in
-        // registers, the first is read again.
-        load(0);
-        float top = largest();
-        if (T::kHalves == 2) {
-          load(1);
-          top = fmaxf(top, largest());
-        }
-        top *= cq;
-        const bool moves = top > base + kLazy;
-        if (__any_sync(0xffffffffu, moves)) {
+        // Moves the base where a logit would overflow an fp16 weight, with what has been
+        // summed on the old one: O (complete up to the chunk before), the sum and, from
+        // the second half, the first half's weights.
+        auto rebase = [&](float top, bool second) {
+          const bool moves = top > base + kHeadroom;
+          if (!__any_sync(0xffffffffu, moves)) return true;
           const float nb = moves ? top : base;
           const float alpha = exp2_approx(base - nb);
           base = nb;
           sum.x *= alpha;
           sum.y *= alpha;
+          if (second) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float w16[16];
+              uint32_t h[16];
+              tmem_ld16(tS + 16 * i, w16);
+              tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {   // in fp32: alpha may be far below fp16's range
+                const uint32_t w = __float_as_uint(w16[u]);
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                h[u] = pack_half2(v.x * alpha, v.y * alpha);
+              }
+              tmem_st16u(tS + 16 * i, h);
+            }
+          }
           if (c > 0) {
-            // O so far is complete: at head_dim 128 barS says so too
-            if (kTiles == 1 && gave_up(barO, chunks - 1)) { dead = true; break; }
+            // at head_dim 128 barS has said that O is complete
+            if (kTiles == 1 && gave_up(barO, chunks - 1)) return false;
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -321,10 +337,11 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
               for (int u = 0; u < 16; ++u) o16[u] *= alpha;
               tmem_st16(tO + 16 * i, o16);
             }
-            tmem_wait_st();
           }
-        }
-        auto weights = [&](int h) {    // P of half h, over the columns it was read from
+          tmem_wait_st();
+          return true;
+        };
+        auto weights = [&](int h) {    // P of half h, over the first columns it was read from
           const float2 c2 = make_float2(cq, cq), b2 = make_float2(-base, -base);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -338,16 +355,23 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
             }
             tmem_st16u(tS + 64 * h + 16 * q, pk);
           }
+        };
+        auto publish = [&](int h) {
           tmem_wait_st();
           tc_fence_before();
           ws_arrive(&pready[2 * y + h]);
         };
+        load(0);
+        if (!rebase(largest() * cq, false)) { dead = true; break; }
+        weights(0);
         if (T::kHalves == 2) {
+          load(1);
+          if (!rebase(largest() * cq, true)) { dead = true; break; }
+          publish(0);      // only now: the second half may have moved its base
           weights(1);
-          load(0);
-          weights(0);
+          publish(1);
         } else {
-          weights(0);
+          publish(0);
         }
       }
       if (dead) break;
@@ -424,28 +448,35 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     uint4 kc[4], vc[4];
     uint32_t ks[4], vs[4];
     int chunks = 0;
+    // unit dw + 4 i of a chunk's 16: an 8-token group of a 128-dim half
+    auto group_of = [&](int i) { return kTok == 128 ? dw + 4 * i : dw + 4 * (i & 1); };
+    auto half_of = [&](int i) { return kTok == 128 ? 0 : i >> 1; };
+    const int psh = 31 - __clz(g.P);                          // log2 of the page size
+    const uint32_t page_rows = (uint32_t)g.Hkv << psh;        // token rows of a page, all heads
     while (!dead && cursor.next(sh, p.seqlens, seg)) {
       const int32_t* pt = p.page_table + (size_t)seg.b * g.MB;
-      auto group_of = [&](int i) { return (dw + 4 * i) % (kTok / 8); };   // 8-token group
-      auto half_of = [&](int i) { return (dw + 4 * i) / (kTok / 8); };    // 128-dim half
       // the two pages of a chunk (the same one twice where pages are as long)
       auto pages_of = [&](int chunk, int& pa, int& pb) {
-        const int b0 = chunk * kTok / g.P, b1 = (chunk * kTok + kTok - 1) / g.P;
+        const int b0 = (chunk * kTok) >> psh, b1 = (chunk * kTok + kTok - 1) >> psh;
         pa = b0 < g.MB && seg.n_all > seg.lo_all ? __ldg(pt + b0) : -1;
         pb = b1 < g.MB && seg.n_all > seg.lo_all ? __ldg(pt + b1) : -1;
+        if (pa >= g.NP) pa = -1;
+        if (pb >= g.NP) pb = -1;
       };
+      const uint32_t head_rows = (uint32_t)seg.kvh << psh;   // token rows of a page before the head's
       auto fetch = [&](int chunk, int pa, int pb, const uint8_t* pool, const uint8_t* sfs,
                        uint4 (&codes)[4], uint32_t (&sc)[4]) {
-        const int first = chunk * kTok / g.P;
+        const int tok0 = chunk * kTok;
+        const bool inner = tok0 >= seg.lo_all && tok0 + kTok <= seg.n_all;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int tok = chunk * kTok + 8 * group_of(i) + r8;
-          const int page = tok / g.P == first ? pa : pb;
+          const int o = 8 * group_of(i) + r8;             // token of the chunk
+          const int page = (o >> psh) ? pb : pa;          // (a chunk is one page or two)
           codes[i] = make_uint4(0u, 0u, 0u, 0u);
           sc[i] = 0u;
           // what no row of the tile sees is not looked at
-          if (page >= 0 && page < g.NP && tok >= seg.lo_all && tok < seg.n_all) {
-            const size_t row = ((size_t)page * g.Hkv + seg.kvh) * g.P + tok % g.P;
+          if (page >= 0 && (inner || (tok0 + o >= seg.lo_all && tok0 + o < seg.n_all))) {
+            const size_t row = (size_t)page * page_rows + head_rows + (o & (g.P - 1));
             codes[i] = ldg128(pool + row * (D / 2) + 64 * half_of(i) + 16 * q);
             sc[i] = ldg16(sfs + row * (D / 16) + 8 * half_of(i) + 2 * q);
           }
@@ -537,12 +568,12 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t == 0 && gave_up(&vready[x], n >> 1)) { dead = true; break; }
-            if (gave_up(&pready[2 * t + 1], n)) { dead = true; break; }
-            tc_fence_after();
-            issue_o(t, t, x, 1, c == 0);
             if (gave_up(&pready[2 * t], n)) { dead = true; break; }
             tc_fence_after();
-            issue_o(t, t, x, 0, false);
+            issue_o(t, t, x, 0, c == 0);
+            if (gave_up(&pready[2 * t + 1], n)) { dead = true; break; }
+            tc_fence_after();
+            issue_o(t, t, x, 1, false);
             if (t == 1) mma_commit_elect(&vfree[x]);
             if (c + 1 < C) {
               if (t == 0 && !chunk_s(c + 1)) { dead = true; break; }
