@@ -127,7 +127,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
   pdl_wait();
   const Span span = plan_span<C::kThreads>(sh, p.seqlens, blockIdx.x, gridDim.x);
   pdl_trigger();
-  if (tid == 0) p.desc[blockIdx.x].b = -1;
+  if (tid == 0) describe_none(sh, p, blockIdx.x);
   if (span.begin >= span.end) return;
 
   // Token row within an 8-token group, by MMA row: see the swizzle below.
@@ -504,21 +504,15 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
         *reinterpret_cast<float4*>(rec + 2 * sh.vt + (size_t)c * D + d) = acc;
       }
     }
-    if (tid == 0 && ends && !begins) {
-      Desc dsc;
-      dsc.b = b; dsc.tile = seg.tile; dsc.kvh = kvh;
-      // the unit's first chunk is todo + c_at before the cursor
-      dsc.first = (int)((cursor.at - todo - seg.c_at) / span.share);
-      p.desc[blockIdx.x] = dsc;
-    }
+    if (tid == 0 && ends) describe(sh, p, span, cursor, seg, blockIdx.x);
     __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------
-// Divided units joined.  CTA (i, y) takes vectors y, y + gridDim.y, ... of the
-// unit that ends in CTA i: with few records a warp per vector, with many (one
-// long request over the whole GPU) all warps on one vector's records.
+// Divided units joined.  CTA (i, y) takes vectors of the unit of descriptor i:
+// with few records a warp per vector, with many (one long request over the whole
+// GPU) all warps on one vector's records.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 
@@ -530,19 +524,18 @@ dense_join_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   const Geom& g = sh.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int last = blockIdx.x;
   pdl_wait();
   pdl_trigger();
-  const Desc d = p.desc[last];
+  const Desc d = p.desc[blockIdx.x];
   if (d.b < 0) return;
-  if (!QSA_IN_BOUNDS(d.b < g.B && d.kvh < g.Hkv && d.first >= 0 && d.first < last, kChkJoin)) return;
+  if (!QSA_IN_BOUNDS(d.b < g.B && d.kvh < g.Hkv && d.first >= 0 && d.first < d.last, kChkJoin)) return;
   const int vec0 = d.tile * sh.vt, vecs = min(sh.vt, g.R * sh.G - vec0);
-  const int parts = last - d.first + 1;
+  const int parts = d.last - d.first + 1;
   const size_t rf = record_floats(sh.vt, D);
   auto record = [&](int i) {   // part i: slot 1 of the first CTA, slot 0 of the others
     return p.records + ((size_t)(d.first + i) * 2 + (i == 0 ? 1 : 0)) * rf;
   };
-  const bool many = parts > 8;
+  const bool many = parts > 24;
   const int ways = many ? 1 : kJoinWarps;   // vectors at a time
   for (int c0 = blockIdx.y * ways; c0 < vecs; c0 += gridDim.y * ways) {
     const int c = many ? c0 : c0 + warp;
@@ -644,7 +637,7 @@ size_t dense_carve(const dense::Shape& s, int ctas, void* workspace, dense::Work
     w->status = reinterpret_cast<int*>(base);
     w->desc = reinterpret_cast<dense::Desc*>(base + off);
   }
-  off += ((size_t)ctas * sizeof(dense::Desc) + 255) / 256 * 256;
+  off += ((size_t)dense::desc_count(s, ctas) * sizeof(dense::Desc) + 255) / 256 * 256;
   if (w) w->records = reinterpret_cast<float*>(base + off);
   off += (size_t)ctas * 2 * dense::record_floats(s.vt, s.g.D) * sizeof(float);
   return (off + 255) / 256 * 256;
@@ -653,7 +646,7 @@ size_t dense_carve(const dense::Shape& s, int ctas, void* workspace, dense::Work
 cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, int ctas,
                               cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, s.vt < 8 ? s.vt : 8);
+  cfg.gridDim = dim3(dense::desc_count(s, ctas), s.vt <= 16 ? 8 : s.vt / dense::kJoinWarps);
   cfg.blockDim = dim3(dense::kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -684,6 +677,7 @@ dense::Shape decode_shape(const Geom& g, int window) {
   s.tok = g.D == 256 ? 32 : (s.vt == 8 ? C128a::TOK : C128b::TOK);
   s.window = window;
   s.least = 16;
+  s.by_unit = dense::unit_count(s) <= dense_sms();
   return s;
 }
 

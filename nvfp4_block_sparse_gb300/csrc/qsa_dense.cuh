@@ -14,9 +14,11 @@
 //
 // A unit inside one CTA is written out by it.  A unit that crosses CTAs leaves
 // a record (base, sum, unscaled output per vector) from each of them: in slot 1
-// of the CTA where it begins, in slot 0 of the others.  The CTA where it ends
-// names it in its descriptor, and a second kernel joins the records in the
-// CTAs' order, whatever order they ended in.
+// of the CTA where it begins, in slot 0 of the others.  The CTA where a unit
+// ends writes its descriptor, and a second kernel joins the records in the
+// CTAs' order, whatever order they ended in.  Descriptors go by unit, or, where
+// there are more units than CTAs, by the CTA where the divided unit ends (there
+// is at most one).
 #pragma once
 
 #include "qsa_common.cuh"
@@ -39,12 +41,14 @@ struct Shape {
   int tok;       // tokens per chunk
   int window;    // tokens a row looks back over; 0: all
   int least;     // chunks a CTA takes at least
+  int by_unit;   // descriptors go by unit (else by CTA)
 };
 
-// One unit's descriptor, written by the CTA where a divided unit ends.
+// A divided unit's descriptor.
 struct Desc {
   int b, tile, kvh;   // b < 0: nothing to join
-  int first;          // CTA where the unit begins
+  int first, last;    // CTAs where the unit begins and ends
+  int pad[3];
 };
 
 struct Work {
@@ -56,7 +60,7 @@ struct Work {
   __nv_bfloat16* out;
   float* lse;
   int* status;
-  Desc* desc;        // [CTAs]
+  Desc* desc;        // [units or CTAs]
   float* records;    // [CTAs][2][vt][2 + D]: bases, sums, outputs
 };
 
@@ -191,12 +195,39 @@ struct Cursor {
   }
 };
 
+// By one thread, for every part that ends a unit (and, where descriptors go by
+// CTA, first for the CTA: `none`).
+__device__ __forceinline__ void describe(const Shape& s, const Work& w, const Span& span,
+                                         const Cursor& cursor, const Seg& seg, int cta) {
+  Desc d;
+  d.b = seg.begins ? -1 : seg.b;
+  d.tile = seg.tile;
+  d.kvh = seg.kvh;
+  // the unit's first chunk is todo + c_at before the cursor
+  d.first = (int)((cursor.at - seg.todo - seg.c_at) / span.share);
+  d.last = cta;
+  if (s.by_unit)
+    w.desc[(seg.b * s.tiles + seg.tile) * s.g.Hkv + seg.kvh] = d;
+  else if (!seg.begins)
+    w.desc[cta] = d;
+}
+__device__ __forceinline__ void describe_none(const Shape& s, const Work& w, int cta) {
+  if (!s.by_unit) w.desc[cta].b = -1;
+}
+
+// Units of a geometry, and how descriptors go.
+inline long long unit_count(const Shape& s) { return (long long)s.g.B * s.tiles * s.g.Hkv; }
+inline int desc_count(const Shape& s, int ctas) {
+  return s.by_unit ? (int)unit_count(s) : ctas;
+}
+
 }  // namespace dense
 
 // The tile kernel (qsa_dense_tile.cu): its units for this geometry, and its launch.
 dense::Shape dense_tile_shape(const Geom& g, int window);
 cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, int ctas,
                               cudaStream_t stream);
+int dense_sms();
 cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, int ctas,
                               cudaStream_t stream);
 // The workspace's parts: status word, descriptors, records.

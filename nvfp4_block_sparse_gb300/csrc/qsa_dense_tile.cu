@@ -59,14 +59,16 @@ struct TT {
   static constexpr int kTok = D == 128 ? 128 : 64;       // tokens per chunk
   static constexpr int kHalves = kTok / 64;              // P is written 64 tokens at a time
   static constexpr int kSoft = 4 * kTiles;               // softmax warps
-  static constexpr int kDeq = D == 128 ? 4 : 8;          // dequantisation warps
+  static constexpr int kDeq = 8;                         // dequantisation warps: four K, four V
   static constexpr int kMma = kSoft + kDeq;              // the MMA warp; its group's others idle
-  static constexpr int kThreads = 512;
-  // Registers per thread after the roles part (of 512 x 128 at launch).
-  static constexpr int kSoftRegs = D == 128 ? 168 : 184;
-  static constexpr int kDeqRegs = D == 128 ? 104 : 112;
-  static constexpr int kMmaRegs = 72;
-  static_assert(32 * (kSoft * kSoftRegs + kDeq * kDeqRegs + 4 * kMmaRegs) <= 512 * 128, "registers");
+  static constexpr int kThreads = 32 * (kMma + 4);
+  // Registers per thread: at launch, and after the roles part.
+  static constexpr int kRegs = D == 128 ? 96 : 128;
+  static constexpr int kSoftRegs = D == 128 ? 144 : 184;
+  static constexpr int kDeqRegs = D == 128 ? 72 : 112;
+  static constexpr int kMmaRegs = D == 128 ? 48 : 72;
+  static_assert(32 * (kSoft * kSoftRegs + kDeq * kDeqRegs + 4 * kMmaRegs) <= kThreads * kRegs,
+                "registers");
   static constexpr int kQBytes = 128 * D * 2;            // Q: D/64 blocks of 128 rows x 128 B
   static constexpr int kBlk = kTok * 128;                // one 64-dim block of a K or V tile
   static constexpr int kKV = (D / 64) * kBlk;            // 32 KB
@@ -186,7 +188,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   pdl_wait();
   const Span span = plan_span<T::kThreads>(sh, p.seqlens, blockIdx.x, gridDim.x);
   pdl_trigger();
-  if (tid == 0) p.desc[blockIdx.x].b = -1;
+  if (tid == 0) describe_none(sh, p, blockIdx.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -427,12 +429,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           rec[sh.vt + c_rec] = l;
         }
       }
-      if (tid == 0 && seg.ends && !seg.begins) {
-        Desc dsc;
-        dsc.b = seg.b; dsc.tile = seg.tile; dsc.kvh = seg.kvh;
-        dsc.first = (int)((cursor.at - seg.todo - seg.c_at) / span.share);
-        p.desc[blockIdx.x] = dsc;
-      }
+      if (tid == 0 && seg.ends) describe(sh, p, span, cursor, seg, blockIdx.x);
     }
   } else if (warp < T::kMma) {
     regs_down<T::kDeqRegs>();
@@ -440,13 +437,17 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     // A 16-byte piece (32 codes, two scales) of eight token rows and four neighbouring
     // pieces per warp and step: 512 contiguous bytes (256 at a time at head_dim 256), and
     // the eight lanes that store together hold eight rows, so the swizzle gives them
-    // distinct banks.  At head_dim 256 four warps convert K and four V.
+    // distinct banks.  Four warps convert K and four V, each set at its tile's pace.
     const int dw = (warp - T::kSoft) & 3;
-    const bool does_k = T::kDeq == 4 || warp - T::kSoft < 4;
-    const bool does_v = T::kDeq == 4 || !does_k;
+    const bool is_v = warp - T::kSoft >= 4;
+    const uint8_t* pool = is_v ? p.v_pool : p.k_pool;
+    const uint8_t* sfs = is_v ? p.v_sf : p.k_sf;
+    uint8_t* tiles = is_v ? sV : sK;
+    uint64_t* ready = is_v ? vready : kready;
+    uint64_t* freed = is_v ? vfree : kfree;
     const int r8 = lane & 7, q = lane >> 3;
-    uint4 kc[4], vc[4];
-    uint32_t ks[4], vs[4];
+    uint4 codes[4];
+    uint32_t sc[4];
     int chunks = 0;
     // unit dw + 4 i of a chunk's 16: an 8-token group of a 128-dim half
     auto group_of = [&](int i) { return kTok == 128 ? dw + 4 * i : dw + 4 * (i & 1); };
@@ -464,8 +465,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         if (pb >= g.NP) pb = -1;
       };
       const uint32_t head_rows = (uint32_t)seg.kvh << psh;   // token rows of a page before the head's
-      auto fetch = [&](int chunk, int pa, int pb, const uint8_t* pool, const uint8_t* sfs,
-                       uint4 (&codes)[4], uint32_t (&sc)[4]) {
+      auto fetch = [&](int chunk, int pa, int pb) {
         const int tok0 = chunk * kTok;
         const bool inner = tok0 >= seg.lo_all && tok0 + kTok <= seg.n_all;
 #pragma unroll
@@ -482,7 +482,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           }
         }
       };
-      auto convert = [&](const uint4 (&codes)[4], const uint32_t (&sc)[4], uint8_t* tile) {
+      auto convert = [&](uint8_t* tile) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int tok = 8 * group_of(i) + r8;
@@ -499,28 +499,16 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       };
       int pa, pb;
       pages_of(seg.chunk0, pa, pb);
-      if (does_k) fetch(seg.chunk0, pa, pb, p.k_pool, p.k_sf, kc, ks);
-      if (does_v) fetch(seg.chunk0, pa, pb, p.v_pool, p.v_sf, vc, vs);
+      fetch(seg.chunk0, pa, pb);
       if (seg.todo > 1) pages_of(seg.chunk0 + 1, pa, pb);
       for (int c = 0; c < seg.todo; ++c, ++chunks) {
         const int x = chunks & 1, use = chunks >> 1;
-        const int next = seg.chunk0 + c + 1;
-        const bool more = c + 1 < seg.todo;
-        if (does_k) {
-          if (use > 0 && gave_up(&kfree[x], use - 1)) { dead = true; break; }
-          convert(kc, ks, sK + x * T::kKV);
-          fence_proxy_async_smem();
-          ws_arrive(&kready[x]);
-          if (more) fetch(next, pa, pb, p.k_pool, p.k_sf, kc, ks);
-        }
-        if (does_v) {
-          if (use > 0 && gave_up(&vfree[x], use - 1)) { dead = true; break; }
-          convert(vc, vs, sV + x * T::kKV);
-          fence_proxy_async_smem();
-          ws_arrive(&vready[x]);
-          if (more) fetch(next, pa, pb, p.v_pool, p.v_sf, vc, vs);
-        }
-        if (c + 2 < seg.todo) pages_of(next + 1, pa, pb);
+        if (use > 0 && gave_up(&freed[x], use - 1)) { dead = true; break; }
+        convert(tiles + x * T::kKV);
+        fence_proxy_async_smem();
+        ws_arrive(&ready[x]);
+        if (c + 1 < seg.todo) fetch(seg.chunk0 + c + 1, pa, pb);
+        if (c + 2 < seg.todo) pages_of(seg.chunk0 + c + 2, pa, pb);
       }
     }
   } else if (regs_down<T::kMmaRegs>(), warp == T::kMma) {
@@ -637,6 +625,7 @@ dense::Shape dense_tile_shape(const Geom& g, int window) {
   s.tok = g.D == 128 ? dense::TT<128>::kTok : dense::TT<256>::kTok;
   s.window = window;
   s.least = 4;
+  s.by_unit = dense::unit_count(s) <= dense_sms();
   return s;
 }
 

@@ -53,9 +53,9 @@ rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
 // Norms, rotation, append.
 //
 // A head of D elements belongs to D/8 lanes, eight elements (16 bytes) each: a
-// warp holds two heads at D = 128, one at D = 256.  A warp takes `heads` heads
-// of one row, in steps of the heads it holds, and keeps the row's cos and sin
-// and the weights in registers meanwhile.  The pairs of the half layout meet by a
+// warp holds two heads at D = 128, one at D = 256.  A warp takes STEPS times the
+// heads it holds of one row, all requested before the first is used, and keeps
+// the row's cos and sin in registers meanwhile.  The pairs of the half layout meet by a
 // shuffle over rotary_dim / 16 lanes (rotary_dim is a multiple of 16, so a
 // lane's eight elements have one partner lane); interleaved pairs are in the lane.
 // ---------------------------------------------------------------------------
@@ -89,7 +89,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int D, bool kAppend>
+template <int D, bool kAppend, int STEPS>
 __global__ void __launch_bounds__(kWarps * 32)
 prologue_kernel(const __grid_constant__ KernelArgs p) {
   constexpr int LPV = D / 8;        // lanes per head
@@ -107,6 +107,21 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
   const int v0 = (int)(item % p.groups) * p.heads;
   const int v1 = min(v0 + p.heads, p.total);
   const int hq = a.q ? g.Hq : 0;
+
+  // all of the warp's heads are requested before anything waits for one
+  uint4 raws[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int hv = v0 + i * VPW + lane / LPV;
+    raws[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (hv < v1) {
+      const __nv_bfloat16* src = hv < hq           ? a.q + r * a.q_stride + (size_t)hv * D
+                                 : hv < hq + g.Hkv ? a.k + r * a.k_stride + (size_t)(hv - hq) * D
+                                                   : a.v + r * a.v_stride +
+                                                         (size_t)(hv - hq - g.Hkv) * D;
+      raws[i] = *reinterpret_cast<const uint4*>(src + e0);
+    }
+  }
 
   // the lane's cos and sin: o = y c + partner s, with the sign of the first
   // half's sine in s
@@ -161,19 +176,15 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
     }
   }
 
-  for (int v = v0; v < v1; v += VPW) {
+#pragma unroll
+  for (int step = 0; step < STEPS; ++step) {
+    if (STEPS > 1 && v0 + step * VPW >= v1) break;
     // warp-wide shuffles below: a lane without a head takes part with zeros
-    const int hv = v + lane / LPV;
+    const int hv = v0 + step * VPW + lane / LPV;
     const bool real = hv < v1;
     const int kind = hv < hq ? 0 : hv < hq + g.Hkv ? 1 : 2;   // query, key, value
     const int head = kind == 0 ? hv : kind == 1 ? hv - hq : hv - hq - g.Hkv;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (real) {
-      const __nv_bfloat16* src = kind == 0   ? a.q + r * a.q_stride
-                                 : kind == 1 ? a.k + r * a.k_stride
-                                             : a.v + r * a.v_stride;
-      raw = *reinterpret_cast<const uint4*>(src + (size_t)head * D + e0);
-    }
+    uint4 raw = raws[step];
     float x[8];
     unpack8(raw, x);
     const bool any_qk = __any_sync(0xffffffffu, real && kind < 2);
@@ -344,8 +355,11 @@ cudaError_t launch_prologue(const Geom& g, const NormRope& nr, const PrologueArg
   p.heads = vpw * steps;
   p.groups = (p.total + p.heads - 1) / p.heads;
   const long long items = T * p.groups;
-  auto* kern = g.D == 256 ? (append ? prologue_kernel<256, true> : prologue_kernel<256, false>)
-                          : (append ? prologue_kernel<128, true> : prologue_kernel<128, false>);
+  auto pick = [&]<int STEPS>() {
+    return g.D == 256 ? (append ? prologue_kernel<256, true, STEPS> : prologue_kernel<256, false, STEPS>)
+                      : (append ? prologue_kernel<128, true, STEPS> : prologue_kernel<128, false, STEPS>);
+  };
+  auto* kern = steps == 4 ? pick.template operator()<4>() : pick.template operator()<1>();
   return launch(kern, dim3((unsigned)((items + kWarps - 1) / kWarps)), dim3(kWarps * 32), pdl,
                 stream, p);
 }
