@@ -528,7 +528,10 @@ dense_join_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   pdl_trigger();
   const Desc d = p.desc[blockIdx.x];
   if (d.b < 0) return;
-  if (!QSA_IN_BOUNDS(d.b < g.B && d.kvh < g.Hkv && d.first >= 0 && d.first < d.last, kChkJoin)) return;
+  // (a part whose waits gave up leaves no descriptor: what is there may be anything)
+  if (!QSA_GUARD(d.b < g.B && d.tile >= 0 && d.tile < sh.tiles && d.kvh >= 0 && d.kvh < g.Hkv &&
+                     d.first >= 0 && d.first < d.last && d.last < sh.ctas, kChkJoin))
+    return;
   const int vec0 = d.tile * sh.vt, vecs = min(sh.vt, g.R * sh.G - vec0);
   const int parts = d.last - d.first + 1;
   const size_t rf = record_floats(sh.vt, D);
@@ -630,23 +633,22 @@ int dense_sms() {
   return sms;
 }
 
-size_t dense_carve(const dense::Shape& s, int ctas, void* workspace, dense::Work* w) {
+size_t dense_carve(const dense::Shape& s, void* workspace, dense::Work* w) {
   size_t off = 256;
   uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
   if (w) {
     w->status = reinterpret_cast<int*>(base);
     w->desc = reinterpret_cast<dense::Desc*>(base + off);
   }
-  off += ((size_t)dense::desc_count(s, ctas) * sizeof(dense::Desc) + 255) / 256 * 256;
+  off += ((size_t)dense::desc_count(s) * sizeof(dense::Desc) + 255) / 256 * 256;
   if (w) w->records = reinterpret_cast<float*>(base + off);
-  off += (size_t)ctas * 2 * dense::record_floats(s.vt, s.g.D) * sizeof(float);
+  off += (size_t)s.ctas * 2 * dense::record_floats(s.vt, s.g.D) * sizeof(float);
   return (off + 255) / 256 * 256;
 }
 
-cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, int ctas,
-                              cudaStream_t stream) {
+cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(dense::desc_count(s, ctas), s.vt <= 16 ? 8 : s.vt / dense::kJoinWarps);
+  cfg.gridDim = dim3(dense::desc_count(s), s.vt <= 16 ? 8 : s.vt / dense::kJoinWarps);
   cfg.blockDim = dim3(dense::kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -677,19 +679,19 @@ dense::Shape decode_shape(const Geom& g, int window) {
   s.tok = g.D == 256 ? 32 : (s.vt == 8 ? C128a::TOK : C128b::TOK);
   s.window = window;
   s.least = 16;
-  s.by_unit = dense::unit_count(s) <= dense_sms();
+  s.ctas = dense_sms();
+  s.by_unit = dense::unit_count(s) <= s.ctas;
   return s;
 }
 
 template <class C>
-cudaError_t launch_decode(const dense::Shape& s, const dense::Work& w, int ctas,
-                          cudaStream_t stream) {
+cudaError_t launch_decode(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
   auto* kern = dense::dense_decode_kernel<C>;
   static_assert(C::kSmem <= 227 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(s.ctas);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
@@ -712,11 +714,10 @@ static dense::Shape dense_shape(const Geom& g, int window) {
 }
 
 size_t dense_workspace_bytes(const Geom& g) {
-  return dense_carve(dense_shape(g, 0), dense_sms(), nullptr, nullptr);
+  return dense_carve(dense_shape(g, 0), nullptr, nullptr);
 }
 
 cudaError_t launch_dense(const Geom& g, const DenseArgs& a, cudaStream_t stream) {
-  const int ctas = dense_sms();
   const dense::Shape s = dense_shape(g, a.window);
   dense::Work w = {};
   w.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
@@ -726,16 +727,16 @@ cudaError_t launch_dense(const Geom& g, const DenseArgs& a, cudaStream_t stream)
   w.sinks = a.sinks;
   w.out = reinterpret_cast<__nv_bfloat16*>(a.out);
   w.lse = a.lse;
-  dense_carve(s, ctas, a.workspace, &w);
+  dense_carve(s, a.workspace, &w);
   cudaError_t e;
   if (use_tiles(g))
-    e = launch_dense_tile(s, w, ctas, stream);
+    e = launch_dense_tile(s, w, stream);
   else if (g.D == 128)
-    e = s.vt == 8 ? launch_decode<C128a>(s, w, ctas, stream) : launch_decode<C128b>(s, w, ctas, stream);
+    e = s.vt == 8 ? launch_decode<C128a>(s, w, stream) : launch_decode<C128b>(s, w, stream);
   else
-    e = s.vt == 8 ? launch_decode<C256a>(s, w, ctas, stream) : launch_decode<C256b>(s, w, ctas, stream);
+    e = s.vt == 8 ? launch_decode<C256a>(s, w, stream) : launch_decode<C256b>(s, w, stream);
   if (e != cudaSuccess) return e;
-  return launch_dense_join(s, w, ctas, stream);
+  return launch_dense_join(s, w, stream);
 }
 
 }  // namespace qsa

@@ -41,6 +41,7 @@ struct Shape {
   int tok;       // tokens per chunk
   int window;    // tokens a row looks back over; 0: all
   int least;     // chunks a CTA takes at least
+  int ctas;      // CTAs of the grid
   int by_unit;   // descriptors go by unit (else by CTA)
 };
 
@@ -217,20 +218,16 @@ __device__ __forceinline__ void describe_none(const Shape& s, const Work& w, int
 
 // Units of a geometry, and how descriptors go.
 inline long long unit_count(const Shape& s) { return (long long)s.g.B * s.tiles * s.g.Hkv; }
-inline int desc_count(const Shape& s, int ctas) {
-  return s.by_unit ? (int)unit_count(s) : ctas;
-}
+inline int desc_count(const Shape& s) { return s.by_unit ? (int)unit_count(s) : s.ctas; }
 
 }  // namespace dense
 
 // The tile kernel (qsa_dense_tile.cu): its units for this geometry, and its launch.
 dense::Shape dense_tile_shape(const Geom& g, int window);
-cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, int ctas,
-                              cudaStream_t stream);
+cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, cudaStream_t stream);
 int dense_sms();
-cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, int ctas,
-                              cudaStream_t stream);
+cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, cudaStream_t stream);
 // The workspace's parts: status word, descriptors, records.
-size_t dense_carve(const dense::Shape& s, int ctas, void* workspace, dense::Work* w);
+size_t dense_carve(const dense::Shape& s, void* workspace, dense::Work* w);
 
 }  // namespace qsa

@@ -6,39 +6,52 @@
 // context rows run on tcgen05 with K/V tiles shared by a group of rows; Known
 // limitations: context rows read the NVFP4 pages dequantised on the way.
 //
-// A CTA takes tiles of 128 query vectors (row, head) of one request and KV
-// head: two tiles at head_dim 128, one at 256, which share every dequantised
-// chunk (128 tokens, 64 at head_dim 256).  4 D flops per (vector, token): the
-// tensor core bounds the work, at 128 x 128 x D fp16 products per chunk and tile for
-// each of
+// The work is 4 D flops per (query vector, token), on the tensor core:
 //   S = Q K^T    A = Q, B = K from shared memory (K-major), D = S in tensor memory
 //   O += P V     A = P from tensor memory, B = V from shared memory (token rows, MN-major)
+// A tile is 128 query vectors (row, head) of one request and KV head: the 128
+// tensor-memory lanes of a CTA.
 //
-// Roles (one CTA per SM, one warp group each unless noted):
+// Pairs of CTAs (more than 128 vectors per KV head): the two SMs of a pair run
+// M = 256 MMAs (cta_group::2) on two tiles at once, each SM holding half of
+// every K and V tile (half the tokens of K, half the dims of V).  So each SM
+// dequantises half of a chunk and feeds half of the B operand from its shared
+// memory; with one SM per tile, operand reads and the dequantised stores fill
+// shared memory's bandwidth and everything else that uses it (barrier probes)
+// crawls.  At head_dim 128 a CTA has two tiles (four per pair), at 256 one.
+// Single CTAs (17 to 128 vectors: verify rows) have one tile, for which the cache's
+// bytes, not the products, are the floor.
+//
+// Roles in a CTA (a warp group each unless noted):
 //   softmax   a thread per vector (tensor-memory lane): its row of S to registers, base
 //             (moved only where a weight would overflow), P = exp2(S c - base) as
 //             fp16 over the columns of S it has read, sums in fp32; 64 tokens at a time, so that
 //             no pass over the chunk comes before the exponentials; at the end
-//             of a part O from tensor memory to the output or to a record
+//             of a part O from tensor memory to the output or to a record.  A group per tile
 //   dequant   codes and scales from the pages straight to registers one chunk ahead (they
 //             are in flight while the chunk before is converted), e2m1 x e4m3 exact in
-//             fp16 into double-buffered K and V tiles (128-byte swizzle)
-//   MMA       one warp issues every MMA in order.  At head_dim 128 the tiles take
-//             turns: O_0, S_0 of the next chunk, O_1, S_1, so that one tile's softmax
-//             runs under the other's products.  At head_dim 256 S has two buffers
-//             and runs two chunks ahead.
+//             fp16 into double-buffered K and V tiles (128-byte swizzle); four warps
+//             convert K and four V, each set at its tile's pace
+//   MMA       one warp (of the pair's first CTA) issues every MMA in order.  With two tiles
+//             they take turns: O_0, S_0 of the next chunk, O_1, S_1, so that one tile's
+//             softmax runs under the other's products; with one, S has two buffers
+//             and runs two chunks ahead.  (A warp per tile, whose MMAs on two accumulators
+//             interleave, took twice the time: runs of MMAs on one accumulator are what
+//             the tensor core pipelines.)
 // P lies over S: S of the next chunk is issued behind the O that reads P, and
 // MMAs of one thread run in order, so no barrier guards the reuse.
 //
-// Tensor memory (512 columns): the S buffers from column 0, O from 256.
-// mbarriers, all waits bounded (2 s; a wait that gives up sets the status word):
-//   qready        Q tiles written; O, S of the part before read    (softmax threads)
-//   kready/vready[x]  K / V tile x written                         (its 128 converting threads)
+// Tensor memory (512 columns): the two S buffers from column 0, O from 256.
+// mbarriers, all waits bounded (2 s; a wait that gives up sets the status word).
+// Arrivals are one per warp; those for the MMA warp go to the first CTA's barrier,
+// commits to both CTAs':
+//   qready        Q tiles written; O, S of the part before read    (softmax warps)
+//   kready/vready[x]  K / V tile x written                         (its four converting warps)
 //   kfree/vfree[x]    MMAs that read tile x complete               (commit)
-//   barS[y]       S buffer y complete -- and, at head_dim 128, every MMA before it,
+//   barS[y]       S buffer y complete -- and, with two tiles, every MMA before it,
 //                 so also the tile's O so far; once more after a part's last O   (commit)
-//   barO          O complete (head_dim 256)                        (commit)
-//   pready[y][h]  half h of P in buffer y written                  (128 softmax threads)
+//   barO          O complete (one tile)                            (commit)
+//   pready[y][h]  half h of P in buffer y written                  (four softmax warps)
 #include "qsa_dense.cuh"
 #include "qsa_tc.cuh"
 
@@ -49,31 +62,35 @@ namespace {
 using namespace tc;
 
 // Bounds-check codes (reported by bounds-checked builds only).
-[[maybe_unused]] constexpr int kChkChunk = 0xA01;   // chunk: token block past the page table
 [[maybe_unused]] constexpr int kChkOut = 0xA02;     // output row out of range
 
-template <int D_>
+template <int D_, int CG_>
 struct TT {
-  static constexpr int D = D_;
-  static constexpr int kTiles = D == 128 ? 2 : 1;        // query tiles of a CTA
-  static constexpr int kTok = D == 128 ? 128 : 64;       // tokens per chunk
+  static constexpr int D = D_, CG = CG_;                 // CG: CTAs per MMA
+  static constexpr int kTiles = D == 128 && CG == 2 ? 2 : 1;   // tiles of a CTA
+  static constexpr int kTok = D == 256 && CG == 1 ? 64 : 128;  // tokens per chunk
   static constexpr int kHalves = kTok / 64;              // P is written 64 tokens at a time
   static constexpr int kSoft = 4 * kTiles;               // softmax warps
   static constexpr int kDeq = 8;                         // dequantisation warps: four K, four V
   static constexpr int kMma = kSoft + kDeq;              // the MMA warp; its group's others idle
   static constexpr int kThreads = 32 * (kMma + 4);
   // Registers per thread: at launch, and after the roles part.
-  static constexpr int kRegs = D == 128 ? 96 : 128;
-  static constexpr int kSoftRegs = D == 128 ? 144 : 184;
-  static constexpr int kDeqRegs = D == 128 ? 72 : 112;
-  static constexpr int kMmaRegs = D == 128 ? 48 : 72;
+  static constexpr int kRegs = kTiles == 2 ? 96 : 128;
+  static constexpr int kSoftRegs = kTiles == 2 ? 144 : 184;
+  static constexpr int kDeqRegs = kTiles == 2 ? 72 : 112;
+  static constexpr int kMmaRegs = kTiles == 2 ? 48 : 72;
   static_assert(32 * (kSoft * kSoftRegs + kDeq * kDeqRegs + 4 * kMmaRegs) <= kThreads * kRegs,
                 "registers");
+  static constexpr int kVecs = 128 * CG * kTiles;        // query vectors of a unit
   static constexpr int kQBytes = 128 * D * 2;            // Q: D/64 blocks of 128 rows x 128 B
-  static constexpr int kBlk = kTok * 128;                // one 64-dim block of a K or V tile
-  static constexpr int kKV = (D / 64) * kBlk;            // 32 KB
+  static constexpr int kKRows = kTok / CG;               // K tile: tokens of this CTA
+  static constexpr int kKBlk = kKRows * 128;             // its 64-dim blocks
+  static constexpr int kKBytes = kKRows * D * 2;
+  static constexpr int kVDims = D / CG;                  // V tile: dims of this CTA
+  static constexpr int kVBlk = kTok * 128;
+  static constexpr int kVBytes = kTok * kVDims * 2;
   static constexpr int kBars = 17;
-  static constexpr int kSmem = 1024 + kTiles * kQBytes + 4 * kKV + kBars * 8 + 24;
+  static constexpr int kSmem = 1024 + kTiles * kQBytes + 2 * kKBytes + 2 * kVBytes + kBars * 8 + 24;
   static constexpr uint32_t kOCol = 256;
 };
 
@@ -125,6 +142,165 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// ---- barriers across the pair ------------------------------------------------
+// A warp's bounded wait: true when it gave up, in every lane.
+__device__ __forceinline__ bool gave_up(uint64_t* bar, uint32_t parity) {
+  return __any_sync(0xffffffffu, !wait_bounded(bar, parity & 1));
+}
+
+// One arrival of the warp at the first CTA's barrier.
+template <int CG>
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    if constexpr (CG == 1)
+      ws_arrive(bar);
+    else
+      asm volatile(
+          "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+          "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+          : "memory");
+  }
+}
+
+// ---- MMAs by one elected lane of a converged warp ------------------------------
+template <int CG>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (CG == 1)
+    mma_f16_elect(d, a, b, idesc, accumulate);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+template <int CG>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (CG == 1)
+    mma_f16_ts_elect(d, a, b, idesc, accumulate);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (CG == 1)
+    mma_commit_elect(bar);
+  else
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+        ".b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---- dequantisation --------------------------------------------------------------
+// Four warps convert this CTA's part of every chunk's K (kV false: kKRows tokens,
+// all dims) or V (all tokens, kVDims dims), a 16-byte piece (32 codes, two
+// scales) per lane and step.  A warp's pieces are neighbours in the page (512
+// contiguous bytes where a row has them) and the eight lanes that store together
+// hold eight rows, so the swizzle gives them distinct banks.
+template <class T, bool kV>
+__device__ __forceinline__ bool dequant_role(const Shape& sh, const Work& p, const Span& span,
+                                             int dw, int rank, uint8_t* tiles, uint64_t* ready,
+                                             uint64_t* freed) {
+  constexpr int D = T::D, kTok = T::kTok;
+  constexpr int kRows = kV ? kTok : T::kKRows, kDims = kV ? T::kVDims : D;
+  constexpr int kPieces = kDims / 32;                  // 16-byte pieces of a row
+  constexpr int kUnits = kRows * kPieces / 128;        // steps of a warp
+  constexpr int kBlk = kV ? T::kVBlk : T::kKBlk, kBytes = kV ? T::kVBytes : T::kKBytes;
+  const Geom& g = sh.g;
+  const int lane = threadIdx.x & 31;
+  const int psh = 31 - __clz(g.P);                          // log2 of the page size
+  const uint32_t page_rows = (uint32_t)g.Hkv << psh;        // token rows of a page, all heads
+  const int row0 = kV ? 0 : rank * kRows;                   // this CTA's first token of a chunk
+  const int dim0 = kV ? rank * kDims : 0;                   // and dim
+  const uint8_t* pool = (kV ? p.v_pool : p.k_pool) + dim0 / 2;
+  const uint8_t* sfs = (kV ? p.v_sf : p.k_sf) + dim0 / 16;
+  // row and piece of step i: eight rows of four pieces, or sixteen of two
+  auto row_of = [&](int i) {
+    const int u = dw + 4 * i;
+    return kPieces >= 4 ? 8 * (u % (kRows / 8)) + (lane & 7) : 16 * u + (lane & 15);
+  };
+  auto piece_of = [&](int i) {
+    const int u = dw + 4 * i;
+    return kPieces >= 4 ? 4 * (u / (kRows / 8)) + (lane >> 3) : lane >> 4;
+  };
+  uint4 codes[kUnits];
+  uint32_t sc[kUnits];
+  int chunks = 0;
+  Cursor cursor(span);
+  Seg seg;
+  while (cursor.next(sh, p.seqlens, seg)) {
+    const int32_t* pt = p.page_table + (size_t)seg.b * g.MB;
+    const uint32_t head_rows = (uint32_t)seg.kvh << psh;   // token rows of a page before the head's
+    // the pages of this CTA's tokens of a chunk: at most four, of 32 tokens and more
+    constexpr int kMaxPages = kRows / (D == 128 ? 64 : 32);
+    int pages[kMaxPages];
+    auto pages_of = [&](int chunk) {
+#pragma unroll
+      for (int i = 0; i < kMaxPages; ++i) {
+        const int beta = (chunk * kTok + row0 + i * (kRows / kMaxPages)) >> psh;
+        pages[i] = beta < g.MB && seg.n_all > seg.lo_all ? __ldg(pt + beta) : -1;
+        if (pages[i] >= g.NP) pages[i] = -1;
+      }
+    };
+    auto fetch = [&](int chunk) {
+      const int tok0 = chunk * kTok + row0;
+      const bool inner = tok0 >= seg.lo_all && tok0 + kRows <= seg.n_all;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int o = row_of(i);                          // token of this CTA's
+        int page = pages[0];
+#pragma unroll
+        for (int k = 1; k < kMaxPages; ++k)
+          if (o >= k * (kRows / kMaxPages)) page = pages[k];
+        codes[i] = make_uint4(0u, 0u, 0u, 0u);
+        sc[i] = 0u;
+        // what no row of the unit sees is not looked at
+        if (page >= 0 && (inner || (tok0 + o >= seg.lo_all && tok0 + o < seg.n_all))) {
+          const size_t row = (size_t)page * page_rows + head_rows + ((tok0 + o) & (g.P - 1));
+          codes[i] = ldg128(pool + row * (D / 2) + 16 * piece_of(i));
+          sc[i] = ldg16(sfs + row * (D / 16) + 2 * piece_of(i));
+        }
+      }
+    };
+    pages_of(seg.chunk0);
+    fetch(seg.chunk0);
+    if (seg.todo > 1) pages_of(seg.chunk0 + 1);
+    for (int c = 0; c < seg.todo; ++c, ++chunks) {
+      const int x = chunks & 1, use = chunks >> 1;
+      if (use > 0 && gave_up(&freed[x], use - 1)) return false;
+      uint8_t* tile = tiles + x * kBytes;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const uint32_t s2 = e4m3x2_to_f16x2(sc[i]);
+        const uint32_t sx[2] = {prmt(s2, 0, 0x1010), prmt(s2, 0, 0x3232)};
+        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int d8 = 4 * piece_of(i) + u;             // eight dims
+          *reinterpret_cast<uint4*>(tile + (d8 >> 3) * kBlk + sw128(row_of(i), d8 & 7)) =
+              dequant8(w[u], sx[u >> 1]);
+        }
+      }
+      fence_proxy_async_smem();
+      warp_arrive<T::CG>(&ready[x]);
+      if (c + 1 < seg.todo) fetch(seg.chunk0 + c + 1);
+      if (c + 2 < seg.todo) pages_of(seg.chunk0 + c + 2);
+    }
+  }
+  return true;
+}
+
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -134,26 +310,23 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// A warp's bounded wait: true when it gave up, in every lane.
-__device__ __forceinline__ bool gave_up(uint64_t* bar, uint32_t parity) {
-  return __any_sync(0xffffffffu, !wait_bounded(bar, parity & 1));
-}
-
-template <int D>
-__global__ void __launch_bounds__(TT<D>::kThreads, 1)
+template <int D, int CG>
+__global__ void __launch_bounds__(TT<D, CG>::kThreads, 1)
 dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work p) {
-  using T = TT<D>;
+  using T = TT<D, CG>;
   constexpr int kTok = T::kTok, kTiles = T::kTiles;
   const Geom& g = sh.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0;          // CTA of the pair
+  const int worker = (int)blockIdx.x / CG;                       // whose part of the work
 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;                                   // [kTiles][kQBytes]
-  uint8_t* sK = sQ + kTiles * T::kQBytes;               // [2][kKV]
-  uint8_t* sV = sK + 2 * T::kKV;                        // [2][kKV]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + 2 * T::kKV);
+  uint8_t* sK = sQ + kTiles * T::kQBytes;               // [2][kKBytes]
+  uint8_t* sV = sK + 2 * T::kKBytes;                    // [2][kVBytes]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + 2 * T::kVBytes);
   uint64_t* kready = bars;
   uint64_t* vready = bars + 2;
   uint64_t* kfree = bars + 4;
@@ -167,35 +340,41 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
 
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&kready[x], 128);
-      mbar_init(&vready[x], 128);
+      mbar_init(&kready[x], 4 * CG);
+      mbar_init(&vready[x], 4 * CG);
       mbar_init(&kfree[x], 1);
       mbar_init(&vfree[x], 1);
       mbar_init(&barS[x], 1);
-      mbar_init(&pready[2 * x], 128);
-      mbar_init(&pready[2 * x + 1], 128);
+      mbar_init(&pready[2 * x], 4 * CG);
+      mbar_init(&pready[2 * x + 1], 4 * CG);
     }
     mbar_init(barO, 1);
     mbar_init(mdone, 1);
-    mbar_init(qready, 32 * T::kSoft);
+    s_tmem[1] = 0u;   // set when a CTA of the pair gave up
+    mbar_init(qready, T::kSoft * CG);
     fence_mbar_init();
   }
   if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(s_tmem)), "r"(512u));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (CG == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(s_tmem)), "r"(512u));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(s_tmem)), "r"(512u));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
   }
   pdl_wait();
-  const Span span = plan_span<T::kThreads>(sh, p.seqlens, blockIdx.x, gridDim.x);
+  const Span span = plan_span<T::kThreads>(sh, p.seqlens, worker, sh.ctas);
   pdl_trigger();
-  if (tid == 0) describe_none(sh, p, blockIdx.x);
+  if (tid == 0 && rank == 0) describe_none(sh, p, worker);
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();    // the pair's barriers are initialised
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   bool dead = false;
-  Cursor cursor(span);
-  Seg seg;
 
   if (warp < T::kSoft) {
     // ==== softmax ==================================================================
@@ -204,11 +383,14 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + T::kOCol + t * D + lane_off;
     uint8_t* q_tile = sQ + t * T::kQBytes;
-    int chunks = 0, s_waits = 0;   // chunks so far; waits on barS (head_dim 128)
+    int chunks = 0, s_waits = 0;   // chunks so far; waits on barS (two tiles)
+    Cursor cursor(span);
+    Seg seg;
     while (!dead && cursor.next(sh, p.seqlens, seg)) {
       // this thread's vector, its Q row as fp16 scaled by a power of two into [256, 512)
-      const int vec = seg.vec0 + t * 128 + row;
-      const bool real = t * 128 + row < seg.vecs;
+      const int at = (t * CG + rank) * 128 + row;          // its number within the unit
+      const int vec = seg.vec0 + at;
+      const bool real = at < seg.vecs;
       const int j = real ? vec / sh.G : 0, head = seg.kvh * sh.G + (real ? vec % sh.G : 0);
       const size_t orow = ((size_t)seg.b * g.R + j) * g.Hq + head;
       const int n = real ? visible_tokens(seg.L, g.R, j, g.MB * g.P) : 0;
@@ -252,7 +434,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      ws_arrive(qready);
+      warp_arrive<CG>(qready);
 
       // pages of a chunk that are there: one bit per 32 tokens
       auto live_of = [&](int chunk) {
@@ -327,7 +509,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
             }
           }
           if (c > 0) {
-            // at head_dim 128 barS has said that O is complete
+            // with two tiles barS has said that O is complete
             if (kTiles == 1 && gave_up(barO, chunks - 1)) return false;
             tc_fence_after();
 #pragma unroll
@@ -361,7 +543,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         auto publish = [&](int h) {
           tmem_wait_st();
           tc_fence_before();
-          ws_arrive(&pready[2 * y + h]);
+          warp_arrive<CG>(&pready[2 * y + h]);
         };
         load(0);
         if (!rebase(largest() * cq, false)) { dead = true; break; }
@@ -378,7 +560,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       }
       if (dead) break;
       // ---- the part's output ---------------------------------------------------------
-      // (head_dim 256: barS of the last chunk says that the O of all but the last two chunks
+      // (one tile: barS of the last chunk says that the O of all but the last two chunks
       // is complete; a phase is only told from its neighbours, so both are waited for)
       const bool late = kTiles == 2 ? gave_up(&barS[t], s_waits)
                                     : ((seg.todo > 1 && gave_up(barO, chunks - 2)) ||
@@ -396,8 +578,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       }
       const float r = whole ? (l > 0.f ? f * p.v_scale / l : 0.f) : 1.f;
       const bool ok = real && QSA_IN_BOUNDS(seg.b < g.B && j < g.R && head < g.Hq, kChkOut);
-      float* rec = p.records + ((size_t)blockIdx.x * 2 + (seg.begins ? 1 : 0)) * record_floats(sh.vt, D);
-      const int c_rec = t * 128 + row;
+      float* rec = p.records + ((size_t)worker * 2 + (seg.begins ? 1 : 0)) * record_floats(sh.vt, D);
 #pragma unroll 2
       for (int i = 0; i < D / 16; ++i) {
         float o16[16];
@@ -415,7 +596,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
           dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
         } else {
-          float4* dst = reinterpret_cast<float4*>(rec + 2 * sh.vt + (size_t)c_rec * D + 16 * i);
+          float4* dst = reinterpret_cast<float4*>(rec + 2 * sh.vt + (size_t)at * D + 16 * i);
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             dst[u] = make_float4(o16[4 * u], o16[4 * u + 1], o16[4 * u + 2], o16[4 * u + 3]);
@@ -425,113 +606,42 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         if (whole) {
           p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
         } else {
-          rec[c_rec] = m;
-          rec[sh.vt + c_rec] = l;
+          rec[at] = m;
+          rec[sh.vt + at] = l;
         }
       }
-      if (tid == 0 && seg.ends) describe(sh, p, span, cursor, seg, blockIdx.x);
+      if (tid == 0 && rank == 0 && seg.ends) describe(sh, p, span, cursor, seg, worker);
     }
   } else if (warp < T::kMma) {
-    regs_down<T::kDeqRegs>();
     // ==== dequantisation =============================================================
-    // A 16-byte piece (32 codes, two scales) of eight token rows and four neighbouring
-    // pieces per warp and step: 512 contiguous bytes (256 at a time at head_dim 256), and
-    // the eight lanes that store together hold eight rows, so the swizzle gives them
-    // distinct banks.  Four warps convert K and four V, each set at its tile's pace.
+    regs_down<T::kDeqRegs>();
     const int dw = (warp - T::kSoft) & 3;
-    const bool is_v = warp - T::kSoft >= 4;
-    const uint8_t* pool = is_v ? p.v_pool : p.k_pool;
-    const uint8_t* sfs = is_v ? p.v_sf : p.k_sf;
-    uint8_t* tiles = is_v ? sV : sK;
-    uint64_t* ready = is_v ? vready : kready;
-    uint64_t* freed = is_v ? vfree : kfree;
-    const int r8 = lane & 7, q = lane >> 3;
-    uint4 codes[4];
-    uint32_t sc[4];
-    int chunks = 0;
-    // unit dw + 4 i of a chunk's 16: an 8-token group of a 128-dim half
-    auto group_of = [&](int i) { return kTok == 128 ? dw + 4 * i : dw + 4 * (i & 1); };
-    auto half_of = [&](int i) { return kTok == 128 ? 0 : i >> 1; };
-    const int psh = 31 - __clz(g.P);                          // log2 of the page size
-    const uint32_t page_rows = (uint32_t)g.Hkv << psh;        // token rows of a page, all heads
-    while (!dead && cursor.next(sh, p.seqlens, seg)) {
-      const int32_t* pt = p.page_table + (size_t)seg.b * g.MB;
-      // the two pages of a chunk (the same one twice where pages are as long)
-      auto pages_of = [&](int chunk, int& pa, int& pb) {
-        const int b0 = (chunk * kTok) >> psh, b1 = (chunk * kTok + kTok - 1) >> psh;
-        pa = b0 < g.MB && seg.n_all > seg.lo_all ? __ldg(pt + b0) : -1;
-        pb = b1 < g.MB && seg.n_all > seg.lo_all ? __ldg(pt + b1) : -1;
-        if (pa >= g.NP) pa = -1;
-        if (pb >= g.NP) pb = -1;
-      };
-      const uint32_t head_rows = (uint32_t)seg.kvh << psh;   // token rows of a page before the head's
-      auto fetch = [&](int chunk, int pa, int pb) {
-        const int tok0 = chunk * kTok;
-        const bool inner = tok0 >= seg.lo_all && tok0 + kTok <= seg.n_all;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int o = 8 * group_of(i) + r8;             // token of the chunk
-          const int page = (o >> psh) ? pb : pa;          // (a chunk is one page or two)
-          codes[i] = make_uint4(0u, 0u, 0u, 0u);
-          sc[i] = 0u;
-          // what no row of the tile sees is not looked at
-          if (page >= 0 && (inner || (tok0 + o >= seg.lo_all && tok0 + o < seg.n_all))) {
-            const size_t row = (size_t)page * page_rows + head_rows + (o & (g.P - 1));
-            codes[i] = ldg128(pool + row * (D / 2) + 64 * half_of(i) + 16 * q);
-            sc[i] = ldg16(sfs + row * (D / 16) + 8 * half_of(i) + 2 * q);
-          }
-        }
-      };
-      auto convert = [&](uint8_t* tile) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tok = 8 * group_of(i) + r8;
-          const uint32_t s2 = e4m3x2_to_f16x2(sc[i]);
-          const uint32_t sx[2] = {prmt(s2, 0, 0x1010), prmt(s2, 0, 0x3232)};
-          const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int piece = 16 * half_of(i) + 4 * q + u;   // 8 dims
-            *reinterpret_cast<uint4*>(tile + (piece >> 3) * T::kBlk + sw128(tok, piece & 7)) =
-                dequant8(w[u], sx[u >> 1]);
-          }
-        }
-      };
-      int pa, pb;
-      pages_of(seg.chunk0, pa, pb);
-      fetch(seg.chunk0, pa, pb);
-      if (seg.todo > 1) pages_of(seg.chunk0 + 1, pa, pb);
-      for (int c = 0; c < seg.todo; ++c, ++chunks) {
-        const int x = chunks & 1, use = chunks >> 1;
-        if (use > 0 && gave_up(&freed[x], use - 1)) { dead = true; break; }
-        convert(tiles + x * T::kKV);
-        fence_proxy_async_smem();
-        ws_arrive(&ready[x]);
-        if (c + 1 < seg.todo) fetch(seg.chunk0 + c + 1, pa, pb);
-        if (c + 2 < seg.todo) pages_of(seg.chunk0 + c + 2, pa, pb);
-      }
-    }
-  } else if (regs_down<T::kMmaRegs>(), warp == T::kMma) {
+    dead = warp - T::kSoft < 4
+               ? !dequant_role<T, false>(sh, p, span, dw, rank, sK, kready, kfree)
+               : !dequant_role<T, true>(sh, p, span, dw, rank, sV, vready, vfree);
+  } else if (regs_down<T::kMmaRegs>(), warp == T::kMma && rank == 0) {
     // ==== MMA issue ==================================================================
-    const uint32_t id_s = f16_idesc(128, kTok), id_o = f16_idesc(128, D) | kIdescBMn;
+    const uint32_t id_s = f16_idesc(128 * CG, kTok), id_o = f16_idesc(128 * CG, D) | kIdescBMn;
+    Cursor cursor(span);
+    Seg seg;
     int s_done = 0, parts = 0;     // chunks whose S was issued in earlier parts; parts
     auto issue_s = [&](int t, int y, int x) {
       const uint64_t dq = sw128_desc(smem_u32(sQ + t * T::kQBytes));
-      const uint64_t dk = sw128_desc(smem_u32(sK + x * T::kKV));
+      const uint64_t dk = sw128_desc(smem_u32(sK + x * T::kKBytes));
 #pragma unroll
       for (int h = 0; h < D / 64; ++h)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_f16_elect(tmem + y * kTok, dq + (uint64_t)((h * 16384 + 32 * ks) >> 4),
-                        dk + (uint64_t)((h * T::kBlk + 32 * ks) >> 4), id_s, (h | ks) ? 1u : 0u);
+          mma_ss<CG>(tmem + y * kTok, dq + (uint64_t)((h * 16384 + 32 * ks) >> 4),
+                     dk + (uint64_t)((h * T::kKBlk + 32 * ks) >> 4), id_s, (h | ks) ? 1u : 0u);
     };
     auto issue_o = [&](int t, int y, int x, int h, bool first) {   // 64 tokens
-      const uint64_t dv = sw128_mn_desc(smem_u32(sV + x * T::kKV), T::kBlk);
+      const uint64_t dv = sw128_mn_desc(smem_u32(sV + x * T::kVBytes), T::kVBlk);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        mma_f16_ts_elect(tmem + T::kOCol + t * D, tmem + y * kTok + 64 * h + 8 * ks,
-                         dv + (uint64_t)((8192 * h + 2048 * ks) >> 4), id_o,
-                         (first && ks == 0) ? 0u : 1u);
+        mma_ts<CG>(tmem + T::kOCol + t * D, tmem + y * kTok + 64 * h + 8 * ks,
+                   dv + (uint64_t)((8192 * h + 2048 * ks) >> 4), id_o,
+                   (first && ks == 0) ? 0u : 1u);
     };
     while (!dead && cursor.next(sh, p.seqlens, seg)) {
       if (gave_up(qready, parts)) { dead = true; break; }
@@ -547,12 +657,13 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       if constexpr (kTiles == 2) {
         if (!chunk_s(0)) { dead = true; break; }
         issue_s(0, 0, s_done & 1);
-        mma_commit_elect(&barS[0]);
+        commit<CG>(&barS[0]);
         issue_s(1, 1, s_done & 1);
-        mma_commit_elect(&barS[1]);
-        mma_commit_elect(&kfree[s_done & 1]);
+        commit<CG>(&barS[1]);
+        commit<CG>(&kfree[s_done & 1]);
         for (int c = 0; c < C && !dead; ++c) {
           const int n = s_done + c, x = n & 1, xn = (n + 1) & 1;
+          const bool more = c + 1 < C;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t == 0 && gave_up(&vready[x], n >> 1)) { dead = true; break; }
@@ -560,37 +671,41 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
             tc_fence_after();
             issue_o(t, t, x, 0, c == 0);
             if (gave_up(&pready[2 * t + 1], n)) { dead = true; break; }
+            if (t == 0 && more && gave_up(&kready[xn], (n + 1) >> 1)) { dead = true; break; }
             tc_fence_after();
             issue_o(t, t, x, 1, false);
-            if (t == 1) mma_commit_elect(&vfree[x]);
-            if (c + 1 < C) {
-              if (t == 0 && !chunk_s(c + 1)) { dead = true; break; }
-              issue_s(t, t, xn);
-            }
-            mma_commit_elect(&barS[t]);
-            if (t == 1 && c + 1 < C) mma_commit_elect(&kfree[xn]);
+            if (more) issue_s(t, t, xn);
+            commit<CG>(&barS[t]);
           }
+          if (dead) break;
+          commit<CG>(&vfree[x]);
+          if (more) commit<CG>(&kfree[xn]);
         }
       } else {
         for (int c = 0; c < 2 && c < C; ++c) {
           const int n = s_done + c;
           if (!chunk_s(c)) { dead = true; break; }
           issue_s(0, n & 1, n & 1);
-          mma_commit_elect(&barS[n & 1]);
-          mma_commit_elect(&kfree[n & 1]);
+          commit<CG>(&barS[n & 1]);
+          commit<CG>(&kfree[n & 1]);
         }
         for (int c = 0; c < C && !dead; ++c) {
           const int n = s_done + c, x = n & 1;
-          if (gave_up(&vready[x], n >> 1) || gave_up(&pready[2 * x], n >> 1)) { dead = true; break; }
-          tc_fence_after();
-          issue_o(0, x, x, 0, c == 0);
-          mma_commit_elect(&vfree[x]);
-          mma_commit_elect(barO);
+          if (gave_up(&vready[x], n >> 1)) { dead = true; break; }
+#pragma unroll
+          for (int h = 0; h < T::kHalves && !dead; ++h) {
+            if (gave_up(&pready[2 * x + h], n >> 1)) { dead = true; break; }
+            tc_fence_after();
+            issue_o(0, x, x, h, c == 0 && h == 0);
+          }
+          if (dead) break;
+          commit<CG>(&vfree[x]);
+          commit<CG>(barO);
           if (c + 2 < C) {
             if (!chunk_s(c + 2)) { dead = true; break; }
             issue_s(0, x, x);
-            mma_commit_elect(&barS[x]);
-            mma_commit_elect(&kfree[x]);
+            commit<CG>(&barS[x]);
+            commit<CG>(&kfree[x]);
           }
         }
       }
@@ -602,60 +717,95 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   // give-up, wait for what the MMA warp issued before its memory goes.
   if (dead) atomicExch(p.status, kStatusWaitTimeout);
   tc_fence_before();
-  const bool any_dead = __syncthreads_or(dead);
+  bool any_dead = __syncthreads_or(dead);
+  if constexpr (CG == 2) {
+    // both CTAs of the pair learn of a give-up in one (the word of a barrier not used again)
+    if (any_dead && tid == 0)
+      asm volatile(
+          "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.u32 [a], %1;\n\t"
+          "mapa.shared::cluster.u32 a, %0, 1;\n\tst.shared::cluster.u32 [a], %1;\n\t}" ::"r"(
+              smem_u32(s_tmem + 1)), "r"(1u)
+          : "memory");
+    cluster_sync();
+    any_dead = s_tmem[1] != 0u;
+  }
   tc_fence_after();
   if (any_dead) {
-    if (warp == T::kMma) mma_commit_elect(mdone);
-    wait_bounded(mdone, 0);
+    if (warp == T::kMma && rank == 0) commit<CG>(mdone);
+    gave_up(mdone, 0);
     __syncthreads();
   }
-  if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  if constexpr (CG == 2) cluster_sync();
+  if (warp == 0) {
+    if constexpr (CG == 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  }
 }
 
 }  // namespace
 }  // namespace dense
 
+// More than one tile of vectors per KV head: pairs of CTAs.
+static bool use_pairs(const Geom& g) { return g.R * (g.Hq / g.Hkv) > 128; }
+
 dense::Shape dense_tile_shape(const Geom& g, int window) {
   dense::Shape s;
+  auto set = [&](auto t) {
+    using T = decltype(t);
+    s.vt = T::kVecs;
+    s.tok = T::kTok;
+    s.ctas = dense_sms() / T::CG;
+  };
   s.g = g;
   s.G = g.Hq / g.Hkv;
-  s.vt = 128 * (g.D == 128 ? dense::TT<128>::kTiles : dense::TT<256>::kTiles);
+  if (use_pairs(g)) {
+    if (g.D == 128) set(dense::TT<128, 2>());
+    else set(dense::TT<256, 2>());
+  } else {
+    if (g.D == 128) set(dense::TT<128, 1>());
+    else set(dense::TT<256, 1>());
+  }
   s.tiles = (g.R * s.G + s.vt - 1) / s.vt;
-  s.tok = g.D == 128 ? dense::TT<128>::kTok : dense::TT<256>::kTok;
   s.window = window;
   s.least = 4;
-  s.by_unit = dense::unit_count(s) <= dense_sms();
+  s.by_unit = dense::unit_count(s) <= s.ctas;
   return s;
 }
 
 namespace {
 
-template <int D>
-cudaError_t launch_tile(const dense::Shape& s, const dense::Work& w, int ctas, cudaStream_t stream) {
-  using T = dense::TT<D>;
-  auto* kern = dense::dense_tile_kernel<D>;
+template <int D, int CG>
+cudaError_t launch_tile(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
+  using T = dense::TT<D, CG>;
+  auto* kern = dense::dense_tile_kernel<D, CG>;
   static_assert(T::kSmem <= 227 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(s.ctas * CG);
   cfg.blockDim = dim3(T::kThreads);
   cfg.dynamicSmemBytes = T::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, s, w);
 }
 
 }  // namespace
 
-cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, int ctas,
-                              cudaStream_t stream) {
-  return s.g.D == 256 ? launch_tile<256>(s, w, ctas, stream) : launch_tile<128>(s, w, ctas, stream);
+cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
+  if (use_pairs(s.g))
+    return s.g.D == 256 ? launch_tile<256, 2>(s, w, stream) : launch_tile<128, 2>(s, w, stream);
+  return s.g.D == 256 ? launch_tile<256, 1>(s, w, stream) : launch_tile<128, 1>(s, w, stream);
 }
 
 }  // namespace qsa
