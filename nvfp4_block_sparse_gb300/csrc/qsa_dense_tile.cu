@@ -25,13 +25,12 @@
 // Roles in a CTA (a warp group each unless noted):
 //   softmax   a thread per vector (tensor-memory lane): its row of S to registers, base
 //             (moved only where a weight would overflow), P = exp2(S c - base) as
-//             fp16 over the columns of S it has read, sums in fp32; 64 tokens at a time, so that
-//             no pass over the chunk comes before the exponentials; at the end
-//             of a part O from tensor memory to the output or to a record.  A group per tile
+//             fp16 over the columns of S it has read, 64 tokens at a time, sums in fp32;
+//             at the end of a part O from tensor memory to the output or to a record.  A
+//             group per tile
 //   dequant   codes and scales from the pages straight to registers one chunk ahead (they
 //             are in flight while the chunk before is converted), e2m1 x e4m3 exact in
-//             fp16 into double-buffered K and V tiles (128-byte swizzle); four warps
-//             convert K and four V, each set at its tile's pace
+//             fp16 into double-buffered K and V tiles (128-byte swizzle)
 //   MMA       one warp (of the pair's first CTA) issues every MMA in order.  With two tiles
 //             they take turns: O_0, S_0 of the next chunk, O_1, S_1, so that one tile's
 //             softmax runs under the other's products; with one, S has two buffers
@@ -71,16 +70,18 @@ struct TT {
   static constexpr int kTok = D == 256 && CG == 1 ? 64 : 128;  // tokens per chunk
   static constexpr int kHalves = kTok / 64;              // P is written 64 tokens at a time
   static constexpr int kSoft = 4 * kTiles;               // softmax warps
-  static constexpr int kDeq = 8;                         // dequantisation warps: four K, four V
+  // Dequantisation warps: four K and four V, or, where a CTA has half of every tile and
+  // two softmax groups, four that convert both.
+  static constexpr int kDeq = kTiles == 2 ? 4 : 8;
   static constexpr int kMma = kSoft + kDeq;              // the MMA warp; its group's others idle
   static constexpr int kThreads = 32 * (kMma + 4);
-  // Registers per thread: at launch, and after the roles part.
-  static constexpr int kRegs = kTiles == 2 ? 96 : 128;
-  static constexpr int kSoftRegs = kTiles == 2 ? 144 : 184;
-  static constexpr int kDeqRegs = kTiles == 2 ? 72 : 112;
-  static constexpr int kMmaRegs = kTiles == 2 ? 48 : 72;
-  static_assert(32 * (kSoft * kSoftRegs + kDeq * kDeqRegs + 4 * kMmaRegs) <= kThreads * kRegs,
-                "registers");
+  // Registers per thread after the roles part (128 at launch): the softmax holds a
+  // row's 128 logits.
+  static constexpr int kSoftRegs = kTiles == 2 ? 176 : 184;
+  static constexpr int kDeqRegs = kTiles == 2 ? 96 : 112;
+  static constexpr int kMmaRegs = kTiles == 2 ? 64 : 72;
+  static_assert(32 * (kSoft * kSoftRegs + kDeq * kDeqRegs + 4 * kMmaRegs) <= kThreads * 128 &&
+                    kThreads == 512, "registers");
   static constexpr int kVecs = 128 * CG * kTiles;        // query vectors of a unit
   static constexpr int kQBytes = 128 * D * 2;            // Q: D/64 blocks of 128 rows x 128 B
   static constexpr int kKRows = kTok / CG;               // K tile: tokens of this CTA
@@ -203,99 +204,121 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // ---- dequantisation --------------------------------------------------------------
-// Four warps convert this CTA's part of every chunk's K (kV false: kKRows tokens,
-// all dims) or V (all tokens, kVDims dims), a 16-byte piece (32 codes, two
-// scales) per lane and step.  A warp's pieces are neighbours in the page (512
+// A converter turns this CTA's part of every chunk's K (kV false: kKRows tokens, all
+// dims) or V (all tokens, kVDims dims) into a tile, four warps with a 16-byte piece
+// (32 codes, two scales) per lane and step.  A warp's pieces are neighbours in the page (512
 // contiguous bytes where a row has them) and the eight lanes that store together
 // hold eight rows, so the swizzle gives them distinct banks.
 template <class T, bool kV>
-__device__ __forceinline__ bool dequant_role(const Shape& sh, const Work& p, const Span& span,
-                                             int dw, int rank, uint8_t* tiles, uint64_t* ready,
-                                             uint64_t* freed) {
-  constexpr int D = T::D, kTok = T::kTok;
-  constexpr int kRows = kV ? kTok : T::kKRows, kDims = kV ? T::kVDims : D;
-  constexpr int kPieces = kDims / 32;                  // 16-byte pieces of a row
-  constexpr int kUnits = kRows * kPieces / 128;        // steps of a warp
-  constexpr int kBlk = kV ? T::kVBlk : T::kKBlk, kBytes = kV ? T::kVBytes : T::kKBytes;
-  const Geom& g = sh.g;
-  const int lane = threadIdx.x & 31;
-  const int psh = 31 - __clz(g.P);                          // log2 of the page size
-  const uint32_t page_rows = (uint32_t)g.Hkv << psh;        // token rows of a page, all heads
-  const int row0 = kV ? 0 : rank * kRows;                   // this CTA's first token of a chunk
-  const int dim0 = kV ? rank * kDims : 0;                   // and dim
-  const uint8_t* pool = (kV ? p.v_pool : p.k_pool) + dim0 / 2;
-  const uint8_t* sfs = (kV ? p.v_sf : p.k_sf) + dim0 / 16;
-  // row and piece of step i: eight rows of four pieces, or sixteen of two
-  auto row_of = [&](int i) {
-    const int u = dw + 4 * i;
-    return kPieces >= 4 ? 8 * (u % (kRows / 8)) + (lane & 7) : 16 * u + (lane & 15);
-  };
-  auto piece_of = [&](int i) {
-    const int u = dw + 4 * i;
-    return kPieces >= 4 ? 4 * (u / (kRows / 8)) + (lane >> 3) : lane >> 4;
-  };
+struct Converter {
+  static constexpr int D = T::D, kTok = T::kTok;
+  static constexpr int kRows = kV ? kTok : T::kKRows, kDims = kV ? T::kVDims : D;
+  static constexpr int kPieces = kDims / 32;                  // 16-byte pieces of a row
+  static constexpr int kUnits = kRows * kPieces / 128;        // steps of a warp
+  static constexpr int kBlk = kV ? T::kVBlk : T::kKBlk, kBytes = kV ? T::kVBytes : T::kKBytes;
+  // the pages of this CTA's tokens of a chunk: at most four, of 32 tokens and more
+  static constexpr int kMaxPages = kRows / (D == 128 ? 64 : 32);
+
+  const uint8_t *pool, *sfs;
+  uint8_t* tiles;
+  uint64_t *ready, *freed;
+  int dw, lane, row0, psh;
+  uint32_t page_rows;
   uint4 codes[kUnits];
   uint32_t sc[kUnits];
+  int pages[kMaxPages];
+
+  __device__ __forceinline__ Converter(const Shape& sh, const Work& p, int dw_, int rank,
+                                       uint8_t* tiles_, uint64_t* ready_, uint64_t* freed_)
+      : tiles(tiles_), ready(ready_), freed(freed_), dw(dw_) {
+    lane = threadIdx.x & 31;
+    psh = 31 - __clz(sh.g.P);                               // log2 of the page size
+    page_rows = (uint32_t)sh.g.Hkv << psh;                  // token rows of a page, all heads
+    row0 = kV ? 0 : rank * kRows;                           // this CTA's first token of a chunk
+    const int dim0 = kV ? rank * kDims : 0;                 // and dim
+    pool = (kV ? p.v_pool : p.k_pool) + dim0 / 2;
+    sfs = (kV ? p.v_sf : p.k_sf) + dim0 / 16;
+  }
+  // row and piece of step i: eight rows of four pieces, or sixteen of two
+  __device__ __forceinline__ int row_of(int i) const {
+    const int u = dw + 4 * i;
+    return kPieces >= 4 ? 8 * (u % (kRows / 8)) + (lane & 7) : 16 * u + (lane & 15);
+  }
+  __device__ __forceinline__ int piece_of(int i) const {
+    const int u = dw + 4 * i;
+    return kPieces >= 4 ? 4 * (u / (kRows / 8)) + (lane >> 3) : lane >> 4;
+  }
+  __device__ __forceinline__ void look_up(const Shape& sh, const Work& p, const Seg& seg, int chunk) {
+    const int32_t* pt = p.page_table + (size_t)seg.b * sh.g.MB;
+#pragma unroll
+    for (int i = 0; i < kMaxPages; ++i) {
+      const int beta = (chunk * kTok + row0 + i * (kRows / kMaxPages)) >> psh;
+      pages[i] = beta < sh.g.MB && seg.n_all > seg.lo_all ? __ldg(pt + beta) : -1;
+      if (pages[i] >= sh.g.NP) pages[i] = -1;
+    }
+  }
+  __device__ __forceinline__ void fetch(const Shape& sh, const Seg& seg, int chunk) {
+    const uint32_t head_rows = (uint32_t)seg.kvh << psh;   // token rows of a page before the head's
+    const int tok0 = chunk * kTok + row0;
+    const bool inner = tok0 >= seg.lo_all && tok0 + kRows <= seg.n_all;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int o = row_of(i);                          // token of this CTA's
+      int page = pages[0];
+#pragma unroll
+      for (int k = 1; k < kMaxPages; ++k)
+        if (o >= k * (kRows / kMaxPages)) page = pages[k];
+      codes[i] = make_uint4(0u, 0u, 0u, 0u);
+      sc[i] = 0u;
+      // what no row of the unit sees is not looked at
+      if (page >= 0 && (inner || (tok0 + o >= seg.lo_all && tok0 + o < seg.n_all))) {
+        const size_t row = (size_t)page * page_rows + head_rows + ((tok0 + o) & (sh.g.P - 1));
+        codes[i] = ldg128(pool + row * (D / 2) + 16 * piece_of(i));
+        sc[i] = ldg16(sfs + row * (D / 16) + 2 * piece_of(i));
+      }
+    }
+  }
+  // Chunk number `chunks` of the CTA into its tile; false when the wait for it gave up.
+  __device__ __forceinline__ bool convert(int chunks) {
+    const int x = chunks & 1, use = chunks >> 1;
+    if (use > 0 && gave_up(&freed[x], use - 1)) return false;
+    uint8_t* tile = tiles + x * kBytes;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const uint32_t s2 = e4m3x2_to_f16x2(sc[i]);
+      const uint32_t sx[2] = {prmt(s2, 0, 0x1010), prmt(s2, 0, 0x3232)};
+      const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int d8 = 4 * piece_of(i) + u;             // eight dims
+        *reinterpret_cast<uint4*>(tile + (d8 >> 3) * kBlk + sw128(row_of(i), d8 & 7)) =
+            dequant8(w[u], sx[u >> 1]);
+      }
+    }
+    fence_proxy_async_smem();
+    warp_arrive<T::CG>(&ready[x]);
+    return true;
+  }
+};
+
+// Every chunk through one converter, or through K's and then V's.
+template <class... C>
+__device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, const Span& span, C... conv) {
   int chunks = 0;
   Cursor cursor(span);
   Seg seg;
   while (cursor.next(sh, p.seqlens, seg)) {
-    const int32_t* pt = p.page_table + (size_t)seg.b * g.MB;
-    const uint32_t head_rows = (uint32_t)seg.kvh << psh;   // token rows of a page before the head's
-    // the pages of this CTA's tokens of a chunk: at most four, of 32 tokens and more
-    constexpr int kMaxPages = kRows / (D == 128 ? 64 : 32);
-    int pages[kMaxPages];
-    auto pages_of = [&](int chunk) {
-#pragma unroll
-      for (int i = 0; i < kMaxPages; ++i) {
-        const int beta = (chunk * kTok + row0 + i * (kRows / kMaxPages)) >> psh;
-        pages[i] = beta < g.MB && seg.n_all > seg.lo_all ? __ldg(pt + beta) : -1;
-        if (pages[i] >= g.NP) pages[i] = -1;
-      }
-    };
-    auto fetch = [&](int chunk) {
-      const int tok0 = chunk * kTok + row0;
-      const bool inner = tok0 >= seg.lo_all && tok0 + kRows <= seg.n_all;
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int o = row_of(i);                          // token of this CTA's
-        int page = pages[0];
-#pragma unroll
-        for (int k = 1; k < kMaxPages; ++k)
-          if (o >= k * (kRows / kMaxPages)) page = pages[k];
-        codes[i] = make_uint4(0u, 0u, 0u, 0u);
-        sc[i] = 0u;
-        // what no row of the unit sees is not looked at
-        if (page >= 0 && (inner || (tok0 + o >= seg.lo_all && tok0 + o < seg.n_all))) {
-          const size_t row = (size_t)page * page_rows + head_rows + ((tok0 + o) & (g.P - 1));
-          codes[i] = ldg128(pool + row * (D / 2) + 16 * piece_of(i));
-          sc[i] = ldg16(sfs + row * (D / 16) + 2 * piece_of(i));
-        }
-      }
-    };
-    pages_of(seg.chunk0);
-    fetch(seg.chunk0);
-    if (seg.todo > 1) pages_of(seg.chunk0 + 1);
+    (conv.look_up(sh, p, seg, seg.chunk0), ...);
+    (conv.fetch(sh, seg, seg.chunk0), ...);
+    if (seg.todo > 1) (conv.look_up(sh, p, seg, seg.chunk0 + 1), ...);
     for (int c = 0; c < seg.todo; ++c, ++chunks) {
-      const int x = chunks & 1, use = chunks >> 1;
-      if (use > 0 && gave_up(&freed[x], use - 1)) return false;
-      uint8_t* tile = tiles + x * kBytes;
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const uint32_t s2 = e4m3x2_to_f16x2(sc[i]);
-        const uint32_t sx[2] = {prmt(s2, 0, 0x1010), prmt(s2, 0, 0x3232)};
-        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int d8 = 4 * piece_of(i) + u;             // eight dims
-          *reinterpret_cast<uint4*>(tile + (d8 >> 3) * kBlk + sw128(row_of(i), d8 & 7)) =
-              dequant8(w[u], sx[u >> 1]);
-        }
-      }
-      fence_proxy_async_smem();
-      warp_arrive<T::CG>(&ready[x]);
-      if (c + 1 < seg.todo) fetch(seg.chunk0 + c + 1);
-      if (c + 2 < seg.todo) pages_of(seg.chunk0 + c + 2);
+      auto step = [&](auto& k) {
+        if (!k.convert(chunks)) return false;
+        if (c + 1 < seg.todo) k.fetch(sh, seg, seg.chunk0 + c + 1);
+        if (c + 2 < seg.todo) k.look_up(sh, p, seg, seg.chunk0 + c + 2);
+        return true;
+      };
+      if (!(step(conv) && ...)) return false;
     }
   }
   return true;
@@ -460,57 +483,37 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         const int tok0 = (seg.chunk0 + c) * kTok;
         const bool edge = tok0 + kTok > seg.n_least || tok0 < seg.lo_most ||
                           now_live != (1u << (kTok / 32)) - 1u;
-        float z[64];
-        auto load = [&](int h) {       // 64 tokens of S, what the row does not see at -inf
-          tmem_ld32(tS + 64 * h, z);
-          tmem_ld32(tS + 64 * h + 32, z + 32);
-          tmem_wait_ld();
-          if (edge) {
+        // The row's logits, those it does not see at -inf.
+        float z[kTok];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              const int tok = tok0 + 64 * h + i;
-              if (tok >= n || tok < lo || !((now_live >> (2 * h + (i >> 5))) & 1u)) z[i] = -INFINITY;
-            }
+        for (int i = 0; i < kTok / 32; ++i) tmem_ld32(tS + 32 * i, z + 32 * i);
+        tmem_wait_ld();
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < kTok; ++i) {
+            const int tok = tok0 + i;
+            if (tok >= n || tok < lo || !((now_live >> (i >> 5)) & 1u)) z[i] = -INFINITY;
           }
-        };
-        auto largest = [&]() {
-          float m8[8];
+        }
+        float m8[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) m8[i] = z[i];
+        for (int i = 0; i < 8; ++i) m8[i] = z[i];
 #pragma unroll
-          for (int i = 8; i < 64; i += 2) m8[(i >> 1) & 7] = fmax3(m8[(i >> 1) & 7], z[i], z[i + 1]);
-          return fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-        };
-        // Moves the base where a logit would overflow an fp16 weight, with what has been
-        // summed on the old one: O (complete up to the chunk before), the sum and, from
-        // the second half, the first half's weights.
-        auto rebase = [&](float top, bool second) {
-          const bool moves = top > base + kHeadroom;
-          if (!__any_sync(0xffffffffu, moves)) return true;
+        for (int i = 8; i < kTok; i += 2) m8[(i >> 1) & 7] = fmax3(m8[(i >> 1) & 7], z[i], z[i + 1]);
+        const float top = cq * fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
+                                     fmaxf(m8[6], m8[7]));
+        // The base moves where a logit would overflow an fp16 weight, and with it what has
+        // been summed on the old one.
+        const bool moves = top > base + kHeadroom;
+        if (__any_sync(0xffffffffu, moves)) {
           const float nb = moves ? top : base;
           const float alpha = exp2_approx(base - nb);
           base = nb;
           sum.x *= alpha;
           sum.y *= alpha;
-          if (second) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float w16[16];
-              uint32_t h[16];
-              tmem_ld16(tS + 16 * i, w16);
-              tmem_wait_ld();
-#pragma unroll
-              for (int u = 0; u < 16; ++u) {   // in fp32: alpha may be far below fp16's range
-                const uint32_t w = __float_as_uint(w16[u]);
-                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                h[u] = pack_half2(v.x * alpha, v.y * alpha);
-              }
-              tmem_st16u(tS + 16 * i, h);
-            }
-          }
           if (c > 0) {
-            // with two tiles barS has said that O is complete
-            if (kTiles == 1 && gave_up(barO, chunks - 1)) return false;
+            // with two tiles barS has said that O is complete up to the chunk before
+            if (kTiles == 1 && gave_up(barO, chunks - 1)) { dead = true; break; }
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -522,40 +525,27 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
               tmem_st16(tO + 16 * i, o16);
             }
           }
-          tmem_wait_st();
-          return true;
-        };
-        auto weights = [&](int h) {    // P of half h, over the first columns it was read from
+        }
+        // P, 64 tokens at a time, over the first columns they were read from.
+#pragma unroll
+        for (int h = 0; h < T::kHalves; ++h) {
           const float2 c2 = make_float2(cq, cq), b2 = make_float2(-base, -base);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 a = fma2(make_float2(z[32 * q + 2 * i], z[32 * q + 2 * i + 1]), c2, b2);
+              const int k = 64 * h + 32 * q + 2 * i;
+              const float2 a = fma2(make_float2(z[k], z[k + 1]), c2, b2);
               const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
               sum = add2(sum, e);
               pk[i] = pack_half2(e.x, e.y);
             }
             tmem_st16u(tS + 64 * h + 16 * q, pk);
           }
-        };
-        auto publish = [&](int h) {
           tmem_wait_st();
           tc_fence_before();
           warp_arrive<CG>(&pready[2 * y + h]);
-        };
-        load(0);
-        if (!rebase(largest() * cq, false)) { dead = true; break; }
-        weights(0);
-        if (T::kHalves == 2) {
-          load(1);
-          if (!rebase(largest() * cq, true)) { dead = true; break; }
-          publish(0);      // only now: the second half may have moved its base
-          weights(1);
-          publish(1);
-        } else {
-          publish(0);
         }
       }
       if (dead) break;
@@ -616,9 +606,15 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     // ==== dequantisation =============================================================
     regs_down<T::kDeqRegs>();
     const int dw = (warp - T::kSoft) & 3;
-    dead = warp - T::kSoft < 4
-               ? !dequant_role<T, false>(sh, p, span, dw, rank, sK, kready, kfree)
-               : !dequant_role<T, true>(sh, p, span, dw, rank, sV, vready, vfree);
+    using CK = Converter<T, false>;
+    using CV = Converter<T, true>;
+    if constexpr (T::kDeq == 4)
+      dead = !convert_all(sh, p, span, CK(sh, p, dw, rank, sK, kready, kfree),
+                          CV(sh, p, dw, rank, sV, vready, vfree));
+    else if (warp - T::kSoft < 4)
+      dead = !convert_all(sh, p, span, CK(sh, p, dw, rank, sK, kready, kfree));
+    else
+      dead = !convert_all(sh, p, span, CV(sh, p, dw, rank, sV, vready, vfree));
   } else if (regs_down<T::kMmaRegs>(), warp == T::kMma && rank == 0) {
     // ==== MMA issue ==================================================================
     const uint32_t id_s = f16_idesc(128 * CG, kTok), id_o = f16_idesc(128 * CG, D) | kIdescBMn;
@@ -661,17 +657,17 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         issue_s(1, 1, s_done & 1);
         commit<CG>(&barS[1]);
         commit<CG>(&kfree[s_done & 1]);
+        // The tiles of a chunk are waited for while the products before it run.
+        if (gave_up(&vready[s_done & 1], s_done >> 1) || (C > 1 && !chunk_s(1))) { dead = true; break; }
         for (int c = 0; c < C && !dead; ++c) {
           const int n = s_done + c, x = n & 1, xn = (n + 1) & 1;
           const bool more = c + 1 < C;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (t == 0 && gave_up(&vready[x], n >> 1)) { dead = true; break; }
             if (gave_up(&pready[2 * t], n)) { dead = true; break; }
             tc_fence_after();
             issue_o(t, t, x, 0, c == 0);
             if (gave_up(&pready[2 * t + 1], n)) { dead = true; break; }
-            if (t == 0 && more && gave_up(&kready[xn], (n + 1) >> 1)) { dead = true; break; }
             tc_fence_after();
             issue_o(t, t, x, 1, false);
             if (more) issue_s(t, t, xn);
@@ -679,7 +675,13 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           }
           if (dead) break;
           commit<CG>(&vfree[x]);
-          if (more) commit<CG>(&kfree[xn]);
+          if (more) {
+            commit<CG>(&kfree[xn]);
+            if (gave_up(&vready[xn], (n + 1) >> 1) || (c + 2 < C && !chunk_s(c + 2))) {
+              dead = true;
+              break;
+            }
+          }
         }
       } else {
         for (int c = 0; c < 2 && c < C; ++c) {
