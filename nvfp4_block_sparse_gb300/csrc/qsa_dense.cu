@@ -676,7 +676,8 @@ dense::Shape decode_shape(const Geom& g, int window) {
   s.G = g.Hq / g.Hkv;
   s.vt = decode_cols(g);
   s.tiles = (g.R * s.G + s.vt - 1) / s.vt;
-  s.tok = g.D == 256 ? 32 : (s.vt == 8 ? C128a::TOK : C128b::TOK);
+  const int tok = g.D == 256 ? 32 : (s.vt == 8 ? C128a::TOK : C128b::TOK);
+  s.tok_sh = tok == 64 ? 6 : 5;
   s.window = window;
   s.least = 16;
   s.ctas = dense_sms();

@@ -38,7 +38,7 @@ struct Shape {
   int G;         // query heads per KV head
   int vt;        // query vectors per tile
   int tiles;     // tiles per request
-  int tok;       // tokens per chunk
+  int tok_sh;    // log2 of the tokens per chunk
   int window;    // tokens a row looks back over; 0: all
   int least;     // chunks a CTA takes at least
   int ctas;      // CTAs of the grid
@@ -73,19 +73,35 @@ __device__ __forceinline__ int first_seen(int n, int window) {
   return window > 0 && n > window ? n - window : 0;
 }
 
-// Chunks [x, y) of (request of length L, tile); x == y: no token.
-__device__ __forceinline__ int2 chunk_range(const Shape& s, int L, int tile) {
+// What the rows of a tile see of a request of length L.
+struct Sight {
+  int vec0, vecs;            // query vectors of the tile
+  int n_all, n_least;        // tokens that the last / first row sees
+  int lo_all, lo_most;       // first token that the first / last row sees
+  int first, count;          // chunks; at least one (with no token: its zeros are written)
+};
+
+__device__ __forceinline__ Sight sight_of(const Shape& s, int L, int tile) {
+  Sight v;
   const int cap = s.g.MB * s.g.P;
-  const int v0 = tile * s.vt, v1 = min(v0 + s.vt, s.g.R * s.G);
-  const int hi = visible_tokens(L, s.g.R, (v1 - 1) / s.G, cap);
-  const int lo = first_seen(visible_tokens(L, s.g.R, v0 / s.G, cap), s.window);
-  if (hi <= lo) return make_int2(0, 0);
-  return make_int2(lo / s.tok, (hi + s.tok - 1) / s.tok);
+  v.vec0 = tile * s.vt;
+  v.vecs = min(s.vt, s.g.R * s.G - v.vec0);
+  v.n_all = visible_tokens(L, s.g.R, (uint32_t)(v.vec0 + v.vecs - 1) / (uint32_t)s.G, cap);
+  v.n_least = visible_tokens(L, s.g.R, (uint32_t)v.vec0 / (uint32_t)s.G, cap);
+  v.lo_all = first_seen(v.n_least, s.window);
+  v.lo_most = first_seen(v.n_all, s.window);
+  v.first = 0;
+  v.count = 1;
+  if (v.n_all > v.lo_all) {
+    v.first = v.lo_all >> s.tok_sh;
+    v.count = ((v.n_all - 1) >> s.tok_sh) + 1 - v.first;
+  }
+  return v;
 }
 
 __device__ __forceinline__ int chunk_count(const Shape& s, const int32_t* seqlens, int group) {
-  const int2 r = chunk_range(s, seqlens[group / s.tiles], group % s.tiles);
-  return max(1, r.y - r.x);
+  const uint32_t b = (uint32_t)group / (uint32_t)s.tiles;
+  return sight_of(s, seqlens[b], group - (int)b * s.tiles).count;
 }
 
 // This CTA's part of the work, in the groups (request, tile) in order, each
@@ -149,15 +165,12 @@ __device__ __forceinline__ Span plan_span(const Shape& s, const int32_t* seqlens
 }
 
 // The part of one unit that a CTA does.
-struct Seg {
+struct Seg : Sight {
   int b, tile, kvh;
+  int L;
   int c_at, todo;            // chunks of the unit before this part, and in it
   bool begins, ends;         // the part holds the unit's first / last chunk
-  int chunk0;                // first chunk (token chunk0 * tok)
-  int L;
-  int vec0, vecs;            // query vectors of the unit
-  int n_all, n_least;        // tokens that the last / first row sees
-  int lo_all, lo_most;       // first token that the first / last row sees
+  int chunk0;                // first chunk of the part
 };
 
 // Walks a span's parts in order; every role of a CTA walks its own copy.
@@ -168,27 +181,19 @@ struct Cursor {
       : at(s.begin), end(s.end), group_at(s.group_at), group(s.group) {}
   __device__ __forceinline__ bool next(const Shape& s, const int32_t* seqlens, Seg& g) {
     if (at >= end) return false;
-    g.b = group / s.tiles;
-    g.tile = group % s.tiles;
+    g.b = (int)((uint32_t)group / (uint32_t)s.tiles);
+    g.tile = group - g.b * s.tiles;
     g.L = seqlens[g.b];
-    const int2 range = chunk_range(s, g.L, g.tile);
-    const int count = max(1, range.y - range.x);
-    const long long in_group = at - group_at;
-    g.kvh = (int)(in_group / count);
-    g.c_at = (int)(in_group % count);
-    g.todo = (int)min((long long)(count - g.c_at), end - at);
+    static_cast<Sight&>(g) = sight_of(s, g.L, g.tile);
+    const uint32_t in_group = (uint32_t)(at - group_at);   // (at most 2^17 chunks of 256 heads)
+    g.kvh = (int)(in_group / (uint32_t)g.count);
+    g.c_at = (int)in_group - g.kvh * g.count;
+    g.todo = (int)min((long long)(g.count - g.c_at), end - at);
     g.begins = g.c_at == 0;
-    g.ends = g.c_at + g.todo == count;
-    g.chunk0 = range.x + g.c_at;
-    const int cap = s.g.MB * s.g.P;
-    g.vec0 = g.tile * s.vt;
-    g.vecs = min(s.vt, s.g.R * s.G - g.vec0);
-    g.n_all = visible_tokens(g.L, s.g.R, (g.vec0 + g.vecs - 1) / s.G, cap);
-    g.n_least = visible_tokens(g.L, s.g.R, g.vec0 / s.G, cap);
-    g.lo_all = first_seen(g.n_least, s.window);
-    g.lo_most = first_seen(g.n_all, s.window);
+    g.ends = g.c_at + g.todo == g.count;
+    g.chunk0 = g.first + g.c_at;
     at += g.todo;
-    if (at == group_at + (long long)count * s.g.Hkv) {
+    if (at == group_at + (long long)g.count * s.g.Hkv) {
       group_at = at;
       ++group;
     }

@@ -28,8 +28,8 @@
 //             fp16 over the columns of S it has read, 64 tokens at a time, sums in fp32;
 //             at the end of a part O from tensor memory to the output or to a record.  A
 //             group per tile
-//   dequant   codes and scales from the pages straight to registers one chunk ahead (they
-//             are in flight while the chunk before is converted), e2m1 x e4m3 exact in
+//   dequant   codes and scales from the pages straight to registers two chunks ahead (they
+//             are in flight while the chunks before are converted), e2m1 x e4m3 exact in
 //             fp16 into double-buffered K and V tiles (128-byte swizzle)
 //   MMA       one warp (of the pair's first CTA) issues every MMA in order.  With two tiles
 //             they take turns: O_0, S_0 of the next chunk, O_1, S_1, so that one tile's
@@ -40,7 +40,9 @@
 // P lies over S: S of the next chunk is issued behind the O that reads P, and
 // MMAs of one thread run in order, so no barrier guards the reuse.
 //
-// Tensor memory (512 columns): the two S buffers from column 0, O from 256.
+// Tensor memory (512 columns): the two S buffers from column 0, O from 256, and for
+// single CTAs Q (384 at head_dim 128, 128 at 256), which leaves shared memory's
+// bandwidth to K and V.
 // mbarriers, all waits bounded (2 s; a wait that gives up sets the status word).
 // Arrivals are one per warp; those for the MMA warp go to the first CTA's barrier,
 // commits to both CTAs':
@@ -49,7 +51,11 @@
 //   kfree/vfree[x]    MMAs that read tile x complete               (commit)
 //   barS[y]       S buffer y complete -- and, with two tiles, every MMA before it,
 //                 so also the tile's O so far; once more after a part's last O   (commit)
-//   barO          O complete (one tile)                            (commit)
+//   barO          O complete up to a chunk (one tile)              (commit)
+//   partO         O complete at the end of a part (one tile)       (commit)
+// A phase of a barrier is only told from its neighbours, so every waiter is at most
+// one phase behind: barO is waited for only where barS has said that the phase
+// before is complete, and the part's end has a barrier of its own.
 //   pready[y][h]  half h of P in buffer y written                  (four softmax warps)
 #include "qsa_dense.cuh"
 #include "qsa_tc.cuh"
@@ -90,9 +96,15 @@ struct TT {
   static constexpr int kVDims = D / CG;                  // V tile: dims of this CTA
   static constexpr int kVBlk = kTok * 128;
   static constexpr int kVBytes = kTok * kVDims * 2;
-  static constexpr int kBars = 17;
-  static constexpr int kSmem = 1024 + kTiles * kQBytes + 2 * kKBytes + 2 * kVBytes + kBars * 8 + 24;
+  static constexpr int kBars = 18;
+  static constexpr int kSmem = 1024 + kTiles * kQBytes + 2 * kKBytes + 2 * kVBytes + kBars * 8 + 24 +
+                               kTiles * 128 * 4;
+  // Tensor-memory columns of O and, for single CTAs, of Q: with half of every operand
+  // missing from the SM's shared memory (a pair's) Q's reads fit there.
   static constexpr uint32_t kOCol = 256;
+  static constexpr bool kQTmem = CG == 1;
+  static constexpr uint32_t kQCol = D == 128 ? 384 : 128;
+  static_assert(kQCol + D / 2 <= 512 && 2 * kTok <= 256, "tensor-memory columns");
 };
 
 // 32 columns of this thread's lane.
@@ -115,15 +127,22 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 // every weight is finite its relative precision does not depend on the base.
 constexpr float kHeadroom = 15.f;
 
-__device__ __forceinline__ uint4 ldg128(const void* p) {
+// Read-only loads, zero where `on` is false.
+__device__ __forceinline__ uint4 ldg128(const void* p, bool on) {
   uint4 r;
-  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\t"
+      "mov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t@q ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w) : "l"(p), "r"((uint32_t)on));
   return r;
 }
-__device__ __forceinline__ uint32_t ldg16(const void* p) {
-  uint16_t r;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
+// (into a 32-bit register: a 16-bit one would be widened on the spot, waiting for the load)
+__device__ __forceinline__ uint32_t ldg16(const void* p, bool on) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\tmov.u32 %0, 0;\n\t"
+      "@q ld.global.nc.u16 %0, [%1];\n\t}"
+      : "=&r"(r) : "l"(p), "r"((uint32_t)on));
   return r;
 }
 
@@ -144,9 +163,29 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // ---- barriers across the pair ------------------------------------------------
-// A warp's bounded wait: true when it gave up, in every lane.
+// One wait of at most about 20 us during which the thread sleeps in hardware.
+__device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+
+// A warp's bounded wait: true when it gave up, in every lane.  It sleeps: a dozen
+// warps polling (and reading the clock) slowed everything else on the SM down several times.
 __device__ __forceinline__ bool gave_up(uint64_t* bar, uint32_t parity) {
-  return __any_sync(0xffffffffu, !wait_bounded(bar, parity & 1));
+  bool ok = sleep_wait(bar, parity & 1);
+  if (!ok) {
+    const unsigned long long t0 = now_ns();
+    while (!(ok = sleep_wait(bar, parity & 1)) && now_ns() - t0 <= kWaitNs) {
+    }
+  }
+  return __any_sync(0xffffffffu, !ok);
 }
 
 // One arrival of the warp at the first CTA's barrier.
@@ -204,18 +243,17 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // ---- dequantisation --------------------------------------------------------------
-// A converter turns this CTA's part of every chunk's K (kV false: kKRows tokens, all
-// dims) or V (all tokens, kVDims dims) into a tile, four warps with a 16-byte piece
-// (32 codes, two scales) per lane and step.  A warp's pieces are neighbours in the page (512
-// contiguous bytes where a row has them) and the eight lanes that store together
-// hold eight rows, so the swizzle gives them distinct banks.
-template <class T, bool kV>
+// A converter turns this CTA's part of every chunk's K (kKRows tokens, all dims) or V
+// (all tokens, kVDims dims) into a tile, four warps with a 16-byte piece
+// (32 codes, two scales) per lane and step.  Neighbouring lanes read neighbouring
+// pieces; eight that store together have two rows (or four) of the 64-dim blocks.
+template <class T, int kRows_, int kDims_>
 struct Converter {
   static constexpr int D = T::D, kTok = T::kTok;
-  static constexpr int kRows = kV ? kTok : T::kKRows, kDims = kV ? T::kVDims : D;
+  static constexpr int kRows = kRows_, kDims = kDims_;        // tokens and dims of the tile
   static constexpr int kPieces = kDims / 32;                  // 16-byte pieces of a row
   static constexpr int kUnits = kRows * kPieces / 128;        // steps of a warp
-  static constexpr int kBlk = kV ? T::kVBlk : T::kKBlk, kBytes = kV ? T::kVBytes : T::kKBytes;
+  static constexpr int kBlk = kRows * 128, kBytes = kRows * kDims * 2;
   // the pages of this CTA's tokens of a chunk: at most four, of 32 tokens and more
   static constexpr int kMaxPages = kRows / (D == 128 ? 64 : 32);
 
@@ -223,76 +261,109 @@ struct Converter {
   uint8_t* tiles;
   uint64_t *ready, *freed;
   int dw, lane, row0, psh;
-  uint32_t page_rows;
-  uint4 codes[kUnits];
-  uint32_t sc[kUnits];
+  size_t page_rows;
+  uint32_t at_c[kUnits], at_s[kUnits];   // a step's codes and scales within their page
+  uint4 codes[2][kUnits];      // two chunks are on their way
+  uint32_t sc[2][kUnits];
   int pages[kMaxPages];
+  // Page ids: lane i has that of block blk0 + i, and `later` of blk0 + 32 + i.  (Looked up
+  // chunk by chunk they would queue behind the chunks' own loads.)
+  int blk0, ids, later;
 
-  __device__ __forceinline__ Converter(const Shape& sh, const Work& p, int dw_, int rank,
-                                       uint8_t* tiles_, uint64_t* ready_, uint64_t* freed_)
-      : tiles(tiles_), ready(ready_), freed(freed_), dw(dw_) {
+  __device__ __forceinline__ Converter(const Shape& sh, const uint8_t* codes_, const uint8_t* scales_,
+                                       int token0, int dim0, int dw_, uint8_t* tiles_,
+                                       uint64_t* ready_, uint64_t* freed_)
+      : pool(codes_ + dim0 / 2), sfs(scales_ + dim0 / 16), tiles(tiles_), ready(ready_), freed(freed_),
+        dw(dw_), row0(token0) {
     lane = threadIdx.x & 31;
     psh = 31 - __clz(sh.g.P);                               // log2 of the page size
-    page_rows = (uint32_t)sh.g.Hkv << psh;                  // token rows of a page, all heads
-    row0 = kV ? 0 : rank * kRows;                           // this CTA's first token of a chunk
-    const int dim0 = kV ? rank * kDims : 0;                 // and dim
-    pool = (kV ? p.v_pool : p.k_pool) + dim0 / 2;
-    sfs = (kV ? p.v_sf : p.k_sf) + dim0 / 16;
+    page_rows = (size_t)sh.g.Hkv << psh;                    // token rows of a page, all heads
   }
   // row and piece of step i: eight rows of four pieces, or sixteen of two
   __device__ __forceinline__ int row_of(int i) const {
     const int u = dw + 4 * i;
-    return kPieces >= 4 ? 8 * (u % (kRows / 8)) + (lane & 7) : 16 * u + (lane & 15);
+    return kPieces >= 4 ? 8 * (u % (kRows / 8)) + (lane >> 2) : 16 * u + (lane >> 1);
   }
   __device__ __forceinline__ int piece_of(int i) const {
     const int u = dw + 4 * i;
-    return kPieces >= 4 ? 4 * (u / (kRows / 8)) + (lane >> 3) : lane >> 4;
+    return kPieces >= 4 ? 4 * (u / (kRows / 8)) + (lane & 3) : lane & 1;
   }
-  __device__ __forceinline__ void look_up(const Shape& sh, const Work& p, const Seg& seg, int chunk) {
-    const int32_t* pt = p.page_table + (size_t)seg.b * sh.g.MB;
-#pragma unroll
-    for (int i = 0; i < kMaxPages; ++i) {
-      const int beta = (chunk * kTok + row0 + i * (kRows / kMaxPages)) >> psh;
-      pages[i] = beta < sh.g.MB && seg.n_all > seg.lo_all ? __ldg(pt + beta) : -1;
-      if (pages[i] >= sh.g.NP) pages[i] = -1;
-    }
+  // which of the chunk's pages step i reads: the same for all four warps
+  __host__ __device__ static constexpr int slot_of(int i) {
+    return (kPieces >= 4 ? 8 * ((4 * i) % (kRows / 8)) : 64 * i) / (kRows / kMaxPages);
   }
-  __device__ __forceinline__ void fetch(const Shape& sh, const Seg& seg, int chunk) {
-    const uint32_t head_rows = (uint32_t)seg.kvh << psh;   // token rows of a page before the head's
-    const int tok0 = chunk * kTok + row0;
-    const bool inner = tok0 >= seg.lo_all && tok0 + kRows <= seg.n_all;
+  __device__ __forceinline__ int page_id(const Shape& sh, const Work& p, const Seg& seg, int beta) {
+    return beta < sh.g.MB && seg.n_all > seg.lo_all
+               ? __ldg(p.page_table + (size_t)seg.b * sh.g.MB + beta) : -1;
+  }
+  __device__ __forceinline__ void begin(const Shape& sh, const Work& p, const Seg& seg) {
+    blk0 = (seg.chunk0 * kTok + row0) >> psh;
+    ids = page_id(sh, p, seg, blk0 + lane);
+    later = page_id(sh, p, seg, blk0 + 32 + lane);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int o = row_of(i);                          // token of this CTA's
-      int page = pages[0];
+      const uint32_t row = ((uint32_t)seg.kvh << psh) + ((row0 + row_of(i)) & (sh.g.P - 1));
+      at_c[i] = row * (D / 2) + 16 * piece_of(i);
+      at_s[i] = row * (D / 16) + 2 * piece_of(i);
+    }
+  }
+  __device__ __forceinline__ void look_up(const Shape& sh, const Work& p, const Seg& seg, int chunk) {
+    const int first = (chunk * kTok + row0) >> psh;
+    if (first - blk0 >= 32) {
+      blk0 += 32;
+      ids = later;
+      later = page_id(sh, p, seg, blk0 + 32 + lane);
+    }
 #pragma unroll
-      for (int k = 1; k < kMaxPages; ++k)
-        if (o >= k * (kRows / kMaxPages)) page = pages[k];
-      codes[i] = make_uint4(0u, 0u, 0u, 0u);
-      sc[i] = 0u;
+    for (int i = 0; i < kMaxPages; ++i) {
+      const int at = ((chunk * kTok + row0 + i * (kRows / kMaxPages)) >> psh) - blk0;
+      const int here = __shfl_sync(0xffffffffu, ids, at & 31);
+      const int next = __shfl_sync(0xffffffffu, later, at & 31);
+      pages[i] = at < 32 ? here : next;
+    }
+  }
+  template <int B>
+  __device__ __forceinline__ void fetch(const Shape& sh, const Seg& seg, int chunk) {
+    const int tok0 = chunk * kTok + row0;
+    const bool inner = tok0 >= seg.lo_all && tok0 + kRows <= seg.n_all;
+    const uint8_t *pc[kMaxPages], *ps[kMaxPages];
+    bool there[kMaxPages];
+#pragma unroll
+    for (int k = 0; k < kMaxPages; ++k) {
+      there[k] = pages[k] >= 0 && pages[k] < sh.g.NP;
+      const size_t row = there[k] ? (size_t)pages[k] * page_rows : 0;
+      pc[k] = pool + row * (D / 2);
+      ps[k] = sfs + row * (D / 16);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int k = slot_of(i), tok = tok0 + row_of(i);
       // what no row of the unit sees is not looked at
-      if (page >= 0 && (inner || (tok0 + o >= seg.lo_all && tok0 + o < seg.n_all))) {
-        const size_t row = (size_t)page * page_rows + head_rows + ((tok0 + o) & (sh.g.P - 1));
-        codes[i] = ldg128(pool + row * (D / 2) + 16 * piece_of(i));
-        sc[i] = ldg16(sfs + row * (D / 16) + 2 * piece_of(i));
-      }
+      const bool on = there[k] && (inner || (tok >= seg.lo_all && tok < seg.n_all));
+      codes[B][i] = ldg128(pc[k] + at_c[i], on);
+      sc[B][i] = ldg16(ps[k] + at_s[i], on);
     }
   }
   // Chunk number `chunks` of the CTA into its tile; false when the wait for it gave up.
+  template <int B>
   __device__ __forceinline__ bool convert(int chunks) {
     const int x = chunks & 1, use = chunks >> 1;
     if (use > 0 && gave_up(&freed[x], use - 1)) return false;
     uint8_t* tile = tiles + x * kBytes;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const uint32_t s2 = e4m3x2_to_f16x2(sc[i]);
+      const uint32_t s2 = e4m3x2_to_f16x2(sc[B][i]);
       const uint32_t sx[2] = {prmt(s2, 0, 0x1010), prmt(s2, 0, 0x3232)};
-      const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+      // Eight lanes store together: two rows of four pieces, whose upper two (another
+      // 64-dim block, the same banks) go in another order; or four rows of two.
+      const bool flip = kPieces >= 4 && (lane & 2);
+      const uint4 c = codes[B][i];
+      const uint32_t w[4] = {flip ? c.z : c.x, flip ? c.w : c.y, flip ? c.x : c.z, flip ? c.y : c.w};
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int d8 = 4 * piece_of(i) + u;             // eight dims
+        const int d8 = 4 * piece_of(i) + (flip ? u ^ 2 : u);   // eight dims
         *reinterpret_cast<uint4*>(tile + (d8 >> 3) * kBlk + sw128(row_of(i), d8 & 7)) =
-            dequant8(w[u], sx[u >> 1]);
+            dequant8(w[u], flip ? sx[(u >> 1) ^ 1] : sx[u >> 1]);
       }
     }
     fence_proxy_async_smem();
@@ -308,17 +379,25 @@ __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, cons
   Cursor cursor(span);
   Seg seg;
   while (cursor.next(sh, p.seqlens, seg)) {
-    (conv.look_up(sh, p, seg, seg.chunk0), ...);
-    (conv.fetch(sh, seg, seg.chunk0), ...);
-    if (seg.todo > 1) (conv.look_up(sh, p, seg, seg.chunk0 + 1), ...);
-    for (int c = 0; c < seg.todo; ++c, ++chunks) {
-      auto step = [&](auto& k) {
-        if (!k.convert(chunks)) return false;
-        if (c + 1 < seg.todo) k.fetch(sh, seg, seg.chunk0 + c + 1);
-        if (c + 2 < seg.todo) k.look_up(sh, p, seg, seg.chunk0 + c + 2);
-        return true;
-      };
-      if (!(step(conv) && ...)) return false;
+    auto get = [&]<int B>(auto& k, int c) {
+      k.look_up(sh, p, seg, seg.chunk0 + c);
+      k.template fetch<B>(sh, seg, seg.chunk0 + c);
+    };
+    (conv.begin(sh, p, seg), ...);
+    (get.template operator()<0>(conv, 0), ...);
+    if (seg.todo > 1) (get.template operator()<1>(conv, 1), ...);
+    auto step = [&]<int B>(auto& k, int c) {
+      if (!k.template convert<B>(chunks)) return false;
+      if (c + 2 < seg.todo) get.template operator()<B>(k, c + 2);
+      return true;
+    };
+    for (int c = 0; c < seg.todo; c += 2) {
+      if (!(step.template operator()<0>(conv, c) && ...)) return false;
+      ++chunks;
+      if (c + 1 < seg.todo) {
+        if (!(step.template operator()<1>(conv, c + 1) && ...)) return false;
+        ++chunks;
+      }
     }
   }
   return true;
@@ -359,7 +438,9 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   uint64_t* barO = bars + 14;
   uint64_t* qready = bars + 15;
   uint64_t* mdone = bars + 16;       // after a give-up: every MMA issued has completed
+  uint64_t* partO = bars + 17;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + T::kBars);
+  float* s_cq = reinterpret_cast<float*>(s_tmem + 6);   // [kTiles][128] logit scales
 
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -372,6 +453,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       mbar_init(&pready[2 * x + 1], 4 * CG);
     }
     mbar_init(barO, 1);
+    mbar_init(partO, 1);
     mbar_init(mdone, 1);
     s_tmem[1] = 0u;   // set when a CTA of the pair gave up
     mbar_init(qready, T::kSoft * CG);
@@ -406,7 +488,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + T::kOCol + t * D + lane_off;
     uint8_t* q_tile = sQ + t * T::kQBytes;
-    int chunks = 0, s_waits = 0;   // chunks so far; waits on barS (two tiles)
+    int chunks = 0, s_waits = 0, parts = 0;   // chunks, waits on barS (two tiles), parts so far
     Cursor cursor(span);
     Seg seg;
     while (!dead && cursor.next(sh, p.seqlens, seg)) {
@@ -418,44 +500,73 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       const size_t orow = ((size_t)seg.b * g.R + j) * g.Hq + head;
       const int n = real ? visible_tokens(seg.L, g.R, j, g.MB * g.P) : 0;
       const int lo = first_seen(n, sh.window);
-      float cq = 1.f;
+      // Q rows as fp16, each scaled by a power of two into [256, 512): eight lanes to a
+      // row, a 16-byte piece of every 64 dims each, all 32 rows of the warp in flight.
+      const uint32_t orow32 = (uint32_t)orow;     // (at most 2^24 rows of 256 heads)
+      constexpr int E = D / 64;                   // pieces per lane
       {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * D);
-        float amax = 0.f;
-        if (real) {
-#pragma unroll 8
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 r = src[i];
-            const uint32_t w4[4] = {r.x, r.y, r.z, r.w};
+        uint4 raw[8][E];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              amax = fmax3(amax, fabsf(__uint_as_float(w4[u] << 16)),
-                           fabsf(__uint_as_float(w4[u] & 0xFFFF0000u)));
-          }
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3);                  // row of the warp
+          const uint32_t from = __shfl_sync(0xffffffffu, orow32, r);
+          const bool there = (t * CG + rank) * 128 + 32 * (warp & 3) + r < seg.vecs;
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)from * D) + (lane & 7);
+#pragma unroll
+          for (int u = 0; u < E; ++u) raw[i][u] = there ? src[8 * u] : make_uint4(0u, 0u, 0u, 0u);
         }
-        const int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
-        int sq = (amax > 0.f) ? 135 - ebits : 0;
-        sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
-        const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
-        const float down = __uint_as_float((uint32_t)(127 - sq) << 23);
-        if (real) cq = p.k_scale * p.sm_scale * kLog2e * down;
-#pragma unroll 8
-        for (int i = 0; i < D / 8; ++i) {
-          uint4 h = make_uint4(0u, 0u, 0u, 0u);
-          if (real) {
-            const uint4 r = src[i];
-            const uint32_t w4[4] = {r.x, r.y, r.z, r.w};
-            uint32_t o[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              o[u] = pack_half2(__uint_as_float(w4[u] << 16) * up,
-                                __uint_as_float(w4[u] & 0xFFFF0000u) * up);
-            h = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int i = 0; i < 8; ++i) {
+          float amax = 0.f;
+#pragma unroll
+          for (int u = 0; u < E; ++u) {
+            const uint32_t w4[4] = {raw[i][u].x, raw[i][u].y, raw[i][u].z, raw[i][u].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              amax = fmax3(amax, fabsf(__uint_as_float(w4[k] << 16)),
+                           fabsf(__uint_as_float(w4[k] & 0xFFFF0000u)));
           }
-          *reinterpret_cast<uint4*>(q_tile + (i >> 3) * 16384 + sw128(row, i & 7)) = h;
+#pragma unroll
+          for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
+          int sq = (amax > 0.f) ? 135 - ebits : 0;
+          sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
+          const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
+          const float down = __uint_as_float((uint32_t)(127 - sq) << 23);
+          const int r = 32 * (warp & 3) + 4 * i + (lane >> 3);
+          if ((lane & 7) == 0) s_cq[t * 128 + r] = p.k_scale * p.sm_scale * kLog2e * down;
+#pragma unroll
+          for (int u = 0; u < E; ++u) {
+            const uint32_t w4[4] = {raw[i][u].x, raw[i][u].y, raw[i][u].z, raw[i][u].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[k] = pack_half2(__uint_as_float(w4[k] << 16) * up,
+                                __uint_as_float(w4[k] & 0xFFFF0000u) * up);
+            *reinterpret_cast<uint4*>(q_tile + u * 16384 + sw128(r, lane & 7)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
         }
       }
-      fence_proxy_async_smem();
+      __syncwarp();
+      const float cq = s_cq[t * 128 + row];
+      if constexpr (T::kQTmem) {
+        // this thread's row to its tensor-memory lane, two dims a column (the A operand)
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t v[16];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int d8 = 4 * i + u;
+            const uint4 x = *reinterpret_cast<const uint4*>(q_tile + (d8 >> 3) * 16384 + sw128(row, d8 & 7));
+            v[4 * u] = x.x; v[4 * u + 1] = x.y; v[4 * u + 2] = x.z; v[4 * u + 3] = x.w;
+          }
+          tmem_st16u(tmem + T::kQCol + lane_off + 16 * i, v);
+        }
+        tmem_wait_st();
+      } else {
+        fence_proxy_async_smem();
+      }
       tc_fence_before();
       warp_arrive<CG>(qready);
 
@@ -515,8 +626,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
             // with two tiles barS has said that O is complete up to the chunk before
             if (kTiles == 1 && gave_up(barO, chunks - 1)) { dead = true; break; }
             tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {   // (rare: kept small, as the instruction cache is)
               float o16[16];
               tmem_ld16(tO + 16 * i, o16);
               tmem_wait_ld();
@@ -550,11 +661,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       }
       if (dead) break;
       // ---- the part's output ---------------------------------------------------------
-      // (one tile: barS of the last chunk says that the O of all but the last two chunks
-      // is complete; a phase is only told from its neighbours, so both are waited for)
-      const bool late = kTiles == 2 ? gave_up(&barS[t], s_waits)
-                                    : ((seg.todo > 1 && gave_up(barO, chunks - 2)) ||
-                                       gave_up(barO, chunks - 1));
+      const bool late = kTiles == 2 ? gave_up(&barS[t], s_waits) : gave_up(partO, parts);
+      ++parts;
       ++s_waits;
       if (late) { dead = true; break; }
       tc_fence_after();
@@ -567,32 +675,49 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         m = nm;
       }
       const float r = whole ? (l > 0.f ? f * p.v_scale / l : 0.f) : 1.f;
-      const bool ok = real && QSA_IN_BOUNDS(seg.b < g.B && j < g.R && head < g.Hq, kChkOut);
+      // O leaves 64 columns at a time by way of the warp's own rows of the Q tile (its last
+      // reader is done), so that rows are written in runs of 128 bytes and more.
       float* rec = p.records + ((size_t)worker * 2 + (seg.begins ? 1 : 0)) * record_floats(sh.vt, D);
-#pragma unroll 2
-      for (int i = 0; i < D / 16; ++i) {
-        float o16[16];
-        tmem_ld16(tO + 16 * i, o16);
+      // 32 rows of 64 floats, in the 4 KB that the warp's rows have of the first two blocks
+      // (no other warp's: it may be writing its next Q)
+      auto box = [&](int rr) { return q_tile + (rr >> 4) * 16384 + (warp & 3) * 4096 + (rr & 15) * 256; };
+      const int at0 = (t * CG + rank) * 128 + 32 * (warp & 3);    // the warp's first vector
+      const int left = min(32, seg.vecs - at0);                   // and how many it has
+      const int sub = lane >> 4, pc = lane & 15;
+#pragma unroll 1
+      for (int d0 = 0; d0 < D && left > 0; d0 += 64) {
+        float o64[64];
+        tmem_ld32(tO + d0, o64);
+        tmem_ld32(tO + d0 + 32, o64 + 32);
         tmem_wait_ld();
-        if (!ok) continue;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)       // 16-byte pieces, swizzled by the row
+          *reinterpret_cast<float4*>(box(lane) + ((i ^ (lane & 15)) << 4)) =
+              make_float4(o64[4 * i] * r, o64[4 * i + 1] * r, o64[4 * i + 2] * r, o64[4 * i + 3] * r);
+        __syncwarp();
         if (whole) {
-          uint32_t h[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(o16[2 * u] * r, o16[2 * u + 1] * r);
-            h[u] = *reinterpret_cast<const uint32_t*>(&x);
+#pragma unroll 4
+          for (int i = 0; i < 16; ++i) {   // two rows at a time, a piece per lane
+            const int rr = 2 * i + sub;
+            const float4 x = *reinterpret_cast<const float4*>(box(rr) + ((pc ^ (rr & 15)) << 4));
+            const uint32_t to = __shfl_sync(0xffffffffu, orow32, rr);
+            const __nv_bfloat162 lo2 = __floats2bfloat162_rn(x.x, x.y), hi2 = __floats2bfloat162_rn(x.z, x.w);
+            if (rr < left && QSA_IN_BOUNDS(to < (size_t)g.B * g.R * g.Hq, kChkOut))
+              *reinterpret_cast<uint2*>(p.out + (size_t)to * D + d0 + 4 * pc) =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
           }
-          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 16 * i);
-          dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
-          dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
         } else {
-          float4* dst = reinterpret_cast<float4*>(rec + 2 * sh.vt + (size_t)at * D + 16 * i);
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            dst[u] = make_float4(o16[4 * u], o16[4 * u + 1], o16[4 * u + 2], o16[4 * u + 3]);
+          float* to = rec + 2 * sh.vt + (size_t)(at0 + sub) * D + d0 + 4 * pc;
+#pragma unroll 4
+          for (int i = 0; i < 16; ++i) {
+            const int rr = 2 * i + sub;
+            const float4 x = *reinterpret_cast<const float4*>(box(rr) + ((pc ^ (rr & 15)) << 4));
+            if (rr < left) *reinterpret_cast<float4*>(to + 2 * i * D) = x;
+          }
         }
+        __syncwarp();
       }
-      if (ok) {
+      if (real) {
         if (whole) {
           p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
         } else {
@@ -606,15 +731,24 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     // ==== dequantisation =============================================================
     regs_down<T::kDeqRegs>();
     const int dw = (warp - T::kSoft) & 3;
-    using CK = Converter<T, false>;
-    using CV = Converter<T, true>;
-    if constexpr (T::kDeq == 4)
-      dead = !convert_all(sh, p, span, CK(sh, p, dw, rank, sK, kready, kfree),
-                          CV(sh, p, dw, rank, sV, vready, vfree));
-    else if (warp - T::kSoft < 4)
-      dead = !convert_all(sh, p, span, CK(sh, p, dw, rank, sK, kready, kfree));
-    else
-      dead = !convert_all(sh, p, span, CV(sh, p, dw, rank, sV, vready, vfree));
+    using CK = Converter<T, T::kKRows, D>;
+    using CV = Converter<T, kTok, T::kVDims>;
+    if constexpr (T::kDeq == 4) {
+      dead = !convert_all(sh, p, span,
+                          CK(sh, p.k_pool, p.k_sf, rank * T::kKRows, 0, dw, sK, kready, kfree),
+                          CV(sh, p.v_pool, p.v_sf, 0, rank * T::kVDims, dw, sV, vready, vfree));
+    } else if constexpr (CG == 1) {   // one shape: one copy of the code for both
+      const bool v = warp - T::kSoft >= 4;
+      dead = !convert_all(sh, p, span,
+                          CK(sh, v ? p.v_pool : p.k_pool, v ? p.v_sf : p.k_sf, 0, 0, dw, v ? sV : sK,
+                             v ? vready : kready, v ? vfree : kfree));
+    } else if (warp - T::kSoft < 4) {
+      dead = !convert_all(sh, p, span,
+                          CK(sh, p.k_pool, p.k_sf, rank * T::kKRows, 0, dw, sK, kready, kfree));
+    } else {
+      dead = !convert_all(sh, p, span,
+                          CV(sh, p.v_pool, p.v_sf, 0, rank * T::kVDims, dw, sV, vready, vfree));
+    }
   } else if (regs_down<T::kMmaRegs>(), warp == T::kMma && rank == 0) {
     // ==== MMA issue ==================================================================
     const uint32_t id_s = f16_idesc(128 * CG, kTok), id_o = f16_idesc(128 * CG, D) | kIdescBMn;
@@ -628,8 +762,12 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       for (int h = 0; h < D / 64; ++h)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_ss<CG>(tmem + y * kTok, dq + (uint64_t)((h * 16384 + 32 * ks) >> 4),
-                     dk + (uint64_t)((h * T::kKBlk + 32 * ks) >> 4), id_s, (h | ks) ? 1u : 0u);
+          if constexpr (T::kQTmem)     // 16 dims (one step): 8 columns
+            mma_ts<CG>(tmem + y * kTok, tmem + T::kQCol + 8 * (4 * h + ks),
+                       dk + (uint64_t)((h * T::kKBlk + 32 * ks) >> 4), id_s, (h | ks) ? 1u : 0u);
+          else
+            mma_ss<CG>(tmem + y * kTok, dq + (uint64_t)((h * 16384 + 32 * ks) >> 4),
+                       dk + (uint64_t)((h * T::kKBlk + 32 * ks) >> 4), id_s, (h | ks) ? 1u : 0u);
     };
     auto issue_o = [&](int t, int y, int x, int h, bool first) {   // 64 tokens
       const uint64_t dv = sw128_mn_desc(smem_u32(sV + x * T::kVBytes), T::kVBlk);
@@ -703,6 +841,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           if (dead) break;
           commit<CG>(&vfree[x]);
           commit<CG>(barO);
+          if (c + 1 == C) commit<CG>(partO);
           if (c + 2 < C) {
             if (!chunk_s(c + 2)) { dead = true; break; }
             issue_s(0, x, x);
@@ -757,7 +896,7 @@ dense::Shape dense_tile_shape(const Geom& g, int window) {
   auto set = [&](auto t) {
     using T = decltype(t);
     s.vt = T::kVecs;
-    s.tok = T::kTok;
+    s.tok_sh = T::kTok == 128 ? 7 : 6;
     s.ctas = dense_sms() / T::CG;
   };
   s.g = g;
