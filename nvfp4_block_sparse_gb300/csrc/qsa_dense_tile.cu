@@ -28,9 +28,8 @@
 //             fp16 over the columns of S it has read, 64 tokens at a time, sums in fp32;
 //             at the end of a part O from tensor memory to the output or to a record.  A
 //             group per tile
-//   dequant   codes and scales from the pages straight to registers two chunks ahead (they
-//             are in flight while the chunks before are converted), e2m1 x e4m3 exact in
-//             fp16 into double-buffered K and V tiles (128-byte swizzle)
+//   dequant   codes and scales from the pages by asynchronous copies some chunks ahead, e2m1 x
+//             e4m3 exact in fp16 into double-buffered K and V tiles (128-byte swizzle)
 //   MMA       one warp (of the pair's first CTA) issues every MMA in order.  With two tiles
 //             they take turns: O_0, S_0 of the next chunk, O_1, S_1, so that one tile's
 //             softmax runs under the other's products; with one, S has two buffers
@@ -40,9 +39,8 @@
 // P lies over S: S of the next chunk is issued behind the O that reads P, and
 // MMAs of one thread run in order, so no barrier guards the reuse.
 //
-// Tensor memory (512 columns): the two S buffers from column 0, O from 256, and for
-// single CTAs Q (384 at head_dim 128, 128 at 256), which leaves shared memory's
-// bandwidth to K and V.
+// Tensor memory (512 columns): the two S buffers from column 0, O from 256, and with one
+// tile Q (384 at head_dim 128, 128 at 256).
 // mbarriers, all waits bounded (2 s; a wait that gives up sets the status word).
 // Arrivals are one per warp; those for the MMA warp go to the first CTA's barrier,
 // commits to both CTAs':
@@ -73,7 +71,7 @@ template <int D_, int CG_>
 struct TT {
   static constexpr int D = D_, CG = CG_;                 // CG: CTAs per MMA
   static constexpr int kTiles = D == 128 && CG == 2 ? 2 : 1;   // tiles of a CTA
-  static constexpr int kTok = D == 256 && CG == 1 ? 64 : 128;  // tokens per chunk
+  static constexpr int kTok = D == 256 ? 64 : 128;       // tokens per chunk
   static constexpr int kHalves = kTok / 64;              // P is written 64 tokens at a time
   static constexpr int kSoft = 4 * kTiles;               // softmax warps
   // Dequantisation warps: four K and four V, or, where a CTA has half of every tile and
@@ -83,28 +81,33 @@ struct TT {
   static constexpr int kThreads = 32 * (kMma + 4);
   // Registers per thread after the roles part (128 at launch): the softmax holds a
   // row's 128 logits.
-  static constexpr int kSoftRegs = kTiles == 2 ? 176 : 184;
-  static constexpr int kDeqRegs = kTiles == 2 ? 96 : 112;
+  static constexpr int kSoftRegs = kTiles == 2 ? 184 : 192;
+  static constexpr int kDeqRegs = kTiles == 2 ? 80 : 96;
   static constexpr int kMmaRegs = kTiles == 2 ? 64 : 72;
   static_assert(32 * (kSoft * kSoftRegs + kDeq * kDeqRegs + 4 * kMmaRegs) <= kThreads * 128 &&
                     kThreads == 512, "registers");
   static constexpr int kVecs = 128 * CG * kTiles;        // query vectors of a unit
-  static constexpr int kQBytes = 128 * D * 2;            // Q: D/64 blocks of 128 rows x 128 B
   static constexpr int kKRows = kTok / CG;               // K tile: tokens of this CTA
   static constexpr int kKBlk = kKRows * 128;             // its 64-dim blocks
   static constexpr int kKBytes = kKRows * D * 2;
   static constexpr int kVDims = D / CG;                  // V tile: dims of this CTA
   static constexpr int kVBlk = kTok * 128;
   static constexpr int kVBytes = kTok * kVDims * 2;
-  static constexpr int kBars = 18;
-  static constexpr int kSmem = 1024 + kTiles * kQBytes + 2 * kKBytes + 2 * kVBytes + kBars * 8 + 24 +
-                               kTiles * 128 * 4;
-  // Tensor-memory columns of O and, for single CTAs, of Q: with half of every operand
-  // missing from the SM's shared memory (a pair's) Q's reads fit there.
+  // Tensor-memory columns of O and of Q, which leaves shared memory's bandwidth to K and
+  // V; with two tiles there is no room and Q stays in shared memory.
   static constexpr uint32_t kOCol = 256;
-  static constexpr bool kQTmem = CG == 1;
+  static constexpr bool kQTmem = kTiles == 1;
   static constexpr uint32_t kQCol = D == 128 ? 384 : 128;
   static_assert(kQCol + D / 2 <= 512 && 2 * kTok <= 256, "tensor-memory columns");
+  // Q tiles (D/64 blocks of 128 rows x 128 B), or, with Q in tensor memory, 8 KB per warp
+  // through which Q and O pass.
+  static constexpr int kQBytes = kQTmem ? 32768 : 128 * D * 2;
+  // Codes and scales on their way: chunks per converting warp.
+  static constexpr int kDepth = kTiles == 2 ? 4 : 3;
+  static constexpr int kRing = kDepth * (kKRows * D + kTok * kVDims) * 9 / 16;
+  static constexpr int kBars = 18;
+  static constexpr int kSmem = 1024 + kTiles * kQBytes + 2 * kKBytes + 2 * kVBytes + kRing +
+                               kBars * 8 + 24 + kTiles * 128 * 4;
 };
 
 // 32 columns of this thread's lane.
@@ -127,23 +130,22 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 // every weight is finite its relative precision does not depend on the base.
 constexpr float kHeadroom = 15.f;
 
-// Read-only loads, zero where `on` is false.
-__device__ __forceinline__ uint4 ldg128(const void* p, bool on) {
-  uint4 r;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\t"
-      "mov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t@q ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-      : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w) : "l"(p), "r"((uint32_t)on));
-  return r;
+// Asynchronous copies of N bytes, zeros where `on` is false.
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool on) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
+                 "r"(on ? N : 0) : "memory");
 }
-// (into a 32-bit register: a 16-bit one would be widened on the spot, waiting for the load)
-__device__ __forceinline__ uint32_t ldg16(const void* p, bool on) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\tmov.u32 %0, 0;\n\t"
-      "@q ld.global.nc.u16 %0, [%1];\n\t}"
-      : "=&r"(r) : "l"(p), "r"((uint32_t)on));
-  return r;
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Two fp32 multiply-adds / additions at once.
@@ -244,127 +246,125 @@ __device__ __forceinline__ void cluster_sync() {
 
 // ---- dequantisation --------------------------------------------------------------
 // A converter turns this CTA's part of every chunk's K (kKRows tokens, all dims) or V
-// (all tokens, kVDims dims) into a tile, four warps with a 16-byte piece
-// (32 codes, two scales) per lane and step.  Neighbouring lanes read neighbouring
-// pieces; eight that store together have two rows (or four) of the 64-dim blocks.
-template <class T, int kRows_, int kDims_>
+// (all tokens, kVDims dims) into a tile, four warps with a 16-byte piece (32 codes,
+// two scales) per lane and step.  Each warp copies its own pieces into its own ring,
+// kDepth - 1 chunks ahead (no barrier, and registers could not cover DRAM's latency).
+// Neighbouring lanes have neighbouring pieces, four of eight rows or two of sixteen; the
+// eight lanes that store together would meet in two 64-dim blocks' same banks, so the
+// upper two pieces of four go in another order.
+//
+// The code is kept small (one copy for K and V where the shapes agree, no
+// unrolling over chunks): with four roles' loops on an SM, instruction-cache misses
+// were its largest stall (windowed verify rows 85 -> 60 us by one copy instead of two).
+template <class T, int kRows, int kDims>
 struct Converter {
   static constexpr int D = T::D, kTok = T::kTok;
-  static constexpr int kRows = kRows_, kDims = kDims_;        // tokens and dims of the tile
   static constexpr int kPieces = kDims / 32;                  // 16-byte pieces of a row
   static constexpr int kUnits = kRows * kPieces / 128;        // steps of a warp
   static constexpr int kBlk = kRows * 128, kBytes = kRows * kDims * 2;
-  // the pages of this CTA's tokens of a chunk: at most four, of 32 tokens and more
-  static constexpr int kMaxPages = kRows / (D == 128 ? 64 : 32);
+  static constexpr int kStage = kUnits * 576;                 // a chunk's pieces and scales
+  static constexpr int kSfRow = kPieces >= 4 ? 8 : 4;         // scale bytes of a step's row
 
   const uint8_t *pool, *sfs;
   uint8_t* tiles;
   uint64_t *ready, *freed;
-  int dw, lane, row0, psh;
-  size_t page_rows;
-  uint32_t at_c[kUnits], at_s[kUnits];   // a step's codes and scales within their page
-  uint4 codes[2][kUnits];      // two chunks are on their way
-  uint32_t sc[2][kUnits];
-  int pages[kMaxPages];
-  // Page ids: lane i has that of block blk0 + i, and `later` of blk0 + 32 + i.  (Looked up
-  // chunk by chunk they would queue behind the chunks' own loads.)
+  uint32_t ring;
+  int row0, psh;
+  uint32_t page_rows;
+  // Per step: token row (of the chunk), place of codes and scales in the page, of the
+  // result in the tile.
+  int row[kUnits];
+  uint32_t at_c[kUnits], at_s[kUnits], at_t[kUnits];
+  // Page ids: lane i has that of block blk0 + i, and `later` of blk0 + 32 + i.
   int blk0, ids, later;
 
   __device__ __forceinline__ Converter(const Shape& sh, const uint8_t* codes_, const uint8_t* scales_,
-                                       int token0, int dim0, int dw_, uint8_t* tiles_,
+                                       int token0, int dim0, int dw, uint8_t* tiles_, uint8_t* ring_,
                                        uint64_t* ready_, uint64_t* freed_)
       : pool(codes_ + dim0 / 2), sfs(scales_ + dim0 / 16), tiles(tiles_), ready(ready_), freed(freed_),
-        dw(dw_), row0(token0) {
-    lane = threadIdx.x & 31;
+        ring(smem_u32(ring_)), row0(token0) {
+    const int lane = threadIdx.x & 31;
     psh = 31 - __clz(sh.g.P);                               // log2 of the page size
-    page_rows = (size_t)sh.g.Hkv << psh;                    // token rows of a page, all heads
-  }
-  // row and piece of step i: eight rows of four pieces, or sixteen of two
-  __device__ __forceinline__ int row_of(int i) const {
-    const int u = dw + 4 * i;
-    return kPieces >= 4 ? 8 * (u % (kRows / 8)) + (lane >> 2) : 16 * u + (lane >> 1);
-  }
-  __device__ __forceinline__ int piece_of(int i) const {
-    const int u = dw + 4 * i;
-    return kPieces >= 4 ? 4 * (u / (kRows / 8)) + (lane & 3) : lane & 1;
-  }
-  // which of the chunk's pages step i reads: the same for all four warps
-  __host__ __device__ static constexpr int slot_of(int i) {
-    return (kPieces >= 4 ? 8 * ((4 * i) % (kRows / 8)) : 64 * i) / (kRows / kMaxPages);
+    page_rows = (uint32_t)sh.g.Hkv << psh;                  // token rows of a page, all heads
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int u = dw + 4 * i;
+      int r, piece;
+      if (kPieces >= 4) {
+        r = 8 * (u % (kRows / 8)) + (lane >> 2);
+        piece = 4 * (u / (kRows / 8)) + (lane & 3);
+      } else {
+        r = 16 * u + (lane >> 1);
+        piece = lane & 1;
+      }
+      row[i] = row0 + r;
+      // eight dims 4 piece + u: block (4 piece) / 8, chunk 4 (piece & 1) + u, by xor
+      at_t[i] = (piece >> 1) * kBlk + sw128(r, 4 * (piece & 1));
+      at_c[i] = 16 * piece;
+      at_s[i] = 8 * (u / (kRows / 8));
+    }
   }
   __device__ __forceinline__ int page_id(const Shape& sh, const Work& p, const Seg& seg, int beta) {
     return beta < sh.g.MB && seg.n_all > seg.lo_all
                ? __ldg(p.page_table + (size_t)seg.b * sh.g.MB + beta) : -1;
   }
   __device__ __forceinline__ void begin(const Shape& sh, const Work& p, const Seg& seg) {
+    const int lane = threadIdx.x & 31;
     blk0 = (seg.chunk0 * kTok + row0) >> psh;
     ids = page_id(sh, p, seg, blk0 + lane);
     later = page_id(sh, p, seg, blk0 + 32 + lane);
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const uint32_t row = ((uint32_t)seg.kvh << psh) + ((row0 + row_of(i)) & (sh.g.P - 1));
-      at_c[i] = row * (D / 2) + 16 * piece_of(i);
-      at_s[i] = row * (D / 16) + 2 * piece_of(i);
-    }
   }
-  __device__ __forceinline__ void look_up(const Shape& sh, const Work& p, const Seg& seg, int chunk) {
-    const int first = (chunk * kTok + row0) >> psh;
-    if (first - blk0 >= 32) {
+  // Requests a chunk into stage `slot`.
+  __device__ __forceinline__ void request(const Shape& sh, const Work& p, const Seg& seg, int chunk,
+                                          int slot) {
+    const int lane = threadIdx.x & 31;
+    const int tok0 = chunk * kTok;
+    if (((tok0 + row0) >> psh) - blk0 >= 32) {
       blk0 += 32;
       ids = later;
       later = page_id(sh, p, seg, blk0 + 32 + lane);
     }
-#pragma unroll
-    for (int i = 0; i < kMaxPages; ++i) {
-      const int at = ((chunk * kTok + row0 + i * (kRows / kMaxPages)) >> psh) - blk0;
-      const int here = __shfl_sync(0xffffffffu, ids, at & 31);
-      const int next = __shfl_sync(0xffffffffu, later, at & 31);
-      pages[i] = at < 32 ? here : next;
-    }
-  }
-  template <int B>
-  __device__ __forceinline__ void fetch(const Shape& sh, const Seg& seg, int chunk) {
-    const int tok0 = chunk * kTok + row0;
-    const bool inner = tok0 >= seg.lo_all && tok0 + kRows <= seg.n_all;
-    const uint8_t *pc[kMaxPages], *ps[kMaxPages];
-    bool there[kMaxPages];
-#pragma unroll
-    for (int k = 0; k < kMaxPages; ++k) {
-      there[k] = pages[k] >= 0 && pages[k] < sh.g.NP;
-      const size_t row = there[k] ? (size_t)pages[k] * page_rows : 0;
-      pc[k] = pool + row * (D / 2);
-      ps[k] = sfs + row * (D / 16);
-    }
+    const uint32_t head_rows = (uint32_t)seg.kvh << psh;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int k = slot_of(i), tok = tok0 + row_of(i);
+      const int tok = tok0 + row[i];
+      // (a step's rows are in one page: the same block in every lane)
+      const int at = (tok >> psh) - blk0;
+      const int page = __shfl_sync(0xffffffffu, at < 32 ? ids : later, at & 31);
       // what no row of the unit sees is not looked at
-      const bool on = there[k] && (inner || (tok >= seg.lo_all && tok < seg.n_all));
-      codes[B][i] = ldg128(pc[k] + at_c[i], on);
-      sc[B][i] = ldg16(ps[k] + at_s[i], on);
+      const bool there = page >= 0 && page < sh.g.NP && tok >= seg.lo_all && tok < seg.n_all;
+      const size_t from = there ? (size_t)page * page_rows + head_rows + (tok & (sh.g.P - 1)) : 0;
+      const uint32_t dst = ring + slot * kStage + i * 576;
+      cp_async<16>(dst + 16 * lane, pool + from * (D / 2) + at_c[i], there);
+      // one lane per row copies the row's scales
+      constexpr int kLanes = kPieces >= 4 ? 4 : 2;
+      if ((lane & (kLanes - 1)) == 0)
+        cp_async<kSfRow>(dst + 512 + 2 * lane, sfs + from * (D / 16) + at_s[i], there);
     }
   }
-  // Chunk number `chunks` of the CTA into its tile; false when the wait for it gave up.
-  template <int B>
-  __device__ __forceinline__ bool convert(int chunks) {
+  // Chunk number `chunks` of the CTA from stage `slot` into its tile; false when the wait
+  // for the tile gave up.
+  __device__ __forceinline__ bool convert(int chunks, int slot) {
+    const int lane = threadIdx.x & 31;
     const int x = chunks & 1, use = chunks >> 1;
     if (use > 0 && gave_up(&freed[x], use - 1)) return false;
     uint8_t* tile = tiles + x * kBytes;
+    const bool flip = kPieces >= 4 && (lane & 2);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const uint32_t s2 = e4m3x2_to_f16x2(sc[B][i]);
-      const uint32_t sx[2] = {prmt(s2, 0, 0x1010), prmt(s2, 0, 0x3232)};
-      // Eight lanes store together: two rows of four pieces, whose upper two (another
-      // 64-dim block, the same banks) go in another order; or four rows of two.
-      const bool flip = kPieces >= 4 && (lane & 2);
-      const uint4 c = codes[B][i];
+      const uint32_t src = ring + slot * kStage + i * 576;
+      uint4 c;
+      uint32_t sf;
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w) : "r"(src + 16 * lane));
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sf) : "r"(src + 512 + 2 * lane));
+      const uint32_t s2 = e4m3x2_to_f16x2(sf);
+      const uint32_t sx[2] = {prmt(s2, 0, flip ? 0x3232 : 0x1010), prmt(s2, 0, flip ? 0x1010 : 0x3232)};
       const uint32_t w[4] = {flip ? c.z : c.x, flip ? c.w : c.y, flip ? c.x : c.z, flip ? c.y : c.w};
+      const uint32_t to = at_t[i] ^ (flip ? 32u : 0u);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int d8 = 4 * piece_of(i) + (flip ? u ^ 2 : u);   // eight dims
-        *reinterpret_cast<uint4*>(tile + (d8 >> 3) * kBlk + sw128(row_of(i), d8 & 7)) =
-            dequant8(w[u], flip ? sx[(u >> 1) ^ 1] : sx[u >> 1]);
-      }
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<uint4*>(tile + (to ^ (16 * u))) = dequant8(w[u], sx[u >> 1]);
     }
     fence_proxy_async_smem();
     warp_arrive<T::CG>(&ready[x]);
@@ -373,33 +373,31 @@ struct Converter {
 };
 
 // Every chunk through one converter, or through K's and then V's.
-template <class... C>
+template <class T, class... C>
 __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, const Span& span, C... conv) {
-  int chunks = 0;
+  constexpr int kAhead = T::kDepth - 1;
+  int chunks = 0, put = 0, take = 0;    // chunks converted; ring stages
   Cursor cursor(span);
   Seg seg;
   while (cursor.next(sh, p.seqlens, seg)) {
-    auto get = [&]<int B>(auto& k, int c) {
-      k.look_up(sh, p, seg, seg.chunk0 + c);
-      k.template fetch<B>(sh, seg, seg.chunk0 + c);
-    };
     (conv.begin(sh, p, seg), ...);
-    (get.template operator()<0>(conv, 0), ...);
-    if (seg.todo > 1) (get.template operator()<1>(conv, 1), ...);
-    auto step = [&]<int B>(auto& k, int c) {
-      if (!k.template convert<B>(chunks)) return false;
-      if (c + 2 < seg.todo) get.template operator()<B>(k, c + 2);
-      return true;
-    };
-    for (int c = 0; c < seg.todo; c += 2) {
-      if (!(step.template operator()<0>(conv, c) && ...)) return false;
+#pragma unroll 1
+    for (int c = -kAhead; c < seg.todo; ++c) {
+      if (c + kAhead < seg.todo) (conv.request(sh, p, seg, seg.chunk0 + c + kAhead, put), ...);
+      cp_async_commit();
+      put = put + 1 == T::kDepth ? 0 : put + 1;
+      if (c < 0) continue;
+      cp_async_wait<kAhead>();
+      __syncwarp();
+      if (!(conv.convert(chunks, take) && ...)) return false;
+      __syncwarp();     // every lane has read the stage before it is requested again
+      take = take + 1 == T::kDepth ? 0 : take + 1;
       ++chunks;
-      if (c + 1 < seg.todo) {
-        if (!(step.template operator()<1>(conv, c + 1) && ...)) return false;
-        ++chunks;
-      }
     }
+    // (with fewer chunks than stages ahead, put has run past take by empty groups)
+    take = put;
   }
+  cp_async_wait<0>();
   return true;
 }
 
@@ -428,7 +426,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   uint8_t* sQ = smem;                                   // [kTiles][kQBytes]
   uint8_t* sK = sQ + kTiles * T::kQBytes;               // [2][kKBytes]
   uint8_t* sV = sK + 2 * T::kKBytes;                    // [2][kVBytes]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + 2 * T::kVBytes);
+  uint8_t* ring = sV + 2 * T::kVBytes;                  // [warp][kDepth][steps x 576]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + T::kRing);
   uint64_t* kready = bars;
   uint64_t* vready = bars + 2;
   uint64_t* kfree = bars + 4;
@@ -503,70 +502,101 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       // Q rows as fp16, each scaled by a power of two into [256, 512): eight lanes to a
       // row, a 16-byte piece of every 64 dims each, all 32 rows of the warp in flight.
       const uint32_t orow32 = (uint32_t)orow;     // (at most 2^24 rows of 256 heads)
-      constexpr int E = D / 64;                   // pieces per lane
       {
-        uint4 raw[8][E];
+        uint4 raw[8][2];       // 128 dims of the warp's rows
+        auto load = [&](int d) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3);                  // row of the warp
-          const uint32_t from = __shfl_sync(0xffffffffu, orow32, r);
-          const bool there = (t * CG + rank) * 128 + 32 * (warp & 3) + r < seg.vecs;
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)from * D) + (lane & 7);
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);                  // row of the warp
+            const uint32_t from = __shfl_sync(0xffffffffu, orow32, r);
+            const bool there = (t * CG + rank) * 128 + 32 * (warp & 3) + r < seg.vecs;
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)from * D) + 16 * d + (lane & 7);
 #pragma unroll
-          for (int u = 0; u < E; ++u) raw[i][u] = there ? src[8 * u] : make_uint4(0u, 0u, 0u, 0u);
+            for (int u = 0; u < 2; ++u) raw[i][u] = there ? src[8 * u] : make_uint4(0u, 0u, 0u, 0u);
+          }
+        };
+        float amax[8], up[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax[i] = 0.f;
+#pragma unroll
+        for (int d = 0; d < D / 128; ++d) {
+          load(d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t w4[4] = {raw[i][u].x, raw[i][u].y, raw[i][u].z, raw[i][u].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                amax[i] = fmax3(amax[i], fabsf(__uint_as_float(w4[k] << 16)),
+                                fabsf(__uint_as_float(w4[k] & 0xFFFF0000u)));
+            }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float amax = 0.f;
 #pragma unroll
-          for (int u = 0; u < E; ++u) {
-            const uint32_t w4[4] = {raw[i][u].x, raw[i][u].y, raw[i][u].z, raw[i][u].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              amax = fmax3(amax, fabsf(__uint_as_float(w4[k] << 16)),
-                           fabsf(__uint_as_float(w4[k] & 0xFFFF0000u)));
-          }
-#pragma unroll
-          for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          const int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
-          int sq = (amax > 0.f) ? 135 - ebits : 0;
+          for (int o = 4; o; o >>= 1) amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], o));
+          const int ebits = (int)((__float_as_uint(amax[i]) >> 23) & 0xFF);
+          int sq = (amax[i] > 0.f) ? 135 - ebits : 0;
           sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
-          const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
+          up[i] = __uint_as_float((uint32_t)(sq + 127) << 23);
           const float down = __uint_as_float((uint32_t)(127 - sq) << 23);
-          const int r = 32 * (warp & 3) + 4 * i + (lane >> 3);
-          if ((lane & 7) == 0) s_cq[t * 128 + r] = p.k_scale * p.sm_scale * kLog2e * down;
+          if ((lane & 7) == 0)
+            s_cq[t * 128 + 32 * (warp & 3) + 4 * i + (lane >> 3)] = p.k_scale * p.sm_scale * kLog2e * down;
+        }
+        auto half8 = [&](const uint4& x, float f) {
+          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+          uint32_t h[4];
 #pragma unroll
-          for (int u = 0; u < E; ++u) {
-            const uint32_t w4[4] = {raw[i][u].x, raw[i][u].y, raw[i][u].z, raw[i][u].w};
-            uint32_t h[4];
+          for (int k = 0; k < 4; ++k)
+            h[k] = pack_half2(__uint_as_float(w4[k] << 16) * f, __uint_as_float(w4[k] & 0xFFFF0000u) * f);
+          return make_uint4(h[0], h[1], h[2], h[3]);
+        };
+        if constexpr (T::kQTmem) {
+          // 128 dims of the warp's rows at a time; each thread then takes its own row to its
+          // tensor-memory lane, two dims a column (the A operand)
+          uint8_t* mine = q_tile + (warp & 3) * 8192;         // 32 rows x 16 pieces, swizzled
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              h[k] = pack_half2(__uint_as_float(w4[k] << 16) * up,
-                                __uint_as_float(w4[k] & 0xFFFF0000u) * up);
-            *reinterpret_cast<uint4*>(q_tile + u * 16384 + sw128(r, lane & 7)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
+          for (int k = D / 128 - 1; k >= 0; --k) {   // (the last dims are still in registers)
+            const int d = k;
+            if (k < D / 128 - 1) load(d);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int r = 4 * i + (lane >> 3), pc = 8 * u + (lane & 7);
+                *reinterpret_cast<uint4*>(mine + r * 256 + ((pc ^ (r & 7)) << 4)) =
+                    half8(raw[i][u], up[i]);
+              }
+            __syncwarp();
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {
+              uint32_t v[16];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const uint4 x = *reinterpret_cast<const uint4*>(
+                    mine + lane * 256 + (((4 * c4 + u) ^ (lane & 7)) << 4));
+                v[4 * u] = x.x; v[4 * u + 1] = x.y; v[4 * u + 2] = x.z; v[4 * u + 3] = x.w;
+              }
+              tmem_st16u(tmem + T::kQCol + lane_off + 64 * d + 16 * c4, v);
+            }
           }
+          tmem_wait_st();
+        } else {
+          static_assert(T::kQTmem || D == 128, "Q in shared memory: 128 dims");
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              *reinterpret_cast<uint4*>(q_tile + u * 16384 +
+                                        sw128(32 * (warp & 3) + 4 * i + (lane >> 3), lane & 7)) =
+                  half8(raw[i][u], up[i]);
+          fence_proxy_async_smem();
         }
       }
       __syncwarp();
       const float cq = s_cq[t * 128 + row];
-      if constexpr (T::kQTmem) {
-        // this thread's row to its tensor-memory lane, two dims a column (the A operand)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t v[16];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int d8 = 4 * i + u;
-            const uint4 x = *reinterpret_cast<const uint4*>(q_tile + (d8 >> 3) * 16384 + sw128(row, d8 & 7));
-            v[4 * u] = x.x; v[4 * u + 1] = x.y; v[4 * u + 2] = x.z; v[4 * u + 3] = x.w;
-          }
-          tmem_st16u(tmem + T::kQCol + lane_off + 16 * i, v);
-        }
-        tmem_wait_st();
-      } else {
-        fence_proxy_async_smem();
-      }
       tc_fence_before();
       warp_arrive<CG>(qready);
 
@@ -675,12 +705,15 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         m = nm;
       }
       const float r = whole ? (l > 0.f ? f * p.v_scale / l : 0.f) : 1.f;
-      // O leaves 64 columns at a time by way of the warp's own rows of the Q tile (its last
-      // reader is done), so that rows are written in runs of 128 bytes and more.
+      // O leaves 64 columns at a time by way of shared memory of the warp's own (its Q rows,
+      // whose last reader is done), so that rows are written in runs of 128 bytes and more.
       float* rec = p.records + ((size_t)worker * 2 + (seg.begins ? 1 : 0)) * record_floats(sh.vt, D);
-      // 32 rows of 64 floats, in the 4 KB that the warp's rows have of the first two blocks
-      // (no other warp's: it may be writing its next Q)
-      auto box = [&](int rr) { return q_tile + (rr >> 4) * 16384 + (warp & 3) * 4096 + (rr & 15) * 256; };
+      // 32 rows of 64 floats, in the warp's 8 KB or in the 4 KB that its rows have of the first
+      // two blocks (no other warp's: it may be writing its next Q)
+      auto box = [&](int rr) {
+        return T::kQTmem ? q_tile + (warp & 3) * 8192 + rr * 256
+                         : q_tile + (rr >> 4) * 16384 + (warp & 3) * 4096 + (rr & 15) * 256;
+      };
       const int at0 = (t * CG + rank) * 128 + 32 * (warp & 3);    // the warp's first vector
       const int left = min(32, seg.vecs - at0);                   // and how many it has
       const int sub = lane >> 4, pc = lane & 15;
@@ -733,21 +766,24 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     const int dw = (warp - T::kSoft) & 3;
     using CK = Converter<T, T::kKRows, D>;
     using CV = Converter<T, kTok, T::kVDims>;
+    static_assert(4 * T::kDepth * (CK::kStage + CV::kStage) == T::kRing, "ring");
+    uint8_t* mine = ring + dw * T::kDepth * CK::kStage;                            // K's part
+    uint8_t* mine_v = ring + T::kDepth * (4 * CK::kStage + dw * CV::kStage);       // V's
     if constexpr (T::kDeq == 4) {
-      dead = !convert_all(sh, p, span,
-                          CK(sh, p.k_pool, p.k_sf, rank * T::kKRows, 0, dw, sK, kready, kfree),
-                          CV(sh, p.v_pool, p.v_sf, 0, rank * T::kVDims, dw, sV, vready, vfree));
+      dead = !convert_all<T>(
+          sh, p, span, CK(sh, p.k_pool, p.k_sf, rank * T::kKRows, 0, dw, sK, mine, kready, kfree),
+          CV(sh, p.v_pool, p.v_sf, 0, rank * T::kVDims, dw, sV, mine_v, vready, vfree));
     } else if constexpr (CG == 1) {   // one shape: one copy of the code for both
       const bool v = warp - T::kSoft >= 4;
-      dead = !convert_all(sh, p, span,
-                          CK(sh, v ? p.v_pool : p.k_pool, v ? p.v_sf : p.k_sf, 0, 0, dw, v ? sV : sK,
-                             v ? vready : kready, v ? vfree : kfree));
+      dead = !convert_all<T>(sh, p, span,
+                             CK(sh, v ? p.v_pool : p.k_pool, v ? p.v_sf : p.k_sf, 0, 0, dw,
+                                v ? sV : sK, v ? mine_v : mine, v ? vready : kready, v ? vfree : kfree));
     } else if (warp - T::kSoft < 4) {
-      dead = !convert_all(sh, p, span,
-                          CK(sh, p.k_pool, p.k_sf, rank * T::kKRows, 0, dw, sK, kready, kfree));
+      dead = !convert_all<T>(sh, p, span, CK(sh, p.k_pool, p.k_sf, rank * T::kKRows, 0, dw, sK, mine,
+                                             kready, kfree));
     } else {
-      dead = !convert_all(sh, p, span,
-                          CV(sh, p.v_pool, p.v_sf, 0, rank * T::kVDims, dw, sV, vready, vfree));
+      dead = !convert_all<T>(sh, p, span, CV(sh, p.v_pool, p.v_sf, 0, rank * T::kVDims, dw, sV, mine_v,
+                                             vready, vfree));
     }
   } else if (regs_down<T::kMmaRegs>(), warp == T::kMma && rank == 0) {
     // ==== MMA issue ==================================================================
