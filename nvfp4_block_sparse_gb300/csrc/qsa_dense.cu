@@ -89,6 +89,87 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   return r;
 }
 
+// A sink's logit joins the denominator: new base and sum, and the factor of what was summed.
+__device__ __forceinline__ void add_sink(float sink, float& m, float& l, float& f) {
+  const float s2 = sink * kLog2e, nm = fmaxf(m, s2);
+  f = exp2_approx(m - nm);
+  l = l * f + exp2_approx(s2 - nm);
+  m = nm;
+}
+
+// The records of a unit's parts (CTAs first..last) joined by a CTA of W warps, in the
+// parts' order: W / vecs warps to a vector, each with every so-manieth part, then their
+// sums in the warps' order.
+template <int D, int W>
+__device__ __forceinline__ void join_parts(const Shape& sh, const Work& p, int b, int vec0, int vecs,
+                                           int kvh, int first, int last, float* s_sum) {
+  constexpr int E = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int parts = last - first + 1, ways = max(W / vecs, 1);
+  const size_t rf = record_floats(sh.vt, D);
+  auto record = [&](int i) {   // slot 1 of the first CTA, slot 0 of the others
+    return p.records + ((size_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * rf;
+  };
+  for (int c0 = 0; c0 < vecs; c0 += W) {
+    const int c = c0 + warp % min(vecs, W), way = warp / min(vecs, W);
+    const bool on = c < vecs && way < ways;
+    float m = kNoBase, l = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    if (on) {
+      for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(record(i) + c));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll 4
+      for (int i = way; i < parts; i += ways) {
+        const float* rec = record(i);
+        const float f = exp2_approx(__ldcg(rec + c) - m);
+        l = fmaf(__ldcg(rec + sh.vt + c), f, l);
+        const float4* src = reinterpret_cast<const float4*>(rec + 2 * sh.vt + (size_t)c * D) + lane * (E / 4);
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e) {
+          const float4 x = __ldcg(src + e);
+          acc[4 * e] = fmaf(x.x, f, acc[4 * e]);
+          acc[4 * e + 1] = fmaf(x.y, f, acc[4 * e + 1]);
+          acc[4 * e + 2] = fmaf(x.z, f, acc[4 * e + 2]);
+          acc[4 * e + 3] = fmaf(x.w, f, acc[4 * e + 3]);
+        }
+      }
+    }
+    if (ways > 1) {
+      float* mine = s_sum + warp * (D + 4);
+#pragma unroll
+      for (int e = 0; e < E; ++e) mine[lane * E + e] = acc[e];
+      if (lane == 0) mine[D] = l;
+      __syncthreads();
+      if (on && way == 0)
+        for (int w = 1; w < ways; ++w) {
+          const float* other = s_sum + (warp + w * min(vecs, W)) * (D + 4);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += other[lane * E + e];
+          l += other[D];
+        }
+    }
+    if (!on || way != 0) continue;
+    const int j = (vec0 + c) / sh.G, head = kvh * sh.G + (vec0 + c) % sh.G;
+    const size_t row = ((size_t)b * sh.g.R + j) * sh.g.Hq + head;
+    float f = 1.f;
+    if (p.sinks) add_sink(p.sinks[head], m, l, f);
+    const float r = l > 0.f ? f * p.v_scale / l : 0.f;
+    uint32_t w2[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[2 * e] * r, acc[2 * e + 1] * r);
+      w2[e] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(p.out + row * D + lane * E) = make_uint2(w2[0], w2[1]);
+    else
+      *reinterpret_cast<uint4*>(p.out + row * D + lane * E) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+    if (lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  }
+}
+
 // D dims, NT tiles of 8 query vectors, W warps with S chunk buffers of TOK tokens.
 template <int D_, int NT_, int W_, int S_, int TOK_>
 struct Cfg {
@@ -100,7 +181,7 @@ struct Cfg {
   static constexpr int kK = TOK * kRow, kSc = TOK * kSf;
   static constexpr int kStage = 2 * kK + 2 * kSc;
   static constexpr int kRing = W * S * kStage;
-  static constexpr int kJoin = W * kCols * (D + 2) * 4;   // the warps' states, over the ring
+  static constexpr int kJoin = W * kCols * (D + 3) * 4;   // the warps' states, over the ring
   static constexpr int kMain = kRing > kJoin ? kRing : kJoin;
   static constexpr int kQ = kCols * D * 2;           // queries in fragment order
   static constexpr int kMisc = kCols * 4 * 3;
@@ -127,7 +208,6 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
   pdl_wait();
   const Span span = plan_span<C::kThreads>(sh, p.seqlens, blockIdx.x, gridDim.x);
   pdl_trigger();
-  if (tid == 0) describe_none(sh, p, blockIdx.x);
   if (span.begin >= span.end) return;
 
   // Token row within an 8-token group, by MMA row: see the swizzle below.
@@ -169,6 +249,20 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
     const int n_all = seg.n_all, n_least = seg.n_least, lo_all = seg.lo_all, lo_most = seg.lo_most;
     const int mine = todo > warp ? (todo - warp + W - 1) / W : 0;   // this warp's chunks
 
+    // ---- the warp's query vectors: on their way while the pages are looked up ----------
+    constexpr int kPer = (kCols + W - 1) / W, E = D / 32;
+    uint2 raw[kPer][E / 4];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int c = warp + i * W;
+      const bool real = c < vecs;
+      const int j = real ? (vec0 + c) / sh.G : 0, hh = real ? (vec0 + c) % sh.G : 0;
+      const size_t row = ((size_t)b * g.R + j) * g.Hq + (size_t)kvh * sh.G + hh;
+#pragma unroll
+      for (int u = 0; u < E / 4; ++u)
+        raw[i][u] = real ? *reinterpret_cast<const uint2*>(p.q + row * D + E * lane + 4 * u)
+                         : make_uint2(0u, 0u);
+    }
     // ---- page ids and copies ---------------------------------------------------
     int pages = -1;          // lane i: the page of this warp's chunk k, k % 32 = i
     uint32_t live = 0u;      // bit k % 32: chunk k has a page and its copies are under way
@@ -212,20 +306,19 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
 
     // ---- queries: fp16, scaled by a power of two into [256, 512), in the order of
     // the lanes that use them: dims 32 tig + 4 s.. of lane (gid, tig), step s ------
-    for (int c = warp; c < kCols; c += W) {
+#pragma unroll
+    for (int n = 0; n < kPer; ++n) {
+      const int c = warp + n * W;
+      if (kCols % W != 0 && c >= kCols) break;
       const bool real = c < vecs;
-      const int j = real ? (vec0 + c) / sh.G : 0, hh = real ? (vec0 + c) % sh.G : 0;
-      const size_t row = ((size_t)b * g.R + j) * g.Hq + (size_t)kvh * sh.G + hh;
-      constexpr int E = D / 32;
+      const int j = real ? (vec0 + c) / sh.G : 0;
       float x[E];
 #pragma unroll
       for (int u = 0; u < E / 4; ++u) {
-        uint2 raw = make_uint2(0u, 0u);
-        if (real) raw = *reinterpret_cast<const uint2*>(p.q + row * D + E * lane + 4 * u);
-        x[4 * u] = __uint_as_float(raw.x << 16);
-        x[4 * u + 1] = __uint_as_float(raw.x & 0xFFFF0000u);
-        x[4 * u + 2] = __uint_as_float(raw.y << 16);
-        x[4 * u + 3] = __uint_as_float(raw.y & 0xFFFF0000u);
+        x[4 * u] = __uint_as_float(raw[n][u].x << 16);
+        x[4 * u + 1] = __uint_as_float(raw[n][u].x & 0xFFFF0000u);
+        x[4 * u + 2] = __uint_as_float(raw[n][u].y << 16);
+        x[4 * u + 3] = __uint_as_float(raw[n][u].y & 0xFFFF0000u);
       }
       float amax = 0.f;
 #pragma unroll
@@ -248,10 +341,10 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
                           pack_half2(x[4 * u + 2] * up, x[4 * u + 3] * up));
       }
       if (lane == 0) {
-        const int n = real ? visible_tokens(L, g.R, j, cap) : 0;
+        const int sees = real ? visible_tokens(L, g.R, j, cap) : 0;
         s_cq[c] = real ? p.k_scale * p.sm_scale * kLog2e * down : 1.f;
-        s_n[c] = n;
-        s_lo[c] = first_seen(n, sh.window);
+        s_n[c] = sees;
+        s_lo[c] = first_seen(sees, sh.window);
       }
     }
     __syncthreads();
@@ -438,73 +531,101 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
     __syncthreads();   // every warp's copies have landed and been read: the ring is free
 
     // ---- the warps' states joined ----------------------------------------------------
+    // Fragment by fragment as the lanes hold them (no bank conflicts): thread (i, t, lane)
+    // adds up the W warps' four values of two vectors and two dims.
     float* j_base = reinterpret_cast<float*>(smem);        // [W][kCols]
     float* j_sum = j_base + W * kCols;                     // [W][kCols]
-    float* j_o = j_sum + W * kCols;                        // [W][kCols][D]
+    float* j_f = j_sum + W * kCols;                        // [W][kCols]
+    float4* j_o = reinterpret_cast<float4*>(j_f + W * kCols);   // [W][DT][NT][32]
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float x = sum[t][e];
 #pragma unroll
         for (int s2 = 4; s2 < 32; s2 <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s2);
-        const int c = 8 * t + 2 * tig + e;
         if (gid == 0) {
-          j_base[warp * kCols + c] = base[t][e];
-          j_sum[warp * kCols + c] = x;
+          j_base[warp * kCols + 8 * t + 2 * tig + e] = base[t][e];
+          j_sum[warp * kCols + 8 * t + 2 * tig + e] = x;
         }
-        // dims (D/8) gid ..: row gid of dim tile i is dim 2i, row gid + 8 is 2i + 1
-        float* dst = j_o + ((size_t)warp * kCols + c) * D + (D / 8) * gid;
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-          *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[i][t][e], o[i][t][2 + e]);
       }
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+        j_o[((warp * DT + i) * NT + t) * 32 + lane] =
+            make_float4(o[i][t][0], o[i][t][1], o[i][t][2], o[i][t][3]);
+    }
     __syncthreads();
-    for (int i = tid; i < vecs * (D / 4); i += C::kThreads) {
-      const int c = i / (D / 4), d = 4 * (i % (D / 4));
+    for (int x = tid; x < W * kCols; x += C::kThreads) {
+      const int c = x % kCols;
       float m = kNoBase;
 #pragma unroll
       for (int w = 0; w < W; ++w) m = fmaxf(m, j_base[w * kCols + c]);
-      float l = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      j_f[x] = exp2_approx(j_base[x] - m);
+    }
+    __syncthreads();
+    const bool whole = begins && ends;
+    float* rec = p.records + ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * record_floats(sh.vt, D);
+    for (int x = tid; x < DT * NT * 32; x += C::kThreads) {
+      const int i = x / (NT * 32), t = (x / 32) % NT;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f}, l[2] = {0.f, 0.f}, m[2] = {kNoBase, kNoBase};
+      const int c0 = 8 * t + 2 * tig;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const float f = exp2_approx(j_base[w * kCols + c] - m);
-        const float4 x = *reinterpret_cast<const float4*>(j_o + ((size_t)w * kCols + c) * D + d);
-        l = fmaf(j_sum[w * kCols + c], f, l);
-        acc.x = fmaf(x.x, f, acc.x);
-        acc.y = fmaf(x.y, f, acc.y);
-        acc.z = fmaf(x.z, f, acc.z);
-        acc.w = fmaf(x.w, f, acc.w);
+        const float4 v = j_o[((w * DT + i) * NT + t) * 32 + lane];
+        const float2 f = *reinterpret_cast<const float2*>(j_f + w * kCols + c0);
+        const float2 ls = *reinterpret_cast<const float2*>(j_sum + w * kCols + c0);
+        const float2 bs = *reinterpret_cast<const float2*>(j_base + w * kCols + c0);
+        acc[0] = fmaf(v.x, f.x, acc[0]);
+        acc[1] = fmaf(v.y, f.y, acc[1]);
+        acc[2] = fmaf(v.z, f.x, acc[2]);
+        acc[3] = fmaf(v.w, f.y, acc[3]);
+        l[0] = fmaf(ls.x, f.x, l[0]);
+        l[1] = fmaf(ls.y, f.y, l[1]);
+        m[0] = fmaxf(m[0], bs.x);
+        m[1] = fmaxf(m[1], bs.y);
       }
-      const int j = (vec0 + c) / sh.G, hh = (vec0 + c) % sh.G;
-      if (begins && ends) {
-        const int head = kvh * sh.G + hh;
-        const size_t row = ((size_t)b * g.R + j) * g.Hq + head;
-        if (!QSA_IN_BOUNDS(b < g.B && j < g.R && head < g.Hq, kChkOut)) continue;
-        if (p.sinks) {
-          const float s2 = p.sinks[head] * kLog2e, nm = fmaxf(m, s2);
-          const float f = exp2_approx(m - nm);
-          l = l * f + exp2_approx(s2 - nm);
-          acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
-          m = nm;
+      const int d = (D / 8) * gid + 2 * i;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = c0 + e;
+        if (c >= vecs) continue;
+        if (whole) {
+          const int j = (vec0 + c) / sh.G, head = kvh * sh.G + (vec0 + c) % sh.G;
+          const size_t row = ((size_t)b * g.R + j) * g.Hq + head;
+          if (!QSA_IN_BOUNDS(b < g.B && j < g.R && head < g.Hq, kChkOut)) continue;
+          float f = 1.f;
+          if (p.sinks) add_sink(p.sinks[head], m[e], l[e], f);
+          const float r = l[e] > 0.f ? f * p.v_scale / l[e] : 0.f;
+          *reinterpret_cast<__nv_bfloat162*>(p.out + row * D + d) =
+              __floats2bfloat162_rn(acc[e] * r, acc[2 + e] * r);
+          if (d == 0) p.lse[row] = l[e] > 0.f ? (m[e] + log2f(l[e])) * kLn2 : -INFINITY;
+        } else {
+          if (d == 0) {
+            rec[c] = m[e];
+            rec[sh.vt + c] = l[e];
+          }
+          *reinterpret_cast<float2*>(rec + 2 * sh.vt + (size_t)c * D + d) = make_float2(acc[e], acc[2 + e]);
         }
-        const float r = l > 0.f ? p.v_scale / l : 0.f;
-        const __nv_bfloat162 a0 = __floats2bfloat162_rn(acc.x * r, acc.y * r);
-        const __nv_bfloat162 a1 = __floats2bfloat162_rn(acc.z * r, acc.w * r);
-        *reinterpret_cast<uint2*>(p.out + row * D + d) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&a0), *reinterpret_cast<const uint32_t*>(&a1));
-        if (d == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-      } else {
-        float* rec = p.records + ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * record_floats(sh.vt, D);
-        if (d == 0) {
-          rec[c] = m;
-          rec[sh.vt + c] = l;
-        }
-        *reinterpret_cast<float4*>(rec + 2 * sh.vt + (size_t)c * D + d) = acc;
       }
     }
-    if (tid == 0 && ends) describe(sh, p, span, cursor, seg, blockIdx.x);
+
+    // ---- a divided unit: the last CTA to be done with it joins its records -------------
+    if (!whole) {
+      const long long start = cursor.at - todo - seg.c_at;      // the unit's first chunk
+      const int first = (int)(start / span.share), last = (int)((start + seg.count - 1) / span.share);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int before = atomicAdd(&p.tickets[last], 1);
+        s_n[0] = before == last - first;
+        if (before == last - first) p.tickets[last] = 0;
+      }
+      __syncthreads();
+      if (s_n[0]) {
+        __threadfence();
+        join_parts<D, W>(sh, p, b, vec0, vecs, kvh, first, last, reinterpret_cast<float*>(smem));
+      }
+    }
     __syncthreads();
   }
 }
@@ -638,8 +759,10 @@ size_t dense_carve(const dense::Shape& s, void* workspace, dense::Work* w) {
   uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
   if (w) {
     w->status = reinterpret_cast<int*>(base);
-    w->desc = reinterpret_cast<dense::Desc*>(base + off);
+    w->tickets = reinterpret_cast<int*>(base + off);
   }
+  off += ((size_t)s.ctas * sizeof(int) + 255) / 256 * 256;
+  if (w) w->desc = reinterpret_cast<dense::Desc*>(base + off);
   off += ((size_t)dense::desc_count(s) * sizeof(dense::Desc) + 255) / 256 * 256;
   if (w) w->records = reinterpret_cast<float*>(base + off);
   off += (size_t)s.ctas * 2 * dense::record_floats(s.vt, s.g.D) * sizeof(float);
@@ -729,15 +852,13 @@ cudaError_t launch_dense(const Geom& g, const DenseArgs& a, cudaStream_t stream)
   w.out = reinterpret_cast<__nv_bfloat16*>(a.out);
   w.lse = a.lse;
   dense_carve(s, a.workspace, &w);
-  cudaError_t e;
-  if (use_tiles(g))
-    e = launch_dense_tile(s, w, stream);
-  else if (g.D == 128)
-    e = s.vt == 8 ? launch_decode<C128a>(s, w, stream) : launch_decode<C128b>(s, w, stream);
-  else
-    e = s.vt == 8 ? launch_decode<C256a>(s, w, stream) : launch_decode<C256b>(s, w, stream);
-  if (e != cudaSuccess) return e;
-  return launch_dense_join(s, w, stream);
+  if (use_tiles(g)) {
+    const cudaError_t e = launch_dense_tile(s, w, stream);
+    return e != cudaSuccess ? e : launch_dense_join(s, w, stream);
+  }
+  if (g.D == 128)
+    return s.vt == 8 ? launch_decode<C128a>(s, w, stream) : launch_decode<C128b>(s, w, stream);
+  return s.vt == 8 ? launch_decode<C256a>(s, w, stream) : launch_decode<C256b>(s, w, stream);
 }
 
 }  // namespace qsa

@@ -18,7 +18,9 @@
 // ends writes its descriptor, and a second kernel joins the records in the
 // CTAs' order, whatever order they ended in.  Descriptors go by unit, or, where
 // there are more units than CTAs, by the CTA where the divided unit ends (there
-// is at most one).
+// is at most one).  The decode kernel's records are small, and the CTA that is
+// last to finish with a unit joins them itself, in the same order (a ticket per
+// CTA where a divided unit ends, which every call leaves at zero).
 #pragma once
 
 #include "qsa_common.cuh"
@@ -62,6 +64,7 @@ struct Work {
   float* lse;
   int* status;
   Desc* desc;        // [units or CTAs]
+  int* tickets;      // [CTAs]
   float* records;    // [CTAs][2][vt][2 + D]: bases, sums, outputs
 };
 
@@ -121,6 +124,26 @@ __device__ __forceinline__ Span plan_span(const Shape& s, const int32_t* seqlens
   __shared__ int s_group;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = s.g.B * s.tiles;
+  if (groups <= 32) {   // a lane per group, every warp for itself
+    const uint32_t hkv = (uint32_t)s.g.Hkv;   // (counts to 2^17, heads to 2^8: within 32 bits)
+    const uint32_t mine = lane < groups ? (uint32_t)chunk_count(s, seqlens, lane) * hkv : 0u;
+    uint32_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const uint32_t total = __shfl_sync(0xffffffffu, x, 31);
+    const uint32_t share = max((total + (uint32_t)ctas - 1) / (uint32_t)ctas, (uint32_t)s.least);
+    Span span;
+    span.share = share;
+    span.begin = (long long)share * cta;
+    span.end = min((long long)total, span.begin + share);
+    const uint32_t past = __ballot_sync(0xffffffffu, (long long)x > span.begin);
+    span.group = past ? __ffs(past) - 1 : 0;
+    span.group_at = __shfl_sync(0xffffffffu, x - mine, span.group);
+    return span;
+  }
   const int per = (groups + NTHR - 1) / NTHR;
   const int g0 = min(groups, tid * per), g1 = min(groups, g0 + per);
   long long mine = 0;
