@@ -569,7 +569,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
       const int i = x / (NT * 32), t = (x / 32) % NT;
       float acc[4] = {0.f, 0.f, 0.f, 0.f}, l[2] = {0.f, 0.f}, m[2] = {kNoBase, kNoBase};
       const int c0 = 8 * t + 2 * tig;
-#pragma unroll
+#pragma unroll 4
       for (int w = 0; w < W; ++w) {
         const float4 v = j_o[((w * DT + i) * NT + t) * 32 + lane];
         const float2 f = *reinterpret_cast<const float2*>(j_f + w * kCols + c0);
@@ -611,8 +611,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
 
     // ---- a divided unit: the last CTA to be done with it joins its records -------------
     if (!whole) {
-      const long long start = cursor.at - todo - seg.c_at;      // the unit's first chunk
-      const int first = (int)(start / span.share), last = (int)((start + seg.count - 1) / span.share);
+      const int first = cursor.first_cta(sh, span.share), last = cursor.last_cta(sh, seg, span.share);
       __threadfence();
       __syncthreads();
       if (tid == 0) {
@@ -803,6 +802,7 @@ dense::Shape decode_shape(const Geom& g, int window) {
   s.tok_sh = tok == 64 ? 6 : 5;
   s.window = window;
   s.least = 16;
+  s.lead = tok == 64 ? 16 : 32;
   s.ctas = dense_sms();
   s.by_unit = dense::unit_count(s) <= s.ctas;
   return s;

@@ -10,7 +10,9 @@
 // zeros.  The units' chunks, one behind the other, are divided evenly over the
 // CTAs of the grid by the requests' actual lengths: CTA i takes chunks
 // [i*share, (i+1)*share).  So every CTA ends at about the same time whatever
-// the lengths, and a single long request still uses the whole GPU.
+// the lengths, and a single long request still uses the whole GPU.  Starting a unit
+// costs as much as some chunks do, so each counts with `lead` chunks more, ahead of its
+// own, that hold nothing.
 //
 // A unit inside one CTA is written out by it.  A unit that crosses CTAs leaves
 // a record (base, sum, unscaled output per vector) from each of them: in slot 1
@@ -43,6 +45,7 @@ struct Shape {
   int tok_sh;    // log2 of the tokens per chunk
   int window;    // tokens a row looks back over; 0: all
   int least;     // chunks a CTA takes at least
+  int lead;      // chunks that a unit counts beyond its own
   int ctas;      // CTAs of the grid
   int by_unit;   // descriptors go by unit (else by CTA)
 };
@@ -104,7 +107,7 @@ __device__ __forceinline__ Sight sight_of(const Shape& s, int L, int tile) {
 
 __device__ __forceinline__ int chunk_count(const Shape& s, const int32_t* seqlens, int group) {
   const uint32_t b = (uint32_t)group / (uint32_t)s.tiles;
-  return sight_of(s, seqlens[b], group - (int)b * s.tiles).count;
+  return sight_of(s, seqlens[b], group - (int)b * s.tiles).count + s.lead;
 }
 
 // This CTA's part of the work, in the groups (request, tile) in order, each
@@ -198,29 +201,42 @@ struct Seg : Sight {
 
 // Walks a span's parts in order; every role of a CTA walks its own copy.
 struct Cursor {
-  long long at, end, group_at;
+  long long at, end, group_at, unit_at;
   int group;
   __device__ __forceinline__ explicit Cursor(const Span& s)
-      : at(s.begin), end(s.end), group_at(s.group_at), group(s.group) {}
+      : at(s.begin), end(s.end), group_at(s.group_at), unit_at(0), group(s.group) {}
   __device__ __forceinline__ bool next(const Shape& s, const int32_t* seqlens, Seg& g) {
-    if (at >= end) return false;
-    g.b = (int)((uint32_t)group / (uint32_t)s.tiles);
-    g.tile = group - g.b * s.tiles;
-    g.L = seqlens[g.b];
-    static_cast<Sight&>(g) = sight_of(s, g.L, g.tile);
-    const uint32_t in_group = (uint32_t)(at - group_at);   // (at most 2^17 chunks of 256 heads)
-    g.kvh = (int)(in_group / (uint32_t)g.count);
-    g.c_at = (int)in_group - g.kvh * g.count;
-    g.todo = (int)min((long long)(g.count - g.c_at), end - at);
-    g.begins = g.c_at == 0;
-    g.ends = g.c_at + g.todo == g.count;
-    g.chunk0 = g.first + g.c_at;
-    at += g.todo;
-    if (at == group_at + (long long)g.count * s.g.Hkv) {
-      group_at = at;
-      ++group;
+    while (at < end) {
+      g.b = (int)((uint32_t)group / (uint32_t)s.tiles);
+      g.tile = group - g.b * s.tiles;
+      g.L = seqlens[g.b];
+      static_cast<Sight&>(g) = sight_of(s, g.L, g.tile);
+      const uint32_t len = (uint32_t)(g.count + s.lead);
+      const uint32_t in_group = (uint32_t)(at - group_at);   // (at most 2^18 chunks of 256 heads)
+      g.kvh = (int)(in_group / len);
+      const int from = (int)(in_group - (uint32_t)g.kvh * len);
+      const int to = (int)min((long long)len, from + (end - at));
+      unit_at = at - from;
+      at += to - from;
+      if (at == group_at + (long long)len * s.g.Hkv) {
+        group_at = at;
+        ++group;
+      }
+      g.c_at = max(from - s.lead, 0);
+      g.todo = max(to - s.lead, 0) - g.c_at;
+      g.begins = g.c_at == 0;
+      g.ends = g.c_at + g.todo == g.count;
+      g.chunk0 = g.first + g.c_at;
+      if (g.todo > 0) return true;
     }
-    return true;
+    return false;
+  }
+  // The CTAs where the unit of the last part begins and ends.
+  __device__ __forceinline__ int first_cta(const Shape& s, long long share) const {
+    return (int)((unit_at + s.lead) / share);
+  }
+  __device__ __forceinline__ int last_cta(const Shape& s, const Seg& g, long long share) const {
+    return (int)((unit_at + s.lead + g.count - 1) / share);
   }
 };
 
@@ -232,8 +248,7 @@ __device__ __forceinline__ void describe(const Shape& s, const Work& w, const Sp
   d.b = seg.begins ? -1 : seg.b;
   d.tile = seg.tile;
   d.kvh = seg.kvh;
-  // the unit's first chunk is todo + c_at before the cursor
-  d.first = (int)((cursor.at - seg.todo - seg.c_at) / span.share);
+  d.first = cursor.first_cta(s, span.share);
   d.last = cta;
   if (s.by_unit)
     w.desc[(seg.b * s.tiles + seg.tile) * s.g.Hkv + seg.kvh] = d;

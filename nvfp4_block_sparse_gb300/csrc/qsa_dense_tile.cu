@@ -947,6 +947,7 @@ dense::Shape dense_tile_shape(const Geom& g, int window) {
   s.tiles = (g.R * s.G + s.vt - 1) / s.vt;
   s.window = window;
   s.least = 4;
+  s.lead = 6;
   s.by_unit = dense::unit_count(s) <= s.ctas;
   return s;
 }
