@@ -66,7 +66,6 @@ struct KernelArgs {
   NormRope nr;
   PrologueArgs a;
   int groups;      // warps per row
-  int heads;       // heads per warp
   int total;       // heads per row: query, key and (append) value heads
 };
 
@@ -89,7 +88,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int D, bool kAppend, int STEPS>
+template <int D, bool kAppend, bool kInter, int STEPS>
 __global__ void __launch_bounds__(kWarps * 32)
 prologue_kernel(const __grid_constant__ KernelArgs p) {
   constexpr int LPV = D / 8;        // lanes per head
@@ -98,14 +97,14 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
   const PrologueArgs& a = p.a;
   const int lane = threadIdx.x & 31;
   const int l = lane % LPV, e0 = 8 * l;   // the lane's first element
-  const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const long long T = (long long)g.B * g.R;
+  const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const uint32_t T = (uint32_t)g.B * (uint32_t)g.R;
   pdl_wait();
   pdl_trigger();
-  const long long r = item / p.groups;
+  const uint32_t r = item / (uint32_t)p.groups;   // (2^24 rows of at most 2^7 warps)
   if (r >= T) return;
-  const int v0 = (int)(item % p.groups) * p.heads;
-  const int v1 = min(v0 + p.heads, p.total);
+  const int v0 = (int)(item - r * (uint32_t)p.groups) * (VPW * STEPS);
+  const int v1 = min(v0 + VPW * STEPS, p.total);
   const int hq = a.q ? g.Hq : 0;
 
   // all of the warp's heads are requested before anything waits for one
@@ -115,10 +114,9 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
     const int hv = v0 + i * VPW + lane / LPV;
     raws[i] = make_uint4(0u, 0u, 0u, 0u);
     if (hv < v1) {
-      const __nv_bfloat16* src = hv < hq           ? a.q + r * a.q_stride + (size_t)hv * D
-                                 : hv < hq + g.Hkv ? a.k + r * a.k_stride + (size_t)(hv - hq) * D
-                                                   : a.v + r * a.v_stride +
-                                                         (size_t)(hv - hq - g.Hkv) * D;
+      const __nv_bfloat16* src = hv < hq           ? a.q + r * a.q_stride + hv * D
+                                 : hv < hq + g.Hkv ? a.k + r * a.k_stride + (hv - hq) * D
+                                                   : a.v + r * a.v_stride + (hv - hq - g.Hkv) * D;
       raws[i] = *reinterpret_cast<const uint4*>(src + e0);
     }
   }
@@ -132,14 +130,18 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) { c[i] = 1.f; s[i] = 0.f; }
   if (turned && v0 < hq + g.Hkv) {
-    const float2* row = reinterpret_cast<const float2*>(a.cs) + r * h;
-    if (p.nr.interleaved) {
+    const float2* row = reinterpret_cast<const float2*>(a.cs) + (size_t)r * h;
+    if (kInter) {
+      const float4* row4 = reinterpret_cast<const float4*>(row + (e0 >> 1));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 t = __ldg(row + (e0 >> 1) + i);
-        c[2 * i] = c[2 * i + 1] = t.x;
-        s[2 * i] = -t.y;
-        s[2 * i + 1] = t.y;
+      for (int i = 0; i < 2; ++i) {
+        const float4 t = __ldg(row4 + i);
+        c[4 * i] = c[4 * i + 1] = t.x;
+        s[4 * i] = -t.y;
+        s[4 * i + 1] = t.y;
+        c[4 * i + 2] = c[4 * i + 3] = t.z;
+        s[4 * i + 2] = -t.w;
+        s[4 * i + 3] = t.w;
       }
     } else {
       const bool first = e0 < h;
@@ -157,25 +159,67 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
   }
 
   // the row's slot in the cache
-  size_t page_row = 0;   // first token row of the page, before the head
+  size_t page_row = 0;
   int slot = 0;
   bool has_slot = false;
-  if (kAppend) {
-    const int b = (int)(r / g.R), j = (int)(r % g.R);
-    const long long pos = (long long)a.seqlens[b] - g.R + j;
+  if (kAppend && v1 > hq) {
+    const uint32_t b = r / (uint32_t)g.R;
+    const long long pos = (long long)a.seqlens[b] - g.R + (int)(r - b * (uint32_t)g.R);
     if (pos >= 0 && pos < (long long)g.MB * g.P) {
-      const int page = a.page_table[(size_t)b * g.MB + (int)(pos / g.P)];
-      slot = (int)(pos % g.P);
+      const int at = (int)pos, beta = at / g.P;
+      const int page = a.page_table[(size_t)b * g.MB + beta];
+      slot = at - beta * g.P;
       has_slot = page >= 0 && page < g.NP;
       page_row = (size_t)(has_slot ? page : 0);
     }
-    // the index key: one warp per row, 16 lanes x 4 B
-    if (v0 == 0 && has_slot && lane < kIndexDim / 4) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(a.ik + r * kIndexDim + 4 * lane);
+    // the index key, by the row's last warp: 16 lanes x 4 B
+    if (v1 == p.total && has_slot && lane < kIndexDim / 4) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(a.ik + (size_t)r * kIndexDim + 4 * lane);
       *reinterpret_cast<uint32_t*>(a.ik_pool + (page_row * g.P + slot) * kIndexDim + 4 * lane) = w;
     }
   }
 
+  // Sums of squares, neighbours first: eight in the lane, then lanes 1, 2, 4, ...
+  // apart.  Four steps' sums are folded into one another on the way (a lane passes on
+  // the sums it does not keep), so that lane i ends with that of step i mod 4, and one
+  // square root and division serve all four.
+  float rms[STEPS];
+  if (v0 < hq + g.Hkv && (a.q_weight || a.k_weight)) {
+    float ss[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      float x[8];
+      unpack8(raws[i], x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(x[k], x[k]);
+#pragma unroll
+      for (int n = 4; n; n >>= 1)
+#pragma unroll
+        for (int k = 0; k < n; ++k) x[k] = __fadd_rn(x[2 * k], x[2 * k + 1]);
+      ss[i] = x[0];
+    }
+    float sum;
+    if constexpr (STEPS == 4) {
+      const bool odd = lane & 1, upper = lane & 2;
+      const float k01 = odd ? ss[1] : ss[0], g01 = odd ? ss[0] : ss[1];
+      const float k23 = odd ? ss[3] : ss[2], g23 = odd ? ss[2] : ss[3];
+      const float s01 = __fadd_rn(k01, __shfl_xor_sync(0xffffffffu, g01, 1));
+      const float s23 = __fadd_rn(k23, __shfl_xor_sync(0xffffffffu, g23, 1));
+      sum = __fadd_rn(upper ? s23 : s01, __shfl_xor_sync(0xffffffffu, upper ? s01 : s23, 2));
+    } else {
+      sum = ss[0];
+    }
+#pragma unroll
+    for (int k = STEPS == 4 ? 4 : 1; k < LPV; k <<= 1)
+      sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, k));
+    const float inv = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(sum * (1.f / D), p.nr.eps)));
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+      rms[i] = STEPS == 4 ? __shfl_sync(0xffffffffu, inv, (lane & ~(LPV - 1)) + i) : inv;
+  }
+
+  float w[8];
+  int w_kind = -1;
 #pragma unroll
   for (int step = 0; step < STEPS; ++step) {
     if (STEPS > 1 && v0 + step * VPW >= v1) break;
@@ -187,39 +231,29 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
     uint4 raw = raws[step];
     float x[8];
     unpack8(raw, x);
-    const bool any_qk = __any_sync(0xffffffffu, real && kind < 2);
-    if (any_qk) {
-      // sum of squares, neighbours first
-      float q[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(x[i], x[i]);
-#pragma unroll
-      for (int n = 4; n; n >>= 1)
-#pragma unroll
-        for (int i = 0; i < n; ++i) q[i] = __fadd_rn(q[2 * i], q[2 * i + 1]);
-      float ss = q[0];
-#pragma unroll
-      for (int o = 1; o < LPV; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
-      const __nv_bfloat16* weight = kind == 0 ? a.q_weight : a.k_weight;
+    if (v0 + step * VPW < hq + g.Hkv) {     // a query or key among the warp's heads
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = x[i];
+      const __nv_bfloat16* weight = kind == 0 ? a.q_weight : a.k_weight;
       if (weight && kind < 2) {
-        const float rms = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(ss * (1.f / D), p.nr.eps)));
-        float w[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(weight + e0)), w);
+        if (kind != w_kind) {
+          w_kind = kind;
+          unpack8(__ldg(reinterpret_cast<const uint4*>(weight + e0)), w);
+          if (p.nr.plus_one) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (p.nr.plus_one) w[i] = __fadd_rn(1.f, w[i]);
-          y[i] = __fmul_rn(__fmul_rn(x[i], rms), w[i]);
+            for (int i = 0; i < 8; ++i) w[i] = __fadd_rn(1.f, w[i]);
+          }
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(__fmul_rn(x[i], rms[step]), w[i]);
       }
       if (rot) {
-        if (p.nr.interleaved) {
+        if (kInter) {
+          if (turned) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float u = y[2 * i], t = y[2 * i + 1];
-            if (turned) {
+            for (int i = 0; i < 4; ++i) {
+              const float u = y[2 * i], t = y[2 * i + 1];
               y[2 * i] = __fadd_rn(__fmul_rn(u, c[2 * i]), __fmul_rn(t, s[2 * i]));
               y[2 * i + 1] = __fadd_rn(__fmul_rn(t, c[2 * i + 1]), __fmul_rn(u, s[2 * i + 1]));
             }
@@ -234,14 +268,14 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
       }
       if (kind < 2) {
         raw = pack8(y);
-        unpack8(raw, x);
+        if (kAppend) unpack8(raw, x);
         if (real && kind == 0)
           *reinterpret_cast<uint4*>(a.q_out + ((size_t)r * g.Hq + head) * D + e0) = raw;
         if (!kAppend && real && kind == 1)
           *reinterpret_cast<uint4*>(a.k_out + ((size_t)r * g.Hkv + head) * D + e0) = raw;
       }
     }
-    if (!kAppend || !__any_sync(0xffffffffu, real && kind > 0)) continue;
+    if (!kAppend || min(v0 + (step + 1) * VPW, v1) <= hq) continue;   // (queries alone)
 
     // keys and values: blocks of 16 (two lanes) to e2m1 codes and an e4m3 scale,
     // as the token store quantises them
@@ -352,16 +386,21 @@ cudaError_t launch_prologue(const Geom& g, const NormRope& nr, const PrologueArg
   // Few rows: a warp per step of heads, for the shortest chain; many rows: four
   // steps per warp share the row's cos and sin.
   const int steps = T * p.total / vpw > 152 * 64 ? 4 : 1;
-  p.heads = vpw * steps;
-  p.groups = (p.total + p.heads - 1) / p.heads;
+  p.groups = (p.total + vpw * steps - 1) / (vpw * steps);
   const long long items = T * p.groups;
-  auto pick = [&]<int STEPS>() {
-    return g.D == 256 ? (append ? prologue_kernel<256, true, STEPS> : prologue_kernel<256, false, STEPS>)
-                      : (append ? prologue_kernel<128, true, STEPS> : prologue_kernel<128, false, STEPS>);
+  auto launch_it = [&]<int D, bool kAppend, bool kInter>() {
+    auto* kern = steps == 4 ? prologue_kernel<D, kAppend, kInter, 4> : prologue_kernel<D, kAppend, kInter, 1>;
+    return launch(kern, dim3((unsigned)((items + kWarps - 1) / kWarps)), dim3(kWarps * 32), pdl,
+                  stream, p);
   };
-  auto* kern = steps == 4 ? pick.template operator()<4>() : pick.template operator()<1>();
-  return launch(kern, dim3((unsigned)((items + kWarps - 1) / kWarps)), dim3(kWarps * 32), pdl,
-                stream, p);
+  auto of_dim = [&]<int D>() {
+    if (append)
+      return nr.interleaved ? launch_it.template operator()<D, true, true>()
+                            : launch_it.template operator()<D, true, false>();
+    return nr.interleaved ? launch_it.template operator()<D, false, true>()
+                          : launch_it.template operator()<D, false, false>();
+  };
+  return g.D == 256 ? of_dim.template operator()<256>() : of_dim.template operator()<128>();
 }
 
 cudaError_t launch_load_tokens(const Geom& g, const int32_t* page_table, const int32_t* seqlens,
