@@ -53,43 +53,110 @@ rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
 // Norms, rotation, append.
 //
 // A head of D elements belongs to D/8 lanes, eight elements (16 bytes) each: a
-// warp holds two heads at D = 128, one at D = 256.  A warp takes STEPS times the
-// heads it holds of one row, all requested before the first is used, and keeps
-// the row's cos and sin in registers meanwhile.  The pairs of the half layout meet by a
+// warp holds two heads at D = 128, one at D = 256.  A warp's turn is STEPS times
+// the heads it holds of one row and kind (query, key or value): all requested
+// before the first is used, and with many rows the next turn's before this
+// one's are worked on.  The row's cos and sin stay in registers meanwhile, and the
+// arithmetic is on packed pairs.  The pairs of the half layout meet by a
 // shuffle over rotary_dim / 16 lanes (rotary_dim is a multiple of 16, so a
 // lane's eight elements have one partner lane); interleaved pairs are in the lane.
+//
+// Bound by instructions before memory: about 100 per head and warp; see the
+// quantiser below for what its divisions cost.
 // ---------------------------------------------------------------------------
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 struct KernelArgs {
   Geom g;
   NormRope nr;
   PrologueArgs a;
-  int groups;      // warps per row
-  int total;       // heads per row: query, key and (append) value heads
+  int turns_q, turns_k, turns;   // turns per row: queries, keys (values as many), all
+  float k_inv6, v_inv6;          // 1 / (6 scale), or 0 where that is far from 1
 };
 
-__device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+// y c + t s, each operation rounded.  Not by packed pairs: the assembler fuses a packed
+// product and sum, which rounds once (seen as one flipped bf16 result in 10^5).  (The
+// squares may be: products of bf16 values are exact.)
+__device__ __forceinline__ float2 turn2(float2 y, float2 c, float2 t, float2 s) {
+  return make_float2(__fadd_rn(__fmul_rn(y.x, c.x), __fmul_rn(t.x, s.x)),
+                     __fadd_rn(__fmul_rn(y.y, c.y), __fmul_rn(t.y, s.y)));
+}
+
+__device__ __forceinline__ void unpack8(const uint4& r, float2 (&x)[4]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x[i].x, x[i].y);
     w[i] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A block of 16 values (this lane has eight, its neighbour the rest), of largest
+// magnitude m, to codes and scale as the token store's divisions give them:
+//   sf = e4m3((m / 6) / scale),  codes = e2m1(x / (e4m3(sf) scale)).
+// Ten IEEE divisions per lane were most of the append's instructions.  A product
+// with a reciprocal is within 2^-21 of the quotient; where 2^-20 to either side rounds
+// to the same code, rounding being monotonic, so does the quotient.  Otherwise (about
+// one block in 10^4), or where the scale is so small or large that the reciprocal is not
+// a normal number (`inv6` = 0), the divisions decide.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t quantise8(const float2 (&x)[4], float m, float scale, float inv6,
+                                              uint32_t& sf) {
+  constexpr float kUp = 1.f + 0x1p-20f, kDown = 1.f - 0x1p-20f;
+  const float t = m * inv6;
+  sf = f32_to_e4m3(t * kUp);
+  if (inv6 == 0.f || sf != f32_to_e4m3(t * kDown)) sf = f32_to_e4m3(__fdiv_rn(__fdiv_rn(m, 6.0f), scale));
+  const float den = __fmul_rn(e4m3_to_f32(sf), scale);
+  if (den == 0.f) return 0u;
+  const float inv = rcp_approx(den);
+  uint32_t up = 0, down = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = mul2(x[i], make_float2(inv, inv));
+    const float2 hi = mul2(y, make_float2(kUp, kUp)), lo = mul2(y, make_float2(kDown, kDown));
+    up |= f32x2_to_e2m1x2(hi.x, hi.y) << (8 * i);
+    down |= f32x2_to_e2m1x2(lo.x, lo.y) << (8 * i);
+  }
+  if (inv6 == 0.f || up != down) {
+    up = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      up |= f32x2_to_e2m1x2(__fdiv_rn(x[i].x, den), __fdiv_rn(x[i].y, den)) << (8 * i);
+  }
+  // codes whose magnitude is zero are +0
+  const uint32_t mag = (up | (up >> 1) | (up >> 2)) & 0x11111111u;
+  return up & (0x77777777u | (mag << 3));
+}
+
 template <int D, bool kAppend, bool kInter, int STEPS>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, STEPS == 1 ? 8 : 5)
 prologue_kernel(const __grid_constant__ KernelArgs p) {
   constexpr int LPV = D / 8;        // lanes per head
   constexpr int VPW = 32 / LPV;     // heads that a warp holds
@@ -97,209 +164,216 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
   const PrologueArgs& a = p.a;
   const int lane = threadIdx.x & 31;
   const int l = lane % LPV, e0 = 8 * l;   // the lane's first element
-  const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const uint32_t T = (uint32_t)g.B * (uint32_t)g.R;
   pdl_wait();
   pdl_trigger();
-  const uint32_t r = item / (uint32_t)p.groups;   // (2^24 rows of at most 2^7 warps)
-  if (r >= T) return;
-  const int v0 = (int)(item - r * (uint32_t)p.groups) * (VPW * STEPS);
-  const int v1 = min(v0 + VPW * STEPS, p.total);
-  const int hq = a.q ? g.Hq : 0;
 
-  // all of the warp's heads are requested before anything waits for one
-  uint4 raws[STEPS];
-#pragma unroll
-  for (int i = 0; i < STEPS; ++i) {
-    const int hv = v0 + i * VPW + lane / LPV;
-    raws[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (hv < v1) {
-      const __nv_bfloat16* src = hv < hq           ? a.q + r * a.q_stride + hv * D
-                                 : hv < hq + g.Hkv ? a.k + r * a.k_stride + (hv - hq) * D
-                                                   : a.v + r * a.v_stride + (hv - hq - g.Hkv) * D;
-      raws[i] = *reinterpret_cast<const uint4*>(src + e0);
-    }
-  }
-
-  // the lane's cos and sin: o = y c + partner s, with the sign of the first
-  // half's sine in s
-  const int rot = p.nr.rot, h = rot >> 1;
-  const bool turned = e0 < rot;
-  int partner = lane;
-  float c[8], s[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) { c[i] = 1.f; s[i] = 0.f; }
-  if (turned && v0 < hq + g.Hkv) {
-    const float2* row = reinterpret_cast<const float2*>(a.cs) + (size_t)r * h;
-    if (kInter) {
-      const float4* row4 = reinterpret_cast<const float4*>(row + (e0 >> 1));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 t = __ldg(row4 + i);
-        c[4 * i] = c[4 * i + 1] = t.x;
-        s[4 * i] = -t.y;
-        s[4 * i + 1] = t.y;
-        c[4 * i + 2] = c[4 * i + 3] = t.z;
-        s[4 * i + 2] = -t.w;
-        s[4 * i + 3] = t.w;
-      }
-    } else {
-      const bool first = e0 < h;
-      partner = first ? lane + h / 8 : lane - h / 8;
-      const float4* row4 = reinterpret_cast<const float4*>(row + (first ? e0 : e0 - h));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 t = __ldg(row4 + i);
-        c[2 * i] = t.x;
-        c[2 * i + 1] = t.z;
-        s[2 * i] = first ? -t.y : t.y;
-        s[2 * i + 1] = first ? -t.w : t.w;
-      }
-    }
-  }
-
-  // the row's slot in the cache
-  size_t page_row = 0;
-  int slot = 0;
-  bool has_slot = false;
-  if (kAppend && v1 > hq) {
-    const uint32_t b = r / (uint32_t)g.R;
-    const long long pos = (long long)a.seqlens[b] - g.R + (int)(r - b * (uint32_t)g.R);
-    if (pos >= 0 && pos < (long long)g.MB * g.P) {
-      const int at = (int)pos, beta = at / g.P;
-      const int page = a.page_table[(size_t)b * g.MB + beta];
-      slot = at - beta * g.P;
-      has_slot = page >= 0 && page < g.NP;
-      page_row = (size_t)(has_slot ? page : 0);
-    }
-    // the index key, by the row's last warp: 16 lanes x 4 B
-    if (v1 == p.total && has_slot && lane < kIndexDim / 4) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(a.ik + (size_t)r * kIndexDim + 4 * lane);
-      *reinterpret_cast<uint32_t*>(a.ik_pool + (page_row * g.P + slot) * kIndexDim + 4 * lane) = w;
-    }
-  }
-
-  // Sums of squares, neighbours first: eight in the lane, then lanes 1, 2, 4, ...
-  // apart.  Four steps' sums are folded into one another on the way (a lane passes on
-  // the sums it does not keep), so that lane i ends with that of step i mod 4, and one
-  // square root and division serve all four.
-  float rms[STEPS];
-  if (v0 < hq + g.Hkv && (a.q_weight || a.k_weight)) {
-    float ss[STEPS];
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      float x[8];
-      unpack8(raws[i], x);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(x[k], x[k]);
-#pragma unroll
-      for (int n = 4; n; n >>= 1)
-#pragma unroll
-        for (int k = 0; k < n; ++k) x[k] = __fadd_rn(x[2 * k], x[2 * k + 1]);
-      ss[i] = x[0];
-    }
-    float sum;
-    if constexpr (STEPS == 4) {
-      const bool odd = lane & 1, upper = lane & 2;
-      const float k01 = odd ? ss[1] : ss[0], g01 = odd ? ss[0] : ss[1];
-      const float k23 = odd ? ss[3] : ss[2], g23 = odd ? ss[2] : ss[3];
-      const float s01 = __fadd_rn(k01, __shfl_xor_sync(0xffffffffu, g01, 1));
-      const float s23 = __fadd_rn(k23, __shfl_xor_sync(0xffffffffu, g23, 1));
-      sum = __fadd_rn(upper ? s23 : s01, __shfl_xor_sync(0xffffffffu, upper ? s01 : s23, 2));
-    } else {
-      sum = ss[0];
-    }
-#pragma unroll
-    for (int k = STEPS == 4 ? 4 : 1; k < LPV; k <<= 1)
-      sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, k));
-    const float inv = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(sum * (1.f / D), p.nr.eps)));
+  // A turn: row, kind (0 query, 1 key, 2 value) and the lane's first head.
+  struct Turn {
+    uint32_t row;
+    int kind, head;
+  };
+  auto turn_of = [&](uint32_t item) {     // (2^24 rows of at most 2^8 turns)
+    Turn t;
+    t.row = item / (uint32_t)p.turns;
+    int i = (int)(item - t.row * (uint32_t)p.turns);
+    t.kind = i < p.turns_q ? 0 : i < p.turns_q + p.turns_k ? 1 : 2;
+    i -= t.kind == 0 ? 0 : t.kind == 1 ? p.turns_q : p.turns_q + p.turns_k;
+    t.head = i * (VPW * STEPS) + lane / LPV;
+    return t;
+  };
+  uint4 coming[STEPS];
+  auto request = [&](const Turn& t) {
+    const __nv_bfloat16* base = t.kind == 0 ? a.q : t.kind == 1 ? a.k : a.v;
+    const long long stride = t.kind == 0 ? a.q_stride : t.kind == 1 ? a.k_stride : a.v_stride;
+    const int heads = t.row >= T ? 0 : t.kind == 0 ? g.Hq : g.Hkv;
+    const __nv_bfloat16* src = base + t.row * stride + t.head * D + e0;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
-      rms[i] = STEPS == 4 ? __shfl_sync(0xffffffffu, inv, (lane & ~(LPV - 1)) + i) : inv;
-  }
+      coming[i] = t.head + i * VPW < heads ? *reinterpret_cast<const uint4*>(src + i * VPW * D)
+                                           : make_uint4(0u, 0u, 0u, 0u);
+  };
 
-  float w[8];
+  float2 w[4];          // the lane's weights of kind w_kind
   int w_kind = -1;
+  uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  Turn now = turn_of(item);
+  request(now);
+  while (now.row < T) {
+    const uint32_t r = now.row;
+    const int kind = now.kind, head0 = now.head, heads = kind == 0 ? g.Hq : g.Hkv;
+    const int left = heads - (head0 - lane / LPV);     // of the warp: steps past it hold nothing
+    uint4 raws[STEPS];
 #pragma unroll
-  for (int step = 0; step < STEPS; ++step) {
-    if (STEPS > 1 && v0 + step * VPW >= v1) break;
-    // warp-wide shuffles below: a lane without a head takes part with zeros
-    const int hv = v0 + step * VPW + lane / LPV;
-    const bool real = hv < v1;
-    const int kind = hv < hq ? 0 : hv < hq + g.Hkv ? 1 : 2;   // query, key, value
-    const int head = kind == 0 ? hv : kind == 1 ? hv - hq : hv - hq - g.Hkv;
-    uint4 raw = raws[step];
-    float x[8];
-    unpack8(raw, x);
-    if (v0 + step * VPW < hq + g.Hkv) {     // a query or key among the warp's heads
-      float y[8];
+    for (int i = 0; i < STEPS; ++i) raws[i] = coming[i];
+    if (STEPS > 1) {
+      item += gridDim.x * kWarps;
+      now = turn_of(item);
+      request(now);
+    } else {
+      now.row = T;
+    }
+
+    // the row's slot in the cache
+    size_t page_row = 0;
+    int slot = 0;
+    bool has_slot = false;
+    if (kAppend && kind != 0) {
+      const uint32_t b = r / (uint32_t)g.R;
+      const long long pos = (long long)a.seqlens[b] - g.R + (int)(r - b * (uint32_t)g.R);
+      if (pos >= 0 && pos < (long long)g.MB * g.P) {
+        const int at = (int)pos, beta = (int)((uint32_t)at / (uint32_t)g.P);
+        const int page = a.page_table[(size_t)b * g.MB + beta];
+        slot = at - beta * g.P;
+        has_slot = page >= 0 && page < g.NP;
+        page_row = (size_t)(has_slot ? page : 0);
+      }
+      // the index key, with the row's first values: 16 lanes x 4 B
+      if (kind == 2 && head0 < VPW && has_slot && lane < kIndexDim / 4) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(a.ik + (size_t)r * kIndexDim + 4 * lane);
+        *reinterpret_cast<uint32_t*>(a.ik_pool + (page_row * g.P + slot) * kIndexDim + 4 * lane) = x;
+      }
+    }
+
+    if (kind < 2) {
+      // the lane's cos and sin: o = y c + partner s, with the sign of the first
+      // half's sine in s
+      const int rot = p.nr.rot, h = rot >> 1;
+      const bool turned = e0 < rot;
+      int partner = lane;
+      float2 c[4], s[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = x[i];
-      const __nv_bfloat16* weight = kind == 0 ? a.q_weight : a.k_weight;
-      if (weight && kind < 2) {
-        if (kind != w_kind) {
-          w_kind = kind;
-          unpack8(__ldg(reinterpret_cast<const uint4*>(weight + e0)), w);
-          if (p.nr.plus_one) {
+      for (int i = 0; i < 4; ++i) c[i] = s[i] = make_float2(0.f, 0.f);
+      if (turned) {
+        const float2* row = reinterpret_cast<const float2*>(a.cs) + (size_t)r * h;
+        if (kInter) {
+          const float4* row4 = reinterpret_cast<const float4*>(row + (e0 >> 1));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = __fadd_rn(1.f, w[i]);
+          for (int i = 0; i < 2; ++i) {
+            const float4 t = __ldg(row4 + i);
+            c[2 * i] = make_float2(t.x, t.x);
+            s[2 * i] = make_float2(-t.y, t.y);
+            c[2 * i + 1] = make_float2(t.z, t.z);
+            s[2 * i + 1] = make_float2(-t.w, t.w);
+          }
+        } else {
+          const bool first = e0 < h;
+          partner = first ? lane + h / 8 : lane - h / 8;
+          const float4* row4 = reinterpret_cast<const float4*>(row + (first ? e0 : e0 - h));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 t = __ldg(row4 + i);
+            c[i] = make_float2(t.x, t.z);
+            s[i] = first ? make_float2(-t.y, -t.w) : make_float2(t.y, t.w);
           }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(__fmul_rn(x[i], rms[step]), w[i]);
       }
-      if (rot) {
+      const __nv_bfloat16* weight = kind == 0 ? a.q_weight : a.k_weight;
+      if (weight && kind != w_kind) {
+        w_kind = kind;
+        unpack8(__ldg(reinterpret_cast<const uint4*>(weight + e0)), w);
+        if (p.nr.plus_one) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = add2(make_float2(1.f, 1.f), w[i]);
+        }
+      }
+
+      // Sums of squares, neighbours first: eight in the lane, then lanes 1, 2, 4, ...
+      // apart.  Four steps' sums are folded into one another on the way (a lane passes on
+      // the sums it does not keep), so that lane i ends with that of step i mod 4, and one
+      // square root and division serve all four.
+      float rms[STEPS];
+      if (weight) {
+        float ss[STEPS];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          ss[i] = 0.f;
+          if (STEPS > 1 && i * VPW >= left) continue;
+          float2 x[4];
+          unpack8(raws[i], x);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = mul2(x[k], x[k]);
+          const float2 u = add2(make_float2(x[0].x, x[1].x), make_float2(x[0].y, x[1].y));
+          const float2 v = add2(make_float2(x[2].x, x[3].x), make_float2(x[2].y, x[3].y));
+          const float2 t = add2(make_float2(u.x, v.x), make_float2(u.y, v.y));
+          ss[i] = __fadd_rn(t.x, t.y);
+        }
+        float sum = ss[0];
+        if constexpr (STEPS == 4) {
+          const bool odd = lane & 1, upper = lane & 2;
+          const float k01 = odd ? ss[1] : ss[0], g01 = odd ? ss[0] : ss[1];
+          const float k23 = odd ? ss[3] : ss[2], g23 = odd ? ss[2] : ss[3];
+          const float s01 = __fadd_rn(k01, __shfl_xor_sync(0xffffffffu, g01, 1));
+          const float s23 = __fadd_rn(k23, __shfl_xor_sync(0xffffffffu, g23, 1));
+          sum = __fadd_rn(upper ? s23 : s01, __shfl_xor_sync(0xffffffffu, upper ? s01 : s23, 2));
+        }
+#pragma unroll
+        for (int k = STEPS == 4 ? 4 : 1; k < LPV; k <<= 1)
+          sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, k));
+        const float inv = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(sum * (1.f / D), p.nr.eps)));
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+          rms[i] = STEPS == 4 ? __shfl_sync(0xffffffffu, inv, (lane & ~(LPV - 1)) + i) : inv;
+      }
+
+      __nv_bfloat16* out = kind == 0 ? a.q_out : a.k_out;
+      if (!kAppend || kind == 0) out += ((size_t)r * heads + head0) * D + e0;
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        if (STEPS > 1 && i * VPW >= left) break;
+        float2 y[4];
+        unpack8(raws[i], y);
+        if (weight) {
+          const float2 m = make_float2(rms[i], rms[i]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = mul2(mul2(y[k], m), w[k]);
+        }
         if (kInter) {
           if (turned) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float u = y[2 * i], t = y[2 * i + 1];
-              y[2 * i] = __fadd_rn(__fmul_rn(u, c[2 * i]), __fmul_rn(t, s[2 * i]));
-              y[2 * i + 1] = __fadd_rn(__fmul_rn(t, c[2 * i + 1]), __fmul_rn(u, s[2 * i + 1]));
-            }
+            for (int k = 0; k < 4; ++k)
+              y[k] = turn2(y[k], c[k], make_float2(y[k].y, y[k].x), s[k]);
           }
-        } else {
+        } else if (rot) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float t = __shfl_sync(0xffffffffu, y[i], partner);
-            if (turned) y[i] = __fadd_rn(__fmul_rn(y[i], c[i]), __fmul_rn(t, s[i]));
+          for (int k = 0; k < 4; ++k) {
+            const float2 t = make_float2(__shfl_sync(0xffffffffu, y[k].x, partner),
+                                         __shfl_sync(0xffffffffu, y[k].y, partner));
+            if (turned) y[k] = turn2(y[k], c[k], t, s[k]);
           }
         }
-      }
-      if (kind < 2) {
-        raw = pack8(y);
-        if (kAppend) unpack8(raw, x);
-        if (real && kind == 0)
-          *reinterpret_cast<uint4*>(a.q_out + ((size_t)r * g.Hq + head) * D + e0) = raw;
-        if (!kAppend && real && kind == 1)
-          *reinterpret_cast<uint4*>(a.k_out + ((size_t)r * g.Hkv + head) * D + e0) = raw;
+        raws[i] = pack8(y);
+        if ((!kAppend || kind == 0) && head0 + i * VPW < heads)
+          *reinterpret_cast<uint4*>(out + i * VPW * D) = raws[i];
       }
     }
-    if (!kAppend || min(v0 + (step + 1) * VPW, v1) <= hq) continue;   // (queries alone)
+    if (!kAppend || kind == 0) continue;
 
     // keys and values: blocks of 16 (two lanes) to e2m1 codes and an e4m3 scale,
     // as the token store quantises them
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    if (!real || kind == 0 || !has_slot) continue;
-    const float scale = kind == 2 ? a.v_scale : a.k_scale;
-    const uint32_t sf = f32_to_e4m3(__fdiv_rn(__fdiv_rn(m, 6.0f), scale));
-    const float den = __fmul_rn(e4m3_to_f32(sf), scale);
-    uint32_t codes = 0;
-    if (den != 0.f) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        codes |= canon_zero(f32x2_to_e2m1x2(__fdiv_rn(x[2 * i], den),
-                                            __fdiv_rn(x[2 * i + 1], den))) << (8 * i);
-    }
-    const size_t row = (page_row * g.Hkv + head) * g.P + slot;
-    if (!QSA_IN_BOUNDS(row < (size_t)g.NP * g.Hkv * g.P, kChkRow)) continue;
+    const float scale = kind == 2 ? a.v_scale : a.k_scale, inv6 = kind == 2 ? p.v_inv6 : p.k_inv6;
     uint8_t* pool = kind == 2 ? a.v_pool : a.k_pool;
     uint8_t* sfp = kind == 2 ? a.v_sf : a.k_sf;
-    *reinterpret_cast<uint32_t*>(pool + row * (D / 2) + 4 * l) = codes;
-    if (!(l & 1)) sfp[row * (D / 16) + (l >> 1)] = (uint8_t)sf;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      if (STEPS > 1 && i * VPW >= left) break;
+      float2 x[4];
+      unpack8(raws[i], x);
+      float m = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      if (head0 + i * VPW < heads && has_slot) {
+        uint32_t sf;
+        const uint32_t codes = quantise8(x, m, scale, inv6, sf);
+        const size_t row = (page_row * g.Hkv + (head0 + i * VPW)) * g.P + slot;
+        if (QSA_IN_BOUNDS(row < (size_t)g.NP * g.Hkv * g.P, kChkRow)) {
+          *reinterpret_cast<uint32_t*>(pool + row * (D / 2) + 4 * l) = codes;
+          if (!(l & 1)) sfp[row * (D / 16) + (l >> 1)] = (uint8_t)sf;
+        }
+      }
+      __syncwarp();
+    }
   }
 }
 
@@ -335,13 +409,13 @@ load_tokens_kernel(Geom g, const int32_t* __restrict__ page_table,
       *reinterpret_cast<const uint32_t*>((is_v ? v_pool : k_pool) + row * (D / 2) + 4 * l);
   const float sf = e4m3_to_f32((is_v ? v_sf : k_sf)[row * (D / 16) + (l >> 1)]);
   const float scale = is_v ? v_scale : k_scale;
-  float x[8];
+  float2 x[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t h2 = e2m1x2_to_f16x2((w >> (8 * i)) & 0xFFu);
     // code * block scale is exact in fp32; the tensor scale rounds once
-    x[2 * i] = __fmul_rn(__half2float(__ushort_as_half((unsigned short)(h2 & 0xFFFFu))) * sf, scale);
-    x[2 * i + 1] = __fmul_rn(__half2float(__ushort_as_half((unsigned short)(h2 >> 16))) * sf, scale);
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    x[i] = make_float2(__fmul_rn(v.x * sf, scale), __fmul_rn(v.y * sf, scale));
   }
   *reinterpret_cast<uint4*>((is_v ? v_out : k_out) + ((size_t)r * g.Hkv + head) * D + 8 * l) = pack8(x);
 }
@@ -380,18 +454,28 @@ cudaError_t launch_prologue(const Geom& g, const NormRope& nr, const PrologueArg
   p.g = g;
   p.nr = nr;
   p.a = a;
-  p.total = (a.q ? g.Hq : 0) + (append ? 2 : 1) * g.Hkv;
+  auto inverse = [](float scale) {
+    const float inv = 1.f / (6.f * scale);
+    return inv > 0x1p-100f && inv < 0x1p100f ? inv : 0.f;
+  };
+  p.k_inv6 = append ? inverse(a.k_scale) : 0.f;
+  p.v_inv6 = append ? inverse(a.v_scale) : 0.f;
   const int vpw = g.D == 128 ? 2 : 1;
   const long long T = (long long)g.B * g.R;
-  // Few rows: a warp per step of heads, for the shortest chain; many rows: four
-  // steps per warp share the row's cos and sin.
-  const int steps = T * p.total / vpw > 152 * 64 ? 4 : 1;
-  p.groups = (p.total + vpw * steps - 1) / (vpw * steps);
-  const long long items = T * p.groups;
+  const int total = (a.q ? g.Hq : 0) + (append ? 2 : 1) * g.Hkv;   // heads per row
+  // Few rows: a turn of one step, for the shortest chain; many rows: four steps
+  // share the row's cos and sin and one square root.
+  const int steps = T * total / vpw > 152 * 64 ? 4 : 1, per = vpw * steps;
+  p.turns_q = a.q ? (g.Hq + per - 1) / per : 0;
+  p.turns_k = (g.Hkv + per - 1) / per;
+  p.turns = p.turns_q + (append ? 2 : 1) * p.turns_k;
+  const long long items = T * p.turns;
   auto launch_it = [&]<int D, bool kAppend, bool kInter>() {
     auto* kern = steps == 4 ? prologue_kernel<D, kAppend, kInter, 4> : prologue_kernel<D, kAppend, kInter, 1>;
-    return launch(kern, dim3((unsigned)((items + kWarps - 1) / kWarps)), dim3(kWarps * 32), pdl,
-                  stream, p);
+    // many rows: five CTAs' warps per SM stay and take turns
+    const long long ctas = (items + kWarps - 1) / kWarps, most = 5 * 152;
+    return launch(kern, dim3((unsigned)(steps == 4 && ctas > most ? most : ctas)), dim3(kWarps * 32),
+                  pdl, stream, p);
   };
   auto of_dim = [&]<int D>() {
     if (append)
