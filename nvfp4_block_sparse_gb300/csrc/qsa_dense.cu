@@ -630,20 +630,19 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
 }
 
 // ---------------------------------------------------------------------------
-// Divided units joined.  CTA (i, y) takes vectors of the unit of descriptor i:
-// with few records a warp per vector, with many (one long request over the whole
-// GPU) all warps on one vector's records.
+// The tile kernel's divided units joined: CTA (i, y, z) takes 32 vectors of the unit of
+// descriptor i, a lane each (a record holds four dims of neighbouring vectors behind one
+// another), its warps eight dims each.  The parts are added in their order, four at a
+// time on their way: with few units the latency of the records is all there is.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 dense_join_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work p) {
-  constexpr int E = D / 32;
-  __shared__ float s_o[kJoinWarps][D];
-  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+  constexpr int N = 2;                      // groups of four dims per thread
   const Geom& g = sh.g;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = blockIdx.z * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
   const Desc d = p.desc[blockIdx.x];
@@ -653,90 +652,49 @@ dense_join_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
                      d.first >= 0 && d.first < d.last && d.last < sh.ctas, kChkJoin))
     return;
   const int vec0 = d.tile * sh.vt, vecs = min(sh.vt, g.R * sh.G - vec0);
+  const int c = blockIdx.y * 32 + lane;
+  if (blockIdx.y * 32 >= vecs) return;
   const int parts = d.last - d.first + 1;
   const size_t rf = record_floats(sh.vt, D);
   auto record = [&](int i) {   // part i: slot 1 of the first CTA, slot 0 of the others
     return p.records + ((size_t)(d.first + i) * 2 + (i == 0 ? 1 : 0)) * rf;
   };
-  const bool many = parts > 24;
-  const int ways = many ? 1 : kJoinWarps;   // vectors at a time
-  for (int c0 = blockIdx.y * ways; c0 < vecs; c0 += gridDim.y * ways) {
-    const int c = many ? c0 : c0 + warp;
-    const int i0 = many ? warp : 0, step = many ? kJoinWarps : 1;
-    float m = kNoBase, l = 0.f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    if (c < vecs) {
-      for (int i = i0 + step * lane; i < parts; i += 32 * step) m = fmaxf(m, record(i)[c]);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (c >= vecs) return;
+  float m = kNoBase, l = 0.f;
 #pragma unroll 4
-      for (int i = i0; i < parts; i += step) {
-        const float* rec = record(i);
-        const float f = exp2_approx(rec[c] - m);
-        l = fmaf(rec[sh.vt + c], f, l);
-        const float4* src = reinterpret_cast<const float4*>(rec + 2 * sh.vt + (size_t)c * D) + lane * (E / 4);
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, record(i)[c]);
+  float4 acc[N];
 #pragma unroll
-        for (int e = 0; e < E / 4; ++e) {
-          const float4 x = src[e];
-          acc[4 * e] = fmaf(x.x, f, acc[4 * e]);
-          acc[4 * e + 1] = fmaf(x.y, f, acc[4 * e + 1]);
-          acc[4 * e + 2] = fmaf(x.z, f, acc[4 * e + 2]);
-          acc[4 * e + 3] = fmaf(x.w, f, acc[4 * e + 3]);
-        }
-      }
+  for (int k = 0; k < N; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float* rec = record(i);
+    const float f = exp2_approx(rec[c] - m);
+    l = fmaf(rec[sh.vt + c], f, l);
+    const float4* src = reinterpret_cast<const float4*>(rec + 2 * sh.vt) + (size_t)(warp * N) * sh.vt + c;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float4 x = src[(size_t)k * sh.vt];
+      acc[k].x = fmaf(x.x, f, acc[k].x);
+      acc[k].y = fmaf(x.y, f, acc[k].y);
+      acc[k].z = fmaf(x.z, f, acc[k].z);
+      acc[k].w = fmaf(x.w, f, acc[k].w);
     }
-    if (many) {   // the warps' parts, in the warps' order
-#pragma unroll
-      for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
-      if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-      }
-      __syncthreads();
-      if (warp == 0) {
-        float mm = kNoBase;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) mm = fmaxf(mm, s_m[w]);
-        l = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-          const float f = exp2_approx(s_m[w] - mm);
-          l = fmaf(s_l[w], f, l);
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(s_o[w][lane * E + e], f, acc[e]);
-        }
-        m = mm;
-      }
-      __syncthreads();
-      if (warp != 0) continue;
-    }
-    if (c >= vecs) continue;
-    const int j = (vec0 + c) / sh.G, head = d.kvh * sh.G + (vec0 + c) % sh.G;
-    const size_t row = ((size_t)d.b * g.R + j) * g.Hq + head;
-    if (p.sinks) {
-      const float s2 = p.sinks[head] * kLog2e, nm = fmaxf(m, s2);
-      const float f = exp2_approx(m - nm);
-      l = l * f + exp2_approx(s2 - nm);
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= f;
-      m = nm;
-    }
-    const float r = l > 0.f ? p.v_scale / l : 0.f;
-    uint32_t w2[E / 2];
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[2 * e] * r, acc[2 * e + 1] * r);
-      w2[e] = *reinterpret_cast<const uint32_t*>(&x);
-    }
-    if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(p.out + row * D + lane * E) = make_uint2(w2[0], w2[1]);
-    else
-      *reinterpret_cast<uint4*>(p.out + row * D + lane * E) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-    if (lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
+  const int j = (int)((uint32_t)(vec0 + c) / (uint32_t)sh.G), head = d.kvh * sh.G + (vec0 + c) - j * sh.G;
+  const size_t row = ((size_t)d.b * g.R + j) * g.Hq + head;
+  float f = 1.f;
+  if (p.sinks) add_sink(p.sinks[head], m, l, f);
+  const float r = l > 0.f ? f * p.v_scale / l : 0.f;
+  __nv_bfloat16* out = p.out + row * D + 4 * warp * N;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[k].x * r, acc[k].y * r);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[k].z * r, acc[k].w * r);
+    *reinterpret_cast<uint2*>(out + 4 * k) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+  if (warp == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace
@@ -770,7 +728,7 @@ size_t dense_carve(const dense::Shape& s, void* workspace, dense::Work* w) {
 
 cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(dense::desc_count(s), s.vt <= 16 ? 8 : s.vt / dense::kJoinWarps);
+  cfg.gridDim = dim3(dense::desc_count(s), s.vt / 32, s.g.D / (8 * dense::kJoinWarps));
   cfg.blockDim = dim3(dense::kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

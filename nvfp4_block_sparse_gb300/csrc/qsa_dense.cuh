@@ -68,7 +68,8 @@ struct Work {
   int* status;
   Desc* desc;        // [units or CTAs]
   int* tickets;      // [CTAs]
-  float* records;    // [CTAs][2][vt][2 + D]: bases, sums, outputs
+  float* records;    // [CTAs][2][vt * (2 + D)]: bases, sums, outputs ([vt][D], or of the tile
+                     // kernel [D/4][vt][4])
 };
 
 __host__ __device__ __forceinline__ size_t record_floats(int vt, int D) {

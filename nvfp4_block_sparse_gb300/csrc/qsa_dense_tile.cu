@@ -705,31 +705,45 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         m = nm;
       }
       const float r = whole ? (l > 0.f ? f * p.v_scale / l : 0.f) : 1.f;
-      // O leaves 64 columns at a time by way of shared memory of the warp's own (its Q rows,
-      // whose last reader is done), so that rows are written in runs of 128 bytes and more.
       float* rec = p.records + ((size_t)worker * 2 + (seg.begins ? 1 : 0)) * record_floats(sh.vt, D);
-      // 32 rows of 64 floats, in the warp's 8 KB or in the 4 KB that its rows have of the first
-      // two blocks (no other warp's: it may be writing its next Q)
-      auto box = [&](int rr) {
-        return T::kQTmem ? q_tile + (warp & 3) * 8192 + rr * 256
-                         : q_tile + (rr >> 4) * 16384 + (warp & 3) * 4096 + (rr & 15) * 256;
-      };
       const int at0 = (t * CG + rank) * 128 + 32 * (warp & 3);    // the warp's first vector
       const int left = min(32, seg.vecs - at0);                   // and how many it has
-      const int sub = lane >> 4, pc = lane & 15;
+      if (!whole) {
+        // a record: four dims of neighbouring vectors behind one another, as the lanes have them
+        float4* to = reinterpret_cast<float4*>(rec + 2 * sh.vt) + at;
 #pragma unroll 1
-      for (int d0 = 0; d0 < D && left > 0; d0 += 64) {
-        float o64[64];
-        tmem_ld32(tO + d0, o64);
-        tmem_ld32(tO + d0 + 32, o64 + 32);
-        tmem_wait_ld();
+        for (int d0 = 0; d0 < D && left > 0; d0 += 32) {
+          float o32[32];
+          tmem_ld32(tO + d0, o32);
+          tmem_wait_ld();
+          if (real)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)       // 16-byte pieces, swizzled by the row
-          *reinterpret_cast<float4*>(box(lane) + ((i ^ (lane & 15)) << 4)) =
-              make_float4(o64[4 * i] * r, o64[4 * i + 1] * r, o64[4 * i + 2] * r, o64[4 * i + 3] * r);
-        __syncwarp();
-        if (whole) {
-#pragma unroll 4
+            for (int i = 0; i < 8; ++i)
+              to[(size_t)(d0 / 4 + i) * sh.vt] =
+                  make_float4(o32[4 * i], o32[4 * i + 1], o32[4 * i + 2], o32[4 * i + 3]);
+        }
+      } else {
+        // O leaves 64 columns at a time by way of shared memory of the warp's own (its Q rows,
+        // whose last reader is done), so that rows are written in runs of 128 bytes.
+        // 32 rows of 64 floats, in the warp's 8 KB or in the 4 KB that its rows have of the first
+        // two blocks (no other warp's: it may be writing its next Q)
+        auto box = [&](int rr) {
+          return T::kQTmem ? q_tile + (warp & 3) * 8192 + rr * 256
+                           : q_tile + (rr >> 4) * 16384 + (warp & 3) * 4096 + (rr & 15) * 256;
+        };
+        const int sub = lane >> 4, pc = lane & 15;
+#pragma unroll 1
+        for (int d0 = 0; d0 < D && left > 0; d0 += 64) {
+          float o64[64];
+          tmem_ld32(tO + d0, o64);
+          tmem_ld32(tO + d0 + 32, o64 + 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)       // 16-byte pieces, swizzled by the row
+            *reinterpret_cast<float4*>(box(lane) + ((i ^ (lane & 15)) << 4)) =
+                make_float4(o64[4 * i] * r, o64[4 * i + 1] * r, o64[4 * i + 2] * r, o64[4 * i + 3] * r);
+          __syncwarp();
+#pragma unroll 8
           for (int i = 0; i < 16; ++i) {   // two rows at a time, a piece per lane
             const int rr = 2 * i + sub;
             const float4 x = *reinterpret_cast<const float4*>(box(rr) + ((pc ^ (rr & 15)) << 4));
@@ -739,16 +753,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
               *reinterpret_cast<uint2*>(p.out + (size_t)to * D + d0 + 4 * pc) =
                   make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
           }
-        } else {
-          float* to = rec + 2 * sh.vt + (size_t)(at0 + sub) * D + d0 + 4 * pc;
-#pragma unroll 4
-          for (int i = 0; i < 16; ++i) {
-            const int rr = 2 * i + sub;
-            const float4 x = *reinterpret_cast<const float4*>(box(rr) + ((pc ^ (rr & 15)) << 4));
-            if (rr < left) *reinterpret_cast<float4*>(to + 2 * i * D) = x;
-          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       if (real) {
         if (whole) {
@@ -947,7 +953,7 @@ dense::Shape dense_tile_shape(const Geom& g, int window) {
   s.tiles = (g.R * s.G + s.vt - 1) / s.vt;
   s.window = window;
   s.least = 4;
-  s.lead = 6;
+  s.lead = 10;
   s.by_unit = dense::unit_count(s) <= s.ctas;
   return s;
 }
