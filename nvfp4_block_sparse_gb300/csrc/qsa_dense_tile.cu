@@ -487,6 +487,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + T::kOCol + t * D + lane_off;
     uint8_t* q_tile = sQ + t * T::kQBytes;
+    const int psh = 31 - __clz(g.P);                   // log2 of the page size
+    const uint32_t all_live = (1u << (kTok >> psh)) - 1u;   // (a chunk is one to four pages)
     int chunks = 0, s_waits = 0, parts = 0;   // chunks, waits on barS (two tiles), parts so far
     Cursor cursor(span);
     Seg seg;
@@ -600,30 +602,32 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       tc_fence_before();
       warp_arrive<CG>(qready);
 
-      // pages of a chunk that are there: one bit per 32 tokens
-      auto live_of = [&](int chunk) {
-        const int tok = chunk * kTok + 32 * lane, beta = tok / g.P;
-        bool ok = false;
-        if (lane < kTok / 32 && beta < g.MB) {
-          const int page = __ldg(p.page_table + (size_t)seg.b * g.MB + beta);
-          ok = page >= 0 && page < g.NP;
-        }
-        return __ballot_sync(0xffffffffu, ok);
+      // Which pages are there: a bit per block, of 32 blocks from blk0 and of the 32 behind
+      // them.  (Looked up chunk by chunk the load's latency would be on every chunk's path.)
+      int blk0 = (seg.chunk0 * kTok) >> psh;
+      auto there_of = [&](int beta) {
+        int page = -1;
+        if (beta < g.MB) page = __ldg(p.page_table + (size_t)seg.b * g.MB + beta);
+        return __ballot_sync(0xffffffffu, page >= 0 && page < g.NP);
       };
+      uint32_t there0 = there_of(blk0 + lane), there1 = there_of(blk0 + 32 + lane);
       float base = kNoBase;
       float2 sum = make_float2(0.f, 0.f);
-      uint32_t live = live_of(seg.chunk0);
       for (int c = 0; c < seg.todo; ++c, ++chunks) {
         const int y = kTiles == 2 ? t : chunks & 1;      // S buffer
         const uint32_t tS = tmem + y * kTok + lane_off;
-        const uint32_t now_live = live;
-        if (c + 1 < seg.todo) live = live_of(seg.chunk0 + c + 1);
+        const int tok0 = (seg.chunk0 + c) * kTok;
+        if ((tok0 >> psh) - blk0 >= 32) {
+          blk0 += 32;
+          there0 = there1;
+          there1 = there_of(blk0 + 32 + lane);
+        }
+        const uint32_t live = __funnelshift_r(there0, there1, (tok0 >> psh) - blk0);   // the chunk's blocks
         if (gave_up(&barS[y], kTiles == 2 ? s_waits : chunks >> 1)) { dead = true; break; }
         ++s_waits;
         tc_fence_after();
-        const int tok0 = (seg.chunk0 + c) * kTok;
         const bool edge = tok0 + kTok > seg.n_least || tok0 < seg.lo_most ||
-                          now_live != (1u << (kTok / 32)) - 1u;
+                          (live & all_live) != all_live;
         // The row's logits, those it does not see at -inf.
         float z[kTok];
 #pragma unroll
@@ -633,7 +637,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
 #pragma unroll
           for (int i = 0; i < kTok; ++i) {
             const int tok = tok0 + i;
-            if (tok >= n || tok < lo || !((now_live >> (i >> 5)) & 1u)) z[i] = -INFINITY;
+            if (tok >= n || tok < lo || !((live >> ((i & ~31) >> psh)) & 1u)) z[i] = -INFINITY;
           }
         }
         float m8[8];
