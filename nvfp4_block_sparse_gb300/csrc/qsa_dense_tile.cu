@@ -205,38 +205,55 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   }
 }
 
-// ---- MMAs by one elected lane of a converged warp ------------------------------
+// ---- MMAs by one lane of a converged warp ---------------------------------------
+// The lane is elected once (`one` is 1 in it): the warp stays converged, so that the
+// descriptors stay in uniform registers, and an MMA costs no election of its own.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r;
+}
 template <int CG>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   if constexpr (CG == 1)
-    mma_f16_elect(d, a, b, idesc, accumulate);
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one));
   else
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one));
 }
 template <int CG>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   if constexpr (CG == 1)
-    mma_f16_ts_elect(d, a, b, idesc, accumulate);
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one));
   else
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one));
 }
 template <int CG>
-__device__ __forceinline__ void commit(uint64_t* bar) {
+__device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
   if constexpr (CG == 1)
-    mma_commit_elect(bar);
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)), "r"(one)
+        : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
         "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
-        ".b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+        ".b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "h"((uint16_t)3), "r"(one)
         : "memory");
 }
 
@@ -797,6 +814,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     }
   } else if (regs_down<T::kMmaRegs>(), warp == T::kMma && rank == 0) {
     // ==== MMA issue ==================================================================
+    const uint32_t one = elect_one();
     const uint32_t id_s = f16_idesc(128 * CG, kTok), id_o = f16_idesc(128 * CG, D) | kIdescBMn;
     Cursor cursor(span);
     Seg seg;
@@ -809,17 +827,17 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           if constexpr (T::kQTmem)     // 16 dims (one step): 8 columns
-            mma_ts<CG>(tmem + y * kTok, tmem + T::kQCol + 8 * (4 * h + ks),
+            mma_ts<CG>(one, tmem + y * kTok, tmem + T::kQCol + 8 * (4 * h + ks),
                        dk + (uint64_t)((h * T::kKBlk + 32 * ks) >> 4), id_s, (h | ks) ? 1u : 0u);
           else
-            mma_ss<CG>(tmem + y * kTok, dq + (uint64_t)((h * 16384 + 32 * ks) >> 4),
+            mma_ss<CG>(one, tmem + y * kTok, dq + (uint64_t)((h * 16384 + 32 * ks) >> 4),
                        dk + (uint64_t)((h * T::kKBlk + 32 * ks) >> 4), id_s, (h | ks) ? 1u : 0u);
     };
     auto issue_o = [&](int t, int y, int x, int h, bool first) {   // 64 tokens
       const uint64_t dv = sw128_mn_desc(smem_u32(sV + x * T::kVBytes), T::kVBlk);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        mma_ts<CG>(tmem + T::kOCol + t * D, tmem + y * kTok + 64 * h + 8 * ks,
+        mma_ts<CG>(one, tmem + T::kOCol + t * D, tmem + y * kTok + 64 * h + 8 * ks,
                    dv + (uint64_t)((8192 * h + 2048 * ks) >> 4), id_o,
                    (first && ks == 0) ? 0u : 1u);
     };
@@ -837,10 +855,10 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       if constexpr (kTiles == 2) {
         if (!chunk_s(0)) { dead = true; break; }
         issue_s(0, 0, s_done & 1);
-        commit<CG>(&barS[0]);
+        commit<CG>(one, &barS[0]);
         issue_s(1, 1, s_done & 1);
-        commit<CG>(&barS[1]);
-        commit<CG>(&kfree[s_done & 1]);
+        commit<CG>(one, &barS[1]);
+        commit<CG>(one, &kfree[s_done & 1]);
         // The tiles of a chunk are waited for while the products before it run.
         if (gave_up(&vready[s_done & 1], s_done >> 1) || (C > 1 && !chunk_s(1))) { dead = true; break; }
         for (int c = 0; c < C && !dead; ++c) {
@@ -855,12 +873,12 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
             tc_fence_after();
             issue_o(t, t, x, 1, false);
             if (more) issue_s(t, t, xn);
-            commit<CG>(&barS[t]);
+            commit<CG>(one, &barS[t]);
           }
           if (dead) break;
-          commit<CG>(&vfree[x]);
+          commit<CG>(one, &vfree[x]);
           if (more) {
-            commit<CG>(&kfree[xn]);
+            commit<CG>(one, &kfree[xn]);
             if (gave_up(&vready[xn], (n + 1) >> 1) || (c + 2 < C && !chunk_s(c + 2))) {
               dead = true;
               break;
@@ -872,8 +890,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           const int n = s_done + c;
           if (!chunk_s(c)) { dead = true; break; }
           issue_s(0, n & 1, n & 1);
-          commit<CG>(&barS[n & 1]);
-          commit<CG>(&kfree[n & 1]);
+          commit<CG>(one, &barS[n & 1]);
+          commit<CG>(one, &kfree[n & 1]);
         }
         for (int c = 0; c < C && !dead; ++c) {
           const int n = s_done + c, x = n & 1;
@@ -885,14 +903,14 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
             issue_o(0, x, x, h, c == 0 && h == 0);
           }
           if (dead) break;
-          commit<CG>(&vfree[x]);
-          commit<CG>(barO);
-          if (c + 1 == C) commit<CG>(partO);
+          commit<CG>(one, &vfree[x]);
+          commit<CG>(one, barO);
+          if (c + 1 == C) commit<CG>(one, partO);
           if (c + 2 < C) {
             if (!chunk_s(c + 2)) { dead = true; break; }
             issue_s(0, x, x);
-            commit<CG>(&barS[x]);
-            commit<CG>(&kfree[x]);
+            commit<CG>(one, &barS[x]);
+            commit<CG>(one, &kfree[x]);
           }
         }
       }
@@ -918,7 +936,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   }
   tc_fence_after();
   if (any_dead) {
-    if (warp == T::kMma && rank == 0) commit<CG>(mdone);
+    if (warp == T::kMma && rank == 0) commit<CG>(elect_one(), mdone);
     gave_up(mdone, 0);
     __syncthreads();
   }
