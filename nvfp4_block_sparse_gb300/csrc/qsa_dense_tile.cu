@@ -28,8 +28,8 @@
 //             fp16 over the columns of S it has read, 64 tokens at a time, sums in fp32;
 //             at the end of a part O from tensor memory to the output or to a record.  A
 //             group per tile
-//   dequant   codes and scales from the pages by asynchronous copies some chunks ahead, e2m1 x
-//             e4m3 exact in fp16 into double-buffered K and V tiles (128-byte swizzle)
+//   copy      one warp: codes and scales of the pages by bulk copies some chunks ahead
+//   dequant   e2m1 x e4m3 exact in fp16 into double-buffered K and V tiles (128-byte swizzle)
 //   MMA       one warp (of the pair's first CTA) issues every MMA in order.  With two tiles
 //             they take turns: O_0, S_0 of the next chunk, O_1, S_1, so that one tile's
 //             softmax runs under the other's products; with one, S has two buffers
@@ -45,6 +45,8 @@
 // Arrivals are one per warp; those for the MMA warp go to the first CTA's barrier,
 // commits to both CTAs':
 //   qready        Q tiles written; O, S of the part before read    (softmax warps)
+//   full[i]       stage i of codes and scales there                (bulk copies)
+//   empty[i]      stage i read                                     (the converting warps)
 //   kready/vready[x]  K / V tile x written                         (its four converting warps)
 //   kfree/vfree[x]    MMAs that read tile x complete               (commit)
 //   barS[y]       S buffer y complete -- and, with two tiles, every MMA before it,
@@ -102,12 +104,15 @@ struct TT {
   // Q tiles (D/64 blocks of 128 rows x 128 B), or, with Q in tensor memory, 8 KB per warp
   // through which Q and O pass.
   static constexpr int kQBytes = kQTmem ? 32768 : 128 * D * 2;
-  // Codes and scales on their way: chunks per converting warp.
-  static constexpr int kDepth = kTiles == 2 ? 4 : 3;
-  static constexpr int kRing = kDepth * (kKRows * D + kTok * kVDims) * 9 / 16;
-  static constexpr int kBars = 18;
+  // Codes and scales on their way: a stage is a chunk, this CTA's K rows and whole V rows.
+  static constexpr int kDepth = CG == 2 ? 4 : 3;
+  static constexpr int kKCodes = kKRows * D / 2, kVCodes = kTok * D / 2;
+  static constexpr int kKPart = kKCodes + kKCodes / 8, kVPart = kVCodes + kVCodes / 8;
+  static constexpr int kStage = kKPart + kVPart;
+  static constexpr int kRing = kDepth * kStage;
+  static constexpr int kBars = 18 + 2 * kDepth;
   static constexpr int kSmem = 1024 + kTiles * kQBytes + 2 * kKBytes + 2 * kVBytes + kRing +
-                               kBars * 8 + 24 + kTiles * 128 * 4;
+                               kBars * 8 + 16 + kDepth * 4 + kTiles * 128 * 4;
 };
 
 // 32 columns of this thread's lane.
@@ -129,24 +134,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 // How far (log2) a logit may exceed the base: fp16 weights reach 65504, and as long as
 // every weight is finite its relative precision does not depend on the base.
 constexpr float kHeadroom = 15.f;
-
-// Asynchronous copies of N bytes, zeros where `on` is false.
-template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool on) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
-                 "r"(on ? N : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // Two fp32 multiply-adds / additions at once.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -261,48 +248,111 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// ---- copies ----------------------------------------------------------------------
+// The copy warp brings every chunk's codes and scales into the ring, kDepth chunks ahead:
+// a piece of a page (as many rows as the chunk has of it) is contiguous, so that a chunk is
+// at most eight bulk copies, one per lane.  Pages that are not there, and pieces that no row
+// of the unit sees, are not copied; `copied` says so (bit per lane of the stage's copies).
+template <class T>
+__device__ __forceinline__ bool copy_all(const Shape& sh, const Work& p, const Span& span, int rank,
+                                         uint8_t* ring, uint64_t* full, uint64_t* empty,
+                                         volatile uint32_t* copied) {
+  const int lane = threadIdx.x & 31;
+  const int psh = 31 - __clz(sh.g.P);
+  const bool scales = lane & 1, v = lane & 2;
+  const int rows = v ? T::kTok : T::kKRows;
+  const int step = min(sh.g.P, rows);                 // rows of a copy
+  const int off = (lane >> 2) * step;                 // its first, in the stage's part
+  const bool mine = lane < 8 && off < rows;
+  const int tok_off = off + (v ? 0 : rank * T::kKRows);
+  const uint32_t row_bytes = scales ? T::D / 16 : T::D / 2, bytes = step * row_bytes;
+  const uint8_t* pool = v ? (scales ? p.v_sf : p.v_pool) : (scales ? p.k_sf : p.k_pool);
+  uint8_t* dst = ring + (v ? T::kKPart + (scales ? T::kVCodes : 0) : (scales ? T::kKCodes : 0)) +
+                 off * row_bytes;
+  const uint64_t policy = policy_evict_normal();   // (other units read the page too)
+  int slot = 0, use = 0;
+  bool ok = true;
+  Cursor cursor(span);
+  Seg seg;
+  while (ok && cursor.next(sh, p.seqlens, seg)) {
+    // page ids: lane i has that of block blk0 + i, and `later` of blk0 + 32 + i
+    auto page_id = [&](int beta) {
+      return beta < sh.g.MB && seg.n_all > seg.lo_all
+                 ? __ldg(p.page_table + (size_t)seg.b * sh.g.MB + beta) : -1;
+    };
+    int blk0 = (seg.chunk0 * T::kTok) >> psh;
+    int ids = page_id(blk0 + lane), later = page_id(blk0 + 32 + lane);
+#pragma unroll 1
+    for (int c = 0; c < seg.todo; ++c) {
+      const int tok0 = (seg.chunk0 + c) * T::kTok, tok = tok0 + tok_off;
+      if ((tok0 >> psh) - blk0 >= 32) {
+        blk0 += 32;
+        ids = later;
+        later = page_id(blk0 + 32 + lane);
+      }
+      const int at = (tok >> psh) - blk0;             // (a chunk is four pages at most)
+      const int here = __shfl_sync(0xffffffffu, ids, at & 31);
+      const int page_later = __shfl_sync(0xffffffffu, later, at & 31);
+      const int page = at < 32 ? here : page_later;
+      const bool there = mine && page >= 0 && page < sh.g.NP && tok < seg.n_all && tok + step > seg.lo_all;
+      const uint32_t which = __ballot_sync(0xffffffffu, there);
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, there ? bytes : 0u);
+      if (use > 0 && gave_up(&empty[slot], use - 1)) { ok = false; break; }
+      if (lane == 0) {
+        copied[slot] = which;
+        mbar_arrive_expect_tx(&full[slot], sum);
+      }
+      __syncwarp();
+      if (there)
+        bulk_g2s(dst + slot * T::kStage,
+                 pool + ((((size_t)page * sh.g.Hkv + seg.kvh) << psh) + (tok & (sh.g.P - 1))) * row_bytes,
+                 bytes, &full[slot], policy);
+      if (++slot == T::kDepth) {
+        slot = 0;
+        ++use;
+      }
+    }
+  }
+  // Nothing may still be on its way when the block ends, whoever gave up: the last use
+  // of each stage.
+  for (int x = 0; x < T::kDepth; ++x) {
+    const int uses = use + (x < slot ? 1 : 0);
+    if (uses > 0 && gave_up(&full[x], uses - 1)) ok = false;
+  }
+  return ok;
+}
+
 // ---- dequantisation --------------------------------------------------------------
 // A converter turns this CTA's part of every chunk's K (kKRows tokens, all dims) or V
 // (all tokens, kVDims dims) into a tile, four warps with a 16-byte piece (32 codes,
-// two scales) per lane and step.  Each warp copies its own pieces into its own ring,
-// kDepth - 1 chunks ahead (no barrier, and registers could not cover DRAM's latency).
-// Neighbouring lanes have neighbouring pieces, four of eight rows or two of sixteen; the
-// eight lanes that store together would meet in two 64-dim blocks' same banks, so the
-// upper two pieces of four go in another order.
+// two scales) per lane and step.  Neighbouring lanes have neighbouring pieces, four of eight
+// rows or two of sixteen; the eight lanes that store together would meet in two 64-dim
+// blocks' same banks, so the upper two pieces of four go in another order.
 //
 // The code is kept small (one copy for K and V where the shapes agree, no
 // unrolling over chunks): with four roles' loops on an SM, instruction-cache misses
 // were its largest stall (windowed verify rows 85 -> 60 us by one copy instead of two).
 template <class T, int kRows, int kDims>
 struct Converter {
-  static constexpr int D = T::D, kTok = T::kTok;
+  static constexpr int D = T::D;
   static constexpr int kPieces = kDims / 32;                  // 16-byte pieces of a row
   static constexpr int kUnits = kRows * kPieces / 128;        // steps of a warp
   static constexpr int kBlk = kRows * 128, kBytes = kRows * kDims * 2;
-  static constexpr int kStage = kUnits * 576;                 // a chunk's pieces and scales
-  static constexpr int kSfRow = kPieces >= 4 ? 8 : 4;         // scale bytes of a step's row
 
-  const uint8_t *pool, *sfs;
   uint8_t* tiles;
   uint64_t *ready, *freed;
-  uint32_t ring;
-  int row0, psh;
-  uint32_t page_rows;
-  // Per step: token row (of the chunk), place of codes and scales in the page, of the
-  // result in the tile.
+  uint32_t part;                 // the stage's part: codes, and behind them scales
+  int row0, lane_sh;
+  // Per step: row of the part, place in it and its scales' place, place in the tile.
   int row[kUnits];
   uint32_t at_c[kUnits], at_s[kUnits], at_t[kUnits];
-  // Page ids: lane i has that of block blk0 + i, and `later` of blk0 + 32 + i.
-  int blk0, ids, later;
 
-  __device__ __forceinline__ Converter(const Shape& sh, const uint8_t* codes_, const uint8_t* scales_,
-                                       int token0, int dim0, int dw, uint8_t* tiles_, uint8_t* ring_,
-                                       uint64_t* ready_, uint64_t* freed_)
-      : pool(codes_ + dim0 / 2), sfs(scales_ + dim0 / 16), tiles(tiles_), ready(ready_), freed(freed_),
-        ring(smem_u32(ring_)), row0(token0) {
+  __device__ __forceinline__ Converter(const Shape& sh, bool v, int token0, int dim0, int dw, uint8_t* ring,
+                                       uint8_t* tiles_, uint64_t* ready_, uint64_t* freed_)
+      : tiles(tiles_), ready(ready_), freed(freed_), part(smem_u32(ring) + (v ? T::kKPart : 0)),
+        row0(token0) {
     const int lane = threadIdx.x & 31;
-    psh = 31 - __clz(sh.g.P);                               // log2 of the page size
-    page_rows = (uint32_t)sh.g.Hkv << psh;                  // token rows of a page, all heads
+    lane_sh = 31 - __clz(min(sh.g.P, kRows));                 // log2 of a copy's rows
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int u = dw + 4 * i;
@@ -314,67 +364,36 @@ struct Converter {
         r = 16 * u + (lane >> 1);
         piece = lane & 1;
       }
-      row[i] = row0 + r;
+      row[i] = r;
       // eight dims 4 piece + u: block (4 piece) / 8, chunk 4 (piece & 1) + u, by xor
       at_t[i] = (piece >> 1) * kBlk + sw128(r, 4 * (piece & 1));
-      at_c[i] = 16 * piece;
-      at_s[i] = 8 * (u / (kRows / 8));
+      at_c[i] = r * (D / 2) + dim0 / 2 + 16 * piece;
+      at_s[i] = kRows * (D / 2) + r * (D / 16) + dim0 / 16 + 2 * piece;
     }
   }
-  __device__ __forceinline__ int page_id(const Shape& sh, const Work& p, const Seg& seg, int beta) {
-    return beta < sh.g.MB && seg.n_all > seg.lo_all
-               ? __ldg(p.page_table + (size_t)seg.b * sh.g.MB + beta) : -1;
-  }
-  __device__ __forceinline__ void begin(const Shape& sh, const Work& p, const Seg& seg) {
-    const int lane = threadIdx.x & 31;
-    blk0 = (seg.chunk0 * kTok + row0) >> psh;
-    ids = page_id(sh, p, seg, blk0 + lane);
-    later = page_id(sh, p, seg, blk0 + 32 + lane);
-  }
-  // Requests a chunk into stage `slot`.
-  __device__ __forceinline__ void request(const Shape& sh, const Work& p, const Seg& seg, int chunk,
-                                          int slot) {
-    const int lane = threadIdx.x & 31;
-    const int tok0 = chunk * kTok;
-    if (((tok0 + row0) >> psh) - blk0 >= 32) {
-      blk0 += 32;
-      ids = later;
-      later = page_id(sh, p, seg, blk0 + 32 + lane);
-    }
-    const uint32_t head_rows = (uint32_t)seg.kvh << psh;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int tok = tok0 + row[i];
-      // (a step's rows are in one page: the same block in every lane)
-      const int at = (tok >> psh) - blk0;
-      const int page = __shfl_sync(0xffffffffu, at < 32 ? ids : later, at & 31);
-      // what no row of the unit sees is not looked at
-      const bool there = page >= 0 && page < sh.g.NP && tok >= seg.lo_all && tok < seg.n_all;
-      const size_t from = there ? (size_t)page * page_rows + head_rows + (tok & (sh.g.P - 1)) : 0;
-      const uint32_t dst = ring + slot * kStage + i * 576;
-      cp_async<16>(dst + 16 * lane, pool + from * (D / 2) + at_c[i], there);
-      // one lane per row copies the row's scales
-      constexpr int kLanes = kPieces >= 4 ? 4 : 2;
-      if ((lane & (kLanes - 1)) == 0)
-        cp_async<kSfRow>(dst + 512 + 2 * lane, sfs + from * (D / 16) + at_s[i], there);
-    }
-  }
-  // Chunk number `chunks` of the CTA from stage `slot` into its tile; false when the wait
-  // for the tile gave up.
-  __device__ __forceinline__ bool convert(int chunks, int slot) {
+  // Chunk number `chunks` of the CTA, from token tok0, out of stage `slot` into its tile; false
+  // when the wait for the tile gave up.
+  __device__ __forceinline__ bool convert(const Seg& seg, int tok0, int chunks, int slot, uint32_t copied,
+                                          bool v) {
     const int lane = threadIdx.x & 31;
     const int x = chunks & 1, use = chunks >> 1;
     if (use > 0 && gave_up(&freed[x], use - 1)) return false;
     uint8_t* tile = tiles + x * kBytes;
+    const uint32_t from = part + slot * T::kStage;
     const bool flip = kPieces >= 4 && (lane & 2);
+    // Rows that no vector of the unit sees, and what was not copied, become zeros by their scales
+    // (a code is always finite).
+    const int first = seg.lo_all - tok0 - row0;
+    const uint32_t seen = (uint32_t)max(seg.n_all - seg.lo_all, 0);
+    const uint32_t bits = copied >> (v ? 2 : 0);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const uint32_t src = ring + slot * kStage + i * 576;
       uint4 c;
       uint32_t sf;
       asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w) : "r"(src + 16 * lane));
-      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sf) : "r"(src + 512 + 2 * lane));
+                   : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w) : "r"(from + at_c[i]));
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sf) : "r"(from + at_s[i]));
+      if ((uint32_t)(row[i] - first) >= seen || !((bits >> (4 * (row[i] >> lane_sh))) & 1u)) sf = 0u;
       const uint32_t s2 = e4m3x2_to_f16x2(sf);
       const uint32_t sx[2] = {prmt(s2, 0, flip ? 0x3232 : 0x1010), prmt(s2, 0, flip ? 0x1010 : 0x3232)};
       const uint32_t w[4] = {flip ? c.z : c.x, flip ? c.w : c.y, flip ? c.x : c.z, flip ? c.y : c.w};
@@ -391,30 +410,33 @@ struct Converter {
 
 // Every chunk through one converter, or through K's and then V's.
 template <class T, class... C>
-__device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, const Span& span, C... conv) {
-  constexpr int kAhead = T::kDepth - 1;
-  int chunks = 0, put = 0, take = 0;    // chunks converted; ring stages
+__device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, const Span& span, uint64_t* full,
+                                            uint64_t* empty, const volatile uint32_t* copied, bool v,
+                                            C... conv) {
+  int chunks = 0, slot = 0, use = 0;
   Cursor cursor(span);
   Seg seg;
   while (cursor.next(sh, p.seqlens, seg)) {
-    (conv.begin(sh, p, seg), ...);
 #pragma unroll 1
-    for (int c = -kAhead; c < seg.todo; ++c) {
-      if (c + kAhead < seg.todo) (conv.request(sh, p, seg, seg.chunk0 + c + kAhead, put), ...);
-      cp_async_commit();
-      put = put + 1 == T::kDepth ? 0 : put + 1;
-      if (c < 0) continue;
-      cp_async_wait<kAhead>();
-      __syncwarp();
-      if (!(conv.convert(chunks, take) && ...)) return false;
-      __syncwarp();     // every lane has read the stage before it is requested again
-      take = take + 1 == T::kDepth ? 0 : take + 1;
+    for (int c = 0; c < seg.todo; ++c) {
+      if (gave_up(&full[slot], use)) return false;
+      const uint32_t bits = copied[slot];
+      bool second = v;
+      auto one = [&](auto& cv) {
+        const bool done = cv.convert(seg, (seg.chunk0 + c) * T::kTok, chunks, slot, bits, second);
+        second = true;
+        return done;
+      };
+      if (!(one(conv) && ...)) return false;
+      // (its lanes' loads are done: warp_arrive's __syncwarp lies behind them)
+      if ((threadIdx.x & 31) == 0) ws_arrive(&empty[slot]);
+      if (++slot == T::kDepth) {
+        slot = 0;
+        ++use;
+      }
       ++chunks;
     }
-    // (with fewer chunks than stages ahead, put has run past take by empty groups)
-    take = put;
   }
-  cp_async_wait<0>();
   return true;
 }
 
@@ -443,7 +465,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   uint8_t* sQ = smem;                                   // [kTiles][kQBytes]
   uint8_t* sK = sQ + kTiles * T::kQBytes;               // [2][kKBytes]
   uint8_t* sV = sK + 2 * T::kKBytes;                    // [2][kVBytes]
-  uint8_t* ring = sV + 2 * T::kVBytes;                  // [warp][kDepth][steps x 576]
+  uint8_t* ring = sV + 2 * T::kVBytes;                  // [kDepth][kStage]
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + T::kRing);
   uint64_t* kready = bars;
   uint64_t* vready = bars + 2;
@@ -455,8 +477,11 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   uint64_t* qready = bars + 15;
   uint64_t* mdone = bars + 16;       // after a give-up: every MMA issued has completed
   uint64_t* partO = bars + 17;
+  uint64_t* full = bars + 18;        // [kDepth]
+  uint64_t* empty = full + T::kDepth;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + T::kBars);
-  float* s_cq = reinterpret_cast<float*>(s_tmem + 6);   // [kTiles][128] logit scales
+  uint32_t* copied = s_tmem + 4;                               // [kDepth]
+  float* s_cq = reinterpret_cast<float*>(copied + T::kDepth);  // [kTiles][128] logit scales
 
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -473,6 +498,10 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     mbar_init(mdone, 1);
     s_tmem[1] = 0u;   // set when a CTA of the pair gave up
     mbar_init(qready, T::kSoft * CG);
+    for (int x = 0; x < T::kDepth; ++x) {
+      mbar_init(&full[x], 1);
+      mbar_init(&empty[x], T::kDeq);
+    }
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -793,26 +822,25 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     const int dw = (warp - T::kSoft) & 3;
     using CK = Converter<T, T::kKRows, D>;
     using CV = Converter<T, kTok, T::kVDims>;
-    static_assert(4 * T::kDepth * (CK::kStage + CV::kStage) == T::kRing, "ring");
-    uint8_t* mine = ring + dw * T::kDepth * CK::kStage;                            // K's part
-    uint8_t* mine_v = ring + T::kDepth * (4 * CK::kStage + dw * CV::kStage);       // V's
-    if constexpr (T::kDeq == 4) {
-      dead = !convert_all<T>(
-          sh, p, span, CK(sh, p.k_pool, p.k_sf, rank * T::kKRows, 0, dw, sK, mine, kready, kfree),
-          CV(sh, p.v_pool, p.v_sf, 0, rank * T::kVDims, dw, sV, mine_v, vready, vfree));
-    } else if constexpr (CG == 1) {   // one shape: one copy of the code for both
-      const bool v = warp - T::kSoft >= 4;
-      dead = !convert_all<T>(sh, p, span,
-                             CK(sh, v ? p.v_pool : p.k_pool, v ? p.v_sf : p.k_sf, 0, 0, dw,
-                                v ? sV : sK, v ? mine_v : mine, v ? vready : kready, v ? vfree : kfree));
-    } else if (warp - T::kSoft < 4) {
-      dead = !convert_all<T>(sh, p, span, CK(sh, p.k_pool, p.k_sf, rank * T::kKRows, 0, dw, sK, mine,
-                                             kready, kfree));
-    } else {
-      dead = !convert_all<T>(sh, p, span, CV(sh, p.v_pool, p.v_sf, 0, rank * T::kVDims, dw, sV, mine_v,
-                                             vready, vfree));
-    }
-  } else if (regs_down<T::kMmaRegs>(), warp == T::kMma && rank == 0) {
+    const bool v = warp - T::kSoft >= 4;
+    const int k0 = rank * T::kKRows, v0 = rank * T::kVDims;
+    if constexpr (T::kDeq == 4)
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, false,
+                             CK(sh, false, k0, 0, dw, ring, sK, kready, kfree),
+                             CV(sh, true, 0, v0, dw, ring, sV, vready, vfree));
+    else if constexpr (CG == 1)   // one shape: one copy of the code for both
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, v,
+                             CK(sh, v, 0, 0, dw, ring, v ? sV : sK, v ? vready : kready, v ? vfree : kfree));
+    else if (!v)
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, false,
+                             CK(sh, false, k0, 0, dw, ring, sK, kready, kfree));
+    else
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, true,
+                             CV(sh, true, 0, v0, dw, ring, sV, vready, vfree));
+  } else if (regs_down<T::kMmaRegs>(), warp == T::kMma + 1) {
+    // ==== copies =====================================================================
+    dead = !copy_all<T>(sh, p, span, rank, ring, full, empty, copied);
+  } else if (warp == T::kMma && rank == 0) {
     // ==== MMA issue ==================================================================
     const uint32_t one = elect_one();
     const uint32_t id_s = f16_idesc(128 * CG, kTok), id_o = f16_idesc(128 * CG, D) | kIdescBMn;
