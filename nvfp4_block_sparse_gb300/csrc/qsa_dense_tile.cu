@@ -112,7 +112,7 @@ struct TT {
   static constexpr int kRing = kDepth * kStage;
   static constexpr int kBars = 18 + 2 * kDepth;
   static constexpr int kSmem = 1024 + kTiles * kQBytes + 2 * kKBytes + 2 * kVBytes + kRing +
-                               kBars * 8 + 16 + kDepth * 4 + kTiles * 128 * 4;
+                               kBars * 8 + 16 + kDepth * 4;
 };
 
 // 32 columns of this thread's lane.
@@ -134,6 +134,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 // How far (log2) a logit may exceed the base: fp16 weights reach 65504, and as long as
 // every weight is finite its relative precision does not depend on the base.
 constexpr float kHeadroom = 15.f;
+
+// Asynchronous copy of 16 bytes, zeros where `on` is false.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Two fp32 multiply-adds / additions at once.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -481,7 +488,6 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   uint64_t* empty = full + T::kDepth;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + T::kBars);
   uint32_t* copied = s_tmem + 4;                               // [kDepth]
-  float* s_cq = reinterpret_cast<float*>(copied + T::kDepth);  // [kTiles][128] logit scales
 
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -547,104 +553,75 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       const size_t orow = ((size_t)seg.b * g.R + j) * g.Hq + head;
       const int n = real ? visible_tokens(seg.L, g.R, j, g.MB * g.P) : 0;
       const int lo = first_seen(n, sh.window);
-      // Q rows as fp16, each scaled by a power of two into [256, 512): eight lanes to a
-      // row, a 16-byte piece of every 64 dims each, all 32 rows of the warp in flight.
+      // Q rows as fp16, each scaled by a power of two into [256, 512).  The warp's 32 rows are
+      // copied into the place of its own, 128 dims at a time (eight lanes to a row, all copies in
+      // flight); then each thread has a row, finds its largest value and turns it into fp16,
+      // in place or (the A operand) into its tensor-memory lane, two dims a column.  With 256
+      // dims the first 128 are copied twice.  In loops, not unrolled: the code runs once per
+      // part, and the instructions' own way to the SM took most of its time.
       const uint32_t orow32 = (uint32_t)orow;     // (at most 2^24 rows of 256 heads)
-      {
-        uint4 raw[8][2];       // 128 dims of the warp's rows
-        auto load = [&](int d) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3);                  // row of the warp
-            const uint32_t from = __shfl_sync(0xffffffffu, orow32, r);
-            const bool there = (t * CG + rank) * 128 + 32 * (warp & 3) + r < seg.vecs;
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)from * D) + 16 * d + (lane & 7);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) raw[i][u] = there ? src[8 * u] : make_uint4(0u, 0u, 0u, 0u);
-          }
-        };
-        float amax[8], up[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax[i] = 0.f;
-#pragma unroll
-        for (int d = 0; d < D / 128; ++d) {
-          load(d);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t w4[4] = {raw[i][u].x, raw[i][u].y, raw[i][u].z, raw[i][u].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                amax[i] = fmax3(amax[i], fabsf(__uint_as_float(w4[k] << 16)),
-                                fabsf(__uint_as_float(w4[k] & 0xFFFF0000u)));
-            }
+      auto q_at = [&](int r, int pc) {            // 16-byte piece of a row of the warp
+        return T::kQTmem ? q_tile + (warp & 3) * 8192 + r * 256 + ((pc ^ (r & 7)) << 4)
+                         : q_tile + (pc >> 3) * 16384 + sw128(32 * (warp & 3) + r, pc & 7);
+      };
+      float amax = 0.f, up = 0.f, cq = 0.f;
+#pragma unroll 1
+      for (int pass = 0; pass < (D == 256 ? 3 : 1); ++pass) {
+        const int d0 = 128 * (pass & 1);
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int r = 2 * i + (lane >> 4), pc = lane & 15;
+          const uint32_t from = __shfl_sync(0xffffffffu, orow32, r);
+          const bool there = (t * CG + rank) * 128 + 32 * (warp & 3) + r < seg.vecs;
+          cp_async16(smem_u32(q_at(r, pc)), p.q + (there ? (size_t)from * D + d0 + 8 * pc : 0), there);
         }
+        cp_async_wait_all();
+        __syncwarp();
+        if (D == 128 || pass < 2) {
+#pragma unroll 4
+          for (int pc = 0; pc < 16; ++pc) {
+            const uint4 x = *reinterpret_cast<const uint4*>(q_at(lane, pc));
+            const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-#pragma unroll
-          for (int o = 4; o; o >>= 1) amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], o));
-          const int ebits = (int)((__float_as_uint(amax[i]) >> 23) & 0xFF);
-          int sq = (amax[i] > 0.f) ? 135 - ebits : 0;
+            for (int k = 0; k < 4; ++k)
+              amax = fmax3(amax, fabsf(__uint_as_float(w4[k] << 16)),
+                           fabsf(__uint_as_float(w4[k] & 0xFFFF0000u)));
+          }
+          const int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
+          int sq = (amax > 0.f) ? 135 - ebits : 0;
           sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
-          up[i] = __uint_as_float((uint32_t)(sq + 127) << 23);
-          const float down = __uint_as_float((uint32_t)(127 - sq) << 23);
-          if ((lane & 7) == 0)
-            s_cq[t * 128 + 32 * (warp & 3) + 4 * i + (lane >> 3)] = p.k_scale * p.sm_scale * kLog2e * down;
+          up = __uint_as_float((uint32_t)(sq + 127) << 23);
+          cq = p.k_scale * p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 - sq) << 23);
         }
-        auto half8 = [&](const uint4& x, float f) {
-          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-          uint32_t h[4];
+        if (D == 128 || pass > 0) {
+          auto half8 = [&](const uint4& x) {
+            const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+            uint32_t h[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            h[k] = pack_half2(__uint_as_float(w4[k] << 16) * f, __uint_as_float(w4[k] & 0xFFFF0000u) * f);
-          return make_uint4(h[0], h[1], h[2], h[3]);
-        };
-        if constexpr (T::kQTmem) {
-          // 128 dims of the warp's rows at a time; each thread then takes its own row to its
-          // tensor-memory lane, two dims a column (the A operand)
-          uint8_t* mine = q_tile + (warp & 3) * 8192;         // 32 rows x 16 pieces, swizzled
+            for (int k = 0; k < 4; ++k)
+              h[k] = pack_half2(__uint_as_float(w4[k] << 16) * up, __uint_as_float(w4[k] & 0xFFFF0000u) * up);
+            return make_uint4(h[0], h[1], h[2], h[3]);
+          };
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t v[16];
 #pragma unroll
-          for (int k = D / 128 - 1; k >= 0; --k) {   // (the last dims are still in registers)
-            const int d = k;
-            if (k < D / 128 - 1) load(d);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int r = 4 * i + (lane >> 3), pc = 8 * u + (lane & 7);
-                *reinterpret_cast<uint4*>(mine + r * 256 + ((pc ^ (r & 7)) << 4)) =
-                    half8(raw[i][u], up[i]);
-              }
-            __syncwarp();
-#pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
-              uint32_t v[16];
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const uint4 x = *reinterpret_cast<const uint4*>(
-                    mine + lane * 256 + (((4 * c4 + u) ^ (lane & 7)) << 4));
+            for (int u = 0; u < 4; ++u) {
+              uint4* at_q = reinterpret_cast<uint4*>(q_at(lane, 4 * c4 + u));
+              const uint4 x = half8(*at_q);
+              if constexpr (T::kQTmem) {
                 v[4 * u] = x.x; v[4 * u + 1] = x.y; v[4 * u + 2] = x.z; v[4 * u + 3] = x.w;
+              } else {
+                *at_q = x;
               }
-              tmem_st16u(tmem + T::kQCol + lane_off + 64 * d + 16 * c4, v);
             }
+            if constexpr (T::kQTmem) tmem_st16u(tmem + T::kQCol + lane_off + d0 / 2 + 16 * c4, v);
           }
-          tmem_wait_st();
-        } else {
-          static_assert(T::kQTmem || D == 128, "Q in shared memory: 128 dims");
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              *reinterpret_cast<uint4*>(q_tile + u * 16384 +
-                                        sw128(32 * (warp & 3) + 4 * i + (lane >> 3), lane & 7)) =
-                  half8(raw[i][u], up[i]);
-          fence_proxy_async_smem();
         }
       }
-      __syncwarp();
-      const float cq = s_cq[t * 128 + row];
+      if constexpr (T::kQTmem) tmem_wait_st();
+      else fence_proxy_async_smem();
       tc_fence_before();
       warp_arrive<CG>(qready);
 
