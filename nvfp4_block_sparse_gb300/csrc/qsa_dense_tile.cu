@@ -384,7 +384,6 @@ struct Converter {
                                           bool v) {
     const int lane = threadIdx.x & 31;
     const int x = chunks & 1, use = chunks >> 1;
-    if (use > 0 && gave_up(&freed[x], use - 1)) return false;
     uint8_t* tile = tiles + x * kBytes;
     const uint32_t from = part + slot * T::kStage;
     const bool flip = kPieces >= 4 && (lane & 2);
@@ -393,13 +392,20 @@ struct Converter {
     const int first = seg.lo_all - tok0 - row0;
     const uint32_t seen = (uint32_t)max(seg.n_all - seg.lo_all, 0);
     const uint32_t bits = copied >> (v ? 2 : 0);
+    uint4 codes[kUnits];       // every step's, so that their latencies overlap
+    uint32_t sfs[kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      uint4 c;
-      uint32_t sf;
       asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w) : "r"(from + at_c[i]));
-      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sf) : "r"(from + at_s[i]));
+                   : "=r"(codes[i].x), "=r"(codes[i].y), "=r"(codes[i].z), "=r"(codes[i].w)
+                   : "r"(from + at_c[i]));
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sfs[i]) : "r"(from + at_s[i]));
+    }
+    if (use > 0 && gave_up(&freed[x], use - 1)) return false;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const uint4 c = codes[i];
+      uint32_t sf = sfs[i];
       if ((uint32_t)(row[i] - first) >= seen || !((bits >> (4 * (row[i] >> lane_sh))) & 1u)) sf = 0u;
       const uint32_t s2 = e4m3x2_to_f16x2(sf);
       const uint32_t sx[2] = {prmt(s2, 0, flip ? 0x3232 : 0x1010), prmt(s2, 0, flip ? 0x1010 : 0x3232)};
