@@ -561,19 +561,19 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       const int lo = first_seen(n, sh.window);
       // Q rows as fp16, each scaled by a power of two into [256, 512).  The warp's 32 rows are
       // copied into the place of its own, 128 dims at a time (eight lanes to a row, all copies in
-      // flight); then each thread has a row, finds its largest value and turns it into fp16,
-      // in place or (the A operand) into its tensor-memory lane, two dims a column.  With 256
-      // dims the first 128 are copied twice.  In loops, not unrolled: the code runs once per
-      // part, and the instructions' own way to the SM took most of its time.
+      // flight); then each thread has a row, finds its largest value and turns the row into fp16,
+      // in place or, for the A operand in tensor memory, in its lane, two dims a column.  In
+      // loops, not unrolled: the code runs once per part, and the instructions' own way to the
+      // SM took most of its time.
       const uint32_t orow32 = (uint32_t)orow;     // (at most 2^24 rows of 256 heads)
       auto q_at = [&](int r, int pc) {            // 16-byte piece of a row of the warp
         return T::kQTmem ? q_tile + (warp & 3) * 8192 + r * 256 + ((pc ^ (r & 7)) << 4)
                          : q_tile + (pc >> 3) * 16384 + sw128(32 * (warp & 3) + r, pc & 7);
       };
-      float amax = 0.f, up = 0.f, cq = 0.f;
+      const uint32_t tQ = tmem + T::kQCol + lane_off;
+      __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
 #pragma unroll 1
-      for (int pass = 0; pass < (D == 256 ? 3 : 1); ++pass) {
-        const int d0 = 128 * (pass & 1);
+      for (int d0 = 0; d0 < D; d0 += 128) {
         __syncwarp();
 #pragma unroll 4
         for (int i = 0; i < 16; ++i) {
@@ -584,46 +584,47 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         }
         cp_async_wait_all();
         __syncwarp();
-        if (D == 128 || pass < 2) {
-#pragma unroll 4
-          for (int pc = 0; pc < 16; ++pc) {
-            const uint4 x = *reinterpret_cast<const uint4*>(q_at(lane, pc));
-            const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              amax = fmax3(amax, fabsf(__uint_as_float(w4[k] << 16)),
-                           fabsf(__uint_as_float(w4[k] & 0xFFFF0000u)));
-          }
-          const int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
-          int sq = (amax > 0.f) ? 135 - ebits : 0;
-          sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
-          up = __uint_as_float((uint32_t)(sq + 127) << 23);
-          cq = p.k_scale * p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 - sq) << 23);
-        }
-        if (D == 128 || pass > 0) {
-          auto half8 = [&](const uint4& x) {
-            const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-            uint32_t h[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              h[k] = pack_half2(__uint_as_float(w4[k] << 16) * up, __uint_as_float(w4[k] & 0xFFFF0000u) * up);
-            return make_uint4(h[0], h[1], h[2], h[3]);
-          };
 #pragma unroll 1
-          for (int c4 = 0; c4 < 4; ++c4) {
-            uint32_t v[16];
+        for (int c4 = 0; c4 < 4; ++c4) {
+          uint32_t v[16];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint4* at_q = reinterpret_cast<uint4*>(q_at(lane, 4 * c4 + u));
-              const uint4 x = half8(*at_q);
-              if constexpr (T::kQTmem) {
-                v[4 * u] = x.x; v[4 * u + 1] = x.y; v[4 * u + 2] = x.z; v[4 * u + 3] = x.w;
-              } else {
-                *at_q = x;
-              }
-            }
-            if constexpr (T::kQTmem) tmem_st16u(tmem + T::kQCol + lane_off + d0 / 2 + 16 * c4, v);
+          for (int u = 0; u < 4; ++u) {
+            const uint4 x = *reinterpret_cast<const uint4*>(q_at(lane, 4 * c4 + u));
+            v[4 * u] = x.x; v[4 * u + 1] = x.y; v[4 * u + 2] = x.z; v[4 * u + 3] = x.w;
           }
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[k])));
+          if constexpr (T::kQTmem) tmem_st16u(tQ + d0 / 2 + 16 * c4, v);
+        }
+      }
+      const float amax = fmaxf(__low2float(top2), __high2float(top2));
+      const int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
+      int sq = (amax > 0.f) ? 135 - ebits : 0;
+      sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
+      const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
+      const float cq = p.k_scale * p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 - sq) << 23);
+      auto half2_of = [&](uint32_t w) {
+        return pack_half2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+      };
+      if constexpr (T::kQTmem) {
+        tmem_wait_st();
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 16) {
+          float raw[16];
+          uint32_t v[16];
+          tmem_ld16(tQ + c, raw);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = half2_of(__float_as_uint(raw[k]));
+          tmem_st16u(tQ + c, v);
+        }
+      } else {
+#pragma unroll 2
+        for (int pc = 0; pc < 16; ++pc) {
+          uint4* at_q = reinterpret_cast<uint4*>(q_at(lane, pc));
+          const uint4 x = *at_q;
+          *at_q = make_uint4(half2_of(x.x), half2_of(x.y), half2_of(x.z), half2_of(x.w));
         }
       }
       if constexpr (T::kQTmem) tmem_wait_st();
