@@ -152,7 +152,7 @@ __device__ __forceinline__ void join_parts(const Shape& sh, const Work& p, int b
         }
     }
     if (!on || way != 0) continue;
-    const int j = (vec0 + c) / sh.G, head = kvh * sh.G + (vec0 + c) % sh.G;
+    const int j = row_of(sh, vec0 + c), head = kvh * sh.G + (vec0 + c) - j * sh.G;
     const size_t row = ((size_t)b * sh.g.R + j) * sh.g.Hq + head;
     float f = 1.f;
     if (p.sinks) add_sink(p.sinks[head], m, l, f);
@@ -182,7 +182,7 @@ struct Cfg {
   static constexpr int kK = TOK * kRow, kSc = TOK * kSf;
   static constexpr int kStage = 2 * kK + 2 * kSc;
   static constexpr int kRing = W * S * kStage;
-  static constexpr int kJoin = W * kCols * (D + 3) * 4;   // the warps' states, over the ring
+  static constexpr int kJoin = W * kCols * (D + 2) * 4;   // the warps' states, over the ring
   static constexpr int kMain = kRing > kJoin ? kRing : kJoin;
   static constexpr int kQ = kCols * D * 2;           // queries in fragment order
   static constexpr int kMisc = kCols * 4 * 3;
@@ -240,6 +240,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
   // (D = 256: four rows per copy, so every other one is four rows on in the swizzle)
   auto c_to = [&](int i) { return (D == 256 && (i & 1) ? c_dst ^ 64u : c_dst) + 512u * i; };
 
+  const int psh = 31 - __clz(g.P);                   // log2 of the page size
   Cursor cursor(span);
   Seg seg;
   while (cursor.next(sh, p.seqlens, seg)) {
@@ -257,7 +258,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
     for (int i = 0; i < kPer; ++i) {
       const int c = warp + i * W;
       const bool real = c < vecs;
-      const int j = real ? (vec0 + c) / sh.G : 0, hh = real ? (vec0 + c) % sh.G : 0;
+      const int j = real ? row_of(sh, vec0 + c) : 0, hh = real ? vec0 + c - j * sh.G : 0;
       const size_t row = ((size_t)b * g.R + j) * g.Hq + (size_t)kvh * sh.G + hh;
 #pragma unroll
       for (int u = 0; u < E / 4; ++u)
@@ -271,7 +272,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
       const int k = k0 + lane;
       pages = -1;
       if (k < mine && n_all > lo_all) {
-        const int beta = (chunk0 + warp + k * W) * TOK / g.P;
+        const int beta = ((chunk0 + warp + k * W) * TOK) >> psh;
         if (QSA_IN_BOUNDS(beta < g.MB, kChkChunk)) pages = p.page_table[(size_t)b * g.MB + beta];
         if (pages < 0 || pages >= g.NP) pages = -1;
       }
@@ -283,7 +284,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
       live = (live & ~(1u << (k & 31))) | ((uint32_t)ok << (k & 31));
       if (ok) {
         const int tok = (chunk0 + warp + k * W) * TOK;
-        const size_t row = ((size_t)page * g.Hkv + kvh) * g.P + tok % g.P;
+        const size_t row = (((size_t)page * g.Hkv + kvh) << psh) + (tok & (g.P - 1));
         const uint32_t st = ring + (k % S) * C::kStage;
         const uint8_t* kc = p.k_pool + row * C::kRow + lane * 16;
         const uint8_t* vc = p.v_pool + row * C::kRow + lane * 16;
@@ -312,7 +313,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
       const int c = warp + n * W;
       if (kCols % W != 0 && c >= kCols) break;
       const bool real = c < vecs;
-      const int j = real ? (vec0 + c) / sh.G : 0;
+      const int j = real ? row_of(sh, vec0 + c) : 0;
       float x[E];
 #pragma unroll
       for (int u = 0; u < E / 4; ++u) {
@@ -536,8 +537,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
     // adds up the W warps' four values of two vectors and two dims.
     float* j_base = reinterpret_cast<float*>(smem);        // [W][kCols]
     float* j_sum = j_base + W * kCols;                     // [W][kCols]
-    float* j_f = j_sum + W * kCols;                        // [W][kCols]
-    float4* j_o = reinterpret_cast<float4*>(j_f + W * kCols);   // [W][DT][NT][32]
+    float4* j_o = reinterpret_cast<float4*>(j_sum + W * kCols);   // [W][DT][NT][32]
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -556,34 +556,30 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
             make_float4(o[i][t][0], o[i][t][1], o[i][t][2], o[i][t][3]);
     }
     __syncthreads();
-    for (int x = tid; x < W * kCols; x += C::kThreads) {
-      const int c = x % kCols;
-      float m = kNoBase;
-#pragma unroll
-      for (int w = 0; w < W; ++w) m = fmaxf(m, j_base[w * kCols + c]);
-      j_f[x] = exp2_approx(j_base[x] - m);
-    }
-    __syncthreads();
     const bool whole = begins && ends;
     float* rec = p.records + ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * record_floats(sh.vt, D);
     for (int x = tid; x < DT * NT * 32; x += C::kThreads) {
       const int i = x / (NT * 32), t = (x / 32) % NT;
       float acc[4] = {0.f, 0.f, 0.f, 0.f}, l[2] = {0.f, 0.f}, m[2] = {kNoBase, kNoBase};
       const int c0 = 8 * t + 2 * tig;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float2 bs = *reinterpret_cast<const float2*>(j_base + w * kCols + c0);
+        m[0] = fmaxf(m[0], bs.x);
+        m[1] = fmaxf(m[1], bs.y);
+      }
 #pragma unroll 4
       for (int w = 0; w < W; ++w) {
         const float4 v = j_o[((w * DT + i) * NT + t) * 32 + lane];
-        const float2 f = *reinterpret_cast<const float2*>(j_f + w * kCols + c0);
         const float2 ls = *reinterpret_cast<const float2*>(j_sum + w * kCols + c0);
         const float2 bs = *reinterpret_cast<const float2*>(j_base + w * kCols + c0);
+        const float2 f = make_float2(exp2_approx(bs.x - m[0]), exp2_approx(bs.y - m[1]));
         acc[0] = fmaf(v.x, f.x, acc[0]);
         acc[1] = fmaf(v.y, f.y, acc[1]);
         acc[2] = fmaf(v.z, f.x, acc[2]);
         acc[3] = fmaf(v.w, f.y, acc[3]);
         l[0] = fmaf(ls.x, f.x, l[0]);
         l[1] = fmaf(ls.y, f.y, l[1]);
-        m[0] = fmaxf(m[0], bs.x);
-        m[1] = fmaxf(m[1], bs.y);
       }
       const int d = (D / 8) * gid + 2 * i;
 #pragma unroll
@@ -591,7 +587,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
         const int c = c0 + e;
         if (c >= vecs) continue;
         if (whole) {
-          const int j = (vec0 + c) / sh.G, head = kvh * sh.G + (vec0 + c) % sh.G;
+          const int j = row_of(sh, vec0 + c), head = kvh * sh.G + (vec0 + c) - j * sh.G;
           const size_t row = ((size_t)b * g.R + j) * g.Hq + head;
           if (!QSA_IN_BOUNDS(b < g.B && j < g.R && head < g.Hq, kChkOut)) continue;
           float f = 1.f;
@@ -677,7 +673,7 @@ dense_join_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     acc.z = fmaf(x.z, f, acc.z);
     acc.w = fmaf(x.w, f, acc.w);
   }
-  const int j = (int)((uint32_t)(vec0 + c) / (uint32_t)sh.G), head = d.kvh * sh.G + (vec0 + c) - j * sh.G;
+  const int j = row_of(sh, vec0 + c), head = d.kvh * sh.G + (vec0 + c) - j * sh.G;
   const size_t row = ((size_t)d.b * g.R + j) * g.Hq + head;
   float f = 1.f;
   if (p.sinks) add_sink(p.sinks[head], m, l, f);
@@ -745,8 +741,7 @@ int decode_cols(const Geom& g) { return g.R * (g.Hq / g.Hkv) <= 8 ? 8 : 16; }
 
 dense::Shape decode_shape(const Geom& g, int window) {
   dense::Shape s;
-  s.g = g;
-  s.G = g.Hq / g.Hkv;
+  dense::set_heads(&s, g);
   s.vt = decode_cols(g);
   s.tiles = (g.R * s.G + s.vt - 1) / s.vt;
   const int tok = g.D == 256 ? 32 : (s.vt == 8 ? C128a::TOK : C128b::TOK);

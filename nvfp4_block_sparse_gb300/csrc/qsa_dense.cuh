@@ -40,6 +40,7 @@ constexpr float kLazy = 8.f;       // log2-domain headroom of the softmax base
 struct Shape {
   Geom g;
   int G;         // query heads per KV head
+  uint32_t g_mul;   // ceil(2^32 / G) for G > 1: divides vector numbers (row_of)
   int vt;        // query vectors per tile
   int tiles;     // tiles per request
   int tok_sh;    // log2 of the tokens per chunk
@@ -76,6 +77,17 @@ __host__ __device__ __forceinline__ size_t record_floats(int vt, int D) {
   return (size_t)vt * (2 + D);
 }
 
+// Row of query vector x, x / G: for x < R G <= 2^19 and G <= 128 the product with
+// ceil(2^32 / G) is too large by less than x G < 2^32, so its upper half is exact.  (A division by
+// a variable is some 40 dependent instructions, and a part's start had eight of them.)
+__device__ __forceinline__ int row_of(const Shape& s, int x) {
+  return s.G == 1 ? x : (int)__umulhi((uint32_t)x, s.g_mul);
+}
+// Request of a group (request, tile): nearly always there is one tile.
+__device__ __forceinline__ int request_of(const Shape& s, int group) {
+  return s.tiles == 1 ? group : (int)((uint32_t)group / (uint32_t)s.tiles);
+}
+
 __device__ __forceinline__ int first_seen(int n, int window) {
   return window > 0 && n > window ? n - window : 0;
 }
@@ -93,8 +105,8 @@ __device__ __forceinline__ Sight sight_of(const Shape& s, int L, int tile) {
   const int cap = s.g.MB * s.g.P;
   v.vec0 = tile * s.vt;
   v.vecs = min(s.vt, s.g.R * s.G - v.vec0);
-  v.n_all = visible_tokens(L, s.g.R, (uint32_t)(v.vec0 + v.vecs - 1) / (uint32_t)s.G, cap);
-  v.n_least = visible_tokens(L, s.g.R, (uint32_t)v.vec0 / (uint32_t)s.G, cap);
+  v.n_all = visible_tokens(L, s.g.R, row_of(s, v.vec0 + v.vecs - 1), cap);
+  v.n_least = visible_tokens(L, s.g.R, row_of(s, v.vec0), cap);
   v.lo_all = first_seen(v.n_least, s.window);
   v.lo_most = first_seen(v.n_all, s.window);
   v.first = 0;
@@ -107,8 +119,8 @@ __device__ __forceinline__ Sight sight_of(const Shape& s, int L, int tile) {
 }
 
 __device__ __forceinline__ int chunk_count(const Shape& s, const int32_t* seqlens, int group) {
-  const uint32_t b = (uint32_t)group / (uint32_t)s.tiles;
-  return sight_of(s, seqlens[b], group - (int)b * s.tiles).count + s.lead;
+  const int b = request_of(s, group);
+  return sight_of(s, seqlens[b], group - b * s.tiles).count + s.lead;
 }
 
 // This CTA's part of the work, in the groups (request, tile) in order, each
@@ -208,7 +220,7 @@ struct Cursor {
       : at(s.begin), end(s.end), group_at(s.group_at), unit_at(0), group(s.group) {}
   __device__ __forceinline__ bool next(const Shape& s, const int32_t* seqlens, Seg& g) {
     while (at < end) {
-      g.b = (int)((uint32_t)group / (uint32_t)s.tiles);
+      g.b = request_of(s, group);
       g.tile = group - g.b * s.tiles;
       g.L = seqlens[g.b];
       static_cast<Sight&>(g) = sight_of(s, g.L, g.tile);
@@ -260,6 +272,12 @@ __device__ __forceinline__ void describe_none(const Shape& s, const Work& w, int
   if (!s.by_unit) w.desc[cta].b = -1;
 }
 
+// The heads' part of a shape.
+inline void set_heads(Shape* s, const Geom& g) {
+  s->g = g;
+  s->G = g.Hq / g.Hkv;
+  s->g_mul = s->G == 1 ? 0u : (uint32_t)(((1ull << 32) + s->G - 1) / s->G);
+}
 // Units of a geometry, and how descriptors go.
 inline long long unit_count(const Shape& s) { return (long long)s.g.B * s.tiles * s.g.Hkv; }
 inline int desc_count(const Shape& s) { return s.by_unit ? (int)unit_count(s) : s.ctas; }

@@ -555,7 +555,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       const int at = (t * CG + rank) * 128 + row;          // its number within the unit
       const int vec = seg.vec0 + at;
       const bool real = at < seg.vecs;
-      const int j = real ? vec / sh.G : 0, head = seg.kvh * sh.G + (real ? vec % sh.G : 0);
+      const int j = real ? row_of(sh, vec) : 0, head = seg.kvh * sh.G + (real ? vec - j * sh.G : 0);
       const size_t orow = ((size_t)seg.b * g.R + j) * g.Hq + head;
       const int n = real ? visible_tokens(seg.L, g.R, j, g.MB * g.P) : 0;
       const int lo = first_seen(n, sh.window);
@@ -975,8 +975,7 @@ dense::Shape dense_tile_shape(const Geom& g, int window) {
     s.tok_sh = T::kTok == 128 ? 7 : 6;
     s.ctas = dense_sms() / T::CG;
   };
-  s.g = g;
-  s.G = g.Hq / g.Hkv;
+  dense::set_heads(&s, g);
   if (use_pairs(g)) {
     if (g.D == 128) set(dense::TT<128, 2>());
     else set(dense::TT<256, 2>());
