@@ -748,7 +748,10 @@ dense::Shape decode_shape(const Geom& g, int window) {
   s.tok_sh = tok == 64 ? 6 : 5;
   s.window = window;
   s.least = 16;
-  s.lead = tok == 64 ? 16 : 32;
+  // A part's start and end take what a CTA's warps take for three and a half chunks each
+  // (16 warps: batched decode 27.9, 26.7, 25.3 and 25.8 us with 16, 32, 48 and 64, long
+  // decode 61.3, 60.3, 59.0 and 57.6).
+  s.lead = 7 * (g.D == 128 && s.vt == 8 ? C128a::W : C128b::W) / 2;
   s.ctas = dense_sms();
   s.by_unit = dense::unit_count(s) <= s.ctas;
   return s;
