@@ -83,9 +83,9 @@ struct TT {
   static constexpr int kThreads = 32 * (kMma + 4);
   // Registers per thread after the roles part (128 at launch): the softmax holds a
   // row's 128 logits.
-  static constexpr int kSoftRegs = kTiles == 2 ? 184 : 192;
-  static constexpr int kDeqRegs = kTiles == 2 ? 80 : 96;
-  static constexpr int kMmaRegs = kTiles == 2 ? 64 : 72;
+  static constexpr int kSoftRegs = kTiles == 2 ? 192 : 192;
+  static constexpr int kDeqRegs = kTiles == 2 ? 72 : 96;
+  static constexpr int kMmaRegs = kTiles == 2 ? 56 : 72;
   static_assert(32 * (kSoft * kSoftRegs + kDeq * kDeqRegs + 4 * kMmaRegs) <= kThreads * 128 &&
                     kThreads == 512, "registers");
   static constexpr int kVecs = 128 * CG * kTiles;        // query vectors of a unit
