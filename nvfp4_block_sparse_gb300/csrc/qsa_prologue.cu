@@ -54,8 +54,8 @@ rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
 //
 // A head of D elements belongs to D/8 lanes, eight elements (16 bytes) each: a
 // warp holds two heads at D = 128, one at D = 256.  A warp's turn is STEPS times
-// the heads it holds of one row and kind (query, key or value): all requested
-// before the first is used, and with many rows the next turn's before this
+// the heads it holds of one row's queries, or of its keys and, in the append, its values
+// behind them (the few of both share a turn): all requested before the first is used, and with many rows the next turn's before this
 // one's are worked on.  The row's cos and sin stay in registers meanwhile, and the
 // arithmetic is on packed pairs.  The pairs of the half layout meet by a
 // shuffle over rotary_dim / 16 lanes (rotary_dim is a multiple of 16, so a
@@ -70,7 +70,7 @@ struct KernelArgs {
   Geom g;
   NormRope nr;
   PrologueArgs a;
-  int turns_q, turns_k, turns;   // turns per row: queries, keys (values as many), all
+  int turns_q, turns;            // turns per row: queries, all
   float k_inv6, v_inv6;          // 1 / (6 scale), or 0 where that is far from 1
 };
 
@@ -168,41 +168,56 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
   pdl_wait();
   pdl_trigger();
 
-  // A turn: row, kind (0 query, 1 key, 2 value) and the lane's first head.
+  // A turn: row, queries (or keys and values) and the lane's first head.
   struct Turn {
     uint32_t row;
-    int kind, head;
+    bool query;
+    int head;
   };
   auto turn_of = [&](uint32_t item) {     // (2^24 rows of at most 2^8 turns)
     Turn t;
     t.row = item / (uint32_t)p.turns;
     int i = (int)(item - t.row * (uint32_t)p.turns);
-    t.kind = i < p.turns_q ? 0 : i < p.turns_q + p.turns_k ? 1 : 2;
-    i -= t.kind == 0 ? 0 : t.kind == 1 ? p.turns_q : p.turns_q + p.turns_k;
+    t.query = i < p.turns_q;
+    i -= t.query ? 0 : p.turns_q;
     t.head = i * (VPW * STEPS) + lane / LPV;
     return t;
   };
+  const int kvs = kAppend ? 2 * g.Hkv : g.Hkv;      // keys and values of a row
+  const int psh = 31 - __clz(g.P);                  // log2 of the page size
   uint4 coming[STEPS];
   auto request = [&](const Turn& t) {
-    const __nv_bfloat16* base = t.kind == 0 ? a.q : t.kind == 1 ? a.k : a.v;
-    const long long stride = t.kind == 0 ? a.q_stride : t.kind == 1 ? a.k_stride : a.v_stride;
-    const int heads = t.row >= T ? 0 : t.kind == 0 ? g.Hq : g.Hkv;
-    const __nv_bfloat16* src = base + t.row * stride + t.head * D + e0;
+    const int heads = t.row >= T ? 0 : t.query ? g.Hq : kvs;
+    if (!kAppend || t.query) {
+      const __nv_bfloat16* src = t.query ? a.q + t.row * a.q_stride : a.k + t.row * a.k_stride;
+      src += t.head * D + e0;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i)
-      coming[i] = t.head + i * VPW < heads ? *reinterpret_cast<const uint4*>(src + i * VPW * D)
-                                           : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < STEPS; ++i)
+        coming[i] = t.head + i * VPW < heads ? *reinterpret_cast<const uint4*>(src + i * VPW * D)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      const __nv_bfloat16* k = a.k + t.row * a.k_stride + e0;
+      const __nv_bfloat16* v = a.v + t.row * a.v_stride + e0;
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int hd = t.head + i * VPW;
+        const __nv_bfloat16* src = hd < g.Hkv ? k + hd * D : v + (hd - g.Hkv) * D;
+        coming[i] = hd < heads ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
   };
 
-  float2 w[4];          // the lane's weights of kind w_kind
-  int w_kind = -1;
+  float2 w[4];          // the lane's weights, of the queries or of the keys
+  int w_of = -1;
   uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);
   Turn now = turn_of(item);
   request(now);
   while (now.row < T) {
     const uint32_t r = now.row;
-    const int kind = now.kind, head0 = now.head, heads = kind == 0 ? g.Hq : g.Hkv;
-    const int left = heads - (head0 - lane / LPV);     // of the warp: steps past it hold nothing
+    const bool query = now.query;
+    const int head0 = now.head, heads = query ? g.Hq : kvs;
+    const int first = head0 - lane / LPV, left = heads - first;   // of the warp: steps past it hold nothing
+    const int turning = query || !kAppend ? left : g.Hkv - first;   // and steps past this only values
     uint4 raws[STEPS];
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) raws[i] = coming[i];
@@ -218,24 +233,23 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
     size_t page_row = 0;
     int slot = 0;
     bool has_slot = false;
-    if (kAppend && kind != 0) {
+    if (kAppend && !query) {
       const uint32_t b = r / (uint32_t)g.R;
       const long long pos = (long long)a.seqlens[b] - g.R + (int)(r - b * (uint32_t)g.R);
       if (pos >= 0 && pos < (long long)g.MB * g.P) {
-        const int at = (int)pos, beta = (int)((uint32_t)at / (uint32_t)g.P);
-        const int page = a.page_table[(size_t)b * g.MB + beta];
-        slot = at - beta * g.P;
+        const int page = a.page_table[(size_t)b * g.MB + ((int)pos >> psh)];
+        slot = (int)pos & (g.P - 1);
         has_slot = page >= 0 && page < g.NP;
         page_row = (size_t)(has_slot ? page : 0);
       }
-      // the index key, with the row's first values: 16 lanes x 4 B
-      if (kind == 2 && head0 < VPW && has_slot && lane < kIndexDim / 4) {
+      // the index key, with the row's first keys: 16 lanes x 4 B
+      if (head0 < VPW && has_slot && lane < kIndexDim / 4) {
         const uint32_t x = *reinterpret_cast<const uint32_t*>(a.ik + (size_t)r * kIndexDim + 4 * lane);
-        *reinterpret_cast<uint32_t*>(a.ik_pool + (page_row * g.P + slot) * kIndexDim + 4 * lane) = x;
+        *reinterpret_cast<uint32_t*>(a.ik_pool + ((page_row << psh) + slot) * kIndexDim + 4 * lane) = x;
       }
     }
 
-    if (kind < 2) {
+    {
       // the lane's cos and sin: o = y c + partner s, with the sign of the first
       // half's sine in s
       const int rot = p.nr.rot, h = rot >> 1;
@@ -268,9 +282,9 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
           }
         }
       }
-      const __nv_bfloat16* weight = kind == 0 ? a.q_weight : a.k_weight;
-      if (weight && kind != w_kind) {
-        w_kind = kind;
+      const __nv_bfloat16* weight = query ? a.q_weight : a.k_weight;
+      if (weight && (int)query != w_of) {
+        w_of = query;
         unpack8(__ldg(reinterpret_cast<const uint4*>(weight + e0)), w);
         if (p.nr.plus_one) {
 #pragma unroll
@@ -288,7 +302,7 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
           ss[i] = 0.f;
-          if (STEPS > 1 && i * VPW >= left) continue;
+          if ((STEPS > 1 || kAppend) && i * VPW >= turning) continue;
           float2 x[4];
           unpack8(raws[i], x);
 #pragma unroll
@@ -316,11 +330,11 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
           rms[i] = STEPS == 4 ? __shfl_sync(0xffffffffu, inv, (lane & ~(LPV - 1)) + i) : inv;
       }
 
-      __nv_bfloat16* out = kind == 0 ? a.q_out : a.k_out;
-      if (!kAppend || kind == 0) out += ((size_t)r * heads + head0) * D + e0;
+      __nv_bfloat16* out = query ? a.q_out : a.k_out;
+      if (!kAppend || query) out += ((size_t)r * heads + head0) * D + e0;
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
-        if (STEPS > 1 && i * VPW >= left) break;
+        if ((STEPS > 1 || kAppend) && i * VPW >= turning) break;
         float2 y[4];
         unpack8(raws[i], y);
         if (weight) {
@@ -342,43 +356,46 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
             if (turned) y[k] = turn2(y[k], c[k], t, s[k]);
           }
         }
-        raws[i] = pack8(y);
-        if ((!kAppend || kind == 0) && head0 + i * VPW < heads)
+        if (!kAppend || query || head0 + i * VPW < g.Hkv) raws[i] = pack8(y);   // (values stay)
+        if ((!kAppend || query) && head0 + i * VPW < heads)
           *reinterpret_cast<uint4*>(out + i * VPW * D) = raws[i];
       }
     }
-    if (!kAppend || kind == 0) continue;
+    if constexpr (kAppend) {
+      if (query) continue;
 
-    // keys and values: blocks of 16 (two lanes) to e2m1 codes and an e4m3 scale,
-    // as the token store quantises them
-    const float scale = kind == 2 ? a.v_scale : a.k_scale, inv6 = kind == 2 ? p.v_inv6 : p.k_inv6;
-    uint8_t* pool = kind == 2 ? a.v_pool : a.k_pool;
-    uint8_t* sfp = kind == 2 ? a.v_sf : a.k_sf;
+      // keys and values: blocks of 16 (two lanes) to e2m1 codes and an e4m3 scale,
+      // as the token store quantises them
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      if (STEPS > 1 && i * VPW >= left) break;
-      float2 x[4];
-      unpack8(raws[i], x);
-      float m = 0.f;
+      for (int i = 0; i < STEPS; ++i) {
+        if (STEPS > 1 && i * VPW >= left) break;
+        float2 x[4];
+        unpack8(raws[i], x);
+        float m = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      if (head0 + i * VPW < heads && has_slot) {
-        uint32_t sf;
-        const uint32_t codes = quantise8(x, m, scale, inv6, sf);
-        const size_t row = (page_row * g.Hkv + (head0 + i * VPW)) * g.P + slot;
-        if (QSA_IN_BOUNDS(row < (size_t)g.NP * g.Hkv * g.P, kChkRow)) {
-          *reinterpret_cast<uint32_t*>(pool + row * (D / 2) + 4 * l) = codes;
-          if (!(l & 1)) sfp[row * (D / 16) + (l >> 1)] = (uint8_t)sf;
+        for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        if (head0 + i * VPW < heads && has_slot) {
+          const bool val = head0 + i * VPW >= g.Hkv;
+          uint8_t* pool = val ? a.v_pool : a.k_pool;
+          uint8_t* sfp = val ? a.v_sf : a.k_sf;
+          uint32_t sf;
+          const uint32_t codes = quantise8(x, m, val ? a.v_scale : a.k_scale, val ? p.v_inv6 : p.k_inv6, sf);
+          const size_t row = (((page_row * g.Hkv + (head0 + i * VPW - (val ? g.Hkv : 0))) << psh)) + slot;
+          if (QSA_IN_BOUNDS(row < (size_t)g.NP * g.Hkv * g.P, kChkRow)) {
+            *reinterpret_cast<uint32_t*>(pool + row * (D / 2) + 4 * l) = codes;
+            if (!(l & 1)) sfp[row * (D / 16) + (l >> 1)] = (uint8_t)sf;
+          }
         }
+        __syncwarp();
       }
-      __syncwarp();
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Cache rows read back: eight elements (4 code bytes, one scale) per lane.
+// Cache rows read back: eight elements (4 code bytes, one scale) per lane; a CTA has
+// neighbouring rows of one head, which are neighbours in their page.
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32)
@@ -387,23 +404,19 @@ load_tokens_kernel(Geom g, const int32_t* __restrict__ page_table,
                    const uint8_t* __restrict__ k_sf, const uint8_t* __restrict__ v_pool,
                    const uint8_t* __restrict__ v_sf, float k_scale, float v_scale,
                    __nv_bfloat16* __restrict__ k_out, __nv_bfloat16* __restrict__ v_out) {
-  constexpr int LPV = D / 8;
-  const long long item = (long long)blockIdx.x * (kWarps * 32 / LPV) + threadIdx.x / LPV;
-  const int l = threadIdx.x % LPV;
-  const long long rows = (long long)g.B * g.R;
+  const uint32_t r = blockIdx.x * blockDim.y + threadIdx.y;
+  const int l = threadIdx.x, psh = 31 - __clz(g.P);
+  const bool is_v = blockIdx.y >= (uint32_t)g.Hkv;
+  const int head = (int)blockIdx.y - (is_v ? g.Hkv : 0);
   pdl_wait();
   pdl_trigger();
-  if (item >= rows * g.Hkv * 2) return;
-  const int head2 = (int)(item % (2 * g.Hkv));
-  const bool is_v = head2 >= g.Hkv;
-  const int head = is_v ? head2 - g.Hkv : head2;
-  const long long r = item / (2 * g.Hkv);
-  const int b = (int)(r / g.R), j = (int)(r % g.R);
-  const long long pos = (long long)seqlens[b] - g.R + j;
+  if (r >= (uint32_t)g.B * (uint32_t)g.R) return;
+  const uint32_t b = r / (uint32_t)g.R;
+  const long long pos = (long long)seqlens[b] - g.R + (int)(r - b * (uint32_t)g.R);
   if (pos < 0 || pos >= (long long)g.MB * g.P) return;
-  const int page = page_table[(size_t)b * g.MB + (int)(pos / g.P)];
+  const int page = page_table[(size_t)b * g.MB + ((int)pos >> psh)];
   if (page < 0 || page >= g.NP) return;
-  const size_t row = ((size_t)page * g.Hkv + head) * g.P + (int)(pos % g.P);
+  const size_t row = (((size_t)page * g.Hkv + head) << psh) + ((int)pos & (g.P - 1));
   if (!QSA_IN_BOUNDS(row < (size_t)g.NP * g.Hkv * g.P, kChkLoad)) return;
   const uint32_t w =
       *reinterpret_cast<const uint32_t*>((is_v ? v_pool : k_pool) + row * (D / 2) + 4 * l);
@@ -467,8 +480,7 @@ cudaError_t launch_prologue(const Geom& g, const NormRope& nr, const PrologueArg
   // share the row's cos and sin and one square root.
   const int steps = T * total / vpw > 152 * 64 ? 4 : 1, per = vpw * steps;
   p.turns_q = a.q ? (g.Hq + per - 1) / per : 0;
-  p.turns_k = (g.Hkv + per - 1) / per;
-  p.turns = p.turns_q + (append ? 2 : 1) * p.turns_k;
+  p.turns = p.turns_q + ((append ? 2 : 1) * g.Hkv + per - 1) / per;
   const long long items = T * p.turns;
   auto launch_it = [&]<int D, bool kAppend, bool kInter>() {
     auto* kern = steps == 4 ? prologue_kernel<D, kAppend, kInter, 4> : prologue_kernel<D, kAppend, kInter, 1>;
@@ -491,10 +503,10 @@ cudaError_t launch_load_tokens(const Geom& g, const int32_t* page_table, const i
                                const uint8_t* k_pool, const uint8_t* k_sf, const uint8_t* v_pool,
                                const uint8_t* v_sf, float k_scale, float v_scale, void* k_out,
                                void* v_out, bool pdl, cudaStream_t stream) {
-  const int per = kWarps * 32 / (g.D / 8);
-  const long long items = (long long)g.B * g.R * g.Hkv * 2;
+  const dim3 block(g.D / 8, kWarps * 32 / (g.D / 8));
+  const unsigned rows = (unsigned)g.B * (unsigned)g.R;
   auto* kern = g.D == 256 ? load_tokens_kernel<256> : load_tokens_kernel<128>;
-  return launch(kern, dim3((unsigned)((items + per - 1) / per)), dim3(kWarps * 32), pdl, stream, g,
+  return launch(kern, dim3((rows + block.y - 1) / block.y, 2 * g.Hkv), block, pdl, stream, g,
                 page_table, seqlens, k_pool, k_sf, v_pool, v_sf, k_scale, v_scale,
                 reinterpret_cast<__nv_bfloat16*>(k_out), reinterpret_cast<__nv_bfloat16*>(v_out));
 }
