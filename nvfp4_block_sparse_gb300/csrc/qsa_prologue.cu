@@ -394,43 +394,64 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// Cache rows read back: eight elements (4 code bytes, one scale) per lane; a CTA has
-// neighbouring rows of one head, which are neighbours in their page.
+// Cache rows read back: eight elements (4 code bytes, one scale) of a key and of its
+// value per lane, for ROWS rows at once: three loads depend on one another (length, page,
+// codes), so what is in flight decides.  A CTA has neighbouring rows of one head, which
+// are neighbours in their page.
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kWarps * 32)
 load_tokens_kernel(Geom g, const int32_t* __restrict__ page_table,
                    const int32_t* __restrict__ seqlens, const uint8_t* __restrict__ k_pool,
                    const uint8_t* __restrict__ k_sf, const uint8_t* __restrict__ v_pool,
                    const uint8_t* __restrict__ v_sf, float k_scale, float v_scale,
                    __nv_bfloat16* __restrict__ k_out, __nv_bfloat16* __restrict__ v_out) {
-  const uint32_t r = blockIdx.x * blockDim.y + threadIdx.y;
-  const int l = threadIdx.x, psh = 31 - __clz(g.P);
-  const bool is_v = blockIdx.y >= (uint32_t)g.Hkv;
-  const int head = (int)blockIdx.y - (is_v ? g.Hkv : 0);
+  const int l = threadIdx.x, psh = 31 - __clz(g.P), head = blockIdx.y;
+  const uint32_t r0 = blockIdx.x * (blockDim.y * ROWS) + threadIdx.y, rows = (uint32_t)g.B * (uint32_t)g.R;
   pdl_wait();
   pdl_trigger();
-  if (r >= (uint32_t)g.B * (uint32_t)g.R) return;
-  const uint32_t b = r / (uint32_t)g.R;
-  const long long pos = (long long)seqlens[b] - g.R + (int)(r - b * (uint32_t)g.R);
-  if (pos < 0 || pos >= (long long)g.MB * g.P) return;
-  const int page = page_table[(size_t)b * g.MB + ((int)pos >> psh)];
-  if (page < 0 || page >= g.NP) return;
-  const size_t row = (((size_t)page * g.Hkv + head) << psh) + ((int)pos & (g.P - 1));
-  if (!QSA_IN_BOUNDS(row < (size_t)g.NP * g.Hkv * g.P, kChkLoad)) return;
-  const uint32_t w =
-      *reinterpret_cast<const uint32_t*>((is_v ? v_pool : k_pool) + row * (D / 2) + 4 * l);
-  const float sf = e4m3_to_f32((is_v ? v_sf : k_sf)[row * (D / 16) + (l >> 1)]);
-  const float scale = is_v ? v_scale : k_scale;
-  float2 x[4];
+  int page[ROWS], slot[ROWS];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t h2 = e2m1x2_to_f16x2((w >> (8 * i)) & 0xFFu);
-    // code * block scale is exact in fp32; the tensor scale rounds once
-    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-    x[i] = make_float2(__fmul_rn(v.x * sf, scale), __fmul_rn(v.y * sf, scale));
+  for (int i = 0; i < ROWS; ++i) {
+    const uint32_t r = r0 + i * blockDim.y, b = r / (uint32_t)g.R;
+    page[i] = -1;
+    if (r >= rows) continue;
+    const long long pos = (long long)seqlens[b] - g.R + (int)(r - b * (uint32_t)g.R);
+    slot[i] = (int)pos & (g.P - 1);
+    if (pos >= 0 && pos < (long long)g.MB * g.P)
+      page[i] = page_table[(size_t)b * g.MB + ((int)pos >> psh)];
+    if (page[i] >= g.NP) page[i] = -1;
   }
-  *reinterpret_cast<uint4*>((is_v ? v_out : k_out) + ((size_t)r * g.Hkv + head) * D + 8 * l) = pack8(x);
+  uint32_t codes[ROWS][2], sfs[ROWS][2];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const size_t row = page[i] < 0 ? 0 : (((size_t)page[i] * g.Hkv + head) << psh) + slot[i];
+    if (!QSA_IN_BOUNDS(row < (size_t)g.NP * g.Hkv * g.P, kChkLoad)) page[i] = -1;
+    if (page[i] < 0) continue;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      codes[i][v] = *reinterpret_cast<const uint32_t*>((v ? v_pool : k_pool) + row * (D / 2) + 4 * l);
+      sfs[i][v] = (v ? v_sf : k_sf)[row * (D / 16) + (l >> 1)];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (page[i] < 0) continue;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const float sf = e4m3_to_f32(sfs[i][v]), scale = v ? v_scale : k_scale;
+      float2 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t h2 = e2m1x2_to_f16x2((codes[i][v] >> (8 * u)) & 0xFFu);
+        // code * block scale is exact in fp32; the tensor scale rounds once
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+        x[u] = make_float2(__fmul_rn(y.x * sf, scale), __fmul_rn(y.y * sf, scale));
+      }
+      __nv_bfloat16* out = v ? v_out : k_out;
+      *reinterpret_cast<uint4*>(out + ((size_t)(r0 + i * blockDim.y) * g.Hkv + head) * D + 8 * l) = pack8(x);
+    }
+  }
 }
 
 template <class... Ex, class... Ac>
@@ -505,8 +526,14 @@ cudaError_t launch_load_tokens(const Geom& g, const int32_t* page_table, const i
                                void* v_out, bool pdl, cudaStream_t stream) {
   const dim3 block(g.D / 8, kWarps * 32 / (g.D / 8));
   const unsigned rows = (unsigned)g.B * (unsigned)g.R;
-  auto* kern = g.D == 256 ? load_tokens_kernel<256> : load_tokens_kernel<128>;
-  return launch(kern, dim3((rows + block.y - 1) / block.y, 2 * g.Hkv), block, pdl, stream, g,
+  // Few rows: one per thread, for the shortest chain (192 rows of 4 heads: 4.1 us, 5.8 with
+  // four); many: four, for more in flight (8188 rows of 2 heads at head_dim 256: 7.3 us, 10.7
+  // with one).
+  const bool many = (long long)rows * g.Hkv > 152 * 16 * (long long)block.y;
+  const unsigned per = block.y * (many ? 4 : 1);
+  auto* kern = many ? (g.D == 256 ? load_tokens_kernel<256, 4> : load_tokens_kernel<128, 4>)
+                    : (g.D == 256 ? load_tokens_kernel<256, 1> : load_tokens_kernel<128, 1>);
+  return launch(kern, dim3((rows + per - 1) / per, g.Hkv), block, pdl, stream, g,
                 page_table, seqlens, k_pool, k_sf, v_pool, v_sf, k_scale, v_scale,
                 reinterpret_cast<__nv_bfloat16*>(k_out), reinterpret_cast<__nv_bfloat16*>(v_out));
 }
