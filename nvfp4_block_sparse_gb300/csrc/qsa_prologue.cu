@@ -156,7 +156,7 @@ __device__ __forceinline__ uint32_t quantise8(const float2 (&x)[4], float m, flo
 }
 
 template <int D, bool kAppend, bool kInter, int STEPS>
-__global__ void __launch_bounds__(kWarps * 32, STEPS == 1 ? 8 : 5)
+__global__ void __launch_bounds__(kWarps * 32, STEPS == 1 ? 8 : kAppend ? 5 : 6)
 prologue_kernel(const __grid_constant__ KernelArgs p) {
   constexpr int LPV = D / 8;        // lanes per head
   constexpr int VPW = 32 / LPV;     // heads that a warp holds
@@ -505,8 +505,9 @@ cudaError_t launch_prologue(const Geom& g, const NormRope& nr, const PrologueArg
   const long long items = T * p.turns;
   auto launch_it = [&]<int D, bool kAppend, bool kInter>() {
     auto* kern = steps == 4 ? prologue_kernel<D, kAppend, kInter, 4> : prologue_kernel<D, kAppend, kInter, 1>;
-    // many rows: five CTAs' warps per SM stay and take turns
-    const long long ctas = (items + kWarps - 1) / kWarps, most = 5 * 152;
+    // many rows: six CTAs per SM stay and take turns, or five of the append, which needs more
+    // registers (two context chunks, norms: 40.4 us with six, 42.4 with five; append 58.1, 56.8)
+    const long long ctas = (items + kWarps - 1) / kWarps, most = (kAppend ? 5 : 6) * 152;
     return launch(kern, dim3((unsigned)(steps == 4 && ctas > most ? most : ctas)), dim3(kWarps * 32),
                   pdl, stream, p);
   };
