@@ -570,11 +570,13 @@ qsa_status_t qsa_load_kv_tokens(const qsa_geom_t *geom, const int32_t *page_tabl
  *
  *   q, pools, scales, page_table, seqlens, out, lse   as in qsa_sparse_decode
  *   window    tokens a row looks back over, itself included; 0: all
- *   sinks     fp32 [Hq], or NULL: a logit per query head that takes part in
+ *   sinks     fp32 [Hq], or NULL: a logit per query head (finite, or -inf: none) that takes part in
  *             the softmax's denominator without a value (-inf: none)
  *   workspace >= qsa_dense_attention_workspace_bytes() bytes, 256-byte
  *             aligned, zero-filled once by qsa_workspace_init(); calls that
- *             share one must not overlap on the GPU
+ *             share one must not overlap on the GPU.  Dense calls of different
+ *             geometries may share one that is large enough for each; other
+ *             calls' workspaces are apart
  *
  * Row j of request b sees n tokens (as above): those at positions
  * max(0, n - window)..n - 1 whose page is valid.

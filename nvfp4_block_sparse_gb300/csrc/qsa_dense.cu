@@ -706,7 +706,9 @@ size_t dense_carve(const dense::Shape& s, void* workspace, dense::Work* w) {
     w->status = reinterpret_cast<int*>(base);
     w->tickets = reinterpret_cast<int*>(base + off);
   }
-  off += ((size_t)s.ctas * sizeof(int) + 255) / 256 * 256;
+  // (the same place for every geometry: a workspace may serve several, and tickets have to
+  // be found at zero)
+  off += ((size_t)dense_sms() * sizeof(int) + 255) / 256 * 256;
   if (w) w->desc = reinterpret_cast<dense::Desc*>(base + off);
   off += ((size_t)dense::desc_count(s) * sizeof(dense::Desc) + 255) / 256 * 256;
   if (w) w->records = reinterpret_cast<float*>(base + off);

@@ -124,6 +124,22 @@ def test_calls_behind_one_another_with_other_lengths(qsa, rows):
     assert torch.equal(first, step.out)
 
 
+def test_geometries_share_a_workspace(qsa):
+    # context rows, verify rows and decode rows by turns on one workspace: what one leaves
+    # there (descriptors that name its last CTA, records) means nothing to the next
+    works = [qw.make_workload(case(batch=b, rows_per_req=r, num_q_heads=4 * hkv, num_kv_heads=hkv,
+                                   head_dim=D, ctx_lo=L, ctx_hi=L, max_blocks=-(-L // 64)), "cuda")
+             for b, r, hkv, D, L in ((3, 40, 1, 128, 18176), (1, 1, 2, 128, 45728), (40, 5, 2, 256, 900),
+                                     (2, 2, 2, 128, 9000), (60, 30, 2, 128, 700), (1, 1, 2, 256, 45000))]
+    steps = [qsa.DenseStep(qw.geometry(w), device="cuda") for w in works]
+    shared = max((s.workspace for s in steps), key=lambda t: t.numel())
+    for s in steps:
+        s.workspace = shared
+    for _ in range(2):
+        for w, s in zip(works, steps):
+            check(w, run(qsa, w, step=s))
+
+
 @pytest.mark.parametrize("k_scale,v_scale,spread", [
     (1e-30, 1e30, 1.0), (1e-38, 3e38, 1.0), (2.0**-126, 2.0**-100, 1e-30), (1.0, 1.0, 0.0),
     (0.01, 448.0 * 6.0, 1e4), (1e20, 1e-20, 1e15), (3e-3, 1 / 3, 100.0),
