@@ -570,8 +570,8 @@ qsa_status_t qsa_load_kv_tokens(const qsa_geom_t *geom, const int32_t *page_tabl
  *
  *   q, pools, scales, page_table, seqlens, out, lse   as in qsa_sparse_decode
  *   window    tokens a row looks back over, itself included; 0: all
- *   sinks     fp32 [Hq], or NULL: a logit per query head (finite, or -inf: none) that takes part in
- *             the softmax's denominator without a value (-inf: none)
+ *   sinks     fp32 [Hq], or NULL: a logit per query head that takes part in
+ *             the softmax's denominator without a value (finite, or -inf: none)
  *   workspace >= qsa_dense_attention_workspace_bytes() bytes, 256-byte
  *             aligned, zero-filled once by qsa_workspace_init(); calls that
  *             share one must not overlap on the GPU.  Dense calls of different
