@@ -12,15 +12,27 @@
 // A tile is 128 query vectors (row, head) of one request and KV head: the 128
 // tensor-memory lanes of a CTA.
 //
-// Pairs of CTAs (more than 128 vectors per KV head): the two SMs of a pair run
-// M = 256 MMAs (cta_group::2) on two tiles at once, each SM holding half of
-// every K and V tile (half the tokens of K, half the dims of V).  So each SM
-// dequantises half of a chunk and feeds half of the B operand from its shared
-// memory; with one SM per tile, operand reads and the dequantised stores fill
-// shared memory's bandwidth and everything else that uses it (barrier probes)
-// crawls.  At head_dim 128 a CTA has two tiles (four per pair), at 256 one.
-// Single CTAs (17 to 128 vectors: verify rows) have one tile, for which the cache's
-// bytes, not the products, are the floor.
+// Pairs of CTAs (more than two tiles of vectors per KV head at head_dim 128,
+// more than one at 256): the two SMs of a pair run M = 256 MMAs (cta_group::2)
+// on two tiles at once, each SM holding half of every K and V tile (half the
+// tokens of K, half the dims of V).  So each SM dequantises half of a chunk and
+// feeds half of the B operand from its shared memory; with one SM per tile,
+// operand reads and the dequantised stores fill shared memory's bandwidth and
+// everything else that uses it (barrier probes) crawls (two context chunks of
+// 1024 rows: 941 us, by pairs 811).  At head_dim 128 a CTA has two tiles (four
+// per pair), at 256 one.  Single CTAs (fewer vectors, from 17 on: verify rows)
+// have one tile, for which the cache's bytes, not the products, are the floor.
+//
+// Measured (GB300, SM clock 2070 MHz):
+//   two context chunks of 1024 rows, 32 heads on 4, behind 30000 tokens: 641 us,
+//   1.62 PFLOP/s (0.82 of the measured cuBLAS rate).  The tensor pipe is active
+//   71 % of the time; a chunk's turn takes 2900 cycles of the 2460 that its MMAs
+//   need, the rest is the softmax's latency between a tile's turns.
+//   32 requests x 4 verify rows, 24 heads on 2, head_dim 256, window 4096: 43 us
+//   for 79 MB (floor 11.8).  Each SM has 21 chunks of 64 tokens, 2000 cycles each
+//   (the K warps' conversion), a start of 8 us (work division, queries, the first
+//   pages; mostly instructions fetched for the first time) and an end of 6 us
+//   (records, the join).
 //
 // Roles in a CTA (a warp group each unless noted):
 //   softmax   a thread per vector (tensor-memory lane): its row of S to registers, base
@@ -201,7 +213,8 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 
 // ---- MMAs by one lane of a converged warp ---------------------------------------
 // The lane is elected once (`one` is 1 in it): the warp stays converged, so that the
-// descriptors stay in uniform registers, and an MMA costs no election of its own.
+// descriptors stay in uniform registers, and an MMA costs no election of its own (two
+// context chunks 737 -> 673 us).
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
@@ -256,7 +269,9 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // ---- copies ----------------------------------------------------------------------
-// The copy warp brings every chunk's codes and scales into the ring, kDepth chunks ahead:
+// The copy warp brings every chunk's codes and scales into the ring, kDepth chunks ahead
+// (copies by the converting warps themselves took a third of their time: windowed verify
+// rows 50 -> 46 us without, two context chunks 673 -> 648):
 // a piece of a page (as many rows as the chunk has of it) is contiguous, so that a chunk is
 // at most eight bulk copies, one per lane.  Pages that are not there, and pieces that no row
 // of the unit sees, are not copied; `copied` says so (bit per lane of the stage's copies).
@@ -964,8 +979,10 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
 }  // namespace
 }  // namespace dense
 
-// More than one tile of vectors per KV head: pairs of CTAs.
-static bool use_pairs(const Geom& g) { return g.R * (g.Hq / g.Hkv) > 128; }
+// Pairs of CTAs where single ones would take more units: a pair's unit is 512 vectors at
+// head_dim 128 and 256 at 256 (4 requests of 8192 tokens, pairs against singles: 160 vectors
+// 38 and 31 us at head_dim 128, 28.9 and 29.5 at 256; 512 vectors 42 and 49, 42 and 44).
+static bool use_pairs(const Geom& g) { return g.R * (g.Hq / g.Hkv) > (g.D == 128 ? 256 : 128); }
 
 dense::Shape dense_tile_shape(const Geom& g, int window) {
   dense::Shape s;
@@ -985,7 +1002,11 @@ dense::Shape dense_tile_shape(const Geom& g, int window) {
   }
   s.tiles = (g.R * s.G + s.vt - 1) / s.vt;
   s.window = window;
-  s.least = 4;
+  // A short context is divided down to two chunks (64 rows over 2048 tokens: 19.2, 21.3,
+  // 24.9 us with two, four, eight); a part's start and end take what ten chunks take
+  // (windowed verify rows 45.3, 43.3, 43.5, 45.0 us with 4, 7, 10, 14, 77 context rows 32.7,
+  // 30.4, 29.3, 29.5).
+  s.least = 2;
   s.lead = 10;
   s.by_unit = dense::unit_count(s) <= s.ctas;
   return s;

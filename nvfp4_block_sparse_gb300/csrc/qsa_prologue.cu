@@ -27,7 +27,8 @@ namespace {
 // Rotation rows.  A frequency is a 64-bit fraction of a turn, so pos * turns
 // modulo 2^64 is the angle as a fraction of a turn whatever the position; its
 // upper 32 bits, signed, lie in [-1/2, 1/2) turn and sincospif takes them
-// without a further reduction.
+// without a further reduction.  4 x 4096 rows of 32 pairs (4.2 MB): 5.3 us; 192 rows of 64
+// pairs: 1.8 us, a launch.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
 rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
@@ -61,8 +62,12 @@ rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
 // shuffle over rotary_dim / 16 lanes (rotary_dim is a multiple of 16, so a
 // lane's eight elements have one partner lane); interleaved pairs are in the lane.
 //
-// Bound by instructions before memory: about 100 per head and warp; see the
-// quantiser below for what its divisions cost.
+// Measured (GB300): norms and rotation of 8192 rows of 24 + 2 heads of 256 (220 MB) 40.4 us,
+// 5.4 TB/s (0.81 of the measured copy rate), instructions issued in 60 % of the cycles: about
+// 100 per head and warp.  The append of 8188 such rows with their values (223 MB) 48.6 us:
+// its keys and values take four times the instructions of a query; see the quantiser below
+// for what its divisions cost.  Steps (8192 rows): a turn per kind 77 us, next turn requested
+// ahead 63.5, four square roots as one 51.7, packed arithmetic 42.
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 4;
 
@@ -498,8 +503,10 @@ cudaError_t launch_prologue(const Geom& g, const NormRope& nr, const PrologueArg
   const long long T = (long long)g.B * g.R;
   const int total = (a.q ? g.Hq : 0) + (append ? 2 : 1) * g.Hkv;   // heads per row
   // Few rows: a turn of one step, for the shortest chain; many rows: four steps
-  // share the row's cos and sin and one square root.
-  const int steps = T * total / vpw > 152 * 64 ? 4 : 1, per = vpw * steps;
+  // share the row's cos and sin and one square root (40 heads of 128: 64 rows 2.1 and 2.9 us
+  // with one and four, 256 rows, 5120 single turns, 3.4 both, 512 rows 5.4 and 5.0, 2048 rows
+  // 16.9 and 11.2).
+  const int steps = T * total / vpw > 152 * 40 ? 4 : 1, per = vpw * steps;
   p.turns_q = a.q ? (g.Hq + per - 1) / per : 0;
   p.turns = p.turns_q + ((append ? 2 : 1) * g.Hkv + per - 1) / per;
   const long long items = T * p.turns;

@@ -129,7 +129,7 @@ def test_geometries_share_a_workspace(qsa):
     # there (descriptors that name its last CTA, records) means nothing to the next
     works = [qw.make_workload(case(batch=b, rows_per_req=r, num_q_heads=4 * hkv, num_kv_heads=hkv,
                                    head_dim=D, ctx_lo=L, ctx_hi=L, max_blocks=-(-L // 64)), "cuda")
-             for b, r, hkv, D, L in ((3, 40, 1, 128, 18176), (1, 1, 2, 128, 45728), (40, 5, 2, 256, 900),
+             for b, r, hkv, D, L in ((3, 80, 1, 128, 18176), (1, 1, 2, 128, 45728), (40, 5, 2, 256, 900),
                                      (2, 2, 2, 128, 9000), (60, 30, 2, 128, 700), (1, 1, 2, 256, 45000))]
     steps = [qsa.DenseStep(qw.geometry(w), device="cuda") for w in works]
     shared = max((s.workspace for s in steps), key=lambda t: t.numel())
