@@ -542,15 +542,15 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
   }
-  pdl_wait();
-  const Span span = plan_span<T::kThreads>(sh, p.seqlens, worker, sh.ctas);
-  pdl_trigger();
-  if (tid == 0 && rank == 0) describe_none(sh, p, worker);
   tc_fence_before();
   if constexpr (CG == 2) cluster_sync();    // the pair's barriers are initialised
   else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  pdl_wait();
+  const Span span = plan_span<T::kThreads>(sh, p.seqlens, worker, sh.ctas);
+  pdl_trigger();
+  if (tid == 0 && rank == 0) describe_none(sh, p, worker);
   bool dead = false;
 
   if (warp < T::kSoft) {
