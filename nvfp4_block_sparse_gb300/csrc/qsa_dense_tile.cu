@@ -587,8 +587,12 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       };
       const uint32_t tQ = tmem + T::kQCol + lane_off;
       __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
+      // A warp without a vector only keeps step with the barriers: its rows of S, P and O are
+      // nobody's.  (With two tiles most warps have one, and the registers for asking cost more:
+      // two context chunks 634 us without, 643 with it.)
+      const bool some = kTiles == 2 || (t * CG + rank) * 128 + 32 * (warp & 3) < seg.vecs;
 #pragma unroll 1
-      for (int d0 = 0; d0 < D; d0 += 128) {
+      for (int d0 = 0; d0 < D && some; d0 += 128) {
         __syncwarp();
 #pragma unroll 4
         for (int i = 0; i < 16; ++i) {
@@ -625,7 +629,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       if constexpr (T::kQTmem) {
         tmem_wait_st();
 #pragma unroll 1
-        for (int c = 0; c < D / 2; c += 16) {
+        for (int c = 0; c < D / 2 && some; c += 16) {
           float raw[16];
           uint32_t v[16];
           tmem_ld16(tQ + c, raw);
@@ -636,7 +640,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         }
       } else {
 #pragma unroll 2
-        for (int pc = 0; pc < 16; ++pc) {
+        for (int pc = 0; pc < 16 && some; ++pc) {
           uint4* at_q = reinterpret_cast<uint4*>(q_at(lane, pc));
           const uint4 x = *at_q;
           *at_q = make_uint4(half2_of(x.x), half2_of(x.y), half2_of(x.z), half2_of(x.w));
@@ -671,6 +675,12 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         if (gave_up(&barS[y], kTiles == 2 ? s_waits : chunks >> 1)) { dead = true; break; }
         ++s_waits;
         tc_fence_after();
+        if (!some) {
+          tc_fence_before();
+#pragma unroll
+          for (int h = 0; h < T::kHalves; ++h) warp_arrive<CG>(&pready[2 * y + h]);
+          continue;
+        }
         const bool edge = tok0 + kTok > seg.n_least || tok0 < seg.lo_most ||
                           (live & all_live) != all_live;
         // The row's logits, those it does not see at -inf.
