@@ -529,7 +529,8 @@ qsa_status_t qsa_qk_norm_rope(const qsa_geom_t *geom, const qsa_norm_rope_t *nor
  * (v rows v_row_stride elements apart) in one launch, with the same bytes as
  * the two calls one after the other: keys are rounded to bf16 before they are
  * quantised.  q and q_out may both be NULL.  Rows without a slot are skipped
- * in the pools; their queries are written all the same.
+ * in the pools; their queries are written all the same.  No two rows may have
+ * the same slot (a page that requests share takes no new rows).
  * Returns QSA_ERR_INVALID_ARG as the two calls do (k_pool, v_pool and the
  * index pointers 4-byte aligned).
  */

@@ -39,7 +39,6 @@
 #include "qsa_dense.cuh"
 
 #include <algorithm>
-#include <mutex>
 
 namespace qsa {
 namespace dense {

@@ -166,6 +166,30 @@ def test_append_far_from_the_middle(qsa, k_scale, v_scale, spread, rows):
         assert torch.equal(two[n], pools[n]), n
 
 
+@pytest.mark.parametrize("rows", [1, 40])
+def test_append_of_infinities_and_nan(qsa, rows):
+    # whatever the values, the fused call leaves the bytes of the two
+    w = qw.make_workload(cache_case(rows_per_req=rows, ctx_lo=rows, ctx_hi=400, max_blocks=7, k=2),
+                         "cuda")
+    T = w["batch"] * rows
+    x = draw(T, 8, 2, 128, 64, seed=8)
+    for i, value in enumerate((float("inf"), float("-inf"), float("nan"), 3e38, 1e-40)):
+        x["k"][:, :, i::37] = value
+        x["v"][:, i % 2, i::41] = value
+    x["v"][0] = float("nan")
+    nr = qsa.make_norm_rope(64)
+    for weight in (None, x["k_weight"]):
+        new = dict(x, k_weight=weight)
+        pools, two = ({n: w[n].clone() for n in POOLS} for _ in range(2))
+        append(qsa, w, dict(new, q=None), nr, pools, None)
+        k2 = torch.empty(T, 2, 128, dtype=torch.bfloat16, device="cuda")
+        qsa.qsa_qk_norm_rope(qw.geometry(w), nr, None, x["k"], None, weight, x["cs"], None, k2)
+        qsa.qsa_store_kv_tokens(qw.geometry(w), k2, x["v"].contiguous(), x["ik_new"], w["k_scale"],
+                                w["v_scale"], w["page_table"], w["seqlens"], *(two[n] for n in POOLS))
+        for n in POOLS:
+            assert torch.equal(two[n], pools[n]), n
+
+
 def test_append_of_a_padded_batch(qsa):
     # rows of requests without a length or a page: queries are written, the pools stay
     w = qw.make_workload(cache_case(batch=6, rows_per_req=4), "cuda")
