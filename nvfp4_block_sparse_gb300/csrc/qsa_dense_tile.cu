@@ -24,7 +24,7 @@
 // have one tile, for which the cache's bytes, not the products, are the floor.
 //
 // Measured (GB300, SM clock 2070 MHz):
-//   two context chunks of 1024 rows, 32 heads on 4, behind 30000 tokens: 641 us,
+//   two context chunks of 1024 rows, 32 heads on 4, behind 30000 tokens: 638 us,
 //   1.62 PFLOP/s (0.82 of the measured cuBLAS rate).  The tensor pipe is active
 //   71 % of the time; a chunk's turn takes 2900 cycles of the 2460 that its MMAs
 //   need, the rest is the softmax's latency between a tile's turns.

@@ -62,9 +62,9 @@ rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
 // shuffle over rotary_dim / 16 lanes (rotary_dim is a multiple of 16, so a
 // lane's eight elements have one partner lane); interleaved pairs are in the lane.
 //
-// Measured (GB300): norms and rotation of 8192 rows of 24 + 2 heads of 256 (220 MB) 40.4 us,
-// 5.4 TB/s (0.81 of the measured copy rate), instructions issued in 60 % of the cycles: about
-// 100 per head and warp.  The append of 8188 such rows with their values (223 MB) 48.6 us:
+// Measured (GB300): norms and rotation of 8192 rows of 24 + 2 heads of 256 (220 MB) 40.2 us,
+// 5.5 TB/s (0.82 of the measured copy rate), instructions issued in 60 % of the cycles: about
+// 100 per head and warp.  The append of 8188 such rows with their values (223 MB) 47 us:
 // its keys and values take four times the instructions of a query; see the quantiser below
 // for what its divisions cost.  Steps (8192 rows): a turn per kind 77 us, next turn requested
 // ahead 63.5, four square roots as one 51.7, packed arithmetic 42.
@@ -179,13 +179,11 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
     bool query;
     int head;
   };
-  auto turn_of = [&](uint32_t item) {     // (2^24 rows of at most 2^8 turns)
+  auto turn_of = [&](uint32_t row, uint32_t i) {     // (the row's turn i)
     Turn t;
-    t.row = item / (uint32_t)p.turns;
-    int i = (int)(item - t.row * (uint32_t)p.turns);
-    t.query = i < p.turns_q;
-    i -= t.query ? 0 : p.turns_q;
-    t.head = i * (VPW * STEPS) + lane / LPV;
+    t.row = row;
+    t.query = i < (uint32_t)p.turns_q;
+    t.head = (int)(i - (t.query ? 0u : (uint32_t)p.turns_q)) * (VPW * STEPS) + lane / LPV;
     return t;
   };
   const int kvs = kAppend ? 2 * g.Hkv : g.Hkv;      // keys and values of a row
@@ -214,8 +212,11 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
 
   float2 w[4];          // the lane's weights, of the queries or of the keys
   int w_of = -1;
-  uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  Turn now = turn_of(item);
+  // turns of all rows one behind the other, this warp's `step` apart (2^24 rows of at most 2^8)
+  const uint32_t turns = p.turns, item = blockIdx.x * kWarps + (threadIdx.x >> 5), step = gridDim.x * kWarps;
+  uint32_t row = item / turns, at = item - row * turns;
+  const uint32_t step_rows = STEPS > 1 ? step / turns : 0u, step_at = STEPS > 1 ? step - step_rows * turns : 0u;
+  Turn now = turn_of(row, at);
   request(now);
   while (now.row < T) {
     const uint32_t r = now.row;
@@ -227,8 +228,13 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) raws[i] = coming[i];
     if (STEPS > 1) {
-      item += gridDim.x * kWarps;
-      now = turn_of(item);
+      row += step_rows;
+      at += step_at;
+      if (at >= turns) {
+        at -= turns;
+        ++row;
+      }
+      now = turn_of(row, at);
       request(now);
     } else {
       now.row = T;
