@@ -143,6 +143,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Waits for tensor-memory loads into v.  The empty statement behind the wait takes the values
+// through, so that no use of them is scheduled ahead of it.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld_of(float (&v)[N]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; i += 16)
+    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]),
+                      "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]), "+f"(v[i + 8]), "+f"(v[i + 9]),
+                      "+f"(v[i + 10]), "+f"(v[i + 11]), "+f"(v[i + 12]), "+f"(v[i + 13]),
+                      "+f"(v[i + 14]), "+f"(v[i + 15]));
+}
+
 // How far (log2) a logit may exceed the base: fp16 weights reach 65504, and as long as
 // every weight is finite its relative precision does not depend on the base.
 constexpr float kHeadroom = 15.f;
@@ -633,7 +646,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           float raw[16];
           uint32_t v[16];
           tmem_ld16(tQ + c, raw);
-          tmem_wait_ld();
+          tmem_wait_ld_of(raw);
 #pragma unroll
           for (int k = 0; k < 16; ++k) v[k] = half2_of(__float_as_uint(raw[k]));
           tmem_st16u(tQ + c, v);
@@ -687,7 +700,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         float z[kTok];
 #pragma unroll
         for (int i = 0; i < kTok / 32; ++i) tmem_ld32(tS + 32 * i, z + 32 * i);
-        tmem_wait_ld();
+        tmem_wait_ld_of(z);
         if (edge) {
 #pragma unroll
           for (int i = 0; i < kTok; ++i) {
@@ -719,7 +732,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
             for (int i = 0; i < D / 16; ++i) {   // (rare: kept small, as the instruction cache is)
               float o16[16];
               tmem_ld16(tO + 16 * i, o16);
-              tmem_wait_ld();
+              tmem_wait_ld_of(o16);
 #pragma unroll
               for (int u = 0; u < 16; ++u) o16[u] *= alpha;
               tmem_st16(tO + 16 * i, o16);
@@ -774,7 +787,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         for (int d0 = 0; d0 < D && left > 0; d0 += 32) {
           float o32[32];
           tmem_ld32(tO + d0, o32);
-          tmem_wait_ld();
+          tmem_wait_ld_of(o32);
           if (real)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -796,7 +809,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           float o64[64];
           tmem_ld32(tO + d0, o64);
           tmem_ld32(tO + d0 + 32, o64 + 32);
-          tmem_wait_ld();
+          tmem_wait_ld_of(o64);
 #pragma unroll
           for (int i = 0; i < 16; ++i)       // 16-byte pieces, swizzled by the row
             *reinterpret_cast<float4*>(box(lane) + ((i ^ (lane & 15)) << 4)) =
