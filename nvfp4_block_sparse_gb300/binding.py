@@ -442,15 +442,19 @@ def _at(t, dtype, name, numel, dev):
 
 def _rows_at(t, heads, dims, name, rows, dev):
     """Pointer and row stride of [rows, heads, dims] bf16 rows whose heads are behind one another."""
+    try:
+        (n, h, d), (row, head, one) = t.shape, t.stride()
+        if (t.dtype is _BF16 and t.get_device() == dev and n >= rows and h == heads and d == dims
+                and one == 1 and (head == dims or heads == 1)):
+            return t.data_ptr(), row if rows > 1 else heads * dims
+    except (AttributeError, ValueError):
+        pass
     _device(t, name)
     if t.dtype is not _BF16 or t.get_device() != dev:
         _refuse(t, _BF16, name, 0, dev)
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] < rows or shape[1] != heads or shape[2] != dims:
-        raise ValueError("%s must be [%d, %d, %d], got %s" % (name, rows, heads, dims, list(shape)))
-    if stride[2] != 1 or (heads > 1 and stride[1] != dims):
-        raise ValueError("%s must have its heads behind one another" % name)
-    return t.data_ptr(), stride[0] if rows > 1 else heads * dims
+    if t.dim() != 3 or t.shape[0] < rows or t.shape[1] != heads or t.shape[2] != dims:
+        raise ValueError("%s must be [%d, %d, %d], got %s" % (name, rows, heads, dims, list(t.shape)))
+    raise ValueError("%s must have its heads behind one another" % name)
 
 
 def _launch(fn, dev, stream, args):
