@@ -92,6 +92,17 @@ def test_tables_longer_than_a_warp(qsa, rows):
     check(w, run(qsa, w, 4500), 4500)
 
 
+@pytest.mark.parametrize("D,P", [(128, 64), (128, 128), (256, 32), (256, 64)])
+@pytest.mark.parametrize("rows,window", [(1, 0), (3, 200), (9, 0), (9, 200), (40, 129), (70, 0), (150, 0),
+                                         (150, 300)])
+def test_page_sizes(qsa, D, P, rows, window):
+    # a chunk of the kernels is a part of a page, one page or several; some are missing
+    w = qw.make_workload(case(batch=3, rows_per_req=rows, head_dim=D, page_size=P, ctx_lo=rows,
+                              ctx_hi=1300, max_blocks=-(-1300 // P), invalid_frac=0.3), "cuda")
+    sinks = sink_of(w, window > 0)
+    check(w, run(qsa, w, window, sinks), window, sinks)
+
+
 @pytest.mark.parametrize("rows", [2, 12, 90])
 def test_two_calls_at_once(qsa, rows):
     # two steps with workspaces of their own, in flight on two streams
