@@ -237,9 +237,8 @@ struct Lay {
 
 
 // One (request b, KV head kvh, head slice, split s) unit of work by the whole
-// CTA.  wait_before_list() runs after the prologue (the queries, the page-table
-// row and the length are in shared memory), before the row's selection is
-// read; after_list() once this CTA's chunk list is built.
+// CTA.  wait_before_list() runs once the page-table row and the length are there,
+// before the row's selection and its queries are read; after_list() once this CTA's chunk list is built.
 template <int NT, int NG, int SG, class Wait, class After>
 __device__ __forceinline__ void attend_cta(const Params& p, int s, int kvh, int slice, int b,
                                            Wait&& wait_before_list, After&& after_list) {
@@ -291,9 +290,9 @@ __device__ __forceinline__ void attend_cta(const Params& p, int s, int kvh, int 
   // Matched by the wait before the first remote write of the merge.
   if (CL > 1) cluster_arrive_relaxed();
 
-  // ---- before the dependency wait: step inputs no kernel of the step writes ----
-  // The page-table row goes to shared memory by asynchronous copies, so its
-  // loads, the queries' and the length's are all in flight together.
+  // ---- before the dependency wait: the page-table row and the length, which no
+  // kernel of the library writes ----
+  // The row goes to shared memory by asynchronous copies, in flight with the length.
   const bool pt_smem = g.MB <= kPtMax;
   if (pt_smem)
     for (int i = tid; i < g.MB; i += kThreads)
@@ -303,44 +302,26 @@ __device__ __forceinline__ void attend_cta(const Params& p, int s, int kvh, int 
   asm volatile("cp.async.commit_group;" ::: "memory");
   const int Lb = p.seqlens[b];
   const int cap = g.MB * g.P;
-  // Queries -> fp16 pre-scaled by a power of two per column (|q|max into
-  // [256, 512): exact, and any bf16 magnitude stays inside fp16 range), one
-  // warp per column, four dims per lane.
-  for (int c = warp; c < kCols; c += NG * kGW) {
-    const int j = c / hs, hh = c - (c / hs) * hs;
-    const bool real = j < R && hh < hreal;
-    uint2 raw = make_uint2(0u, 0u);
-    if (real) {
-      const int h = kvh * G + h0 + hh;
-      raw = *reinterpret_cast<const uint2*>(p.q + ((size_t)(b * R + j) * g.Hq + h) * kD + 4 * lane);
-    }
-    const __nv_bfloat162 lo = *reinterpret_cast<const __nv_bfloat162*>(&raw.x);
-    const __nv_bfloat162 hi = *reinterpret_cast<const __nv_bfloat162*>(&raw.y);
-    const float v0 = __low2float(lo), v1 = __high2float(lo);
-    const float v2 = __low2float(hi), v3 = __high2float(hi);
-    float amax = fmaxf(fmaxf(fabsf(v0), fabsf(v1)), fmaxf(fabsf(v2), fabsf(v3)));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
-    int sq = (amax > 0.f) ? 135 - ebits : 0;
-    sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
-    const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
-    const float down = __uint_as_float((uint32_t)(127 - sq) << 23);
-    // 16-byte unit j = lane / 2 of the row sits at qunit(c, j) (a swizzle
-    // that spreads the fragment reads below over all banks).
-    __half2* dst = reinterpret_cast<__half2*>(qs + c * kD + 8 * qunit(c, lane >> 1) + 4 * (lane & 1));
-    dst[0] = __floats2half2_rn(v0 * up, v1 * up);
-    dst[1] = __floats2half2_rn(v2 * up, v3 * up);
-    if (lane == 0) {
-      col_cq[c] = real ? p.k_scale * p.sm_scale * kLog2e * down : 0.f;
-      col_n[c] = real ? visible_tokens(Lb, R, j, cap) : 0;
-      col_row[c] = real ? j : -1;
-    }
-  }
   if (tid == 0) misc[1] = 0;   // set when a bounded wait gives up
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  wait_before_list();   // the selections come from an earlier kernel or CTA
+  // The selections come from an earlier kernel or CTA; so may the queries, which the
+  // norm and rotation kernel writes: both are read behind this wait only.
+  wait_before_list();
+
+  // The warp's columns of the queries (one warp per column, four dims per lane): on
+  // their way while the chunk list is built, used once the copies have been issued.
+  constexpr int kQPerWarp = (kCols + NG * kGW - 1) / (NG * kGW);
+  uint2 raw[kQPerWarp];
+#pragma unroll
+  for (int i = 0; i < kQPerWarp; ++i) {
+    const int c = warp + i * NG * kGW;
+    const int j = c / hs, hh = c - (c / hs) * hs;
+    raw[i] = make_uint2(0u, 0u);
+    if (c < kCols && j < R && hh < hreal)
+      raw[i] = *reinterpret_cast<const uint2*>(
+          p.q + ((size_t)(b * R + j) * g.Hq + kvh * G + h0 + hh) * kD + 4 * lane);
+  }
 
   // ---- this CTA's chunks ----------------------------------------------------
   // Candidate chunk c of the row (entry c >> csh, part c & csh) belongs to
@@ -412,6 +393,39 @@ __device__ __forceinline__ void attend_cta(const Params& p, int s, int kvh, int 
     fence_proxy_async_smem();   // after the union's scratch in the stage region
     issue(grp + NG * lane);
   }
+
+  // Queries -> fp16 pre-scaled by a power of two per column (|q|max into
+  // [256, 512): exact, and any bf16 magnitude stays inside fp16 range).
+#pragma unroll
+  for (int i = 0; i < kQPerWarp; ++i) {
+    const int c = warp + i * NG * kGW;
+    if (kCols % (NG * kGW) != 0 && c >= kCols) break;
+    const int j = c / hs, hh = c - (c / hs) * hs;
+    const bool real = j < R && hh < hreal;
+    const __nv_bfloat162 lo = *reinterpret_cast<const __nv_bfloat162*>(&raw[i].x);
+    const __nv_bfloat162 hi = *reinterpret_cast<const __nv_bfloat162*>(&raw[i].y);
+    const float v0 = __low2float(lo), v1 = __high2float(lo);
+    const float v2 = __low2float(hi), v3 = __high2float(hi);
+    float amax = fmaxf(fmaxf(fabsf(v0), fabsf(v1)), fmaxf(fabsf(v2), fabsf(v3)));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
+    int sq = (amax > 0.f) ? 135 - ebits : 0;
+    sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
+    const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
+    const float down = __uint_as_float((uint32_t)(127 - sq) << 23);
+    // 16-byte unit j = lane / 2 of the row sits at qunit(c, j) (a swizzle
+    // that spreads the fragment reads below over all banks).
+    __half2* dst = reinterpret_cast<__half2*>(qs + c * kD + 8 * qunit(c, lane >> 1) + 4 * (lane & 1));
+    dst[0] = __floats2half2_rn(v0 * up, v1 * up);
+    dst[1] = __floats2half2_rn(v2 * up, v3 * up);
+    if (lane == 0) {
+      col_cq[c] = real ? p.k_scale * p.sm_scale * kLog2e * down : 0.f;
+      col_n[c] = real ? visible_tokens(Lb, R, j, cap) : 0;
+      col_row[c] = real ? j : -1;
+    }
+  }
+  __syncthreads();
 
   // ---- per-column state and fragments --------------------------------------
   // Per lane column: cq, and the row (low 4 bits, 15 = padding) with the

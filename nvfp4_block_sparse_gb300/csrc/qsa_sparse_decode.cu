@@ -542,26 +542,26 @@ sparse_decode_kernel(Params p) {
     fence_mbar_init();
   }
 
-  // ---- before the dependency wait: what does not depend on the selection ---
-  // The queries, the request's page-table row and its length are step inputs
-  // that no kernel of the step writes; the selection kernel triggers its
-  // dependents only after its own wait returned, so they are complete here.
+  // ---- before the dependency wait: the page-table row and the length, which no kernel of
+  // the library writes ---
   const bool pt_in_smem = g.MB <= kPtRowMax;
   if (pt_in_smem)
     for (int i = tid; i < g.MB; i += kThreads) s_pt[i] = p.page_table[(size_t)b * g.MB + i];
   const int L = p.seqlens[b];
   const int cap = g.MB * g.P;
-  {
-    // Queries -> fp16 pre-scaled by a power of two per column, one warp per
-    // column.  The scale maps |q|max into [256, 512): exact, and keeps bf16
-    // queries of any magnitude inside fp16 range.  2^sq and its inverse are
-    // built from exponent bits (|sq| <= 126 keeps both normal).
-    // Lane holds D/32 consecutive dims (4 or 8), read as D/128 8-byte words.
-    // Columns in passes of kQPerWarp per warp (one pass for decode rows).
-    constexpr int kQPerWarp = ONE ? (kHsp + kWarps - 1) / kWarps : (kMaxRows * kHsp + kWarps - 1) / kWarps;
-    constexpr int kQw = D / 128;
-    for (int cb = 0; cb < ncols; cb += kQPerWarp * kWarps) {
-    uint2 raw[kQPerWarp][kQw];
+  __syncthreads();   // barriers and page-table row visible to every warp
+  pdl_wait();        // the selections come from an earlier kernel, and so may the queries
+
+  // Queries -> fp16 pre-scaled by a power of two per column, one warp per
+  // column.  The scale maps |q|max into [256, 512): exact, and keeps bf16
+  // queries of any magnitude inside fp16 range.  2^sq and its inverse are
+  // built from exponent bits (|sq| <= 126 keeps both normal).
+  // Lane holds D/32 consecutive dims (4 or 8), read as D/128 8-byte words.
+  // Columns in passes of kQPerWarp per warp (one pass for decode rows).
+  constexpr int kQPerWarp = ONE ? (kHsp + kWarps - 1) / kWarps : (kMaxRows * kHsp + kWarps - 1) / kWarps;
+  constexpr int kQw = D / 128;
+  uint2 raw[kQPerWarp][kQw];
+  auto load_q = [&](int cb) {
 #pragma unroll
     for (int ci = 0; ci < kQPerWarp; ++ci) {
       const int c = cb + warp + ci * kWarps;
@@ -576,6 +576,8 @@ sparse_decode_kernel(Params p) {
         for (int u = 0; u < kQw; ++u) raw[ci][u] = src[u];
       }
     }
+  };
+  auto store_q = [&](int cb) {
 #pragma unroll
     for (int ci = 0; ci < kQPerWarp; ++ci) {
       const int c = cb + warp + ci * kWarps;
@@ -606,37 +608,8 @@ sparse_decode_kernel(Params p) {
         col_n[c] = visible_tokens(L, R, r0 + c / kHsp, cap);
       }
     }
-    }
-  }
-
-  __syncthreads();   // barriers, page-table row and queries visible to every warp
-
-  // Each consumer's query fragments and column constants, into registers.
-  const int cbase = jw * kHsp;
-  float cq[NTR][2];
-  int nrow = 0;                                 // tokens this row sees
-  // Q^T fragments: column nt*8+gid of the row, dims [D/4*tig, D/4*(tig+1)).
-  uint32_t qf[NTR][D / 8];
-  if (!producer) {
-#pragma unroll
-    for (int nt = 0; nt < NTR; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) cq[nt][e] = col_cq[cbase + nt * 8 + 2 * tig + e];
-    nrow = col_n[cbase];
-#pragma unroll
-    for (int nt = 0; nt < NTR; ++nt) {
-      const uint4* src =
-          reinterpret_cast<const uint4*>(qs + (cbase + nt * 8 + gid) * D + (D / 4) * tig);
-#pragma unroll
-      for (int v4 = 0; v4 < D / 32; ++v4) {
-        const uint4 x = src[v4];
-        qf[nt][4 * v4 + 0] = x.x; qf[nt][4 * v4 + 1] = x.y;
-        qf[nt][4 * v4 + 2] = x.z; qf[nt][4 * v4 + 3] = x.w;
-      }
-    }
-  }
-  __syncthreads();   // the query tile (in the stage region) is no longer read
-  pdl_wait();        // the selections come from the preceding kernel
+  };
+  load_q(0);   // (on its way while the chunks are listed)
 
   const int csh = (g.P == 2 * kChunk) ? 1 : 0;  // stages per page: 1 << csh
   // Self-issued: each warp lists its own chunks straight from its row's
@@ -693,7 +666,42 @@ sparse_decode_kernel(Params p) {
       wcnt += __popc(vm);
     }
     __syncwarp();
-  } else {
+  }
+
+  store_q(0);
+  for (int cb = kQPerWarp * kWarps; cb < ncols; cb += kQPerWarp * kWarps) {
+    load_q(cb);
+    store_q(cb);
+  }
+  __syncthreads();   // queries visible to every warp
+
+  // Each consumer's query fragments and column constants, into registers.
+  const int cbase = jw * kHsp;
+  float cq[NTR][2];
+  int nrow = 0;                                 // tokens this row sees
+  // Q^T fragments: column nt*8+gid of the row, dims [D/4*tig, D/4*(tig+1)).
+  uint32_t qf[NTR][D / 8];
+  if (!producer) {
+#pragma unroll
+    for (int nt = 0; nt < NTR; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) cq[nt][e] = col_cq[cbase + nt * 8 + 2 * tig + e];
+    nrow = col_n[cbase];
+#pragma unroll
+    for (int nt = 0; nt < NTR; ++nt) {
+      const uint4* src =
+          reinterpret_cast<const uint4*>(qs + (cbase + nt * 8 + gid) * D + (D / 4) * tig);
+#pragma unroll
+      for (int v4 = 0; v4 < D / 32; ++v4) {
+        const uint4 x = src[v4];
+        qf[nt][4 * v4 + 0] = x.x; qf[nt][4 * v4 + 1] = x.y;
+        qf[nt][4 * v4 + 2] = x.z; qf[nt][4 * v4 + 3] = x.w;
+      }
+    }
+  }
+  __syncthreads();   // the query tile (in the stage region) is no longer read
+
+  if constexpr (!ONE) {
   for (int i = tid; i < R * k; i += kThreads) {
     const int v = p.sel[(size_t)b * R * k + i];
     s_sel[i] = (v >= 0 && v < g.MB) ? v : -1;
