@@ -143,19 +143,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Waits for tensor-memory loads into v.  The empty statement behind the wait takes the values
-// through, so that no use of them is scheduled ahead of it.
-template <int N>
-__device__ __forceinline__ void tmem_wait_ld_of(float (&v)[N]) {
-  tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < N; i += 16)
-    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]),
-                      "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]), "+f"(v[i + 8]), "+f"(v[i + 9]),
-                      "+f"(v[i + 10]), "+f"(v[i + 11]), "+f"(v[i + 12]), "+f"(v[i + 13]),
-                      "+f"(v[i + 14]), "+f"(v[i + 15]));
-}
-
 // How far (log2) a logit may exceed the base: fp16 weights reach 65504, and as long as
 // every weight is finite its relative precision does not depend on the base.
 constexpr float kHeadroom = 15.f;

@@ -425,7 +425,7 @@ sparse_prefill_kernel(Params p) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) z[16 * q4 + i] = v16[i];
     }
-    tmem_wait_ld();
+    tmem_wait_ld_of(z);
     float cmax = -INFINITY;   // log2 units
     if (member) {
       if (tok0 + kTok > nrow) {
@@ -482,7 +482,7 @@ sparse_prefill_kernel(Params p) {
       for (int q8 = 0; q8 < D / 16; ++q8) {
         float o16[16];
         tmem_ld16(tO + lane_off + 16 * q8, o16);
-        tmem_wait_ld();
+        tmem_wait_ld_of(o16);
 #pragma unroll
         for (int i = 0; i < 16; ++i) o16[i] *= alpha;
         tmem_st16(tO + lane_off + 16 * q8, o16);
@@ -530,7 +530,7 @@ sparse_prefill_kernel(Params p) {
       float o16[16];
       if (C > 0) {
         tmem_ld16(tO + lane_off + 16 * q8, o16);
-        tmem_wait_ld();
+        tmem_wait_ld_of(o16);
       }
       uint32_t h[8];
 #pragma unroll
@@ -1140,7 +1140,7 @@ sparse_prefill_ws_kernel(Params p) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[16 * q4 + i] = v16[i];
         }
-        tmem_wait_ld();
+        tmem_wait_ld_of(z);
       }
       tc_fence_before();
       ws_arrive(&sfree[tt * SB + c % SB]);   // S buffer loaded: S(c + SB) may overwrite it
@@ -1185,7 +1185,7 @@ sparse_prefill_ws_kernel(Params p) {
         for (int q8 = 0; q8 < D / 16; ++q8) {
           float o16[16];
           tmem_ld16(tO(tt) + lane_off + 16 * q8, o16);
-          tmem_wait_ld();
+          tmem_wait_ld_of(o16);
 #pragma unroll
           for (int i = 0; i < 16; ++i) o16[i] *= alpha;
           tmem_st16(tO(tt) + lane_off + 16 * q8, o16);
@@ -1243,7 +1243,7 @@ sparse_prefill_ws_kernel(Params p) {
       float o16[16];
       if (C > 0) {
         tmem_ld16(tO(tt) + lane_off + 16 * q8, o16);
-        tmem_wait_ld();
+        tmem_wait_ld_of(o16);
       }
       uint32_t h[8];
 #pragma unroll
