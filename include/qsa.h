@@ -583,7 +583,9 @@ qsa_status_t qsa_load_kv_tokens(const qsa_geom_t *geom, const int32_t *page_tabl
  * max(0, n - window)..n - 1 whose page is valid.
  *   z_t = sm_scale * q . K_t,  lse = ln(sum_t exp(z_t) [+ exp(sink)]),
  *   out = sum_t exp(z_t - lse) V_t
- * A row that sees no token gets out = 0 and lse = the sink, or -inf.  What the
+ * A row that sees no token gets out = 0 and lse = the sink, or -inf.  A row
+ * whose queries are not finite, or that sees keys that are not, gets no finite
+ * lse or out, and not -inf either; other rows are not touched by it.  What the
  * cache holds at positions that no row of the request sees is not looked at.
  * The work is divided evenly over the GPU by the requests' actual lengths and
  * joined by log-sum-exp in a fixed order: the same inputs give the same bits.

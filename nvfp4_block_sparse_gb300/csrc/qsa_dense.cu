@@ -162,7 +162,7 @@ __device__ __forceinline__ void join_parts(const Shape& sh, const Work& p, int b
     const size_t row = ((size_t)b * sh.g.R + j) * sh.g.Hq + head;
     float f = 1.f;
     if (p.sinks) add_sink(p.sinks[head], m, l, f);
-    const float r = l > 0.f ? f * p.v_scale / l : 0.f;
+    const float r = l == 0.f ? 0.f : f * p.v_scale / l;
     uint32_t w2[E / 2];
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) {
@@ -173,7 +173,7 @@ __device__ __forceinline__ void join_parts(const Shape& sh, const Work& p, int b
       *reinterpret_cast<uint2*>(p.out + row * D + lane * E) = make_uint2(w2[0], w2[1]);
     else
       *reinterpret_cast<uint4*>(p.out + row * D + lane * E) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-    if (lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -598,10 +598,10 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
           if (!QSA_IN_BOUNDS(b < g.B && j < g.R && head < g.Hq, kChkOut)) continue;
           float f = 1.f;
           if (p.sinks) add_sink(p.sinks[head], m[e], l[e], f);
-          const float r = l[e] > 0.f ? f * p.v_scale / l[e] : 0.f;
+          const float r = l[e] == 0.f ? 0.f : f * p.v_scale / l[e];
           *reinterpret_cast<__nv_bfloat162*>(p.out + row * D + d) =
               __floats2bfloat162_rn(acc[e] * r, acc[2 + e] * r);
-          if (d == 0) p.lse[row] = l[e] > 0.f ? (m[e] + log2f(l[e])) * kLn2 : -INFINITY;
+          if (d == 0) p.lse[row] = l[e] == 0.f ? -INFINITY : (m[e] + log2f(l[e])) * kLn2;
         } else {
           if (d == 0) {
             rec[c] = m[e];
@@ -683,12 +683,12 @@ dense_join_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   const size_t row = ((size_t)d.b * g.R + j) * g.Hq + head;
   float f = 1.f;
   if (p.sinks) add_sink(p.sinks[head], m, l, f);
-  const float r = l > 0.f ? f * p.v_scale / l : 0.f;
+  const float r = l == 0.f ? 0.f : f * p.v_scale / l;
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * r, acc.y * r);
   const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * r, acc.w * r);
   *reinterpret_cast<uint2*>(p.out + row * D + 4 * warp) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  if (warp == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (warp == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace

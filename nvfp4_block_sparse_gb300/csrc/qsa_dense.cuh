@@ -32,6 +32,8 @@ namespace dense {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// (A vector that sees nothing has a sum of exactly 0, and lse = -inf; a NaN in its queries or
+// keys makes its sum NaN, which out and lse pass on.)
 // The softmax base before a vector has seen a token: low enough for every
 // logit to move it, finite so that differences with -inf stay -inf.
 constexpr float kNoBase = -1e30f;

@@ -763,7 +763,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         l = l * f + exp2_approx(s2 - nm);
         m = nm;
       }
-      const float r = whole ? (l > 0.f ? f * p.v_scale / l : 0.f) : 1.f;
+      const float r = whole ? (l == 0.f ? 0.f : f * p.v_scale / l) : 1.f;
       float* rec = p.records + ((size_t)worker * 2 + (seg.begins ? 1 : 0)) * record_floats(sh.vt, D);
       const int at0 = (t * CG + rank) * 128 + 32 * (warp & 3);    // the warp's first vector
       const int left = min(32, seg.vecs - at0);                   // and how many it has
@@ -817,7 +817,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       }
       if (real) {
         if (whole) {
-          p.lse[orow] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         } else {
           rec[at] = m;
           rec[sh.vt + at] = l;
