@@ -583,6 +583,8 @@ qsa_status_t qsa_load_kv_tokens(const qsa_geom_t *geom, const int32_t *page_tabl
  * max(0, n - window)..n - 1 whose page is valid.
  *   z_t = sm_scale * q . K_t,  lse = ln(sum_t exp(z_t) [+ exp(sink)]),
  *   out = sum_t exp(z_t - lse) V_t
+ * The scales may be far apart: only the logits z_t themselves have to be finite
+ * in fp32.
  * A row that sees no token gets out = 0 and lse = the sink, or -inf.  A row
  * whose queries are not finite, or that sees keys that are not, gets no finite
  * lse or out, and not -inf either; other rows are not touched by it.  What the

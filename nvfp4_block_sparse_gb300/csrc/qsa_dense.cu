@@ -39,6 +39,7 @@
 #include "qsa_dense.cuh"
 
 #include <algorithm>
+#include <cmath>
 
 namespace qsa {
 namespace dense {
@@ -337,7 +338,6 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
       int sq = (amax > 0.f) ? 135 - ebits : 0;
       sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
       const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
-      const float down = __uint_as_float((uint32_t)(127 - sq) << 23);
       // dims d..d+3 are step s = (d % 32) / 4 of lane (c % 8, (d / 32) % 4), of the upper
       // eight steps past dim 128
 #pragma unroll
@@ -350,7 +350,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
       }
       if (lane == 0) {
         const int sees = real ? visible_tokens(L, g.R, j, cap) : 0;
-        s_cq[c] = real ? p.k_scale * p.sm_scale * kLog2e * down : 1.f;
+        s_cq[c] = real ? logit_factor(p, sq) : 1.f;
         s_n[c] = sees;
         s_lo[c] = first_seen(sees, sh.window);
       }
@@ -807,7 +807,8 @@ cudaError_t launch_dense(const Geom& g, const DenseArgs& a, cudaStream_t stream)
   dense::Work w = {};
   w.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
   w.k_pool = a.k_pool; w.k_sf = a.k_sf; w.v_pool = a.v_pool; w.v_sf = a.v_sf;
-  w.k_scale = a.k_scale; w.v_scale = a.v_scale; w.sm_scale = a.sm_scale;
+  w.v_scale = a.v_scale;
+  w.z_mant = (float)frexp((double)a.k_scale * a.sm_scale * 1.4426950408889634, &w.z_exp);
   w.page_table = a.page_table; w.seqlens = a.seqlens;
   w.sinks = a.sinks;
   w.out = reinterpret_cast<__nv_bfloat16*>(a.out);

@@ -63,7 +63,9 @@ struct Desc {
 struct Work {
   const __nv_bfloat16* q;
   const uint8_t *k_pool, *k_sf, *v_pool, *v_sf;
-  float k_scale, v_scale, sm_scale;
+  float v_scale;
+  float z_mant;      // k_scale sm_scale log2(e) = z_mant 2^z_exp, z_mant in [1/2, 1)
+  int z_exp;
   const int32_t *page_table, *seqlens;
   const float* sinks;
   __nv_bfloat16* out;
@@ -74,6 +76,15 @@ struct Work {
   float* records;    // [CTAs][2][vt * (2 + D)]: bases, sums, outputs ([vt][D], or of the tile
                      // kernel [D/4][vt][4])
 };
+
+// Factor from the products of a vector scaled by 2^sq to its log2 logits.  The scales may be
+// far apart in size, so their product and the power of two meet as exponents; kept a positive
+// normal number, so that a logit masked by -inf stays -inf (logits that small are all alike).
+__device__ __forceinline__ float logit_factor(const Work& w, int sq) {
+  const int e = min(max(w.z_exp - sq, -252), 252), half = e >> 1;
+  auto pow2 = [](int n) { return __uint_as_float((uint32_t)(n + 127) << 23); };
+  return fminf(fmaxf(w.z_mant * pow2(half) * pow2(e - half), 0x1p-126f), 0x1.fffffep127f);
+}
 
 __host__ __device__ __forceinline__ size_t record_floats(int vt, int D) {
   return (size_t)vt * (2 + D);

@@ -622,7 +622,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       int sq = (amax > 0.f) ? 135 - ebits : 0;
       sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
       const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
-      const float cq = p.k_scale * p.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 - sq) << 23);
+      const float cq = logit_factor(p, sq);
       auto half2_of = [&](uint32_t w) {
         return pack_half2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
       };

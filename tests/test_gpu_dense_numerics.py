@@ -1,6 +1,7 @@
 """GPU tests of dense attention's numbers where they can go wrong: contexts so
-long that a lost page hardly shows, and queries and values that are NaN or
-infinite.  The bounds are derived in dense_bounds.py."""
+long that a lost page hardly shows, scales whose product leaves fp32, and
+queries, keys and values that are NaN or infinite.  The bounds are derived in
+dense_bounds.py."""
 import numpy as np
 import pytest
 import torch
@@ -62,12 +63,42 @@ def test_long_contexts(qsa, name, L):
 
 
 def test_divided_and_whole_units_together(qsa):
-    # lengths from one token to 45728 in one call: some units are divided, some are not
+    # lengths from a row to 9000 tokens in one call: some units are divided, some are not
     for name in ("decode_8", "hd256_decode_16", "tile"):
         w = workload(name, 9000, batch=5)
         R = w["rows_per_req"]
         w["seqlens"] = torch.tensor([9000, R, 700, 4097, 8191], dtype=torch.int32, device="cuda")
         check(w, run(qsa, w))
+
+
+# (factor on k_scale, on sm_scale, on the queries): powers of two, so that nothing is rounded
+@pytest.mark.parametrize("factors", [(2.0**-100, 2.0**-20, 2.0**120), (2.0**-120, 1.0, 2.0**120),
+                                     (2.0**100, 2.0**10, 2.0**-110), (1.0, 2.0**-120, 2.0**120)])
+@pytest.mark.parametrize("name", ["decode_8", "hd256_decode_16", "tile", "tile_pair", "hd256_tile_pair"])
+def test_scales_far_apart_cancel(qsa, name, factors):
+    w = workload(name, 1111, invalid_frac=0.2)
+    q = w["q"].float()
+    w["q"] = torch.where(q.abs() < 2.0**-10, 0.0, q).to(torch.bfloat16)   # (stays normal when scaled)
+    a, b, c = factors
+    far = dict(w, k_scale=w["k_scale"] * a, sm_scale=w["sm_scale"] * b, q=(w["q"].double() * c).to(torch.bfloat16))
+    # The scales are fp32 arguments: k_scale 2^-120 lies below 2^-126, where fp32's steps are 2^-149,
+    # so the call sees its multiple of 2^-149, and that one times 2^120 is what it has to agree with.
+    w.update(k_scale=float(np.float32(far["k_scale"])) / a, sm_scale=float(np.float32(far["sm_scale"])) / b)
+    plain = run(qsa, w, 700)
+    assert torch.isfinite(far["q"]).all()
+    got = run(qsa, far, 700)
+    assert torch.equal(got.out, plain.out) and torch.equal(got.lse, plain.lse)
+
+
+@pytest.mark.parametrize("factors", [(1e-30, 1e-20, 1.0), (1e-38, 1e-38, 1.0), (1e-20, 1e-3, 1e-37)])
+@pytest.mark.parametrize("name", ["decode_8", "hd256_decode_16", "tile", "tile_pair", "hd256_tile_pair"])
+def test_logits_that_vanish(qsa, name, factors):
+    # every visible token counts alike; masked ones (ends, holes, the window) do not count
+    w = workload(name, 1111, invalid_frac=0.2)
+    a, b, c = factors
+    w.update(k_scale=a, sm_scale=b, q=(w["q"].double() * c).to(torch.bfloat16))
+    for window in (0, 700):
+        check(w, run(qsa, w, window), window, alike=True)
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
@@ -105,3 +136,17 @@ def test_values_that_are_not_finite(qsa, name):
     keep = torch.ones(w["head_dim"], dtype=torch.bool, device="cuda")
     keep[48:64] = False
     assert torch.equal(got.out[..., keep], clean.out[..., keep])
+
+
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_keys_that_are_not_finite(qsa, name):
+    # a NaN scale of a block of keys: no finite result for rows that see it, nothing for the others
+    w = workload(name, 1500, batch=2)
+    clean = run(qsa, w, 1000)
+    w["k_sf"][int(w["page_table"][1, 700 // w["page_size"]]), :, 700 % w["page_size"], 3] = 0x7F
+    got = run(qsa, w, 1000)
+    half = got.lse.shape[0] // 2
+    assert torch.equal(got.lse[:half], clean.lse[:half]) and torch.equal(got.out[:half], clean.out[:half])
+    assert torch.isnan(got.lse[half:]).all() and torch.isnan(got.out[half:]).all()
+    late = run(qsa, w, 100)                  # a window behind it
+    assert torch.isfinite(late.lse).all() and torch.isfinite(late.out).all()
