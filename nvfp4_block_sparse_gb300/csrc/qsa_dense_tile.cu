@@ -143,10 +143,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// How far (log2) a logit may exceed the base: fp16 weights reach 65504, and as long as
-// every weight is finite its relative precision does not depend on the base.
-constexpr float kHeadroom = 15.f;
-
 // Asynchronous copy of 16 bytes, zeros where `on` is false.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
@@ -706,7 +702,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         // been summed on the old one.
         const bool moves = top > base + kHeadroom;
         if (__any_sync(0xffffffffu, moves)) {
-          const float nb = moves ? top : base;
+          const float nb = moves ? top - kBelow : base;
           const float alpha = exp2_approx(base - nb);
           base = nb;
           sum.x *= alpha;

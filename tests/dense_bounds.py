@@ -9,8 +9,8 @@ logit, A the largest sum_d |q_d K_d| of a token (scales included):
   (2 dz + 2^-18) sum p |V|   logits: D / 16 steps of the matrix instruction and two more
                              roundings, dz = (D / 16 + 2) 2^-23 A; the exponent's fp32 argument
                              (up to 2^6: 2^-19) and its approximation
-  2^-35 e^(M - lse) sum |V|  weights below 2^-14 of the base's are subnormal, half a step of
-                             2^-24; the base lies 2^10 below the largest logit or lower
+  2^-33 e^(M - lse) sum |V|  weights below 2^-14 of the base's are subnormal, half a step of
+                             2^-24; the base lies 2^8 below the largest logit or lower
 and of lse  2 dz + 2^-17 + 2^-21 |lse|.
 """
 import numpy as np
@@ -60,7 +60,7 @@ def dense(w, window=0, sinks=None, q=None, alike=False):
                 weights = 2.0**-11 * mag if alike else 8 * 2.0**-11 * np.sqrt(p**2 @ vv**2)
                 tol[r, hs] = (2.0**-8 * np.abs(out[r, hs]) + weights
                               + (2 * dz + 2.0**-18)[:, None] * mag
-                              + 2.0**-35 * np.exp(top - lse[r, hs])[:, None] * vv.sum(0))
+                              + 2.0**-33 * np.exp(top - lse[r, hs])[:, None] * vv.sum(0))
                 lse_tol[r, hs] = 2 * dz + 2.0**-17 + 2.0**-21 * np.abs(lse[r, hs])
     return out, lse, tol, lse_tol
 

@@ -1,7 +1,7 @@
 """GPU tests of dense attention's numbers where they can go wrong: contexts so
-long that a lost page hardly shows, scales whose product leaves fp32, and
-queries, keys and values that are NaN or infinite.  The bounds are derived in
-dense_bounds.py."""
+long that a lost page hardly shows, rows whose weights span many powers of two,
+scales whose product leaves fp32, and queries, keys and values that are NaN or
+infinite.  The bounds are derived in dense_bounds.py."""
 import numpy as np
 import pytest
 import torch
@@ -69,6 +69,51 @@ def test_divided_and_whole_units_together(qsa):
         R = w["rows_per_req"]
         w["seqlens"] = torch.tensor([9000, R, 700, 4097, 8191], dtype=torch.int32, device="cuda")
         check(w, run(qsa, w))
+
+
+def dominated(name, gap, period, L=8256):
+    """Every period-th token, without values, is `gap` nats above the others, whose logits are
+    zero and whose values are all positive: the output is what the others add up to."""
+    w = workload(name, L)
+    w["k_pool"].zero_()
+    w["k_sf"].fill_(0x38)                 # 1
+    w["k_scale"], w["sm_scale"] = 1.0, 1 / 16
+    w["v_pool"].bitwise_and_(0x77)        # no sign
+    P = w["page_size"]
+    q = torch.zeros_like(w["q"])
+    q[..., :16] = 1.0
+    w["q"] = q
+    sf = torch.tensor(float(gap)).to(torch.float8_e4m3fn)
+    assert float(sf) == gap
+    for t in range(0, L, period):
+        page, slot = int(w["page_table"][0, t // P]), t % P
+        w["k_pool"][page, :, slot, :8] = 0x22            # sixteen ones
+        w["k_sf"][page, :, slot, 0] = int(sf.view(torch.uint8))
+        w["v_sf"][page, :, slot] = 0
+    return w
+
+
+@pytest.mark.parametrize("period", [32, 64, 8256])
+@pytest.mark.parametrize("gap", [8, 12, 14, 16])
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_weights_far_below_the_largest(qsa, name, gap, period):
+    w = dominated(name, gap, period)
+    check(w, run(qsa, w), alike=True)
+
+
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_weights_far_above_the_first(qsa, name):
+    # the other way round: the largest logits come last, after many small ones, and each step is
+    # one that a base with headroom does not follow at once
+    L = 4096
+    w = dominated(name, 1, 1, L)
+    P = w["page_size"]
+    w["v_sf"].copy_(workload(name, L)["v_sf"])
+    steps = [1, 2, 4, 8, 10, 12, 14, 16, 18, 20, 22, 24, 26, 28, 30, 32]
+    for t in range(L):
+        sf = torch.tensor(float(steps[t * len(steps) // L])).to(torch.float8_e4m3fn)
+        w["k_sf"][int(w["page_table"][0, t // P]), :, t % P, 0] = int(sf.view(torch.uint8))
+    check(w, run(qsa, w), alike=True)
 
 
 # (factor on k_scale, on sm_scale, on the queries): powers of two, so that nothing is rounded
