@@ -422,15 +422,17 @@ qsa_status_t qsa_sparse_prefill(const qsa_geom_t *geom, const void *q_bf16,
  *                        f_i within original_context - low) / (high - low),
  *                        clamped to [0, 1]
  * A positive attention_factor replaces the factor on cos and sin.  A plan
- * holds each frequency as a 64-bit fraction of a turn, so that the angle of
- * any 32-bit position is its product modulo one turn, exact to the plan's
- * 53-bit frequency.
+ * holds each frequency as a 64-bit fraction of a turn, right to its last bit,
+ * so that the angle of any 32-bit position is its product modulo one turn,
+ * within 2^-33 turns.
  *
  *   rotary_dim  16..256, a multiple of 16
  *   theta       > 1; factor > 0 (LINEAR, YARN, WAVELENGTH)
  *   original_context > 0, 0 < low < high (YARN, WAVELENGTH)
  *
- * Returns QSA_ERR_INVALID_ARG for null pointers and values outside these.
+ * Returns QSA_ERR_INVALID_ARG for null pointers, values outside these, scaled
+ * frequencies of 2^32 radians per position or more, and a factor on cos and sin
+ * that is zero or infinite in fp32; the plan is then left as it was.
  */
 #define QSA_ROPE_MAX_PAIRS 128
 

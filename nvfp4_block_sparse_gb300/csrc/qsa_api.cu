@@ -23,6 +23,59 @@ std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};
 
 bool positive(double x) { return x > 0.0 && isfinite(x); }
 
+// A number as the unevaluated sum of two doubles, about 100 bits: a rotation plan's frequencies
+// are multiplied by positions up to 2^31, so 53 bits would show in the angle.
+struct Two {
+  double hi, lo;
+};
+Two two_sum(double a, double b) {
+  const double s = a + b, v = s - a;
+  return {s, (a - (s - v)) + (b - v)};
+}
+Two joined(double a, double b) {   // |a| >= |b|
+  const double s = a + b;
+  return {s, b - (s - a)};
+}
+Two operator+(Two a, Two b) {
+  const Two s = two_sum(a.hi, b.hi), t = two_sum(a.lo, b.lo);
+  const Two u = joined(s.hi, s.lo + t.hi);
+  return joined(u.hi, u.lo + t.lo);
+}
+Two operator-(Two a, Two b) { return a + Two{-b.hi, -b.lo}; }
+Two operator*(Two a, Two b) {
+  const double p = a.hi * b.hi;
+  return joined(p, fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+Two operator/(Two a, Two b) {
+  const double q = a.hi / b.hi;
+  const Two r = a - b * Two{q, 0.0};
+  const double q2 = r.hi / b.hi;
+  const Two r2 = r - b * Two{q2, 0.0};
+  return joined(q, q2) + Two{r2.hi / b.hi, 0.0};
+}
+constexpr Two kTurnsPerRadian = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};   // 1 / (2 pi)
+
+// theta^(-1/n): the rounded one, improved by Newton's steps on theta r^n = 1.
+Two root(double theta, int n) {
+  Two r = {pow(theta, -1.0 / n), 0.0};
+  for (int step = 0; step < 2; ++step) {
+    Two p = {theta, 0.0};
+    for (int i = 0; i < n; ++i) p = p * r;
+    const Two d = Two{1.0, 0.0} - p;
+    r = r + Two{r.hi * (d.hi / n), 0.0};
+  }
+  return r;
+}
+
+// The fraction of a number of turns, in 2^-64 turns, to nearest.
+uint64_t turn_fraction(Two t) {
+  t = t - Two{floor(t.hi), 0.0};   // whole turns change nothing
+  if (t.hi < 0.0) t = t + Two{1.0, 0.0};
+  const double a = ldexp(t.hi, 64), whole = floor(a);
+  const double rest = floor((a - whole) + ldexp(t.lo, 64) + 0.5);
+  return (whole < 0x1p64 ? (uint64_t)whole : 0u) + (uint64_t)(int64_t)rest;
+}
+
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 // max_rows: 8 for the decode / verify attention and the rollback; the index
@@ -397,31 +450,35 @@ qsa_status_t qsa_rope_init(const qsa_rope_config_t* config, qsa_rope_t* rope) {
     last = fmin(ceil(per * log(c.original_context / (c.low * two_pi))), c.rotary_dim - 1.0);
     last = fmax(last, first + 1e-3);
   }
-  for (int i = 0; i < QSA_ROPE_MAX_PAIRS; ++i) {
-    if (i >= pairs) {
-      rope->turns[i] = 0;
-      continue;
-    }
-    double f = pow(c.theta, -2.0 * i / c.rotary_dim);
+  qsa_rope_t plan = {};
+  const Two one = {1.0, 0.0}, factor = {c.factor, 0.0}, r = root(c.theta, pairs);
+  Two plain = one;
+  for (int i = 0; i < pairs; ++i, plain = plain * r) {
+    Two f = plain;
     if (c.scaling == QSA_ROPE_LINEAR) {
-      f /= c.factor;
-    } else if (c.scaling == QSA_ROPE_YARN) {
-      const double m = fmin(fmax((i - first) / (last - first), 0.0), 1.0);
-      f = f * (1.0 - m) + f / c.factor * m;
-    } else if (c.scaling == QSA_ROPE_WAVELENGTH) {
-      const double turns = c.original_context * f / two_pi;
-      const double m = fmin(fmax((turns - c.low) / (c.high - c.low), 0.0), 1.0);
-      f = f * m + f / c.factor * (1.0 - m);
+      f = f / factor;
+    } else if (banded) {
+      Two m;   // the scaled frequency's share
+      if (c.scaling == QSA_ROPE_YARN) {
+        m = Two{i - first, 0.0} / Two{last - first, 0.0};
+      } else {
+        const Two turns = Two{c.original_context, 0.0} * f * kTurnsPerRadian;
+        m = one - (turns - Two{c.low, 0.0}) / two_sum(c.high, -c.low);
+      }
+      if (!(m.hi > 0.0)) m = {0.0, 0.0};
+      if (m.hi >= 1.0) m = one;
+      f = f * (one - m) + f / factor * m;
     }
-    double t = f / two_pi;
-    t -= floor(t);   // whole turns change nothing
-    rope->turns[i] = (uint64_t)ldexp(t, 64);
+    if (!(f.hi < 0x1p32)) return QSA_ERR_INVALID_ARG;
+    plan.turns[i] = turn_fraction(f * kTurnsPerRadian);
   }
   double amplitude = c.attention_factor;
   if (amplitude == 0.0)
     amplitude = c.scaling == QSA_ROPE_YARN && c.factor > 1.0 ? 0.1 * log(c.factor) + 1.0 : 1.0;
-  rope->amplitude = (float)amplitude;
-  rope->rotary_dim = c.rotary_dim;
+  plan.amplitude = (float)amplitude;
+  if (!positive(plan.amplitude)) return QSA_ERR_INVALID_ARG;
+  plan.rotary_dim = c.rotary_dim;
+  *rope = plan;
   return QSA_OK;
 }
 

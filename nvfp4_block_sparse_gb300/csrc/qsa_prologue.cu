@@ -25,9 +25,10 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Rotation rows.  A frequency is a 64-bit fraction of a turn, so pos * turns
-// modulo 2^64 is the angle as a fraction of a turn whatever the position; its
-// upper 32 bits, signed, lie in [-1/2, 1/2) turn and sincospif takes them
-// without a further reduction.  4 x 4096 rows of 32 pairs (4.2 MB): 5.3 us; 192 rows of 64
+// modulo 2^64 is the angle as a fraction of a turn whatever the position, and
+// sincospif takes it without a further reduction.  Errors: its one unit in the last place
+// (6e-8), the correction's and the amplitude's roundings (3e-8, 6e-8 amplitude), the bits
+// below 2^-32 turn (1e-9).  4 x 4096 rows of 32 pairs (4.2 MB): 5.3 us; 192 rows of 64
 // pairs: 1.8 us, a launch.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
@@ -43,10 +44,15 @@ rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
     const long long pos = positions ? positions[r]
                                     : (long long)seqlens[r / R] - R + (int)(r % R);
     const unsigned long long phase = (unsigned long long)pos * turns;
-    const float turn = (float)(int)(phase >> 32) * 0x1p-31f;   // half turns
+    // The upper 32 bits, signed, lie in [-1/2, 1/2) turn.  fp32 holds 24 of them; the others turn
+    // sine and cosine by less than 1e-7, to first order.
+    const int bits = (int)(phase >> 32);
+    const float top = (float)bits;
+    const float rest = (float)(bits - __float2int_rn(top)) * (3.14159265f * 0x1p-31f);
     float s, c;
-    sincospif(turn, &s, &c);
-    cs[r * pairs + threadIdx.x] = make_float2(c * rope.amplitude, s * rope.amplitude);
+    sincospif(top * 0x1p-31f, &s, &c);
+    cs[r * pairs + threadIdx.x] = make_float2(fmaf(-s, rest, c) * rope.amplitude,
+                                              fmaf(c, rest, s) * rope.amplitude);
   }
 }
 
