@@ -47,7 +47,7 @@ namespace {
 // Bounds-check codes (reported by bounds-checked builds only).
 [[maybe_unused]] constexpr int kChkChunk = 0x901;   // chunk: page id or token offset out of range
 [[maybe_unused]] constexpr int kChkOut = 0x902;     // output row out of range
-[[maybe_unused]] constexpr int kChkJoin = 0x903;    // descriptor out of range
+[[maybe_unused]] constexpr int kChkJoin = 0x903;    // descriptor, or the CTAs of a divided unit, out of range
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -160,6 +160,7 @@ __device__ __forceinline__ void join_parts(const Shape& sh, const Work& p, int b
     if (!on || way != 0) continue;
     const int j = row_of(sh, vec0 + c), head = kvh * sh.G + (vec0 + c) - j * sh.G;
     const size_t row = ((size_t)b * sh.g.R + j) * sh.g.Hq + head;
+    if (!QSA_IN_BOUNDS(b < sh.g.B && j < sh.g.R && head < sh.g.Hq, kChkOut)) continue;
     float f = 1.f;
     if (p.sinks) add_sink(p.sinks[head], m, l, f);
     const float r = l == 0.f ? 0.f : f * p.v_scale / l;
@@ -286,7 +287,9 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
     auto issue = [&](int k) {
       if ((k & 31) == 0 && k < mine) load_pages(k);
       const int page = __shfl_sync(0xffffffffu, pages, k & 31);
-      const bool ok = k < mine && page >= 0;
+      const bool ok = k < mine && page >= 0 &&
+                      QSA_IN_BOUNDS((((chunk0 + warp + k * W) * TOK) & (g.P - 1)) + TOK <= g.P &&
+                                        kvh < g.Hkv && b < g.B, kChkChunk);
       live = (live & ~(1u << (k & 31))) | ((uint32_t)ok << (k & 31));
       if (ok) {
         const int tok = (chunk0 + warp + k * W) * TOK;
@@ -616,7 +619,9 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
       const int first = cursor.first_cta(sh, span.share), last = cursor.last_cta(sh, seg, span.share);
       __threadfence();
       __syncthreads();
-      if (tid == 0) {
+      if (tid == 0 && !QSA_IN_BOUNDS(first >= 0 && first < last && last < sh.ctas, kChkJoin)) {
+        s_n[0] = 0;
+      } else if (tid == 0) {
         const int before = atomicAdd(&p.tickets[last], 1);
         s_n[0] = before == last - first;
         if (before == last - first) p.tickets[last] = 0;
@@ -680,6 +685,7 @@ dense_join_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   }
   const int j = row_of(sh, vec0 + c), head = d.kvh * sh.G + (vec0 + c) - j * sh.G;
   const size_t row = ((size_t)d.b * g.R + j) * g.Hq + head;
+  if (!QSA_IN_BOUNDS(j < g.R && head < g.Hq, kChkOut)) return;
   float f = 1.f;
   if (p.sinks) add_sink(p.sinks[head], m, l, f);
   const float r = l == 0.f ? 0.f : f * p.v_scale / l;

@@ -79,7 +79,9 @@ namespace {
 using namespace tc;
 
 // Bounds-check codes (reported by bounds-checked builds only).
+[[maybe_unused]] constexpr int kChkChunk = 0xA01;   // copy: token offset or place in the ring out of range
 [[maybe_unused]] constexpr int kChkOut = 0xA02;     // output row out of range
+[[maybe_unused]] constexpr int kChkRecord = 0xA03;  // record's slot out of range
 
 template <int D_, int CG_>
 struct TT {
@@ -312,7 +314,11 @@ __device__ __forceinline__ bool copy_all(const Shape& sh, const Work& p, const S
       const int here = __shfl_sync(0xffffffffu, ids, at & 31);
       const int page_later = __shfl_sync(0xffffffffu, later, at & 31);
       const int page = at < 32 ? here : page_later;
-      const bool there = mine && page >= 0 && page < sh.g.NP && tok < seg.n_all && tok + step > seg.lo_all;
+      const bool there =
+          mine && page >= 0 && page < sh.g.NP && tok < seg.n_all && tok + step > seg.lo_all &&
+          QSA_IN_BOUNDS(tok >= 0 && (tok & (sh.g.P - 1)) + step <= sh.g.P && slot < T::kDepth &&
+                            off + step <= rows && seg.kvh < sh.g.Hkv && seg.b < sh.g.B && at < 64,
+                        kChkChunk);
       const uint32_t which = __ballot_sync(0xffffffffu, there);
       const uint32_t sum = __reduce_add_sync(0xffffffffu, there ? bytes : 0u);
       if (use > 0 && gave_up(&empty[slot], use - 1)) { ok = false; break; }
@@ -761,6 +767,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       }
       const float r = whole ? (l == 0.f ? 0.f : f * p.v_scale / l) : 1.f;
       float* rec = p.records + ((size_t)worker * 2 + (seg.begins ? 1 : 0)) * record_floats(sh.vt, D);
+      const bool rec_ok = QSA_IN_BOUNDS(worker < sh.ctas && at < sh.vt, kChkRecord);
       const int at0 = (t * CG + rank) * 128 + 32 * (warp & 3);    // the warp's first vector
       const int left = min(32, seg.vecs - at0);                   // and how many it has
       if (!whole) {
@@ -771,7 +778,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           float o32[32];
           tmem_ld32(tO + d0, o32);
           tmem_wait_ld_of(o32);
-          if (real)
+          if (real && rec_ok)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               to[(size_t)(d0 / 4 + i) * sh.vt] =
@@ -813,8 +820,9 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       }
       if (real) {
         if (whole) {
-          p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        } else {
+          if (QSA_IN_BOUNDS(orow < (size_t)g.B * g.R * g.Hq, kChkOut))
+            p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        } else if (rec_ok) {
           rec[at] = m;
           rec[sh.vt + at] = l;
         }
