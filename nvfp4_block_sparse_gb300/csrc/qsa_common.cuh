@@ -280,6 +280,14 @@ cudaError_t launch_select_topk(const Geom& g, const int32_t* scores, const int32
                                int k, int window, int32_t* sel, int32_t* nsel, bool pdl,
                                cudaStream_t stream);
 
+// SMs of the current device (of a GB300 where there is none to ask).
+inline int sm_count() {
+  int dev = 0, sms = 152;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
 // The step's rotation rows, head norms with the rotation, and cache rows read
 // back (qsa_prologue.cu).  `rows` of q, k and v are row strides in elements.
 struct NormRope {

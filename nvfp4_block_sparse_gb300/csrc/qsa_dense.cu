@@ -703,13 +703,6 @@ dense_join_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
 // Host side
 // ---------------------------------------------------------------------------
 
-int dense_sms() {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 size_t dense_carve(const dense::Shape& s, void* workspace, dense::Work* w) {
   size_t off = 256;
   uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
@@ -719,7 +712,7 @@ size_t dense_carve(const dense::Shape& s, void* workspace, dense::Work* w) {
   }
   // (the same place for every geometry: a workspace may serve several, and tickets have to
   // be found at zero)
-  off += ((size_t)dense_sms() * sizeof(int) + 255) / 256 * 256;
+  off += ((size_t)sm_count() * sizeof(int) + 255) / 256 * 256;
   if (w) w->desc = reinterpret_cast<dense::Desc*>(base + off);
   off += ((size_t)dense::desc_count(s) * sizeof(dense::Desc) + 255) / 256 * 256;
   if (w) w->records = reinterpret_cast<float*>(base + off);
@@ -767,7 +760,7 @@ dense::Shape decode_shape(const Geom& g, int window) {
   // (16 warps: batched decode 27.9, 26.7, 25.3 and 25.8 us with 16, 32, 48 and 64, long
   // decode 61.3, 60.3, 59.0 and 57.6).
   s.lead = 7 * (g.D == 128 && s.vt == 8 ? C128a::W : C128b::W) / 2;
-  s.ctas = dense_sms();
+  s.ctas = sm_count();
   s.by_unit = dense::unit_count(s) <= s.ctas;
   return s;
 }

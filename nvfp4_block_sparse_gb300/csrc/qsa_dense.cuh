@@ -308,7 +308,6 @@ inline int desc_count(const Shape& s) { return s.by_unit ? (int)unit_count(s) : 
 // The tile kernel (qsa_dense_tile.cu): its units for this geometry, and its launch.
 dense::Shape dense_tile_shape(const Geom& g, int window);
 cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, cudaStream_t stream);
-int dense_sms();
 cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, cudaStream_t stream);
 // The workspace's parts: status word, descriptors, records.
 size_t dense_carve(const dense::Shape& s, void* workspace, dense::Work* w);

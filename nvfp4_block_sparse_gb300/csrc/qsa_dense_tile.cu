@@ -1004,7 +1004,7 @@ dense::Shape dense_tile_shape(const Geom& g, int window) {
     using T = decltype(t);
     s.vt = T::kVecs;
     s.tok_sh = T::kTok == 128 ? 7 : 6;
-    s.ctas = dense_sms() / T::CG;
+    s.ctas = sm_count() / T::CG;
   };
   dense::set_heads(&s, g);
   if (use_pairs(g)) {

@@ -494,7 +494,8 @@ cudaError_t launch_rope_rows(const Geom& g, const qsa_rope_t& rope, const int32_
   const dim3 block(pairs, 256 / pairs);
   const long long T = (long long)g.B * g.R;
   const long long ctas = (T + block.y - 1) / block.y;
-  return launch(rope_rows_kernel, dim3((unsigned)(ctas < 2432 ? ctas : 2432)), block, pdl, stream,
+  const long long most = 16 * sm_count();   // (what is resident takes turns)
+  return launch(rope_rows_kernel, dim3((unsigned)(ctas < most ? ctas : most)), block, pdl, stream,
                 g.R, T, rope, seqlens, positions, reinterpret_cast<float2*>(cs));
 }
 
@@ -518,7 +519,7 @@ cudaError_t launch_prologue(const Geom& g, const NormRope& nr, const PrologueArg
   // share the row's cos and sin and one square root (40 heads of 128: 64 rows 2.1 and 2.9 us
   // with one and four, 256 rows, 5120 single turns, 3.4 both, 512 rows 5.4 and 5.0, 2048 rows
   // 16.9 and 11.2).
-  const int steps = T * total / vpw > 152 * 40 ? 4 : 1, per = vpw * steps;
+  const int sms = sm_count(), steps = T * total / vpw > sms * 40 ? 4 : 1, per = vpw * steps;
   p.turns_q = a.q ? (g.Hq + per - 1) / per : 0;
   p.turns = p.turns_q + ((append ? 2 : 1) * g.Hkv + per - 1) / per;
   const long long items = T * p.turns;
@@ -526,7 +527,7 @@ cudaError_t launch_prologue(const Geom& g, const NormRope& nr, const PrologueArg
     auto* kern = steps == 4 ? prologue_kernel<D, kAppend, kInter, 4> : prologue_kernel<D, kAppend, kInter, 1>;
     // many rows: six CTAs per SM stay and take turns, or five of the append, which needs more
     // registers (two context chunks, norms: 40.4 us with six, 42.4 with five; append 58.1, 56.8)
-    const long long ctas = (items + kWarps - 1) / kWarps, most = (kAppend ? 5 : 6) * 152;
+    const long long ctas = (items + kWarps - 1) / kWarps, most = (kAppend ? 5 : 6) * sms;
     return launch(kern, dim3((unsigned)(steps == 4 && ctas > most ? most : ctas)), dim3(kWarps * 32),
                   pdl, stream, p);
   };
@@ -549,7 +550,7 @@ cudaError_t launch_load_tokens(const Geom& g, const int32_t* page_table, const i
   // Few rows: one per thread, for the shortest chain (192 rows of 4 heads: 4.1 us, 5.8 with
   // four); many: four, for more in flight (8188 rows of 2 heads at head_dim 256: 7.3 us, 10.7
   // with one).
-  const bool many = (long long)rows * g.Hkv > 152 * 16 * (long long)block.y;
+  const bool many = (long long)rows * g.Hkv > sm_count() * 16 * (long long)block.y;
   const unsigned per = block.y * (many ? 4 : 1);
   auto* kern = many ? (g.D == 256 ? load_tokens_kernel<256, 4> : load_tokens_kernel<128, 4>)
                     : (g.D == 256 ? load_tokens_kernel<256, 1> : load_tokens_kernel<128, 1>);
