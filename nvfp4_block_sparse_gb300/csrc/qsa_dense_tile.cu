@@ -97,7 +97,7 @@ struct TT {
   static constexpr int kThreads = 32 * (kMma + 4);
   // Registers per thread after the roles part (128 at launch): the softmax holds a
   // row's 128 logits.
-  static constexpr int kSoftRegs = kTiles == 2 ? 192 : 192;
+  static constexpr int kSoftRegs = 192;
   static constexpr int kDeqRegs = kTiles == 2 ? 72 : 96;
   static constexpr int kMmaRegs = kTiles == 2 ? 56 : 72;
   static_assert(32 * (kSoft * kSoftRegs + kDeq * kDeqRegs + 4 * kMmaRegs) <= kThreads * 128 &&
@@ -887,7 +887,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       ++parts;
       tc_fence_after();
       const int C = seg.todo;
-      auto chunk_s = [&](int c) {   // S of chunk c (head_dim 256), of both tiles' turns below
+      auto chunk_s = [&](int c) {   // waits for K of chunk c
         const int n = s_done + c, x = n & 1;
         if (gave_up(&kready[x], n >> 1)) return false;
         tc_fence_after();
