@@ -89,3 +89,71 @@ def test_queries_of_the_launch_before(qsa, geometry, prologue, attention):
     torch.cuda.synchronize()
     for i in range(40):
         assert torch.equal(got[i], out[i % 2]) and torch.equal(got_lse[i], lse[i % 2]), i
+
+
+def alternate(write, read, results):
+    """write(i) and read(out) by turns, i = 0, 1, 0, ..: 30 times without a synchronise, compared
+    with what a synchronise between the two gives."""
+    want = []
+    for i in range(2):
+        write(i)
+        torch.cuda.synchronize()
+        out = results()
+        read(out)
+        torch.cuda.synchronize()
+        want.append(out)
+    assert not torch.equal(want[0][0], want[1][0])
+    got = [results() for _ in range(30)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        write(i % 2)
+        read(out)
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        for a, b in zip(out, want[i % 2]):
+            assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("rows", [1, 3, 12, 70])
+@pytest.mark.parametrize("geometry", sorted(GEOMS))
+def test_a_dense_step_back_to_back(qsa, geometry, rows):
+    # rotation rows -> norms, rotation and append -> dense attention, and the rows read back, each
+    # directly behind the one that writes what it reads
+    case = qw.Case(name="order", seed=62, batch=8, rows_per_req=rows, ctx_lo=300, ctx_hi=700, k=6,
+                   window=2, **GEOMS[geometry])
+    w = qw.make_workload(case, "cuda")
+    step = qsa.DenseStep(qw.geometry(w))
+    T, Hq, Hkv, D = 8 * rows, w["num_q_heads"], w["num_kv_heads"], w["head_dim"]
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    news = []
+    for _ in range(2):
+        x = torch.randn(T, Hq + 2 * Hkv, D, generator=gen, device="cuda").to(torch.bfloat16)
+        news.append(dict(q=x[:, :Hq], k=x[:, Hq:Hq + Hkv], v=x[:, Hq + Hkv:], q_weight=None, k_weight=None,
+                         ik_new=torch.randint(-127, 128, (T, 64), generator=gen, device="cuda").to(torch.int8)))
+    ropes = [qsa.make_rope(rotary_dim=64, theta=t) for t in (1e4, 1e6)]
+    nr = qsa.make_norm_rope(64)
+    cs = torch.empty(T, 32, 2, device="cuda")
+
+    def write(i):
+        qsa.qsa_rope_rows(step.cg, ropes[i], w["seqlens"], cs)
+        step.store(w, news[i], nr, cs)
+
+    def read(out):
+        step.run(w, q=step.q, out=out[0], lse=out[1])
+        qsa.qsa_load_kv_tokens(step.cg, w["page_table"], w["seqlens"], w["k_pool"], w["k_sf"], w["v_pool"],
+                               w["v_sf"], w["k_scale"], w["v_scale"], out[2], out[3])
+
+    def read_back_first(out):
+        qsa.qsa_load_kv_tokens(step.cg, w["page_table"], w["seqlens"], w["k_pool"], w["k_sf"], w["v_pool"],
+                               w["v_sf"], w["k_scale"], w["v_scale"], out[2], out[3])
+        step.run(w, q=step.q, out=out[0], lse=out[1])
+
+    def results():
+        return [torch.zeros(T, Hq, D, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(T, Hq, device="cuda"),
+                torch.zeros(T, Hkv, D, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(T, Hkv, D, dtype=torch.bfloat16, device="cuda")]
+
+    alternate(write, read, results)
+    alternate(write, read_back_first, results)
+    assert step.status() == 0
