@@ -309,13 +309,14 @@ __device__ __forceinline__ void attend_cta(const Params& p, int s, int kvh, int 
   // norm and rotation kernel writes: both are read behind this wait only.
   wait_before_list();
 
-  // The warp's columns of the queries (one warp per column, four dims per lane): on
-  // their way while the chunk list is built, used once the copies have been issued.
+  // The warp's columns of the queries (one warp per column, four dims per lane), on their
+  // way while warp 0 builds the chunk list; the last warps have the first columns, so that
+  // warp 0 has none where there are fewer columns than warps.
   constexpr int kQPerWarp = (kCols + NG * kGW - 1) / (NG * kGW);
   uint2 raw[kQPerWarp];
 #pragma unroll
   for (int i = 0; i < kQPerWarp; ++i) {
-    const int c = warp + i * NG * kGW;
+    const int c = NG * kGW - 1 - warp + i * NG * kGW;
     const int j = c / hs, hh = c - (c / hs) * hs;
     raw[i] = make_uint2(0u, 0u);
     if (c < kCols && j < R && hh < hreal)
@@ -359,6 +360,38 @@ __device__ __forceinline__ void attend_cta(const Params& p, int s, int kvh, int 
     }
     if (lane == 0) misc[0] = min(cnt, p.list_cap);
   }
+
+  // Queries -> fp16 pre-scaled by a power of two per column (|q|max into
+  // [256, 512): exact, and any bf16 magnitude stays inside fp16 range).
+#pragma unroll
+  for (int i = 0; i < kQPerWarp; ++i) {
+    const int c = NG * kGW - 1 - warp + i * NG * kGW;
+    if (c >= kCols) break;
+    const int j = c / hs, hh = c - (c / hs) * hs;
+    const bool real = j < R && hh < hreal;
+    const __nv_bfloat162 lo = *reinterpret_cast<const __nv_bfloat162*>(&raw[i].x);
+    const __nv_bfloat162 hi = *reinterpret_cast<const __nv_bfloat162*>(&raw[i].y);
+    const float v0 = __low2float(lo), v1 = __high2float(lo);
+    const float v2 = __low2float(hi), v3 = __high2float(hi);
+    float amax = fmaxf(fmaxf(fabsf(v0), fabsf(v1)), fmaxf(fabsf(v2), fabsf(v3)));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
+    int sq = (amax > 0.f) ? 135 - ebits : 0;
+    sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
+    const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
+    const float down = __uint_as_float((uint32_t)(127 - sq) << 23);
+    // 16-byte unit j = lane / 2 of the row sits at qunit(c, j) (a swizzle
+    // that spreads the fragment reads below over all banks).
+    __half2* dst = reinterpret_cast<__half2*>(qs + c * kD + 8 * qunit(c, lane >> 1) + 4 * (lane & 1));
+    dst[0] = __floats2half2_rn(v0 * up, v1 * up);
+    dst[1] = __floats2half2_rn(v2 * up, v3 * up);
+    if (lane == 0) {
+      col_cq[c] = real ? p.k_scale * p.sm_scale * kLog2e * down : 0.f;
+      col_n[c] = real ? visible_tokens(Lb, R, j, cap) : 0;
+      col_row[c] = real ? j : -1;
+    }
+  }
   __syncthreads();
   const int nch = misc[0];
   after_list();
@@ -393,39 +426,6 @@ __device__ __forceinline__ void attend_cta(const Params& p, int s, int kvh, int 
     fence_proxy_async_smem();   // after the union's scratch in the stage region
     issue(grp + NG * lane);
   }
-
-  // Queries -> fp16 pre-scaled by a power of two per column (|q|max into
-  // [256, 512): exact, and any bf16 magnitude stays inside fp16 range).
-#pragma unroll
-  for (int i = 0; i < kQPerWarp; ++i) {
-    const int c = warp + i * NG * kGW;
-    if (kCols % (NG * kGW) != 0 && c >= kCols) break;
-    const int j = c / hs, hh = c - (c / hs) * hs;
-    const bool real = j < R && hh < hreal;
-    const __nv_bfloat162 lo = *reinterpret_cast<const __nv_bfloat162*>(&raw[i].x);
-    const __nv_bfloat162 hi = *reinterpret_cast<const __nv_bfloat162*>(&raw[i].y);
-    const float v0 = __low2float(lo), v1 = __high2float(lo);
-    const float v2 = __low2float(hi), v3 = __high2float(hi);
-    float amax = fmaxf(fmaxf(fabsf(v0), fabsf(v1)), fmaxf(fabsf(v2), fabsf(v3)));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const int ebits = (int)((__float_as_uint(amax) >> 23) & 0xFF);
-    int sq = (amax > 0.f) ? 135 - ebits : 0;
-    sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
-    const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
-    const float down = __uint_as_float((uint32_t)(127 - sq) << 23);
-    // 16-byte unit j = lane / 2 of the row sits at qunit(c, j) (a swizzle
-    // that spreads the fragment reads below over all banks).
-    __half2* dst = reinterpret_cast<__half2*>(qs + c * kD + 8 * qunit(c, lane >> 1) + 4 * (lane & 1));
-    dst[0] = __floats2half2_rn(v0 * up, v1 * up);
-    dst[1] = __floats2half2_rn(v2 * up, v3 * up);
-    if (lane == 0) {
-      col_cq[c] = real ? p.k_scale * p.sm_scale * kLog2e * down : 0.f;
-      col_n[c] = real ? visible_tokens(Lb, R, j, cap) : 0;
-      col_row[c] = real ? j : -1;
-    }
-  }
-  __syncthreads();
 
   // ---- per-column state and fragments --------------------------------------
   // Per lane column: cq, and the row (low 4 bits, 15 = padding) with the
