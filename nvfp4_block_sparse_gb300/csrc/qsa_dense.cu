@@ -29,12 +29,15 @@
 // The base of a vector moves only when a logit comes near fp16's end above it (kHeadroom);
 // sums are fp32 per lane and joined at the end.
 //
-// Measured (GB300): 4 requests of 131072 tokens, 32 heads on 4 of 128 (302 MB): 59 us,
-// 5.1 TB/s (0.77 of the measured copy rate); 8 requests of 9000 to 32768 (92 MB): 25.4 us,
-// 3.6 TB/s; one row over 4096 tokens: 9.9 us.  Within the loop over chunks the copies
-// run at 0.95 of the copy rate; the rest is each part's start (division of the
-// work, lookup, first pages: 3 us), the join of the warps' states (1.5 us) and of a
-// divided unit's records (1 to 4 us), and the launch.
+// Measured (GB300): 4 requests of 131072 tokens, 32 heads on 4 of 128 (302 MB): 58.4 us,
+// 5.2 TB/s (0.77 of the measured copy rate); 8 requests of 9000 to 32768 (92 MB): 27.2 us,
+// 3.4 TB/s; one row over 4096 tokens: 9.7 us.  In the loop over chunks the copies run at
+// 0.95 of the copy rate in the long case and 0.89 in the batched one; the rest is each part's
+// start (division of the work 0.7 us, lookup and first pages 1.4 to 2.9), the join of the
+// warps' states (1.3) and of a divided unit's records (1.3, to 5 in the CTA that joins), and
+// the launch.  The other shapes (8 requests of 16384 tokens, 75 MB, floor 11.3 us): 16 vectors
+// on 4 KV heads of 128 30.0 us, 8 on 2 of 256 24.1, 12 on 2 of 256 33.9 (a second tile of eight
+// columns with half its products unused); 4 requests of 131072 tokens, 12 on 2 of 256, 81.5 us.
 #include "qsa_dense.cuh"
 
 #include <algorithm>
@@ -758,7 +761,9 @@ dense::Shape decode_shape(const Geom& g, int window) {
   s.least = 16;   // a chunk per warp (one row over 4096 tokens: 9.8, 9.7, 11.1 us with 8, 16, 32)
   // A part's start and end take what a CTA's warps take for three and a half chunks each
   // (16 warps: batched decode 27.9, 26.7, 25.3 and 25.8 us with 16, 32, 48 and 64, long
-  // decode 61.3, 60.3, 59.0 and 57.6).
+  // decode 61.3, 60.3, 59.0 and 57.6; 8 warps, 12 vectors of 256: 8 requests of up to 32768
+  // tokens 44.8, 43.4, 42.0, 39.4, 39.9, 40.1 with 8, 12, 20, 28, 36 and 52, 4 of 131072 79.9,
+  // 85.1, 82.2, 81.5, 80.7, 81.0; 16 vectors of 128: 32.4, 32.1, 30.7, 30.1, 30.7, 31.5).
   s.lead = 7 * (g.D == 128 && s.vt == 8 ? C128a::W : C128b::W) / 2;
   s.ctas = sm_count();
   s.by_unit = dense::unit_count(s) <= s.ctas;
@@ -788,8 +793,11 @@ cudaError_t launch_decode(const dense::Shape& s, const dense::Work& w, cudaStrea
 
 // The tile kernel (128 to 512 query vectors per unit on tcgen05) takes more query vectors per
 // KV head than one unit of the decode kernel's: with two units the cache is dequantised twice
-// (16 requests of 16384 tokens, 32 vectors: 76 us against 74 us at head_dim 128, 64 against 77 at
-// 256; 48 vectors: 77 against 106 and 65 against 108).
+// (16 requests of 16384 tokens, 32 vectors, tiles and two units: 64 us and 78 at head_dim 256;
+// 48 vectors in three units 77 and 108 at 128, 65 and 108 at 256).  At head_dim 128 two units
+// and tiles are alike up to 32 vectors: 76.8 us and 75.8 for that batch, 197.6 and 198.7 for 48
+// requests, 57.5 and 61.0 for 64 of 2048 tokens, 25.3 and 27.8 for 32 in windows of 1024, but 17.4
+// and 14.3 for two of 4096, 54.7 and 47.0 for one of 131072.  One rule for both head dims.
 static bool use_tiles(const Geom& g) { return g.R * (g.Hq / g.Hkv) > 16; }
 
 static dense::Shape dense_shape(const Geom& g, int window) {

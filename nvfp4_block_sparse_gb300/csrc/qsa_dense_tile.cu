@@ -24,15 +24,19 @@
 // have one tile, for which the cache's bytes, not the products, are the floor.
 //
 // Measured (GB300, SM clock 2070 MHz):
-//   two context chunks of 1024 rows, 32 heads on 4, behind 30000 tokens: 638 us,
-//   1.62 PFLOP/s (0.82 of the measured cuBLAS rate).  The tensor pipe is active
-//   71 % of the time; a chunk's turn takes 2900 cycles of the 2460 that its MMAs
-//   need, the rest is the softmax's latency between a tile's turns.
-//   32 requests x 4 verify rows, 24 heads on 2, head_dim 256, window 4096: 43 us
-//   for 79 MB (floor 11.8).  Each SM has 21 chunks of 64 tokens, 2000 cycles each
-//   (the K warps' conversion), a start of 8 us (work division, queries, the first
-//   pages; mostly instructions fetched for the first time) and an end of 6 us
-//   (records, the join).
+//   two context chunks of 1024 rows, 32 heads on 4, behind 30000 tokens: 638 to 650 us,
+//   1.6 PFLOP/s (0.81 of the measured cuBLAS rate).  The tensor pipe is active
+//   70 % of the time: a chunk's turn takes 2940 cycles of which its MMAs need 2048,
+//   the rest is the softmax's latency between a tile's turns.
+//   The same at 24 heads on 2 of 256: 964 us, 1.68 PFLOP/s (0.85); 4 x 256 rows of
+//   these over 16384 tokens 270 us (floor 208).
+//   32 requests x 4 verify rows, 24 heads on 2, head_dim 256, window 4096: 44 us
+//   for 79 MB (floor 11.8).  A CTA has 30 chunks of 64 tokens, 1780 cycles each (the K
+//   warps' conversion, shared memory; the MMAs need 1024, 80 of the tile's 128 rows hold
+//   no vector), a start of 5.6 us (work division 0.7,
+//   queries 4.3, first pages and S 0.6), a record (1.2 us), and the join kernel with its
+//   launch (9 us).  16 requests x 4 rows of 32 heads on 4 of 128 over 16384 tokens: 77 us
+//   for 151 MB (floor 22.6).
 //
 // Roles in a CTA (a warp group each unless noted):
 //   softmax   a thread per vector (tensor-memory lane): its row of S to registers, base

@@ -28,8 +28,10 @@ namespace {
 // modulo 2^64 is the angle as a fraction of a turn whatever the position, and
 // sincospif takes it without a further reduction.  Errors: its one unit in the last place
 // (6e-8), the correction's and the amplitude's roundings (3e-8, 6e-8 amplitude), the bits
-// below 2^-32 turn (1e-9).  4 x 4096 rows of 32 pairs (4.2 MB): 5.3 us; 192 rows of 64
-// pairs: 1.8 us, a launch.
+// below 2^-32 turn (1e-9).  4 x 4096 rows of 32 pairs (4.2 MB): 5.1 us, bound by the
+// lanes' reads of their frequencies from the parameters, which are served an address at a time
+// (that unit is 84 % busy; instructions would issue in 2.4 us); 192 rows of 64 pairs: 1.5 us,
+// a launch.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
 rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
@@ -68,9 +70,9 @@ rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
 // shuffle over rotary_dim / 16 lanes (rotary_dim is a multiple of 16, so a
 // lane's eight elements have one partner lane); interleaved pairs are in the lane.
 //
-// Measured (GB300): norms and rotation of 8192 rows of 24 + 2 heads of 256 (220 MB) 40.2 us,
-// 5.5 TB/s (0.82 of the measured copy rate), instructions issued in 60 % of the cycles: about
-// 100 per head and warp.  The append of 8188 such rows with their values (223 MB) 47 us:
+// Measured (GB300): norms and rotation of 8192 rows of 24 + 2 heads of 256 (220 MB) 39.8 us,
+// 5.5 TB/s (0.83 of the measured copy rate), instructions issued in 61 % of the cycles: about
+// 100 per head and warp.  The append of 8188 such rows with their values (223 MB) 47.8 us:
 // its keys and values take four times the instructions of a query; see the quantiser below
 // for what its divisions cost.  Steps (8192 rows): a turn per kind 77 us, next turn requested
 // ahead 63.5, four square roots as one 51.7, packed arithmetic 42.
@@ -413,7 +415,9 @@ prologue_kernel(const __grid_constant__ KernelArgs p) {
 // ---------------------------------------------------------------------------
 // Cache rows read back: eight elements (4 code bytes, one scale) of a key and of its
 // value per lane, for ROWS rows at once: three loads depend on one another (length, page,
-// codes), so what is in flight decides.  A CTA has neighbouring rows of one head, which
+// codes), so what is in flight decides: waiting for loads is
+// its largest stall, 3.2 cycles an instruction (16 code bytes a lane would be fewer and wider
+// loads).  A CTA has neighbouring rows of one head, which
 // are neighbours in their page.
 // ---------------------------------------------------------------------------
 template <int D, int ROWS>
