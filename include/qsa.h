@@ -585,8 +585,9 @@ qsa_status_t qsa_load_kv_tokens(const qsa_geom_t *geom, const int32_t *page_tabl
  * max(0, n - window)..n - 1 whose page is valid.
  *   z_t = sm_scale * q . K_t,  lse = ln(sum_t exp(z_t) [+ exp(sink)]),
  *   out = sum_t exp(z_t - lse) V_t
- * The scales may be far apart: only the logits z_t themselves have to be finite
- * in fp32.  Logits, sums and outputs are fp32; query elements below 2^-26 of
+ * The scales may be far apart: only the logits z_t themselves count.  They are
+ * fp32, so beyond 2^20 in magnitude weights are as coarse as their steps, and
+ * beyond 2^24 nothing is left of them.  Logits, sums and outputs are fp32; query elements below 2^-26 of
  * their row's largest are rounded to steps of 2^-32 of it; weights exp(z_t - lse)
  * are rounded to 11 bits before the product with V, those below 2^-22 of the
  * row's largest to steps of 2^-32 of it.

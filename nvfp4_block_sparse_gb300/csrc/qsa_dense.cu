@@ -494,7 +494,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
               const float p1 = exp2_approx(fmaf(z[m][t][2 * hf + 1], cq[t][1], -base[t][1]));
               sum[t][0] += p0;
               sum[t][1] += p1;
-              pb[t][hf] = movmatrix_trans(pack_half2(p0, p1));
+              pb[t][hf] = movmatrix_trans(pack_weights(p0, p1));
             }
           uint32_t lo2[2][D / 64], hi2[2][D / 64], sc[2][D / 128];
 #pragma unroll

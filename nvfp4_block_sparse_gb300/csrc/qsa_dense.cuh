@@ -47,6 +47,15 @@ constexpr float kNoBase = -1e30f;
 constexpr float kHeadroom = 15.9f;
 constexpr float kBelow = 8.f;
 
+// Two weights as fp16.  Their exponents' arguments are a logit's exact product less a rounded
+// base, off by the base's fp32 step: with logits of 2^20 and more a weight just inside the
+// headroom would pass 65504, and stays there instead.
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 struct Shape {
   Geom g;
   int G;         // query heads per KV head

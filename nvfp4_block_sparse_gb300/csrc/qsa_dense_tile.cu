@@ -745,7 +745,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
               const float2 a = fma2(make_float2(z[k], z[k + 1]), c2, b2);
               const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
               sum = add2(sum, e);
-              pk[i] = pack_half2(e.x, e.y);
+              pk[i] = pack_weights(e.x, e.y);
             }
             tmem_st16u(tS + 64 * h + 16 * q, pk);
           }

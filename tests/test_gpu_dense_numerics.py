@@ -195,3 +195,34 @@ def test_keys_that_are_not_finite(qsa, name):
     assert torch.isnan(got.lse[half:]).all() and torch.isnan(got.out[half:]).all()
     late = run(qsa, w, 100)                  # a window behind it
     assert torch.isfinite(late.lse).all() and torch.isfinite(late.out).all()
+
+
+@pytest.mark.parametrize("size", [2.0**17, 2.0**19, 2.0**21, 2.0**23])
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_logits_large_in_magnitude(qsa, name, size):
+    # all logits near `size`, whose fp32 steps the exponents' arguments inherit: weights near fp16's
+    # end must not pass it.  Every token's logit is the row's offset plus 0 to 14.
+    L = 8000
+    w = workload(name, L)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    w["k_pool"].zero_()
+    w["k_pool"][..., :16] = 0x22                                    # thirty-two ones
+    w["k_sf"].fill_(0x38)                                           # 1
+    level = torch.rand(w["k_sf"].shape[:3], generator=gen, device="cuda") * torch.rand(
+        (w["num_pages"], 1, 1), generator=gen, device="cuda") * 448
+    w["k_sf"][..., 1] = level.to(torch.float8_e4m3fn).view(torch.uint8)
+    w["k_scale"], w["sm_scale"] = 1.0, 1 / 16
+    q = torch.zeros_like(w["q"], dtype=torch.float32)
+    rows = q.view(-1, w["head_dim"])
+    rows[:, :16] = size * (1 + torch.arange(rows.shape[0], device="cuda")[:, None] / 128)
+    rows[:, 16:32] = 2.0**-5
+    w["q"] = q.to(torch.bfloat16)
+    step = run(qsa, w)
+    out, lse, _, _ = dense_bounds.dense(cr.host(w))
+    # the products' sums in steps of 2^-23 of up to 4 size, D / 16 of them, two roundings more
+    dz = (w["head_dim"] / 16 + 2) * 2.0**-23 * 4 * size
+    got = step.lse.cpu().numpy()
+    assert np.isfinite(got).all() and np.abs(got - lse).max() <= dz + 2.0**-18 * size
+    values = cr.values(w["v_pool"].cpu().numpy(), w["v_sf"].cpu().numpy()) * w["v_scale"]
+    got = step.out.float().cpu().numpy()
+    assert np.isfinite(got).all() and np.abs(got).max() <= 1.01 * np.abs(values).max()
