@@ -587,10 +587,10 @@ qsa_status_t qsa_load_kv_tokens(const qsa_geom_t *geom, const int32_t *page_tabl
  *   out = sum_t exp(z_t - lse) V_t
  * The scales may be far apart: only the logits z_t themselves count.  They are
  * fp32, so beyond 2^20 in magnitude weights are as coarse as their steps, and
- * beyond 2^24 nothing is left of them.  Logits, sums and outputs are fp32; query elements below 2^-26 of
- * their row's largest are rounded to steps of 2^-32 of it; weights exp(z_t - lse)
- * are rounded to 11 bits before the product with V, those below 2^-22 of the
- * row's largest to steps of 2^-32 of it.
+ * beyond 2^24 nothing is left of them.  Logits, sums and outputs are fp32;
+ * query elements below 2^-26 of their row's largest are rounded to steps of
+ * 2^-32 of it; weights exp(z_t - lse) are rounded to 11 bits before the product
+ * with V, those below 2^-22 of the row's largest to steps of 2^-32 of it.
  * A row that sees no token gets out = 0 and lse = the sink, or -inf.  A row
  * whose queries are not finite, or that sees keys that are not, gets no finite
  * lse or out, and not -inf either; other rows are not touched by it.  What the
