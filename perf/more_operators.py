@@ -45,29 +45,29 @@ def _prompt(name, B, lo, hi, Hq, Hkv, D, window=0, sinks=False, spare=0):
 def listed():
     return [
         # the angles of a decode batch of image conversations, axes interleaved: latency
-        _axes("axes rows, decode", 64, "24,20,20", "interleaved", 131072),
+        _axes("axes rows: decode", 64, "24,20,20", "interleaved", 131072),
         # the angles of packed prompts with images, a section of the head per axis
-        _axes("axes rows, prompts", 16384, "16,24,24", "sections", 32768),
+        _axes("axes rows: prompts", 16384, "16,24,24", "sections", 32768),
         # a speculative step's rows appended behind partly filled blocks, and read back
-        _cache("cache, verify step", 48, 4, 4, 4, 128, 64, 32768, False),
+        _cache("cache: verify step", 48, 4, 4, 4, 128, 64, 32768, False),
         # packed prompts of different lengths written behind short prefixes, and read back
-        _cache("cache, prompts", 6, 700, 2047, 2, 256, 32, 300, True),
+        _cache("cache: prompts", 6, 700, 2047, 2, 256, 32, 300, True),
         # a single request's decode row: latency
-        _dense("dense, tiny decode", 1, 1, 8, 1, 128, 64, 4096, 4096),
+        _dense("dense: tiny decode", 1, 1, 8, 1, 128, 64, 4096, 4096),
         # a decode batch of mixed lengths, some pages missing
-        _dense("dense, batched decode", 8, 1, 32, 4, 128, 64, 9000, 32768, holes=True),
+        _dense("dense: batched decode", 8, 1, 32, 4, 128, 64, 9000, 32768, holes=True),
         # a speculative step at head_dim 256 on a sliding-window layer with sinks
-        _dense("dense, windowed verify", 32, 4, 24, 2, 256, 32, 8192, 16384, window=4096, sinks=True),
+        _dense("dense: windowed verify", 32, 4, 24, 2, 256, 32, 8192, 16384, window=4096, sinks=True),
         # context chunks of two requests behind long prefixes
-        _dense("dense, context", 2, 512, 32, 4, 128, 64, 14000, 16384),
+        _dense("dense: context", 2, 512, 32, 4, 128, 64, 14000, 16384),
         # one short prompt: latency
-        _prompt("prompt, short", 1, 77, 77, 8, 1, 128),
+        _prompt("prompt: short", 1, 77, 77, 8, 1, 128),
         # packed prompts of odd lengths at head_dim 256, rows to spare behind the last
-        _prompt("prompt, ragged", 6, 100, 2047, 24, 2, 256, spare=50),
+        _prompt("prompt: ragged", 6, 100, 2047, 24, 2, 256, spare=50),
         # packed prompts on a sliding-window layer with sinks
-        _prompt("prompt, windowed", 4, 3000, 4096, 32, 4, 128, window=1024, sinks=True),
+        _prompt("prompt: windowed", 4, 3000, 4096, 32, 4, 128, window=1024, sinks=True),
         # the large one: a long prompt
-        _prompt("prompt, long", 1, 8192, 8192, 32, 4, 128),
+        _prompt("prompt: long", 1, 8192, 8192, 32, 4, 128),
     ]
 
 
