@@ -480,6 +480,61 @@ qsa_status_t qsa_rope_rows(const qsa_geom_t *geom, const qsa_rope_t *rope,
                            float *cs, cudaStream_t stream);
 
 /*
+ * Rotary positions with several axes (time, height and width of images and
+ * video): every frequency turns by the position on its own axis.
+ *
+ * qsa_rope_axes_init (host only; launches nothing) turns a configuration, as of
+ * qsa_rope_init, and the number of pairs of each axis (pairs[a] >= 1, together
+ * rotary_dim / 2) into a plan.  The layouts:
+ *   QSA_AXES_SECTIONS     one spectrum of rotary_dim / 2 frequencies: the first
+ *                         pairs[0] of them are axis 0's, the next pairs[1] axis
+ *                         1's, ...
+ *   QSA_AXES_INTERLEAVED  the same spectrum: pair i is axis a = i mod axes' where
+ *                         a > 0 and i < axes * pairs[a], otherwise axis 0's
+ *                         (which leaves axis 0 its pairs[0]; refused where the
+ *                         counts do not come out)
+ *   QSA_AXES_SPECTRA      sections whose axes have a spectrum each: pair j of axis
+ *                         a's has theta^(-j / pairs[a]), scaled as a plan of
+ *                         rotary_dim 2 pairs[a] is
+ *
+ *   axes   1..QSA_ROPE_MAX_AXES
+ *
+ * Returns QSA_ERR_INVALID_ARG as qsa_rope_init does, and for axes or pairs
+ * outside these; the plan is then left as it was.
+ */
+#define QSA_ROPE_MAX_AXES 4
+
+typedef enum {
+    QSA_AXES_SECTIONS = 0,
+    QSA_AXES_INTERLEAVED = 1,
+    QSA_AXES_SPECTRA = 2
+} qsa_rope_layout_t;
+
+typedef struct {
+    qsa_rope_t rope;
+    int axes;
+    uint8_t axis[QSA_ROPE_MAX_PAIRS];      /* of each pair             */
+} qsa_rope_axes_t;
+
+qsa_status_t qsa_rope_axes_init(const qsa_rope_config_t *config, int axes, const int *pairs,
+                                int layout, qsa_rope_axes_t *plan);
+
+/*
+ * Rotation rows of positions with several axes, as the prologue calls take them.
+ *
+ *   positions  int32 [axes, rows]   any 32-bit positions
+ *   rows       0..2^24 (0: nothing is launched)
+ *   cs         fp32 [rows, rotary_dim / 2, 2]   output: (cos, sin) * amplitude
+ *
+ * Absolute error as of qsa_rope_rows; a plan of one axis gives its bits.
+ * Returns QSA_ERR_INVALID_ARG for null pointers, a plan that
+ * qsa_rope_axes_init did not fill, rows outside these or cs not 16-byte
+ * aligned.
+ */
+qsa_status_t qsa_rope_axes_rows(const qsa_rope_axes_t *plan, const int32_t *positions,
+                                int64_t rows, float *cs, cudaStream_t stream);
+
+/*
  * Norms of queries and keys for each head, with the rotation in the same
  * pass.  TensorRT-LLM PR #20276 ("Qwen3.8-Flash-Next NVFP4 target"),
  * Performance (what runs on the fast paths): the attention prologue does QK
@@ -567,6 +622,56 @@ qsa_status_t qsa_load_kv_tokens(const qsa_geom_t *geom, const int32_t *page_tabl
                                 void *v_out_bf16, cudaStream_t stream);
 
 /*
+ * The 8-bit cache: keys and values of the same pages as e4m3 codes with one
+ * power of two for each block of 16 tokens and KV head.
+ *
+ *   k_pool, v_pool  uint8 [NP, Hkv, P, D]       e4m3 codes
+ *   k_exp, v_exp    uint8 [NP, Hkv, P / 16]     exponents plus 127: an element is
+ *                                               code * 2^(exp - 127)
+ *
+ * qsa_store_kv_tokens_fp8 appends the requests' newest rows.
+ *
+ *   k, v        bf16, row r at k + r * k_row_stride (elements), its Hkv heads of
+ *               D behind one another
+ *   cu_rows     NULL: row b*R + j is the token at position L_b - R + j, as in
+ *               qsa_store_kv_tokens.  Or int32 [B + 1], rising: request b's rows
+ *               are rows cu_rows[b]..cu_rows[b + 1] - 1, its newest
+ *               n_b = cu_rows[b + 1] - cu_rows[b] tokens (whole prompts of any
+ *               lengths; R does not matter then)
+ *   total_rows  rows that k and v have, with cu_rows: 0..2^24 (0: nothing is
+ *               launched); rows outside cu_rows are not looked at
+ *
+ * A block takes the least exponent e in [-32, 64] with |x| <= 448 2^e for its
+ * finite new elements x; where tokens of it stay (the first new row is not its
+ * first token) not less than it had, and those tokens' codes are rounded again
+ * to the new one (exact but for values below 2^-6 of it, which keep steps of
+ * 2^-9).  New codes are e4m3_rne(x 2^-e), beyond 448 held at it; elements that
+ * are not finite become NaN.  Rows without a slot are skipped, and of the pools
+ * only the blocks of stored rows change.  No two rows may have the same slot,
+ * and no two requests may append to the same block.
+ *
+ * qsa_load_kv_tokens_fp8 reads the requests' newest rows back as bf16 (exact):
+ * k_out, v_out [rows, Hkv, D]; rows without a slot are left as they were.
+ *
+ * Both return QSA_ERR_INVALID_ARG for null pointers, row strides below the
+ * heads' D elements or not a multiple of 8, total_rows outside these, k, v,
+ * outputs or code pools not 16-byte aligned; geometry and device checks as for
+ * the other calls (rows_per_req up to 4096).
+ */
+qsa_status_t qsa_store_kv_tokens_fp8(const qsa_geom_t *geom, const void *k_bf16,
+                                     int64_t k_row_stride, const void *v_bf16,
+                                     int64_t v_row_stride, const int32_t *cu_rows,
+                                     int64_t total_rows, const int32_t *page_table,
+                                     const int32_t *seqlens, uint8_t *k_pool, uint8_t *k_exp,
+                                     uint8_t *v_pool, uint8_t *v_exp, cudaStream_t stream);
+qsa_status_t qsa_load_kv_tokens_fp8(const qsa_geom_t *geom, const int32_t *cu_rows,
+                                    int64_t total_rows, const int32_t *page_table,
+                                    const int32_t *seqlens, const uint8_t *k_pool,
+                                    const uint8_t *k_exp, const uint8_t *v_pool,
+                                    const uint8_t *v_exp, void *k_out_bf16, void *v_out_bf16,
+                                    cudaStream_t stream);
+
+/*
  * Dense attention over the NVFP4 paged cache: the layers of a model that do
  * not select blocks, for decode rows (R = 1), verify rows and context row
  * groups (R up to 4096), over contexts of any length the page table holds.
@@ -639,7 +744,7 @@ void qsa_debug_set_wait_ns(unsigned long long ns);
  * Codes are 0xF0S: F the source file (1 decode-row attention, 2 decode and
  * verify attention, 3 index scores, 4 selection, 5 token store, 6 rollback,
  * 7 row-tile attention, 8 norms, rotation and cache rows, 9 and A dense
- * attention), S the check.  Not thread-safe against concurrent
+ * attention, B the 8-bit cache's rows), S the check.  Not thread-safe against concurrent
  * calls of the library.
  */
 int qsa_debug_bounds_status(void);

@@ -23,7 +23,9 @@ from .binding import (EXPORTS, QsaError, load, make_geom, qsa_geom_t, qsa_index_
                       qsa_status_string, qsa_store_kv_tokens, qsa_workspace_init,
                       qsa_workspace_status, make_rope, make_norm_rope, qsa_rope_t, qsa_norm_rope_t,
                       qsa_rope_rows, qsa_qk_norm_rope, qsa_store_kv_tokens_rope,
-                      qsa_load_kv_tokens, qsa_dense_attention, qsa_dense_attention_workspace_bytes)
+                      qsa_load_kv_tokens, qsa_dense_attention, qsa_dense_attention_workspace_bytes,
+                      make_rope_axes, qsa_rope_axes_t, qsa_rope_axes_rows, qsa_store_kv_tokens_fp8,
+                      qsa_load_kv_tokens_fp8)
 
 __all__ = [
     "EXPORTS", "QsaError", "load", "make_geom", "qsa_geom_t", "qsa_index_scores",
@@ -37,7 +39,8 @@ __all__ = [
     "qsa_status_string", "qsa_store_kv_tokens", "qsa_workspace_init", "qsa_workspace_status",
     "make_rope", "make_norm_rope", "qsa_rope_t", "qsa_norm_rope_t", "qsa_rope_rows",
     "qsa_qk_norm_rope", "qsa_store_kv_tokens_rope", "qsa_load_kv_tokens", "qsa_dense_attention",
-    "qsa_dense_attention_workspace_bytes",
+    "qsa_dense_attention_workspace_bytes", "make_rope_axes", "qsa_rope_axes_t", "qsa_rope_axes_rows",
+    "qsa_store_kv_tokens_fp8", "qsa_load_kv_tokens_fp8",
     "DecodeStep", "DenseStep", "MAX_DECODE_ROWS",
 ]
 

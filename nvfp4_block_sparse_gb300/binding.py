@@ -50,8 +50,13 @@ EXPORTS = (
     "qsa_load_kv_tokens",
     "qsa_dense_attention_workspace_bytes",
     "qsa_dense_attention",
+    "qsa_rope_axes_init",
+    "qsa_rope_axes_rows",
+    "qsa_store_kv_tokens_fp8",
+    "qsa_load_kv_tokens_fp8",
 )
 
+ROPE_LAYOUTS = {"sections": 0, "interleaved": 1, "spectra": 2}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "yarn": 2, "wavelength": 3}
 
 
@@ -76,6 +81,10 @@ class qsa_rope_config_t(ctypes.Structure):
 class qsa_rope_t(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int), ("amplitude", ctypes.c_float),
                 ("turns", ctypes.c_uint64 * 128)]
+
+
+class qsa_rope_axes_t(ctypes.Structure):
+    _fields_ = [("rope", qsa_rope_t), ("axes", ctypes.c_int), ("axis", ctypes.c_uint8 * 128)]
 
 
 class qsa_norm_rope_t(ctypes.Structure):
@@ -166,6 +175,16 @@ def load(build_if_missing: bool = False):
                                              [f32, f32] + [_vp] * 9)
     lib.qsa_load_kv_tokens.restype = st
     lib.qsa_load_kv_tokens.argtypes = [G] + [_vp] * 6 + [f32, f32] + [_vp] * 3
+    AX = ctypes.POINTER(qsa_rope_axes_t)
+    lib.qsa_rope_axes_init.restype = st
+    lib.qsa_rope_axes_init.argtypes = [ctypes.POINTER(qsa_rope_config_t), ctypes.c_int,
+                                       ctypes.POINTER(ctypes.c_int), ctypes.c_int, AX]
+    lib.qsa_rope_axes_rows.restype = st
+    lib.qsa_rope_axes_rows.argtypes = [AX, _vp, i64, _vp, _vp]
+    lib.qsa_store_kv_tokens_fp8.restype = st
+    lib.qsa_store_kv_tokens_fp8.argtypes = [G, _vp, i64, _vp, i64, _vp, i64] + [_vp] * 7
+    lib.qsa_load_kv_tokens_fp8.restype = st
+    lib.qsa_load_kv_tokens_fp8.argtypes = [G, _vp, i64] + [_vp] * 9
     lib.qsa_dense_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.qsa_dense_attention_workspace_bytes.argtypes = [G]
     lib.qsa_dense_attention.restype = st
@@ -472,19 +491,43 @@ def _launch(fn, dev, stream, args):
         _check(fn.__name__, st)
 
 
+def _rope_config(rotary_dim, theta, scaling, factor, original_context, beta_fast, beta_slow,
+                 low_freq, high_freq, attention_factor):
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
+    low, high = (beta_slow, beta_fast) if scaling == "yarn" else (low_freq, high_freq)
+    return qsa_rope_config_t(int(rotary_dim), ROPE_SCALINGS[scaling], float(theta), float(factor),
+                             float(original_context), float(low), float(high),
+                             float(attention_factor))
+
+
 def make_rope(rotary_dim, theta, scaling="none", factor=1.0, original_context=0.0, beta_fast=32.0,
               beta_slow=1.0, low_freq=1.0, high_freq=4.0, attention_factor=0.0) -> qsa_rope_t:
     """A rotation plan (qsa_rope_init): ``scaling`` is "none", "linear", "yarn" (beta_fast,
     beta_slow: turns within original_context) or "wavelength" (low_freq, high_freq likewise)."""
-    if scaling not in ROPE_SCALINGS:
-        raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
-    low, high = (beta_slow, beta_fast) if scaling == "yarn" else (low_freq, high_freq)
-    cfg = qsa_rope_config_t(int(rotary_dim), ROPE_SCALINGS[scaling], float(theta), float(factor),
-                            float(original_context), float(low), float(high),
-                            float(attention_factor))
+    cfg = _rope_config(rotary_dim, theta, scaling, factor, original_context, beta_fast, beta_slow,
+                       low_freq, high_freq, attention_factor)
     rope = qsa_rope_t()
     _check("qsa_rope_init", load().qsa_rope_init(ctypes.byref(cfg), ctypes.byref(rope)))
     return rope
+
+
+def make_rope_axes(pairs, theta, layout="sections", scaling="none", factor=1.0, original_context=0.0,
+                   beta_fast=32.0, beta_slow=1.0, low_freq=1.0, high_freq=4.0,
+                   attention_factor=0.0) -> qsa_rope_axes_t:
+    """A rotation plan of several position axes (qsa_rope_axes_init): ``pairs`` of each axis,
+    together rotary_dim / 2; ``layout`` is "sections", "interleaved" or "spectra"; the rest as
+    make_rope."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError("layout must be one of %s" % ", ".join(ROPE_LAYOUTS))
+    pairs = [int(n) for n in pairs]
+    cfg = _rope_config(2 * sum(pairs), theta, scaling, factor, original_context, beta_fast, beta_slow,
+                       low_freq, high_freq, attention_factor)
+    plan = qsa_rope_axes_t()
+    _check("qsa_rope_axes_init", load().qsa_rope_axes_init(
+        ctypes.byref(cfg), len(pairs), (ctypes.c_int * max(len(pairs), 1))(*pairs), ROPE_LAYOUTS[layout],
+        ctypes.byref(plan)))
+    return plan
 
 
 def make_norm_rope(rotary_dim, interleaved=False, eps=1e-6, weight_plus_one=False) -> qsa_norm_rope_t:
@@ -503,6 +546,18 @@ def qsa_rope_rows(geom, rope, seqlens, cs, positions=None, stream=None):
         None if seqlens is None else _at(seqlens, _I32, "seqlens", B, dev),
         None if positions is None else _at(positions, _I32, "positions", T, dev),
         _at(cs, _F32, "cs", T * rope.rotary_dim, dev)))
+
+
+def qsa_rope_axes_rows(plan, positions, cs, stream=None):
+    """Rotation rows of ``positions`` int32 [axes, T]: cs fp32 [T, rotary_dim / 2, 2]."""
+    dev = _device(cs, "cs")
+    if not isinstance(positions, torch.Tensor) or positions.dim() != 2 or positions.shape[0] != plan.axes:
+        raise ValueError("positions must be int32 [%d, T]" % plan.axes)
+    T = positions.shape[1]
+    args = (ctypes.byref(plan), _at(positions, _I32, "positions", plan.axes * T, dev), T,
+            _at(cs, _F32, "cs", T * plan.rope.rotary_dim, dev))
+    if T:
+        _launch(load().qsa_rope_axes_rows, dev, stream, args)
 
 
 def qsa_qk_norm_rope(geom, norm_rope, q, k, q_weight, k_weight, cs, q_out, k_out, stream=None):
@@ -563,6 +618,47 @@ def qsa_load_kv_tokens(geom, page_table, seqlens, k_pool, k_sf, v_pool, v_sf, k_
         _at(k_pool, _U8, "k_pool", n // 2, dev), _at(k_sf, _U8, "k_sf", n // 16, dev),
         _at(v_pool, _U8, "v_pool", n // 2, dev), _at(v_sf, _U8, "v_sf", n // 16, dev),
         k_scale, v_scale, _at(k_out, _BF16, "k_out", m, dev), _at(v_out, _BF16, "v_out", m, dev)))
+
+
+def _pools8(g, k_pool, k_exp, v_pool, v_exp, dev):
+    n = g.num_pages * g.page_size * g.num_kv_heads
+    return (_at(k_pool, _U8, "k_pool", n * g.head_dim, dev), _at(k_exp, _U8, "k_exp", n // 16, dev),
+            _at(v_pool, _U8, "v_pool", n * g.head_dim, dev), _at(v_exp, _U8, "v_exp", n // 16, dev))
+
+
+def qsa_store_kv_tokens_fp8(geom, k, v, page_table, seqlens, k_pool, k_exp, v_pool, v_exp,
+                            cu_rows=None, stream=None):
+    """Appends the requests' newest rows k, v [T, Hkv, D] (views into one projection's rows, say) to
+    the 8-bit cache; with ``cu_rows`` int32 [B + 1] request b's are rows cu_rows[b]..cu_rows[b + 1] - 1."""
+    g = _geom(geom)
+    B, Hkv, D = g.batch, g.num_kv_heads, g.head_dim
+    dev = _device(k, "k")
+    T = B * g.rows_per_req if cu_rows is None else k.shape[0]
+    kp, ks = _rows_at(k, Hkv, D, "k", T, dev)
+    vp, vs = _rows_at(v, Hkv, D, "v", T, dev)
+    args = (ctypes.byref(g), kp, ks, vp, vs,
+            None if cu_rows is None else _at(cu_rows, _I32, "cu_rows", B + 1, dev), T,
+            _at(page_table, _I32, "page_table", B * g.max_blocks, dev), _at(seqlens, _I32, "seqlens", B, dev),
+            *_pools8(g, k_pool, k_exp, v_pool, v_exp, dev))
+    if T:
+        _launch(load().qsa_store_kv_tokens_fp8, dev, stream, args)
+
+
+def qsa_load_kv_tokens_fp8(geom, page_table, seqlens, k_pool, k_exp, v_pool, v_exp, k_out, v_out,
+                           cu_rows=None, stream=None):
+    """The requests' newest rows of the 8-bit cache as bf16 [T, Hkv, D], rows as in
+    qsa_store_kv_tokens_fp8."""
+    g = _geom(geom)
+    B = g.batch
+    dev = _device(k_out, "k_out")
+    T = B * g.rows_per_req if cu_rows is None else k_out.shape[0]
+    m = T * g.num_kv_heads * g.head_dim
+    args = (ctypes.byref(g), None if cu_rows is None else _at(cu_rows, _I32, "cu_rows", B + 1, dev), T,
+            _at(page_table, _I32, "page_table", B * g.max_blocks, dev), _at(seqlens, _I32, "seqlens", B, dev),
+            *_pools8(g, k_pool, k_exp, v_pool, v_exp, dev),
+            _at(k_out, _BF16, "k_out", m, dev), _at(v_out, _BF16, "v_out", m, dev))
+    if T:
+        _launch(load().qsa_load_kv_tokens_fp8, dev, stream, args)
 
 
 def qsa_dense_attention_workspace_bytes(geom) -> int:

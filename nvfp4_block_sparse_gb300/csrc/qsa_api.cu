@@ -21,6 +21,8 @@ using qsa::Geom;
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};
 
+constexpr int64_t kMaxPackedRows = 1LL << 24;   // rows of all requests of a call, as B R
+
 bool positive(double x) { return x > 0.0 && isfinite(x); }
 
 // A number as the unevaluated sum of two doubles, about 100 bits: a rotation plan's frequencies
@@ -74,6 +76,74 @@ uint64_t turn_fraction(Two t) {
   const double a = ldexp(t.hi, 64), whole = floor(a);
   const double rest = floor((a - whole) + ldexp(t.lo, 64) + 0.5);
   return (whole < 0x1p64 ? (uint64_t)whole : 0u) + (uint64_t)(int64_t)rest;
+}
+
+// The checks of a rotation's configuration.
+qsa_status_t check_rope_config(const qsa_rope_config_t* config) {
+  if (!config) return QSA_ERR_INVALID_ARG;
+  const qsa_rope_config_t& c = *config;
+  if (c.rotary_dim < 16 || c.rotary_dim > 2 * QSA_ROPE_MAX_PAIRS || c.rotary_dim % 16 != 0)
+    return QSA_ERR_INVALID_ARG;
+  if (c.scaling < QSA_ROPE_PLAIN || c.scaling > QSA_ROPE_WAVELENGTH) return QSA_ERR_INVALID_ARG;
+  if (!(c.theta > 1.0) || !isfinite(c.theta)) return QSA_ERR_INVALID_ARG;
+  if (!(c.attention_factor >= 0.0) || !isfinite(c.attention_factor)) return QSA_ERR_INVALID_ARG;
+  const bool banded = c.scaling == QSA_ROPE_YARN || c.scaling == QSA_ROPE_WAVELENGTH;
+  if (c.scaling != QSA_ROPE_PLAIN && !positive(c.factor)) return QSA_ERR_INVALID_ARG;
+  if (banded && (!positive(c.original_context) || !positive(c.low) || !positive(c.high) ||
+                 !(c.low < c.high)))
+    return QSA_ERR_INVALID_ARG;
+  return QSA_OK;
+}
+
+// The scaled frequencies of `pairs` pairs, as turns per position.
+qsa_status_t spectrum(const qsa_rope_config_t& c, int pairs, uint64_t* out) {
+  const double two_pi = 6.283185307179586476925;
+  const bool banded = c.scaling == QSA_ROPE_YARN || c.scaling == QSA_ROPE_WAVELENGTH;
+  // YARN: the dims that turn `high` and `low` times within the original context
+  double first = 0.0, last = 1.0;
+  if (c.scaling == QSA_ROPE_YARN) {
+    const double per = 2 * pairs / (2.0 * log(c.theta));
+    first = fmax(floor(per * log(c.original_context / (c.high * two_pi))), 0.0);
+    last = fmin(ceil(per * log(c.original_context / (c.low * two_pi))), 2 * pairs - 1.0);
+    last = fmax(last, first + 1e-3);
+  }
+  const Two one = {1.0, 0.0}, factor = {c.factor, 0.0}, r = root(c.theta, pairs);
+  Two plain = one;
+  for (int i = 0; i < pairs; ++i, plain = plain * r) {
+    Two f = plain;
+    if (c.scaling == QSA_ROPE_LINEAR) {
+      f = f / factor;
+    } else if (banded) {
+      Two m;   // the scaled frequency's share
+      if (c.scaling == QSA_ROPE_YARN) {
+        m = Two{i - first, 0.0} / Two{last - first, 0.0};
+      } else {
+        const Two turns = Two{c.original_context, 0.0} * f * kTurnsPerRadian;
+        m = one - (turns - Two{c.low, 0.0}) / two_sum(c.high, -c.low);
+      }
+      if (!(m.hi > 0.0)) m = {0.0, 0.0};
+      if (m.hi >= 1.0) m = one;
+      f = f * (one - m) + f / factor * m;
+    }
+    if (!(f.hi < 0x1p32)) return QSA_ERR_INVALID_ARG;
+    out[i] = turn_fraction(f * kTurnsPerRadian);
+  }
+  return QSA_OK;
+}
+
+// A plan's other fields.
+qsa_status_t finish_plan(const qsa_rope_config_t& c, qsa_rope_t* plan) {
+  double amplitude = c.attention_factor;
+  if (amplitude == 0.0)
+    amplitude = c.scaling == QSA_ROPE_YARN && c.factor > 1.0 ? 0.1 * log(c.factor) + 1.0 : 1.0;
+  plan->amplitude = (float)amplitude;
+  plan->rotary_dim = c.rotary_dim;
+  return positive(plan->amplitude) ? QSA_OK : QSA_ERR_INVALID_ARG;
+}
+
+bool plan_ok(const qsa_rope_t& rope) {
+  return rope.rotary_dim >= 16 && rope.rotary_dim <= 2 * QSA_ROPE_MAX_PAIRS &&
+         rope.rotary_dim % 16 == 0 && positive(rope.amplitude);
 }
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -189,6 +259,27 @@ qsa::NormRope to_norm_rope(const qsa_norm_rope_t* nr) {
   return r;
 }
 
+// What the calls on the 8-bit cache's rows check alike, and their common arguments.
+qsa_status_t cache8_args(const qsa_geom_t* geom, const int32_t* cu_rows, int64_t total_rows,
+                         const int32_t* page_table, const int32_t* seqlens, const uint8_t* k_pool,
+                         const uint8_t* k_exp, const uint8_t* v_pool, const uint8_t* v_exp,
+                         qsa::Cache8Args* a) {
+  const qsa_status_t st = check_geom(geom, qsa::kMaxContextRows);
+  if (st != QSA_OK) return st;
+  if (!page_table || !seqlens || !k_pool || !k_exp || !v_pool || !v_exp) return QSA_ERR_INVALID_ARG;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16)) return QSA_ERR_INVALID_ARG;
+  if (cu_rows && (total_rows < 0 || total_rows > kMaxPackedRows)) return QSA_ERR_INVALID_ARG;
+  a->cu = cu_rows;
+  a->rows = cu_rows ? total_rows : (int64_t)geom->batch * geom->rows_per_req;
+  a->page_table = page_table;
+  a->seqlens = seqlens;
+  a->k_pool = const_cast<uint8_t*>(k_pool);   // (the read-back only reads them)
+  a->k_exp = const_cast<uint8_t*>(k_exp);
+  a->v_pool = const_cast<uint8_t*>(v_pool);
+  a->v_exp = const_cast<uint8_t*>(v_exp);
+  return QSA_OK;
+}
+
 qsa_status_t check_dense_geom(const qsa_geom_t* geom) {
   qsa_status_t st = check_geom(geom, qsa::kMaxContextRows);
   if (st != QSA_OK) return st;
@@ -217,7 +308,7 @@ int qsa_debug_bounds_status(void) {
   for (int v : {qsa::bounds_word_attend(), qsa::bounds_word_decode(), qsa::bounds_word_index(),
                 qsa::bounds_word_select(), qsa::bounds_word_store(), qsa::bounds_word_rollback(),
                 qsa::bounds_word_prefill(), qsa::bounds_word_prologue(), qsa::bounds_word_dense(),
-                qsa::bounds_word_dense_tile()}) {
+                qsa::bounds_word_dense_tile(), qsa::bounds_word_cache8()}) {
     if (v < 0) return -1;
     if (first == 0) first = v;
   }
@@ -428,58 +519,67 @@ qsa_status_t qsa_sparse_prefill(const qsa_geom_t* geom, const void* q_bf16,
 }
 
 qsa_status_t qsa_rope_init(const qsa_rope_config_t* config, qsa_rope_t* rope) {
-  if (!config || !rope) return QSA_ERR_INVALID_ARG;
-  const qsa_rope_config_t& c = *config;
-  if (c.rotary_dim < 16 || c.rotary_dim > 2 * QSA_ROPE_MAX_PAIRS || c.rotary_dim % 16 != 0)
-    return QSA_ERR_INVALID_ARG;
-  if (c.scaling < QSA_ROPE_PLAIN || c.scaling > QSA_ROPE_WAVELENGTH) return QSA_ERR_INVALID_ARG;
-  if (!(c.theta > 1.0) || !isfinite(c.theta)) return QSA_ERR_INVALID_ARG;
-  if (!(c.attention_factor >= 0.0) || !isfinite(c.attention_factor)) return QSA_ERR_INVALID_ARG;
-  const bool banded = c.scaling == QSA_ROPE_YARN || c.scaling == QSA_ROPE_WAVELENGTH;
-  if (c.scaling != QSA_ROPE_PLAIN && !positive(c.factor)) return QSA_ERR_INVALID_ARG;
-  if (banded && (!positive(c.original_context) || !positive(c.low) || !positive(c.high) ||
-                 !(c.low < c.high)))
-    return QSA_ERR_INVALID_ARG;
-  const double two_pi = 6.283185307179586476925;
-  const int pairs = c.rotary_dim / 2;
-  // YARN: the dims that turn `high` and `low` times within the original context
-  double first = 0.0, last = 1.0;
-  if (c.scaling == QSA_ROPE_YARN) {
-    const double per = c.rotary_dim / (2.0 * log(c.theta));
-    first = fmax(floor(per * log(c.original_context / (c.high * two_pi))), 0.0);
-    last = fmin(ceil(per * log(c.original_context / (c.low * two_pi))), c.rotary_dim - 1.0);
-    last = fmax(last, first + 1e-3);
-  }
+  if (!rope) return QSA_ERR_INVALID_ARG;
+  qsa_status_t st = check_rope_config(config);
+  if (st != QSA_OK) return st;
   qsa_rope_t plan = {};
-  const Two one = {1.0, 0.0}, factor = {c.factor, 0.0}, r = root(c.theta, pairs);
-  Two plain = one;
-  for (int i = 0; i < pairs; ++i, plain = plain * r) {
-    Two f = plain;
-    if (c.scaling == QSA_ROPE_LINEAR) {
-      f = f / factor;
-    } else if (banded) {
-      Two m;   // the scaled frequency's share
-      if (c.scaling == QSA_ROPE_YARN) {
-        m = Two{i - first, 0.0} / Two{last - first, 0.0};
-      } else {
-        const Two turns = Two{c.original_context, 0.0} * f * kTurnsPerRadian;
-        m = one - (turns - Two{c.low, 0.0}) / two_sum(c.high, -c.low);
-      }
-      if (!(m.hi > 0.0)) m = {0.0, 0.0};
-      if (m.hi >= 1.0) m = one;
-      f = f * (one - m) + f / factor * m;
-    }
-    if (!(f.hi < 0x1p32)) return QSA_ERR_INVALID_ARG;
-    plan.turns[i] = turn_fraction(f * kTurnsPerRadian);
+  st = spectrum(*config, config->rotary_dim / 2, plan.turns);
+  if (st == QSA_OK) st = finish_plan(*config, &plan);
+  if (st == QSA_OK) *rope = plan;
+  return st;
+}
+
+qsa_status_t qsa_rope_axes_init(const qsa_rope_config_t* config, int axes, const int* pairs,
+                                int layout, qsa_rope_axes_t* plan) {
+  if (!pairs || !plan) return QSA_ERR_INVALID_ARG;
+  qsa_status_t st = check_rope_config(config);
+  if (st != QSA_OK) return st;
+  if (axes < 1 || axes > QSA_ROPE_MAX_AXES) return QSA_ERR_INVALID_ARG;
+  if (layout < QSA_AXES_SECTIONS || layout > QSA_AXES_SPECTRA) return QSA_ERR_INVALID_ARG;
+  const int all = config->rotary_dim / 2;
+  int left = all;
+  for (int a = 0; a < axes; ++a) {
+    if (pairs[a] < 1 || pairs[a] > left) return QSA_ERR_INVALID_ARG;
+    left -= pairs[a];
   }
-  double amplitude = c.attention_factor;
-  if (amplitude == 0.0)
-    amplitude = c.scaling == QSA_ROPE_YARN && c.factor > 1.0 ? 0.1 * log(c.factor) + 1.0 : 1.0;
-  plan.amplitude = (float)amplitude;
-  if (!positive(plan.amplitude)) return QSA_ERR_INVALID_ARG;
-  plan.rotary_dim = c.rotary_dim;
-  *rope = plan;
-  return QSA_OK;
+  if (left != 0) return QSA_ERR_INVALID_ARG;
+  qsa_rope_axes_t p = {};
+  p.axes = axes;
+  if (layout == QSA_AXES_INTERLEAVED) {
+    int count[QSA_ROPE_MAX_AXES] = {};
+    for (int i = 0; i < all; ++i) {
+      const int a = i % axes;
+      p.axis[i] = (uint8_t)(a > 0 && i < axes * pairs[a] ? a : 0);
+      ++count[p.axis[i]];
+    }
+    for (int a = 0; a < axes; ++a)
+      if (count[a] != pairs[a]) return QSA_ERR_INVALID_ARG;
+  } else {
+    for (int a = 0, i = 0; a < axes; ++a)
+      for (int j = 0; j < pairs[a]; ++j) p.axis[i++] = (uint8_t)a;
+  }
+  if (layout == QSA_AXES_SPECTRA) {
+    for (int a = 0, i = 0; a < axes && st == QSA_OK; i += pairs[a++])
+      st = spectrum(*config, pairs[a], p.rope.turns + i);
+  } else {
+    st = spectrum(*config, all, p.rope.turns);
+  }
+  if (st == QSA_OK) st = finish_plan(*config, &p.rope);
+  if (st == QSA_OK) *plan = p;
+  return st;
+}
+
+qsa_status_t qsa_rope_axes_rows(const qsa_rope_axes_t* plan, const int32_t* positions,
+                                int64_t rows, float* cs, cudaStream_t stream) {
+  if (!plan || !positions || !cs || !aligned(cs, 16)) return QSA_ERR_INVALID_ARG;
+  if (!plan_ok(plan->rope) || plan->axes < 1 || plan->axes > QSA_ROPE_MAX_AXES)
+    return QSA_ERR_INVALID_ARG;
+  for (int i = 0; i < plan->rope.rotary_dim / 2; ++i)
+    if (plan->axis[i] >= plan->axes) return QSA_ERR_INVALID_ARG;
+  if (rows < 0 || rows > kMaxPackedRows) return QSA_ERR_INVALID_ARG;
+  const qsa_status_t st = check_device();
+  if (st != QSA_OK || rows == 0) return st;
+  return from_cuda(qsa::launch_rope_axes(*plan, positions, rows, cs, true, stream));
 }
 
 qsa_status_t qsa_rope_rows(const qsa_geom_t* geom, const qsa_rope_t* rope, const int32_t* seqlens,
@@ -487,9 +587,7 @@ qsa_status_t qsa_rope_rows(const qsa_geom_t* geom, const qsa_rope_t* rope, const
   qsa_status_t st = check_geom(geom, qsa::kMaxContextRows);
   if (st != QSA_OK) return st;
   if (!rope || (!seqlens && !positions) || !cs || !aligned(cs, 8)) return QSA_ERR_INVALID_ARG;
-  if (rope->rotary_dim < 16 || rope->rotary_dim > 2 * QSA_ROPE_MAX_PAIRS ||
-      rope->rotary_dim % 16 != 0 || !positive(rope->amplitude))
-    return QSA_ERR_INVALID_ARG;
+  if (!plan_ok(*rope)) return QSA_ERR_INVALID_ARG;
   st = check_device();
   if (st != QSA_OK) return st;
   return from_cuda(qsa::launch_rope_rows(to_geom(geom), *rope, seqlens, positions, cs, true, stream));
@@ -584,6 +682,47 @@ qsa_status_t qsa_load_kv_tokens(const qsa_geom_t* geom, const int32_t* page_tabl
   return from_cuda(qsa::launch_load_tokens(to_geom(geom), page_table, seqlens, k_pool, k_sf, v_pool,
                                            v_sf, k_scale, v_scale, k_out_bf16, v_out_bf16, true,
                                            stream));
+}
+
+qsa_status_t qsa_store_kv_tokens_fp8(const qsa_geom_t* geom, const void* k_bf16,
+                                     int64_t k_row_stride, const void* v_bf16,
+                                     int64_t v_row_stride, const int32_t* cu_rows,
+                                     int64_t total_rows, const int32_t* page_table,
+                                     const int32_t* seqlens, uint8_t* k_pool, uint8_t* k_exp,
+                                     uint8_t* v_pool, uint8_t* v_exp, cudaStream_t stream) {
+  qsa::Cache8Args a = {};
+  qsa_status_t st = cache8_args(geom, cu_rows, total_rows, page_table, seqlens, k_pool, k_exp,
+                                v_pool, v_exp, &a);
+  if (st != QSA_OK) return st;
+  if (!rows_ok(k_bf16, k_row_stride, geom->num_kv_heads, geom->head_dim) ||
+      !rows_ok(v_bf16, v_row_stride, geom->num_kv_heads, geom->head_dim))
+    return QSA_ERR_INVALID_ARG;
+  st = check_device();
+  if (st != QSA_OK || a.rows == 0) return st;
+  a.k = reinterpret_cast<const __nv_bfloat16*>(k_bf16);
+  a.v = reinterpret_cast<const __nv_bfloat16*>(v_bf16);
+  a.k_stride = k_row_stride;
+  a.v_stride = v_row_stride;
+  return from_cuda(qsa::launch_cache8(to_geom(geom), a, true, true, stream));
+}
+
+qsa_status_t qsa_load_kv_tokens_fp8(const qsa_geom_t* geom, const int32_t* cu_rows,
+                                    int64_t total_rows, const int32_t* page_table,
+                                    const int32_t* seqlens, const uint8_t* k_pool,
+                                    const uint8_t* k_exp, const uint8_t* v_pool,
+                                    const uint8_t* v_exp, void* k_out_bf16, void* v_out_bf16,
+                                    cudaStream_t stream) {
+  qsa::Cache8Args a = {};
+  qsa_status_t st = cache8_args(geom, cu_rows, total_rows, page_table, seqlens, k_pool, k_exp,
+                                v_pool, v_exp, &a);
+  if (st != QSA_OK) return st;
+  if (!k_out_bf16 || !v_out_bf16 || !aligned(k_out_bf16, 16) || !aligned(v_out_bf16, 16))
+    return QSA_ERR_INVALID_ARG;
+  st = check_device();
+  if (st != QSA_OK || a.rows == 0) return st;
+  a.k_out = reinterpret_cast<__nv_bfloat16*>(k_out_bf16);
+  a.v_out = reinterpret_cast<__nv_bfloat16*>(v_out_bf16);
+  return from_cuda(qsa::launch_cache8(to_geom(geom), a, false, true, stream));
 }
 
 size_t qsa_dense_attention_workspace_bytes(const qsa_geom_t* geom) {

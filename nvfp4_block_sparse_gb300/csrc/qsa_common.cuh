@@ -310,12 +310,27 @@ struct PrologueArgs {
 };
 cudaError_t launch_rope_rows(const Geom& g, const qsa_rope_t& rope, const int32_t* seqlens,
                              const int32_t* positions, float* cs, bool pdl, cudaStream_t stream);
+cudaError_t launch_rope_axes(const qsa_rope_axes_t& plan, const int32_t* positions, long long rows,
+                             float* cs, bool pdl, cudaStream_t stream);
 cudaError_t launch_prologue(const Geom& g, const NormRope& nr, const PrologueArgs& a, bool pdl,
                             cudaStream_t stream);
 cudaError_t launch_load_tokens(const Geom& g, const int32_t* page_table, const int32_t* seqlens,
                                const uint8_t* k_pool, const uint8_t* k_sf, const uint8_t* v_pool,
                                const uint8_t* v_sf, float k_scale, float v_scale, void* k_out,
                                void* v_out, bool pdl, cudaStream_t stream);
+
+// The 8-bit cache's rows (qsa_cache8.cu): appended, or read back.
+struct Cache8Args {
+  const __nv_bfloat16 *k, *v;        // append
+  long long k_stride, v_stride;      // row strides in elements
+  const int32_t* cu;                 // [B + 1], or null: R rows of each request
+  long long rows;                    // of all requests
+  const int32_t *page_table, *seqlens;
+  uint8_t *k_pool, *k_exp, *v_pool, *v_exp;
+  __nv_bfloat16 *k_out, *v_out;      // read-back
+};
+cudaError_t launch_cache8(const Geom& g, const Cache8Args& a, bool append, bool pdl,
+                          cudaStream_t stream);
 
 // Dense attention (qsa_dense.cu): the workspace's bytes and the launches.
 struct DenseArgs {
@@ -354,6 +369,7 @@ int bounds_word_prefill();
 int bounds_word_prologue();
 int bounds_word_dense();
 int bounds_word_dense_tile();
+int bounds_word_cache8();
 #endif
 
 // Bound of the attention kernels' waits for their chunk copies, in ns

@@ -33,6 +33,18 @@ namespace {
 // (that unit is 84 % busy; instructions would issue in 2.4 us); 192 rows of 64 pairs: 1.5 us,
 // a launch.
 // ---------------------------------------------------------------------------
+// (cos, sin) of a 64-bit fraction of a turn, times the amplitude.
+__device__ __forceinline__ float2 turn(unsigned long long phase, float amplitude) {
+  // The upper 32 bits, signed, lie in [-1/2, 1/2) turn.  fp32 holds 24 of them; the others turn
+  // sine and cosine by less than 1e-7, to first order.
+  const int bits = (int)(phase >> 32);
+  const float top = (float)bits;
+  const float rest = (float)(bits - __float2int_rn(top)) * (3.14159265f * 0x1p-31f);
+  float s, c;
+  sincospif(top * 0x1p-31f, &s, &c);
+  return make_float2(fmaf(-s, rest, c) * amplitude, fmaf(c, rest, s) * amplitude);
+}
+
 __global__ void __launch_bounds__(256)
 rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
                  const int32_t* __restrict__ seqlens, const int32_t* __restrict__ positions,
@@ -45,16 +57,52 @@ rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
        r += (long long)gridDim.x * blockDim.y) {
     const long long pos = positions ? positions[r]
                                     : (long long)seqlens[r / R] - R + (int)(r % R);
-    const unsigned long long phase = (unsigned long long)pos * turns;
-    // The upper 32 bits, signed, lie in [-1/2, 1/2) turn.  fp32 holds 24 of them; the others turn
-    // sine and cosine by less than 1e-7, to first order.
-    const int bits = (int)(phase >> 32);
-    const float top = (float)bits;
-    const float rest = (float)(bits - __float2int_rn(top)) * (3.14159265f * 0x1p-31f);
-    float s, c;
-    sincospif(top * 0x1p-31f, &s, &c);
-    cs[r * pairs + threadIdx.x] = make_float2(fmaf(-s, rest, c) * rope.amplitude,
-                                              fmaf(c, rest, s) * rope.amplitude);
+    cs[r * pairs + threadIdx.x] = turn((unsigned long long)pos * turns, rope.amplitude);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rotation rows of positions with several axes: as above, each pair by the position on its
+// own axis.  A thread has two neighbouring pairs of every so-manieth row, four rows' positions
+// requested at once.  The plan passes through shared memory once per CTA: read from the
+// parameters by every warp, an address at a time, it took longer than the rows.
+// ---------------------------------------------------------------------------
+constexpr int kAxesRows = 4;
+
+__global__ void __launch_bounds__(512)
+rope_axes_kernel(uint32_t T, const __grid_constant__ qsa_rope_axes_t plan,
+                 const int32_t* __restrict__ positions, float4* __restrict__ cs) {
+  __shared__ unsigned long long s_turns[QSA_ROPE_MAX_PAIRS];
+  __shared__ uint32_t s_axis[QSA_ROPE_MAX_PAIRS];
+  const int half = blockDim.x, threads = half * blockDim.y;
+  for (int i = threadIdx.y * half + threadIdx.x; i < 2 * half; i += threads) {
+    s_turns[i] = plan.rope.turns[i];
+    s_axis[i] = plan.axis[i];
+  }
+  __syncthreads();
+  const int x = threadIdx.x;
+  const unsigned long long t0 = s_turns[2 * x], t1 = s_turns[2 * x + 1];
+  const int32_t* p0 = positions + (size_t)s_axis[2 * x] * T;
+  const int32_t* p1 = positions + (size_t)s_axis[2 * x + 1] * T;
+  const uint32_t step = gridDim.x * blockDim.y;
+  pdl_wait();
+  pdl_trigger();
+  for (uint32_t r = blockIdx.x * blockDim.y + threadIdx.y; r < T; r += kAxesRows * step) {
+    int a[kAxesRows], b[kAxesRows];
+#pragma unroll
+    for (int i = 0; i < kAxesRows; ++i) {
+      const uint32_t row = r + i * step;
+      a[i] = row < T ? p0[row] : 0;
+      b[i] = row < T ? p1[row] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kAxesRows; ++i) {
+      const uint32_t row = r + i * step;
+      if (row >= T) break;
+      const float2 u = turn((unsigned long long)(long long)a[i] * t0, plan.rope.amplitude);
+      const float2 v = turn((unsigned long long)(long long)b[i] * t1, plan.rope.amplitude);
+      cs[(size_t)row * half + x] = make_float4(u.x, u.y, v.x, v.y);
+    }
   }
 }
 
@@ -501,6 +549,19 @@ cudaError_t launch_rope_rows(const Geom& g, const qsa_rope_t& rope, const int32_
   const long long most = 16 * sm_count();   // (what is resident takes turns)
   return launch(rope_rows_kernel, dim3((unsigned)(ctas < most ? ctas : most)), block, pdl, stream,
                 g.R, T, rope, seqlens, positions, reinterpret_cast<float2*>(cs));
+}
+
+cudaError_t launch_rope_axes(const qsa_rope_axes_t& plan, const int32_t* positions, long long rows,
+                             float* cs, bool pdl, cudaStream_t stream) {
+  const int half = plan.rope.rotary_dim / 4;
+  // Few rows: small CTAs, a row or two each, on many SMs; many: two large ones per SM, so that
+  // the plan is read few times.
+  const int sms = sm_count();
+  const int threads = rows * half <= sms * 256LL ? 64 : 512;
+  const dim3 block(half, threads / half);
+  const long long ctas = (rows + block.y - 1) / block.y, most = 2 * sms;
+  return launch(rope_axes_kernel, dim3((unsigned)(threads == 512 && ctas > most ? most : ctas)), block, pdl,
+                stream, (uint32_t)rows, plan, positions, reinterpret_cast<float4*>(cs));
 }
 
 cudaError_t launch_prologue(const Geom& g, const NormRope& nr, const PrologueArgs& a, bool pdl,
