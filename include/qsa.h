@@ -720,6 +720,34 @@ qsa_status_t qsa_dense_attention(const qsa_geom_t *geom, const void *q_bf16,
                                  size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Dense attention over the 8-bit cache: as qsa_dense_attention, for the same
+ * geometries, rows, windows, sinks and divisions of work, with K = e4m3(code)
+ * 2^(exp - 127) and V likewise.
+ *
+ *   k_pool, k_exp, v_pool, v_exp   as qsa_store_kv_tokens_fp8 writes them;
+ *             exponent bytes outside 95..191 are taken as the nearest of these
+ *   workspace >= qsa_dense_attention_fp8_workspace_bytes() bytes, as there (and
+ *             it may be shared with qsa_dense_attention's calls as theirs may)
+ *
+ * Precision is qsa_dense_attention's; weights are rounded to 11 bits times their
+ * block's scale of V, so "2^-22 of the row's largest" is of the largest
+ * exp(z_t) 2^exp; and weights below 2^-38 of the row's largest may be missing from
+ * the sum where V's scales are as far apart as can be.  Codes that are NaN make
+ * the rows that see their keys not finite, and a value that is makes so the rows
+ * of its request too that look at its block of 128 tokens without seeing it.
+ *
+ * Returns as qsa_dense_attention; k_exp and v_exp are 16-byte aligned.
+ */
+size_t qsa_dense_attention_fp8_workspace_bytes(const qsa_geom_t *geom);
+qsa_status_t qsa_dense_attention_fp8(const qsa_geom_t *geom, const void *q_bf16,
+                                     const uint8_t *k_pool, const uint8_t *k_exp,
+                                     const uint8_t *v_pool, const uint8_t *v_exp, float sm_scale,
+                                     const int32_t *page_table, const int32_t *seqlens,
+                                     int window, const float *sinks, void *out_bf16, float *lse,
+                                     void *workspace, size_t workspace_bytes,
+                                     cudaStream_t stream);
+
+/*
  * Diagnostics: sets the bound, in nanoseconds, of the waits of the head_dim
  * 128 sparse decode kernel for its page copies (2 s by default; 0 restores
  * the default).  Process-wide, for tests of the timeout reporting: a bound
@@ -744,7 +772,7 @@ void qsa_debug_set_wait_ns(unsigned long long ns);
  * Codes are 0xF0S: F the source file (1 decode-row attention, 2 decode and
  * verify attention, 3 index scores, 4 selection, 5 token store, 6 rollback,
  * 7 row-tile attention, 8 norms, rotation and cache rows, 9 and A dense
- * attention, B the 8-bit cache's rows), S the check.  Not thread-safe against concurrent
+ * attention, B the 8-bit cache's rows, C dense attention over it), S the check.  Not thread-safe against concurrent
  * calls of the library.
  */
 int qsa_debug_bounds_status(void);

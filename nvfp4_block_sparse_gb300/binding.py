@@ -54,6 +54,8 @@ EXPORTS = (
     "qsa_rope_axes_rows",
     "qsa_store_kv_tokens_fp8",
     "qsa_load_kv_tokens_fp8",
+    "qsa_dense_attention_fp8_workspace_bytes",
+    "qsa_dense_attention_fp8",
 )
 
 ROPE_LAYOUTS = {"sections": 0, "interleaved": 1, "spectra": 2}
@@ -185,6 +187,11 @@ def load(build_if_missing: bool = False):
     lib.qsa_store_kv_tokens_fp8.argtypes = [G, _vp, i64, _vp, i64, _vp, i64] + [_vp] * 7
     lib.qsa_load_kv_tokens_fp8.restype = st
     lib.qsa_load_kv_tokens_fp8.argtypes = [G, _vp, i64] + [_vp] * 9
+    lib.qsa_dense_attention_fp8_workspace_bytes.restype = ctypes.c_size_t
+    lib.qsa_dense_attention_fp8_workspace_bytes.argtypes = [G]
+    lib.qsa_dense_attention_fp8.restype = st
+    lib.qsa_dense_attention_fp8.argtypes = ([G] + [_vp] * 5 + [f32, _vp, _vp, ctypes.c_int] +
+                                            [_vp] * 4 + [ctypes.c_size_t, _vp])
     lib.qsa_dense_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.qsa_dense_attention_workspace_bytes.argtypes = [G]
     lib.qsa_dense_attention.restype = st
@@ -678,6 +685,25 @@ def qsa_dense_attention(geom, q, k_pool, k_sf, v_pool, v_sf, k_scale, v_scale, s
         _at(k_pool, _U8, "k_pool", n // 2, dev), _at(k_sf, _U8, "k_sf", n // 16, dev),
         _at(v_pool, _U8, "v_pool", n // 2, dev), _at(v_sf, _U8, "v_sf", n // 16, dev),
         k_scale, v_scale, sm_scale, _at(page_table, _I32, "page_table", B * g.max_blocks, dev),
+        _at(seqlens, _I32, "seqlens", B, dev), window,
+        None if sinks is None else _at(sinks, _F32, "sinks", g.num_q_heads, dev),
+        _at(out, _BF16, "out", m * D, dev), _at(lse, _F32, "lse", m, dev),
+        _at(workspace, _U8, "workspace", 0, dev), workspace.numel()))
+
+
+def qsa_dense_attention_fp8_workspace_bytes(geom) -> int:
+    return int(load().qsa_dense_attention_fp8_workspace_bytes(ctypes.byref(_geom(geom))))
+
+
+def qsa_dense_attention_fp8(geom, q, k_pool, k_exp, v_pool, v_exp, sm_scale, page_table, seqlens, out,
+                            lse, workspace, window=0, sinks=None, stream=None):
+    """qsa_dense_attention over the 8-bit cache."""
+    g = _geom(geom)
+    B, m, D = g.batch, g.batch * g.rows_per_req * g.num_q_heads, g.head_dim
+    dev = _device(q, "q")
+    _launch(load().qsa_dense_attention_fp8, dev, stream, (
+        ctypes.byref(g), _at(q, _BF16, "q", m * D, dev), *_pools8(g, k_pool, k_exp, v_pool, v_exp, dev),
+        sm_scale, _at(page_table, _I32, "page_table", B * g.max_blocks, dev),
         _at(seqlens, _I32, "seqlens", B, dev), window,
         None if sinks is None else _at(sinks, _F32, "sinks", g.num_q_heads, dev),
         _at(out, _BF16, "out", m * D, dev), _at(lse, _F32, "lse", m, dev),

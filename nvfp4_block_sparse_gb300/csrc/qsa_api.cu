@@ -308,7 +308,8 @@ int qsa_debug_bounds_status(void) {
   for (int v : {qsa::bounds_word_attend(), qsa::bounds_word_decode(), qsa::bounds_word_index(),
                 qsa::bounds_word_select(), qsa::bounds_word_store(), qsa::bounds_word_rollback(),
                 qsa::bounds_word_prefill(), qsa::bounds_word_prologue(), qsa::bounds_word_dense(),
-                qsa::bounds_word_dense_tile(), qsa::bounds_word_cache8()}) {
+                qsa::bounds_word_dense_tile(), qsa::bounds_word_cache8(),
+                qsa::bounds_word_dense8()}) {
     if (v < 0) return -1;
     if (first == 0) first = v;
   }
@@ -758,6 +759,40 @@ qsa_status_t qsa_dense_attention(const qsa_geom_t* geom, const void* q_bf16,
   a.window = window; a.sinks = sinks;
   a.out = out_bf16; a.lse = lse; a.workspace = workspace;
   return from_cuda(qsa::launch_dense(g, a, stream));
+}
+
+size_t qsa_dense_attention_fp8_workspace_bytes(const qsa_geom_t* geom) {
+  return check_dense_geom(geom) == QSA_OK ? qsa::dense8_workspace_bytes(to_geom(geom)) : 0;
+}
+
+qsa_status_t qsa_dense_attention_fp8(const qsa_geom_t* geom, const void* q_bf16,
+                                     const uint8_t* k_pool, const uint8_t* k_exp,
+                                     const uint8_t* v_pool, const uint8_t* v_exp, float sm_scale,
+                                     const int32_t* page_table, const int32_t* seqlens, int window,
+                                     const float* sinks, void* out_bf16, float* lse,
+                                     void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  qsa_status_t st = check_dense_geom(geom);
+  if (st != QSA_OK) return st;
+  if (!q_bf16 || !k_pool || !k_exp || !v_pool || !v_exp || !page_table || !seqlens || !out_bf16 || !lse)
+    return QSA_ERR_INVALID_ARG;
+  if (window < 0) return QSA_ERR_INVALID_ARG;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(k_exp, 16) || !aligned(v_exp, 16) ||
+      !aligned(q_bf16, 16) || !aligned(out_bf16, 16))
+    return QSA_ERR_INVALID_ARG;
+  if (!positive(sm_scale)) return QSA_ERR_INVALID_ARG;
+  const Geom g = to_geom(geom);
+  if (!workspace || workspace_bytes < qsa::dense8_workspace_bytes(g) || !aligned(workspace, 256))
+    return QSA_ERR_WORKSPACE;
+  st = check_device();
+  if (st != QSA_OK) return st;
+  qsa::DenseArgs a = {};
+  a.q = q_bf16;
+  a.k_pool = k_pool; a.k_sf = k_exp; a.v_pool = v_pool; a.v_sf = v_exp;
+  a.sm_scale = sm_scale;
+  a.page_table = page_table; a.seqlens = seqlens;
+  a.window = window; a.sinks = sinks;
+  a.out = out_bf16; a.lse = lse; a.workspace = workspace;
+  return from_cuda(qsa::launch_dense8(g, a, stream));
 }
 
 int qsa_select_sparse_decode_fused(const qsa_geom_t* geom) {

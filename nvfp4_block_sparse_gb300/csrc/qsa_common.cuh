@@ -346,6 +346,9 @@ struct DenseArgs {
 };
 size_t dense_workspace_bytes(const Geom& g);
 cudaError_t launch_dense(const Geom& g, const DenseArgs& a, cudaStream_t stream);
+// The same over the 8-bit cache (qsa_dense8.cu): k_sf and v_sf are the exponents, no k_scale, v_scale.
+size_t dense8_workspace_bytes(const Geom& g);
+cudaError_t launch_dense8(const Geom& g, const DenseArgs& a, cudaStream_t stream);
 
 struct DecodePlan {
   int splits;        // KV splits per (request, KV head, query group)
@@ -370,6 +373,7 @@ int bounds_word_prologue();
 int bounds_word_dense();
 int bounds_word_dense_tile();
 int bounds_word_cache8();
+int bounds_word_dense8();
 #endif
 
 // Bound of the attention kernels' waits for their chunk copies, in ns

@@ -79,7 +79,7 @@ struct Desc {
 
 struct Work {
   const __nv_bfloat16* q;
-  const uint8_t *k_pool, *k_sf, *v_pool, *v_sf;
+  const uint8_t *k_pool, *k_sf, *v_pool, *v_sf;   // (8-bit pages: k_sf and v_sf are the exponents)
   float v_scale;
   float z_mant;      // k_scale sm_scale log2(e) = z_mant 2^z_exp, z_mant in [1/2, 1)
   int z_exp;
@@ -314,9 +314,10 @@ inline int desc_count(const Shape& s) { return s.by_unit ? (int)unit_count(s) : 
 
 }  // namespace dense
 
-// The tile kernel (qsa_dense_tile.cu): its units for this geometry, and its launch.
+// The tile kernel (qsa_dense_tile.cu): its units for this geometry, and its launch over NVFP4
+// or (e8) 8-bit pages.
 dense::Shape dense_tile_shape(const Geom& g, int window);
-cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, cudaStream_t stream);
+cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, bool e8, cudaStream_t stream);
 cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, cudaStream_t stream);
 // The workspace's parts: status word, descriptors, records.
 size_t dense_carve(const dense::Shape& s, void* workspace, dense::Work* w);

@@ -76,6 +76,8 @@
 #include "qsa_dense.cuh"
 #include "qsa_tc.cuh"
 
+#include <type_traits>
+
 namespace qsa {
 namespace dense {
 namespace {
@@ -87,9 +89,11 @@ using namespace tc;
 [[maybe_unused]] constexpr int kChkOut = 0xA02;     // output row out of range
 [[maybe_unused]] constexpr int kChkRecord = 0xA03;  // record's slot out of range
 
-template <int D_, int CG_>
+// E8: the 8-bit cache's pages instead of NVFP4's (see "8-bit pages" below).
+template <int D_, int CG_, bool E8_>
 struct TT {
   static constexpr int D = D_, CG = CG_;                 // CG: CTAs per MMA
+  static constexpr bool E8 = E8_;
   static constexpr int kTiles = D == 128 && CG == 2 ? 2 : 1;   // tiles of a CTA
   static constexpr int kTok = D == 256 ? 64 : 128;       // tokens per chunk
   static constexpr int kHalves = kTok / 64;              // P is written 64 tokens at a time
@@ -123,14 +127,19 @@ struct TT {
   // through which Q and O pass.
   static constexpr int kQBytes = kQTmem ? 32768 : 128 * D * 2;
   // Codes and scales on their way: a stage is a chunk, this CTA's K rows and whole V rows.
-  static constexpr int kDepth = CG == 2 ? 4 : 3;
-  static constexpr int kKCodes = kKRows * D / 2, kVCodes = kTok * D / 2;
-  static constexpr int kKPart = kKCodes + kKCodes / 8, kVPart = kVCodes + kVCodes / 8;
+  static constexpr int kDepth = CG == 2 ? 4 : E8 ? 2 : 3;   // (what there is room for)
+  static constexpr int kRow = E8 ? D : D / 2;            // code bytes of a token
+  static constexpr int kKCodes = kKRows * kRow, kVCodes = kTok * kRow;
+  static constexpr int kKPart = kKCodes + (E8 ? 0 : kKCodes / 8), kVPart = kVCodes + (E8 ? 0 : kVCodes / 8);
   static constexpr int kStage = kKPart + kVPart;
   static constexpr int kRing = kDepth * kStage;
   static constexpr int kBars = 18 + 2 * kDepth;
+  // Exponents of a chunk's blocks: eight bytes of K and eight of V, in a ring of their own.
+  static constexpr int kExpSlots = E8 ? 8 : 0;
+  static_assert(!E8 || kExpSlots >= kDepth + 2, "exponents' ring");
   static constexpr int kSmem = 1024 + kTiles * kQBytes + 2 * kKBytes + 2 * kVBytes + kRing +
-                               kBars * 8 + 16 + kDepth * 4;
+                               kBars * 8 + 16 + (E8 ? 16 : kDepth * 4) + kExpSlots * 16;
+  static_assert(kVecs <= 512 && (!E8 || kDepth <= 4), "a unit's vectors; what is copied of each stage");
 };
 
 // 32 columns of this thread's lane.
@@ -280,21 +289,22 @@ __device__ __forceinline__ void cluster_sync() {
 template <class T>
 __device__ __forceinline__ bool copy_all(const Shape& sh, const Work& p, const Span& span, int rank,
                                          uint8_t* ring, uint64_t* full, uint64_t* empty,
-                                         volatile uint32_t* copied) {
+                                         volatile uint32_t* copied, uint8_t* exps) {
   const int lane = threadIdx.x & 31;
   const int psh = 31 - __clz(sh.g.P);
-  const bool scales = lane & 1, v = lane & 2;
+  const bool scales = lane & 1, v = lane & 2;         // (8-bit: no copies of scales)
   const int rows = v ? T::kTok : T::kKRows;
   const int step = min(sh.g.P, rows);                 // rows of a copy
   const int off = (lane >> 2) * step;                 // its first, in the stage's part
-  const bool mine = lane < 8 && off < rows;
+  const bool mine = lane < 8 && off < rows && !(T::E8 && scales);
   const int tok_off = off + (v ? 0 : rank * T::kKRows);
-  const uint32_t row_bytes = scales ? T::D / 16 : T::D / 2, bytes = step * row_bytes;
+  const uint32_t row_bytes = scales ? T::D / 16 : T::kRow, bytes = step * row_bytes;
   const uint8_t* pool = v ? (scales ? p.v_sf : p.v_pool) : (scales ? p.k_sf : p.k_pool);
   uint8_t* dst = ring + (v ? T::kKPart + (scales ? T::kVCodes : 0) : (scales ? T::kKCodes : 0)) +
                  off * row_bytes;
   const uint64_t policy = policy_evict_normal();   // (other units read the page too)
   int slot = 0, use = 0;
+  [[maybe_unused]] int chunks = 0;
   bool ok = true;
   Cursor cursor(span);
   Seg seg;
@@ -306,6 +316,21 @@ __device__ __forceinline__ bool copy_all(const Shape& sh, const Work& p, const S
     };
     int blk0 = (seg.chunk0 * T::kTok) >> psh;
     int ids = page_id(blk0 + lane), later = page_id(blk0 + 32 + lane);
+    // 8-bit: lane i has the exponent of block i & 7 of the chunk, of K (i < 8) or of V
+    auto exp_of = [&](int tok0) {
+      const int tok = tok0 + 16 * (lane & 7), at = (tok >> psh) - blk0;
+      const int here = __shfl_sync(0xffffffffu, ids, at & 31);
+      const int page_later = __shfl_sync(0xffffffffu, later, at & 31);
+      const int page = at < 32 ? here : page_later;
+      uint32_t e = 127u;
+      if (lane < 16 && 16 * (lane & 7) < T::kTok && page >= 0 && page < sh.g.NP && tok < seg.n_all &&
+          tok + 16 > seg.lo_all)
+        e = __ldg((lane < 8 ? p.k_sf : p.v_sf) +
+                  (((((size_t)page * sh.g.Hkv + seg.kvh) << psh) + (tok & (sh.g.P - 1))) >> 4));
+      return e;
+    };
+    [[maybe_unused]] uint32_t exp_next = 0;
+    if constexpr (T::E8) exp_next = exp_of(seg.chunk0 * T::kTok);
 #pragma unroll 1
     for (int c = 0; c < seg.todo; ++c) {
       const int tok0 = (seg.chunk0 + c) * T::kTok, tok = tok0 + tok_off;
@@ -326,15 +351,32 @@ __device__ __forceinline__ bool copy_all(const Shape& sh, const Work& p, const S
       const uint32_t which = __ballot_sync(0xffffffffu, there);
       const uint32_t sum = __reduce_add_sync(0xffffffffu, there ? bytes : 0u);
       if (use > 0 && gave_up(&empty[slot], use - 1)) { ok = false; break; }
-      if (lane == 0) {
-        copied[slot] = which;
-        mbar_arrive_expect_tx(&full[slot], sum);
+      if constexpr (!T::E8) {
+        if (lane == 0) {
+          copied[slot] = which;
+          mbar_arrive_expect_tx(&full[slot], sum);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       if (there)
         bulk_g2s(dst + slot * T::kStage,
                  pool + ((((size_t)page * sh.g.Hkv + seg.kvh) << psh) + (tok & (sh.g.P - 1))) * row_bytes,
                  bytes, &full[slot], policy);
+      if constexpr (T::E8) {
+        // The exponents are written before the stage's one arrival (the copies' bytes may be
+        // counted before they are expected: without the arrival the phase stays).  Their place
+        // was last chunk - kExpSlots', which every softmax warp is done with: the stage was
+        // free, so V of chunk - kDepth was converted, for which the MMAs that read the weights of
+        // chunk - kDepth - 2 had completed.
+        if (lane < 16) exps[16 * (chunks & (T::kExpSlots - 1)) + lane] = (uint8_t)min(max(exp_next, 95u), 191u);
+        __syncwarp();
+        if (lane == 0) {
+          copied[slot] = which;
+          mbar_arrive_expect_tx(&full[slot], sum);
+        }
+        ++chunks;
+        if (c + 1 < seg.todo) exp_next = exp_of(tok0 + T::kTok);
+      }
       if (++slot == T::kDepth) {
         slot = 0;
         ++use;
@@ -442,6 +484,89 @@ struct Converter {
   }
 };
 
+// ---- 8-bit pages -----------------------------------------------------------------
+// e4m3 codes with a power of two per 16 tokens (qsa_dense8.cu): codes become fp16 as they are,
+// without a product, and the softmax threads have the scales: a block's power of two of K
+// in the factor of its logits, that of V in the exponent of its weights, taken out
+// again from the sum of the block's weights.  The copy warp brings the exponents, which are
+// too short for bulk copies.
+//
+// A lane has a 16-byte piece (16 codes, two 16-byte pieces of the tile) per step; a row's pieces belong to
+// neighbouring lanes, of eight of them the upper four store their two in the other order
+// (their 64-dim block has the same banks).
+template <class T, int kRows, int kDims>
+struct Converter8 {
+  static constexpr int D = T::D;
+  static constexpr int kPieces = kDims / 16;                  // 16-byte pieces of a row
+  static constexpr int kUnits = kRows * kPieces / 128;        // steps of a warp
+  static constexpr int kStepRows = 128 / kPieces;             // rows from one step to the next
+  static constexpr int kBlk = kRows * 128, kBytes = kRows * kDims * 2;
+  static_assert(kStepRows % 8 == 0, "a step keeps a row's place in the swizzle");
+
+  uint8_t* tiles;
+  uint64_t *ready, *freed;
+  uint32_t part, at_c, at_t;     // the stage's codes; the lane's first piece there and in the tile
+  int row0, lane_sh, row;
+  bool flip;
+
+  __device__ __forceinline__ Converter8(const Shape& sh, bool v, int token0, int dim0, int dw, uint8_t* ring,
+                                        uint8_t* tiles_, uint64_t* ready_, uint64_t* freed_)
+      : tiles(tiles_), ready(ready_), freed(freed_), part(smem_u32(ring) + (v ? T::kKPart : 0)), row0(token0) {
+    const int lane = threadIdx.x & 31, piece = lane % kPieces;
+    lane_sh = 31 - __clz(min(sh.g.P, kRows));                 // log2 of a copy's rows
+    row = (32 / kPieces) * dw + lane / kPieces;
+    flip = kPieces >= 8 && (lane & 4);
+    at_c = row * D + dim0 + 16 * piece;
+    at_t = ((piece >> 2) * kBlk + sw128(row, 2 * (piece & 3))) ^ (flip ? 16u : 0u);
+  }
+  __device__ __forceinline__ bool convert(const Seg& seg, int tok0, int chunks, int slot, uint32_t copied,
+                                          bool v) {
+    const int x = chunks & 1, use = chunks >> 1;
+    uint8_t* tile = tiles + x * kBytes;
+    const uint32_t from = part + slot * T::kStage + at_c;
+    const int first = seg.lo_all - tok0 - row0;
+    const uint32_t seen = (uint32_t)max(seg.n_all - seg.lo_all, 0);
+    const uint32_t bits = copied >> (v ? 2 : 0);
+    uint4 codes[kUnits];       // every step's, so that their latencies overlap
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(codes[i].x), "=r"(codes[i].y), "=r"(codes[i].z), "=r"(codes[i].w)
+                   : "r"(from + i * kStepRows * D));
+    if (use > 0 && gave_up(&freed[x], use - 1)) return false;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      uint4 c = codes[i];
+      const int r = row + i * kStepRows;
+      // rows that no vector of the unit sees, and what was not copied, are zeros (a code may be NaN)
+      if ((uint32_t)(r - first) >= seen || !((bits >> (4 * (r >> lane_sh))) & 1u)) c = make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t w[4] = {flip ? c.z : c.x, flip ? c.w : c.y, flip ? c.x : c.z, flip ? c.y : c.w};
+      const uint32_t to = at_t + i * (kStepRows / 8) * 1024;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        *reinterpret_cast<uint4*>(tile + (to ^ (16 * u))) =
+            make_uint4(e4m3x2_to_f16x2(w[2 * u] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * u] >> 16),
+                       e4m3x2_to_f16x2(w[2 * u + 1] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * u + 1] >> 16));
+    }
+    fence_proxy_async_smem();
+    warp_arrive<T::CG>(&ready[x]);
+    return true;
+  }
+};
+
+// A block's factor of its logits, its exponent of V (log2), and 2^-that: from byte i of a chunk's
+// exponents.
+struct Block8 {
+  float c, ve, back;
+  __device__ __forceinline__ Block8(const uint4& e, int i, float cq) {
+    const uint32_t kw = i < 4 ? e.x : e.y, vw = i < 4 ? e.z : e.w;
+    c = cq * __uint_as_float(((kw >> (8 * (i & 3))) & 0xFFu) << 23);
+    const uint32_t v = (vw >> (8 * (i & 3))) & 0xFFu;
+    ve = __uint_as_float(0x4B000000u | v) - 8388735.f;      // 2^23 + v, exact
+    back = __uint_as_float(0x7F000000u - (v << 23));
+  }
+};
+
 // Every chunk through one converter, or through K's and then V's.
 template <class T, class... C>
 __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, const Span& span, uint64_t* full,
@@ -483,10 +608,10 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int D, int CG>
-__global__ void __launch_bounds__(TT<D, CG>::kThreads, 1)
+template <int D, int CG, bool E8>
+__global__ void __launch_bounds__(TT<D, CG, E8>::kThreads, 1)
 dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work p) {
-  using T = TT<D, CG>;
+  using T = TT<D, CG, E8>;
   constexpr int kTok = T::kTok, kTiles = T::kTiles;
   const Geom& g = sh.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -515,6 +640,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   uint64_t* empty = full + T::kDepth;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + T::kBars);
   uint32_t* copied = s_tmem + 4;                               // [kDepth]
+  uint8_t* exps = reinterpret_cast<uint8_t*>(copied + 4);   // [kExpSlots][16]
 
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -628,7 +754,9 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       int sq = (amax > 0.f) ? 135 - ebits : 0;
       sq = sq > 126 ? 126 : (sq < -126 ? -126 : sq);
       const float up = __uint_as_float((uint32_t)(sq + 127) << 23);
-      const float cq = logit_factor(p, sq);
+      float cq = logit_factor(p, sq);
+      // (times a block's power of two it stays above zero and finite: a masked logit stays -inf)
+      if constexpr (E8) cq = fminf(fmaxf(cq, 0x1p-117f), 0x1p62f);
       auto half2_of = [&](uint32_t w) {
         return pack_half2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
       };
@@ -701,13 +829,28 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
             if (tok >= n || tok < lo || !((live >> ((i & ~31) >> psh)) & 1u)) z[i] = -INFINITY;
           }
         }
-        float m8[8];
+        float top;
+        [[maybe_unused]] uint4 ex = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (E8) {
+          ex = *reinterpret_cast<const uint4*>(exps + 16 * (chunks & (T::kExpSlots - 1)));
+          top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m8[i] = z[i];
+          for (int i = 0; i < kTok / 16; ++i) {
+            const Block8 blk(ex, i, cq);
+            float m = fmaxf(z[16 * i], z[16 * i + 1]);
 #pragma unroll
-        for (int i = 8; i < kTok; i += 2) m8[(i >> 1) & 7] = fmax3(m8[(i >> 1) & 7], z[i], z[i + 1]);
-        const float top = cq * fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
-                                     fmaxf(m8[6], m8[7]));
+            for (int k = 2; k < 16; k += 2) m = fmax3(m, z[16 * i + k], z[16 * i + k + 1]);
+            top = fmaxf(top, fmaf(m, blk.c, blk.ve));
+          }
+        } else {
+          float m8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m8[i] = z[i];
+#pragma unroll
+          for (int i = 8; i < kTok; i += 2) m8[(i >> 1) & 7] = fmax3(m8[(i >> 1) & 7], z[i], z[i + 1]);
+          top = cq * fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
+                                       fmaxf(m8[6], m8[7]));
+        }
         // The base moves where a logit would overflow an fp16 weight, and with it what has
         // been summed on the old one.
         const bool moves = top > base + kHeadroom;
@@ -735,17 +878,36 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         // P, 64 tokens at a time, over the first columns they were read from.
 #pragma unroll
         for (int h = 0; h < T::kHalves; ++h) {
-          const float2 c2 = make_float2(cq, cq), b2 = make_float2(-base, -base);
+          float2 c2 = make_float2(cq, cq), b2 = make_float2(-base, -base);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             uint32_t pk[16];
+            if constexpr (E8) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int k = 64 * h + 32 * q + 2 * i;
-              const float2 a = fma2(make_float2(z[k], z[k + 1]), c2, b2);
-              const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
-              sum = add2(sum, e);
-              pk[i] = pack_weights(e.x, e.y);
+              for (int u = 0; u < 2; ++u) {       // a block of 16 tokens
+                const Block8 blk(ex, 4 * h + 2 * q + u, cq);
+                c2 = make_float2(blk.c, blk.c);
+                b2 = make_float2(blk.ve - base, blk.ve - base);
+                float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const int k = 64 * h + 32 * q + 16 * u + 2 * i;
+                  const float2 a = fma2(make_float2(z[k], z[k + 1]), c2, b2);
+                  const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
+                  part = add2(part, e);
+                  pk[8 * u + i] = pack_weights(e.x, e.y);
+                }
+                sum = fma2(part, make_float2(blk.back, blk.back), sum);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int k = 64 * h + 32 * q + 2 * i;
+                const float2 a = fma2(make_float2(z[k], z[k + 1]), c2, b2);
+                const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
+                sum = add2(sum, e);
+                pk[i] = pack_weights(e.x, e.y);
+              }
             }
             tmem_st16u(tS + 64 * h + 16 * q, pk);
           }
@@ -837,8 +999,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     // ==== dequantisation =============================================================
     regs_down<T::kDeqRegs>();
     const int dw = (warp - T::kSoft) & 3;
-    using CK = Converter<T, T::kKRows, D>;
-    using CV = Converter<T, kTok, T::kVDims>;
+    using CK = std::conditional_t<E8, Converter8<T, T::kKRows, D>, Converter<T, T::kKRows, D>>;
+    using CV = std::conditional_t<E8, Converter8<T, kTok, T::kVDims>, Converter<T, kTok, T::kVDims>>;
     const bool v = warp - T::kSoft >= 4;
     const int k0 = rank * T::kKRows, v0 = rank * T::kVDims;
     if constexpr (T::kDeq == 4)
@@ -856,7 +1018,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
                              CV(sh, true, 0, v0, dw, ring, sV, vready, vfree));
   } else if (regs_down<T::kMmaRegs>(), warp == T::kMma + 1) {
     // ==== copies =====================================================================
-    dead = !copy_all<T>(sh, p, span, rank, ring, full, empty, copied);
+    dead = !copy_all<T>(sh, p, span, rank, ring, full, empty, copied, exps);
   } else if (warp == T::kMma && rank == 0) {
     // ==== MMA issue ==================================================================
     const uint32_t one = elect_one();
@@ -1012,11 +1174,11 @@ dense::Shape dense_tile_shape(const Geom& g, int window) {
   };
   dense::set_heads(&s, g);
   if (use_pairs(g)) {
-    if (g.D == 128) set(dense::TT<128, 2>());
-    else set(dense::TT<256, 2>());
+    if (g.D == 128) set(dense::TT<128, 2, false>());   // (8-bit pages alike)
+    else set(dense::TT<256, 2, false>());
   } else {
-    if (g.D == 128) set(dense::TT<128, 1>());
-    else set(dense::TT<256, 1>());
+    if (g.D == 128) set(dense::TT<128, 1, false>());
+    else set(dense::TT<256, 1, false>());
   }
   s.tiles = (g.R * s.G + s.vt - 1) / s.vt;
   s.window = window;
@@ -1032,10 +1194,10 @@ dense::Shape dense_tile_shape(const Geom& g, int window) {
 
 namespace {
 
-template <int D, int CG>
+template <int D, int CG, bool E8>
 cudaError_t launch_tile(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
-  using T = dense::TT<D, CG>;
-  auto* kern = dense::dense_tile_kernel<D, CG>;
+  using T = dense::TT<D, CG, E8>;
+  auto* kern = dense::dense_tile_kernel<D, CG, E8>;
   static_assert(T::kSmem <= 227 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   if (e != cudaSuccess) return e;
@@ -1056,12 +1218,17 @@ cudaError_t launch_tile(const dense::Shape& s, const dense::Work& w, cudaStream_
   return cudaLaunchKernelEx(&cfg, kern, s, w);
 }
 
+template <bool E8>
+cudaError_t launch_tiles(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
+  if (use_pairs(s.g))
+    return s.g.D == 256 ? launch_tile<256, 2, E8>(s, w, stream) : launch_tile<128, 2, E8>(s, w, stream);
+  return s.g.D == 256 ? launch_tile<256, 1, E8>(s, w, stream) : launch_tile<128, 1, E8>(s, w, stream);
+}
+
 }  // namespace
 
-cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
-  if (use_pairs(s.g))
-    return s.g.D == 256 ? launch_tile<256, 2>(s, w, stream) : launch_tile<128, 2>(s, w, stream);
-  return s.g.D == 256 ? launch_tile<256, 1>(s, w, stream) : launch_tile<128, 1>(s, w, stream);
+cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, bool e8, cudaStream_t stream) {
+  return e8 ? launch_tiles<true>(s, w, stream) : launch_tiles<false>(s, w, stream);
 }
 
 }  // namespace qsa

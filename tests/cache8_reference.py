@@ -124,3 +124,84 @@ def geometry(seed, B, R, Hkv, D, P, lo, hi, G=4, holes=0.0, spare=2):
 def on_gpu(w, device="cuda"):
     return {n: torch.from_numpy(np.ascontiguousarray(x)).to(device) if isinstance(x, np.ndarray) else x
             for n, x in w.items()}
+
+
+# ---------------------------------------------------------------------------
+# attention in 64 bits, with a bound of the kernels' error for every output
+# ---------------------------------------------------------------------------
+
+def attend(q, k, v, sm, extra=None, exps=None, weight=2.0**-11, alike=False):
+    """One KV head's vectors q [G, D] over the tokens k, v [n, D] they see: out, lse and their bounds.
+
+    With p the normalised weights, M the largest logit, A the largest sum_d |q_d K_d| of a token:
+      2^-8 |out|                    the output's bf16 (half a step)
+      8 weight sqrt(sum p^2 V^2)    the weights' roundings to nearest of up to `weight` each
+                                    (Hoeffding: beyond 8 with probability 2 e^-32); rows whose weights
+                                    are alike round alike, `alike`: weight sum p |V|
+      (2 dz + 2^-17) sum p |V|      logits: D / 16 steps of the matrix instruction and two more
+                                    roundings, dz = (D / 16 + 2) 2^-23 A; the exponent's fp32
+                                    argument (below 2^7: half a step of 2^-17, twice) and its approximation
+      2^-33 max(e^(z - lse) 2^e) sum |V| 2^-e     with fp16 weights (exps: the tokens' exponents of V, 0
+                                    without): those below 2^-14 of the base's are subnormal, half a step
+                                    of 2^-24; the base lies 2^8 below the largest or lower
+    and of lse  2 dz + 2^-16 + 2^-21 |lse|."""
+    G, D = q.shape
+    if not len(k):
+        # (a sink alone: its fp32 products with log2(e) and ln(2), two roundings and two rounded
+        # constants of 2^-24 each)
+        lse = np.full(G, -np.inf) if extra is None else np.asarray(extra, dtype=np.float64)
+        return np.zeros((G, D)), lse, np.zeros((G, D)), 4 * 2.0**-24 * np.abs(lse)
+    z = q @ k.T * sm
+    top = z.max(-1) if extra is None else np.maximum(z.max(-1), extra)
+    total = np.exp(z - top[:, None]).sum(-1)
+    if extra is not None:
+        total = total + np.exp(extra - top)
+    lse = top + np.log(total)
+    p, a = np.exp(z - lse[:, None]), np.abs(v)
+    out, mag = p @ v, p @ a
+    dz = (D / 16 + 2) * 2.0**-23 * (np.abs(q) @ np.abs(k).T).max(-1) * sm
+    spread = weight * mag if alike else 8 * weight * np.sqrt(p**2 @ a**2)
+    tol = 2.0**-8 * np.abs(out) + spread + (2 * dz + 2.0**-17)[:, None] * mag
+    if weight == 2.0**-11:
+        two = np.ones(len(k)) if exps is None else np.exp2(exps.astype(np.float64) - 127)
+        tol = tol + 2.0**-33 * (p * two).max(-1)[:, None] * (a / two[:, None]).sum(0)
+    return out, lse, tol, 2 * dz + 2.0**-16 + 2.0**-21 * np.abs(lse)
+
+
+def dense(w, window=0, sinks=None, q=None, alike=False):
+    """Dense attention over the 8-bit cache of w (on the host): out, lse and their bounds."""
+    B, R, Hq, Hkv, D, P, MB, NP = (w[n] for n in ("batch", "rows_per_req", "num_q_heads", "num_kv_heads",
+                                                  "head_dim", "page_size", "max_blocks", "num_pages"))
+    G, q = Hq // Hkv, np.asarray(w["q"] if q is None else q, dtype=np.float64)
+    res = [np.zeros((B * R, Hq, D)), np.zeros((B * R, Hq)), np.zeros((B * R, Hq, D)), np.zeros((B * R, Hq))]
+    for b in range(B):
+        n = [min(max(int(w["seqlens"][b]) - R + 1 + j, 0), MB * P) for j in range(R)]
+        blocks = np.array([i for i in range(-(-n[-1] // P)) if 0 <= w["page_table"][b, i] < NP], dtype=np.int64)
+        pages = w["page_table"][b, blocks]
+        at = (blocks.reshape(-1, 1) * P + np.arange(P)).reshape(-1)
+        for h in range(Hkv):
+            ex = [np.clip(w[x][pages, h], 95, 191) for x in ("k_exp", "v_exp")]
+            k = cached(w["k_pool"][pages, h], ex[0]).reshape(len(at), D)
+            v = cached(w["v_pool"][pages, h], ex[1]).reshape(len(at), D)
+            ve = np.repeat(ex[1], BLOCK, -1).reshape(-1)
+            hs = slice(h * G, (h + 1) * G)
+            for j in range(R):
+                see = (at < n[j]) & (at >= (n[j] - window if window else 0))
+                extra = None if sinks is None else np.asarray(sinks, dtype=np.float64)[hs]
+                got = attend(q[b * R + j, hs], k[see], v[see], float(np.float32(w["sm_scale"])), extra, ve[see],
+                             alike=alike)
+                for r, x in zip(res, got):
+                    r[b * R + j, hs] = x
+    return res
+
+
+def compare(got, got_lse, ref):
+    """Asserts that results (tensors) are within the bounds of a reference's."""
+    out, lse, tol, lse_tol = ref
+    got, got_lse = got.detach().double().cpu().numpy(), got_lse.detach().double().cpu().numpy()
+    err = np.abs(got - out)
+    assert (err <= tol).all(), (np.nanmax(err), np.nanmax(err / np.maximum(tol, 1e-300)), np.isnan(err).sum())
+    fin = np.isfinite(lse)
+    np.testing.assert_array_equal(np.isneginf(got_lse), ~fin)
+    e = np.abs(got_lse[fin] - lse[fin])
+    assert (e <= lse_tol[fin]).all(), (e.max(), (e / lse_tol[fin]).max())

@@ -1,0 +1,236 @@
+"""Dense attention over the 8-bit cache on the GPU against 64 bits: every kernel
+(few vectors, tiles, pairs of CTAs), masks that leave rows empty, scales far apart,
+and what pages hold where nobody looks."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache8_reference as c8
+import nvfp4_block_sparse_gb300 as qsa
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def geom(w):
+    return qsa.make_geom(**{n: w[n] for n in qsa.GEOM_FIELDS})
+
+
+def queries(w, seed=0, scale=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    Hq = w["num_q_heads"]
+    x = torch.randn(w["batch"] * w["rows_per_req"], Hq, w["head_dim"], generator=g, device=DEV)
+    return (x * torch.linspace(0.5, 2.0, Hq, device=DEV)[:, None] * scale).to(torch.bfloat16)
+
+
+def run(w, q, window=0, sinks=None, d=None, ws=None, stream=None):
+    d = c8.on_gpu(w) if d is None else d
+    g = geom(w)
+    if ws is None:
+        ws = torch.empty(qsa.qsa_dense_attention_fp8_workspace_bytes(g), dtype=torch.uint8, device=DEV)
+        qsa.qsa_workspace_init(ws)
+    T = w["batch"] * w["rows_per_req"]
+    out = torch.full((T, w["num_q_heads"], w["head_dim"]), 9.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T, w["num_q_heads"]), 9.0, device=DEV)
+    qsa.qsa_dense_attention_fp8(g, q, d["k_pool"], d["k_exp"], d["v_pool"], d["v_exp"], w["sm_scale"], d["page_table"],
+                                d["seqlens"], out, lse, ws, window=window, sinks=sinks, stream=stream)
+    torch.cuda.synchronize()
+    assert qsa.qsa_workspace_status(ws) == 0
+    return out, lse
+
+
+def check(w, window=0, sinks=False, seed=0, scale=1.0, alike=False, q=None):
+    q = queries(w, seed, scale) if q is None else q
+    s = torch.linspace(-2, 6, w["num_q_heads"], device=DEV) if sinks else None
+    out, lse = run(w, q, window, s)
+    c8.compare(out, lse, c8.dense(w, window, None if s is None else s.cpu().numpy(), q.float().cpu().numpy(), alike))
+
+
+# every kernel: vectors per KV head 1, 3, 8 (one tile of eight), 12, 16; 18, 40, 100, 130 (tiles), 300 and
+# more (pairs at both head dims)
+@pytest.mark.parametrize("D,P", [(128, 64), (128, 128), (256, 32), (256, 64)])
+@pytest.mark.parametrize("B,R,Hkv,G,lo,hi,window,sinks,holes", [
+    (1, 1, 1, 1, 1, 1, 0, False, 0), (3, 1, 2, 3, 1, 700, 0, False, 0), (5, 2, 3, 4, 1, 500, 100, True, 0.2),
+    (2, 3, 1, 4, 2000, 2500, 0, True, 0.1), (4, 4, 2, 4, 3, 900, 37, False, 0), (3, 6, 2, 3, 300, 1100, 0, False, 0.1),
+    (2, 10, 1, 4, 1, 1300, 0, True, 0), (2, 25, 2, 4, 20, 900, 200, False, 0.1), (1, 130, 1, 1, 100, 700, 0, False, 0),
+    (2, 75, 1, 4, 50, 1500, 0, False, 0.1), (1, 77, 2, 8, 900, 900, 130, True, 0), (1, 40, 1, 16, 30, 33, 1, False, 0)])
+def test_dense(D, P, B, R, Hkv, G, lo, hi, window, sinks, holes):
+    w = c8.geometry(D + B + R, B, R, Hkv, D, P, lo, hi, G=G, holes=holes)
+    check(w, window, sinks)
+
+
+@pytest.mark.parametrize("D,P", [(128, 64), (256, 32)])
+@pytest.mark.parametrize("R,G", [(1, 4), (4, 4), (9, 4), (70, 8)])
+def test_rows_that_see_nothing(D, P, R, G):
+    w = c8.geometry(2, 5, R, 2, D, P, 1, 300, G=G)
+    w["seqlens"] = np.array([0, max(R - 2, 0), R + 1, 200, 64], np.int32)
+    w["page_table"][3] = -1
+    w["page_table"][4] = w["num_pages"]
+    for sinks in (False, True):
+        check(w, sinks=sinks)
+        check(w, window=3, sinks=sinks)
+
+
+@pytest.mark.parametrize("R,G", [(1, 8), (2, 8), (5, 8), (64, 8)])
+@pytest.mark.parametrize("D,P", [(128, 128), (256, 64)])
+def test_scales_far_apart(D, P, R, G):
+    """Blocks of V and K whose scales differ as far as they can, zeros among them."""
+    w = c8.geometry(3, 2, R, 1, D, P, 400, 640, G=G)
+    rng = np.random.default_rng(1)
+    w["v_exp"] = rng.integers(95, 192, w["v_exp"].shape).astype(np.uint8)
+    w["k_exp"] = rng.integers(100, 120, w["k_exp"].shape).astype(np.uint8)
+    w["v_exp"][::3], w["v_pool"][::3] = 95, 0
+    check(w, alike=True)
+    # all values tiny, or all huge
+    for e in (95, 191):
+        w["v_exp"][:] = e
+        check(w)
+
+
+def test_sinks_next_to_zeros():
+    """First tokens that take nearly all the weight and have values of nothing."""
+    for R in (1, 3, 40):
+        w = c8.geometry(4, 2, R, 2, 128, 64, 300, 500, G=4)
+        q = queries(w)
+        first = w["page_table"][:, 0]
+        w["v_pool"][first, :, :16] = 0
+        w["v_exp"][first, :, 0] = 95
+        w["k_pool"][first, :, 0] = c8.codes_of(np.broadcast_to(q[0, 0].float().cpu().numpy() * 30, (2, 2, 128)).clip(-448, 448))
+        w["k_exp"][first, :, 0] = 127
+        check(w, q=q, alike=True)
+
+
+@pytest.mark.parametrize("R,G", [(1, 4), (4, 4), (9, 4), (70, 8)])
+@pytest.mark.parametrize("D,P", [(128, 64), (256, 32)])
+def test_what_nobody_sees(R, G, D, P):
+    """NaN codes and exponents of any bits behind the last token, before the window and in spare pages."""
+    w = c8.geometry(5, 3, R, 2, D, P, 200, 400, G=G)
+    q, window = queries(w), 60 + R
+    plain = run(w, q, window)
+    for b in range(3):
+        L = int(w["seqlens"][b])
+        for i in range(w["max_blocks"]):
+            page = w["page_table"][b, i]
+            for slot in range(P):
+                tok = i * P + slot
+                if tok >= L or tok < L - R + 1 - window:
+                    for n in ("k_pool", "v_pool"):
+                        w[n][page, :, slot] = 0x7F if slot % 2 else 0xFF
+                    whole = range(tok - tok % 16, tok - tok % 16 + 16)
+                    if all(t >= L or t < L - R + 1 - window for t in whole):
+                        for n in ("k_exp", "v_exp"):
+                            w[n][page, :, slot // 16] = 255 if i % 2 else 0
+    got = run(w, q, window)
+    assert all(torch.equal(a, b) for a, b in zip(plain, got))
+
+
+@pytest.mark.parametrize("R,G", [(1, 4), (9, 4), (70, 8)])
+def test_not_finite(R, G):
+    """A row with NaN or infinite queries, and the rows that see a NaN key, have no finite lse or out; others
+    are as they were."""
+    w = c8.geometry(6, 3, R, 1, 128, 64, 200, 400, G=G)
+    q = queries(w)
+    plain = run(w, q)
+    q2 = q.clone()
+    q2[0, 0, 5], q2[R, 1, 7] = math.nan, math.inf
+    out, lse = run(w, q2)
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    hit[0, 0] = hit[R, 1] = True
+    assert not torch.isfinite(lse[hit]).any() and not torch.isneginf(lse[hit]).any() and torch.isnan(out[hit]).all()
+    assert torch.equal(out[~hit], plain[0][~hit]) and torch.equal(lse[~hit], plain[1][~hit])
+    w["k_pool"][w["page_table"][2, 1], 0, 3, 17] = 0x7F
+    out, lse = run(w, q)
+    assert torch.isnan(lse[2 * R:]).all() and torch.isnan(out[2 * R:]).all()
+    assert torch.equal(out[:2 * R], plain[0][:2 * R])
+
+
+def test_large_logits_and_small_queries():
+    for R, G in ((1, 4), (3, 4), (9, 4)):
+        w = c8.geometry(7, 2, R, 2, 128, 64, 300, 500, G=G)
+        check(w, scale=1e-30)
+        w["sm_scale"] = 1e-6
+        check(w)
+        w["sm_scale"] = 1.0         # logits of some tens to a hundred: one token takes all
+        check(w, scale=0.5, alike=True)
+
+
+@pytest.mark.parametrize("R,G", [(1, 4), (4, 4), (70, 8)])
+def test_same_bits_streams_graphs_shared_workspace(R, G):
+    w = c8.geometry(8, 4, R, 2, 128, 64, 1000, 3000, G=G)
+    d, q = c8.on_gpu(w), queries(w)
+    g = geom(w)
+    # one workspace for both caches' calls, and for another geometry
+    other = c8.geometry(9, 2, 3, 2, 256, 32, 50, 90, G=2)
+    n = max(qsa.qsa_dense_attention_fp8_workspace_bytes(x) for x in (g, geom(other)))
+    ws = torch.empty(max(n, qsa.qsa_dense_attention_workspace_bytes(g)), dtype=torch.uint8, device=DEV)
+    qsa.qsa_workspace_init(ws)
+    plain = run(w, q, d=d, ws=ws)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        run(other, queries(other), ws=ws)
+        got = run(w, q, d=d, ws=ws, stream=side)
+        assert all(torch.equal(a, b) for a, b in zip(plain, got))
+    out, lse = torch.empty_like(plain[0]), torch.empty_like(plain[1])
+    call = lambda: qsa.qsa_dense_attention_fp8(g, q, d["k_pool"], d["k_exp"], d["v_pool"], d["v_exp"],  # noqa: E731
+                                               w["sm_scale"], d["page_table"], d["seqlens"], out, lse, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
+    d["seqlens"].sub_(700)              # the captured call follows the lengths
+    graph.replay()
+    torch.cuda.synchronize()
+    want = run(dict(w, seqlens=w["seqlens"] - 700), q)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_against_the_nvfp4_cache():
+    """Values that both caches hold exactly give the same attention within the outputs' rounding."""
+    w = c8.geometry(10, 2, 3, 2, 128, 64, 300, 400, G=4)
+    rng = np.random.default_rng(0)
+    vals = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+    for n in ("k", "v"):
+        code = rng.integers(0, 16, (w["num_pages"], 2, 64, 128)).astype(np.uint8)
+        w[n + "4"] = code[..., 0::2] | code[..., 1::2] << 4
+        w[n + "4_sf"] = np.full((w["num_pages"], 2, 64, 8), 0x38, np.uint8)      # 1.0
+        w[n + "_pool"] = c8.codes_of(np.where(code & 8, -1, 1) * vals[code & 7])
+        w[n + "_exp"][:] = 127
+    d, q = c8.on_gpu(w), queries(w)
+    got = run(w, q, d=d)
+    g = geom(w)
+    ws = torch.empty(qsa.qsa_dense_attention_workspace_bytes(g), dtype=torch.uint8, device=DEV)
+    qsa.qsa_workspace_init(ws)
+    out, lse = torch.empty_like(got[0]), torch.empty_like(got[1])
+    qsa.qsa_dense_attention(g, q, d["k4"], d["k4_sf"], d["v4"], d["v4_sf"], 1.0, 1.0, w["sm_scale"], d["page_table"],
+                            d["seqlens"], out, lse, ws)
+    c8.compare(out, lse, c8.dense(w, q=q.float().cpu().numpy()))
+    c8.compare(*got, c8.dense(w, q=q.float().cpu().numpy()))
+
+
+def test_refused():
+    w = c8.geometry(11, 2, 3, 2, 128, 64, 30, 60)
+    d, q = c8.on_gpu(w), queries(w)
+    g = geom(w)
+    ws = torch.empty(qsa.qsa_dense_attention_fp8_workspace_bytes(g), dtype=torch.uint8, device=DEV)
+    qsa.qsa_workspace_init(ws)
+    out, lse = torch.empty_like(q), torch.empty(6, 8, device=DEV)
+    def call(q=q, out=out, lse=lse, ws=ws, sm=0.1, **kw):
+        a = dict(d, **{k: v for k, v in kw.items() if k not in ("window", "sinks")})
+        qsa.qsa_dense_attention_fp8(g, q, a["k_pool"], a["k_exp"], a["v_pool"], a["v_exp"], sm, a["page_table"],
+                                    a["seqlens"], out, lse, ws, window=kw.get("window", 0), sinks=kw.get("sinks"))
+    call()
+    for kw in (dict(q=q[:5]), dict(q=q.cpu()), dict(out=out[:, :4]), dict(lse=lse[:5]), dict(k_exp=d["k_exp"][1:]),
+               dict(v_pool=d["v_pool"][:, :1]), dict(sinks=torch.zeros(7, device=DEV)), dict(q=q.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    for kw in (dict(q=q.half()), dict(lse=lse.double()), dict(v_exp=d["v_exp"].to(torch.int8))):
+        with pytest.raises(TypeError):
+            call(**kw)
+    for kw in (dict(ws=ws[:-256]), dict(sm=0.0), dict(sm=math.nan), dict(window=-1), dict(ws=ws[1:])):
+        with pytest.raises(qsa.QsaError):
+            call(**kw)
