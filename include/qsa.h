@@ -748,6 +748,50 @@ qsa_status_t qsa_dense_attention_fp8(const qsa_geom_t *geom, const void *q_bf16,
                                      cudaStream_t stream);
 
 /*
+ * Attention over whole prompts, before they are in a cache (or without one):
+ * B sequences packed behind one another, causal, grouped heads.
+ *
+ *   q          bf16, row r at q + r * q_row_stride (elements), its Hq heads of D
+ *              behind one another; k and v likewise with Hkv heads
+ *   cu_seqlens int32 [B + 1], rising: sequence b is rows cu_seqlens[b]..
+ *              cu_seqlens[b + 1] - 1; lengths of 0 are allowed
+ *   total_rows rows that q, k and v have: 0..2^24 (0: nothing is launched).
+ *              cu_seqlens beyond it is held at it
+ *   window     tokens a row looks back over, itself included; 0: all
+ *   sinks      fp32 [Hq], or NULL, as in qsa_dense_attention
+ *   out        bf16 [total_rows, Hq, D], lse fp32 [total_rows, Hq]   output; rows
+ *              of no sequence are left as they were
+ *   workspace  >= qsa_prompt_attention_workspace_bytes() bytes (its status word),
+ *              256-byte aligned, zero-filled once by qsa_workspace_init()
+ *
+ * Row i of a sequence sees its rows max(0, i + 1 - window)..i.  Of the geometry
+ * batch, the heads and head_dim matter.  Logits, sums and outputs are fp32,
+ * weights exp(z_t - lse) are rounded to bf16 (8 bits) before the product with V.
+ * What lies outside a sequence's rows is not looked at.  Keys that are not
+ * finite make so the rows that see them, and values that are not also rows
+ * of their sequence up to 512 before them.
+ * The result does not depend on how the work is divided: the same inputs give
+ * the same bits.
+ *
+ * Returns QSA_ERR_INVALID_ARG for null pointers, row strides below the heads' D
+ * elements, not a multiple of 8 or of 2^39 and more, total_rows outside these,
+ * window < 0, sm_scale not positive and finite, q, k, v or out not 16-byte
+ * aligned; QSA_ERR_UNSUPPORTED for more than 128 query heads per KV head;
+ * QSA_ERR_WORKSPACE for a missing, short or misaligned workspace; geometry and
+ * device checks as for the other calls.  A bounded device wait that gives up is
+ * reported through qsa_workspace_status().
+ */
+size_t qsa_prompt_attention_workspace_bytes(const qsa_geom_t *geom, int64_t total_rows);
+qsa_status_t qsa_prompt_attention(const qsa_geom_t *geom, const void *q_bf16,
+                                  int64_t q_row_stride, const void *k_bf16,
+                                  int64_t k_row_stride, const void *v_bf16,
+                                  int64_t v_row_stride, const int32_t *cu_seqlens,
+                                  int64_t total_rows, float sm_scale, int window,
+                                  const float *sinks, void *out_bf16, float *lse,
+                                  void *workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/*
  * Diagnostics: sets the bound, in nanoseconds, of the waits of the head_dim
  * 128 sparse decode kernel for its page copies (2 s by default; 0 restores
  * the default).  Process-wide, for tests of the timeout reporting: a bound
@@ -772,7 +816,8 @@ void qsa_debug_set_wait_ns(unsigned long long ns);
  * Codes are 0xF0S: F the source file (1 decode-row attention, 2 decode and
  * verify attention, 3 index scores, 4 selection, 5 token store, 6 rollback,
  * 7 row-tile attention, 8 norms, rotation and cache rows, 9 and A dense
- * attention, B the 8-bit cache's rows, C dense attention over it), S the check.  Not thread-safe against concurrent
+ * attention, B the 8-bit cache's rows, C dense attention over it, D prompt
+ * attention), S the check.  Not thread-safe against concurrent
  * calls of the library.
  */
 int qsa_debug_bounds_status(void);

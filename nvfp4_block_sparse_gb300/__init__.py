@@ -26,7 +26,8 @@ from .binding import (EXPORTS, QsaError, load, make_geom, qsa_geom_t, qsa_index_
                       qsa_load_kv_tokens, qsa_dense_attention, qsa_dense_attention_workspace_bytes,
                       make_rope_axes, qsa_rope_axes_t, qsa_rope_axes_rows, qsa_store_kv_tokens_fp8,
                       qsa_load_kv_tokens_fp8, qsa_dense_attention_fp8,
-                      qsa_dense_attention_fp8_workspace_bytes)
+                      qsa_dense_attention_fp8_workspace_bytes, qsa_prompt_attention,
+                      qsa_prompt_attention_workspace_bytes)
 
 __all__ = [
     "EXPORTS", "QsaError", "load", "make_geom", "qsa_geom_t", "qsa_index_scores",
@@ -42,7 +43,7 @@ __all__ = [
     "qsa_qk_norm_rope", "qsa_store_kv_tokens_rope", "qsa_load_kv_tokens", "qsa_dense_attention",
     "qsa_dense_attention_workspace_bytes", "make_rope_axes", "qsa_rope_axes_t", "qsa_rope_axes_rows",
     "qsa_store_kv_tokens_fp8", "qsa_load_kv_tokens_fp8", "qsa_dense_attention_fp8",
-    "qsa_dense_attention_fp8_workspace_bytes",
+    "qsa_dense_attention_fp8_workspace_bytes", "qsa_prompt_attention", "qsa_prompt_attention_workspace_bytes",
     "DecodeStep", "DenseStep", "MAX_DECODE_ROWS",
 ]
 

@@ -56,6 +56,8 @@ EXPORTS = (
     "qsa_load_kv_tokens_fp8",
     "qsa_dense_attention_fp8_workspace_bytes",
     "qsa_dense_attention_fp8",
+    "qsa_prompt_attention_workspace_bytes",
+    "qsa_prompt_attention",
 )
 
 ROPE_LAYOUTS = {"sections": 0, "interleaved": 1, "spectra": 2}
@@ -187,6 +189,11 @@ def load(build_if_missing: bool = False):
     lib.qsa_store_kv_tokens_fp8.argtypes = [G, _vp, i64, _vp, i64, _vp, i64] + [_vp] * 7
     lib.qsa_load_kv_tokens_fp8.restype = st
     lib.qsa_load_kv_tokens_fp8.argtypes = [G, _vp, i64] + [_vp] * 9
+    lib.qsa_prompt_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.qsa_prompt_attention_workspace_bytes.argtypes = [G, i64]
+    lib.qsa_prompt_attention.restype = st
+    lib.qsa_prompt_attention.argtypes = ([G, _vp, i64, _vp, i64, _vp, i64, _vp, i64, f32, ctypes.c_int] +
+                                         [_vp] * 4 + [ctypes.c_size_t, _vp])
     lib.qsa_dense_attention_fp8_workspace_bytes.restype = ctypes.c_size_t
     lib.qsa_dense_attention_fp8_workspace_bytes.argtypes = [G]
     lib.qsa_dense_attention_fp8.restype = st
@@ -708,3 +715,26 @@ def qsa_dense_attention_fp8(geom, q, k_pool, k_exp, v_pool, v_exp, sm_scale, pag
         None if sinks is None else _at(sinks, _F32, "sinks", g.num_q_heads, dev),
         _at(out, _BF16, "out", m * D, dev), _at(lse, _F32, "lse", m, dev),
         _at(workspace, _U8, "workspace", 0, dev), workspace.numel()))
+
+
+def qsa_prompt_attention_workspace_bytes(geom, total_rows) -> int:
+    return int(load().qsa_prompt_attention_workspace_bytes(ctypes.byref(_geom(geom)), int(total_rows)))
+
+
+def qsa_prompt_attention(geom, q, k, v, cu_seqlens, sm_scale, out, lse, workspace, window=0, sinks=None,
+                         stream=None):
+    """Causal attention of packed sequences: q [T, Hq, D], k and v [T, Hkv, D] (views into one
+    projection's rows, say), sequence b in rows cu_seqlens[b]..cu_seqlens[b + 1] - 1 (int32 [B + 1])."""
+    g = _geom(geom)
+    Hq, Hkv, D = g.num_q_heads, g.num_kv_heads, g.head_dim
+    dev = _device(q, "q")
+    T = q.shape[0]
+    qp, qs = _rows_at(q, Hq, D, "q", T, dev)
+    kp, ks = _rows_at(k, Hkv, D, "k", T, dev)
+    vp, vs = _rows_at(v, Hkv, D, "v", T, dev)
+    args = (ctypes.byref(g), qp, qs, kp, ks, vp, vs, _at(cu_seqlens, _I32, "cu_seqlens", g.batch + 1, dev), T,
+            sm_scale, window, None if sinks is None else _at(sinks, _F32, "sinks", Hq, dev),
+            _at(out, _BF16, "out", T * Hq * D, dev), _at(lse, _F32, "lse", T * Hq, dev),
+            _at(workspace, _U8, "workspace", 0, dev), workspace.numel())
+    if T:
+        _launch(load().qsa_prompt_attention, dev, stream, args)

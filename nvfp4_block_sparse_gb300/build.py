@@ -18,7 +18,8 @@ BOUNDS_LIB = os.path.join(HERE, "libqsa_bounds.so")
 SOURCES = ["qsa_api.cu", "qsa_index_scores.cu", "qsa_select_topk.cu", "qsa_sparse_decode.cu",
            "qsa_attend.cu",
            "qsa_sparse_decode_noalloc.cu", "qsa_store_tokens.cu", "qsa_rollback.cu",
-           "qsa_sparse_prefill.cu", "qsa_prologue.cu", "qsa_dense.cu", "qsa_dense_tile.cu", "qsa_cache8.cu", "qsa_dense8.cu"]
+           "qsa_sparse_prefill.cu", "qsa_prologue.cu", "qsa_dense.cu", "qsa_dense_tile.cu", "qsa_cache8.cu", "qsa_dense8.cu",
+           "qsa_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

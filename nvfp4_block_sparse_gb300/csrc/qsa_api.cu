@@ -286,6 +286,12 @@ qsa_status_t check_dense_geom(const qsa_geom_t* geom) {
   return geom->num_q_heads / geom->num_kv_heads > 128 ? QSA_ERR_UNSUPPORTED : QSA_OK;
 }
 
+qsa_status_t check_prompt(const qsa_geom_t* geom, int64_t total_rows) {
+  const qsa_status_t st = check_dense_geom(geom);
+  if (st != QSA_OK) return st;
+  return total_rows < 0 || total_rows > kMaxPackedRows ? QSA_ERR_INVALID_ARG : QSA_OK;
+}
+
 }  // namespace
 
 namespace qsa {
@@ -309,7 +315,7 @@ int qsa_debug_bounds_status(void) {
                 qsa::bounds_word_select(), qsa::bounds_word_store(), qsa::bounds_word_rollback(),
                 qsa::bounds_word_prefill(), qsa::bounds_word_prologue(), qsa::bounds_word_dense(),
                 qsa::bounds_word_dense_tile(), qsa::bounds_word_cache8(),
-                qsa::bounds_word_dense8()}) {
+                qsa::bounds_word_dense8(), qsa::bounds_word_prompt()}) {
     if (v < 0) return -1;
     if (first == 0) first = v;
   }
@@ -793,6 +799,40 @@ qsa_status_t qsa_dense_attention_fp8(const qsa_geom_t* geom, const void* q_bf16,
   a.window = window; a.sinks = sinks;
   a.out = out_bf16; a.lse = lse; a.workspace = workspace;
   return from_cuda(qsa::launch_dense8(g, a, stream));
+}
+
+size_t qsa_prompt_attention_workspace_bytes(const qsa_geom_t* geom, int64_t total_rows) {
+  return check_prompt(geom, total_rows) == QSA_OK ? 256 : 0;
+}
+
+qsa_status_t qsa_prompt_attention(const qsa_geom_t* geom, const void* q_bf16, int64_t q_row_stride,
+                                  const void* k_bf16, int64_t k_row_stride, const void* v_bf16,
+                                  int64_t v_row_stride, const int32_t* cu_seqlens,
+                                  int64_t total_rows, float sm_scale, int window,
+                                  const float* sinks, void* out_bf16, float* lse, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream) {
+  qsa_status_t st = check_prompt(geom, total_rows);
+  if (st != QSA_OK) return st;
+  if (!cu_seqlens || !out_bf16 || !lse || !aligned(out_bf16, 16) || window < 0 || !positive(sm_scale))
+    return QSA_ERR_INVALID_ARG;
+  // (a tensor map's strides have 40 bits of bytes)
+  if (!rows_ok(q_bf16, q_row_stride, geom->num_q_heads, geom->head_dim) ||
+      !rows_ok(k_bf16, k_row_stride, geom->num_kv_heads, geom->head_dim) ||
+      !rows_ok(v_bf16, v_row_stride, geom->num_kv_heads, geom->head_dim) ||
+      q_row_stride >= (1LL << 39) || k_row_stride >= (1LL << 39) || v_row_stride >= (1LL << 39))
+    return QSA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < 256 || !aligned(workspace, 256)) return QSA_ERR_WORKSPACE;
+  st = check_device();
+  if (st != QSA_OK || total_rows == 0) return st;
+  qsa::PromptArgs a = {};
+  a.q = q_bf16; a.k = k_bf16; a.v = v_bf16;
+  a.q_stride = q_row_stride; a.k_stride = k_row_stride; a.v_stride = v_row_stride;
+  a.rows = total_rows;
+  a.cu = cu_seqlens;
+  a.sm_scale = sm_scale;
+  a.window = window; a.sinks = sinks;
+  a.out = out_bf16; a.lse = lse; a.workspace = workspace;
+  return from_cuda(qsa::launch_prompt(to_geom(geom), a, stream));
 }
 
 int qsa_select_sparse_decode_fused(const qsa_geom_t* geom) {

@@ -350,6 +350,21 @@ cudaError_t launch_dense(const Geom& g, const DenseArgs& a, cudaStream_t stream)
 size_t dense8_workspace_bytes(const Geom& g);
 cudaError_t launch_dense8(const Geom& g, const DenseArgs& a, cudaStream_t stream);
 
+// Attention over whole packed prompts (qsa_prompt.cu).
+struct PromptArgs {
+  const void *q, *k, *v;
+  long long q_stride, k_stride, v_stride;   // row strides in elements
+  long long rows;
+  const int32_t* cu;         // [B + 1]
+  float sm_scale;
+  int window;                // tokens a row looks back over, itself included; 0: all
+  const float* sinks;        // [Hq], or null
+  void* out;
+  float* lse;
+  void* workspace;
+};
+cudaError_t launch_prompt(const Geom& g, const PromptArgs& a, cudaStream_t stream);
+
 struct DecodePlan {
   int splits;        // KV splits per (request, KV head, query group)
   int qgroups;       // query-column groups per (request, KV head)
@@ -374,6 +389,7 @@ int bounds_word_dense();
 int bounds_word_dense_tile();
 int bounds_word_cache8();
 int bounds_word_dense8();
+int bounds_word_prompt();
 #endif
 
 // Bound of the attention kernels' waits for their chunk copies, in ns

@@ -195,6 +195,37 @@ def dense(w, window=0, sinks=None, q=None, alike=False):
     return res
 
 
+def prompt(q, k, v, cu, sm, window=0, sinks=None, alike=False):
+    """Packed causal attention q [T, Hq, D], k, v [T, Hkv, D]: out, lse (NaN in rows of no sequence)
+    and their bounds: as of attend(), with bf16 weights."""
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    G = Hq // Hkv
+    res = [np.full((T, Hq, D), np.nan), np.full((T, Hq), np.nan), np.zeros((T, Hq, D)), np.zeros((T, Hq))]
+    for a, b in zip(cu[:-1], cu[1:]):
+        n = b - a
+        if n == 0:
+            continue
+        back = np.arange(n)[:, None] - np.arange(n)
+        see = (back >= 0) & ((back < window) if window else True)
+        for h in range(Hq):
+            kk, vv, qq = k[a:b, h // G], v[a:b, h // G], q[a:b, h]
+            z = np.where(see, qq @ kk.T * sm, -np.inf)
+            top = z.max(-1) if sinks is None else np.maximum(z.max(-1), sinks[h])
+            total = np.exp(z - top[:, None]).sum(-1) + (0 if sinks is None else np.exp(sinks[h] - top))
+            lse = top + np.log(total)
+            p, mag_v = np.exp(z - lse[:, None]), np.abs(vv)
+            out, mag = p @ vv, p @ mag_v
+            dz = (D / 16 + 2) * 2.0**-23 * np.where(see, np.abs(qq) @ np.abs(kk).T, 0).max(-1) * sm
+            spread = 2.0**-9 * mag * (2 if alike else 1)
+            if not alike:     # (Hoeffding where there are many, the sum of all roundings where there are few)
+                spread = np.minimum(spread * 2, 8 * 2.0**-9 * np.sqrt(p**2 @ mag_v**2))
+            res[0][a:b, h], res[1][a:b, h] = out, lse
+            res[2][a:b, h] = 2.0**-8 * np.abs(out) + spread + (2 * dz + 2.0**-17)[:, None] * mag
+            res[3][a:b, h] = 2 * dz + 2.0**-16 + 2.0**-21 * np.abs(lse)
+    return res
+
+
 def compare(got, got_lse, ref):
     """Asserts that results (tensors) are within the bounds of a reference's."""
     out, lse, tol, lse_tol = ref
