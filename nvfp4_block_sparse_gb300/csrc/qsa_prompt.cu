@@ -12,7 +12,8 @@
 // heads that share it, as one TMA box brings them, so that a chunk of keys is read once for
 // all its heads and short sequences still fill tiles.  A unit is the tiles of a pair of CTAs
 // (cta_group::2: each SM has half of every K and V tile, and feeds half of the B operand): four
-// at head_dim 128, two at 256.  It walks its chunks of 128 tokens up to the last row's own.
+// at head_dim 128, two at 256.  It walks its chunks of 128 tokens from the first that its rows see up to
+// the last row's own.
 //
 // Units of one sequence differ in length (causal).  They are dealt to the pairs longest first,
 // there and back: the r-th turn goes to pairs 0, 1, ... where r is even and ..., 1, 0 where it
@@ -23,6 +24,18 @@
 // bf16 has fp32's exponents, so no weight is lost to the base; it is the exact maximum of the first
 // tokens, and moves when a later logit is 2^8 above it.
 //
+// Measured (GB300): 8192 tokens, 32 heads on 4 of 128: 324 us, 1.70 PFLOP/s (0.88 of the measured
+// cuBLAS rate); 16 on 2 of 256: 272 us, 2.02 PFLOP/s; 4 prompts of 3000 to 4096 with a window of
+// 1024: 169 us; 6 of 329 to 1993, 24 on 2 of 256: 97 us; one of 77: 7.8 us.  A chunk's turn of two
+// tiles takes 3130 cycles of which its MMAs need 2048: from one tile's S to its next O pass S's
+// commit (450 cycles until a warp sees it), the softmax (ld 180, maximum 500, weights 800) and P's
+// arrival (300), and the other tile's products cover 1024 of that.  One tile with three S
+// buffers and two or three groups of softmax warps takes fewer cycles (2 x 1380), but reads K and V
+// twice as often, and at that load the clock falls (1.72 GHz instead of 2.07): 347 to 360 us.  Half rows on
+// twice the softmax warps: 398; output warps of their own with Q in two buffers: 346; the maximum after the
+// first weights and P in four parts: 388.  What counted: the output's stores in runs of 64 bytes
+// (windowed 187 -> 169, 64 prompts of 50 to 150 71 -> 55), the MMA warp's loops rolled.
+//
 // Roles in a CTA:
 //   softmax   four warps a tile, a thread per vector: its row of S to registers, P = exp2(S c -
 //             base) as bf16 over the columns it has read, 64 tokens at a time; at a unit's end O from
@@ -31,7 +44,8 @@
 //   relay     one warp: tells the first CTA's MMA warp that a stage is there, and zeroes V rows
 //             that no row of the unit sees (another sequence's, or what lies behind the last)
 //   MMA       one warp of the first CTA.  At head_dim 128 two tiles take turns: O_0, S_0 of the next
-//             chunk, O_1, S_1; at 256 one tile has two S buffers and S runs ahead
+//             chunk, O_1, S_1; at 256 one tile has two S buffers and S runs ahead.  Its code comes from far,
+//             between the softmax warps' long loops, so its loops over MMAs are rolled
 //
 // Tensor memory (512 columns): S buffers at 0 and 128, O from 256.
 // mbarriers, all waits bounded (2 s; a wait that gives up sets the status word):
@@ -41,6 +55,9 @@
 //   barS[y]            S buffer y complete (and with two tiles the tile's O of the chunk before)
 //   pready[y][h]       half h of P in buffer y written (four warps of each CTA)
 //   barO               O complete up to a chunk (one tile), partO[t]  at a unit's end
+// A phase of a barrier is only told from its neighbours, so every waiter is at most one phase
+// behind: barO is waited for only where barS has said that the phase before is complete, and
+// a unit's end has a barrier of its own.
 #include "qsa_tc_pair.cuh"
 
 #include <cuda.h>
@@ -104,7 +121,7 @@ struct Unit {
   int row0, rows;          // the unit's rows within it
   int kvh;
   int n_all, lo_all;       // tokens: past the last that its last row sees, first that its first row sees
-  int chunk0, chunks;
+  int chunks;              // of 128 tokens from lo_all on
 };
 
 // Walks a worker's units; by whole warps.  With up to 32 sequences a lane has one, and the
@@ -179,8 +196,7 @@ struct Walker {
       if (!QSA_IN_BOUNDS(u.row0 >= 0 && u.rows > 0 && u.start + u.n <= a.T, kChkUnit)) continue;
       u.n_all = u.row0 + u.rows;
       u.lo_all = a.window > 0 ? max(u.row0 + 1 - a.window, 0) : 0;
-      u.chunk0 = u.lo_all / kTok;
-      u.chunks = (u.n_all - 1) / kTok + 1 - u.chunk0;
+      u.chunks = (u.n_all - u.lo_all + kTok - 1) / kTok;
       return true;
     }
   }
@@ -286,11 +302,11 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       const bool some = __any_sync(0xffffffffu, real);   // (a warp without a row only keeps step)
       float base = kNoBase;
       float2 sum = make_float2(0.f, 0.f);
-      const int unit_chunks = u.chunks, chunk0 = u.chunk0;
+      const int unit_chunks = u.chunks, lo_all = u.lo_all;
       for (int c = 0; c < unit_chunks; ++c, ++chunks) {
         const int y = kTiles == 2 ? t : chunks & 1;      // S buffer
         const uint32_t tS = tmem + y * kTok + lane_off;
-        const int tok0 = (chunk0 + c) * kTok;
+        const int tok0 = lo_all + c * kTok;
         if (gave_up(&barS[y], kTiles == 2 ? s_waits : chunks >> 1)) { dead = true; break; }
         ++s_waits;
         tc_fence_after();
@@ -376,19 +392,45 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       }
       const float r = f / l;                             // (a row sees itself at least)
       const bool store = real && QSA_IN_BOUNDS(orow < (size_t)a.T * a.Hq, kChkOut);
+      uint32_t row4[4], rows4 = 0u;                      // the rows of this lane and its three neighbours (below 2^32)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        row4[k] = __shfl_sync(0xffffffffu, (uint32_t)orow, (lane & 28) + k);
+        rows4 |= (uint32_t)__shfl_sync(0xffffffffu, (int)store, (lane & 28) + k) << k;
+      }
 #pragma unroll 1
       for (int d0 = 0; d0 < D && some; d0 += 32) {
         float o32[32];
         tmem_ld32(tO + d0, o32);
         tmem_wait_ld_of(o32);
-        if (store)
+        uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+        for (int k = 0; k < 16; ++k) w[k] = pack_bf16(o32[2 * k] * r, o32[2 * k + 1] * r);
+        // Four lanes' rows of four 16-byte pieces transposed: lane j then has piece j of each of the four
+        // rows, so that a store writes runs of 64 bytes.
+        const bool odd = lane & 1, upper = lane & 2;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = pack_bf16(o32[8 * i + 2 * k] * r, o32[8 * i + 2 * k + 1] * r);
-            *reinterpret_cast<uint4*>(a.out + orow * D + d0 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int x = 0; x < 4; ++x) {
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            const uint32_t p = w[4 * c + x], q = w[4 * c + 4 + x];
+            const uint32_t g = __shfl_xor_sync(0xffffffffu, odd ? p : q, 1);
+            w[4 * c + x] = odd ? g : p;
+            w[4 * c + 4 + x] = odd ? q : g;
           }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t p = w[4 * c + x], q = w[4 * c + 8 + x];
+            const uint32_t g = __shfl_xor_sync(0xffffffffu, upper ? p : q, 2);
+            w[4 * c + x] = upper ? g : p;
+            w[4 * c + 8 + x] = upper ? q : g;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (rows4 >> k & 1u)
+            *reinterpret_cast<uint4*>(a.out + (size_t)row4[k] * D + d0 + 8 * (lane & 3)) =
+                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
       }
       if (store) a.lse[orow] = (base + log2f(l)) * kLn2;
     }
@@ -402,7 +444,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       const uint32_t q_bytes = (uint32_t)(kTiles * (D / 64) * 128 * a.rho * a.G);
       while (!dead && walk.next(u)) {
         for (int c = 0; c < u.chunks && !dead; ++c) {
-          const int tok = u.start + (u.chunk0 + c) * kTok;
+          const int tok = u.start + u.lo_all + c * kTok;
 #pragma unroll 1
           for (int v = 0; v < 2; ++v, ++pos) {
             const int s = pos % T::kStages, use = pos / T::kStages;
@@ -448,18 +490,16 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       // ==== relay ====================================================================
       while (!dead && walk.next(u)) {
         for (int c = 0; c < u.chunks && !dead; ++c) {
-          const int tok0 = (u.chunk0 + c) * kTok;
+          const int tok0 = u.lo_all + c * kTok;
 #pragma unroll 1
           for (int v = 0; v < 2; ++v, ++pos) {
             const int s = pos % T::kStages, use = pos / T::kStages;
             if (gave_up(&full[s], use)) { dead = true; break; }
-            if (v && (tok0 + kTok > u.n_all || tok0 < u.lo_all)) {
+            if (v && tok0 + kTok > u.n_all) {
               // rows of V that no vector of the unit sees may hold anything; 0 keeps 0 x V at 0
-              for (int x = lane; x < T::kStage / 16; x += 32) {
-                const int tok = tok0 + ((x >> 3) & (kTok - 1));
-                if (tok >= u.n_all || tok < u.lo_all)
+              for (int x = lane; x < T::kStage / 16; x += 32)
+                if (tok0 + ((x >> 3) & (kTok - 1)) >= u.n_all)
                   *reinterpret_cast<uint4*>(ring + s * T::kStage + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
-              }
               fence_proxy_async_smem();
             }
             warp_arrive<CG>(&ready[s]);
@@ -477,6 +517,9 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);   // instruction descriptor: bf16 A and B
       const uint32_t id_s = f16_idesc(256, kTok) | kBf16, id_o = f16_idesc(256, D) | kBf16 | kIdescBMn;
       int chunk = 0;                                       // chunks of earlier units
+      const uint32_t q_lo = (uint32_t)sw128_desc(smem_u32(sQ)), r_lo = (uint32_t)sw128_desc(smem_u32(ring));
+      const uint32_t v_lo = (uint32_t)sw128_mn_desc(smem_u32(ring), T::kVBlk);
+      constexpr uint64_t kHi = (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
       auto slot_k = [&](int n) { return (2 * n) % T::kStages; };
       auto slot_v = [&](int n) { return (2 * n + 1) % T::kStages; };
       auto there = [&](int p) {                            // waits for the stage at position p
@@ -485,21 +528,22 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         return ok;
       };
       auto issue_s = [&](int t, int y, int n) {
-        const uint64_t dq = sw128_desc(smem_u32(sQ + t * T::kQBytes));
-        const uint64_t dk = sw128_desc(smem_u32(ring + slot_k(n) * T::kStage));
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x)
+        uint32_t dq = q_lo + t * (T::kQBytes >> 4), dk = r_lo + slot_k(n) * (T::kStage >> 4);
+#pragma unroll 1
+        for (int x = 0; x < D / 64; ++x) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma_ss<CG>(one, tmem + y * kTok, dq + (uint64_t)((x * T::kQBlk + 32 * ks) >> 4),
-                       dk + (uint64_t)((x * T::kKBlk + 32 * ks) >> 4), id_s, (x | ks) ? 1u : 0u);
+            mma_ss<CG>(one, tmem + y * kTok, kHi | (dq + 2 * ks), kHi | (dk + 2 * ks), id_s, (x | ks) ? 1u : 0u);
+          dq += T::kQBlk >> 4;
+          dk += T::kKBlk >> 4;
+        }
       };
       auto issue_o = [&](int t, int y, int n, int h, bool first) {   // 64 tokens
-        const uint64_t dv = sw128_mn_desc(smem_u32(ring + slot_v(n) * T::kStage), T::kVBlk);
+        const uint32_t dv = v_lo + slot_v(n) * (T::kStage >> 4) + 512 * h;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_ts<CG>(one, tmem + T::kOCol + t * D, tmem + y * kTok + 32 * h + 8 * ks,
-                     dv + (uint64_t)((8192 * h + 2048 * ks) >> 4), id_o, (first && ks == 0) ? 0u : 1u);
+          mma_ts<CG>(one, tmem + T::kOCol + t * D, tmem + y * kTok + 32 * h + 8 * ks, kHi | (dv + 128 * ks), id_o,
+                     (first && ks == 0) ? 0u : 1u);
       };
       while (!dead && walk.next(u)) {
         const int C = u.chunks;
