@@ -428,7 +428,7 @@ Shape decode8_shape(const Geom& g, int window) {
   s.tok_sh = g.D == 128 ? 5 : 4;
   s.window = window;
   s.least = 16;
-  s.lead = 28;
+  s.lead = g.D == 128 ? 48 : 68;
   s.ctas = sm_count();
   s.by_unit = unit_count(s) <= s.ctas;
   return s;
@@ -441,7 +441,7 @@ Shape decode8_shape(const Geom& g, int window) {
 static bool use_tiles(const Geom& g) { return g.R * (g.Hq / g.Hkv) > 16; }
 
 static dense::Shape dense8_shape(const Geom& g, int window) {
-  return use_tiles(g) ? dense_tile_shape(g, window) : dense::decode8_shape(g, window);
+  return use_tiles(g) ? dense_tile_shape(g, window, true) : dense::decode8_shape(g, window);
 }
 
 size_t dense8_workspace_bytes(const Geom& g) {

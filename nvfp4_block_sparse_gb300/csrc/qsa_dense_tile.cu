@@ -134,11 +134,11 @@ struct TT {
   static constexpr int kStage = kKPart + kVPart;
   static constexpr int kRing = kDepth * kStage;
   static constexpr int kBars = 18 + 2 * kDepth;
-  // Exponents of a chunk's blocks: eight bytes of K and eight of V, in a ring of their own.
-  static constexpr int kExpSlots = E8 ? 8 : 0;
+  // Scales of a chunk's blocks, in a ring of their own: eight floats 2^ke, ve and 2^-ve each.
+  static constexpr int kExpSlots = E8 ? 8 : 0, kExpFloats = 24;
   static_assert(!E8 || kExpSlots >= kDepth + 2, "exponents' ring");
   static constexpr int kSmem = 1024 + kTiles * kQBytes + 2 * kKBytes + 2 * kVBytes + kRing +
-                               kBars * 8 + 16 + (E8 ? 16 : kDepth * 4) + kExpSlots * 16;
+                               kBars * 8 + 16 + (E8 ? 16 : kDepth * 4) + kExpSlots * kExpFloats * 4;
   static_assert(kVecs <= 512 && (!E8 || kDepth <= 4), "a unit's vectors; what is copied of each stage");
 };
 
@@ -159,7 +159,7 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 template <class T>
 __device__ __forceinline__ bool copy_all(const Shape& sh, const Work& p, const Span& span, int rank,
                                          uint8_t* ring, uint64_t* full, uint64_t* empty,
-                                         volatile uint32_t* copied, uint8_t* exps) {
+                                         volatile uint32_t* copied, float* exps) {
   const int lane = threadIdx.x & 31;
   const int psh = 31 - __clz(sh.g.P);
   const bool scales = lane & 1, v = lane & 2;         // (8-bit: no copies of scales)
@@ -238,7 +238,12 @@ __device__ __forceinline__ bool copy_all(const Shape& sh, const Work& p, const S
         // was last chunk - kExpSlots', which every softmax warp is done with: the stage was
         // free, so V of chunk - kDepth was converted, for which the MMAs that read the weights of
         // chunk - kDepth - 2 had completed.
-        if (lane < 16) exps[16 * (chunks & (T::kExpSlots - 1)) + lane] = (uint8_t)min(max(exp_next, 95u), 191u);
+        if (lane < 16) {
+          const uint32_t e = min(max(exp_next, 95u), 191u);
+          float* to = exps + T::kExpFloats * (chunks & (T::kExpSlots - 1)) + lane;
+          *to = lane < 8 ? __uint_as_float(e << 23) : (float)((int)e - 127);
+          if (lane >= 8) to[8] = __uint_as_float(0x7F000000u - (e << 23));
+        }
         __syncwarp();
         if (lane == 0) {
           copied[slot] = which;
@@ -359,7 +364,8 @@ struct Converter {
 // without a product, and the softmax threads have the scales: a block's power of two of K
 // in the factor of its logits, that of V in the exponent of its weights, taken out
 // again from the sum of the block's weights.  The copy warp brings the exponents, which are
-// too short for bulk copies.
+// too short for bulk copies, as the floats that the softmax takes (bytes, taken apart by every
+// thread of it, made a chunk's turn 600 cycles longer for a tile).
 //
 // A lane has a 16-byte piece (16 codes, two 16-byte pieces of the tile) per step; a row's pieces belong to
 // neighbouring lanes, of eight of them the upper four store their two in the other order
@@ -376,8 +382,8 @@ struct Converter8 {
   uint8_t* tiles;
   uint64_t *ready, *freed;
   uint32_t part, at_c, at_t;     // the stage's codes; the lane's first piece there and in the tile
+  uint32_t all;                  // a chunk's copies: bit 4 i for the i-th
   int row0, lane_sh, row;
-  bool flip;
 
   __device__ __forceinline__ Converter8(const Shape& sh, bool v, int token0, int dim0, int dw, uint8_t* ring,
                                         uint8_t* tiles_, uint64_t* ready_, uint64_t* freed_)
@@ -385,55 +391,49 @@ struct Converter8 {
     const int lane = threadIdx.x & 31, piece = lane % kPieces;
     lane_sh = 31 - __clz(min(sh.g.P, kRows));                 // log2 of a copy's rows
     row = (32 / kPieces) * dw + lane / kPieces;
-    flip = kPieces >= 8 && (lane & 4);
-    at_c = row * D + dim0 + 16 * piece;
-    at_t = ((piece >> 2) * kBlk + sw128(row, 2 * (piece & 3))) ^ (flip ? 16u : 0u);
+    const int copies = kRows >> lane_sh;
+    all = 0x1111u & ((1u << (4 * copies)) - 1u);
+    const uint32_t flip = kPieces >= 8 && (lane & 4) ? 1u : 0u;
+    at_c = (row * D + dim0 + 16 * piece) ^ (8 * flip);
+    at_t = ((piece >> 2) * kBlk + sw128(row, 2 * (piece & 3))) ^ (16 * flip);
   }
   __device__ __forceinline__ bool convert(const Seg& seg, int tok0, int chunks, int slot, uint32_t copied,
                                           bool v) {
     const int x = chunks & 1, use = chunks >> 1;
     uint8_t* tile = tiles + x * kBytes;
     const uint32_t from = part + slot * T::kStage + at_c;
-    const int first = seg.lo_all - tok0 - row0;
-    const uint32_t seen = (uint32_t)max(seg.n_all - seg.lo_all, 0);
-    const uint32_t bits = copied >> (v ? 2 : 0);
-    uint4 codes[kUnits];       // every step's, so that their latencies overlap
+    uint2 codes[kUnits][2];    // every step's, so that their latencies overlap; the half to be stored first
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
-      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(codes[i].x), "=r"(codes[i].y), "=r"(codes[i].z), "=r"(codes[i].w)
-                   : "r"(from + i * kStepRows * D));
-    if (use > 0 && gave_up(&freed[x], use - 1)) return false;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      uint4 c = codes[i];
-      const int r = row + i * kStepRows;
-      // rows that no vector of the unit sees, and what was not copied, are zeros (a code may be NaN)
-      if ((uint32_t)(r - first) >= seen || !((bits >> (4 * (r >> lane_sh))) & 1u)) c = make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t w[4] = {flip ? c.z : c.x, flip ? c.w : c.y, flip ? c.x : c.z, flip ? c.y : c.w};
-      const uint32_t to = at_t + i * (kStepRows / 8) * 1024;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        *reinterpret_cast<uint4*>(tile + (to ^ (16 * u))) =
-            make_uint4(e4m3x2_to_f16x2(w[2 * u] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * u] >> 16),
-                       e4m3x2_to_f16x2(w[2 * u + 1] & 0xFFFFu), e4m3x2_to_f16x2(w[2 * u + 1] >> 16));
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                     : "=r"(codes[i][u].x), "=r"(codes[i][u].y)
+                     : "r"((from + i * kStepRows * D) ^ (8 * u)));
+    // rows that no vector of the unit sees, and what was not copied, are zeros (a code may be NaN)
+    const int first = seg.lo_all - tok0 - row0, seen = max(seg.n_all - seg.lo_all, 0);
+    const uint32_t bits = copied >> (v ? 2 : 0);
+    if (first > 0 || first + seen < kRows || (bits & all) != all) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int r = row + i * kStepRows;
+        if ((uint32_t)(r - first) >= (uint32_t)seen || !((bits >> (4 * (r >> lane_sh))) & 1u))
+          codes[i][0] = codes[i][1] = make_uint2(0u, 0u);
+      }
     }
+    if (use > 0 && gave_up(&freed[x], use - 1)) return false;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint2 c = codes[i][u];
+        *reinterpret_cast<uint4*>(tile + ((at_t + i * (kStepRows / 8) * 1024) ^ (16 * u))) =
+            make_uint4(e4m3x2_to_f16x2(c.x & 0xFFFFu), e4m3x2_to_f16x2(c.x >> 16), e4m3x2_to_f16x2(c.y & 0xFFFFu),
+                       e4m3x2_to_f16x2(c.y >> 16));
+      }
     fence_proxy_async_smem();
     warp_arrive<T::CG>(&ready[x]);
     return true;
-  }
-};
-
-// A block's factor of its logits, its exponent of V (log2), and 2^-that: from byte i of a chunk's
-// exponents.
-struct Block8 {
-  float c, ve, back;
-  __device__ __forceinline__ Block8(const uint4& e, int i, float cq) {
-    const uint32_t kw = i < 4 ? e.x : e.y, vw = i < 4 ? e.z : e.w;
-    c = cq * __uint_as_float(((kw >> (8 * (i & 3))) & 0xFFu) << 23);
-    const uint32_t v = (vw >> (8 * (i & 3))) & 0xFFu;
-    ve = __uint_as_float(0x4B000000u | v) - 8388735.f;      // 2^23 + v, exact
-    back = __uint_as_float(0x7F000000u - (v << 23));
   }
 };
 
@@ -501,7 +501,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   uint64_t* empty = full + T::kDepth;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + T::kBars);
   uint32_t* copied = s_tmem + 4;                               // [kDepth]
-  uint8_t* exps = reinterpret_cast<uint8_t*>(copied + 4);   // [kExpSlots][16]
+  float* exps = reinterpret_cast<float*>(copied + 4);          // [kExpSlots][2^ke, ve, 2^-ve]
 
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -691,17 +691,23 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           }
         }
         float top;
-        [[maybe_unused]] uint4 ex = make_uint4(0u, 0u, 0u, 0u);
+        [[maybe_unused]] const float4* ex =
+            reinterpret_cast<const float4*>(exps + T::kExpFloats * (chunks & (T::kExpSlots - 1)));
+        // A block's factor of its logits, its exponent of V (log2) and 2^-that.
+        [[maybe_unused]] float bc[kTok / 16];
+        auto of = [](const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
         if constexpr (E8) {
-          ex = *reinterpret_cast<const uint4*>(exps + 16 * (chunks & (T::kExpSlots - 1)));
           top = -INFINITY;
 #pragma unroll
           for (int i = 0; i < kTok / 16; ++i) {
-            const Block8 blk(ex, i, cq);
-            float m = fmaxf(z[16 * i], z[16 * i + 1]);
+            bc[i] = cq * of(ex[i >> 2], i & 3);
+            float m = fmaxf(z[16 * i], z[16 * i + 1]), m2 = fmaxf(z[16 * i + 2], z[16 * i + 3]);
 #pragma unroll
-            for (int k = 2; k < 16; k += 2) m = fmax3(m, z[16 * i + k], z[16 * i + k + 1]);
-            top = fmaxf(top, fmaf(m, blk.c, blk.ve));
+            for (int k = 4; k < 16; k += 4) {
+              m = fmax3(m, z[16 * i + k], z[16 * i + k + 1]);
+              m2 = fmax3(m2, z[16 * i + k + 2], z[16 * i + k + 3]);
+            }
+            top = fmaxf(top, fmaf(fmaxf(m, m2), bc[i], of(ex[2 + (i >> 2)], i & 3)));
           }
         } else {
           float m8[8];
@@ -746,9 +752,10 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
             if constexpr (E8) {
 #pragma unroll
               for (int u = 0; u < 2; ++u) {       // a block of 16 tokens
-                const Block8 blk(ex, 4 * h + 2 * q + u, cq);
-                c2 = make_float2(blk.c, blk.c);
-                b2 = make_float2(blk.ve - base, blk.ve - base);
+                const int n16 = 4 * h + 2 * q + u;
+                const float vb = of(ex[2 + (n16 >> 2)], n16 & 3) - base, back = of(ex[4 + (n16 >> 2)], n16 & 3);
+                c2 = make_float2(bc[n16], bc[n16]);
+                b2 = make_float2(vb, vb);
                 float2 part = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -758,7 +765,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
                   part = add2(part, e);
                   pk[8 * u + i] = pack_weights(e.x, e.y);
                 }
-                sum = fma2(part, make_float2(blk.back, blk.back), sum);
+                sum = fma2(part, make_float2(back, back), sum);
               }
             } else {
 #pragma unroll
@@ -1023,9 +1030,11 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
 // Pairs of CTAs where single ones would take more units: a pair's unit is 512 vectors at
 // head_dim 128 and 256 at 256 (4 requests of 8192 tokens, pairs against singles: 160 vectors
 // 38 and 31 us at head_dim 128, 28.9 and 29.5 at 256; 512 vectors 42 and 49, 42 and 44).
-static bool use_pairs(const Geom& g) { return g.R * (g.Hq / g.Hkv) > (g.D == 128 ? 256 : 128); }
+static bool use_pairs(const Geom& g, bool e8) {
+  return g.R * (g.Hq / g.Hkv) > (e8 ? (g.D == 128 ? 256 : 128) : g.D == 128 ? 256 : 128);
+}
 
-dense::Shape dense_tile_shape(const Geom& g, int window) {
+dense::Shape dense_tile_shape(const Geom& g, int window, bool e8) {
   dense::Shape s;
   auto set = [&](auto t) {
     using T = decltype(t);
@@ -1034,7 +1043,7 @@ dense::Shape dense_tile_shape(const Geom& g, int window) {
     s.ctas = sm_count() / T::CG;
   };
   dense::set_heads(&s, g);
-  if (use_pairs(g)) {
+  if (use_pairs(g, e8)) {
     if (g.D == 128) set(dense::TT<128, 2, false>());   // (8-bit pages alike)
     else set(dense::TT<256, 2, false>());
   } else {
@@ -1081,7 +1090,7 @@ cudaError_t launch_tile(const dense::Shape& s, const dense::Work& w, cudaStream_
 
 template <bool E8>
 cudaError_t launch_tiles(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
-  if (use_pairs(s.g))
+  if (use_pairs(s.g, E8))
     return s.g.D == 256 ? launch_tile<256, 2, E8>(s, w, stream) : launch_tile<128, 2, E8>(s, w, stream);
   return s.g.D == 256 ? launch_tile<256, 1, E8>(s, w, stream) : launch_tile<128, 1, E8>(s, w, stream);
 }
