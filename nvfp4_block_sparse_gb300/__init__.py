@@ -44,7 +44,7 @@ __all__ = [
     "qsa_dense_attention_workspace_bytes", "make_rope_axes", "qsa_rope_axes_t", "qsa_rope_axes_rows",
     "qsa_store_kv_tokens_fp8", "qsa_load_kv_tokens_fp8", "qsa_dense_attention_fp8",
     "qsa_dense_attention_fp8_workspace_bytes", "qsa_prompt_attention", "qsa_prompt_attention_workspace_bytes",
-    "DecodeStep", "DenseStep", "MAX_DECODE_ROWS",
+    "DecodeStep", "DenseStep", "PromptStep", "MAX_DECODE_ROWS",
 ]
 
 # Rows per request the decode / verify attention takes; longer row groups
@@ -178,12 +178,17 @@ class DenseStep:
     layers that attend to every cached token (or the newest ``window``) instead
     of selected blocks, over the same cache and page table as DecodeStep, with
     any number of rows per request.  ``store`` is the prologue (norms, rotation,
-    append) into the workload's pools, ``run`` the attention."""
+    append) into the workload's pools, ``run`` the attention.  ``cache`` is
+    "nvfp4" or "fp8": the 8-bit cache, whose workload has k_exp and v_exp
+    instead of k_sf, v_sf, the tensor scales and the index keys."""
 
-    def __init__(self, geom: dict, window: int = 0, device="cuda"):
+    def __init__(self, geom: dict, window: int = 0, device="cuda", cache: str = "nvfp4"):
+        if cache not in ("nvfp4", "fp8"):
+            raise ValueError("cache must be nvfp4 or fp8")
         self.geom = {n: int(geom[n]) for n in GEOM_FIELDS}
         self.cg = make_geom(**self.geom)
         self.window = int(window)
+        self.cache = cache
         T, Hq, D = (self.geom["batch"] * self.geom["rows_per_req"], self.geom["num_q_heads"],
                     self.geom["head_dim"])
         dev = torch.device(device)
@@ -194,9 +199,12 @@ class DenseStep:
         self.out = self.results[:out_bytes].view(torch.bfloat16).view(T, Hq, D)
         self.lse = self.results[lse_off:].view(torch.float32).view(T, Hq)
         self.q = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-        nbytes = qsa_dense_attention_workspace_bytes(self.cg)
+        nbytes = (qsa_dense_attention_fp8_workspace_bytes if cache == "fp8"
+                  else qsa_dense_attention_workspace_bytes)(self.cg)
         if nbytes == 0:
             raise QsaError("qsa_dense_attention_workspace_bytes", 1, "invalid geometry")
+        if cache == "fp8":
+            self.k = torch.empty((T, self.geom["num_kv_heads"], D), dtype=torch.bfloat16, device=dev)
         with torch.cuda.device(dev):
             self.workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
             qsa_workspace_init(self.workspace)
@@ -209,7 +217,13 @@ class DenseStep:
     def store(self, w: dict, new: dict, norm_rope, cs, stream=None):
         """Appends the rows ``new`` (q, k, v, ik_new, and the norms' q_weight and
         k_weight or None) to the pools of ``w``; the rotated queries are left in
-        ``self.q``."""
+        ``self.q``.  (The 8-bit cache has no index keys: no ``ik_new``.)"""
+        if self.cache == "fp8":
+            qsa_qk_norm_rope(self.cg, norm_rope, new["q"], new["k"], new["q_weight"], new["k_weight"], cs, self.q,
+                             self.k, stream)
+            qsa_store_kv_tokens_fp8(self.cg, self.k, new["v"], w["page_table"], w["seqlens"], w["k_pool"],
+                                    w["k_exp"], w["v_pool"], w["v_exp"], stream=stream)
+            return self
         qsa_store_kv_tokens_rope(self.cg, norm_rope, new["q"], new["k"], new["v"], new["ik_new"],
                                  new["q_weight"], new["k_weight"], cs, w["k_scale"], w["v_scale"],
                                  w["page_table"], w["seqlens"], self.q, w["k_pool"], w["k_sf"],
@@ -218,10 +232,74 @@ class DenseStep:
 
     def run(self, w: dict, q=None, sinks=None, stream=None, sm_scale=None, out=None, lse=None):
         """Attention of ``q`` (default: the workload's own) over the cache of ``w``."""
+        if self.cache == "fp8":
+            qsa_dense_attention_fp8(self.cg, w["q"] if q is None else q, w["k_pool"], w["k_exp"], w["v_pool"],
+                                    w["v_exp"], float(w["sm_scale"]) if sm_scale is None else float(sm_scale),
+                                    w["page_table"], w["seqlens"], self.out if out is None else out,
+                                    self.lse if lse is None else lse, self.workspace, window=self.window,
+                                    sinks=sinks, stream=stream)
+            return self
         qsa_dense_attention(self.cg, w["q"] if q is None else q, w["k_pool"], w["k_sf"],
                             w["v_pool"], w["v_sf"], w["k_scale"], w["v_scale"],
                             float(w["sm_scale"]) if sm_scale is None else float(sm_scale),
                             w["page_table"], w["seqlens"], self.out if out is None else out,
                             self.lse if lse is None else lse, self.workspace, window=self.window,
                             sinks=sinks, stream=stream)
+        return self
+
+
+class PromptStep:
+    """Device buffers for a layer's attention over whole prompts: ``geom``'s batch of sequences,
+    packed into ``rows`` rows at most.  ``run`` normalises and rotates the rows, attends within each
+    sequence, and appends them to the 8-bit cache of a workload, if one is given, so that dense steps
+    with ``cache="fp8"`` go on from there."""
+
+    def __init__(self, geom: dict, rows: int, window: int = 0, device="cuda"):
+        self.geom = {n: int(geom[n]) for n in GEOM_FIELDS}
+        self.cg = make_geom(**self.geom)
+        self.rows, self.window = int(rows), int(window)
+        Hq, Hkv, D = self.geom["num_q_heads"], self.geom["num_kv_heads"], self.geom["head_dim"]
+        dev = torch.device(device)
+        self.q = torch.empty((self.rows, Hq, D), dtype=torch.bfloat16, device=dev)
+        self.k = torch.empty((self.rows, Hkv, D), dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty((self.rows, Hq, D), dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty((self.rows, Hq), dtype=torch.float32, device=dev)
+        nbytes = qsa_prompt_attention_workspace_bytes(self.cg, self.rows)
+        if nbytes == 0:
+            raise QsaError("qsa_prompt_attention_workspace_bytes", 1, "invalid geometry")
+        with torch.cuda.device(dev):
+            self.workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+            qsa_workspace_init(self.workspace)
+
+    def status(self) -> int:
+        """Device status word of this step's workspace: 0 when every bounded
+        wait completed."""
+        return qsa_workspace_status(self.workspace)
+
+    def run(self, new: dict, cu_seqlens, norm_rope, cs, sm_scale: float, w: dict | None = None, sinks=None,
+            stream=None):
+        """Rows ``new`` (q [T, Hq, D], k and v [T, Hkv, D], and the norms' q_weight and k_weight or None)
+        of the sequences at ``cu_seqlens`` (int32 [B + 1]); ``cs`` their rotation rows.  ``w`` (optional):
+        a workload whose 8-bit pools take the rows as its requests' newest tokens.  Results in ``out`` and
+        ``lse``, T rows each."""
+        T = new["k"].shape[0]
+        if T > self.rows:
+            raise ValueError("%d rows, the step has room for %d" % (T, self.rows))
+        if T == 0:
+            return self
+        q, k = self.q[:T], self.k[:T]
+        # (norms and rotation do not ask which sequence a row is of: as many requests of few rows as there
+        # are, and what is left of them as requests of one)
+        per = -(-T // 65535)
+        for first, batch, rows in ((0, T // per, per), (T // per * per, T % per, 1)):
+            if batch:
+                part = slice(first, first + batch * rows)
+                qsa_qk_norm_rope(make_geom(**dict(self.geom, batch=batch, rows_per_req=rows)), norm_rope,
+                                 new["q"][part], new["k"][part], new["q_weight"], new["k_weight"],
+                                 None if cs is None else cs[part], q[part], k[part], stream)
+        qsa_prompt_attention(self.cg, q, k, new["v"], cu_seqlens, sm_scale, self.out[:T], self.lse[:T],
+                             self.workspace, window=self.window, sinks=sinks, stream=stream)
+        if w is not None:
+            qsa_store_kv_tokens_fp8(self.cg, k, new["v"], w["page_table"], w["seqlens"], w["k_pool"], w["k_exp"],
+                                    w["v_pool"], w["v_exp"], cu_rows=cu_seqlens, stream=stream)
         return self
