@@ -606,7 +606,7 @@ cudaError_t launch_decode(const dense::Shape& s, const dense::Work& w, cudaStrea
 static bool use_tiles(const Geom& g) { return g.R * (g.Hq / g.Hkv) > 16; }
 
 static dense::Shape dense_shape(const Geom& g, int window) {
-  return use_tiles(g) ? dense_tile_shape(g, window, false) : decode_shape(g, window);
+  return use_tiles(g) ? dense_tile_shape(g, window) : decode_shape(g, window);
 }
 
 size_t dense_workspace_bytes(const Geom& g) {

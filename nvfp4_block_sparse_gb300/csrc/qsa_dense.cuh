@@ -316,7 +316,7 @@ inline int desc_count(const Shape& s) { return s.by_unit ? (int)unit_count(s) : 
 
 // The tile kernel (qsa_dense_tile.cu): its units for this geometry, and its launch over NVFP4
 // or (e8) 8-bit pages.
-dense::Shape dense_tile_shape(const Geom& g, int window, bool e8);
+dense::Shape dense_tile_shape(const Geom& g, int window);
 cudaError_t launch_dense_tile(const dense::Shape& s, const dense::Work& w, bool e8, cudaStream_t stream);
 cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, cudaStream_t stream);
 // The workspace's parts: status word, descriptors, records.

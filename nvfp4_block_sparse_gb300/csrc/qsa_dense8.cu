@@ -441,7 +441,7 @@ Shape decode8_shape(const Geom& g, int window) {
 static bool use_tiles(const Geom& g) { return g.R * (g.Hq / g.Hkv) > 16; }
 
 static dense::Shape dense8_shape(const Geom& g, int window) {
-  return use_tiles(g) ? dense_tile_shape(g, window, true) : dense::decode8_shape(g, window);
+  return use_tiles(g) ? dense_tile_shape(g, window) : dense::decode8_shape(g, window);
 }
 
 size_t dense8_workspace_bytes(const Geom& g) {

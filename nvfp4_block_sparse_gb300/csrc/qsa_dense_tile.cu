@@ -369,7 +369,8 @@ struct Converter {
 //
 // A lane has a 16-byte piece (16 codes, two 16-byte pieces of the tile) per step; a row's pieces belong to
 // neighbouring lanes, of eight of them the upper four store their two in the other order
-// (their 64-dim block has the same banks).
+// (their 64-dim block has the same banks).  (Loads of the piece's halves in the order of their
+// stores, without the selects, have conflicts of their own: 227 us for 224.)
 template <class T, int kRows, int kDims>
 struct Converter8 {
   static constexpr int D = T::D;
@@ -394,7 +395,7 @@ struct Converter8 {
     const int copies = kRows >> lane_sh;
     all = 0x1111u & ((1u << (4 * copies)) - 1u);
     const uint32_t flip = kPieces >= 8 && (lane & 4) ? 1u : 0u;
-    at_c = (row * D + dim0 + 16 * piece) ^ (8 * flip);
+    at_c = row * D + dim0 + 16 * piece;
     at_t = ((piece >> 2) * kBlk + sw128(row, 2 * (piece & 3))) ^ (16 * flip);
   }
   __device__ __forceinline__ bool convert(const Seg& seg, int tok0, int chunks, int slot, uint32_t copied,
@@ -405,11 +406,10 @@ struct Converter8 {
     uint2 codes[kUnits][2];    // every step's, so that their latencies overlap; the half to be stored first
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                     : "=r"(codes[i][u].x), "=r"(codes[i][u].y)
-                     : "r"((from + i * kStepRows * D) ^ (8 * u)));
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(codes[i][0].x), "=r"(codes[i][0].y), "=r"(codes[i][1].x), "=r"(codes[i][1].y)
+                   : "r"(from + i * kStepRows * D));
+    const bool flip = kPieces >= 8 && (threadIdx.x & 4);
     // rows that no vector of the unit sees, and what was not copied, are zeros (a code may be NaN)
     const int first = seg.lo_all - tok0 - row0, seen = max(seg.n_all - seg.lo_all, 0);
     const uint32_t bits = copied >> (v ? 2 : 0);
@@ -426,7 +426,7 @@ struct Converter8 {
     for (int i = 0; i < kUnits; ++i)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint2 c = codes[i][u];
+        const uint2 c = flip ? codes[i][u ^ 1] : codes[i][u];
         *reinterpret_cast<uint4*>(tile + ((at_t + i * (kStepRows / 8) * 1024) ^ (16 * u))) =
             make_uint4(e4m3x2_to_f16x2(c.x & 0xFFFFu), e4m3x2_to_f16x2(c.x >> 16), e4m3x2_to_f16x2(c.y & 0xFFFFu),
                        e4m3x2_to_f16x2(c.y >> 16));
@@ -656,6 +656,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       };
       uint32_t there0 = there_of(blk0 + lane), there1 = there_of(blk0 + 32 + lane);
       float base = kNoBase;
+      [[maybe_unused]] float most = -INFINITY;
       float2 sum = make_float2(0.f, 0.f);
       for (int c = 0; c < seg.todo; ++c, ++chunks) {
         const int y = kTiles == 2 ? t : chunks & 1;      // S buffer
@@ -678,6 +679,15 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         }
         const bool edge = tok0 + kTok > seg.n_least || tok0 < seg.lo_most ||
                           (live & all_live) != all_live;
+        // The blocks' scales.  (With two tiles, whose turns the softmax bounds, before the logits:
+        // 220 us for 224 in 2 x 512 context rows; with one 36.4 for 35.5, 160 vectors.)
+        [[maybe_unused]] float4 ex[E8 ? 6 : 1];
+        auto scales = [&]() {
+          const float4* from = reinterpret_cast<const float4*>(exps + T::kExpFloats * (chunks & (T::kExpSlots - 1)));
+#pragma unroll
+          for (int i = 0; i < 6; ++i) ex[i] = from[i];
+        };
+        if constexpr (E8 && kTiles == 2) scales();
         // The row's logits, those it does not see at -inf.
         float z[kTok];
 #pragma unroll
@@ -691,12 +701,11 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           }
         }
         float top;
-        [[maybe_unused]] const float4* ex =
-            reinterpret_cast<const float4*>(exps + T::kExpFloats * (chunks & (T::kExpSlots - 1)));
         // A block's factor of its logits, its exponent of V (log2) and 2^-that.
         [[maybe_unused]] float bc[kTok / 16];
         auto of = [](const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
         if constexpr (E8) {
+          if constexpr (kTiles == 1) scales();
           top = -INFINITY;
 #pragma unroll
           for (int i = 0; i < kTok / 16; ++i) {
@@ -720,9 +729,15 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         }
         // The base moves where a logit would overflow an fp16 weight, and with it what has
         // been summed on the old one.
-        const bool moves = top > base + kHeadroom;
+        // (8-bit: then for every vector of the warp, to below its largest so far, as it is the warp
+        // that waits: 2 x 512 context rows with logits up to a deviation of 2 220 us before, 205
+        // now, 199 where nothing moves; 4 x 256 rows of 24 heads on 2 of 256 350 and 316.  By a
+        // power of two, so that a vector's results do not hang on its neighbours'.)
+        if constexpr (E8) most = fmaxf(most, top);
+        bool moves = top > base + kHeadroom;
         if (__any_sync(0xffffffffu, moves)) {
-          const float nb = moves ? top - kBelow : base;
+          if constexpr (E8) moves = most > base + kBelow;
+          const float nb = moves ? (E8 ? floorf(most) : top) - kBelow : base;
           const float alpha = exp2_approx(base - nb);
           base = nb;
           sum.x *= alpha;
@@ -1030,11 +1045,11 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
 // Pairs of CTAs where single ones would take more units: a pair's unit is 512 vectors at
 // head_dim 128 and 256 at 256 (4 requests of 8192 tokens, pairs against singles: 160 vectors
 // 38 and 31 us at head_dim 128, 28.9 and 29.5 at 256; 512 vectors 42 and 49, 42 and 44).
-static bool use_pairs(const Geom& g, bool e8) {
-  return g.R * (g.Hq / g.Hkv) > (e8 ? (g.D == 128 ? 256 : 128) : g.D == 128 ? 256 : 128);
+static bool use_pairs(const Geom& g) {
+  return g.R * (g.Hq / g.Hkv) > (g.D == 128 ? 256 : 128);
 }
 
-dense::Shape dense_tile_shape(const Geom& g, int window, bool e8) {
+dense::Shape dense_tile_shape(const Geom& g, int window) {
   dense::Shape s;
   auto set = [&](auto t) {
     using T = decltype(t);
@@ -1043,7 +1058,7 @@ dense::Shape dense_tile_shape(const Geom& g, int window, bool e8) {
     s.ctas = sm_count() / T::CG;
   };
   dense::set_heads(&s, g);
-  if (use_pairs(g, e8)) {
+  if (use_pairs(g)) {
     if (g.D == 128) set(dense::TT<128, 2, false>());   // (8-bit pages alike)
     else set(dense::TT<256, 2, false>());
   } else {
@@ -1090,7 +1105,7 @@ cudaError_t launch_tile(const dense::Shape& s, const dense::Work& w, cudaStream_
 
 template <bool E8>
 cudaError_t launch_tiles(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
-  if (use_pairs(s.g, E8))
+  if (use_pairs(s.g))
     return s.g.D == 256 ? launch_tile<256, 2, E8>(s, w, stream) : launch_tile<128, 2, E8>(s, w, stream);
   return s.g.D == 256 ? launch_tile<256, 1, E8>(s, w, stream) : launch_tile<128, 1, E8>(s, w, stream);
 }

@@ -234,3 +234,30 @@ def test_refused():
     for kw in (dict(ws=ws[:-256]), dict(sm=0.0), dict(sm=math.nan), dict(window=-1), dict(ws=ws[1:])):
         with pytest.raises(qsa.QsaError):
             call(**kw)
+
+
+@pytest.mark.parametrize("D,R,G", [(128, 2, 4), (128, 40, 4), (128, 160, 4), (256, 2, 6), (256, 40, 6), (256, 160, 6)])
+def test_every_code(D, R, G):
+    """A window of one token: each row's output is that token's V, the code times its power of two, to the
+    bit, for every finite code and for exponents at both ends; a NaN code makes every row that sees it NaN."""
+    w = c8.geometry(13, 1, R, 1, D, 64, R + 70, R + 70, G=G)
+    rng = np.random.default_rng(D + R)
+    finite = np.array([c for c in range(256) if c & 0x7F != 0x7F], np.uint8)
+    for page in w["v_pool"]:
+        page[:] = rng.permutation(np.resize(finite, page.size)).reshape(page.shape)
+    w["v_exp"][:] = rng.choice(np.array([95, 96, 120, 127, 134, 190, 191], np.uint8), w["v_exp"].shape)
+    q = queries(w)
+    out, _ = run(w, q, 1)
+    L, want = int(w["seqlens"][0]), np.empty((R, D))
+    for r in range(R):
+        page, slot = w["page_table"][0, (L - R + r) // 64], (L - R + r) % 64
+        code = torch.from_numpy(w["v_pool"][page, 0, slot]).view(torch.float8_e4m3fn).double().numpy()
+        want[r] = code * 2.0 ** (int(w["v_exp"][page, 0, slot // 16]) - 127)
+    np.testing.assert_array_equal(out.double().cpu().numpy(), np.broadcast_to(want[:, None], out.shape))
+    for sign, pool in ((0x7F, "v_pool"), (0xFF, "v_pool"), (0x7F, "k_pool"), (0xFF, "k_pool")):
+        x = dict(w, **{pool: w[pool].copy()})
+        x[pool][w["page_table"][0, (L - 1) // 64], 0, (L - 1) % 64, 7] = sign
+        out, lse = run(x, q, 1)
+        assert torch.isnan(out[-1, :, 7]).all() and torch.isfinite(lse[-1]).all() == (pool == "v_pool")
+        if pool == "k_pool":
+            assert torch.isnan(out[-1]).all()
