@@ -717,7 +717,7 @@ cudaError_t launch_prompt(const Geom& g, const PromptArgs& p, cudaStream_t strea
   a.T = (int)p.rows;
   a.rho = 128 / a.G;
   a.window = p.window;
-  a.c = (float)((double)p.sm_scale * 1.4426950408889634);
+  a.c = (float)std::min((double)p.sm_scale * 1.4426950408889634, 3e38);
   a.cu = p.cu;
   a.sinks = p.sinks;
   a.out = reinterpret_cast<__nv_bfloat16*>(p.out);
