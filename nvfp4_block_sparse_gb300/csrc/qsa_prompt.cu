@@ -17,16 +17,18 @@
 //
 // Units of one sequence differ in length (causal).  They are dealt to the pairs longest first,
 // there and back: the r-th turn goes to pairs 0, 1, ... where r is even and ..., 1, 0 where it
-// is odd, so that all end within about a unit's difference, without a ticket or a message; every role finds its
-// units for itself.
+// is odd, so that all end within about a unit's difference, without a ticket or a message; the copy warp of
+// each CTA finds them and leaves them to the other roles.
 //
 // Weights are bf16, as V is (one kind of operand per MMA): eight bits each, of sums that are fp32.
 // bf16 has fp32's exponents, so no weight is lost to the base; it is the exact maximum of the first
 // tokens, and moves when a later logit is 2^8 above it.
 //
-// Measured (GB300): 8192 tokens, 32 heads on 4 of 128: 324 us, 1.70 PFLOP/s (0.88 of the measured
-// cuBLAS rate); 16 on 2 of 256: 272 us, 2.02 PFLOP/s; 4 prompts of 3000 to 4096 with a window of
-// 1024: 169 us; 6 of 329 to 1993, 24 on 2 of 256: 97 us; one of 77: 7.8 us.  A chunk's turn of two
+// Measured (GB300): 8192 tokens, 32 heads on 4 of 128: 310 us, 1.77 PFLOP/s (0.92 of the measured
+// cuBLAS rate); 16 on 2 of 256: 272 to 284 us, 1.94 to 2.02 PFLOP/s; 4 prompts of 3000 to 4096 with a
+// window of 1024: 150 us; 6 of 329 to 1993, 24 on 2 of 256: 94 to 108 us (one tile to a CTA: each chunk
+// is 64 KB a CTA from L2, 9 TB/s over the GPU, and the time changes from process to process); 64 of 50 to
+// 150: 42 us; one of 77: 7.2 us.  A chunk's turn of two
 // tiles takes 3130 cycles of which its MMAs need 2048: from one tile's S to its next O pass S's
 // commit (450 cycles until a warp sees it), the softmax (ld 180, maximum 500, weights 800) and P's
 // arrival (300), and the other tile's products cover 1024 of that.  One tile with three S
@@ -34,7 +36,8 @@
 // twice as often, and at that load the clock falls (1.72 GHz instead of 2.07): 347 to 360 us.  Half rows on
 // twice the softmax warps: 398; output warps of their own with Q in two buffers: 346; the maximum after the
 // first weights and P in four parts: 388.  What counted: the output's stores in runs of 64 bytes
-// (windowed 187 -> 169, 64 prompts of 50 to 150 71 -> 55), the MMA warp's loops rolled.
+// (windowed 187 -> 169, 64 prompts of 50 to 150 71 -> 55), the MMA warp's loops rolled, units found by one
+// role (170 -> 163, 55 -> 49), masks as words of bits (163 -> 150, 49 -> 42, long 316 -> 310).
 //
 // Roles in a CTA:
 //   softmax   four warps a tile, a thread per vector: its row of S to registers, P = exp2(S c -
@@ -79,6 +82,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoBase = -1e30f;
 constexpr float kHeadroom = 8.f;
 constexpr int kTok = 128;              // tokens per chunk
+constexpr int kUnits = 4;              // units in shared memory
 
 struct Args {
   int B, Hq, Hkv, G, T;
@@ -110,21 +114,54 @@ struct PT {
   static constexpr int kKBlk = 64 * 128;                 // 64 dims of 64 tokens
   static constexpr int kVBlk = kTok * 128;               // 64 dims of 128 tokens
   static constexpr uint32_t kOCol = 256;
-  static constexpr int kBars = 3 * kStages + 3 + 2 + 4 + 1 + 2 + 1;
-  static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStage + kBars * 8 + 16;
+  static constexpr int kBars = 3 * kStages + 3 + 2 + 4 + 1 + 2 + 1 + kUnits;
+  static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStage + kUnits * 32 + kBars * 8 + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 // ---- units -----------------------------------------------------------------------
 struct Unit {
-  int start, n;            // the sequence's first row and its rows
-  int row0, rows;          // the unit's rows within it
+  int start, row0, rows;   // the sequence's first row; the unit's rows within it
   int kvh;
   int n_all, lo_all;       // tokens: past the last that its last row sees, first that its first row sees
-  int chunks;              // of 128 tokens from lo_all on
+  int chunks;              // of 128 tokens from lo_all on; 0: there is no unit more
 };
 
-// Walks a worker's units; by whole warps.  With up to 32 sequences a lane has one, and the
+// The units that the copy warp has found, for the other roles of its CTA.  (Each for itself, every
+// role's units began with the search, and its code was there four times.)  A slot is written again
+// when its readers are done with it: the copy warp finds unit i + 4 behind its copies of unit i + 3,
+// which waited for unit i + 2's Q to be free, so that the MMA warp and both relays had come to unit i + 2 and
+// the softmax warps to unit i + 1.
+struct Units {
+  int4* slots;             // [kUnits][2]
+  uint64_t* there;         // [kUnits]
+  int at;
+
+  __device__ __forceinline__ void put(const Unit& u) {
+    const int s = at % kUnits;
+    if ((threadIdx.x & 31) == 0) {
+      slots[2 * s] = make_int4(u.start, u.row0, u.rows, u.kvh);
+      slots[2 * s + 1] = make_int4(u.n_all, u.lo_all, u.chunks, 0);
+      ws_arrive(&there[s]);
+    }
+    __syncwarp();
+    ++at;
+  }
+  // The next unit; false behind the last one and where the wait gave up (then dead is set).
+  __device__ __forceinline__ bool next(Unit& u, bool& dead) {
+    const int s = at % kUnits;
+    if (gave_up(&there[s], at / kUnits)) {
+      dead = true;
+      return false;
+    }
+    ++at;
+    const int4 a = slots[2 * s], b = slots[2 * s + 1];
+    u = Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+    return u.chunks > 0;
+  }
+};
+
+// Walks a worker's units; the copy warp's.  With up to 32 sequences a lane has one, and the
 // units go by their number within their sequence, last (longest) first.  With more sequences
 // the slots of a sequence begin at cu[b] / U + b, which leaves room for all its tiles (and some
 // slots empty) and can be searched; their order then matters little.
@@ -161,7 +198,7 @@ struct Walker {
       if (at >= units) continue;
       const int slot = (int)(at / a.Hkv);
       u.kvh = (int)(at - (long long)slot * a.Hkv);
-      int tile;
+      int tile, rows;      // the unit's number within its sequence, the sequence's rows
       if (a.B <= 32) {
         // the largest i with more than `slot` tiles numbered i or higher
         const int tiles = (n + U - 1) / U;
@@ -178,7 +215,7 @@ struct Walker {
         const uint32_t mine = __ballot_sync(0xffffffffu, tiles > tile && __popc(have & ((1u << lane) - 1u)) == nth);
         const int b = __ffs(mine) - 1;
         u.start = __shfl_sync(0xffffffffu, start, b);
-        u.n = __shfl_sync(0xffffffffu, n, b);
+        rows = __shfl_sync(0xffffffffu, n, b);
       } else {
         int lo = 0, hi = a.B;
         while (hi - lo > 1) {
@@ -186,14 +223,14 @@ struct Walker {
           if (min(max(__ldg(a.cu + mid), 0), a.T) / U + mid <= slot) lo = mid;
           else hi = mid;
         }
-        range(lo, u.start, u.n);
+        range(lo, u.start, rows);
         tile = slot - (min(max(__ldg(a.cu + lo), 0), a.T) / U + lo);
-        if (tile < 0 || tile >= (u.n + U - 1) / U) continue;
-        tile = (u.n + U - 1) / U - 1 - tile;
+        if (tile < 0 || tile >= (rows + U - 1) / U) continue;
+        tile = (rows + U - 1) / U - 1 - tile;
       }
       u.row0 = tile * U;
-      u.rows = min(U, u.n - u.row0);
-      if (!QSA_IN_BOUNDS(u.row0 >= 0 && u.rows > 0 && u.start + u.n <= a.T, kChkUnit)) continue;
+      u.rows = min(U, rows - u.row0);
+      if (!QSA_IN_BOUNDS(u.row0 >= 0 && u.rows > 0 && u.start + rows <= a.T, kChkUnit)) continue;
       u.n_all = u.row0 + u.rows;
       u.lo_all = a.window > 0 ? max(u.row0 + 1 - a.window, 0) : 0;
       u.chunks = (u.n_all - u.lo_all + kTok - 1) / kTok;
@@ -230,7 +267,8 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;                                    // [kTiles][kQBytes]
   uint8_t* ring = sQ + kTiles * T::kQBytes;              // [kStages][kStage]
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + T::kStages * T::kStage);
+  int4* s_units = reinterpret_cast<int4*>(ring + T::kStages * T::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_units + 2 * kUnits);
   uint64_t* free_ = full + T::kStages;
   uint64_t* ready = free_ + T::kStages;
   uint64_t* qfull = ready + T::kStages;
@@ -241,7 +279,8 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
   uint64_t* barO = pready + 4;
   uint64_t* partO = barO + 1;                            // [2]
   uint64_t* mdone = partO + 2;                           // after a give-up: every MMA issued has completed
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(mdone + 1);
+  uint64_t* uthere = mdone + 1;                          // [kUnits]
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(uthere + kUnits);
 
   if (tid == 0) {
     for (int s = 0; s < T::kStages; ++s) {
@@ -258,6 +297,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       mbar_init(&pready[2 * x + 1], 4 * CG);
       mbar_init(&partO[x], 1);
     }
+    for (int s = 0; s < kUnits; ++s) mbar_init(&uthere[s], 1);
     mbar_init(barO, 1);
     mbar_init(mdone, 1);
     s_tmem[1] = 0u;   // set when a CTA of the pair gave up
@@ -276,6 +316,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
   pdl_trigger();
   const int unit_rows = 2 * kTiles * a.rho;
   bool dead = false;
+  Units units{s_units, uthere, 0};
 
   if (warp < T::kSoft) {
     // ==== softmax ==================================================================
@@ -287,9 +328,8 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
     const int my_head = row % a.G;
     const bool in_tile = row < a.rho * a.G;
     int chunks = 0, s_waits = 0, parts = 0;     // chunks, waits on barS (two tiles), units so far
-    Walker walk(a, unit_rows, worker, workers);
     Unit u;
-    bool more = walk.next(u);
+    bool more = units.next(u, dead);
     while (!dead && more) {
       const bool real = in_tile && my_row < u.rows;
       const int n = real ? u.row0 + my_row + 1 : 0;
@@ -322,10 +362,16 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         for (int i = 0; i < kTok / 32; ++i) tmem_ld32(tS + 32 * i, z + 32 * i);
         tmem_wait_ld_of(z);
         if (tok0 + kTok > n_least || tok0 < lo_most) {
+          // (a word of bits for 32 tokens: a third of the code that two comparisons a token take)
           const int end = n - tok0, begin = lo - tok0;
+          auto below = [](int x) { return x >= 32 ? 0xFFFFFFFFu : x <= 0 ? 0u : (1u << x) - 1u; };
 #pragma unroll
-          for (int i = 0; i < kTok; ++i)
-            if (i >= end || i < begin) z[i] = -INFINITY;
+          for (int w = 0; w < kTok / 32; ++w) {
+            const uint32_t sees = below(end - 32 * w) & ~below(begin - 32 * w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((sees >> i) & 1u)) z[32 * w + i] = -INFINITY;
+          }
         }
         float m8[8];
 #pragma unroll
@@ -379,8 +425,8 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       }
       if (dead) break;
       // ---- the unit's output, the next unit found meanwhile ------------------------------
-      more = walk.next(u);
-      if (gave_up(&partO[t], parts)) { dead = true; break; }
+      more = units.next(u, dead);
+      if (dead || gave_up(&partO[t], parts)) { dead = true; break; }
       ++parts;
       tc_fence_after();
       float l = sum.x + sum.y, f = 1.f;
@@ -436,13 +482,14 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
     }
   } else {
     if constexpr (kTiles == 2) regs_down<T::kOtherRegs>();
-    Walker walk(a, unit_rows, worker, workers);
     Unit u;
     int pos = 0, parts = 0;                              // stages so far (two per chunk), units
     if (warp == T::kCopy) {
       // ==== copies =================================================================
       const uint32_t q_bytes = (uint32_t)(kTiles * (D / 64) * 128 * a.rho * a.G);
+      Walker walk(a, unit_rows, worker, workers);
       while (!dead && walk.next(u)) {
+        units.put(u);
         for (int c = 0; c < u.chunks && !dead; ++c) {
           const int tok = u.start + u.lo_all + c * kTok;
 #pragma unroll 1
@@ -480,7 +527,9 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
           }
         }
       }
+      if (!dead) units.put(Unit{});
       // Nothing may still be on its way when the block ends, whoever gave up.
+#pragma unroll 1
       for (int s = 0; s < T::kStages; ++s) {
         const int uses = pos / T::kStages + (s < pos % T::kStages ? 1 : 0);
         if (uses > 0 && gave_up(&full[s], uses - 1)) dead = true;
@@ -488,7 +537,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       if (parts > 0 && gave_up(qfull, parts - 1)) dead = true;
     } else if (warp == T::kRelay) {
       // ==== relay ====================================================================
-      while (!dead && walk.next(u)) {
+      while (!dead && units.next(u, dead)) {
         for (int c = 0; c < u.chunks && !dead; ++c) {
           const int tok0 = u.lo_all + c * kTok;
 #pragma unroll 1
@@ -545,7 +594,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
           mma_ts<CG>(one, tmem + T::kOCol + t * D, tmem + y * kTok + 32 * h + 8 * ks, kHi | (dv + 128 * ks), id_o,
                      (first && ks == 0) ? 0u : 1u);
       };
-      while (!dead && walk.next(u)) {
+      while (!dead && units.next(u, dead)) {
         const int C = u.chunks;
         if (gave_up(qready, parts) || !there(2 * chunk)) { dead = true; break; }
         ++parts;
