@@ -125,9 +125,15 @@ struct TT {
   static_assert(kQCol + D / 2 <= 512 && 2 * kTok <= 256, "tensor-memory columns");
   // Q tiles (D/64 blocks of 128 rows x 128 B), or, with Q in tensor memory, 8 KB per warp
   // through which Q and O pass.
-  static constexpr int kQBytes = kQTmem ? 32768 : 128 * D * 2;
+  // Single CTAs over 8-bit pages at head_dim 256 leave that out (a thread reads its row of Q by itself,
+  // rows of O are transposed between four lanes) for a third stage, as their copies' latency bounds
+  // them: 48 vectors a KV head, 16 requests of 8192 to 16384 tokens, 66.3 us before, 59.0 now, windowed
+  // verify rows 52.9 and 47.8.  (At head_dim 128 the softmax does: 76.7 and 77.2; pages asked for in L2
+  // ahead of their copies, 63.3 with two stages, 59.7 with three.)
+  static constexpr bool kPass = !(E8 && CG == 1 && D == 256);
+  static constexpr int kQBytes = !kPass ? 0 : kQTmem ? 32768 : 128 * D * 2;
   // Codes and scales on their way: a stage is a chunk, this CTA's K rows and whole V rows.
-  static constexpr int kDepth = CG == 2 ? 4 : E8 ? 2 : 3;   // (what there is room for)
+  static constexpr int kDepth = CG == 2 ? 4 : E8 && kPass ? 2 : 3;   // (what there is room for)
   static constexpr int kRow = E8 ? D : D / 2;            // code bytes of a token
   static constexpr int kKCodes = kKRows * kRow, kVCodes = kTok * kRow;
   static constexpr int kKPart = kKCodes + (E8 ? 0 : kKCodes / 8), kVPart = kVCodes + (E8 ? 0 : kVCodes / 8);
@@ -584,8 +590,30 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       // nobody's.  (With two tiles most warps have one, and the registers for asking cost more:
       // two context chunks 634 us without, 643 with it.)
       const bool some = kTiles == 2 || (t * CG + rank) * 128 + 32 * (warp & 3) < seg.vecs;
+      if constexpr (!T::kPass) {
+        const uint4* from = reinterpret_cast<const uint4*>(p.q + (real ? orow * D : 0));
 #pragma unroll 1
-      for (int d0 = 0; d0 < D && some; d0 += 128) {
+        for (int d0 = 0; d0 < D && some; d0 += 128) {
+          uint4 x[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = real ? __ldg(from + d0 / 8 + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t v[16];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint4 y = x[4 * c4 + u];
+              v[4 * u] = y.x; v[4 * u + 1] = y.y; v[4 * u + 2] = y.z; v[4 * u + 3] = y.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[k])));
+            tmem_st16u(tQ + d0 / 2 + 16 * c4, v);
+          }
+        }
+      }
+#pragma unroll 1
+      for (int d0 = 0; d0 < D && some && T::kPass; d0 += 128) {
         __syncwarp();
 #pragma unroll 4
         for (int i = 0; i < 16; ++i) {
@@ -832,6 +860,32 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
             for (int i = 0; i < 8; ++i)
               to[(size_t)(d0 / 4 + i) * sh.vt] =
                   make_float4(o32[4 * i], o32[4 * i + 1], o32[4 * i + 2], o32[4 * i + 3]);
+        }
+      } else if constexpr (!T::kPass) {
+        uint32_t row4[4], rows4 = 0u;                    // the rows of this lane and its three neighbours
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          row4[k] = __shfl_sync(0xffffffffu, orow32, (lane & 28) + k);
+          rows4 |= (uint32_t)((lane & 28) + k < left && QSA_IN_BOUNDS(row4[k] < (size_t)g.B * g.R * g.Hq, kChkOut))
+                   << k;
+        }
+#pragma unroll 1
+        for (int d0 = 0; d0 < D && left > 0; d0 += 32) {
+          float o32[32];
+          tmem_ld32(tO + d0, o32);
+          tmem_wait_ld_of(o32);
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(o32[2 * k] * r, o32[2 * k + 1] * r);
+            w[k] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          transpose4(w, lane);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (rows4 >> k & 1u)
+              *reinterpret_cast<uint4*>(p.out + (size_t)row4[k] * D + d0 + 8 * (lane & 3)) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
       } else {
         // O leaves 64 columns at a time by way of shared memory of the warp's own (its Q rows,

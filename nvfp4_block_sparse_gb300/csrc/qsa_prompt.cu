@@ -452,26 +452,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         uint32_t w[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) w[k] = pack_bf16(o32[2 * k] * r, o32[2 * k + 1] * r);
-        // Four lanes' rows of four 16-byte pieces transposed: lane j then has piece j of each of the four
-        // rows, so that a store writes runs of 64 bytes.
-        const bool odd = lane & 1, upper = lane & 2;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-#pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            const uint32_t p = w[4 * c + x], q = w[4 * c + 4 + x];
-            const uint32_t g = __shfl_xor_sync(0xffffffffu, odd ? p : q, 1);
-            w[4 * c + x] = odd ? g : p;
-            w[4 * c + 4 + x] = odd ? q : g;
-          }
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t p = w[4 * c + x], q = w[4 * c + 8 + x];
-            const uint32_t g = __shfl_xor_sync(0xffffffffu, upper ? p : q, 2);
-            w[4 * c + x] = upper ? g : p;
-            w[4 * c + 8 + x] = upper ? q : g;
-          }
-        }
+        transpose4(w, lane);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (rows4 >> k & 1u)

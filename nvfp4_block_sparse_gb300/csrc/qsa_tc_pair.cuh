@@ -40,6 +40,30 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// ---- rows of neighbouring lanes ------------------------------------------------
+// Four lanes' rows of four 16-byte pieces transposed: lane j then has piece j of each of the four rows,
+// so that a store writes runs of 64 bytes.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[16], int lane) {
+  const bool odd = lane & 1, upper = lane & 2;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) {
+      const uint32_t p = w[4 * c + x], q = w[4 * c + 4 + x];
+      const uint32_t g = __shfl_xor_sync(0xffffffffu, odd ? p : q, 1);
+      w[4 * c + x] = odd ? g : p;
+      w[4 * c + 4 + x] = odd ? q : g;
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t p = w[4 * c + x], q = w[4 * c + 8 + x];
+      const uint32_t g = __shfl_xor_sync(0xffffffffu, upper ? p : q, 2);
+      w[4 * c + x] = upper ? g : p;
+      w[4 * c + 8 + x] = upper ? q : g;
+    }
+  }
+}
+
 // ---- barriers across the pair ------------------------------------------------
 // One wait of at most about 20 us during which the thread sleeps in hardware.
 __device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity) {
