@@ -19,7 +19,11 @@
 // there before the first is rounded, without reading anything twice.  So a block is
 // written by one warp whatever the rows' number, nothing waits for anybody else, and
 // requests of any lengths, packed or not, are the same to it.
-// Bound by the rows' bytes: 2 in and 1 out per element.
+// Bound by the rows' bytes: 2 in and 1 out per element, for few rows by two chains of length, page and
+// row.  Measured (GB300, both calls behind one another on the GPU): 6 packed prompts of 700 to 2047
+// tokens, 2 heads of 256, append and read-back 15.7 us for 52.9 MB, of which the append takes the larger
+// half (a block's 16 rows are 127 registers of a thread: a quarter of the SM's warps; 0.8 of its time
+// it waits for the one look at lengths and pages and the one at the rows); 48 requests of 4 rows 5.2 us.
 #include "qsa_common.cuh"
 
 namespace qsa {
@@ -259,7 +263,8 @@ load8_kernel(const __grid_constant__ Geom g, const __grid_constant__ Cache8Args 
 cudaError_t launch_cache8(const Geom& g, const Cache8Args& a, bool append, bool pdl,
                           cudaStream_t stream) {
   // Rows per CTA: as many as leave every SM eight CTAs, so that a decode step's few rows are
-  // spread and a prompt's blocks are found by one look per block.
+  // spread (48 requests of 4 rows: 5.2 us; in CTAs of 16 rows 12 SMs would do them) and a prompt's
+  // blocks are found by one look per block.
   const long long sms = sm_count();
   int rows = 1;
   while (rows < kRows && a.rows > rows * sms * 8) rows *= 2;

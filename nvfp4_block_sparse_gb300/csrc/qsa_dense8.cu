@@ -20,7 +20,12 @@
 // largest z + ve is at least 2^8 of fp32's normal range of 2^-126: a token whose V is as small
 // as can be next to the largest still counts in the sum down to weights of 2^-38.
 //
-// Bound by the cache's bytes: 2 D + 1/8 per token and KV head.
+// Bound by the cache's bytes: 2 D + 1/8 per token and KV head.  Measured (GB300): 8 rows of 32 heads on 4
+// of 128 over up to 32768 tokens each 33.6 us for 163 MB (floor 24.0), 16 of 8192 to 16384 38.8 us for 202 MB
+// (5.2 TB/s, 0.77 of the copy rate; at 12 vectors a KV head 45.6); 24 on 2 of 256, 16 of these, 47.6; one
+// row over 4096 tokens 9.8.  A warp's own chain (page, copy, S, weights, O) bounds it: the issue slots are
+// 30 % busy, two warps to a scheduler; more warps with fewer tokens or stages each are slower (12 warps of
+// 16 tokens 41.4 for 33.6), and so is turning codes to fp16 by their bits instead of conversions (39.4).
 #include "qsa_dense_parts.cuh"
 
 #include <cmath>
@@ -428,6 +433,9 @@ Shape decode8_shape(const Geom& g, int window) {
   s.tok_sh = g.D == 128 ? 5 : 4;
   s.window = window;
   s.least = 16;
+  // A part's start and end take what this many chunks take (batched decode 34.5, 33.9, 33.4, 33.6 us with
+  // 28, 40, 48 and 68; 12 vectors of 256, 8 requests of 16384 tokens 42.2, 39.5, 37.5, 37.9 with 28, 40,
+  // 68 and 84).
   s.lead = g.D == 128 ? 48 : 68;
   s.ctas = sm_count();
   s.by_unit = unit_count(s) <= s.ctas;
@@ -437,7 +445,10 @@ Shape decode8_shape(const Geom& g, int window) {
 }  // namespace
 }  // namespace dense
 
-// Above 16 vectors per KV head the tile kernel, as over NVFP4 pages (see there).
+// Above 16 vectors per KV head the tile kernel, as over NVFP4 pages (see there).  16 requests of 8192 to
+// 16384 tokens, tiles and units of 16 here: 24 and 32 vectors 76.6 and 74.6 us at head_dim 128, 65.1 and
+// 73.3 at 256 (tiles since then 59), 48 76.4 and 104; units of 32 vectors at 128 65.4 us, but 19.5 for 15.2
+// with one request of 2000 tokens and 113 at 48 vectors.
 static bool use_tiles(const Geom& g) { return g.R * (g.Hq / g.Hkv) > 16; }
 
 static dense::Shape dense8_shape(const Geom& g, int window) {

@@ -373,6 +373,12 @@ struct Converter {
 // too short for bulk copies, as the floats that the softmax takes (bytes, taken apart by every
 // thread of it, made a chunk's turn 600 cycles longer for a tile).
 //
+// Measured (GB300): two context chunks of 512 rows, 32 heads on 4 of 128, behind 14000 to 16384 tokens 205 us
+// (1.22 PFLOP/s; NVFP4 pages 185: their codes are half the bytes to read from shared memory, and their
+// scales are gone before the softmax; without the second kernel that joins the parts 190); 4 x 256 rows of
+// 24 heads on 2 of 256 over 16384 319 us, 1.28 PFLOP/s; windowed verify rows (32 requests x 4 rows, 24 heads
+// on 2 of 256, window 4096) 47.8 us for 138 MB, 7 of them the join.
+//
 // A lane has a 16-byte piece (16 codes, two 16-byte pieces of the tile) per step; a row's pieces belong to
 // neighbouring lanes, of eight of them the upper four store their two in the other order
 // (their 64-dim block has the same banks).  (Loads of the piece's halves in the order of their

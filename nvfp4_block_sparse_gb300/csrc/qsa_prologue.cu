@@ -66,6 +66,8 @@ rope_rows_kernel(int R, long long T, const __grid_constant__ qsa_rope_t rope,
 // own axis.  A thread has two neighbouring pairs of every so-manieth row, four rows' positions
 // requested at once.  The plan passes through shared memory once per CTA: read from the
 // parameters by every warp, an address at a time, it took longer than the rows.
+// Measured (GB300): 16384 positions of 3 axes, 64 pairs, 3.1 us for 8.6 MB (floor 1.3, a launch 1.3);
+// 64 positions 1.4 us.
 // ---------------------------------------------------------------------------
 constexpr int kAxesRows = 4;
 
