@@ -447,12 +447,12 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
 // ---------------------------------------------------------------------------
 // The tile kernel's divided units joined: CTA (i, y, z) takes 32 vectors of the unit of
 // descriptor i, a lane each (a record holds four dims of neighbouring vectors behind one
-// another), its warps four dims each.  The parts are added in their order, eight at a
-// time on their way: with few units the latency of the records is all there is (a quarter
-// of a chunk of 77 rows' time; four dims instead of eight 31.4 -> 29.7 us there, and
-// 43.5 -> 43.7 us where there are many units).
+// another), its warps eight dims each.  The parts are added in their order.  The latency of the
+// records is all there is, so up to three parts are asked for at once, their bases and sums with
+// them (windowed verify rows over 8-bit pages 47.7 -> 45.3 us, 2 x 512 context rows 206.7 -> 202.0;
+// with four or sixteen dims 45.6 and 45.4, 203.1 and 203.4), and eight of more.
 // ---------------------------------------------------------------------------
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8, kJoinQuads = 2;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
@@ -477,19 +477,53 @@ dense_join_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   };
   if (c >= vecs) return;
   float m = kNoBase, l = 0.f;
+  float4 acc[kJoinQuads];
+#pragma unroll
+  for (int q = 0; q < kJoinQuads; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto quad = [&](const float* rec, int q) {
+    return reinterpret_cast<const float4*>(rec + 2 * sh.vt)[(size_t)(warp * kJoinQuads + q) * sh.vt + c];
+  };
+  auto add = [&](float mi, float li, const float4 (&x)[kJoinQuads]) {
+    const float f = exp2_approx(mi - m);
+    l = fmaf(li, f, l);
+#pragma unroll
+    for (int q = 0; q < kJoinQuads; ++q) {
+      acc[q].x = fmaf(x[q].x, f, acc[q].x);
+      acc[q].y = fmaf(x[q].y, f, acc[q].y);
+      acc[q].z = fmaf(x[q].z, f, acc[q].z);
+      acc[q].w = fmaf(x[q].w, f, acc[q].w);
+    }
+  };
+  constexpr int kFew = 3;
+  if (parts <= kFew) {           // (the usual: everything asked for at once)
+    float mi[kFew], li[kFew];
+    float4 x[kFew][kJoinQuads];
+#pragma unroll
+    for (int i = 0; i < kFew; ++i)
+      if (i < parts) {
+        const float* rec = record(i);
+        mi[i] = rec[c];
+        li[i] = rec[sh.vt + c];
+#pragma unroll
+        for (int q = 0; q < kJoinQuads; ++q) x[i][q] = quad(rec, q);
+      }
+#pragma unroll
+    for (int i = 0; i < kFew; ++i)
+      if (i < parts) m = fmaxf(m, mi[i]);
+#pragma unroll
+    for (int i = 0; i < kFew; ++i)
+      if (i < parts) add(mi[i], li[i], x[i]);
+  } else {
 #pragma unroll 8
-  for (int i = 0; i < parts; ++i) m = fmaxf(m, record(i)[c]);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < parts; ++i) m = fmaxf(m, record(i)[c]);
 #pragma unroll 8
-  for (int i = 0; i < parts; ++i) {
-    const float* rec = record(i);
-    const float f = exp2_approx(rec[c] - m);
-    l = fmaf(rec[sh.vt + c], f, l);
-    const float4 x = reinterpret_cast<const float4*>(rec + 2 * sh.vt)[(size_t)warp * sh.vt + c];
-    acc.x = fmaf(x.x, f, acc.x);
-    acc.y = fmaf(x.y, f, acc.y);
-    acc.z = fmaf(x.z, f, acc.z);
-    acc.w = fmaf(x.w, f, acc.w);
+    for (int i = 0; i < parts; ++i) {
+      const float* rec = record(i);
+      float4 x[kJoinQuads];
+#pragma unroll
+      for (int q = 0; q < kJoinQuads; ++q) x[q] = quad(rec, q);
+      add(rec[c], rec[sh.vt + c], x);
+    }
   }
   const int j = row_of(sh, vec0 + c), head = d.kvh * sh.G + (vec0 + c) - j * sh.G;
   const size_t row = ((size_t)d.b * g.R + j) * g.Hq + head;
@@ -497,10 +531,13 @@ dense_join_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   float f = 1.f;
   if (p.sinks) add_sink(p.sinks[head], m, l, f);
   const float r = l == 0.f ? 0.f : f * p.v_scale / l;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * r, acc.y * r);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * r, acc.w * r);
-  *reinterpret_cast<uint2*>(p.out + row * D + 4 * warp) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  uint2* to = reinterpret_cast<uint2*>(p.out + row * D) + warp * kJoinQuads;
+#pragma unroll
+  for (int q = 0; q < kJoinQuads; ++q) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[q].x * r, acc[q].y * r);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[q].z * r, acc[q].w * r);
+    to[q] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
   if (warp == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
@@ -531,7 +568,7 @@ size_t dense_carve(const dense::Shape& s, void* workspace, dense::Work* w) {
 cudaError_t launch_dense_join(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(dense::desc_count(s), (std::min(s.vt, s.g.R * s.G) + 31) / 32,
-                     s.g.D / (4 * dense::kJoinWarps));
+                     s.g.D / (4 * dense::kJoinQuads * dense::kJoinWarps));
   cfg.blockDim = dim3(dense::kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -373,11 +373,11 @@ struct Converter {
 // too short for bulk copies, as the floats that the softmax takes (bytes, taken apart by every
 // thread of it, made a chunk's turn 600 cycles longer for a tile).
 //
-// Measured (GB300): two context chunks of 512 rows, 32 heads on 4 of 128, behind 14000 to 16384 tokens 205 us
-// (1.22 PFLOP/s; NVFP4 pages 185: their codes are half the bytes to read from shared memory, and their
+// Measured (GB300): two context chunks of 512 rows, 32 heads on 4 of 128, behind 14000 to 16384 tokens 202 us
+// (1.24 PFLOP/s; NVFP4 pages 182: their codes are half the bytes to read from shared memory, and their
 // scales are gone before the softmax; without the second kernel that joins the parts 190); 4 x 256 rows of
 // 24 heads on 2 of 256 over 16384 319 us, 1.28 PFLOP/s; windowed verify rows (32 requests x 4 rows, 24 heads
-// on 2 of 256, window 4096) 47.8 us for 138 MB, 7 of them the join.
+// on 2 of 256, window 4096) 45.2 us for 138 MB, 4 to 5 of them the join.
 //
 // A lane has a 16-byte piece (16 codes, two 16-byte pieces of the tile) per step; a row's pieces belong to
 // neighbouring lanes, of eight of them the upper four store their two in the other order
@@ -602,7 +602,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         for (int d0 = 0; d0 < D && some; d0 += 128) {
           uint4 x[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = real ? __ldg(from + d0 / 8 + i) : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < 16; ++i) x[i] = real ? from[d0 / 8 + i] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int c4 = 0; c4 < 4; ++c4) {
             uint32_t v[16];
