@@ -767,6 +767,9 @@ qsa_status_t qsa_dense_attention_fp8(const qsa_geom_t *geom, const void *q_bf16,
  * Row i of a sequence sees its rows max(0, i + 1 - window)..i.  Of the geometry
  * batch, the heads and head_dim matter.  Logits, sums and outputs are fp32,
  * weights exp(z_t - lse) are rounded to bf16 (8 bits) before the product with V.
+ * The weights' sum is as good for a row of 2^24 tokens as for one of 128; the
+ * products are added to out 16 tokens at a time, and each addition rounds what is
+ * there (for n tokens at most n 2^-27 of sum_t exp(z_t - lse) |V_t|).
  * What lies outside a sequence's rows is not looked at.  Keys that are not
  * finite make so the rows that see them, and values that are not also rows
  * of their sequence up to 512 before them.

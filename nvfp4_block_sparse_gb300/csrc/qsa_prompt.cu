@@ -341,7 +341,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       const int lo_most = __reduce_max_sync(0xffffffffu, real ? lo : 0);
       const bool some = __any_sync(0xffffffffu, real);   // (a warp without a row only keeps step)
       float base = kNoBase;
-      float2 sum = make_float2(0.f, 0.f);
+      RowSum sum;
       const int unit_chunks = u.chunks, lo_all = u.lo_all;
       for (int c = 0; c < unit_chunks; ++c, ++chunks) {
         const int y = kTiles == 2 ? t : chunks & 1;      // S buffer
@@ -384,8 +384,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
           const float nb = moves ? top : base;
           const float alpha = exp2_approx(base - nb);
           base = nb;
-          sum.x *= alpha;
-          sum.y *= alpha;
+          sum.scale(alpha);
           if (c > 0) {
             // with two tiles barS has said that O is complete up to the chunk before
             if (kTiles == 1 && gave_up(barO, chunks - 1)) { dead = true; break; }
@@ -403,6 +402,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         }
         // P, 64 tokens at a time, over the first columns they were read from.
         const float2 c2 = make_float2(a.c, a.c), b2 = make_float2(-base, -base);
+        float2 part = make_float2(0.f, 0.f);               // the chunk's weights
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -413,7 +413,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
               const int k = 64 * h + 32 * q + 2 * i;
               const float2 x = fma2(make_float2(z[k], z[k + 1]), c2, b2);
               const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-              sum = add2(sum, e);
+              part = add2(part, e);
               pk[i] = pack_bf16(e.x, e.y);
             }
             tmem_st16u(tS + 32 * h + 16 * q, pk);
@@ -422,6 +422,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
           tc_fence_before();
           warp_arrive<CG>(&pready[2 * y + h]);
         }
+        sum.add(part);
       }
       if (dead) break;
       // ---- the unit's output, the next unit found meanwhile ------------------------------
@@ -429,7 +430,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       if (dead || gave_up(&partO[t], parts)) { dead = true; break; }
       ++parts;
       tc_fence_after();
-      float l = sum.x + sum.y, f = 1.f;
+      float l = sum.total(), f = 1.f;
       if (a.sinks && real) {
         const float s2 = a.sinks[head] * kLog2e, nm = fmaxf(base, s2);
         f = exp2_approx(base - nm);

@@ -40,6 +40,27 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// The sum of a long row's weights, joined chunk by chunk with what each addition's rounding loses (Kahan,
+// 1965): next to 2^24 others of its size a weight would vanish, and of weights that are alike all
+// roundings go one way (131072 tokens of one row in plain sums: lse off by 1.5e-3).  A chunk's own
+// weights are added up first, so this is four packed operations in 128 tokens, for the even tokens and for the
+// odd ones (one sum of both, which the next chunk waits for: a prompt of 8192 tokens 311 -> 320 us; so 311).
+struct RowSum {
+  float2 sum = make_float2(0.f, 0.f), lost = make_float2(0.f, 0.f);
+  __device__ __forceinline__ void add(float2 part) {
+    const float2 minus = make_float2(-1.f, -1.f), y = add2(part, lost), t = add2(sum, y);
+    lost = fma2(fma2(sum, minus, t), minus, y);          // y - (t - sum)
+    sum = t;
+  }
+  __device__ __forceinline__ void scale(float f) {
+    sum.x *= f;
+    sum.y *= f;
+    lost.x *= f;
+    lost.y *= f;
+  }
+  __device__ __forceinline__ float total() const { return sum.x + sum.y; }
+};
+
 // ---- rows of neighbouring lanes ------------------------------------------------
 // Four lanes' rows of four 16-byte pieces transposed: lane j then has piece j of each of the four rows,
 // so that a store writes runs of 64 bytes.

@@ -225,3 +225,22 @@ def test_refused():
         with pytest.raises(qsa.QsaError):
             call(**kw)
     call(q=q[:0], k=k[:0], v=v[:0], cu=torch.zeros(3, dtype=torch.int32, device=DEV))      # no rows
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("gap", [17.625, 0.357])
+def test_sums_of_long_rows(D, gap):
+    """131072 tokens: a first one whose weight the others', 2^-25.4 of it each, would vanish next to; and others
+    of 0.7 of the first's, which are alike to the last bit."""
+    n, cu = 131072, packed([131072])
+    q, k, v = inputs(n, 1, 1, D)
+    q[:], k[:] = 0, 0
+    q[..., 0], k[0, 0, 0] = 1, gap
+    out, lse = run(q, k, v, cu, sm=1.0)
+    kh, vh = host(k[:, 0], v[:, 0])
+    for r in (60000, 100000, n - 2, n - 1):
+        want = c8.attend(host(q[r])[0], kh[:r + 1], vh[:r + 1], 1.0, weight=2.0**-8, alike=True)
+        # lse as of attend().  out: each of the n / 16 products that are added to it one after the other rounds what
+        # is there, by a step of 2^-23 at most
+        mag = np.exp(kh[None, :r + 1, 0] - want[1][:, None]) @ np.abs(vh[:r + 1])
+        c8.compare(out[r], lse[r], [want[0], want[1], want[2] + (r / 16 + 1) * 2.0**-23 * mag, want[3]])
