@@ -691,7 +691,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       uint32_t there0 = there_of(blk0 + lane), there1 = there_of(blk0 + 32 + lane);
       float base = kNoBase;
       [[maybe_unused]] float most = -INFINITY;
-      float2 sum = make_float2(0.f, 0.f);
+      RowSum sum;
+      float2 part = make_float2(0.f, 0.f);                 // the chunk's weights
       for (int c = 0; c < seg.todo; ++c, ++chunks) {
         const int y = kTiles == 2 ? t : chunks & 1;      // S buffer
         const uint32_t tS = tmem + y * kTok + lane_off;
@@ -726,6 +727,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         float z[kTok];
 #pragma unroll
         for (int i = 0; i < kTok / 32; ++i) tmem_ld32(tS + 32 * i, z + 32 * i);
+        // (the chunk before's, while the loads are on their way: two context chunks 630 us; behind the weights 636)
+        sum.add(part);
         tmem_wait_ld_of(z);
         if (edge) {
 #pragma unroll
@@ -774,8 +777,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           const float nb = moves ? (E8 ? floorf(most) : top) - kBelow : base;
           const float alpha = exp2_approx(base - nb);
           base = nb;
-          sum.x *= alpha;
-          sum.y *= alpha;
+          sum.scale(alpha);
           if (c > 0) {
             // with two tiles barS has said that O is complete up to the chunk before
             if (kTiles == 1 && gave_up(barO, chunks - 1)) { dead = true; break; }
@@ -792,6 +794,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
           }
         }
         // P, 64 tokens at a time, over the first columns they were read from.
+        part = make_float2(0.f, 0.f);
 #pragma unroll
         for (int h = 0; h < T::kHalves; ++h) {
           float2 c2 = make_float2(cq, cq), b2 = make_float2(-base, -base);
@@ -805,16 +808,16 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
                 const float vb = of(ex[2 + (n16 >> 2)], n16 & 3) - base, back = of(ex[4 + (n16 >> 2)], n16 & 3);
                 c2 = make_float2(bc[n16], bc[n16]);
                 b2 = make_float2(vb, vb);
-                float2 part = make_float2(0.f, 0.f);
+                float2 block = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                   const int k = 64 * h + 32 * q + 16 * u + 2 * i;
                   const float2 a = fma2(make_float2(z[k], z[k + 1]), c2, b2);
                   const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
-                  part = add2(part, e);
+                  block = add2(block, e);
                   pk[8 * u + i] = pack_weights(e.x, e.y);
                 }
-                sum = fma2(part, make_float2(back, back), sum);
+                part = fma2(block, make_float2(back, back), part);
               }
             } else {
 #pragma unroll
@@ -822,7 +825,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
                 const int k = 64 * h + 32 * q + 2 * i;
                 const float2 a = fma2(make_float2(z[k], z[k + 1]), c2, b2);
                 const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
-                sum = add2(sum, e);
+                part = add2(part, e);
                 pk[i] = pack_weights(e.x, e.y);
               }
             }
@@ -840,7 +843,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
       ++s_waits;
       if (late) { dead = true; break; }
       tc_fence_after();
-      float l = sum.x + sum.y, m = base, f = 1.f;
+      sum.add(part);
+      float l = sum.total(), m = base, f = 1.f;
       const bool whole = seg.begins && seg.ends;
       if (whole && p.sinks && real) {
         const float s2 = p.sinks[head] * kLog2e, nm = fmaxf(m, s2);

@@ -261,3 +261,54 @@ def test_every_code(D, R, G):
         assert torch.isnan(out[-1, :, 7]).all() and torch.isfinite(lse[-1]).all() == (pool == "v_pool")
         if pool == "k_pool":
             assert torch.isnan(out[-1]).all()
+
+
+@pytest.mark.parametrize("cache", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("D,R,G", [(128, 1, 4), (128, 5, 4), (128, 40, 8), (256, 1, 4), (256, 3, 8), (256, 20, 8)])
+def test_sums_of_long_rows(cache, D, R, G):
+    """160 requests of the same 131072 tokens, so that each is summed in a piece: a first token next to whose weight
+    the others', e^-18 of it each, would vanish; and others of 0.7 of the first's, alike to the last bit."""
+    P, B, L = 64, 160, 131072
+    NP = L // P
+    w = dict(batch=B, rows_per_req=R, num_q_heads=G, num_kv_heads=1, head_dim=D, index_dim=64, page_size=P,
+             max_blocks=NP, num_pages=NP, sm_scale=1.0)
+    table = np.random.default_rng(1).permutation(NP).astype(np.int32)
+    v = np.random.default_rng(0).integers(0, 8, (NP, 1, P, D)).astype(np.uint8)
+    e2m1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+    vals = e2m1[v[table]].reshape(L, D)
+    d = dict(page_table=torch.from_numpy(table).to(DEV).repeat(B, 1),
+             seqlens=torch.full((B,), L, dtype=torch.int32, device=DEV))
+    q = torch.zeros(B * R, G, D, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 1
+    for gap in (18.0, 0.375):
+        if cache == "fp8":
+            d["k_pool"] = torch.zeros(NP, 1, P, D, dtype=torch.uint8, device=DEV)
+            d["k_pool"][table[0], 0, 0, 0] = int(c8.codes_of([gap])[0])
+            d["v_pool"] = torch.from_numpy(c8.codes_of(e2m1)[v]).to(DEV)
+            d["k_exp"] = torch.full((NP, 1, P // 16), 127, dtype=torch.uint8, device=DEV)
+            d["v_exp"] = d["k_exp"].clone()
+            out, lse = run(w, q, d=d)
+        else:
+            d["k_pool"] = torch.zeros(NP, 1, P, D // 2, dtype=torch.uint8, device=DEV)
+            d["v_pool"] = torch.from_numpy(v[..., 0::2] | v[..., 1::2] << 4).to(DEV)
+            for n in ("k", "v"):
+                d[n + "_sf"] = torch.full((NP, 1, P, D // 16), 0x38, dtype=torch.uint8, device=DEV)      # 1.0
+            d["k_pool"][table[0], 0, 0, 0] = 5                                                           # 3.0
+            d["k_sf"][table[0], 0, 0, 0] = int(c8.codes_of([gap / 3])[0])
+            ws = torch.empty(qsa.qsa_dense_attention_workspace_bytes(geom(w)), dtype=torch.uint8, device=DEV)
+            qsa.qsa_workspace_init(ws)
+            out, lse = torch.empty_like(q), torch.empty(B * R, G, device=DEV)
+            qsa.qsa_dense_attention(geom(w), q, d["k_pool"], d["k_sf"], d["v_pool"], d["v_sf"], 1.0, 1.0, 1.0,
+                                    d["page_table"], d["seqlens"], out, lse, ws)
+            assert qsa.qsa_workspace_status(ws) == 0
+        k = np.zeros((L, D))
+        k[0, 0] = gap
+        for r in (0, R - 1):
+            n = L - R + 1 + r
+            ref, ref_lse, tol, lse_tol = c8.attend(np.eye(1, D).repeat(G, 0), k[:n], vals[:n], 1.0,
+                                                   exps=np.full(n, 127), alike=True)
+            # (and of out: each of the n / 16 products that are added to it one after the other rounds what is
+            # there, by a step of 2^-23 at most; all values are positive)
+            tol = tol + (n / 16 + 1) * 2.0**-23 * ref
+            for b in (0, B // 2, B - 1):
+                c8.compare(out[b * R + r], lse[b * R + r], [ref, ref_lse, tol, lse_tol])
