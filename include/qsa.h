@@ -771,8 +771,8 @@ qsa_status_t qsa_dense_attention_fp8(const qsa_geom_t *geom, const void *q_bf16,
  * products are added to out 16 tokens at a time, and each addition rounds what is
  * there (for n tokens at most n 2^-27 of sum_t exp(z_t - lse) |V_t|).
  * What lies outside a sequence's rows is not looked at.  Keys that are not
- * finite make so the rows that see them, and values that are not also rows
- * of their sequence up to 512 before them.
+ * finite make so the rows that see them, and values the rows that see them, in
+ * the value's dim; other rows have the bits that they have without them.
  * The result does not depend on how the work is divided: the same inputs give
  * the same bits.
  *

@@ -45,7 +45,8 @@
 //             tensor memory to the output
 //   copy      one warp: Q, K and V by TMA into a ring of stages
 //   relay     one warp: tells the first CTA's MMA warp that a stage is there, and zeroes V rows
-//             that no row of the unit sees (another sequence's, or what lies behind the last)
+//             that no row of the unit sees (another sequence's, or what lies behind the last) and
+//             elements that are not finite (see "Values that are not finite")
 //   MMA       one warp of the first CTA.  At head_dim 128 two tiles take turns: O_0, S_0 of the next
 //             chunk, O_1, S_1; at 256 one tile has two S buffers and S runs ahead.  Its code comes from far,
 //             between the softmax warps' long loops, so its loops over MMAs are rolled
@@ -91,6 +92,8 @@ struct Args {
   float c;                 // sm_scale log2(e)
   const int32_t* cu;       // [B + 1]
   const float* sinks;
+  const __nv_bfloat16* v;  // as map_v has it; its row stride in elements
+  long long v_stride;
   __nv_bfloat16* out;      // [T][Hq][D]
   float* lse;              // [T][Hq]
   int* status;
@@ -115,7 +118,7 @@ struct PT {
   static constexpr int kVBlk = kTok * 128;               // 64 dims of 128 tokens
   static constexpr uint32_t kOCol = 256;
   static constexpr int kBars = 3 * kStages + 3 + 2 + 4 + 1 + 2 + 1 + kUnits;
-  static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStage + kUnits * 32 + kBars * 8 + 16;
+  static constexpr int kSmem = 1024 + kTiles * kQBytes + kStages * kStage + kUnits * 32 + kBars * 8 + 16 + kUnits * 8;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -154,12 +157,88 @@ struct Units {
       dead = true;
       return false;
     }
-    ++at;
-    const int4 a = slots[2 * s], b = slots[2 * s + 1];
-    u = Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+    u = before(at++);
     return u.chunks > 0;
   }
+  // Unit `nth`, which the reader has come to and is not yet two units past.
+  __device__ __forceinline__ Unit before(int nth) const {
+    const int s = nth % kUnits;
+    const int4 a = slots[2 * s], b = slots[2 * s + 1];
+    return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+  }
 };
+
+// ---- values that are not finite ----------------------------------------------------
+// A weight of 0 times a V that is not finite is NaN: of a token that some rows of the unit see and
+// others do not (from the second row's on, and those that the last row has left behind), such a value would
+// reach rows that do not see it.  The relay takes these out of the tile and leaves a note; behind such a unit,
+// rows get what the MMA left out, from V as it lies in memory.  The notes say for which unit (its number from 1
+// on) rather than whether, so that nobody has to take them back; each of the pair's relays, which has half of the
+// dims, leaves one in both CTAs, ahead of the arrival that lets the chunk's products begin. Only tokens of
+// that kind are looked at, with one multiply-add for two elements: the relay's instructions are taken from the
+// softmax warps' (64 prompts of 50 to 150 tokens, 32 heads on 4 of 128, 38.8 us without, 41.0 with; windowed 150.0
+// and 150.6, a window of 64 49.8 and 49.8, long 307.5 and 307.6; the whole chunk, four instructions an element, 38.9 and
+// 43.0, 150.0 and 156, 49.8 and 58).
+struct Partly {            // tokens of the unit's sequence that not all of its rows see: those before `left`
+  int left, right;         // and those from `right` on
+  __device__ __forceinline__ Partly(const Unit& u, int window)
+      : left(window > 0 ? u.n_all - window : 0), right(u.row0 + 1) {}
+};
+// Bits 15 and 31 for two bf16 that are not finite (the others are anything).
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
+__device__ __forceinline__ uint32_t not_finite8(const uint4& x) {
+  return (not_finite2(x.x) | not_finite2(x.y) | not_finite2(x.z) | not_finite2(x.w)) & 0x80008000u;
+}
+// Zeros times eight bf16, added to `sum`: NaN from the first one on that is not finite.
+__device__ __forceinline__ __nv_bfloat162 zeros_or_nan(const uint4& x, __nv_bfloat162 sum) {
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), zero, sum);
+  return sum;
+}
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {      // those as zeros
+  return w & ~(((not_finite2(w) & 0x80008000u) >> 15) * 0xFFFFu);
+}
+__device__ __forceinline__ void note_both(uint32_t* at, uint32_t value) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.u32 [a], %1;\n\t"
+      "mapa.shared::cluster.u32 a, %0, 1;\n\tst.shared::cluster.u32 [a], %1;\n\tfence.acq_rel.cluster;\n\t}" ::"r"(
+          smem_u32(at)), "r"(value)
+      : "memory");
+}
+
+// Adds to a row's output the values that are not finite of the tokens that it sees and other rows of the unit
+// do not.  v: token 0 of the sequence.
+template <int D>
+__device__ __forceinline__ void add_not_finite(const Unit& u, int window, const __nv_bfloat16* v, long long stride, int lo,
+                                               int n, __nv_bfloat16* out) {
+  const Partly part(u, window);
+#pragma unroll 1
+  for (int d = 0; d < D; d += 8) {
+    float add[8] = {};
+    bool any = false;
+#pragma unroll 1
+    for (int t = lo; t < n; ++t) {
+      if (t >= part.left && t < part.right) t = part.right;
+      if (t >= n) break;
+      const uint4 x = *reinterpret_cast<const uint4*>(v + t * stride + d);
+      if (!not_finite8(x)) continue;
+      any = true;
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t odd = w[k] & ~finite2(w[k]);
+        add[2 * k] += __uint_as_float(odd << 16);
+        add[2 * k + 1] += __uint_as_float(odd & 0xFFFF0000u);
+      }
+    }
+    if (!any) continue;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (add[k] != 0.f) out[d + k] = __float2bfloat16_rn(__bfloat162float(out[d + k]) + add[k]);
+  }
+}
 
 // Walks a worker's units; the copy warp's.  With up to 32 sequences a lane has one, and the
 // units go by their number within their sequence, last (longest) first.  With more sequences
@@ -281,6 +360,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
   uint64_t* mdone = partO + 2;                           // after a give-up: every MMA issued has completed
   uint64_t* uthere = mdone + 1;                          // [kUnits]
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(uthere + kUnits);
+  uint32_t* s_odd = s_tmem + 4;                          // [kUnits][CTA]: number of a unit with V that is not finite
 
   if (tid == 0) {
     for (int s = 0; s < T::kStages; ++s) {
@@ -301,6 +381,7 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
     mbar_init(barO, 1);
     mbar_init(mdone, 1);
     s_tmem[1] = 0u;   // set when a CTA of the pair gave up
+    for (int i = 0; i < 2 * kUnits; ++i) s_odd[i] = 0u;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -461,6 +542,14 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
                 make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
       }
       if (store) a.lse[orow] = (base + log2f(l)) * kLn2;
+      const uint2 odd = *reinterpret_cast<const uint2*>(s_odd + 2 * ((parts - 1) % kUnits));
+      if (__builtin_expect(odd.x == (uint32_t)parts || odd.y == (uint32_t)parts, false)) {
+        const Unit was = units.before(parts - 1);
+        __syncwarp();                                    // (the row was stored by its neighbours)
+        if (store)
+          add_not_finite<D>(was, a.window, a.v + was.start * a.v_stride + was.kvh * D, a.v_stride, lo, n,
+                            a.out + orow * D);
+      }
     }
   } else {
     if constexpr (kTiles == 2) regs_down<T::kOtherRegs>();
@@ -519,27 +608,56 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
       if (parts > 0 && gave_up(qfull, parts - 1)) dead = true;
     } else if (warp == T::kRelay) {
       // ==== relay ====================================================================
+      // Q of the first unit as soon as it is there (S waits for it), of the others, which follows the last S of
+      // the unit before, behind V, which has long been there.
+      auto q_relayed = [&]() {
+        if (gave_up(qfull, parts)) dead = true;
+        else warp_arrive<CG>(qready);
+        ++parts;
+        return !dead;
+      };
       while (!dead && units.next(u, dead)) {
+        const int nth = units.at;                        // from 1 on
+        const Partly part(u, a.window);
         for (int c = 0; c < u.chunks && !dead; ++c) {
           const int tok0 = u.lo_all + c * kTok;
 #pragma unroll 1
           for (int v = 0; v < 2; ++v, ++pos) {
             const int s = pos % T::kStages, use = pos / T::kStages;
+            if (v && nth == 1 && c == 0 && !q_relayed()) break;
             if (gave_up(&full[s], use)) { dead = true; break; }
-            if (v && tok0 + kTok > u.n_all) {
+            if (v && (tok0 + kTok > part.right || tok0 < part.left)) {
+              uint4* tile = reinterpret_cast<uint4*>(ring + s * T::kStage);
               // rows of V that no vector of the unit sees may hold anything; 0 keeps 0 x V at 0
-              for (int x = lane; x < T::kStage / 16; x += 32)
-                if (tok0 + ((x >> 3) & (kTok - 1)) >= u.n_all)
-                  *reinterpret_cast<uint4*>(ring + s * T::kStage + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+              for (int x = 8 * max(u.n_all - tok0, 0) + lane; x < 8 * kTok; x += 32)
+#pragma unroll
+                for (int i = 0; i < T::kStage / T::kVBlk; ++i)
+                  tile[i * (T::kVBlk / 16) + x] = make_uint4(0u, 0u, 0u, 0u);
+              __nv_bfloat162 odd = __float2bfloat162_rn(0.f);
+#pragma unroll 1
+              for (int side = 0; side < 2; ++side) {
+                const int from = side ? max(part.right - tok0, 0) : 0;
+                const int to = min(side ? u.n_all : min(part.left, part.right), tok0 + kTok) - tok0;
+#pragma unroll 4
+                for (int x = 8 * from + lane; x < 8 * to; x += 32)
+#pragma unroll
+                  for (int i = 0; i < T::kStage / T::kVBlk; ++i) odd = zeros_or_nan(tile[i * (T::kVBlk / 16) + x], odd);
+              }
+              if (__any_sync(0xffffffffu, __hisnan(odd.x) || __hisnan(odd.y))) {
+#pragma unroll 1
+                for (int x = lane; x < T::kStage / 16; x += 32) {
+                  const int tok = tok0 + ((x >> 3) & (kTok - 1));
+                  const uint4 y = tile[x];
+                  if (tok < part.left || tok >= part.right)
+                    tile[x] = make_uint4(finite2(y.x), finite2(y.y), finite2(y.z), finite2(y.w));
+                }
+                if (lane == 0) note_both(&s_odd[2 * ((nth - 1) % kUnits) + rank], (uint32_t)nth);
+              }
               fence_proxy_async_smem();
             }
             warp_arrive<CG>(&ready[s]);
           }
-          if (c == 0 && !dead) {
-            if (gave_up(qfull, parts)) { dead = true; break; }
-            warp_arrive<CG>(qready);
-            ++parts;
-          }
+          if (nth > 1 && c == 0 && !dead) q_relayed();
         }
       }
     } else if (warp == T::kMma && rank == 0) {
@@ -751,6 +869,8 @@ cudaError_t launch_prompt(const Geom& g, const PromptArgs& p, cudaStream_t strea
   a.c = (float)std::min((double)p.sm_scale * 1.4426950408889634, 3e38);
   a.cu = p.cu;
   a.sinks = p.sinks;
+  a.v = reinterpret_cast<const __nv_bfloat16*>(p.v);
+  a.v_stride = p.v_stride;
   a.out = reinterpret_cast<__nv_bfloat16*>(p.out);
   a.lse = p.lse;
   a.status = reinterpret_cast<int*>(p.workspace);

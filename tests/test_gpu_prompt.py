@@ -244,3 +244,52 @@ def test_sums_of_long_rows(D, gap):
         # is there, by a step of 2^-23 at most
         mag = np.exp(kh[None, :r + 1, 0] - want[1][:, None]) @ np.abs(vh[:r + 1])
         c8.compare(out[r], lse[r], [want[0], want[1], want[2] + (r / 16 + 1) * 2.0**-23 * mag, want[3]])
+
+
+def spoiled(v, G, cu, window, at):
+    """v with elements that are not finite put at `at` (row, KV head, dim, value), and what the outputs have of them:
+    the rows that see them, in that dim, their sum."""
+    x, add = v.clone(), torch.zeros(v.shape[0], v.shape[1] * G, v.shape[2], device=DEV)
+    for row, h, d, value in at:
+        x[row, h, d] = value
+        end = min(b for b in cu if b > row)
+        end = min(end, row + window) if window else end
+        add[row:end, h * G:(h + 1) * G, d] += value
+    return x, add
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("G", [1, 4, 8])
+@pytest.mark.parametrize("window", [0, 1, 50, 128, 700])
+def test_values_that_a_row_does_not_see(D, G, window):
+    """Values that are not finite make so the rows that see them, in their dims, and nothing else: not the rows
+    ahead of them, and not those that have left them behind."""
+    cu = packed([1400, 3, 700])
+    q, k, v = inputs(cu[-1], 2 * G, 2, D)
+    rng = np.random.default_rng(G)
+    kinds = [math.nan, math.inf, -math.inf]
+    at = [(int(r), int(rng.integers(2)), int(rng.integers(D)), kinds[int(rng.integers(3))])
+          for r in rng.integers(0, cu[-1], 12)]
+    at += [(0, 0, 0, math.nan), (1399, 1, D - 1, math.inf), (1401, 0, 5, math.inf), (1402, 0, 5, -math.inf),
+           (cu[-1] - 1, 1, 64, math.nan)]
+    plain, plain_lse = run(q, k, v, cu, window=window)
+    x, add = spoiled(v, G, cu, window, at)
+    out, lse = run(q, k, x, cu, window=window)
+    assert torch.equal(lse, plain_lse)
+    want = (plain.float() + add).to(torch.bfloat16)
+    bad = ~((out == want) | (out.isnan() & want.isnan()))
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:3].tolist())
+
+
+def test_values_that_a_row_does_not_see_many_sequences():
+    """The same where each CTA has many units, some with such values and some without."""
+    rng = np.random.default_rng(3)
+    cu = packed(rng.integers(1, 300, 400))
+    for D in (128, 256):
+        q, k, v = inputs(cu[-1], 8, 2, D)
+        at = [(int(r), int(rng.integers(2)), int(rng.integers(D)), math.nan) for r in rng.integers(0, cu[-1], 60)]
+        plain, plain_lse = run(q, k, v, cu)
+        x, add = spoiled(v, 4, cu, 0, at)
+        out, lse = run(q, k, x, cu)
+        want = (plain.float() + add).to(torch.bfloat16)
+        assert torch.equal(lse, plain_lse) and torch.equal(out.nan_to_num(7.0), want.nan_to_num(7.0))
