@@ -732,9 +732,9 @@ qsa_status_t qsa_dense_attention(const qsa_geom_t *geom, const void *q_bf16,
  * Precision is qsa_dense_attention's; weights are rounded to 11 bits times their
  * block's scale of V, so "2^-22 of the row's largest" is of the largest
  * exp(z_t) 2^exp; and weights below 2^-38 of the row's largest may be missing from
- * the sum where V's scales are as far apart as can be.  Codes that are NaN make
- * the rows that see their keys not finite, and a value that is makes so the rows
- * of its request too that look at its block of 128 tokens without seeing it.
+ * the sum where V's scales are as far apart as can be.  Keys with NaN codes make
+ * the rows that see them not finite, and values with NaN codes make NaN of the
+ * rows that see them, in the codes' dims, and of nothing else.
  *
  * Returns as qsa_dense_attention; k_exp and v_exp are 16-byte aligned.
  */

@@ -56,6 +56,10 @@ __device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
   return r;
 }
 
+// Which of four e4m3 codes are NaN: the upper bits of their bytes.  And the codes with those as zeros.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xFFu); }
+
 struct Shape {
   Geom g;
   int G;         // query heads per KV head

@@ -107,6 +107,9 @@ dense8_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ W
   // (32 / kPr rows per copy: that many rows on in the swizzle)
   auto c_to = [&](int i) { return (c_dst ^ (uint32_t)((((32 / kPr) * i) & 7) << 4)) + 512u * i; };
 
+  // the dims of rows gid and gid + 8 of output tile i: this one and the next
+  auto first_dim = [](int gid, int i) { return 128 * (i >> 3) + 16 * gid + 2 * (i & 7); };
+
   const int psh = 31 - __clz(g.P);                   // log2 of the page size
   Cursor cursor(span);
   Seg seg;
@@ -116,6 +119,7 @@ dense8_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ W
     const int vec0 = seg.vec0, vecs = seg.vecs, cap = g.MB * g.P;
     const int n_all = seg.n_all, n_least = seg.n_least, lo_all = seg.lo_all, lo_most = seg.lo_most;
     const int mine = todo > warp ? (todo - warp + W - 1) / W : 0;   // this warp's chunks
+    const bool partly = n_least < n_all || lo_all < lo_most;        // not all vectors see the same
 
     // ---- the warp's query vectors: on their way while the pages are looked up ----------
     constexpr int kPer = (kCols + W - 1) / W, E = D / 32;
@@ -254,6 +258,56 @@ dense8_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ W
                            : "memory");
           }
           __syncwarp();
+        }
+        if (partly && edge) {
+          // Tokens that some of the vectors see and others do not: a NaN among their codes goes to the outputs
+          // of those that see it, and out of V, where it would reach all (0 x NaN).  (Four rows of a window of 1024
+          // 19.1 us without this, 19.5 so; 16 requests x 4 rows of 8192 to 16384 tokens 45.6 and 45.8.)
+          const uint32_t sv = st + C::kK;
+          // (the pieces x of these tokens; between lo_most and n_least all see them)
+          auto pieces = [&](auto&& each) {
+#pragma unroll 1
+            for (int side = 0; side < 2; ++side) {
+              const int from = max((side ? n_least : lo_all) - tok0, 0), to = min((side ? n_all : lo_most) - tok0, TOK);
+#pragma unroll 1
+              for (int x = from * kPr + lane; x < to * kPr; x += 32) each(x);
+            }
+          };
+          uint32_t odd = 0u;
+          pieces([&](int x) {
+            const uint4 y = lds128(sv + 16 * x);
+            odd |= nan_codes(y.x) | nan_codes(y.y) | nan_codes(y.z) | nan_codes(y.w);
+          });
+          if (__any_sync(0xffffffffu, odd != 0u)) {
+#pragma unroll 1
+            for (int r = 0; r < TOK; ++r) {
+              const int tok = tok0 + r;
+              if (tok >= lo_most && tok < n_least) continue;
+#pragma unroll
+              for (int i = 0; i < DT; ++i) {
+                const int d = first_dim(gid, i);
+                uint16_t two;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(two) : "r"(sv + r * C::kRow + swz(r, d >> 4) * 16 + (d & 15)));
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int c = 8 * t + 2 * tig + e;
+                    if (tok >= s_n[c] || tok < s_lo[c]) continue;
+                    if ((two & 0x7F) == 0x7F) o[i][t][e] = __uint_as_float(0x7FC00000u);
+                    if ((two & 0x7F00) == 0x7F00) o[i][t][2 + e] = __uint_as_float(0x7FC00000u);
+                  }
+              }
+            }
+            __syncwarp();
+            pieces([&](int x) {
+              const uint4 y = lds128(sv + 16 * x);
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sv + 16 * x), "r"(without_nan(y.x)),
+                           "r"(without_nan(y.y)), "r"(without_nan(y.z)), "r"(without_nan(y.w))
+                           : "memory");
+            });
+            __syncwarp();
+          }
         }
         // S^T
         float z[MT][NT][4];
@@ -396,7 +450,7 @@ dense8_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ W
     __syncthreads();   // every warp's copies have landed and been read: the ring is free
 
     finish_unit<C, kChkOut, kChkJoin>(sh, p, span, cursor, seg, smem, s_n, o, base, sum,
-                                      [](int gid, int i) { return 128 * (i >> 3) + 16 * gid + 2 * (i & 7); });
+                                      first_dim);
     __syncthreads();
   }
 }

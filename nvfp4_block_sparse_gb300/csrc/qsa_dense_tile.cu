@@ -325,7 +325,7 @@ struct Converter {
   // Chunk number `chunks` of the CTA, from token tok0, out of stage `slot` into its tile; false
   // when the wait for the tile gave up.
   __device__ __forceinline__ bool convert(const Seg& seg, int tok0, int chunks, int slot, uint32_t copied,
-                                          bool v) {
+                                          bool v, uint32_t*) {
     const int lane = threadIdx.x & 31;
     const int x = chunks & 1, use = chunks >> 1;
     uint8_t* tile = tiles + x * kBytes;
@@ -364,6 +364,82 @@ struct Converter {
     return true;
   }
 };
+
+// ---- values that are not finite ----------------------------------------------------
+// A weight of 0 times a V that is not finite is NaN: of a token that some of the unit's vectors see and others
+// do not, such a value would reach the others.  A converter leaves these values out of the tile and leaves a
+// note (in a pair, whose converters have half of the dims each, in both CTAs), ahead of the arrival that lets
+// the MMAs begin.  Where there is one, the CTA goes through all its parts once more when everything is done, and
+// vectors get what was left out from the pages themselves.  (Measured, 2 x 512 context rows, 24 vectors of 128,
+// windowed verify, 4 x 256 rows of 256: without any of it 203.5, 76.8, 45.4 and 313 us; so 207, 78.4, 45.5 and 307; looked
+// for in the codes' registers instead of the stored tile 209, 84, 46.0 and 308; given to the vectors by the softmax
+// warps at the end of each part 210, 79.5, 46.2 and 318, by a function that these call 240, 93, 45.9 and 329.)
+__device__ __forceinline__ bool partly_seen(const Seg& seg, int tok) {
+  return tok < seg.n_all && tok >= seg.lo_all && (tok >= seg.n_least || tok < seg.lo_most);
+}
+// Whether the `tokens` from tok0 on can have such tokens.
+__device__ __forceinline__ bool any_partly(const Seg& seg, int tok0, int tokens) {
+  return (seg.n_least < seg.n_all && tok0 + tokens > seg.n_least) || (seg.lo_all < seg.lo_most && tok0 < seg.lo_most);
+}
+// Bits 15 and 31 for two fp16 that are not finite (the others are anything), and those as zeros.
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return (w & 0x7C007C00u) + 0x04000400u; }
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  return w & ~(((not_finite2(w) & 0x80008000u) >> 15) * 0xFFFFu);
+}
+template <int CG>
+__device__ __forceinline__ void leave_note(uint32_t* at) {
+  if constexpr (CG == 1)
+    *reinterpret_cast<volatile uint32_t*>(at) = 1u;
+  else
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.u32 [a], %1;\n\t"
+        "mapa.shared::cluster.u32 a, %0, 1;\n\tst.shared::cluster.u32 [a], %1;\n\tfence.acq_rel.cluster;\n\t}" ::"r"(
+            smem_u32(at)), "r"(1u)
+        : "memory");
+}
+// By all threads: for the CTA's vectors of each of its parts, NaN in the dims of the NaN codes of the tokens that
+// they see and others do not, where their output or their record is.  Sixteen dims of a vector a thread.
+template <class T>
+__device__ __forceinline__ void add_not_finite(const Shape& sh, const Work& p, int worker, int rank) {
+  const Geom& g = sh.g;
+  const int psh = 31 - __clz(g.P);
+  const float nan = __uint_as_float(0x7FC00000u);
+  Cursor cursor(plan_span<T::kThreads>(sh, p.seqlens, worker, sh.ctas));
+  Seg seg;
+  while (cursor.next(sh, p.seqlens, seg)) {
+    const bool whole = seg.begins && seg.ends;
+    float* rec = p.records + ((size_t)worker * 2 + (seg.begins ? 1 : 0)) * record_floats(sh.vt, T::D) + 2 * sh.vt;
+#pragma unroll 1
+    for (int x = threadIdx.x; x < T::kTiles * 128 * (T::D / 16); x += T::kThreads) {
+      const int row = x / (T::D / 16), d0 = 16 * (x % (T::D / 16));
+      const int at = ((row >> 7) * T::CG + rank) * 128 + (row & 127);
+      if (at >= seg.vecs) continue;
+      const int vec = seg.vec0 + at, j = row_of(sh, vec), head = seg.kvh * sh.G + vec - j * sh.G;
+      const int n = visible_tokens(seg.L, g.R, j, g.MB * g.P), lo = first_seen(n, sh.window);
+      __nv_bfloat16* out = p.out + (((size_t)seg.b * g.R + j) * g.Hq + head) * T::D;
+      if (!QSA_IN_BOUNDS(seg.b < g.B && j < g.R && head < g.Hq, kChkOut) ||
+          !QSA_IN_BOUNDS(worker < sh.ctas && at < sh.vt, kChkRecord))
+        continue;
+      const int to = min(n, (seg.chunk0 + seg.todo) * T::kTok);
+#pragma unroll 1
+      for (int tok = max(lo, seg.chunk0 * T::kTok); tok < to; ++tok) {
+        if (tok >= seg.lo_most && tok < seg.n_least) tok = seg.n_least;       // (all see these)
+        if (tok >= to) break;
+        const int page = __ldg(p.page_table + (size_t)seg.b * g.MB + (tok >> psh));
+        if (page < 0 || page >= g.NP) continue;
+        const uint8_t* codes = p.v_pool + ((((size_t)page * g.Hkv + seg.kvh) << psh) + (tok & (g.P - 1))) * T::D + d0;
+        const uint4 c = *reinterpret_cast<const uint4*>(codes);
+        if ((nan_codes(c.x) | nan_codes(c.y) | nan_codes(c.z) | nan_codes(c.w)) == 0u) continue;
+#pragma unroll 1
+        for (int d = d0; d < d0 + 16; ++d) {
+          if ((codes[d - d0] & 0x7F) != 0x7F) continue;
+          if (whole) out[d] = __float2bfloat16_rn(nan);
+          else rec[((size_t)(d >> 2) * sh.vt + at) * 4 + (d & 3)] = nan;
+        }
+      }
+    }
+  }
+}
 
 // ---- 8-bit pages -----------------------------------------------------------------
 // e4m3 codes with a power of two per 16 tokens (qsa_dense8.cu): codes become fp16 as they are,
@@ -411,7 +487,7 @@ struct Converter8 {
     at_t = ((piece >> 2) * kBlk + sw128(row, 2 * (piece & 3))) ^ (16 * flip);
   }
   __device__ __forceinline__ bool convert(const Seg& seg, int tok0, int chunks, int slot, uint32_t copied,
-                                          bool v) {
+                                          bool v, uint32_t* note) {
     const int x = chunks & 1, use = chunks >> 1;
     uint8_t* tile = tiles + x * kBytes;
     const uint32_t from = part + slot * T::kStage + at_c;
@@ -443,6 +519,20 @@ struct Converter8 {
             make_uint4(e4m3x2_to_f16x2(c.x & 0xFFFFu), e4m3x2_to_f16x2(c.x >> 16), e4m3x2_to_f16x2(c.y & 0xFFFFu),
                        e4m3x2_to_f16x2(c.y >> 16));
       }
+    if (v && any_partly(seg, tok0, T::kTok)) {
+      bool odd = false;
+#pragma unroll 1
+      for (int i = 0; i < 2 * kUnits; ++i) {               // this lane's pieces as stored
+        uint4* at = reinterpret_cast<uint4*>(tile + ((at_t + (i >> 1) * (kStepRows / 8) * 1024) ^ (16 * (i & 1))));
+        const uint4 y = *at;
+        if (partly_seen(seg, tok0 + row + (i >> 1) * kStepRows) &&
+            ((not_finite2(y.x) | not_finite2(y.y) | not_finite2(y.z) | not_finite2(y.w)) & 0x80008000u)) {
+          *at = make_uint4(finite2(y.x), finite2(y.y), finite2(y.z), finite2(y.w));
+          odd = true;
+        }
+      }
+      if (__any_sync(0xffffffffu, odd) && (threadIdx.x & 31) == 0) leave_note<T::CG>(note);
+    }
     fence_proxy_async_smem();
     warp_arrive<T::CG>(&ready[x]);
     return true;
@@ -453,7 +543,7 @@ struct Converter8 {
 template <class T, class... C>
 __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, const Span& span, uint64_t* full,
                                             uint64_t* empty, const volatile uint32_t* copied, bool v,
-                                            C... conv) {
+                                            uint32_t* note, C... conv) {
   int chunks = 0, slot = 0, use = 0;
   Cursor cursor(span);
   Seg seg;
@@ -464,7 +554,7 @@ __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, cons
       const uint32_t bits = copied[slot];
       bool second = v;
       auto one = [&](auto& cv) {
-        const bool done = cv.convert(seg, (seg.chunk0 + c) * T::kTok, chunks, slot, bits, second);
+        const bool done = cv.convert(seg, (seg.chunk0 + c) * T::kTok, chunks, slot, bits, second, note);
         second = true;
         return done;
       };
@@ -529,6 +619,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     mbar_init(partO, 1);
     mbar_init(mdone, 1);
     s_tmem[1] = 0u;   // set when a CTA of the pair gave up
+    s_tmem[2] = 0u;   // set when V has values that are not finite
     mbar_init(qready, T::kSoft * CG);
     for (int x = 0; x < T::kDepth; ++x) {
       mbar_init(&full[x], 1);
@@ -951,17 +1042,17 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     const bool v = warp - T::kSoft >= 4;
     const int k0 = rank * T::kKRows, v0 = rank * T::kVDims;
     if constexpr (T::kDeq == 4)
-      dead = !convert_all<T>(sh, p, span, full, empty, copied, false,
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, false, s_tmem + 2,
                              CK(sh, false, k0, 0, dw, ring, sK, kready, kfree),
                              CV(sh, true, 0, v0, dw, ring, sV, vready, vfree));
     else if constexpr (CG == 1)   // one shape: one copy of the code for both
-      dead = !convert_all<T>(sh, p, span, full, empty, copied, v,
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, v, s_tmem + 2,
                              CK(sh, v, 0, 0, dw, ring, v ? sV : sK, v ? vready : kready, v ? vfree : kfree));
     else if (!v)
-      dead = !convert_all<T>(sh, p, span, full, empty, copied, false,
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, false, s_tmem + 2,
                              CK(sh, false, k0, 0, dw, ring, sK, kready, kfree));
     else
-      dead = !convert_all<T>(sh, p, span, full, empty, copied, true,
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, true, s_tmem + 2,
                              CV(sh, true, 0, v0, dw, ring, sV, vready, vfree));
   } else if (regs_down<T::kMmaRegs>(), warp == T::kMma + 1) {
     // ==== copies =====================================================================
@@ -1094,6 +1185,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     gave_up(mdone, 0);
     __syncthreads();
   }
+  if constexpr (E8)
+    if (!any_dead && *reinterpret_cast<volatile uint32_t*>(s_tmem + 2) != 0u) add_not_finite<T>(sh, p, worker, rank);
   if constexpr (CG == 2) cluster_sync();
   if (warp == 0) {
     if constexpr (CG == 1)
@@ -1147,7 +1240,7 @@ template <int D, int CG, bool E8>
 cudaError_t launch_tile(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
   using T = dense::TT<D, CG, E8>;
   auto* kern = dense::dense_tile_kernel<D, CG, E8>;
-  static_assert(T::kSmem <= 227 * 1024, "shared memory");
+  static_assert(T::kSmem + 1024 <= 227 * 1024, "shared memory (and plan_span's, which takes up 1024 bytes here)");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -312,3 +312,41 @@ def test_sums_of_long_rows(cache, D, R, G):
             tol = tol + (n / 16 + 1) * 2.0**-23 * ref
             for b in (0, B // 2, B - 1):
                 c8.compare(out[b * R + r], lse[b * R + r], [ref, ref_lse, tol, lse_tol])
+
+
+@pytest.mark.parametrize("R,G", [(1, 4), (3, 4), (4, 4), (9, 4), (30, 4), (70, 8), (200, 3)])
+@pytest.mark.parametrize("D,P", [(128, 64), (128, 128), (256, 32), (256, 64)])
+@pytest.mark.parametrize("B,window", [(3, 0), (3, 1), (3, 100), (200, 0), (200, 33)])
+def test_values_that_a_row_does_not_see(B, window, D, P, R, G):
+    """A NaN code of V makes NaN of the rows that see it, in its dim, and of nothing else: not of the rows ahead of it,
+    and not of those that have left it behind.  (200 requests: whole units; 3: divided ones.)"""
+    lo, hi = R + 300, R + (900 if B < 100 else 400)
+    MB = -(-hi // P)
+    NP = B * MB + 2
+    gen, rng = torch.Generator(device=DEV).manual_seed(R), np.random.default_rng(R)
+    w = dict(batch=B, rows_per_req=R, num_q_heads=2 * G, num_kv_heads=2, head_dim=D, index_dim=64, page_size=P,
+             max_blocks=MB, num_pages=NP, sm_scale=D**-0.5)
+    table = rng.permutation(NP)[:B * MB].reshape(B, MB).astype(np.int32)
+    lens = rng.integers(lo, hi + 1, B).astype(np.int32)
+    d = dict(page_table=torch.from_numpy(table).to(DEV), seqlens=torch.from_numpy(lens).to(DEV))
+    for n in ("k", "v"):
+        code = torch.randint(0, 256, (NP, 2, P, D), generator=gen, dtype=torch.uint8, device=DEV)
+        code[(code & 0x7F) > 0x50] &= 0xBF                               # finite and of moderate size
+        d[n + "_pool"] = code
+        d[n + "_exp"] = torch.randint(120, 124, (NP, 2, P // 16), generator=gen, dtype=torch.uint8, device=DEV)
+    q = queries(w)
+    plain = run(w, q, window, d=d)
+    nan = torch.zeros(B * R, 2 * G, D, dtype=torch.bool, device=DEV)
+    for b in sorted({0, 1, 2, B // 2, B - 1}):
+        old = int(lens[b]) - R                             # row j sees tokens up to old + j
+        for tok in [old + R - 1, old, 0, *rng.integers(max(0, old - 200), old + R, 9)]:
+            h, dim = int(rng.integers(2)), int(rng.integers(D))
+            d["v_pool"][int(table[b, tok // P]), h, int(tok) % P, dim] = 0x7F if rng.integers(2) else 0xFF
+            first, end = max(0, int(tok) - old), R if not window else min(R, int(tok) + window - old)
+            if end > first:
+                nan[b * R + first:b * R + end, h * G:(h + 1) * G, dim] = True
+    out, lse = run(w, q, window, d=d)
+    assert torch.equal(lse, plain[1])
+    wrong = out.isnan() != nan
+    assert not wrong.any(), (int(wrong.sum()), wrong.nonzero()[:3].tolist())
+    assert torch.equal(out[~nan], plain[0][~nan])
