@@ -652,6 +652,8 @@ qsa_status_t qsa_load_kv_tokens(const qsa_geom_t *geom, const int32_t *page_tabl
  *
  * qsa_load_kv_tokens_fp8 reads the requests' newest rows back as bf16 (exact):
  * k_out, v_out [rows, Hkv, D]; rows without a slot are left as they were.
+ * Exponent bytes outside 95..191, which the append does not write, are taken as
+ * the nearest of these, as in qsa_dense_attention_fp8.
  *
  * Both return QSA_ERR_INVALID_ARG for null pointers, row strides below the
  * heads' D elements or not a multiple of 8, total_rows outside these, k, v,

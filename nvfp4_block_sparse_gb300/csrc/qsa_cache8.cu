@@ -243,7 +243,7 @@ load8_kernel(const __grid_constant__ Geom g, const __grid_constant__ Cache8Args 
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       if (!to[u]) continue;
-      const float s = pow2(exps[u]);
+      const float s = pow2(min(max(exps[u], kLeastExp), kMostExp));   // (as attention takes them)
       uint32_t o[4];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {

@@ -229,3 +229,19 @@ def test_refused():
     with pytest.raises(qsa.QsaError):
         call(k=torch.empty(6 * 300 + 4, dtype=torch.bfloat16, device=DEV)[4:].as_strided((6, 2, 128), (300, 128, 1)))
     call(k=x[:0, :2], v=x[:0, 2:4], cu=torch.zeros(3, dtype=torch.int32, device=DEV))     # no rows
+
+
+def test_exponents_of_any_bits_are_read_back():
+    """Exponent bytes outside the append's range count as the nearest of it, as they do in attention."""
+    for D, P in ((128, 64), (256, 32)):
+        w = c8.geometry(12, 3, 40, 2, D, P, 100, 130)
+        rng = np.random.default_rng(D)
+        for n in ("k_exp", "v_exp"):
+            w[n][:] = rng.choice(np.array([0, 1, 94, 95, 127, 191, 192, 254, 255], np.uint8), w[n].shape)
+        d = c8.on_gpu(w)
+        out = [torch.full((120, 2, D), 3.5, dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+        qsa.qsa_load_kv_tokens_fp8(geom(w), d["page_table"], d["seqlens"], *(d[n] for n in POOLS), *out)
+        pools = [w["k_pool"], np.clip(w["k_exp"], 95, 191), w["v_pool"], np.clip(w["v_exp"], 95, 191)]
+        want = c8.load(w, pools, 120, *(np.full((120, 2, D), 3.5) for _ in "kv"))
+        for got, x in zip(out, want):
+            np.testing.assert_array_equal(got.double().cpu().numpy(), x)
