@@ -650,6 +650,15 @@ qsa_status_t qsa_load_kv_tokens(const qsa_geom_t *geom, const int32_t *page_tabl
  * only the blocks of stored rows change.  No two rows may have the same slot,
  * and no two requests may append to the same block.
  *
+ * So rows change what the earlier tokens of their block are worth, and taking
+ * rows back by the length alone does not undo that: a rejected draft with large
+ * values leaves its block's exponent, and the accepted tokens rounded to it.  A
+ * caller that may reject rows copies the codes and exponents of the blocks that
+ * the step appends to (of positions L_b - n_b..L_b - 1) before the append, writes
+ * them back behind the step, and appends the accepted rows again: the cache is
+ * then as if those had been appended alone.  (qsa_rollback_gather and _restore
+ * know the NVFP4 planes only.)
+ *
  * qsa_load_kv_tokens_fp8 reads the requests' newest rows back as bf16 (exact):
  * k_out, v_out [rows, Hkv, D]; rows without a slot are left as they were.
  * Exponent bytes outside 95..191, which the append does not write, are taken as
@@ -767,7 +776,8 @@ qsa_status_t qsa_dense_attention_fp8(const qsa_geom_t *geom, const void *q_bf16,
  *              256-byte aligned, zero-filled once by qsa_workspace_init()
  *
  * Row i of a sequence sees its rows max(0, i + 1 - window)..i.  Of the geometry
- * batch, the heads and head_dim matter.  Logits, sums and outputs are fp32,
+ * batch, the heads and head_dim matter.  Logits, sums and outputs are fp32 (of
+ * logits beyond 2^24 in magnitude nothing is left, as in qsa_dense_attention),
  * weights exp(z_t - lse) are rounded to bf16 (8 bits) before the product with V.
  * The weights' sum is as good for a row of 2^24 tokens as for one of 128; the
  * products are added to out 16 tokens at a time, and each addition rounds what is

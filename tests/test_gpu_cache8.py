@@ -245,3 +245,27 @@ def test_exponents_of_any_bits_are_read_back():
         want = c8.load(w, pools, 120, *(np.full((120, 2, D), 3.5) for _ in "kv"))
         for got, x in zip(out, want):
             np.testing.assert_array_equal(got.double().cpu().numpy(), x)
+
+
+def test_rejected_rows_taken_back():
+    """A step's rows raise the scales of the blocks they go to; the bytes of these blocks, kept before the step
+    and written back behind it, leave the cache as if the step had been of the accepted rows alone."""
+    w = c8.geometry(13, 4, 6, 2, 128, 64, 30, 200)
+    d, x = c8.on_gpu(w), rows(24, 2, 128, 4)
+    x[2::6] *= 1000                                     # a draft with large values, later rejected
+    k, v = x[:, :2], x[:, 2:4]
+    args = lambda lens: (d["page_table"], lens, *(d[n] for n in POOLS))  # noqa: E731
+    first, last = d["seqlens"].long() - 6, d["seqlens"].long() - 1
+    blocks = torch.stack([first // 16, last // 16], 1)                             # [B, 2], of six rows at most two
+    page, at = d["page_table"].long().gather(1, blocks // 4), blocks % 4
+    view = lambda n: d[n].view(d[n].shape[0], 2, 4, -1)  # noqa: E731
+    kept = [view(n)[page, :, at].clone() for n in POOLS]
+    qsa.qsa_store_kv_tokens_fp8(geom(w), k, v, *args(d["seqlens"]))
+    for n, x0 in zip(POOLS, kept):
+        view(n)[page, :, at] = x0
+    two = [t.view(4, 6, 2, 128)[:, :2].reshape(8, 2, 128) for t in (k, v)]         # two of the six accepted
+    qsa.qsa_store_kv_tokens_fp8(geom(w, rows_per_req=2), *two, *args(d["seqlens"] - 4))
+    w2 = dict(w, rows_per_req=2, seqlens=w["seqlens"] - 4)
+    ref = c8.store(w2, *(t.float().cpu().numpy() for t in two))
+    for n, r in zip(POOLS, ref):
+        np.testing.assert_array_equal(d[n].cpu().numpy(), r, err_msg=n)
