@@ -860,7 +860,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
         // (8-bit: then for every vector of the warp, to below its largest so far, as it is the warp
         // that waits: 2 x 512 context rows with logits up to a deviation of 2 220 us before, 205
         // now, 199 where nothing moves; 4 x 256 rows of 24 heads on 2 of 256 350 and 316.  By a
-        // power of two, so that a vector's results do not hang on its neighbours'.)
+        // power of two, so that what a vector has summed so far is rescaled exactly; its later weights
+        // are rounded at another base, so that its last bits may hang on when its neighbours' bases move.)
         if constexpr (E8) most = fmaxf(most, top);
         bool moves = top > base + kHeadroom;
         if (__any_sync(0xffffffffu, moves)) {

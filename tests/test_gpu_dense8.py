@@ -350,3 +350,15 @@ def test_values_that_a_row_does_not_see(B, window, D, P, R, G):
     wrong = out.isnan() != nan
     assert not wrong.any(), (int(wrong.sum()), wrong.nonzero()[:3].tolist())
     assert torch.equal(out[~nan], plain[0][~nan])
+
+
+def test_a_neighbour_whose_logits_rise():
+    """One vector whose logits rise far in a late chunk, so that its warp's bases move: its neighbours keep to the
+    same bounds as it."""
+    for R, G in ((9, 4), (70, 8)):
+        w = c8.geometry(15, 2, R, 1, 128, 64, 1500, 1500, G=G)
+        q = queries(w)
+        for page in w["page_table"][:, 1400 // 64]:
+            two = 2.0 ** (int(w["k_exp"][page, 0, 1400 % 64 // 16]) - 127)
+            w["k_pool"][page, 0, 1400 % 64] = c8.codes_of((2 * q[3, 1].float().cpu().numpy() / two).clip(-448, 448))
+        check(w, q=q, alike=True)
