@@ -568,6 +568,7 @@ __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, cons
       ++chunks;
     }
   }
+  if ((threadIdx.x & 31) == 0) note[1] = (uint32_t)chunks;
   return true;
 }
 
@@ -620,6 +621,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     mbar_init(mdone, 1);
     s_tmem[1] = 0u;   // set when a CTA of the pair gave up
     s_tmem[2] = 0u;   // set when V has values that are not finite
+    s_tmem[3] = 0u;   // chunks of the CTA in all, when it is done
     mbar_init(qready, T::kSoft * CG);
     for (int x = 0; x < T::kDepth; ++x) {
       mbar_init(&full[x], 1);
@@ -1185,6 +1187,16 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     if (warp == T::kMma && rank == 0) commit<CG>(elect_one(), mdone);
     gave_up(mdone, 0);
     __syncthreads();
+  }
+  if (!any_dead && warp == 0) {
+    // Nor may an arrival of the MMAs' commits that nobody else waits for be on its way when the block ends: the
+    // softmax warps wait for a part's last products, not for the barriers that are told of them next.  A lane
+    // waits for each.
+    const int chunks = (int)*reinterpret_cast<volatile uint32_t*>(s_tmem + 3), x = lane & 1;
+    const bool o = lane == 4;
+    uint64_t* bar = o ? barO : lane & 2 ? &vfree[x] : &kfree[x];
+    if (lanes_gave_up(bar, o ? chunks - 1 : (chunks - 1 - x) >> 1, o ? kTiles == 1 && chunks > 0 : lane < 4 && x < chunks))
+      atomicExch(p.status, kStatusWaitTimeout);
   }
   if constexpr (E8)
     if (!any_dead && *reinterpret_cast<volatile uint32_t*>(s_tmem + 2) != 0u) add_not_finite<T>(sh, p, worker, rank);

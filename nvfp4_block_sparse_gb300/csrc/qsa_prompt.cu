@@ -606,6 +606,15 @@ prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMa
         if (uses > 0 && gave_up(&full[s], uses - 1)) dead = true;
       }
       if (parts > 0 && gave_up(qfull, parts - 1)) dead = true;
+      // Nor may an arrival of the MMAs' commits that nobody else waits for: the softmax warps wait for a unit's
+      // last products, not for the barriers that are told of them next.  A lane waits for each.
+      if (!dead) {
+        static_assert(T::kStages + 2 <= 32, "lanes");
+        const bool stage = lane < T::kStages, o = lane == T::kStages + 1;
+        uint64_t* bar = stage ? &free_[lane] : o ? barO : qfree;
+        const int last = stage ? (pos - 1 - lane) / T::kStages : o ? pos / 2 - 1 : parts - 1;
+        dead = lanes_gave_up(bar, last, stage ? lane < pos : o ? kTiles == 1 && pos > 0 : lane == T::kStages && parts > 0);
+      }
     } else if (warp == T::kRelay) {
       // ==== relay ====================================================================
       // Q of the first unit as soon as it is there (S waits for it), of the others, which follows the last S of

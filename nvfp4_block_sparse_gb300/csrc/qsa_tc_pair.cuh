@@ -111,6 +111,17 @@ __device__ __forceinline__ bool gave_up(uint64_t* bar, uint32_t parity) {
   return __any_sync(0xffffffffu, !ok);
 }
 
+// The same for a barrier of each lane's own, where it has one.
+__device__ __forceinline__ bool lanes_gave_up(uint64_t* bar, uint32_t parity, bool mine) {
+  bool ok = !mine || sleep_wait(bar, parity & 1);
+  if (!ok) {
+    const unsigned long long t0 = now_ns();
+    while (!(ok = sleep_wait(bar, parity & 1)) && now_ns() - t0 <= kWaitNs) {
+    }
+  }
+  return __any_sync(0xffffffffu, !ok);
+}
+
 // One arrival of the warp at the first CTA's barrier.
 template <int CG>
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
