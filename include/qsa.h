@@ -706,7 +706,9 @@ qsa_status_t qsa_load_kv_tokens_fp8(const qsa_geom_t *geom, const int32_t *cu_ro
  * beyond 2^24 nothing is left of them.  Logits, sums and outputs are fp32;
  * query elements below 2^-26 of their row's largest are rounded to steps of
  * 2^-32 of it; weights exp(z_t - lse) are rounded to 11 bits before the product
- * with V, those below 2^-22 of the row's largest to steps of 2^-32 of it.
+ * with V, those below 2^-22 of the row's largest to steps of 2^-32 of it; the
+ * tensor cores cut each product off at 2^-25 of the largest of what they add, so
+ * that out may lose up to n 2^-24 of sum_t exp(z_t - lse) |V_t| of n tokens.
  * A row that sees no token gets out = 0 and lse = the sink, or -inf.  A row
  * whose queries are not finite, or that sees keys that are not, gets no finite
  * lse or out, and not -inf either; other rows are not touched by it.  What the
@@ -779,9 +781,10 @@ qsa_status_t qsa_dense_attention_fp8(const qsa_geom_t *geom, const void *q_bf16,
  * batch, the heads and head_dim matter.  Logits, sums and outputs are fp32 (of
  * logits beyond 2^24 in magnitude nothing is left, as in qsa_dense_attention),
  * weights exp(z_t - lse) are rounded to bf16 (8 bits) before the product with V.
- * The weights' sum is as good for a row of 2^24 tokens as for one of 128; the
- * products are added to out 16 tokens at a time, and each addition rounds what is
- * there (for n tokens at most n 2^-27 of sum_t exp(z_t - lse) |V_t|).
+ * The weights' sum is as good for a row of 2^24 tokens as for one of 128.  Their
+ * products with V are added by the tensor cores, which cut each off at 2^-25 of the
+ * largest of what they add (measured): out may lose up to n 2^-24 of
+ * sum_t exp(z_t - lse) |V_t| for a row that sees n tokens.
  * What lies outside a sequence's rows is not looked at.  Keys that are not
  * finite make so the rows that see them, and values the rows that see them, in
  * the value's dim; other rows have the bits that they have without them.

@@ -243,7 +243,8 @@ __device__ __forceinline__ void add_not_finite(const Unit& u, int window, const 
 // Walks a worker's units; the copy warp's.  With up to 32 sequences a lane has one, and the
 // units go by their number within their sequence, last (longest) first.  With more sequences
 // the slots of a sequence begin at cu[b] / U + b, which leaves room for all its tiles (and some
-// slots empty) and can be searched; their order then matters little.
+// slots empty) and can be searched: units then go in their sequences' order (39 prompts of 100 tokens and one of
+// 4096, 32 heads on 4 of 128: 106 us with the long one first, 111 with it last, 129 with it in the middle).
 struct Walker {
   const Args& a;
   int U, worker, workers, turn;
