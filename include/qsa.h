@@ -711,7 +711,9 @@ qsa_status_t qsa_load_kv_tokens_fp8(const qsa_geom_t *geom, const int32_t *cu_ro
  * that out may lose up to n 2^-24 of sum_t exp(z_t - lse) |V_t| of n tokens.
  * A row that sees no token gets out = 0 and lse = the sink, or -inf.  A row
  * whose queries are not finite, or that sees keys that are not, gets no finite
- * lse or out, and not -inf either; other rows are not touched by it.  What the
+ * lse or out, and not -inf either; other rows are not touched by it.  Values
+ * that are not (a NaN scale) make NaN of the rows that see them, in the scale's
+ * 16 dims, and of nothing else.  What the
  * cache holds at positions that no row of the request sees is not looked at.
  * The work is divided evenly over the GPU by the requests' actual lengths and
  * joined by log-sum-exp in a fixed order: the same inputs give the same bits.

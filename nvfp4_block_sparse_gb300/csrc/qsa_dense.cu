@@ -98,7 +98,8 @@ struct Cfg {
   static constexpr int DT = D / 16;                  // dim tiles of O
 };
 
-template <class C>
+// kRows: more than one row of each request, so that not all vectors see the same tokens.
+template <class C, bool kRows>
 __global__ void __launch_bounds__(C::kThreads, 1)
 dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work p) {
   constexpr int D = C::D, NT = C::NT, W = C::W, S = C::S, TOK = C::TOK;
@@ -155,6 +156,7 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
     const int vec0 = seg.vec0, vecs = seg.vecs, cap = g.MB * g.P;
     const int n_all = seg.n_all, n_least = seg.n_least, lo_all = seg.lo_all, lo_most = seg.lo_most;
     const int mine = todo > warp ? (todo - warp + W - 1) / W : 0;   // this warp's chunks
+    const bool partly = kRows && (n_least < n_all || lo_all < lo_most);   // not all vectors see the same
 
     // ---- the warp's query vectors: on their way while the pages are looked up ----------
     constexpr int kPer = (kCols + W - 1) / W, E = D / 32;
@@ -290,6 +292,48 @@ dense_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Wo
                 asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(a + 8 * i), "r"(0u) : "memory");
             }
           __syncwarp();
+        }
+        if (partly && edge) {
+          // Tokens that some of the vectors see and others do not: a NaN among the scales of V goes to the outputs
+          // of those that see it, and out of V, where it would reach all (0 x NaN).  (As in qsa_dense8.cu.)
+          const uint32_t sv = st + 2 * C::kK + C::kSc;
+          // (between lo_most and n_least all see them)
+          auto scales = [&](auto&& each) {
+#pragma unroll 1
+            for (int side = 0; side < 2; ++side) {
+              const int from = max((side ? n_least : lo_all) - tok0, 0), to = min((side ? n_all : lo_most) - tok0, TOK);
+#pragma unroll 1
+              for (int x = from * C::kSf + lane; x < to * C::kSf; x += 32) each(sv + x);
+            }
+          };
+          bool odd = false;
+          scales([&](uint32_t at) { odd |= (lds8(at) & 0x7Fu) == 0x7Fu; });
+          if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+            for (int r = 0; r < TOK; ++r) {
+              const int tok = tok0 + r;
+              if (tok >= lo_most && tok < n_least) continue;
+#pragma unroll
+              for (int h = 0; h < D / 128; ++h) {          // 16 dims: output tiles 8 h.. of rows gid and gid + 8
+                if ((lds8(sv + r * C::kSf + gid * (D / 128) + h) & 0x7Fu) != 0x7Fu) continue;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int c = 8 * t + 2 * tig + e;
+                    if (tok >= s_n[c] || tok < s_lo[c]) continue;
+#pragma unroll
+                    for (int i = 8 * h; i < 8 * h + 8; ++i)
+                      o[i][t][e] = o[i][t][2 + e] = __uint_as_float(0x7FC00000u);
+                  }
+              }
+            }
+            __syncwarp();
+            scales([&](uint32_t at) {
+              if ((lds8(at) & 0x7Fu) == 0x7Fu) asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "h"((uint16_t)0) : "memory");
+            });
+            __syncwarp();
+          }
         }
         // S^T
         float z[MT][NT][4];
@@ -614,7 +658,9 @@ dense::Shape decode_shape(const Geom& g, int window) {
 
 template <class C>
 cudaError_t launch_decode(const dense::Shape& s, const dense::Work& w, cudaStream_t stream) {
-  auto* kern = dense::dense_decode_kernel<C>;
+  // (a single row has a kernel without what vectors that see different tokens need: batched decode 25.2 us, and
+  // 26.1 with it)
+  auto* kern = s.g.R > 1 ? dense::dense_decode_kernel<C, true> : dense::dense_decode_kernel<C, false>;
   static_assert(C::kSmem <= 227 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;

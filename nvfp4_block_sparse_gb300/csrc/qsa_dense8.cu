@@ -67,7 +67,8 @@ __device__ __forceinline__ uint32_t load_exps(const uint8_t* p) {
   return __vminu4(__vmaxu4(x, 0x5F5F5F5Fu), 0xBFBFBFBFu);
 }
 
-template <class C>
+// kRows: as in the NVFP4 kernel.
+template <class C, bool kRows>
 __global__ void __launch_bounds__(C::kThreads, 1)
 dense8_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work p) {
   constexpr int D = C::D, NT = C::NT, W = C::W, S = C::S, TOK = C::TOK;
@@ -119,7 +120,7 @@ dense8_decode_kernel(const __grid_constant__ Shape sh, const __grid_constant__ W
     const int vec0 = seg.vec0, vecs = seg.vecs, cap = g.MB * g.P;
     const int n_all = seg.n_all, n_least = seg.n_least, lo_all = seg.lo_all, lo_most = seg.lo_most;
     const int mine = todo > warp ? (todo - warp + W - 1) / W : 0;   // this warp's chunks
-    const bool partly = n_least < n_all || lo_all < lo_most;        // not all vectors see the same
+    const bool partly = kRows && (n_least < n_all || lo_all < lo_most);   // not all vectors see the same
 
     // ---- the warp's query vectors: on their way while the pages are looked up ----------
     constexpr int kPer = (kCols + W - 1) / W, E = D / 32;
@@ -462,7 +463,7 @@ using C256b = Cfg8<256, 2, 8, 3, 16>;
 
 template <class C>
 cudaError_t launch_decode8(const Shape& s, const Work& w, cudaStream_t stream) {
-  auto* kern = dense8_decode_kernel<C>;
+  auto* kern = s.g.R > 1 ? dense8_decode_kernel<C, true> : dense8_decode_kernel<C, false>;
   static_assert(C::kSmem <= 227 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;

@@ -46,6 +46,8 @@
 //             group per tile
 //   copy      one warp: codes and scales of the pages by bulk copies some chunks ahead
 //   dequant   e2m1 x e4m3 exact in fp16 into double-buffered K and V tiles (128-byte swizzle)
+//   inspector one warp (NVFP4 pages): takes values that are not finite out of stages with tokens that some vectors
+//             see and others do not (see "Values that are not finite")
 //   MMA       one warp (of the pair's first CTA) issues every MMA in order.  With two tiles
 //             they take turns: O_0, S_0 of the next chunk, O_1, S_1, so that one tile's
 //             softmax runs under the other's products; with one, S has two buffers
@@ -62,7 +64,7 @@
 // commits to both CTAs':
 //   qready        Q tiles written; O, S of the part before read    (softmax warps)
 //   full[i]       stage i of codes and scales there                (bulk copies)
-//   empty[i]      stage i read                                     (the converting warps)
+//   empty[i]      stage i read                                     (the converting warps, the inspector)
 //   kready/vready[x]  K / V tile x written                         (its four converting warps)
 //   kfree/vfree[x]    MMAs that read tile x complete               (commit)
 //   barS[y]       S buffer y complete -- and, with two tiles, every MMA before it,
@@ -88,6 +90,9 @@ using namespace tc;
 [[maybe_unused]] constexpr int kChkChunk = 0xA01;   // copy: token offset or place in the ring out of range
 [[maybe_unused]] constexpr int kChkOut = 0xA02;     // output row out of range
 [[maybe_unused]] constexpr int kChkRecord = 0xA03;  // record's slot out of range
+
+// In `copied`: the chunk has tokens that some vectors see and others do not (see "Values that are not finite").
+constexpr uint32_t kMarked = 0x80000000u;
 
 // E8: the 8-bit cache's pages instead of NVFP4's (see "8-bit pages" below).
 template <int D_, int CG_, bool E8_>
@@ -144,7 +149,7 @@ struct TT {
   static constexpr int kExpSlots = E8 ? 8 : 0, kExpFloats = 24;
   static_assert(!E8 || kExpSlots >= kDepth + 2, "exponents' ring");
   static constexpr int kSmem = 1024 + kTiles * kQBytes + 2 * kKBytes + 2 * kVBytes + kRing +
-                               kBars * 8 + 16 + (E8 ? 16 : kDepth * 4) + kExpSlots * kExpFloats * 4;
+                               kBars * 8 + 16 + (E8 ? 16 : kDepth * 4 + 4) + kExpSlots * kExpFloats * 4;
   static_assert(kVecs <= 512 && (!E8 || kDepth <= 4), "a unit's vectors; what is copied of each stage");
 };
 
@@ -226,10 +231,12 @@ __device__ __forceinline__ bool copy_all(const Shape& sh, const Work& p, const S
                         kChkChunk);
       const uint32_t which = __ballot_sync(0xffffffffu, there);
       const uint32_t sum = __reduce_add_sync(0xffffffffu, there ? bytes : 0u);
+      [[maybe_unused]] const uint32_t mark = (seg.n_least < seg.n_all && tok0 + T::kTok > seg.n_least) ||
+                                    (seg.lo_all < seg.lo_most && tok0 < seg.lo_most) ? kMarked : 0u;
       if (use > 0 && gave_up(&empty[slot], use - 1)) { ok = false; break; }
       if constexpr (!T::E8) {
         if (lane == 0) {
-          copied[slot] = which;
+          copied[slot] = which | mark;
           mbar_arrive_expect_tx(&full[slot], sum);
         }
         __syncwarp();
@@ -367,13 +374,19 @@ struct Converter {
 
 // ---- values that are not finite ----------------------------------------------------
 // A weight of 0 times a V that is not finite is NaN: of a token that some of the unit's vectors see and others
-// do not, such a value would reach the others.  A converter leaves these values out of the tile and leaves a
-// note (in a pair, whose converters have half of the dims each, in both CTAs), ahead of the arrival that lets
-// the MMAs begin.  Where there is one, the CTA goes through all its parts once more when everything is done, and
-// vectors get what was left out from the pages themselves.  (Measured, 2 x 512 context rows, 24 vectors of 128,
-// windowed verify, 4 x 256 rows of 256: without any of it 203.5, 76.8, 45.4 and 313 us; so 207, 78.4, 45.5 and 307; looked
-// for in the codes' registers instead of the stored tile 209, 84, 46.0 and 308; given to the vectors by the softmax
-// warps at the end of each part 210, 79.5, 46.2 and 318, by a function that these call 240, 93, 45.9 and 329.)
+// do not, such a value would reach the others.  These values are left out of the tile, and a note is left;
+// where there is one, the CTA goes through all its parts once more when everything is done, and vectors get
+// what was left out from the pages themselves.  (Given to the vectors by the softmax warps at the end of each part,
+// it cost them registers: 2 x 512 context rows over 8-bit pages 207 -> 210 us, by a function that these call 240.)
+// 8-bit pages: the converters look at the tiles that they have stored, and leave the note (in a pair, whose
+// converters have half of the dims each, in both CTAs) ahead of the arrival that lets the MMAs begin.  (Measured,
+// 2 x 512 context rows, 24 vectors of 128, windowed verify, 4 x 256 rows of 256: without any of it 203.5, 76.8, 45.4 and
+// 313 us; so 207, 78.4, 45.5 and 307; looked for in the codes' registers instead 209, 84, 46.0 and 308; by the
+// inspector 208, 82, 46.5 and 306.)
+// NVFP4 pages: the inspector, a warp of its own, puts zeros for NaN scales in the stages that the copy warp has marked
+// as having such tokens, and the converters wait for it there.  (Two context chunks, windowed verify rows:
+// without 636 and 40.7 us; so 642 and 41.4; looked for by the converters, which have 72 registers, 663 to 680 and
+// 42 to 43.)
 __device__ __forceinline__ bool partly_seen(const Seg& seg, int tok) {
   return tok < seg.n_all && tok >= seg.lo_all && (tok >= seg.n_least || tok < seg.lo_most);
 }
@@ -397,8 +410,72 @@ __device__ __forceinline__ void leave_note(uint32_t* at) {
             smem_u32(at)), "r"(1u)
         : "memory");
 }
-// By all threads: for the CTA's vectors of each of its parts, NaN in the dims of the NaN codes of the tokens that
-// they see and others do not, where their output or their record is.  Sixteen dims of a vector a thread.
+// A converter's bounded wait for the inspector to come past marked chunk n: true when it gave up.
+__device__ __forceinline__ bool not_inspected(const uint32_t* past, uint32_t n) {
+  auto there = [&]() {
+    uint32_t x;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(x) : "r"(smem_u32(past)) : "memory");
+    return x > n;
+  };
+  bool ok = there();
+  if (!ok) {
+    const unsigned long long t0 = now_ns();
+    while (!(ok = there()) && now_ns() - t0 <= kWaitNs) {
+    }
+  }
+  return __any_sync(0xffffffffu, !ok);
+}
+template <class T>
+__device__ __forceinline__ bool inspect_all(const Shape& sh, const Work& p, const Span& span, uint8_t* ring,
+                                            uint64_t* full, uint64_t* empty, const volatile uint32_t* copied,
+                                            uint32_t* past, uint32_t* note) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kWords = T::D / 64;                      // scales of a token
+  int slot = 0, use = 0;
+  uint32_t chunks = 0;
+  Cursor cursor(span);
+  Seg seg;
+  while (cursor.next(sh, p.seqlens, seg)) {
+#pragma unroll 1
+    for (int c = 0; c < seg.todo; ++c, ++chunks) {
+      if (gave_up(&full[slot], use)) return false;
+      if (copied[slot] & kMarked) {
+        const int tok0 = (seg.chunk0 + c) * T::kTok;
+        uint32_t* v = reinterpret_cast<uint32_t*>(ring + slot * T::kStage + T::kKPart + T::kVCodes);
+        uint32_t odd = 0u;
+        // (between lo_most and n_least all see them)
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+          const int from = max((side ? seg.n_least : seg.lo_all) - tok0, 0);
+          const int to = min((side ? seg.n_all : seg.lo_most) - tok0, T::kTok);
+#pragma unroll 2
+          for (int x = from * kWords + lane; x < to * kWords; x += 32) {
+            const uint32_t w = v[x], bad = nan_codes(w);
+            if (bad) v[x] = without_nan(w);
+            odd |= bad;
+          }
+        }
+        if (__any_sync(0xffffffffu, odd != 0u)) {
+          if (lane == 0) *note = 1u;
+          fence_proxy_async_smem();                      // (ahead of the stage's next copies)
+        }
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(past)), "r"(chunks + 1u) : "memory");
+      }
+      __syncwarp();
+      if (lane == 0) ws_arrive(&empty[slot]);
+      if (++slot == T::kDepth) {
+        slot = 0;
+        ++use;
+      }
+    }
+  }
+  return true;
+}
+
+// By all threads: for the CTA's vectors of each of its parts, NaN in the dims of the NaN codes (or scales) of the
+// tokens that they see and others do not, where their output or their record is.  Sixteen dims of a vector a thread.
 template <class T>
 __device__ __forceinline__ void add_not_finite(const Shape& sh, const Work& p, int worker, int rank) {
   const Geom& g = sh.g;
@@ -427,12 +504,15 @@ __device__ __forceinline__ void add_not_finite(const Shape& sh, const Work& p, i
         if (tok >= to) break;
         const int page = __ldg(p.page_table + (size_t)seg.b * g.MB + (tok >> psh));
         if (page < 0 || page >= g.NP) continue;
-        const uint8_t* codes = p.v_pool + ((((size_t)page * g.Hkv + seg.kvh) << psh) + (tok & (g.P - 1))) * T::D + d0;
-        const uint4 c = *reinterpret_cast<const uint4*>(codes);
-        if ((nan_codes(c.x) | nan_codes(c.y) | nan_codes(c.z) | nan_codes(c.w)) == 0u) continue;
+        const size_t at_tok = (((size_t)page * g.Hkv + seg.kvh) << psh) + (tok & (g.P - 1));
+        const uint8_t* codes = T::E8 ? p.v_pool + at_tok * T::D + d0 : p.v_sf + at_tok * (T::D / 16) + d0 / 16;
+        if constexpr (T::E8) {
+          const uint4 c = *reinterpret_cast<const uint4*>(codes);
+          if ((nan_codes(c.x) | nan_codes(c.y) | nan_codes(c.z) | nan_codes(c.w)) == 0u) continue;
+        }
 #pragma unroll 1
         for (int d = d0; d < d0 + 16; ++d) {
-          if ((codes[d - d0] & 0x7F) != 0x7F) continue;
+          if ((codes[T::E8 ? d - d0 : 0] & 0x7F) != 0x7F) continue;
           if (whole) out[d] = __float2bfloat16_rn(nan);
           else rec[((size_t)(d >> 2) * sh.vt + at) * 4 + (d & 3)] = nan;
         }
@@ -543,7 +623,7 @@ struct Converter8 {
 template <class T, class... C>
 __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, const Span& span, uint64_t* full,
                                             uint64_t* empty, const volatile uint32_t* copied, bool v,
-                                            uint32_t* note, C... conv) {
+                                            uint32_t* words, const uint32_t* past, C... conv) {
   int chunks = 0, slot = 0, use = 0;
   Cursor cursor(span);
   Seg seg;
@@ -552,9 +632,11 @@ __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, cons
     for (int c = 0; c < seg.todo; ++c) {
       if (gave_up(&full[slot], use)) return false;
       const uint32_t bits = copied[slot];
+      if constexpr (!T::E8)
+        if ((v || sizeof...(C) == 2) && (bits & kMarked) && not_inspected(past, chunks)) return false;
       bool second = v;
       auto one = [&](auto& cv) {
-        const bool done = cv.convert(seg, (seg.chunk0 + c) * T::kTok, chunks, slot, bits, second, note);
+        const bool done = cv.convert(seg, (seg.chunk0 + c) * T::kTok, chunks, slot, bits, second, words);
         second = true;
         return done;
       };
@@ -568,7 +650,7 @@ __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, cons
       ++chunks;
     }
   }
-  if ((threadIdx.x & 31) == 0) note[1] = (uint32_t)chunks;
+  if ((threadIdx.x & 31) == 0) words[1] = (uint32_t)chunks;
   return true;
 }
 
@@ -605,6 +687,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + T::kBars);
   uint32_t* copied = s_tmem + 4;                               // [kDepth]
   float* exps = reinterpret_cast<float*>(copied + 4);          // [kExpSlots][2^ke, ve, 2^-ve]
+  // NVFP4: the marked chunk that the inspector has last come past, from 1 on
+  [[maybe_unused]] uint32_t* past = copied + T::kDepth;
 
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -622,10 +706,11 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     s_tmem[1] = 0u;   // set when a CTA of the pair gave up
     s_tmem[2] = 0u;   // set when V has values that are not finite
     s_tmem[3] = 0u;   // chunks of the CTA in all, when it is done
+    if constexpr (!E8) *past = 0u;
     mbar_init(qready, T::kSoft * CG);
     for (int x = 0; x < T::kDepth; ++x) {
       mbar_init(&full[x], 1);
-      mbar_init(&empty[x], T::kDeq);
+      mbar_init(&empty[x], T::kDeq + (E8 ? 0 : 1));
     }
     fence_mbar_init();
   }
@@ -1045,21 +1130,24 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     const bool v = warp - T::kSoft >= 4;
     const int k0 = rank * T::kKRows, v0 = rank * T::kVDims;
     if constexpr (T::kDeq == 4)
-      dead = !convert_all<T>(sh, p, span, full, empty, copied, false, s_tmem + 2,
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, false, s_tmem + 2, past,
                              CK(sh, false, k0, 0, dw, ring, sK, kready, kfree),
                              CV(sh, true, 0, v0, dw, ring, sV, vready, vfree));
     else if constexpr (CG == 1)   // one shape: one copy of the code for both
-      dead = !convert_all<T>(sh, p, span, full, empty, copied, v, s_tmem + 2,
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, v, s_tmem + 2, past,
                              CK(sh, v, 0, 0, dw, ring, v ? sV : sK, v ? vready : kready, v ? vfree : kfree));
     else if (!v)
-      dead = !convert_all<T>(sh, p, span, full, empty, copied, false, s_tmem + 2,
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, false, s_tmem + 2, past,
                              CK(sh, false, k0, 0, dw, ring, sK, kready, kfree));
     else
-      dead = !convert_all<T>(sh, p, span, full, empty, copied, true, s_tmem + 2,
+      dead = !convert_all<T>(sh, p, span, full, empty, copied, true, s_tmem + 2, past,
                              CV(sh, true, 0, v0, dw, ring, sV, vready, vfree));
   } else if (regs_down<T::kMmaRegs>(), warp == T::kMma + 1) {
     // ==== copies =====================================================================
     dead = !copy_all<T>(sh, p, span, rank, ring, full, empty, copied, exps);
+  } else if (warp == T::kMma + 2) {
+    // ==== inspection =================================================================
+    if constexpr (!E8) dead = !inspect_all<T>(sh, p, span, ring, full, empty, copied, past, s_tmem + 2);
   } else if (warp == T::kMma && rank == 0) {
     // ==== MMA issue ==================================================================
     const uint32_t one = elect_one();
@@ -1198,8 +1286,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     if (lanes_gave_up(bar, o ? chunks - 1 : (chunks - 1 - x) >> 1, o ? kTiles == 1 && chunks > 0 : lane < 4 && x < chunks))
       atomicExch(p.status, kStatusWaitTimeout);
   }
-  if constexpr (E8)
-    if (!any_dead && *reinterpret_cast<volatile uint32_t*>(s_tmem + 2) != 0u) add_not_finite<T>(sh, p, worker, rank);
+  if (!any_dead && *reinterpret_cast<volatile uint32_t*>(s_tmem + 2) != 0u) add_not_finite<T>(sh, p, worker, rank);
   if constexpr (CG == 2) cluster_sync();
   if (warp == 0) {
     if constexpr (CG == 1)

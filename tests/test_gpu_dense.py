@@ -246,3 +246,49 @@ def test_a_step_of_the_whole_run(qsa):
     torch.cuda.synchronize()
     assert (sparse.out.float() - step.out.float()).abs().max() <= 2.0**-7 * step.out.float().abs().max()
     assert (sparse.lse - step.lse).abs().max() <= 2e-4
+
+
+@pytest.mark.parametrize("R,G", [(1, 4), (3, 4), (4, 4), (9, 4), (30, 4), (70, 8), (200, 3)])
+@pytest.mark.parametrize("D,P", [(128, 64), (128, 128), (256, 32), (256, 64)])
+@pytest.mark.parametrize("B,window", [(3, 0), (3, 100), (200, 0), (200, 33)])
+def test_values_that_a_row_does_not_see(qsa, B, window, D, P, R, G):
+    """A NaN scale of V makes NaN of the rows that see it, in its 16 dims, and of nothing else: not of the rows ahead
+    of it, and not of those that have left it behind.  (200 requests: whole units; 3: divided ones.)"""
+    dev = "cuda"
+    lo, hi = R + 300, R + (900 if B < 100 else 400)
+    MB = -(-hi // P)
+    NP = B * MB + 2
+    gen, rng = torch.Generator(device=dev).manual_seed(R), np.random.default_rng(R)
+    g = qsa.make_geom(batch=B, rows_per_req=R, num_q_heads=2 * G, num_kv_heads=2, head_dim=D, index_dim=64,
+                      page_size=P, max_blocks=MB, num_pages=NP)
+    table = rng.permutation(NP)[:B * MB].reshape(B, MB).astype(np.int32)
+    lens = rng.integers(lo, hi + 1, B).astype(np.int32)
+    pools = []
+    for _ in "kv":
+        pools += [torch.randint(0, 256, (NP, 2, P, D // 2), generator=gen, dtype=torch.uint8, device=dev),
+                  torch.randint(0x28, 0x38, (NP, 2, P, D // 16), generator=gen, dtype=torch.uint8, device=dev)]
+    q = torch.randn(B * R, 2 * G, D, generator=gen, device=dev).to(torch.bfloat16)
+    ws = torch.empty(qsa.qsa_dense_attention_workspace_bytes(g), dtype=torch.uint8, device=dev)
+    qsa.qsa_workspace_init(ws)
+
+    def call():
+        out, lse = torch.empty_like(q), torch.empty(B * R, 2 * G, device=dev)
+        qsa.qsa_dense_attention(g, q, *pools, 1.0, 1.0, D**-0.5, torch.from_numpy(table).to(dev),
+                                torch.from_numpy(lens).to(dev), out, lse, ws, window=window)
+        assert qsa.qsa_workspace_status(ws) == 0
+        return out, lse
+    plain = call()
+    nan = torch.zeros(B * R, 2 * G, D, dtype=torch.bool, device=dev)
+    for b in sorted({0, 1, 2, B // 2, B - 1}):
+        old = int(lens[b]) - R                             # row j sees tokens up to old + j
+        for tok in [old + R - 1, old, 0, *rng.integers(max(0, old - 200), old + R, 9)]:
+            h, group = int(rng.integers(2)), int(rng.integers(D // 16))
+            pools[3][int(table[b, tok // P]), h, int(tok) % P, group] = 0x7F if rng.integers(2) else 0xFF
+            first, end = max(0, int(tok) - old), R if not window else min(R, int(tok) + window - old)
+            if end > first:
+                nan[b * R + first:b * R + end, h * G:(h + 1) * G, 16 * group:16 * group + 16] = True
+    out, lse = call()
+    assert torch.equal(lse, plain[1])
+    wrong = out.isnan() != nan
+    assert not wrong.any(), (int(wrong.sum()), wrong.nonzero()[:3].tolist())
+    assert torch.equal(out[~nan], plain[0][~nan])
