@@ -46,8 +46,7 @@
 //             group per tile
 //   copy      one warp: codes and scales of the pages by bulk copies some chunks ahead
 //   dequant   e2m1 x e4m3 exact in fp16 into double-buffered K and V tiles (128-byte swizzle)
-//   inspector one warp (NVFP4 pages): takes values that are not finite out of stages with tokens that some vectors
-//             see and others do not (see "Values that are not finite")
+//   inspector one warp (NVFP4 pages, two tiles): see "Values that are not finite"
 //   MMA       one warp (of the pair's first CTA) issues every MMA in order.  With two tiles
 //             they take turns: O_0, S_0 of the next chunk, O_1, S_1, so that one tile's
 //             softmax runs under the other's products; with one, S has two buffers
@@ -99,6 +98,7 @@ template <int D_, int CG_, bool E8_>
 struct TT {
   static constexpr int D = D_, CG = CG_;                 // CG: CTAs per MMA
   static constexpr bool E8 = E8_;
+  static constexpr bool kInspect = !E8 && D == 128 && CG == 2;   // (an inspector: see "Values that are not finite")
   static constexpr int kTiles = D == 128 && CG == 2 ? 2 : 1;   // tiles of a CTA
   static constexpr int kTok = D == 256 ? 64 : 128;       // tokens per chunk
   static constexpr int kHalves = kTok / 64;              // P is written 64 tokens at a time
@@ -149,7 +149,7 @@ struct TT {
   static constexpr int kExpSlots = E8 ? 8 : 0, kExpFloats = 24;
   static_assert(!E8 || kExpSlots >= kDepth + 2, "exponents' ring");
   static constexpr int kSmem = 1024 + kTiles * kQBytes + 2 * kKBytes + 2 * kVBytes + kRing +
-                               kBars * 8 + 16 + (E8 ? 16 : kDepth * 4 + 4) + kExpSlots * kExpFloats * 4;
+                               kBars * 8 + 16 + (E8 ? 16 : kDepth * 20 + 4) + kExpSlots * kExpFloats * 4;
   static_assert(kVecs <= 512 && (!E8 || kDepth <= 4), "a unit's vectors; what is copied of each stage");
 };
 
@@ -159,6 +159,44 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool o
                : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// ---- values that are not finite ----------------------------------------------------
+// A weight of 0 times a V that is not finite is NaN: of a token that some of the unit's vectors see and others
+// do not, such a value would reach the others.  The converters leave these values out of the tile and leave a note
+// (in a pair, whose converters have half of the dims each, in both CTAs) ahead of the arrival that lets the MMAs
+// begin.  Where there is one, the CTA goes through all its parts once more when everything is done, and vectors
+// get what was left out from the pages themselves.  (Given to the vectors by the softmax warps at the end of each part
+// it cost them registers: 2 x 512 context rows over 8-bit pages 207 -> 210 us, by a function that these call 240.)
+// 8-bit pages: looked for in the tiles as stored.  (2 x 512 context rows, 24 vectors of 128, windowed verify, 4 x 256
+// rows of 256: without any of it 203.5, 76.8, 45.4 and 313 us; so 207, 78.4, 45.5 and 307; in the codes' registers
+// 209, 84, 46.0 and 308.)
+// NVFP4 pages: in the scales of the stages that the copy warp marks as having such tokens, which the same lane
+// reads next.  Where four warps convert both K and V they have no registers left for it (two context chunks 656 us),
+// and a warp of its own, the inspector, does it, which they wait for at marked stages (646; 637 without; with an
+// inspector for all, 16 requests x 4 rows of 32 heads on 4 of 128 86 us instead of 79, windowed verify 41.8 for 41.5).
+__device__ __forceinline__ bool partly_seen(const Seg& seg, int tok) {
+  return tok < seg.n_all && tok >= seg.lo_all && (tok >= seg.n_least || tok < seg.lo_most);
+}
+// Whether the `tokens` from tok0 on can have such tokens.
+__device__ __forceinline__ bool any_partly(const Seg& seg, int tok0, int tokens) {
+  return (seg.n_least < seg.n_all && tok0 + tokens > seg.n_least) || (seg.lo_all < seg.lo_most && tok0 < seg.lo_most);
+}
+// Bits 15 and 31 for two fp16 that are not finite (the others are anything), and those as zeros.
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return (w & 0x7C007C00u) + 0x04000400u; }
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  return w & ~(((not_finite2(w) & 0x80008000u) >> 15) * 0xFFFFu);
+}
+template <int CG>
+__device__ __forceinline__ void leave_note(uint32_t* at) {
+  if constexpr (CG == 1)
+    *reinterpret_cast<volatile uint32_t*>(at) = 1u;
+  else
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.u32 [a], %1;\n\t"
+        "mapa.shared::cluster.u32 a, %0, 1;\n\tst.shared::cluster.u32 [a], %1;\n\tfence.acq_rel.cluster;\n\t}" ::"r"(
+            smem_u32(at)), "r"(1u)
+        : "memory");
+}
 
 // ---- copies ----------------------------------------------------------------------
 // The copy warp brings every chunk's codes and scales into the ring, kDepth chunks ahead
@@ -170,7 +208,7 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 template <class T>
 __device__ __forceinline__ bool copy_all(const Shape& sh, const Work& p, const Span& span, int rank,
                                          uint8_t* ring, uint64_t* full, uint64_t* empty,
-                                         volatile uint32_t* copied, float* exps) {
+                                         volatile uint32_t* copied, float* exps, int* sides) {
   const int lane = threadIdx.x & 31;
   const int psh = 31 - __clz(sh.g.P);
   const bool scales = lane & 1, v = lane & 2;         // (8-bit: no copies of scales)
@@ -231,12 +269,18 @@ __device__ __forceinline__ bool copy_all(const Shape& sh, const Work& p, const S
                         kChkChunk);
       const uint32_t which = __ballot_sync(0xffffffffu, there);
       const uint32_t sum = __reduce_add_sync(0xffffffffu, there ? bytes : 0u);
-      [[maybe_unused]] const uint32_t mark = (seg.n_least < seg.n_all && tok0 + T::kTok > seg.n_least) ||
-                                    (seg.lo_all < seg.lo_most && tok0 < seg.lo_most) ? kMarked : 0u;
       if (use > 0 && gave_up(&empty[slot], use - 1)) { ok = false; break; }
       if constexpr (!T::E8) {
         if (lane == 0) {
-          copied[slot] = which | mark;
+          const bool marked = any_partly(seg, tok0, T::kTok);
+          if (marked) {
+            int* at_slot = sides + 4 * slot;
+            at_slot[0] = seg.lo_all - tok0;
+            at_slot[1] = seg.lo_most - tok0;
+            at_slot[2] = seg.n_least - tok0;
+            at_slot[3] = seg.n_all - tok0;
+          }
+          copied[slot] = which | (marked ? kMarked : 0u);
           mbar_arrive_expect_tx(&full[slot], sum);
         }
         __syncwarp();
@@ -332,7 +376,7 @@ struct Converter {
   // Chunk number `chunks` of the CTA, from token tok0, out of stage `slot` into its tile; false
   // when the wait for the tile gave up.
   __device__ __forceinline__ bool convert(const Seg& seg, int tok0, int chunks, int slot, uint32_t copied,
-                                          bool v, uint32_t*) {
+                                          bool v, uint32_t* note) {
     const int lane = threadIdx.x & 31;
     const int x = chunks & 1, use = chunks >> 1;
     uint8_t* tile = tiles + x * kBytes;
@@ -343,6 +387,26 @@ struct Converter {
     const int first = seg.lo_all - tok0 - row0;
     const uint32_t seen = (uint32_t)max(seg.n_all - seg.lo_all, 0);
     const uint32_t bits = copied >> (v ? 2 : 0);
+    if (!T::kInspect && v && (copied & kMarked)) {
+      // NaN among the scales of tokens that some vectors see and others do not: zeros in the stage, where
+      // this lane alone reads them
+      const int* at_slot = reinterpret_cast<const int*>(note + 2 + T::kDepth) + 4 * slot;   // (behind `copied`)
+      bool odd = false;
+#pragma unroll 1
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = ((threadIdx.x >> 5) & 3) + 4 * i;
+        const int r = kPieces >= 4 ? 8 * (u % (kRows / 8)) + (lane >> 2) : 16 * u + (lane >> 1);
+        const int up = kPieces >= 4 ? 4 * (u / (kRows / 8)) : 0;      // (pieces on from the first step's)
+        const uint32_t at = from + at_s[0] + (r - row[0]) * (D / 16) + 2 * up;
+        uint32_t sf;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sf) : "r"(at));
+        if (nan_codes(sf) != 0u && ((r >= at_slot[0] && r < at_slot[1]) || (r >= at_slot[2] && r < at_slot[3]))) {
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)without_nan(sf)) : "memory");
+          odd = true;
+        }
+      }
+      if (__any_sync(0xffffffffu, odd) && lane == 0) leave_note<T::CG>(note);
+    }
     uint4 codes[kUnits];       // every step's, so that their latencies overlap
     uint32_t sfs[kUnits];
 #pragma unroll
@@ -372,44 +436,6 @@ struct Converter {
   }
 };
 
-// ---- values that are not finite ----------------------------------------------------
-// A weight of 0 times a V that is not finite is NaN: of a token that some of the unit's vectors see and others
-// do not, such a value would reach the others.  These values are left out of the tile, and a note is left;
-// where there is one, the CTA goes through all its parts once more when everything is done, and vectors get
-// what was left out from the pages themselves.  (Given to the vectors by the softmax warps at the end of each part,
-// it cost them registers: 2 x 512 context rows over 8-bit pages 207 -> 210 us, by a function that these call 240.)
-// 8-bit pages: the converters look at the tiles that they have stored, and leave the note (in a pair, whose
-// converters have half of the dims each, in both CTAs) ahead of the arrival that lets the MMAs begin.  (Measured,
-// 2 x 512 context rows, 24 vectors of 128, windowed verify, 4 x 256 rows of 256: without any of it 203.5, 76.8, 45.4 and
-// 313 us; so 207, 78.4, 45.5 and 307; looked for in the codes' registers instead 209, 84, 46.0 and 308; by the
-// inspector 208, 82, 46.5 and 306.)
-// NVFP4 pages: the inspector, a warp of its own, puts zeros for NaN scales in the stages that the copy warp has marked
-// as having such tokens, and the converters wait for it there.  (Two context chunks, windowed verify rows:
-// without 636 and 40.7 us; so 642 and 41.4; looked for by the converters, which have 72 registers, 663 to 680 and
-// 42 to 43.)
-__device__ __forceinline__ bool partly_seen(const Seg& seg, int tok) {
-  return tok < seg.n_all && tok >= seg.lo_all && (tok >= seg.n_least || tok < seg.lo_most);
-}
-// Whether the `tokens` from tok0 on can have such tokens.
-__device__ __forceinline__ bool any_partly(const Seg& seg, int tok0, int tokens) {
-  return (seg.n_least < seg.n_all && tok0 + tokens > seg.n_least) || (seg.lo_all < seg.lo_most && tok0 < seg.lo_most);
-}
-// Bits 15 and 31 for two fp16 that are not finite (the others are anything), and those as zeros.
-__device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return (w & 0x7C007C00u) + 0x04000400u; }
-__device__ __forceinline__ uint32_t finite2(uint32_t w) {
-  return w & ~(((not_finite2(w) & 0x80008000u) >> 15) * 0xFFFFu);
-}
-template <int CG>
-__device__ __forceinline__ void leave_note(uint32_t* at) {
-  if constexpr (CG == 1)
-    *reinterpret_cast<volatile uint32_t*>(at) = 1u;
-  else
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.u32 [a], %1;\n\t"
-        "mapa.shared::cluster.u32 a, %0, 1;\n\tst.shared::cluster.u32 [a], %1;\n\tfence.acq_rel.cluster;\n\t}" ::"r"(
-            smem_u32(at)), "r"(1u)
-        : "memory");
-}
 // A converter's bounded wait for the inspector to come past marked chunk n: true when it gave up.
 __device__ __forceinline__ bool not_inspected(const uint32_t* past, uint32_t n) {
   auto there = [&]() {
@@ -474,6 +500,7 @@ __device__ __forceinline__ bool inspect_all(const Shape& sh, const Work& p, cons
   return true;
 }
 
+// ---- values that are not finite: what vectors get in the end ------------------------
 // By all threads: for the CTA's vectors of each of its parts, NaN in the dims of the NaN codes (or scales) of the
 // tokens that they see and others do not, where their output or their record is.  Sixteen dims of a vector a thread.
 template <class T>
@@ -623,7 +650,7 @@ struct Converter8 {
 template <class T, class... C>
 __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, const Span& span, uint64_t* full,
                                             uint64_t* empty, const volatile uint32_t* copied, bool v,
-                                            uint32_t* words, const uint32_t* past, C... conv) {
+                                            uint32_t* note, const uint32_t* past, C... conv) {
   int chunks = 0, slot = 0, use = 0;
   Cursor cursor(span);
   Seg seg;
@@ -632,11 +659,11 @@ __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, cons
     for (int c = 0; c < seg.todo; ++c) {
       if (gave_up(&full[slot], use)) return false;
       const uint32_t bits = copied[slot];
-      if constexpr (!T::E8)
-        if ((v || sizeof...(C) == 2) && (bits & kMarked) && not_inspected(past, chunks)) return false;
+      if constexpr (T::kInspect)
+        if ((bits & kMarked) && not_inspected(past, chunks)) return false;
       bool second = v;
       auto one = [&](auto& cv) {
-        const bool done = cv.convert(seg, (seg.chunk0 + c) * T::kTok, chunks, slot, bits, second, words);
+        const bool done = cv.convert(seg, (seg.chunk0 + c) * T::kTok, chunks, slot, bits, second, note);
         second = true;
         return done;
       };
@@ -650,7 +677,7 @@ __device__ __forceinline__ bool convert_all(const Shape& sh, const Work& p, cons
       ++chunks;
     }
   }
-  if ((threadIdx.x & 31) == 0) words[1] = (uint32_t)chunks;
+  if ((threadIdx.x & 31) == 0) note[1] = (uint32_t)chunks;
   return true;
 }
 
@@ -687,8 +714,8 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + T::kBars);
   uint32_t* copied = s_tmem + 4;                               // [kDepth]
   float* exps = reinterpret_cast<float*>(copied + 4);          // [kExpSlots][2^ke, ve, 2^-ve]
-  // NVFP4: the marked chunk that the inspector has last come past, from 1 on
-  [[maybe_unused]] uint32_t* past = copied + T::kDepth;
+  // NVFP4: behind where the tokens of each marked stage lie, the chunk that the inspector has last come past, from 1 on
+  [[maybe_unused]] uint32_t* past = copied + 5 * T::kDepth;
 
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -710,7 +737,7 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
     mbar_init(qready, T::kSoft * CG);
     for (int x = 0; x < T::kDepth; ++x) {
       mbar_init(&full[x], 1);
-      mbar_init(&empty[x], T::kDeq + (E8 ? 0 : 1));
+      mbar_init(&empty[x], T::kDeq + (T::kInspect ? 1 : 0));
     }
     fence_mbar_init();
   }
@@ -1144,10 +1171,10 @@ dense_tile_kernel(const __grid_constant__ Shape sh, const __grid_constant__ Work
                              CV(sh, true, 0, v0, dw, ring, sV, vready, vfree));
   } else if (regs_down<T::kMmaRegs>(), warp == T::kMma + 1) {
     // ==== copies =====================================================================
-    dead = !copy_all<T>(sh, p, span, rank, ring, full, empty, copied, exps);
-  } else if (warp == T::kMma + 2) {
+    dead = !copy_all<T>(sh, p, span, rank, ring, full, empty, copied, exps, reinterpret_cast<int*>(copied + T::kDepth));
+  } else if (T::kInspect && warp == T::kMma + 2) {
     // ==== inspection =================================================================
-    if constexpr (!E8) dead = !inspect_all<T>(sh, p, span, ring, full, empty, copied, past, s_tmem + 2);
+    if constexpr (T::kInspect) dead = !inspect_all<T>(sh, p, span, ring, full, empty, copied, past, s_tmem + 2);
   } else if (warp == T::kMma && rank == 0) {
     // ==== MMA issue ==================================================================
     const uint32_t one = elect_one();
