@@ -1,6 +1,6 @@
-// qsa_dense_tile.cu -- dense attention over the NVFP4 paged cache for many
-// query vectors per KV head (context row groups, wide verify rows), on the
-// fifth-generation tensor cores.
+// qsa_dense_tile.cu -- dense attention over the NVFP4 paged cache, or the 8-bit one
+// (E8: see "8-bit pages"), for many query vectors per KV head (context row groups,
+// wide verify rows), on the fifth-generation tensor cores.
 //
 // TensorRT-LLM PR #20276 ("Qwen3.8-Flash-Next NVFP4 target"), Performance:
 // context rows run on tcgen05 with K/V tiles shared by a group of rows; Known
@@ -23,19 +23,19 @@
 // per pair), at 256 one.  Single CTAs (fewer vectors, from 17 on: verify rows)
 // have one tile, for which the cache's bytes, not the products, are the floor.
 //
-// Measured (GB300, SM clock 2070 MHz):
-//   two context chunks of 1024 rows, 32 heads on 4, behind 30000 tokens: 638 to 650 us,
-//   1.6 PFLOP/s (0.81 of the measured cuBLAS rate).  The tensor pipe is active
+// Measured over NVFP4 pages (GB300, SM clock 2070 MHz):
+//   two context chunks of 1024 rows, 32 heads on 4, behind 30000 tokens: 646 us,
+//   1.57 PFLOP/s (0.81 of the measured cuBLAS rate).  The tensor pipe is active
 //   70 % of the time: a chunk's turn takes 2940 cycles of which its MMAs need 2048,
 //   the rest is the softmax's latency between a tile's turns.
-//   The same at 24 heads on 2 of 256: 964 us, 1.68 PFLOP/s (0.85); 4 x 256 rows of
-//   these over 16384 tokens 270 us (floor 208).
-//   32 requests x 4 verify rows, 24 heads on 2, head_dim 256, window 4096: 44 us
+//   The same at 24 heads on 2 of 256: 966 us, 1.68 PFLOP/s (0.85); 4 x 256 rows of
+//   these over 16384 tokens 268 us (floor 208).
+//   32 requests x 4 verify rows, 24 heads on 2, head_dim 256, window 4096: 41.5 us
 //   for 79 MB (floor 11.8).  A CTA has 30 chunks of 64 tokens, 1780 cycles each (the K
 //   warps' conversion, shared memory; the MMAs need 1024, 80 of the tile's 128 rows hold
 //   no vector), a start of 5.6 us (work division 0.7,
 //   queries 4.3, first pages and S 0.6), a record (1.2 us), and the join kernel with its
-//   launch (9 us).  16 requests x 4 rows of 32 heads on 4 of 128 over 16384 tokens: 77 us
+//   launch (5 to 6 us).  16 requests x 4 rows of 32 heads on 4 of 128 over 16384 tokens: 79 us
 //   for 151 MB (floor 22.6).
 //
 // Roles in a CTA (a warp group each unless noted):
@@ -45,7 +45,8 @@
 //             at the end of a part O from tensor memory to the output or to a record.  A
 //             group per tile
 //   copy      one warp: codes and scales of the pages by bulk copies some chunks ahead
-//   dequant   e2m1 x e4m3 exact in fp16 into double-buffered K and V tiles (128-byte swizzle)
+//   dequant   e2m1 x e4m3 (8-bit pages: e4m3 alone) exact in fp16 into double-buffered K and V tiles
+//             (128-byte swizzle)
 //   inspector one warp (NVFP4 pages, two tiles): see "Values that are not finite"
 //   MMA       one warp (of the pair's first CTA) issues every MMA in order.  With two tiles
 //             they take turns: O_0, S_0 of the next chunk, O_1, S_1, so that one tile's
@@ -556,11 +557,11 @@ __device__ __forceinline__ void add_not_finite(const Shape& sh, const Work& p, i
 // too short for bulk copies, as the floats that the softmax takes (bytes, taken apart by every
 // thread of it, made a chunk's turn 600 cycles longer for a tile).
 //
-// Measured (GB300): two context chunks of 512 rows, 32 heads on 4 of 128, behind 14000 to 16384 tokens 202 us
-// (1.24 PFLOP/s; NVFP4 pages 182: their codes are half the bytes to read from shared memory, and their
+// Measured (GB300): two context chunks of 512 rows, 32 heads on 4 of 128, behind 14000 to 16384 tokens 207 us
+// (1.21 PFLOP/s; NVFP4 pages 182: their codes are half the bytes to read from shared memory, and their
 // scales are gone before the softmax; without the second kernel that joins the parts 190); 4 x 256 rows of
-// 24 heads on 2 of 256 over 16384 319 us, 1.28 PFLOP/s; windowed verify rows (32 requests x 4 rows, 24 heads
-// on 2 of 256, window 4096) 45.2 us for 138 MB, 4 to 5 of them the join.
+// 24 heads on 2 of 256 over 16384 306 us, 1.34 PFLOP/s; windowed verify rows (32 requests x 4 rows, 24 heads
+// on 2 of 256, window 4096) 45.7 us for 138 MB, 4 to 5 of them the join.
 //
 // A lane has a 16-byte piece (16 codes, two 16-byte pieces of the tile) per step; a row's pieces belong to
 // neighbouring lanes, of eight of them the upper four store their two in the other order

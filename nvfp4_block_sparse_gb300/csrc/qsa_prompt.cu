@@ -22,13 +22,14 @@
 //
 // Weights are bf16, as V is (one kind of operand per MMA): eight bits each, of sums that are fp32.
 // bf16 has fp32's exponents, so no weight is lost to the base; it is the exact maximum of the first
-// tokens, and moves when a later logit is 2^8 above it.
+// tokens, and moves when a later logit is 2^8 above it.  (Two bf16 terms a weight would have 16 bits, and the
+// products with V twice as long.)
 //
 // Measured (GB300): 8192 tokens, 32 heads on 4 of 128: 310 us, 1.77 PFLOP/s (0.92 of the measured
 // cuBLAS rate); 16 on 2 of 256: 272 to 284 us, 1.94 to 2.02 PFLOP/s; 4 prompts of 3000 to 4096 with a
-// window of 1024: 150 us; 6 of 329 to 1993, 24 on 2 of 256: 94 to 108 us (one tile to a CTA: each chunk
+// window of 1024: 151 us; 6 of 329 to 1993, 24 on 2 of 256: 95 to 112 us (one tile to a CTA: each chunk
 // is 64 KB a CTA from L2, 9 TB/s over the GPU, and the time changes from process to process); 64 of 50 to
-// 150: 42 us; one of 77: 7.2 us.  A chunk's turn of two
+// 150: 38 to 41 us; one of 77: 7.1 us.  A chunk's turn of two
 // tiles takes 3130 cycles of which its MMAs need 2048: from one tile's S to its next O pass S's
 // commit (450 cycles until a warp sees it), the softmax (ld 180, maximum 500, weights 800) and P's
 // arrival (300), and the other tile's products cover 1024 of that.  One tile with three S
